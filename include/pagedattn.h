@@ -67,6 +67,7 @@ typedef enum pa_status {
 #define PA_DEVERR_SLOT         0x2u  /* slot_mapping entry >= P * page_size         */
 #define PA_DEVERR_CONTEXT_LEN  0x4u  /* context_lens entry < 0 or > max_pages*ps    */
 #define PA_DEVERR_TIMEOUT      0x8u  /* pipeline wait gave up                       */
+#define PA_DEVERR_POSITION     0x10u /* positions entry outside [0, table_len)      */
 
 /* Problem sizes shared by every call. */
 typedef struct pa_shape {
@@ -235,6 +236,56 @@ pa_status pa_prefill(const void *query, const void *key_pages,
 pa_status pa_append_kv_fp8(const void *key, const void *value, void *key_pages,
                            void *value_pages, const int32_t *slot_mapping, int32_t page_size,
                            float k_scale, float v_scale, pa_shape shape, void *stream);
+
+/*
+ * From a fused QKV projection to the cache in one pass: the norm of every
+ * query and key head row, the position rotation, and the write path (Reading
+ * vLLM's PagedAttention Kernel, 3.2: the cache holds rotated keys and plain
+ * values). The queries it writes are pa_attention's, the K/V rows those of
+ * pa_append_kv.
+ *   qkv          bf16. Token (b, i) is a row of (H_q + 2 H_kv) D elements at
+ *                element b * qkv_batch_stride + i * qkv_token_stride: H_q query
+ *                heads, then H_kv key heads, then H_kv value heads. 16-byte
+ *                aligned, strides in elements, multiples of 8, at least a row.
+ *   q_weight, k_weight   [D] bf16, 16-byte aligned: x * rsqrt(mean(x^2) + eps)
+ *                * weight for each head row; NULL: no norm of queries / keys.
+ *   cos_sin      [table_len, rotary_dim] fp32, 16-byte aligned: for each
+ *                position the cosines of the rotary_dim / 2 angles, then their
+ *                sines (made once, in as many bits as far positions need).
+ *   rotary_dim   R, a multiple of 16 up to D: the first R elements of a head
+ *                row are rotated, in pairs (i, i + R/2), or (2i, 2i + 1) when
+ *                interleaved. 0: no rotation (cos_sin, positions unused).
+ *   positions    [B, L] int32, each token's row of cos_sin. A token's position
+ *                and its slot are independent (an evicted cache is shorter
+ *                than the text). An entry outside [0, table_len) records
+ *                PA_DEVERR_POSITION and is moved to the nearer end.
+ *   query        [B, H_q, L, D] bf16 out, must not overlap qkv. Row i is token
+ *                i's: for pa_attention, whose rows are the newest, a request
+ *                with fewer than L tokens has its padding tokens first.
+ *   slot_mapping [B, L] int32 as for pa_append_kv. A token with slot < 0 is
+ *                padding: no K/V is written, and its query row holds the
+ *                result for the position clamped into the table (not recorded).
+ *   shape        num_q_heads, num_kv_heads, head_dim, q_len = L, num_pages,
+ *                batch; max_pages is unused.
+ * fp32 arithmetic; queries and bf16 rows are rounded once, e4m3 rows (the
+ * _fp8 form, head_dim 128) are the codes pa_append_kv_fp8 gives for the
+ * unrounded values. Values are copied bit for bit into bf16 pools.
+ */
+pa_status pa_qk_norm_rope_append(const void *qkv, int64_t qkv_batch_stride,
+                                 int64_t qkv_token_stride, const void *q_weight,
+                                 const void *k_weight, float eps, const float *cos_sin,
+                                 int32_t rotary_dim, int32_t table_len, int interleaved,
+                                 const int32_t *positions, void *query, void *key_pages,
+                                 void *value_pages, const int32_t *slot_mapping,
+                                 int32_t page_size, pa_shape shape, void *stream);
+pa_status pa_qk_norm_rope_append_fp8(const void *qkv, int64_t qkv_batch_stride,
+                                     int64_t qkv_token_stride, const void *q_weight,
+                                     const void *k_weight, float eps, const float *cos_sin,
+                                     int32_t rotary_dim, int32_t table_len, int interleaved,
+                                     const int32_t *positions, void *query, void *key_pages,
+                                     void *value_pages, const int32_t *slot_mapping,
+                                     int32_t page_size, float k_scale, float v_scale,
+                                     pa_shape shape, void *stream);
 
 /*
  * pa_decode over e4m3 pools: the same split-KV schedule, arguments,

@@ -32,6 +32,7 @@ PA_DEVERR_PAGE_ID = 0x1
 PA_DEVERR_SLOT = 0x2
 PA_DEVERR_CONTEXT_LEN = 0x4
 PA_DEVERR_TIMEOUT = 0x8
+PA_DEVERR_POSITION = 0x10
 
 LIB_PATH = _build.LIB
 
@@ -123,6 +124,12 @@ def _load() -> ctypes.CDLL:
     lib.pa_status_string.restype = ctypes.c_char_p
     lib.pa_version.argtypes = []
     lib.pa_version.restype = ctypes.c_char_p
+    i64 = ctypes.c_int64
+    qk = [vp, i64, i64, vp, vp, f32, vp, i32, i32, ctypes.c_int, vp, vp, vp, vp, vp, i32]
+    lib.pa_qk_norm_rope_append.argtypes = qk + [pa_shape, vp]
+    lib.pa_qk_norm_rope_append.restype = ctypes.c_int
+    lib.pa_qk_norm_rope_append_fp8.argtypes = qk + [f32, f32, pa_shape, vp]
+    lib.pa_qk_norm_rope_append_fp8.restype = ctypes.c_int
     lib.pa_debug_arm_wait_timeout.argtypes = []
     lib.pa_debug_arm_wait_timeout.restype = None
     lib.pa_debug_prefill_variant.argtypes = [ctypes.c_int]
@@ -267,6 +274,133 @@ def pa_append_kv_fp8(key: torch.Tensor, value: torch.Tensor, key_pages: torch.Te
                                int(page_size), float(k_scale), float(v_scale), shape,
                                _stream(stream))
     _check(st, "pa_append_kv_fp8")
+
+
+def _on_device(device: torch.device, stream, tensors):
+    """(raw stream, guard or None) of a call whose tensors all live on
+    `device`: the given stream or the device's current one, and a guard that
+    makes the device current where it is not."""
+    for name, t in tensors:
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} is on {t.device}, expected {device}")
+    raw = torch._C._cuda_getCurrentRawStream(device.index) if stream is None else _stream(stream)
+    guard = None if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+    return raw, guard
+
+
+def _launch(fn, what: str, guard, *args) -> None:
+    if guard is None:
+        st = fn(*args)
+    else:
+        with guard:
+            st = fn(*args)
+    if st != PA_OK:
+        raise PagedAttentionError(st, what)
+
+
+def _scratch(need: int, device: torch.device, stream) -> torch.Tensor:
+    """A workspace of this call alone: the allocator orders its reuse on the
+    stream that the call runs on (a capture's lives in the graph's pool)."""
+    buf = torch.empty(max(int(need), 16), dtype=torch.uint8, device=device)
+    _keep_for(buf, stream)
+    return buf
+
+
+def _keep_for(t: torch.Tensor, stream) -> None:
+    """Memory allocated on the current stream for a call on `stream`."""
+    if stream is None:
+        return
+    if not isinstance(stream, torch.cuda.Stream):
+        if int(stream) == torch.cuda.current_stream(t.device).cuda_stream:
+            return
+        stream = torch.cuda.ExternalStream(int(stream), device=t.device)
+    t.record_stream(stream)
+
+
+def _qk_norm_rope_append(qkv, q_weight, k_weight, cos_sin, positions, key_pages, value_pages,
+                         slot_mapping, page_size, scales, eps, interleaved, query, stream):
+    fp8 = bool(scales)
+    what = "pa_qk_norm_rope_append_fp8" if fp8 else "pa_qk_norm_rope_append"
+    pool_dtype = torch.uint8 if fp8 else torch.bfloat16
+    if qkv.dim() != 3:
+        raise ValueError("qkv must be [B, L, (H_q + 2 H_kv) * D]")
+    B, L, width = qkv.shape
+    P, H_kv, ps, D = key_pages.shape
+    if ps != page_size or value_pages.shape != key_pages.shape:
+        raise ValueError("page pool shape does not match page_size")
+    H_q = width // D - 2 * H_kv
+    if H_q <= 0 or (H_q + 2 * H_kv) * D != width:
+        raise ValueError("qkv's rows are not (H_q + 2 H_kv) heads of the pools' head_dim")
+    if tuple(slot_mapping.shape) != (B, L):
+        raise ValueError("slot_mapping must be [B, L]")
+    if not qkv.is_cuda:
+        raise ValueError("qkv must be a CUDA tensor")
+    if qkv.dtype != torch.bfloat16:
+        raise TypeError(f"qkv must be torch.bfloat16, got {qkv.dtype}")
+    if qkv.stride(2) != 1:
+        raise ValueError("qkv's rows must be contiguous")
+    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if w is not None and tuple(w.shape) != (D,):
+            raise ValueError(f"{name} must be [D]")
+    R = table_len = 0
+    if cos_sin is not None:
+        if positions is None or tuple(positions.shape) != (B, L):
+            raise ValueError("positions must be [B, L]")
+        if cos_sin.dim() != 2:
+            raise ValueError("cos_sin must be [table_len, rotary_dim]")
+        table_len, R = cos_sin.shape
+    device = qkv.device
+    raw, guard = _on_device(device, stream, (
+        ("q_weight", q_weight), ("k_weight", k_weight), ("cos_sin", cos_sin),
+        ("positions", positions), ("key_pages", key_pages), ("value_pages", value_pages),
+        ("slot_mapping", slot_mapping), ("query", query)))
+    if query is None:
+        query = torch.empty((B, H_q, L, D), dtype=torch.bfloat16, device=device)
+        _keep_for(query, stream)
+    elif tuple(query.shape) != (B, H_q, L, D):
+        raise ValueError("query must be [B, H_q, L, D]")
+    if B == 0 or L == 0:
+        return query
+    shape = pa_shape(B, H_q, H_kv, D, L, P, 0)
+    # the strides of an axis of one element say nothing
+    bs = qkv.stride(0) if B > 1 else L * width
+    ts = qkv.stride(1) if L > 1 else width
+    _launch(getattr(_lib, what), what, guard, qkv.data_ptr(), bs, ts,
+            None if q_weight is None else _dev_ptr(q_weight, torch.bfloat16, "q_weight"),
+            None if k_weight is None else _dev_ptr(k_weight, torch.bfloat16, "k_weight"),
+            float(eps), None if cos_sin is None else _dev_ptr(cos_sin, torch.float32, "cos_sin"),
+            R, table_len, int(bool(interleaved)),
+            None if cos_sin is None else _dev_ptr(positions, torch.int32, "positions"),
+            _dev_ptr(query, torch.bfloat16, "query"), _dev_ptr(key_pages, pool_dtype, "key_pages"),
+            _dev_ptr(value_pages, pool_dtype, "value_pages"),
+            _dev_ptr(slot_mapping, torch.int32, "slot_mapping"), int(page_size), *scales, shape, raw)
+    return query
+
+
+def pa_qk_norm_rope_append(qkv: torch.Tensor, q_weight: Optional[torch.Tensor],
+                           k_weight: Optional[torch.Tensor], cos_sin: Optional[torch.Tensor],
+                           positions: Optional[torch.Tensor], key_pages: torch.Tensor,
+                           value_pages: torch.Tensor, slot_mapping: torch.Tensor, page_size: int,
+                           eps: float = 1e-6, interleaved: bool = False,
+                           query: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """A fused QKV projection's rows qkv [B, L, (H_q + 2 H_kv) * D] bf16 (any
+    batch and token strides) to the cache: per-head norms (weights [D], None:
+    no norm), rotation by cos_sin [table_len, R] fp32 at positions [B, L]
+    (None: no rotation), k and v rows into the pages at slot_mapping [B, L].
+    Returns the queries [B, H_q, L, D]."""
+    return _qk_norm_rope_append(qkv, q_weight, k_weight, cos_sin, positions, key_pages,
+                                value_pages, slot_mapping, page_size, (), eps, interleaved, query,
+                                stream)
+
+
+def pa_qk_norm_rope_append_fp8(qkv, q_weight, k_weight, cos_sin, positions, key_pages, value_pages,
+                               slot_mapping, page_size: int, k_scale: float, v_scale: float,
+                               eps: float = 1e-6, interleaved: bool = False, query=None,
+                               stream=None) -> torch.Tensor:
+    """pa_qk_norm_rope_append into uint8 e4m3 pools, code = e4m3(x / scale)."""
+    return _qk_norm_rope_append(qkv, q_weight, k_weight, cos_sin, positions, key_pages,
+                                value_pages, slot_mapping, page_size,
+                                (float(k_scale), float(v_scale)), eps, interleaved, query, stream)
 
 
 def pa_decode_fp8(query, key_pages, value_pages, block_table, context_lens, page_size: int,

@@ -40,19 +40,13 @@ namespace {
 
 constexpr int kMaxDevices = 64;
 
-struct DeviceInfo {
-    bool ready = false;
-    int id = 0;
-    int sm_count = 0;
-    int max_smem_optin = 0;
-    unsigned* err = nullptr;  // device address of g_device_error
-};
-
 std::mutex g_mutex;
 thread_local bool t_arm_unset_wait = false;  // test support, see pa_debug_arm_wait_timeout
 thread_local int t_prefill_variant = 0;      // see pa_debug_prefill_variant
 DeviceInfo g_devices[kMaxDevices];
 PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
+
+}  // namespace
 
 pa_status device_info(DeviceInfo** out)
 {
@@ -79,6 +73,8 @@ pa_status device_info(DeviceInfo** out)
     *out = &d;
     return PA_OK;
 }
+
+namespace {
 
 pa_status get_encoder(PFN_cuTensorMapEncodeTiled_v12000* fn)
 {
@@ -790,6 +786,127 @@ pa_status pa_append_kv_fp8(const void* key, const void* value, void* key_pages,
     a.v_scale = v_scale;
     return launch_append(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? PA_OK
                                                                                : PA_ERR_CUDA;
+}
+
+namespace {
+
+bool ranges_overlap(const void* p, uint64_t p_bytes, const void* q, uint64_t q_bytes)
+{
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+    return a < b + q_bytes && b < a + p_bytes;
+}
+
+// Both pools' forms: fp8 with their scales, or bf16 (scales 1).
+pa_status run_norm_rope_append(const void* qkv, int64_t batch_stride, int64_t token_stride,
+                               const void* q_weight, const void* k_weight, float eps,
+                               const float* cos_sin, int32_t rotary_dim, int32_t table_len,
+                               int interleaved, const int32_t* positions, void* query,
+                               void* key_pages, void* value_pages, const int32_t* slot_mapping,
+                               int32_t page_size, int fp8, float k_scale, float v_scale,
+                               const pa_shape& s, void* stream)
+{
+    if (!qkv || !query || !key_pages || !value_pages || !slot_mapping)
+        return PA_ERR_INVALID_ARG;
+    if (s.batch <= 0 || s.num_q_heads <= 0 || s.num_kv_heads <= 0 || s.q_len < 0 ||
+        s.num_pages <= 0 || s.head_dim <= 0)
+        return PA_ERR_INVALID_ARG;
+    if (!aligned16(qkv) || !aligned16(query) || !aligned16(key_pages) || !aligned16(value_pages) ||
+        !aligned16(q_weight) || !aligned16(k_weight) || !aligned16(cos_sin))
+        return PA_ERR_INVALID_ARG;
+    if ((q_weight || k_weight) && (!(eps >= 0.f) || !isfinite(eps)))
+        return PA_ERR_INVALID_ARG;
+    if (fp8 && (!(k_scale > 0.f) || !isfinite(k_scale) || !(v_scale > 0.f) || !isfinite(v_scale)))
+        return PA_ERR_INVALID_ARG;
+    if (rotary_dim < 0 || rotary_dim > s.head_dim ||
+        (rotary_dim > 0 && (!cos_sin || !positions || table_len <= 0)))
+        return PA_ERR_INVALID_ARG;
+    if ((s.head_dim != 64 && s.head_dim != 128) || (fp8 && s.head_dim != 128) ||
+        rotary_dim % 16 != 0)
+        return PA_ERR_UNSUPPORTED;
+    if (s.num_q_heads % s.num_kv_heads != 0 || !pow2_in(page_size, 1, 256))
+        return PA_ERR_UNSUPPORTED;
+    const int64_t heads = int64_t(s.num_q_heads) + 2 * int64_t(s.num_kv_heads);
+    if (heads >= (1 << 20) || int64_t(s.batch) * s.q_len * heads >= (int64_t(1) << 34))
+        return PA_ERR_UNSUPPORTED;
+    const int64_t row = heads * s.head_dim;
+    if (token_stride % 8 != 0 || batch_stride % 8 != 0 || token_stride < 0 || batch_stride < 0 ||
+        (s.q_len > 1 && token_stride < row) || (s.batch > 1 && batch_stride < row))
+        return PA_ERR_INVALID_ARG;
+    DeviceInfo* dev;
+    pa_status st = device_info(&dev);
+    if (st != PA_OK)
+        return st;
+    if (s.q_len == 0)
+        return PA_OK;
+    // The rows are read by other threads than those that write the queries.
+    const uint64_t in_bytes =
+        2 * uint64_t((s.batch - 1) * batch_stride + (s.q_len - 1) * token_stride + row);
+    const uint64_t q_bytes = 2 * uint64_t(s.batch) * s.num_q_heads * s.q_len * s.head_dim;
+    if (ranges_overlap(qkv, in_bytes, query, q_bytes))
+        return PA_ERR_INVALID_ARG;
+    NormRopeArgs a;
+    memset(&a, 0, sizeof a);
+    a.qkv = static_cast<const uint16_t*>(qkv);
+    a.batch_stride = batch_stride;
+    a.token_stride = token_stride;
+    a.q_weight = static_cast<const uint16_t*>(q_weight);
+    a.k_weight = static_cast<const uint16_t*>(k_weight);
+    a.cos_sin = cos_sin;
+    a.positions = positions;
+    a.query = static_cast<uint16_t*>(query);
+    a.key_pages = static_cast<uint16_t*>(key_pages);
+    a.value_pages = static_cast<uint16_t*>(value_pages);
+    a.slot_mapping = slot_mapping;
+    a.err = dev->err;
+    a.B = s.batch;
+    a.L = s.q_len;
+    a.H_q = s.num_q_heads;
+    a.H_kv = s.num_kv_heads;
+    a.D = s.head_dim;
+    while ((1 << a.ps_shift) < page_size)
+        ++a.ps_shift;
+    a.num_pages = s.num_pages;
+    a.rotary_dim = rotary_dim;
+    a.table_len = table_len;
+    a.interleaved = interleaved ? 1 : 0;
+    a.fp8 = fp8;
+    a.eps = eps;
+    a.k_scale = k_scale;
+    a.v_scale = v_scale;
+    return launch_norm_rope_append(a, static_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? PA_OK
+               : PA_ERR_CUDA;
+}
+
+}  // namespace
+
+pa_status pa_qk_norm_rope_append(const void* qkv, int64_t qkv_batch_stride,
+                                 int64_t qkv_token_stride, const void* q_weight,
+                                 const void* k_weight, float eps, const float* cos_sin,
+                                 int32_t rotary_dim, int32_t table_len, int interleaved,
+                                 const int32_t* positions, void* query, void* key_pages,
+                                 void* value_pages, const int32_t* slot_mapping,
+                                 int32_t page_size, pa_shape shape, void* stream)
+{
+    return run_norm_rope_append(qkv, qkv_batch_stride, qkv_token_stride, q_weight, k_weight, eps,
+                                cos_sin, rotary_dim, table_len, interleaved, positions, query,
+                                key_pages, value_pages, slot_mapping, page_size, 0, 1.f, 1.f,
+                                shape, stream);
+}
+
+pa_status pa_qk_norm_rope_append_fp8(const void* qkv, int64_t qkv_batch_stride,
+                                     int64_t qkv_token_stride, const void* q_weight,
+                                     const void* k_weight, float eps, const float* cos_sin,
+                                     int32_t rotary_dim, int32_t table_len, int interleaved,
+                                     const int32_t* positions, void* query, void* key_pages,
+                                     void* value_pages, const int32_t* slot_mapping,
+                                     int32_t page_size, float k_scale, float v_scale,
+                                     pa_shape shape, void* stream)
+{
+    return run_norm_rope_append(qkv, qkv_batch_stride, qkv_token_stride, q_weight, k_weight, eps,
+                                cos_sin, rotary_dim, table_len, interleaved, positions, query,
+                                key_pages, value_pages, slot_mapping, page_size, 1, k_scale,
+                                v_scale, shape, stream);
 }
 
 pa_status pa_decode_fp8(const void* query, const void* key_pages, const void* value_pages,

@@ -16,11 +16,22 @@ constexpr unsigned PA_DEVERR_PAGE_ID_BIT = 0x1u;
 constexpr unsigned PA_DEVERR_SLOT_BIT = 0x2u;
 constexpr unsigned PA_DEVERR_CONTEXT_LEN_BIT = 0x4u;
 constexpr unsigned PA_DEVERR_TIMEOUT_BIT = 0x8u;
+constexpr unsigned PA_DEVERR_POSITION_BIT = 0x10u;
 
 // Longest a kernel waits for one pipeline phase before giving up, and the
 // limit of every later wait of a block that already gave up once.
 constexpr uint64_t kWaitLimitNs = 1000000000ull;
 constexpr uint64_t kShortWaitLimitNs = 20000000ull;
+
+// The current device's properties, looked up once.
+struct DeviceInfo {
+    bool ready = false;
+    int id = 0;
+    int sm_count = 0;
+    int max_smem_optin = 0;
+    unsigned* err = nullptr;  // device address of the error word
+};
+pa_status device_info(DeviceInfo** out);
 
 // ---------------------------------------------------------------------------
 // Write path
@@ -38,6 +49,29 @@ struct AppendArgs {
 };
 
 cudaError_t launch_append(const AppendArgs& a, cudaStream_t stream);
+
+// Norms, rotation and append of a fused QKV projection's rows.
+struct NormRopeArgs {
+    const uint16_t* qkv;          // row of token (b, i) at b * batch_stride + i * token_stride:
+    int64_t batch_stride;         // H_q query heads, H_kv key heads, H_kv value heads of D
+    int64_t token_stride;
+    const uint16_t* q_weight;     // [D] bf16, or null: no norm
+    const uint16_t* k_weight;
+    const float* cos_sin;         // [table_len, rotary_dim]: cos of the angles, then sin
+    const int32_t* positions;     // [B, L]
+    uint16_t* query;              // [B, H_q, L, D]
+    uint16_t* key_pages;          // [P, H_kv, ps, D] bf16, or e4m3 codes
+    uint16_t* value_pages;
+    const int32_t* slot_mapping;  // [B, L]
+    unsigned* err;
+    int32_t B, L, H_q, H_kv, D, ps_shift, num_pages;
+    int32_t rotary_dim, table_len, interleaved;
+    int32_t gpt;                  // set by the launcher: lane groups per token
+    int32_t fp8;
+    float eps, k_scale, v_scale;
+};
+
+cudaError_t launch_norm_rope_append(NormRopeArgs a, cudaStream_t stream);
 
 struct GatherArgs {
     const uint16_t* key_pages;    // [P, H_kv, ps, D]
