@@ -433,6 +433,47 @@ pa_status pa_attention(const void *query, const void *key_pages,
                        size_t workspace_bytes, void *stream);
 
 /*
+ * Eviction by accumulated attention weight: cuts every request to at most
+ * `keep` cached tokens. For each request and KV head it keeps the first
+ * `sinks` positions, the last `recent` ones, and of the positions between
+ * those of the highest weight in weight_pages (ties to the lowest position; a
+ * NaN counts as below every number, -0 as +0), `keep` in all, and moves their
+ * K, V and weight rows, in the order of their positions, to positions
+ * 0 .. keep - 1 of dst_block_table's pages. KV heads keep different positions
+ * but the same number, so a request has one context length afterwards. A
+ * request of `keep` tokens or fewer keeps all of them.
+ *   key_pages, value_pages  [P, H_kv, page_size, D] bf16 (_fp8: e4m3 codes,
+ *                    head_dim 128); weight_pages [P, H_kv, page_size] fp32.
+ *   dst_block_table  [B, dst_max_pages] int32. The block table itself: in
+ *                    place; slots behind the kept ones keep their contents.
+ *                    Another table: entry i of a request is either entry i of
+ *                    its own block_table row, or a page that no request of the
+ *                    call reads and no other entry names (pages shared by
+ *                    requests are evicted into fresh ones). At least
+ *                    min(keep, max_pages * page_size) tokens wide; entries
+ *                    behind the kept rows are not read.
+ *   kept             [B, H_kv, keep] int32 out: the kept positions, ascending,
+ *                    -1 behind the last.
+ *   new_lens         [B] int32 out: min(context_lens, keep). kept and new_lens
+ *                    overlap neither each other, the tables nor context_lens.
+ *   sinks + recent <= keep.
+ *   shape            batch, num_kv_heads, head_dim, num_pages, max_pages.
+ * A page id outside the pool (PA_DEVERR_PAGE_ID) counts as lowest weights when
+ * choosing, and its rows are not moved. The rotation of a moved key stays that
+ * of its token's own position. Two kernels on `stream`.
+ */
+pa_status pa_kv_evict(void *key_pages, void *value_pages, float *weight_pages,
+                      const int32_t *block_table, const int32_t *context_lens,
+                      int32_t page_size, int32_t keep, int32_t sinks, int32_t recent,
+                      const int32_t *dst_block_table, int32_t dst_max_pages,
+                      int32_t *kept, int32_t *new_lens, pa_shape shape, void *stream);
+pa_status pa_kv_evict_fp8(void *key_pages, void *value_pages, float *weight_pages,
+                          const int32_t *block_table, const int32_t *context_lens,
+                          int32_t page_size, int32_t keep, int32_t sinks, int32_t recent,
+                          const int32_t *dst_block_table, int32_t dst_max_pages,
+                          int32_t *kept, int32_t *new_lens, pa_shape shape, void *stream);
+
+/*
  * Synchronises `stream`, then reads and clears the device error word of the
  * current device. *flags (may be NULL) receives the PA_DEVERR_* bits seen
  * since the last call. Returns PA_OK when no bit was set,
@@ -463,6 +504,16 @@ void pa_kv_cache_destroy(pa_kv_cache *cache);
 /* A new request with no tokens; PA_ERR_INVALID_ARG if seq_id exists. */
 pa_status pa_kv_cache_add(pa_kv_cache *cache, int64_t seq_id);
 pa_status pa_kv_cache_release(pa_kv_cache *cache, int64_t seq_id);
+
+/*
+ * Cuts seq_id to its first new_len tokens (0 .. the tokens it has) and gives
+ * back the pages behind them, last page first: the host side of pa_kv_evict in
+ * place, whose new length min(context length, keep) the host knows without
+ * reading the device. The pages may be handed out to work that follows on the
+ * same stream. PA_ERR_INVALID_ARG (nothing changed) for an unknown seq_id or
+ * another new_len.
+ */
+pa_status pa_kv_cache_truncate(pa_kv_cache *cache, int64_t seq_id, int32_t new_len);
 
 /* Pages not held by any request; -1 on a null cache. */
 int32_t pa_kv_cache_free_pages(const pa_kv_cache *cache);

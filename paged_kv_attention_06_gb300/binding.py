@@ -130,6 +130,13 @@ def _load() -> ctypes.CDLL:
     lib.pa_qk_norm_rope_append.restype = ctypes.c_int
     lib.pa_qk_norm_rope_append_fp8.argtypes = qk + [f32, f32, pa_shape, vp]
     lib.pa_qk_norm_rope_append_fp8.restype = ctypes.c_int
+    ev = [vp, vp, vp, vp, vp, i32, i32, i32, i32, vp, i32, vp, vp, pa_shape, vp]
+    lib.pa_kv_evict.argtypes = ev
+    lib.pa_kv_evict.restype = ctypes.c_int
+    lib.pa_kv_evict_fp8.argtypes = ev
+    lib.pa_kv_evict_fp8.restype = ctypes.c_int
+    lib.pa_kv_cache_truncate.argtypes = [vp, i64, i32]
+    lib.pa_kv_cache_truncate.restype = ctypes.c_int
     lib.pa_debug_arm_wait_timeout.argtypes = []
     lib.pa_debug_arm_wait_timeout.restype = None
     lib.pa_debug_prefill_variant.argtypes = [ctypes.c_int]
@@ -401,6 +408,75 @@ def pa_qk_norm_rope_append_fp8(qkv, q_weight, k_weight, cos_sin, positions, key_
     return _qk_norm_rope_append(qkv, q_weight, k_weight, cos_sin, positions, key_pages,
                                 value_pages, slot_mapping, page_size,
                                 (float(k_scale), float(v_scale)), eps, interleaved, query, stream)
+
+
+def _kv_evict(what, pool_dtype, key_pages, value_pages, weight_pages, block_table, context_lens,
+              page_size, keep, sinks, recent, dst_block_table, kept, new_lens, stream):
+    P, H_kv, ps, D = key_pages.shape
+    if ps != page_size or value_pages.shape != key_pages.shape:
+        raise ValueError("page pool shape does not match page_size")
+    if tuple(weight_pages.shape) != (P, H_kv, ps):
+        raise ValueError("weight_pages must be [P, H_kv, page_size]")
+    B = block_table.shape[0]
+    if block_table.dim() != 2 or tuple(context_lens.shape) != (B,):
+        raise ValueError("block_table must be [B, max_pages] and context_lens [B]")
+    dst = block_table if dst_block_table is None else dst_block_table
+    if dst.dim() != 2 or dst.shape[0] != B:
+        raise ValueError("dst_block_table must be [B, dst_max_pages]")
+    device = key_pages.device
+    if device.type != "cuda":
+        raise ValueError("key_pages must be a CUDA tensor")
+    raw, guard = _on_device(device, stream, (
+        ("value_pages", value_pages), ("weight_pages", weight_pages), ("block_table", block_table),
+        ("context_lens", context_lens), ("dst_block_table", dst), ("kept", kept),
+        ("new_lens", new_lens)))
+    if kept is None:
+        kept = torch.empty((B, H_kv, max(int(keep), 0)), dtype=torch.int32, device=device)
+        _keep_for(kept, stream)
+    elif tuple(kept.shape) != (B, H_kv, keep):
+        raise ValueError("kept must be [B, H_kv, keep]")
+    if new_lens is None:
+        new_lens = torch.empty((B,), dtype=torch.int32, device=device)
+        _keep_for(new_lens, stream)
+    elif tuple(new_lens.shape) != (B,):
+        raise ValueError("new_lens must be [B]")
+    if B == 0:
+        return kept, new_lens
+    shape = pa_shape(B, H_kv, H_kv, D, 1, P, block_table.shape[1])
+    _launch(getattr(_lib, what), what, guard, _dev_ptr(key_pages, pool_dtype, "key_pages"),
+            _dev_ptr(value_pages, pool_dtype, "value_pages"),
+            _dev_ptr(weight_pages, torch.float32, "weight_pages"),
+            _dev_ptr(block_table, torch.int32, "block_table"),
+            _dev_ptr(context_lens, torch.int32, "context_lens"), int(page_size), int(keep),
+            int(sinks), int(recent), _dev_ptr(dst, torch.int32, "dst_block_table"), dst.shape[1],
+            _dev_ptr(kept, torch.int32, "kept"), _dev_ptr(new_lens, torch.int32, "new_lens"), shape,
+            raw)
+    return kept, new_lens
+
+
+def pa_kv_evict(key_pages: torch.Tensor, value_pages: torch.Tensor, weight_pages: torch.Tensor,
+                block_table: torch.Tensor, context_lens: torch.Tensor, page_size: int, keep: int,
+                sinks: int = 0, recent: int = 0, dst_block_table: Optional[torch.Tensor] = None,
+                kept: Optional[torch.Tensor] = None, new_lens: Optional[torch.Tensor] = None,
+                stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Cuts every request to at most `keep` tokens per KV head: the first
+    `sinks`, the last `recent`, and the others of the highest weight in
+    weight_pages [P, H_kv, page_size] fp32; their rows move, in order, to the
+    front of dst_block_table's pages (None: in place). Returns (kept [B, H_kv,
+    keep] int32 positions, new_lens [B] int32)."""
+    return _kv_evict("pa_kv_evict", torch.bfloat16, key_pages, value_pages, weight_pages,
+                     block_table, context_lens, page_size, keep, sinks, recent, dst_block_table,
+                     kept, new_lens, stream)
+
+
+def pa_kv_evict_fp8(key_pages, value_pages, weight_pages, block_table, context_lens,
+                    page_size: int, keep: int, sinks: int = 0, recent: int = 0,
+                    dst_block_table=None, kept=None, new_lens=None,
+                    stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """pa_kv_evict over uint8 e4m3 pools (the codes move as they are)."""
+    return _kv_evict("pa_kv_evict_fp8", torch.uint8, key_pages, value_pages, weight_pages,
+                     block_table, context_lens, page_size, keep, sinks, recent, dst_block_table,
+                     kept, new_lens, stream)
 
 
 def pa_decode_fp8(query, key_pages, value_pages, block_table, context_lens, page_size: int,
@@ -743,6 +819,12 @@ class KVCache:
 
     def release(self, seq_id: int) -> None:
         _check(_lib.pa_kv_cache_release(self._h, int(seq_id)), "pa_kv_cache_release")
+
+    def truncate(self, seq_id: int, new_len: int) -> None:
+        """Cut a request to its first new_len tokens and free the pages behind
+        them (after pa_kv_evict in place: min(context length, keep))."""
+        _check(_lib.pa_kv_cache_truncate(self._h, int(seq_id), int(new_len)),
+               "pa_kv_cache_truncate")
 
     @property
     def free_pages(self) -> int:

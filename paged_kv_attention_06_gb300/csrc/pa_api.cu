@@ -11,6 +11,7 @@
 #include <algorithm>
 #include <atomic>
 #include <chrono>
+#include <initializer_list>
 #include <mutex>
 
 #include "../../include/pagedattn.h"
@@ -907,6 +908,100 @@ pa_status pa_qk_norm_rope_append_fp8(const void* qkv, int64_t qkv_batch_stride,
                                 cos_sin, rotary_dim, table_len, interleaved, positions, query,
                                 key_pages, value_pages, slot_mapping, page_size, 1, k_scale,
                                 v_scale, shape, stream);
+}
+
+namespace {
+
+pa_status run_evict(void* key_pages, void* value_pages, float* weight_pages,
+                    const int32_t* block_table, const int32_t* context_lens, int32_t page_size,
+                    int32_t keep, int32_t sinks, int32_t recent, const int32_t* dst_block_table,
+                    int32_t dst_max_pages, int32_t* kept, int32_t* new_lens, int fp8,
+                    const pa_shape& s, void* stream)
+{
+    if (!key_pages || !value_pages || !weight_pages || !block_table || !context_lens ||
+        !dst_block_table || !kept || !new_lens)
+        return PA_ERR_INVALID_ARG;
+    if (s.batch <= 0 || s.num_kv_heads <= 0 || s.num_pages <= 0 || s.max_pages <= 0 ||
+        s.head_dim <= 0 || dst_max_pages <= 0)
+        return PA_ERR_INVALID_ARG;
+    if (keep <= 0 || sinks < 0 || recent < 0 || int64_t(sinks) + recent > keep)
+        return PA_ERR_INVALID_ARG;
+    if (!aligned16(key_pages) || !aligned16(value_pages) ||
+        (reinterpret_cast<uintptr_t>(weight_pages) & 3u) != 0)
+        return PA_ERR_INVALID_ARG;
+    if ((s.head_dim != 64 && s.head_dim != 128) || (fp8 && s.head_dim != 128) ||
+        !pow2_in(page_size, 1, 256))
+        return PA_ERR_UNSUPPORTED;
+    if (int64_t(s.num_pages) * s.num_kv_heads * page_size >= (int64_t(1) << 31) ||
+        int64_t(s.max_pages) * page_size >= (int64_t(1) << 30) ||
+        int64_t(dst_max_pages) * page_size >= (int64_t(1) << 30) || keep >= (1 << 30) ||
+        int64_t(s.batch) * s.num_kv_heads >= (int64_t(1) << 24))
+        return PA_ERR_UNSUPPORTED;
+    // Every kept row needs a place.
+    const int64_t most = std::min(int64_t(keep), int64_t(s.max_pages) * page_size);
+    if (int64_t(dst_max_pages) * page_size < most)
+        return PA_ERR_INVALID_ARG;
+    // The kernels read the lengths and the table after new_lens and kept are written.
+    const uint64_t heads = uint64_t(s.batch) * s.num_kv_heads;
+    const uint64_t kept_bytes = heads * keep * 4, len_bytes = uint64_t(s.batch) * 4;
+    for (const void* out : {static_cast<const void*>(kept), static_cast<const void*>(new_lens)}) {
+        const uint64_t bytes = out == kept ? kept_bytes : len_bytes;
+        if (ranges_overlap(out, bytes, context_lens, len_bytes) ||
+            ranges_overlap(out, bytes, block_table, uint64_t(s.batch) * s.max_pages * 4) ||
+            ranges_overlap(out, bytes, dst_block_table, uint64_t(s.batch) * dst_max_pages * 4))
+            return PA_ERR_INVALID_ARG;
+    }
+    DeviceInfo* dev;
+    pa_status st = device_info(&dev);
+    if (st != PA_OK)
+        return st;
+    EvictArgs a;
+    memset(&a, 0, sizeof a);
+    a.key_pages = key_pages;
+    a.value_pages = value_pages;
+    a.weight_pages = weight_pages;
+    a.block_table = block_table;
+    a.dst_table = dst_block_table;
+    a.context_lens = context_lens;
+    a.kept = kept;
+    a.new_lens = new_lens;
+    a.err = dev->err;
+    a.B = s.batch;
+    a.H_kv = s.num_kv_heads;
+    a.row_bytes = s.head_dim * (fp8 ? 1 : 2);
+    while ((1 << a.ps_shift) < page_size)
+        ++a.ps_shift;
+    a.num_pages = s.num_pages;
+    a.max_pages = s.max_pages;
+    a.dst_max_pages = dst_max_pages;
+    a.keep = keep;
+    a.sinks = sinks;
+    a.recent = recent;
+    return launch_evict(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+}  // namespace
+
+pa_status pa_kv_evict(void* key_pages, void* value_pages, float* weight_pages,
+                      const int32_t* block_table, const int32_t* context_lens, int32_t page_size,
+                      int32_t keep, int32_t sinks, int32_t recent, const int32_t* dst_block_table,
+                      int32_t dst_max_pages, int32_t* kept, int32_t* new_lens, pa_shape shape,
+                      void* stream)
+{
+    return run_evict(key_pages, value_pages, weight_pages, block_table, context_lens, page_size,
+                     keep, sinks, recent, dst_block_table, dst_max_pages, kept, new_lens, 0, shape,
+                     stream);
+}
+
+pa_status pa_kv_evict_fp8(void* key_pages, void* value_pages, float* weight_pages,
+                          const int32_t* block_table, const int32_t* context_lens,
+                          int32_t page_size, int32_t keep, int32_t sinks, int32_t recent,
+                          const int32_t* dst_block_table, int32_t dst_max_pages, int32_t* kept,
+                          int32_t* new_lens, pa_shape shape, void* stream)
+{
+    return run_evict(key_pages, value_pages, weight_pages, block_table, context_lens, page_size,
+                     keep, sinks, recent, dst_block_table, dst_max_pages, kept, new_lens, 1, shape,
+                     stream);
 }
 
 pa_status pa_decode_fp8(const void* query, const void* key_pages, const void* value_pages,

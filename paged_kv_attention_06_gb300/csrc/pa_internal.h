@@ -73,6 +73,25 @@ struct NormRopeArgs {
 
 cudaError_t launch_norm_rope_append(NormRopeArgs a, cudaStream_t stream);
 
+// Eviction: the slots to keep of every (request, KV head), moved to the front
+// of the destination table's pages.
+struct EvictArgs {
+    void* key_pages;              // [P, H_kv, ps, D], row_bytes each row
+    void* value_pages;
+    float* weight_pages;          // [P, H_kv, ps]
+    const int32_t* block_table;   // [B, max_pages]
+    const int32_t* dst_table;     // [B, dst_max_pages]; the block table: in place
+    const int32_t* context_lens;  // [B]
+    int32_t* kept;                // [B, H_kv, keep]
+    int32_t* new_lens;            // [B]
+    unsigned* err;
+    int32_t B, H_kv, row_bytes, ps_shift, num_pages, max_pages, dst_max_pages;
+    int32_t keep, sinks, recent;
+    int32_t slices;               // set by the launcher: column slices of a row
+};
+
+cudaError_t launch_evict(EvictArgs a, cudaStream_t stream);
+
 struct GatherArgs {
     const uint16_t* key_pages;    // [P, H_kv, ps, D]
     const uint16_t* value_pages;

@@ -128,6 +128,30 @@ pa_status pa_kv_cache_release(pa_kv_cache* cache, int64_t seq_id)
     return PA_OK;
 }
 
+pa_status pa_kv_cache_truncate(pa_kv_cache* cache, int64_t seq_id, int32_t new_len)
+{
+    if (!cache)
+        return PA_ERR_INVALID_ARG;
+    auto it = cache->seqs.find(seq_id);
+    if (it == cache->seqs.end() || new_len < 0 || new_len > it->second.len)
+        return PA_ERR_INVALID_ARG;
+    Sequence& s = it->second;
+    const size_t held = (size_t(new_len) + cache->page_size - 1) / size_t(cache->page_size);
+    const size_t give = s.pages.size() - held;
+    try {
+        cache->free_list.reserve(cache->free_list.size() + give);
+    } catch (const std::bad_alloc&) {
+        return PA_ERR_NO_PAGES;   // no host memory; nothing changed
+    }
+    for (size_t k = 0; k < give; ++k) {
+        cache->free_list.push_back(s.pages.back());
+        s.pages.pop_back();
+    }
+    cache->held -= int32_t(give);
+    s.len = new_len;
+    return PA_OK;
+}
+
 int32_t pa_kv_cache_free_pages(const pa_kv_cache* cache)
 {
     return cache ? cache->num_pages - cache->held : -1;
