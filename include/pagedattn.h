@@ -433,6 +433,66 @@ pa_status pa_attention(const void *query, const void *key_pages,
                        size_t workspace_bytes, void *stream);
 
 /*
+ * pa_decode with a sliding window and a few first tokens that stay visible:
+ * query row i of a request, at position p = context_lens - L + i, sees the
+ * keys j <= p with j > p - window or j < sinks (always causal). A row at a
+ * negative position returns zeros.
+ *   window >= 1, sinks >= 0.
+ * Only the pages that hold a key some row sees are touched: block_table
+ * entries of the others are not read and may hold anything, so a cache can give
+ * back the pages between the sinks and the window. Within the pages that are
+ * read, slots that no row of the call sees may hold any bytes; a slot that one
+ * row sees and another does not has to hold numbers (0 * NaN in P . V).
+ * Other arguments, the workspace (pa_decode_workspace_bytes) and the errors as
+ * for pa_decode / pa_decode_fp8.
+ */
+pa_status pa_decode_window(const void *query, const void *key_pages, const void *value_pages,
+                           const int32_t *block_table, const int32_t *context_lens,
+                           int32_t page_size, float scale, int32_t window, int32_t sinks,
+                           void *out, pa_shape shape, int32_t max_context_len, void *workspace,
+                           size_t workspace_bytes, void *stream);
+pa_status pa_decode_window_fp8(const void *query, const void *key_pages, const void *value_pages,
+                               const int32_t *block_table, const int32_t *context_lens,
+                               int32_t page_size, float scale, float k_scale, float v_scale,
+                               int32_t window, int32_t sinks, void *out, pa_shape shape,
+                               int32_t max_context_len, void *workspace, size_t workspace_bytes,
+                               void *stream);
+
+/*
+ * pa_decode that also accumulates the attention weight of every cached slot,
+ * for pa_kv_evict. With w[j] = sum of the softmax weights that the G * L rows
+ * of a KV group give to position j (a row that sees no key gives none):
+ *   weight_pages[slot of j] = decay * weight_pages[slot of j] + w[j]
+ * and = w[j] for the L newest positions (their slots are new) and for every
+ * position when decay is 0 (the slots are then not read, so a first call with
+ * decay 0, for example over a prompt's last rows, sets a pool up).
+ *   weight_pages     [P, H_kv, page_size] fp32, updated in place.
+ *   decay            finite, >= 0 (1: plain sum).
+ *   max_context_len  > 0, bounds context_lens and sizes the workspace; a longer
+ *                    entry records PA_DEVERR_CONTEXT_LEN and is cut to it.
+ *   workspace        pa_decode_weights_workspace_bytes(shape, max_context_len)
+ *                    bytes (the decode's, 4 bytes per row and position, 8 per
+ *                    row), 16-byte aligned, any contents; calls sharing one
+ *                    must not overlap on the GPU.
+ * Pages shared by requests of one call must not be used here (two requests
+ * would update one slot). Weights are summed in fp32, rows in order. Three
+ * kernels on `stream`.
+ */
+size_t pa_decode_weights_workspace_bytes(pa_shape shape, int32_t max_context_len);
+pa_status pa_decode_weights(const void *query, const void *key_pages, const void *value_pages,
+                            float *weight_pages, const int32_t *block_table,
+                            const int32_t *context_lens, int32_t page_size, float scale,
+                            int causal, float decay, void *out, pa_shape shape,
+                            int32_t max_context_len, void *workspace, size_t workspace_bytes,
+                            void *stream);
+pa_status pa_decode_weights_fp8(const void *query, const void *key_pages, const void *value_pages,
+                                float *weight_pages, const int32_t *block_table,
+                                const int32_t *context_lens, int32_t page_size, float scale,
+                                float k_scale, float v_scale, int causal, float decay, void *out,
+                                pa_shape shape, int32_t max_context_len, void *workspace,
+                                size_t workspace_bytes, void *stream);
+
+/*
  * Eviction by accumulated attention weight: cuts every request to at most
  * `keep` cached tokens. For each request and KV head it keeps the first
  * `sinks` positions, the last `recent` ones, and of the positions between

@@ -137,6 +137,19 @@ def _load() -> ctypes.CDLL:
     lib.pa_kv_evict_fp8.restype = ctypes.c_int
     lib.pa_kv_cache_truncate.argtypes = [vp, i64, i32]
     lib.pa_kv_cache_truncate.restype = ctypes.c_int
+    tables = [vp, vp, vp, vp, vp, i32, f32]
+    tail = [vp, pa_shape, i32, vp, sz, vp]
+    lib.pa_decode_window.argtypes = tables + [i32, i32] + tail
+    lib.pa_decode_window.restype = ctypes.c_int
+    lib.pa_decode_window_fp8.argtypes = tables + [f32, f32, i32, i32] + tail
+    lib.pa_decode_window_fp8.restype = ctypes.c_int
+    lib.pa_decode_weights_workspace_bytes.argtypes = [pa_shape, i32]
+    lib.pa_decode_weights_workspace_bytes.restype = sz
+    wtables = [vp, vp, vp, vp, vp, vp, i32, f32]
+    lib.pa_decode_weights.argtypes = wtables + [ctypes.c_int, f32] + tail
+    lib.pa_decode_weights.restype = ctypes.c_int
+    lib.pa_decode_weights_fp8.argtypes = wtables + [f32, f32, ctypes.c_int, f32] + tail
+    lib.pa_decode_weights_fp8.restype = ctypes.c_int
     lib.pa_debug_arm_wait_timeout.argtypes = []
     lib.pa_debug_arm_wait_timeout.restype = None
     lib.pa_debug_prefill_variant.argtypes = [ctypes.c_int]
@@ -477,6 +490,130 @@ def pa_kv_evict_fp8(key_pages, value_pages, weight_pages, block_table, context_l
     return _kv_evict("pa_kv_evict_fp8", torch.uint8, key_pages, value_pages, weight_pages,
                      block_table, context_lens, page_size, keep, sinks, recent, dst_block_table,
                      kept, new_lens, stream)
+
+
+def _paged(query, key_pages, value_pages, block_table, context_lens, page_size, scale, out,
+           workspace, pool_dtype, stream, more=()):
+    """Checks shared by the attention calls below: (shape, the five leading
+    pointers, scale, out, raw stream, device guard)."""
+    B, H_q, L, D = query.shape
+    if not query.is_cuda:
+        raise ValueError("query must be a CUDA tensor")
+    if key_pages.dim() != 4 or key_pages.shape[2] != page_size or value_pages.shape != key_pages.shape:
+        raise ValueError("page pool shape does not match page_size")
+    if block_table.dim() != 2 or block_table.shape[0] != B or tuple(context_lens.shape) != (B,):
+        raise ValueError("block_table must be [B, max_pages] and context_lens [B]")
+    if scale is None:
+        scale = 1.0 / math.sqrt(D)
+    shape = make_shape(query.shape, key_pages.shape, block_table.shape[1])
+    device = query.device
+    raw, guard = _on_device(device, stream, (
+        ("key_pages", key_pages), ("value_pages", value_pages), ("block_table", block_table),
+        ("context_lens", context_lens), ("out", out), ("workspace", workspace)) + more)
+    ptrs = (_dev_ptr(query, torch.bfloat16, "query"), _dev_ptr(key_pages, pool_dtype, "key_pages"),
+            _dev_ptr(value_pages, pool_dtype, "value_pages"))
+    tables = (_dev_ptr(block_table, torch.int32, "block_table"),
+              _dev_ptr(context_lens, torch.int32, "context_lens"))
+    if out is None:
+        out = torch.empty_like(query)
+        _keep_for(out, stream)
+    elif out.shape != query.shape:
+        raise ValueError("out must have the query's shape")
+    return shape, ptrs, tables, float(scale), out, _dev_ptr(out, torch.bfloat16, "out"), raw, guard
+
+
+def _sized(fn, guard, *args) -> int:
+    """A workspace size, asked of the library with the call's device current."""
+    if guard is None:
+        return int(fn(*args))
+    with guard:
+        return int(fn(*args))
+
+
+def _window(what, query, key_pages, value_pages, block_table, context_lens, page_size, scales,
+            window, sinks, scale, out, max_context_len, workspace, stream, size):
+    shape, ptrs, tables, scale, out, out_ptr, raw, guard = _paged(
+        query, key_pages, value_pages, block_table, context_lens, page_size, scale, out, workspace,
+        torch.uint8 if scales else torch.bfloat16, stream)
+    if workspace is None:
+        workspace = _scratch(size(shape, guard), query.device, stream)
+    _launch(getattr(_lib, what), what, guard, *ptrs, *tables, int(page_size), scale, *scales,
+            int(window), int(sinks), out_ptr, shape, int(max_context_len), workspace.data_ptr(),
+            workspace.numel() * workspace.element_size(), raw)
+    return out
+
+
+def pa_decode_window(query: torch.Tensor, key_pages: torch.Tensor, value_pages: torch.Tensor,
+                     block_table: torch.Tensor, context_lens: torch.Tensor, page_size: int,
+                     window: int, sinks: int = 0, scale: Optional[float] = None,
+                     out: Optional[torch.Tensor] = None, max_context_len: int = 0,
+                     workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """pa_decode where the row at position p sees keys j <= p with
+    j > p - window or j < sinks; pages that no row sees are not touched."""
+    return _window("pa_decode_window", query, key_pages, value_pages, block_table, context_lens,
+                   page_size, (), window, sinks, scale, out, max_context_len, workspace, stream,
+                   lambda shape, guard: _sized(_lib.pa_decode_workspace_bytes, guard, shape))
+
+
+def pa_decode_window_fp8(query, key_pages, value_pages, block_table, context_lens, page_size: int,
+                         k_scale: float, v_scale: float, window: int, sinks: int = 0,
+                         scale: Optional[float] = None, out=None, max_context_len: int = 0,
+                         workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """pa_decode_window over uint8 e4m3 pools."""
+    return _window("pa_decode_window_fp8", query, key_pages, value_pages, block_table,
+                   context_lens, page_size, (float(k_scale), float(v_scale)), window, sinks, scale,
+                   out, max_context_len, workspace, stream,
+                   lambda shape, guard: _sized(_lib.pa_decode_workspace_bytes, guard, shape))
+
+
+def pa_decode_weights_workspace_bytes(shape: pa_shape, max_context_len: int,
+                                      device: Optional[torch.device] = None) -> int:
+    with torch.cuda.device(device if device is not None else torch.cuda.current_device()):
+        return int(_lib.pa_decode_weights_workspace_bytes(shape, int(max_context_len)))
+
+
+def _weights(what, query, key_pages, value_pages, weight_pages, block_table, context_lens,
+             page_size, scales, max_context_len, decay, scale, causal, out, workspace, stream):
+    if tuple(weight_pages.shape) != tuple(key_pages.shape[:3]):
+        raise ValueError("weight_pages must be [P, H_kv, page_size]")
+    shape, ptrs, tables, scale, out, out_ptr, raw, guard = _paged(
+        query, key_pages, value_pages, block_table, context_lens, page_size, scale, out, workspace,
+        torch.uint8 if scales else torch.bfloat16, stream, (("weight_pages", weight_pages),))
+    if workspace is None:
+        workspace = _scratch(_sized(_lib.pa_decode_weights_workspace_bytes, guard, shape,
+                                    int(max_context_len)), query.device, stream)
+    _launch(getattr(_lib, what), what, guard, *ptrs,
+            _dev_ptr(weight_pages, torch.float32, "weight_pages"), *tables, int(page_size), scale,
+            *scales, int(bool(causal)), float(decay), out_ptr, shape, int(max_context_len),
+            workspace.data_ptr(), workspace.numel() * workspace.element_size(), raw)
+    return out
+
+
+def pa_decode_weights(query: torch.Tensor, key_pages: torch.Tensor, value_pages: torch.Tensor,
+                      weight_pages: torch.Tensor, block_table: torch.Tensor,
+                      context_lens: torch.Tensor, page_size: int, max_context_len: int,
+                      decay: float = 1.0, scale: Optional[float] = None, causal: bool = True,
+                      out: Optional[torch.Tensor] = None,
+                      workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """pa_decode that also updates weight_pages [P, H_kv, page_size] fp32:
+    every slot's weight becomes decay * old + the attention weight its position
+    got, summed over the group's heads and the rows (old: 0 for the L newest
+    positions, and everywhere when decay is 0). max_context_len bounds
+    context_lens."""
+    return _weights("pa_decode_weights", query, key_pages, value_pages, weight_pages, block_table,
+                    context_lens, page_size, (), max_context_len, decay, scale, causal, out,
+                    workspace, stream)
+
+
+def pa_decode_weights_fp8(query, key_pages, value_pages, weight_pages, block_table, context_lens,
+                          page_size: int, k_scale: float, v_scale: float, max_context_len: int,
+                          decay: float = 1.0, scale: Optional[float] = None, causal: bool = True,
+                          out=None, workspace: Optional[torch.Tensor] = None,
+                          stream=None) -> torch.Tensor:
+    """pa_decode_weights over uint8 e4m3 pools."""
+    return _weights("pa_decode_weights_fp8", query, key_pages, value_pages, weight_pages,
+                    block_table, context_lens, page_size, (float(k_scale), float(v_scale)),
+                    max_context_len, decay, scale, causal, out, workspace, stream)
 
 
 def pa_decode_fp8(query, key_pages, value_pages, block_table, context_lens, page_size: int,

@@ -417,6 +417,16 @@ DecodePlan decode_plan(const pa_shape& s, bool fp8)
 
 namespace {
 
+// What a split-KV call does beyond full attention.
+struct DecodeExtra {
+    DecodeMode mode = kFull;
+    int32_t window = 0, sinks = 0;   // kWindow
+    float* scores = nullptr;         // kScores
+    float2* row_state = nullptr;
+    int64_t score_stride = 0;
+    int32_t score_cap = 0;
+};
+
 // Runs the split-KV kernel. whole_segments = 1 gives every block whole
 // segments (no partial states, no workspace).
 pa_status run_split_kv(const void* query, const void* key_pages, const void* value_pages,
@@ -424,7 +434,8 @@ pa_status run_split_kv(const void* query, const void* key_pages, const void* val
                        int32_t page_size, float scale, int causal, void* out,
                        const pa_shape& s, int32_t max_context_len, void* workspace,
                        size_t workspace_bytes, int whole_segments, cudaStream_t stream,
-                       int dense = 0, int fp8 = 0, float k_scale = 1.f, float v_scale = 1.f)
+                       int dense = 0, int fp8 = 0, float k_scale = 1.f, float v_scale = 1.f,
+                       const DecodeExtra& extra = DecodeExtra())
 {
     DeviceInfo* dev;
     pa_status st = device_info(&dev);
@@ -445,7 +456,14 @@ pa_status run_split_kv(const void* query, const void* key_pages, const void* val
     if (whole_segments) {
         grid = nseg < grid_max ? nseg : grid_max;
     } else if (max_context_len > 0) {
-        const int64_t gran = (int64_t(max_context_len) + kDecodeTokens - 1) / kDecodeTokens;
+        int64_t gran = (int64_t(max_context_len) + kDecodeTokens - 1) / kDecodeTokens;
+        if (extra.mode == kWindow) {
+            // a sliding window's two runs of keys, the second from a page border
+            const int64_t runs =
+                (int64_t(extra.sinks) + kDecodeTokens - 1) / kDecodeTokens +
+                (int64_t(extra.window) + s.q_len + 2 * kDecodeTokens - 3) / kDecodeTokens;
+            gran = std::min(gran, runs);
+        }
         const int64_t bound = nseg * (gran > 0 ? gran : 1);
         if (bound < grid)
             grid = bound;
@@ -494,6 +512,13 @@ pa_status run_split_kv(const void* query, const void* key_pages, const void* val
     a.causal = causal ? 1 : 0;
     a.fp8 = fp8 ? 1 : 0;
     a.v_scale = fp8 ? v_scale : 1.f;
+    a.mode = extra.mode;
+    a.window = extra.window;
+    a.sinks = extra.sinks;
+    a.scores = extra.scores;
+    a.row_state = extra.row_state;
+    a.score_stride = extra.score_stride;
+    a.score_cap = extra.score_cap;
     a.debug_unset_wait = t_arm_unset_wait ? 1 : 0;
     t_arm_unset_wait = false;
     CUtensorMap qmap;
@@ -1035,6 +1060,188 @@ pa_status pa_decode(const void* query, const void* key_pages, const void* value_
     return run_split_kv(query, key_pages, value_pages, block_table, context_lens, page_size,
                         scale, causal, out, shape, max_context_len, workspace, workspace_bytes,
                         0, static_cast<cudaStream_t>(stream));
+}
+
+namespace {
+
+bool bad_scales(float k_scale, float v_scale)
+{
+    return !(k_scale > 0.f) || !isfinite(k_scale) || !(v_scale > 0.f) || !isfinite(v_scale);
+}
+
+// Checks of a sliding window, and the window cut to what positions can reach.
+pa_status check_window(int32_t window, int32_t sinks, int32_t* cut)
+{
+    if (window <= 0 || sinks < 0)
+        return PA_ERR_INVALID_ARG;
+    *cut = std::min(window, 1 << 30);
+    return PA_OK;
+}
+
+pa_status run_decode_window(const void* query, const void* key_pages, const void* value_pages,
+                            const int32_t* block_table, const int32_t* context_lens,
+                            int32_t page_size, float scale, int fp8, float k_scale, float v_scale,
+                            int32_t window, int32_t sinks, void* out, const pa_shape& shape,
+                            int32_t max_context_len, void* workspace, size_t workspace_bytes,
+                            void* stream)
+{
+    pa_status st = check_attention(query, key_pages, value_pages, block_table, context_lens,
+                                   page_size, scale, out, shape);
+    if (st != PA_OK)
+        return st;
+    DecodeExtra extra;
+    extra.mode = kWindow;
+    if ((st = check_window(window, sinks, &extra.window)) != PA_OK)
+        return st;
+    extra.sinks = std::min(sinks, 1 << 30);
+    if (fp8 && bad_scales(k_scale, v_scale))
+        return PA_ERR_INVALID_ARG;
+    if (fp8 && shape.head_dim != 128)
+        return PA_ERR_UNSUPPORTED;
+    return run_split_kv(query, key_pages, value_pages, block_table, context_lens, page_size, scale,
+                        1, out, shape, max_context_len, workspace, workspace_bytes, 0,
+                        static_cast<cudaStream_t>(stream), 0, fp8, k_scale, v_scale, extra);
+}
+
+// Workspace of a weight-accumulating decode: the decode's, then the scores of
+// every row (score_stride columns), then the row states.
+struct WeightPlan {
+    size_t score_off = 0, state_off = 0, total = 0;
+    int64_t stride = 0;
+};
+
+pa_status plan_weights(const pa_shape& s, int32_t max_context_len, WeightPlan* p)
+{
+    if (max_context_len <= 0)
+        return PA_ERR_INVALID_ARG;
+    const size_t decode = pa_decode_workspace_bytes(s);
+    if (decode == 0)
+        return PA_ERR_UNSUPPORTED;
+    p->stride = (int64_t(max_context_len) + 63) / 64 * 64;
+    const int64_t rows = int64_t(s.batch) * s.num_q_heads * s.q_len;
+    if (max_context_len > (1 << 30) || rows >= (int64_t(1) << 31) ||
+        rows * p->stride >= (int64_t(1) << 38))
+        return PA_ERR_UNSUPPORTED;
+    p->score_off = (decode + 255) & ~size_t(255);
+    p->state_off = p->score_off + size_t(rows) * size_t(p->stride) * sizeof(float);
+    p->total = p->state_off + size_t(rows) * sizeof(float2);
+    return PA_OK;
+}
+
+pa_status run_decode_weights(const void* query, const void* key_pages, const void* value_pages,
+                             float* weight_pages, const int32_t* block_table,
+                             const int32_t* context_lens, int32_t page_size, float scale, int fp8,
+                             float k_scale, float v_scale, int causal, float decay, void* out,
+                             const pa_shape& shape, int32_t max_context_len, void* workspace,
+                             size_t workspace_bytes, void* stream)
+{
+    pa_status st = check_attention(query, key_pages, value_pages, block_table, context_lens,
+                                   page_size, scale, out, shape);
+    if (st != PA_OK)
+        return st;
+    if (!weight_pages || (reinterpret_cast<uintptr_t>(weight_pages) & 3u) != 0 ||
+        !(decay >= 0.f) || !isfinite(decay) || max_context_len <= 0)
+        return PA_ERR_INVALID_ARG;
+    if (fp8 && bad_scales(k_scale, v_scale))
+        return PA_ERR_INVALID_ARG;
+    if (fp8 && shape.head_dim != 128)
+        return PA_ERR_UNSUPPORTED;
+    DeviceInfo* dev;
+    if ((st = device_info(&dev)) != PA_OK)
+        return st;
+    WeightPlan p;
+    if ((st = plan_weights(shape, max_context_len, &p)) != PA_OK)
+        return st;
+    if (!workspace || workspace_bytes < p.total || (reinterpret_cast<uintptr_t>(workspace) & 15u))
+        return PA_ERR_WORKSPACE;
+    uint8_t* w = static_cast<uint8_t*>(workspace);
+    DecodeExtra extra;
+    extra.mode = kScores;
+    extra.scores = reinterpret_cast<float*>(w + p.score_off);
+    extra.row_state = reinterpret_cast<float2*>(w + p.state_off);
+    extra.score_stride = p.stride;
+    extra.score_cap = max_context_len;
+    WeightArgs a;
+    memset(&a, 0, sizeof a);
+    a.scores = extra.scores;
+    a.row_state = extra.row_state;
+    a.weight_pages = weight_pages;
+    a.block_table = block_table;
+    a.context_lens = context_lens;
+    a.err = dev->err;
+    a.score_stride = p.stride;
+    a.B = shape.batch;
+    a.H_kv = shape.num_kv_heads;
+    a.R = int32_t(int64_t(shape.num_q_heads / shape.num_kv_heads) * shape.q_len);
+    a.L = shape.q_len;
+    while ((1 << a.ps_shift) < page_size)
+        ++a.ps_shift;
+    a.max_pages = shape.max_pages;
+    a.num_pages = shape.num_pages;
+    a.score_cap = max_context_len;
+    a.decay = decay;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    st = run_split_kv(query, key_pages, value_pages, block_table, context_lens, page_size, scale,
+                      causal, out, shape, max_context_len, workspace, p.score_off, 0, s, 0, fp8,
+                      k_scale, v_scale, extra);
+    if (st != PA_OK)
+        return st;
+    return launch_accumulate_weights(a, s) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+}  // namespace
+
+pa_status pa_decode_window(const void* query, const void* key_pages, const void* value_pages,
+                           const int32_t* block_table, const int32_t* context_lens,
+                           int32_t page_size, float scale, int32_t window, int32_t sinks, void* out,
+                           pa_shape shape, int32_t max_context_len, void* workspace,
+                           size_t workspace_bytes, void* stream)
+{
+    return run_decode_window(query, key_pages, value_pages, block_table, context_lens, page_size,
+                             scale, 0, 1.f, 1.f, window, sinks, out, shape, max_context_len,
+                             workspace, workspace_bytes, stream);
+}
+
+pa_status pa_decode_window_fp8(const void* query, const void* key_pages, const void* value_pages,
+                               const int32_t* block_table, const int32_t* context_lens,
+                               int32_t page_size, float scale, float k_scale, float v_scale,
+                               int32_t window, int32_t sinks, void* out, pa_shape shape,
+                               int32_t max_context_len, void* workspace, size_t workspace_bytes,
+                               void* stream)
+{
+    return run_decode_window(query, key_pages, value_pages, block_table, context_lens, page_size,
+                             scale, 1, k_scale, v_scale, window, sinks, out, shape,
+                             max_context_len, workspace, workspace_bytes, stream);
+}
+
+size_t pa_decode_weights_workspace_bytes(pa_shape shape, int32_t max_context_len)
+{
+    WeightPlan p;
+    return plan_weights(shape, max_context_len, &p) == PA_OK ? p.total : 0;
+}
+
+pa_status pa_decode_weights(const void* query, const void* key_pages, const void* value_pages,
+                            float* weight_pages, const int32_t* block_table,
+                            const int32_t* context_lens, int32_t page_size, float scale,
+                            int causal, float decay, void* out, pa_shape shape,
+                            int32_t max_context_len, void* workspace, size_t workspace_bytes,
+                            void* stream)
+{
+    return run_decode_weights(query, key_pages, value_pages, weight_pages, block_table,
+                              context_lens, page_size, scale, 0, 1.f, 1.f, causal, decay, out,
+                              shape, max_context_len, workspace, workspace_bytes, stream);
+}
+
+pa_status pa_decode_weights_fp8(const void* query, const void* key_pages, const void* value_pages,
+                                float* weight_pages, const int32_t* block_table,
+                                const int32_t* context_lens, int32_t page_size, float scale,
+                                float k_scale, float v_scale, int causal, float decay, void* out,
+                                pa_shape shape, int32_t max_context_len, void* workspace,
+                                size_t workspace_bytes, void* stream)
+{
+    return run_decode_weights(query, key_pages, value_pages, weight_pages, block_table,
+                              context_lens, page_size, scale, 1, k_scale, v_scale, causal, decay,
+                              out, shape, max_context_len, workspace, workspace_bytes, stream);
 }
 
 pa_status pa_gather_kv(const void* key_pages, const void* value_pages, const int32_t* block_table,

@@ -98,6 +98,68 @@ __device__ __forceinline__ int clamp_context(int n, int cap, unsigned* err)
     return n;
 }
 
+// Longest context: what the block table holds, and with kScores the rows of
+// scores too.
+template <int kMode>
+__device__ __forceinline__ int context_cap(const DecodeArgs& a)
+{
+    const int cap = a.max_pages * a.ps;
+    return kMode == kScores ? min(cap, a.score_cap) : cap;
+}
+
+// The keys that a segment of a request of n tokens visits, as granules of
+// kDecodeTokens tokens. kWindow (a sliding window of `window` keys, and the
+// first `sinks`): the granules of [0, sinks), then those from `start`, the
+// first key that some row sees through the window (first_seen) rounded down to
+// a page (or to 64 tokens within a larger page), so that no page is touched
+// that no row sees; one run from 0 where the two would meet. Row i sits at
+// position n - L + i. Otherwise one run of all n keys.
+struct Span {
+    int sink_granules;   // granules of the first run
+    int start;           // first token of the second run
+    int first_seen;      // first token that some row sees through the window
+    int granules;        // of both runs, at least 1
+};
+template <int kMode>
+__device__ __forceinline__ Span span_of(const DecodeArgs& a, int n)
+{
+    Span s;
+    s.sink_granules = 0;
+    s.start = 0;
+    s.first_seen = 0;
+    if constexpr (kMode == kWindow) {
+        s.first_seen = int(max(int64_t(0), int64_t(n) - a.L - a.window + 1));
+        const int start = s.first_seen & ~(a.box_rows - 1);
+        if (start > a.sinks) {
+            s.sink_granules = (a.sinks + kDecodeTokens - 1) / kDecodeTokens;
+            s.start = start;
+        }
+    }
+    s.granules = max(1, s.sink_granules + (n - s.start + kDecodeTokens - 1) / kDecodeTokens);
+    return s;
+}
+// First token of granule g, and the end of its run of keys.
+template <int kMode>
+__device__ __forceinline__ int2 granule_tokens(const DecodeArgs& a, const Span& s, int g, int n)
+{
+    if constexpr (kMode == kWindow) {
+        if (g < s.sink_granules)
+            return make_int2(g * kDecodeTokens, a.sinks);
+        return make_int2(s.start + (g - s.sink_granules) * kDecodeTokens, n);
+    }
+    return make_int2(g * kDecodeTokens, n);
+}
+
+// Whether a key of its run that is no later than the row's position lies
+// behind the row's window (low: the window's first key) and past the sinks.
+template <int kMode>
+__device__ __forceinline__ bool hidden(const DecodeArgs& a, int tok, int low, bool first_run)
+{
+    if constexpr (kMode == kWindow)
+        return tok >= a.sinks && (first_run || tok < low);
+    return false;
+}
+
 struct SegmentPos {
     int b, h, ms, seg;  // request, KV head, segment within the (b, h) rows
     int64_t seg_start;  // first granule of the segment in the stream
@@ -199,7 +261,9 @@ __device__ __forceinline__ void granules_at_units(const int32_t* pre, const int3
     finish(lo1, u1, p1);
 }
 
-template <int D, bool F8 = false, int TG = 1>
+// kMode: kFull, kWindow (Span above), or kScores (the scores of every row and
+// the row states go to the workspace too, for the accumulation of weights).
+template <int D, bool F8 = false, int TG = 1, int kMode = kFull>
 __global__ void __launch_bounds__(kThreads, 2)
     decode_kernel(const __grid_constant__ CUtensorMap key_map,
                   const __grid_constant__ CUtensorMap value_map,
@@ -223,7 +287,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
     const int per_req = a.H_kv * a.MS;
-    const int cap = a.max_pages * a.ps;
+    const int cap = context_cap<kMode>(a);
 
     // Set-up that reads no input runs before the wait below, overlapping the
     // tail of the previous kernel in the stream: the pipeline barriers and
@@ -280,7 +344,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                 if (b < a.B) {
                     const int n =
                         real ? clamp_context(a.context_lens[b], cap, a.err) : 64 * kDecodeTokens;
-                    const int gs = max(1, (n + kDecodeTokens - 1) / kDecodeTokens);
+                    const int gs = span_of<kMode>(a, n).granules;
                     gbr[b] = gs;
                     g = gs * per_req;
                 }
@@ -394,14 +458,28 @@ __global__ void __launch_bounds__(kThreads, 2)
                 if (w + 32 + lane < a.max_pages)
                     e1 = __ldg(bt + w + 32 + lane);
             };
-            int wb = a.dense ? 0 : (int((x - sp.seg_start) * kDecodeTokens) >> ps_shift) & ~63;
+            const Span span = span_of<kMode>(a, n);
+            // Windows count from the first page of the run of keys (page 0
+            // except in the second run of a sliding window).
+            int w0 = 0, wb = 0;
+            bool second = false;
             int c0, c1, n0, n1;
-            load_window(wb, c0, c1);
-            load_window(wb + 64, n0, n1);
+            auto seek = [&](int g) {       // windows for granule g and on
+                if constexpr (kMode == kWindow) {
+                    second = g >= span.sink_granules;
+                    w0 = second ? span.start >> ps_shift : 0;
+                }
+                const int lp = granule_tokens<kMode>(a, span, g, n).x >> ps_shift;
+                wb = a.dense ? 0 : w0 + ((lp - w0) & ~63);
+                load_window(wb, c0, c1);
+                load_window(wb + 64, n0, n1);
+            };
+            seek(int(x - sp.seg_start));
             // The TMA row of each box of granule xx (boxes lane and lane + 32).
             auto translate = [&](int64_t xx, int& nbox, int& ra, int& rb) {
-                const int t0 = int(xx - sp.seg_start) * kDecodeTokens;
-                const int nvalid = min(kDecodeTokens, n - t0);
+                const int2 tk = granule_tokens<kMode>(a, span, int(xx - sp.seg_start), n);
+                const int t0 = tk.x;
+                const int nvalid = min(kDecodeTokens, tk.y - t0);
                 ra = rb = 0;
                 if (a.dense) {
                     // one page per request holding the whole context (t < n <= ps)
@@ -415,6 +493,10 @@ __global__ void __launch_bounds__(kThreads, 2)
                 }
                 nbox = nvalid > 0 ? (nvalid + box - 1) >> box_shift : 0;
                 const int lp0 = t0 >> ps_shift;
+                if constexpr (kMode == kWindow) {
+                    if (!second && int(xx - sp.seg_start) >= span.sink_granules)
+                        seek(int(xx - sp.seg_start));
+                }
                 while (lp0 >= wb + 64) {     // warp-uniform: move to the next window
                     wb += 64;
                     c0 = n0;
@@ -537,6 +619,22 @@ __global__ void __launch_bounds__(kThreads, 2)
         return (int64_t(p.b) * a.H_q + p.h * a.G + g) * a.L + i;
     };
 
+    // kScores: two neighbouring scores of fragment row rw (log2 domain, -inf
+    // where hidden) to row rg of the (request, KV head)'s rows of score_stride;
+    // and the row's final (max, sum).
+    auto store_scores = [&](const SegmentPos& p, int rw, int tok, float s0, float s1) {
+        const int rg = tile_row(p, rw);
+        if (rg < a.R)
+            *reinterpret_cast<float2*>(a.scores +
+                                       ((int64_t(p.b) * a.H_kv + p.h) * a.R + rg) * a.score_stride + tok) =
+                make_float2(s0 * a.scale_log2, s1 * a.scale_log2);
+    };
+    auto store_state = [&](const SegmentPos& p, int rw, float m, float l) {
+        const int rg = tile_row(p, rw);
+        if (rg < a.R)
+            a.row_state[(int64_t(p.b) * a.H_kv + p.h) * a.R + rg] = make_float2(m, l);
+    };
+
     if constexpr (F8) {
         // ---- e4m3 pages: warp w owns tokens [16 w, 16 w + 16) of every granule.
         // It reads their codes straight from the stage (ldmatrix on the byte
@@ -581,6 +679,11 @@ __global__ void __launch_bounds__(kThreads, 2)
                 lim[rr] = a.causal ? min(n - a.L + i, n - 1) : n - 1;
             }
             const int lim_min = __reduce_min_sync(0xffffffffu, min(lim[0], lim[1]));
+            const Span span = span_of<kMode>(a, n);
+            const int low[2] = {lim[0] - a.window + 1, lim[1] - a.window + 1};
+            const int low_max = kMode == kWindow
+                                    ? __reduce_max_sync(0xffffffffu, max(low[0], low[1]))
+                                    : 0;
             float m_run[2] = {-INFINITY, -INFINITY};
             float l_run[2] = {0.f, 0.f};
             float o[kONF][4];
@@ -589,8 +692,9 @@ __global__ void __launch_bounds__(kThreads, 2)
                 o[nt][0] = o[nt][1] = o[nt][2] = o[nt][3] = 0.f;
 
             for (; x < piece_end; ++x) {
-                const int t0 = int(x - sp.seg_start) * kDecodeTokens;
-                const int nvalid = min(kDecodeTokens, n - t0);
+                const int2 tk = granule_tokens<kMode>(a, span, int(x - sp.seg_start), n);
+                const int t0 = tk.x;
+                const int nvalid = min(kDecodeTokens, tk.y - t0);
                 const bool ok = mbar_wait_warp(&full[stage], phase, misc, a.err);
                 if (need_q) {
                     const uint8_t* qs = smem + Lay::kQ + stage * Lay::kQStageBytes;
@@ -611,6 +715,21 @@ __global__ void __launch_bounds__(kThreads, 2)
                     need_q = false;
                 }
                 const bool live = ok && nvalid > r_lo;
+                if constexpr (kMode == kWindow) {
+                    // V rows between the first keys and the window: no row sees
+                    // them, whatever they hold
+                    const int d0 = max(a.sinks - t0, r_lo);
+                    const int d1 = min(min(span.first_seen - t0, nvalid), r_lo + kWT);
+                    if (live && d0 < d1) {
+                        for (int idx = lane; idx < (d1 - d0) * 8; idx += 32) {
+                            const int r = d0 + idx / 8, c = idx % 8;
+                            *reinterpret_cast<uint4*>(v_half(stage, 0) + r * 128 + ((c ^ (r & swz)) << 4)) =
+                                make_uint4(0, 0, 0, 0);
+                        }
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                    }
+                }
                 if (live && nvalid < r_lo + kWT) {
                     // V rows of this warp past the context hold stale codes
                     // (NaN among them): zero them (P is 0 there, 0 * NaN is not)
@@ -647,15 +766,24 @@ __global__ void __launch_bounds__(kThreads, 2)
                                               e4m3x2_hi_to_f16x2(r4[u]));
                         }
                     }
-                    if (t0 + r_lo + kWT - 1 > lim_min) {
+                    if (t0 + r_lo + kWT - 1 > lim_min || (kMode == kWindow && t0 + r_lo < low_max)) {
+                        const bool first_run = int(x - sp.seg_start) < span.sink_granules;
 #pragma unroll
                         for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
                             for (int j = 0; j < 4; ++j) {
                                 const int tok = t0 + r_lo + nt * 8 + 2 * quad + (j & 1);
-                                if (tok > lim[j >> 1])
+                                if (tok > lim[j >> 1] || hidden<kMode>(a, tok, low[j >> 1], first_run))
                                     sc[nt][j] = -INFINITY;
                             }
+                    }
+                    if constexpr (kMode == kScores) {
+#pragma unroll
+                        for (int rr = 0; rr < 2; ++rr)
+#pragma unroll
+                            for (int nt = 0; nt < 2; ++nt)
+                                store_scores(sp, row0 + rr * 8, t0 + r_lo + nt * 8 + 2 * quad,
+                                             sc[nt][2 * rr], sc[nt][2 * rr + 1]);
                     }
                     float mx[2], mu[2], mn[2];
                     bool changed = false;
@@ -801,6 +929,10 @@ __global__ void __launch_bounds__(kThreads, 2)
                     const int64_t orow = out_row(sp, row0 + rr * 8);
                     if (orow < 0)
                         continue;
+                    if constexpr (kMode == kScores) {
+                        if (warp == 0 && quad == 0)
+                            store_state(sp, row0 + rr * 8, Mr[rr], Lr[rr]);
+                    }
                     const float inv = Lr[rr] > 0.f ? a.v_scale / Lr[rr] : 0.f;
                     uint16_t* dst = a.out + orow * D + col0 + 2 * quad;
 #pragma unroll
@@ -850,6 +982,10 @@ __global__ void __launch_bounds__(kThreads, 2)
             lim[rr] = a.causal ? min(n - a.L + i, n - 1) : n - 1;
         }
         const int lim_min = __reduce_min_sync(0xffffffffu, min(lim[0], lim[1]));
+        const Span span = span_of<kMode>(a, n);
+        const int low[2] = {lim[0] - a.window + 1, lim[1] - a.window + 1};
+        const int low_max =
+            kMode == kWindow ? __reduce_max_sync(0xffffffffu, max(low[0], low[1])) : 0;
 
         float m_run[2] = {-INFINITY, -INFINITY};
         float l_run[2] = {0.f, 0.f};
@@ -859,8 +995,9 @@ __global__ void __launch_bounds__(kThreads, 2)
             o[nt][0] = o[nt][1] = o[nt][2] = o[nt][3] = 0.f;
 
         for (; x < piece_end; ++x) {
-            const int t0 = int(x - sp.seg_start) * kDecodeTokens;
-            const int nvalid = min(kDecodeTokens, n - t0);
+            const int2 tk = granule_tokens<kMode>(a, span, int(x - sp.seg_start), n);
+            const int t0 = tk.x;
+            const int nvalid = min(kDecodeTokens, tk.y - t0);
             const bool ok = mbar_wait_warp(&full[stage], phase, misc, a.err);
             if (need_q) {
                 const uint8_t* qs = smem + Lay::kQ + stage * Lay::kQStageBytes +
@@ -876,6 +1013,30 @@ __global__ void __launch_bounds__(kThreads, 2)
                 need_q = false;
             }
             bool wrote = false;
+            if constexpr (kMode == kWindow) {
+                // V rows between the first keys and the window: no row sees
+                // them, whatever they hold. As below, the warps of one tile
+                // zero their own columns, those of several meet at a barrier.
+                const int d0 = max(a.sinks - t0, 0), d1 = min(span.first_seen - t0, nvalid);
+                if (d0 < d1) {
+                    constexpr int kChunks = (TG == 1 ? kCols : D) / 8;
+                    if (ok) {
+                        for (int idx = TG == 1 ? lane : int(threadIdx.x); idx < (d1 - d0) * kChunks;
+                             idx += TG == 1 ? 32 : kConsumerThreads) {
+                            const int r = d0 + idx / kChunks;
+                            const int ch = (TG == 1 ? col0 / 8 : 0) + idx % kChunks;
+                            *reinterpret_cast<uint4*>(v_half(stage, ch >> 3) + r * 128 +
+                                                      (((ch & 7) ^ (r & swz)) << 4)) =
+                                make_uint4(0, 0, 0, 0);
+                        }
+                        wrote = true;
+                    }
+                    if constexpr (TG == 1)
+                        __syncwarp();
+                    else
+                        named_barrier_sync(1, kConsumerThreads);
+                }
+            }
             if (nvalid > 0 && nvalid < kDecodeTokens) {
                 // Zero the V rows past the context: P is 0 there, but 0 * NaN
                 // is not. One row tile per segment: each warp zeroes its own
@@ -938,14 +1099,27 @@ __global__ void __launch_bounds__(kThreads, 2)
                 }
                 // Mask (select to -inf, never multiply) only where some row's
                 // last visible position falls inside this granule.
-                if (t0 + kDecodeTokens - 1 > lim_min) {
+                if (t0 + kDecodeTokens - 1 > lim_min || (kMode == kWindow && t0 < low_max)) {
+                    const bool first_run = int(x - sp.seg_start) < span.sink_granules;
 #pragma unroll
                     for (int nt = 0; nt < kSN; ++nt)
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
                             const int tok = t0 + nt * 8 + 2 * quad + (j & 1);
-                            if (tok > lim[j >> 1])
+                            if (tok > lim[j >> 1] || hidden<kMode>(a, tok, low[j >> 1], first_run))
                                 sc[nt][j] = -INFINITY;
+                        }
+                }
+                if constexpr (kMode == kScores) {
+                    // The warps of a tile hold the same scores: each stores its
+                    // share of the granule's token columns.
+#pragma unroll
+                    for (int nt = 0; nt < kSN; ++nt)
+                        if (nt / (kSN / kWPT) == warp % kWPT) {
+#pragma unroll
+                            for (int rr = 0; rr < 2; ++rr)
+                                store_scores(sp, row0 + rr * 8, t0 + nt * 8 + 2 * quad, sc[nt][2 * rr],
+                                             sc[nt][2 * rr + 1]);
                         }
                 }
                 // Online softmax in the log2 domain: m_run is kept scaled
@@ -1048,6 +1222,10 @@ __global__ void __launch_bounds__(kThreads, 2)
                 const int64_t orow = out_row(sp, row0 + rr * 8);
                 if (orow < 0)
                     continue;
+                if constexpr (kMode == kScores) {
+                    if (warp % kWPT == 0 && quad == 0)
+                        store_state(sp, row0 + rr * 8, m_run[rr], l_run[rr]);
+                }
                 const float inv = l_run[rr] > 0.f ? 1.f / l_run[rr] : 0.f;
                 uint16_t* dst = a.out + orow * D + col0 + 2 * quad;
 #pragma unroll
@@ -1089,7 +1267,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 // o = sum acc_k 2^(m_k - M) / l, as one running pass over the pieces with
 // up to eight of them in flight.
 constexpr int kMergeThreads = 256;
-template <int D>
+template <int D, int kMode = kFull>
 __global__ void __launch_bounds__(kMergeThreads) decode_merge_kernel(const DecodeArgs a, int decode_grid)
 {
     constexpr int kTileFloats = kDecodeRows * (D + 2);
@@ -1105,11 +1283,11 @@ __global__ void __launch_bounds__(kMergeThreads) decode_merge_kernel(const Decod
     const int seg = blockIdx.x;
     const int per_req = a.H_kv * a.MS;
     const int b = seg / per_req, hm = seg - b * per_req;
-    const int cap = a.max_pages * a.ps;
+    const int cap = context_cap<kMode>(a);
     auto granules = [&](int q) {
         int n = a.context_lens[q];
         n = n < 0 ? 0 : (n > cap ? cap : n);
-        return max(1, (n + kDecodeTokens - 1) / kDecodeTokens);
+        return span_of<kMode>(a, n).granules;
     };
     long long before = 0, total = 0;
     for (int q = tid; q < a.B; q += blockDim.x) {
@@ -1141,9 +1319,12 @@ __global__ void __launch_bounds__(kMergeThreads) decode_merge_kernel(const Decod
     const int64_t u0 = seg_start + int64_t(a.piece_units) * (seg + 1);
     const int64_t first = block_of_unit(u0, units, grid);
     const int64_t last = block_of_unit(u0 + gb - 1, units, grid);
+    // The decode grid has completed: its partials are visible. (Every block
+    // waits, so that this grid does not end before the one it follows and a
+    // kernel that waits for this one has waited for both.)
+    grid_dependency_wait();
     if (first == last)
         return;  // finished and written by one decode block
-    grid_dependency_wait();  // the decode grid has completed: its partials are visible
 
     const int r = tid >> 4;
     const int c0 = (tid & 15) * kCols;
@@ -1196,6 +1377,10 @@ __global__ void __launch_bounds__(kMergeThreads) decode_merge_kernel(const Decod
                 }
             }
         }
+        if constexpr (kMode == kScores) {
+            if (c0 == 0)
+                a.row_state[(int64_t(b) * a.H_kv + h) * a.R + rg] = make_float2(Mx, L2);
+        }
         const float inv = L2 > 0.f ? 1.f / L2 : 0.f;
         uint16_t* dst = a.out + orow * D + c0;
 #pragma unroll
@@ -1233,19 +1418,38 @@ using DecodeKernel = void (*)(CUtensorMap, CUtensorMap, CUtensorMap, DecodeArgs)
 
 // The instantiation for (head_dim, e4m3 pages, row tiles per segment), with
 // its index in the table of raised shared-memory limits.
-DecodeKernel decode_kernel_for(int D, bool fp8, int TG, int* index)
+template <int kMode>
+DecodeKernel decode_kernel_of(int D, bool fp8, int TG, int* index)
 {
     if (fp8) {
         *index = 0;
-        return decode_kernel<128, true>;
+        return decode_kernel<128, true, 1, kMode>;
     }
     const int t = TG == 4 ? 2 : TG == 2 ? 1 : 0;
     *index = 1 + (D == 64 ? 0 : 3) + t;
     if (D == 64)
-        return t == 2 ? decode_kernel<64, false, 4> : t == 1 ? decode_kernel<64, false, 2>
-                                                              : decode_kernel<64>;
-    return t == 2 ? decode_kernel<128, false, 4> : t == 1 ? decode_kernel<128, false, 2>
-                                                           : decode_kernel<128>;
+        return t == 2 ? decode_kernel<64, false, 4, kMode> : t == 1 ? decode_kernel<64, false, 2, kMode>
+                                                                     : decode_kernel<64, false, 1, kMode>;
+    return t == 2 ? decode_kernel<128, false, 4, kMode> : t == 1 ? decode_kernel<128, false, 2, kMode>
+                                                                  : decode_kernel<128, false, 1, kMode>;
+}
+
+DecodeKernel decode_kernel_for(int mode, int D, bool fp8, int TG, int* index)
+{
+    const DecodeKernel k = mode == kWindow   ? decode_kernel_of<kWindow>(D, fp8, TG, index)
+                           : mode == kScores ? decode_kernel_of<kScores>(D, fp8, TG, index)
+                                             : decode_kernel_of<kFull>(D, fp8, TG, index);
+    *index += 7 * mode;
+    return k;
+}
+
+using MergeKernel = void (*)(DecodeArgs, int);
+template <int D>
+MergeKernel merge_kernel_for(int mode)
+{
+    return mode == kWindow   ? decode_merge_kernel<D, kWindow>
+           : mode == kScores ? decode_merge_kernel<D, kScores>
+                             : decode_merge_kernel<D, kFull>;
 }
 
 }  // namespace
@@ -1257,13 +1461,13 @@ cudaError_t launch_decode(const CUtensorMap& key_map, const CUtensorMap& value_m
     // The dynamic shared-memory limit is raised once per (device, kernel)
     // and only grows.
     constexpr int kMaxDev = 64;
-    static std::atomic<int> smem_set[kMaxDev][7];
+    static std::atomic<int> smem_set[kMaxDev][7 * kDecodeModes];
     const bool fp8 = a.fp8 != 0;
     if ((fp8 && (a.D != 128 || a.TG != 1)) || (a.TG != 1 && a.TG != 2 && a.TG != 4))
         return cudaErrorInvalidValue;
     const int smem = int(decode_smem_bytes(a.D, a.B, fp8, a.TG));
     int di = 0;
-    const DecodeKernel kern = decode_kernel_for(a.D, fp8, a.TG, &di);
+    const DecodeKernel kern = decode_kernel_for(a.mode, a.D, fp8, a.TG, &di);
     if (device < 0 || device >= kMaxDev)
         return cudaErrorInvalidDevice;
     if (smem_set[device][di].load(std::memory_order_relaxed) < smem) {
@@ -1295,8 +1499,8 @@ cudaError_t launch_decode(const CUtensorMap& key_map, const CUtensorMap& value_m
     mcfg.gridDim = dim3(unsigned(int64_t(a.B) * a.H_kv * a.MS));
     mcfg.blockDim = dim3(kMergeThreads);
     mcfg.dynamicSmemBytes = 0;
-    return a.D == 64 ? cudaLaunchKernelEx(&mcfg, decode_merge_kernel<64>, ma, grid)
-                     : cudaLaunchKernelEx(&mcfg, decode_merge_kernel<128>, ma, grid);
+    return cudaLaunchKernelEx(&mcfg, a.D == 64 ? merge_kernel_for<64>(a.mode) : merge_kernel_for<128>(a.mode),
+                              ma, grid);
 }
 
 }  // namespace pa

@@ -133,6 +133,10 @@ struct DecodePlan {
 };
 DecodePlan decode_plan(const pa_shape& s, bool fp8);
 
+// What a decode kernel attends to and leaves: everything; a sliding window and
+// the first keys; everything, with the scores and row states kept.
+enum DecodeMode : int { kFull = 0, kWindow = 1, kScores = 2, kDecodeModes = 3 };
+
 struct DecodeArgs {
     const uint16_t* q;            // [B, H_q, L, D]
     uint16_t* out;                // [B, H_q, L, D]
@@ -157,6 +161,13 @@ struct DecodeArgs {
     int32_t causal;
     int32_t fp8;        // 1: K/V pages hold e4m3 codes (head_dim 128)
     float v_scale;      // e4m3 pages: the value scale (1 otherwise)
+    int32_t mode;       // DecodeMode
+    int32_t window;     // kWindow: keys a row sees, its own among them
+    int32_t sinks;      // kWindow: first keys that stay visible
+    float* scores;      // kScores: [B * H_kv][R][score_stride], log2 domain
+    float2* row_state;  // kScores: [B * H_kv][R] (max, sum)
+    int64_t score_stride;      // a multiple of 64, at least score_cap
+    int32_t score_cap;         // kScores: longest context
     int32_t debug_unset_wait;  // test support: block 0 first waits on a barrier
                                // that nothing arrives at (times out, flags)
 };
@@ -167,6 +178,23 @@ size_t decode_workspace_bytes(int64_t nseg, int grid_max, int D, int TG);
 cudaError_t launch_decode(const CUtensorMap& key_map, const CUtensorMap& value_map,
                           const CUtensorMap& q_map, const DecodeArgs& a, int grid, int device,
                           cudaStream_t stream);
+
+// Accumulation of attention weights: weight_pages[slot of j] = decay * old (0
+// for the L newest positions, or where decay is 0) + sum over the R rows of
+// 2^(score - max) / sum.
+struct WeightArgs {
+    const float* scores;          // as in DecodeArgs
+    const float2* row_state;
+    float* weight_pages;          // [P, H_kv, ps]
+    const int32_t* block_table;
+    const int32_t* context_lens;
+    unsigned* err;
+    int64_t score_stride;
+    int32_t B, H_kv, R, L, ps_shift, max_pages, num_pages, score_cap;
+    int32_t chunks;               // set by the launcher: blocks per (request, KV head)
+    float decay;
+};
+cudaError_t launch_accumulate_weights(WeightArgs a, cudaStream_t stream);
 
 // ---------------------------------------------------------------------------
 // Prefill on the 5th-generation tensor cores (D = 128, page_size >= 8)
