@@ -459,6 +459,54 @@ pa_status pa_decode_window_fp8(const void *query, const void *key_pages, const v
                                void *stream);
 
 /*
+ * Prefill with a sliding window and first tokens that stay visible: the rows,
+ * masks and page rules of pa_decode_window on pa_prefill's tensor-core kernel
+ * (two query heads of a KV group per block), each tile of 128 query rows
+ * visiting the tiles of the sinks and those its rows see through the window.
+ * Needs no workspace.
+ */
+pa_status pa_prefill_window(const void *query, const void *key_pages, const void *value_pages,
+                            const int32_t *block_table, const int32_t *context_lens,
+                            int32_t page_size, float scale, int32_t window, int32_t sinks,
+                            void *out, pa_shape shape, void *stream);
+
+/*
+ * The dispatch of the two: pa_decode_window or pa_prefill_window, by
+ * pa_attention_route's rule on the keys a row can reach (the smaller of
+ * max_context_len, where known, and sinks + window + L). The workspace is
+ * needed on the decode route only: pa_attention_window_workspace_bytes bytes (0
+ * also for invalid sizes), 16-byte aligned, any contents.
+ */
+size_t pa_attention_window_workspace_bytes(pa_shape shape, int32_t page_size,
+                                           int32_t max_context_len, int32_t window, int32_t sinks);
+pa_status pa_attention_window(const void *query, const void *key_pages, const void *value_pages,
+                              const int32_t *block_table, const int32_t *context_lens,
+                              int32_t page_size, float scale, int32_t window, int32_t sinks,
+                              void *out, pa_shape shape, int32_t max_context_len, void *workspace,
+                              size_t workspace_bytes, void *stream);
+
+/*
+ * The dispatch for e4m3 pools (head_dim 128): pa_decode_window_fp8 for L <= 8;
+ * otherwise the tokens that some row of the call sees are copied into bf16
+ * pages of 128 tokens in the workspace, exactly, and pa_prefill_window's kernel
+ * attends over the copies (k_scale in the softmax scale, v_scale in the output),
+ * as pa_prefill_fp8 does for full attention. max_context_len bounds
+ * context_lens; on the second route a longer entry records
+ * PA_DEVERR_CONTEXT_LEN and is cut to the next multiple of 128.
+ *   workspace  pa_attention_window_fp8_workspace_bytes bytes (0: invalid
+ *              sizes), 256-byte aligned, any contents.
+ */
+size_t pa_attention_window_fp8_workspace_bytes(pa_shape shape, int32_t page_size,
+                                               int32_t max_context_len, int32_t window,
+                                               int32_t sinks);
+pa_status pa_attention_window_fp8(const void *query, const void *key_pages,
+                                  const void *value_pages, const int32_t *block_table,
+                                  const int32_t *context_lens, int32_t page_size, float scale,
+                                  float k_scale, float v_scale, int32_t window, int32_t sinks,
+                                  void *out, pa_shape shape, int32_t max_context_len,
+                                  void *workspace, size_t workspace_bytes, void *stream);
+
+/*
  * pa_decode that also accumulates the attention weight of every cached slot,
  * for pa_kv_evict. With w[j] = sum of the softmax weights that the G * L rows
  * of a KV group give to position j (a row that sees no key gives none):

@@ -143,6 +143,15 @@ def _load() -> ctypes.CDLL:
     lib.pa_decode_window.restype = ctypes.c_int
     lib.pa_decode_window_fp8.argtypes = tables + [f32, f32, i32, i32] + tail
     lib.pa_decode_window_fp8.restype = ctypes.c_int
+    lib.pa_prefill_window.argtypes = tables + [i32, i32, vp, pa_shape, vp]
+    lib.pa_prefill_window.restype = ctypes.c_int
+    lib.pa_attention_window.argtypes = tables + [i32, i32] + tail
+    lib.pa_attention_window.restype = ctypes.c_int
+    lib.pa_attention_window_fp8.argtypes = tables + [f32, f32, i32, i32] + tail
+    lib.pa_attention_window_fp8.restype = ctypes.c_int
+    for f in (lib.pa_attention_window_workspace_bytes, lib.pa_attention_window_fp8_workspace_bytes):
+        f.argtypes = [pa_shape, i32, i32, i32, i32]
+        f.restype = sz
     lib.pa_decode_weights_workspace_bytes.argtypes = [pa_shape, i32]
     lib.pa_decode_weights_workspace_bytes.restype = sz
     wtables = [vp, vp, vp, vp, vp, vp, i32, f32]
@@ -564,6 +573,68 @@ def pa_decode_window_fp8(query, key_pages, value_pages, block_table, context_len
                    context_lens, page_size, (float(k_scale), float(v_scale)), window, sinks, scale,
                    out, max_context_len, workspace, stream,
                    lambda shape, guard: _sized(_lib.pa_decode_workspace_bytes, guard, shape))
+
+
+def pa_prefill_window(query: torch.Tensor, key_pages: torch.Tensor, value_pages: torch.Tensor,
+                      block_table: torch.Tensor, context_lens: torch.Tensor, page_size: int,
+                      window: int, sinks: int = 0, scale: Optional[float] = None,
+                      out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """pa_decode_window's result on the tensor-core prefill kernel."""
+    shape, ptrs, tables, scale, out, out_ptr, raw, guard = _paged(
+        query, key_pages, value_pages, block_table, context_lens, page_size, scale, out, None,
+        torch.bfloat16, stream)
+    _launch(_lib.pa_prefill_window, "pa_prefill_window", guard, *ptrs, *tables, int(page_size),
+            scale, int(window), int(sinks), out_ptr, shape, raw)
+    return out
+
+
+def pa_attention_window_workspace_bytes(shape: pa_shape, page_size: int, max_context_len: int,
+                                        window: int, sinks: int,
+                                        device: Optional[torch.device] = None) -> int:
+    with torch.cuda.device(device if device is not None else torch.cuda.current_device()):
+        return int(_lib.pa_attention_window_workspace_bytes(shape, int(page_size),
+                                                            int(max_context_len), int(window),
+                                                            int(sinks)))
+
+
+def pa_attention_window_fp8_workspace_bytes(shape: pa_shape, page_size: int, max_context_len: int,
+                                            window: int, sinks: int,
+                                            device: Optional[torch.device] = None) -> int:
+    with torch.cuda.device(device if device is not None else torch.cuda.current_device()):
+        return int(_lib.pa_attention_window_fp8_workspace_bytes(shape, int(page_size),
+                                                                int(max_context_len), int(window),
+                                                                int(sinks)))
+
+
+def pa_attention_window(query: torch.Tensor, key_pages: torch.Tensor, value_pages: torch.Tensor,
+                        block_table: torch.Tensor, context_lens: torch.Tensor, page_size: int,
+                        window: int, sinks: int = 0, scale: Optional[float] = None,
+                        out: Optional[torch.Tensor] = None, max_context_len: int = 0,
+                        workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """The dispatch: pa_decode_window for short queries, pa_prefill_window
+    beyond."""
+    return _window("pa_attention_window", query, key_pages, value_pages, block_table, context_lens,
+                   page_size, (), window, sinks, scale, out, max_context_len, workspace, stream,
+                   lambda shape, guard: _sized(_lib.pa_attention_window_workspace_bytes, guard,
+                                               shape, int(page_size), int(max_context_len),
+                                               int(window), int(sinks)))
+
+
+def pa_attention_window_fp8(query, key_pages, value_pages, block_table, context_lens,
+                            page_size: int, k_scale: float, v_scale: float, window: int,
+                            sinks: int = 0, scale: Optional[float] = None, out=None,
+                            max_context_len: Optional[int] = None,
+                            workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """The dispatch for uint8 e4m3 pools. max_context_len bounds context_lens;
+    None reads context_lens.max() (a device-to-host copy)."""
+    if max_context_len is None:
+        max_context_len = int(context_lens.max().item())
+    return _window("pa_attention_window_fp8", query, key_pages, value_pages, block_table,
+                   context_lens, page_size, (float(k_scale), float(v_scale)), window, sinks, scale,
+                   out, max_context_len, workspace, stream,
+                   lambda shape, guard: _sized(_lib.pa_attention_window_fp8_workspace_bytes, guard,
+                                               shape, int(page_size), int(max_context_len),
+                                               int(window), int(sinks)))
 
 
 def pa_decode_weights_workspace_bytes(shape: pa_shape, max_context_len: int,

@@ -393,6 +393,64 @@ pa_status run_prefill_tc(const void* query, const void* key_pages, const void* v
     return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
+// Prefill with a sliding window on the pairs kernel (every head_dim, page size
+// and group size; whole items). PA_ERR_UNSUPPORTED where its register split is
+// not available.
+pa_status run_prefill_window(const void* query, const void* key_pages, const void* value_pages,
+                             const int32_t* block_table, const int32_t* context_lens,
+                             int32_t page_size, float scale, int32_t window, int32_t sinks,
+                             float out_scale, void* out, const pa_shape& s, cudaStream_t stream)
+{
+    DeviceInfo* dev;
+    pa_status st = device_info(&dev);
+    if (st != PA_OK)
+        return st;
+    if (prefill_pairs_smem_bytes(s.head_dim) > size_t(dev->max_smem_optin))
+        return PA_ERR_UNSUPPORTED;
+    const int64_t n_qtiles = (int64_t(s.q_len) + 127) / 128;
+    const int64_t q_rows = int64_t(s.batch) * s.num_q_heads * s.q_len;
+    if (int64_t(s.batch) * s.num_q_heads * n_qtiles >= (int64_t(1) << 31) ||
+        q_rows >= (int64_t(1) << 31))
+        return PA_ERR_UNSUPPORTED;
+    const uint32_t box = uint32_t(page_size < 128 ? page_size : 128);
+    const uint64_t kv_rows = uint64_t(s.num_pages) * s.num_kv_heads * page_size;
+    const uint32_t cols = uint32_t(s.head_dim);
+    CUtensorMap qmap, kmap, vmap, omap;
+    if ((st = encode_rows_map(&qmap, query, uint64_t(q_rows), 128u, cols)) != PA_OK ||
+        (st = encode_rows_map(&kmap, key_pages, kv_rows, box, cols)) != PA_OK ||
+        (st = encode_rows_map(&vmap, value_pages, kv_rows, box, cols)) != PA_OK ||
+        (st = encode_out_map(&omap, out, uint64_t(s.batch) * s.num_q_heads, uint64_t(s.q_len),
+                             cols)) != PA_OK)
+        return st;
+    PrefillArgs a;
+    memset(&a, 0, sizeof a);
+    a.out = static_cast<uint16_t*>(out);
+    a.block_table = block_table;
+    a.context_lens = context_lens;
+    a.err = dev->err;
+    a.B = s.batch;
+    a.H_q = s.num_q_heads;
+    a.H_kv = s.num_kv_heads;
+    a.L = s.q_len;
+    a.ps = page_size;
+    a.max_pages = s.max_pages;
+    a.num_pages = s.num_pages;
+    a.G = s.num_q_heads / s.num_kv_heads;
+    a.n_qtiles = int32_t(n_qtiles);
+    a.box_rows = int32_t(box);
+    a.scale_log2 = scale * 1.4426950408889634f;
+    a.causal = 1;
+    a.out_scale = out_scale;
+    a.D = s.head_dim;
+    a.key_pages = static_cast<const uint16_t*>(key_pages);
+    a.value_pages = static_cast<const uint16_t*>(value_pages);
+    a.window = window;
+    a.sinks = sinks;
+    const cudaError_t e = launch_prefill_pairs(qmap, kmap, vmap, omap, a, dev->id, dev->sm_count,
+                                               nullptr, 0, stream);
+    return e == cudaSuccess ? PA_OK : e == cudaErrorNotSupported ? PA_ERR_UNSUPPORTED : PA_ERR_CUDA;
+}
+
 // (request, KV head, 16-row tile) count of a call: the limit kMaxSegments
 // applies to it.
 int64_t decode_segments(const pa_shape& s)
@@ -1103,6 +1161,45 @@ pa_status run_decode_window(const void* query, const void* key_pages, const void
                         static_cast<cudaStream_t>(stream), 0, fp8, k_scale, v_scale, extra);
 }
 
+// Prefill over e4m3 pools with a sliding window: the tokens that some row sees
+// as bf16 copies (P1 pages of 128 tokens a request), and their table of P2
+// entries a request.
+struct WindowCopyPlan {
+    int64_t P1 = 0, P2 = 0;
+    pa_shape copy{};
+    size_t kv_bytes = 0, table_off = 0, total = 0;
+};
+
+pa_status plan_window_copy(const pa_shape& s, int32_t max_context_len, int32_t window,
+                           int32_t sinks, WindowCopyPlan* p)
+{
+    if (max_context_len < 0 || s.batch <= 0 || s.num_kv_heads <= 0 || s.num_q_heads <= 0 ||
+        s.q_len <= 0)
+        return PA_ERR_INVALID_ARG;
+    p->P2 = fp8_copy_pages(max_context_len);
+    p->P1 = fp8_window_pages(max_context_len, window, sinks, s.q_len);
+    const int64_t pages = int64_t(s.batch) * p->P1;
+    if (pages * s.num_kv_heads * 128 >= (int64_t(1) << 31) || p->P2 * 128 >= (int64_t(1) << 30) ||
+        int64_t(s.batch) * p->P2 >= (int64_t(1) << 31))
+        return PA_ERR_UNSUPPORTED;
+    p->copy = s;
+    p->copy.num_pages = int32_t(pages);
+    p->copy.max_pages = int32_t(p->P2);
+    p->kv_bytes = size_t(pages) * s.num_kv_heads * 128 * 128 * 2;
+    p->table_off = 2 * p->kv_bytes;
+    p->total = p->table_off + size_t(s.batch) * size_t(p->P2) * 4;
+    return PA_OK;
+}
+
+// Keys that a row of the call can see at most: the context that matters to the
+// choice of the kernel.
+int32_t window_reach(const pa_shape& s, int32_t max_context_len, int32_t window, int32_t sinks)
+{
+    const int64_t reach = int64_t(window) + sinks + s.q_len;
+    return max_context_len > 0 && max_context_len < reach ? max_context_len
+                                                          : int32_t(std::min<int64_t>(reach, 1 << 30));
+}
+
 // Workspace of a weight-accumulating decode: the decode's, then the scores of
 // every row (score_stride columns), then the row states.
 struct WeightPlan {
@@ -1212,6 +1309,140 @@ pa_status pa_decode_window_fp8(const void* query, const void* key_pages, const v
     return run_decode_window(query, key_pages, value_pages, block_table, context_lens, page_size,
                              scale, 1, k_scale, v_scale, window, sinks, out, shape,
                              max_context_len, workspace, workspace_bytes, stream);
+}
+
+pa_status pa_prefill_window(const void* query, const void* key_pages, const void* value_pages,
+                            const int32_t* block_table, const int32_t* context_lens,
+                            int32_t page_size, float scale, int32_t window, int32_t sinks,
+                            void* out, pa_shape shape, void* stream)
+{
+    pa_status st = check_attention(query, key_pages, value_pages, block_table, context_lens,
+                                   page_size, scale, out, shape);
+    if (st != PA_OK)
+        return st;
+    DecodeExtra extra;
+    extra.mode = kWindow;
+    if ((st = check_window(window, sinks, &extra.window)) != PA_OK)
+        return st;
+    extra.sinks = std::min(sinks, 1 << 30);
+    st = run_prefill_window(query, key_pages, value_pages, block_table, context_lens, page_size,
+                            scale, extra.window, extra.sinks, 1.f, out, shape,
+                            static_cast<cudaStream_t>(stream));
+    if (st != PA_ERR_UNSUPPORTED)
+        return st;
+    // Without the pairs kernel's register split: the split-KV kernel with
+    // whole segments per block, as pa_prefill.
+    return run_split_kv(query, key_pages, value_pages, block_table, context_lens, page_size, scale,
+                        1, out, shape, 0, nullptr, 0, 1, static_cast<cudaStream_t>(stream), 0, 0,
+                        1.f, 1.f, extra);
+}
+
+size_t pa_attention_window_workspace_bytes(pa_shape shape, int32_t page_size,
+                                           int32_t max_context_len, int32_t window, int32_t sinks)
+{
+    if (!pow2_in(page_size, 1, 256) || window <= 0 || sinks < 0 || max_context_len < 0)
+        return 0;
+    return pa_attention_route(shape, window_reach(shape, max_context_len, window, sinks)) == 0
+               ? pa_decode_workspace_bytes(shape)
+               : 0;
+}
+
+pa_status pa_attention_window(const void* query, const void* key_pages, const void* value_pages,
+                              const int32_t* block_table, const int32_t* context_lens,
+                              int32_t page_size, float scale, int32_t window, int32_t sinks,
+                              void* out, pa_shape shape, int32_t max_context_len, void* workspace,
+                              size_t workspace_bytes, void* stream)
+{
+    if (window <= 0 || sinks < 0 || max_context_len < 0)
+        return PA_ERR_INVALID_ARG;
+    const int32_t route =
+        pa_attention_route(shape, window_reach(shape, max_context_len, window, sinks));
+    if (route < 0)
+        return PA_ERR_INVALID_ARG;
+    if (route == 0)
+        return pa_decode_window(query, key_pages, value_pages, block_table, context_lens,
+                                page_size, scale, window, sinks, out, shape, max_context_len,
+                                workspace, workspace_bytes, stream);
+    return pa_prefill_window(query, key_pages, value_pages, block_table, context_lens, page_size,
+                             scale, window, sinks, out, shape, stream);
+}
+
+size_t pa_attention_window_fp8_workspace_bytes(pa_shape shape, int32_t page_size,
+                                               int32_t max_context_len, int32_t window,
+                                               int32_t sinks)
+{
+    const int32_t route = route_fp8(shape);
+    if (!pow2_in(page_size, 1, 256) || route < 0 || shape.head_dim != 128 || window <= 0 || sinks < 0 || max_context_len < 0)
+        return 0;
+    if (route == 0)
+        return pa_decode_workspace_bytes(shape);
+    WindowCopyPlan p;
+    return plan_window_copy(shape, max_context_len, std::min(window, 1 << 30),
+                            std::min(sinks, 1 << 30), &p) == PA_OK
+               ? p.total
+               : 0;
+}
+
+pa_status pa_attention_window_fp8(const void* query, const void* key_pages,
+                                  const void* value_pages, const int32_t* block_table,
+                                  const int32_t* context_lens, int32_t page_size, float scale,
+                                  float k_scale, float v_scale, int32_t window, int32_t sinks,
+                                  void* out, pa_shape shape, int32_t max_context_len,
+                                  void* workspace, size_t workspace_bytes, void* stream)
+{
+    const int32_t route = route_fp8(shape);
+    if (route < 0)
+        return PA_ERR_INVALID_ARG;
+    if (route == 0)
+        return pa_decode_window_fp8(query, key_pages, value_pages, block_table, context_lens,
+                                    page_size, scale, k_scale, v_scale, window, sinks, out, shape,
+                                    max_context_len, workspace, workspace_bytes, stream);
+    pa_status st = check_attention(query, key_pages, value_pages, block_table, context_lens,
+                                   page_size, scale, out, shape);
+    if (st != PA_OK)
+        return st;
+    int32_t cut = 0;
+    if ((st = check_window(window, sinks, &cut)) != PA_OK)
+        return st;
+    const int32_t first = std::min(sinks, 1 << 30);
+    if (bad_scales(k_scale, v_scale))
+        return PA_ERR_INVALID_ARG;
+    if (shape.head_dim != 128)
+        return PA_ERR_UNSUPPORTED;
+    DeviceInfo* dev;
+    if ((st = device_info(&dev)) != PA_OK)
+        return st;
+    WindowCopyPlan p;
+    if ((st = plan_window_copy(shape, max_context_len, cut, first, &p)) != PA_OK)
+        return st;
+    if (!workspace || workspace_bytes < p.total || (reinterpret_cast<uintptr_t>(workspace) & 255u))
+        return PA_ERR_WORKSPACE;
+    uint8_t* w = static_cast<uint8_t*>(workspace);
+    Fp8PagesArgs c;
+    memset(&c, 0, sizeof c);
+    c.key_pages = static_cast<const uint8_t*>(key_pages);
+    c.value_pages = static_cast<const uint8_t*>(value_pages);
+    c.block_table = block_table;
+    c.context_lens = context_lens;
+    c.key_out = reinterpret_cast<uint16_t*>(w);
+    c.value_out = reinterpret_cast<uint16_t*>(w + p.kv_bytes);
+    c.table_out = reinterpret_cast<int32_t*>(w + p.table_off);
+    c.err = dev->err;
+    c.B = shape.batch;
+    c.H_kv = shape.num_kv_heads;
+    c.ps = page_size;
+    c.max_pages = shape.max_pages;
+    c.num_pages = shape.num_pages;
+    c.P2 = int32_t(p.P2);
+    c.P1 = int32_t(p.P1);
+    c.window = cut;
+    c.sinks = first;
+    c.L = shape.q_len;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (launch_fp8_pages_to_bf16(c, s) != cudaSuccess)
+        return PA_ERR_CUDA;
+    return run_prefill_window(query, c.key_out, c.value_out, c.table_out, context_lens, 128,
+                              scale * k_scale, cut, first, v_scale, out, p.copy, s);
 }
 
 size_t pa_decode_weights_workspace_bytes(pa_shape shape, int32_t max_context_len)

@@ -47,6 +47,11 @@ __device__ __forceinline__ uint2 e4m3x4_to_bf16x4(uint32_t w)
     return make_uint2(r[0], r[1]);
 }
 
+// With a sliding window (kWin) the copy pages of a request are those of the
+// sinks, then those from the first token on that some row sees through the
+// window; of the tokens in them only those that some row sees are read (the
+// pages of the others may be gone), the rest are zeros.
+template <bool kWin>
 __global__ void __launch_bounds__(256) fp8_pages_to_bf16_kernel(const Fp8PagesArgs a)
 {
     // Launched with programmatic stream serialization: wait for the previous
@@ -54,20 +59,31 @@ __global__ void __launch_bounds__(256) fp8_pages_to_bf16_kernel(const Fp8PagesAr
     grid_dependency_wait();
     grid_launch_dependents();
     int64_t blk = blockIdx.x;
-    const int p2 = int(blk % a.P2);
-    blk /= a.P2;
+    const int per = kWin ? a.P1 : a.P2;                     // copy pages per request
+    const int p1 = int(blk % per);
+    blk /= per;
     const int h = int(blk % a.H_kv);
     const int b = int(blk / a.H_kv);
-    const int64_t page = int64_t(b) * a.P2 + p2;            // page of the copy
-    if (h == 0 && threadIdx.x == 0)
-        a.table_out[page] = int32_t(page);
+    const int64_t page = int64_t(b) * per + p1;             // page of the copy
     const int cap = min(a.max_pages * a.ps, a.P2 * kCopyRows);
     int n = a.context_lens[b];
     if (n < 0 || n > cap) {
-        if (h == 0 && p2 == 0 && threadIdx.x == 0)
+        if (h == 0 && p1 == 0 && threadIdx.x == 0)
             atomicOr(a.err, PA_DEVERR_CONTEXT_LEN_BIT);
         n = n < 0 ? 0 : cap;
     }
+    int p2 = p1;                                            // the tokens' place in the table
+    int first_seen = 0;
+    if constexpr (kWin) {
+        first_seen = int(max(int64_t(0), int64_t(n) - a.L - a.window + 1));
+        const int sink_pages = min(a.P2, (a.sinks + kCopyRows - 1) / kCopyRows);
+        if (p1 >= sink_pages)
+            p2 = max(sink_pages, first_seen / kCopyRows) + p1 - sink_pages;
+        if (p2 >= a.P2)
+            return;
+    }
+    if (h == 0 && threadIdx.x == 0)
+        a.table_out[int64_t(b) * a.P2 + p2] = int32_t(page);
     const int t0 = p2 * kCopyRows;
     if (t0 >= n)
         return;
@@ -78,7 +94,7 @@ __global__ void __launch_bounds__(256) fp8_pages_to_bf16_kernel(const Fp8PagesAr
         const int r = idx >> 3, c = idx & 7;
         const int t = t0 + r;
         uint4 kc = make_uint4(0, 0, 0, 0), vc = make_uint4(0, 0, 0, 0);
-        if (t < n) {
+        if (t < n && (!kWin || t >= first_seen || t < a.sinks)) {
             const int lp = t / a.ps;
             int phys = bt[lp];
             if (unsigned(phys) >= unsigned(a.num_pages)) {
@@ -109,9 +125,17 @@ int64_t fp8_copy_pages(int64_t max_context_len)
     return p > 0 ? p : 1;
 }
 
+int64_t fp8_window_pages(int64_t max_context_len, int64_t window, int64_t sinks, int64_t L)
+{
+    const int64_t all = fp8_copy_pages(max_context_len);
+    const int64_t sink_pages = (sinks + kCopyRows - 1) / kCopyRows;
+    const int64_t seen = (window + L + kCopyRows - 2) / kCopyRows + 1;   // from any token of a page
+    return sink_pages + seen < all ? sink_pages + seen : all;
+}
+
 cudaError_t launch_fp8_pages_to_bf16(const Fp8PagesArgs& a, cudaStream_t stream)
 {
-    const int64_t blocks = int64_t(a.B) * a.H_kv * a.P2;
+    const int64_t blocks = int64_t(a.B) * a.H_kv * (a.window > 0 ? a.P1 : a.P2);
     if (blocks <= 0 || blocks >= (int64_t(1) << 31))
         return cudaErrorInvalidValue;
     cudaLaunchAttribute attr[1];
@@ -123,8 +147,8 @@ cudaError_t launch_fp8_pages_to_bf16(const Fp8PagesArgs& a, cudaStream_t stream)
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, fp8_pages_to_bf16_kernel, a);
-    return e;
+    return cudaLaunchKernelEx(&cfg, a.window > 0 ? fp8_pages_to_bf16_kernel<true> : fp8_pages_to_bf16_kernel<false>,
+                              a);
 }
 
 }  // namespace pa

@@ -226,6 +226,9 @@ struct PrefillArgs {
     unsigned long long* arrive;   // [grid][2][4]
     uint64_t stamp;               // this launch's stamp (never 0)
     int32_t piece_last;           // test setting: receiving blocks run the piece last
+    // Pairs kernel: a sliding window of `window` keys (0: none; causal) and the
+    // first `sinks` keys.
+    int32_t window, sinks;
 };
 
 // Prefill over e4m3 pools: bf16 copies of the visible K/V tokens, in pages
@@ -241,8 +244,14 @@ struct Fp8PagesArgs {
     int32_t* table_out;           // [B, P2]: b * P2 + p
     unsigned* err;
     int32_t B, H_kv, ps, max_pages, num_pages;
-    int32_t P2;                   // copy pages per request: ceil(max_context_len / 128)
+    int32_t P2;                   // table entries per request: ceil(max_context_len / 128)
+    // A sliding window (0: none) over rows of length L: only the tokens that
+    // some row sees are copied, P1 copy pages per request (P2 without a window).
+    int32_t window, sinks, L;
+    int32_t P1;
 };
+// Copy pages per request with a sliding window.
+int64_t fp8_window_pages(int64_t max_context_len, int64_t window, int64_t sinks, int64_t L);
 int64_t fp8_copy_pages(int64_t max_context_len);
 cudaError_t launch_fp8_pages_to_bf16(const Fp8PagesArgs& a, cudaStream_t stream);
 

@@ -120,6 +120,9 @@ static_assert(kMmaDone < Layout<128>::kNumBars, "barrier count");
 // head 0, the first K/V tile run here, the role (below), the tail piece's
 // state slot (its donor block).
 enum { kEB = 0, kET, kEH0, kEH1, kEHK, kEN, kENT, kEDup, kEK0, kERole, kESlot, kEntry = 12 };
+// With a sliding window (kWin) an item's tiles are those of the sinks, then
+// those from the window's first page on: kEK0 holds the number of the first,
+// kESlot the first key of the second (there are no pieces then).
 // Item roles: the whole item here; the item's last tiles here, state left
 // for its first block (run first on the receiving block); the item's first
 // tiles here, merged at the end with the state its last tiles left.
@@ -350,6 +353,26 @@ __device__ __forceinline__ void piece_arrive_receiver(const uint4* state, const 
     }
 }
 
+// The keys of an item with a sliding window: tiles of 128 keys over [0,
+// sinks), then from `start`, the first key that the item's first row sees
+// through the window (first_seen) rounded down to a page (or 128 keys within a
+// larger page), so that no page is touched that no row sees; one run from 0
+// where the two would meet. `keys`: one past the last key that a row sees.
+struct WindowSpan {
+    int sink_tiles, start, first_seen, tiles;
+};
+__device__ __forceinline__ WindowSpan window_span(const PrefillArgs& a, int n, int row0, int keys)
+{
+    WindowSpan s;
+    s.first_seen = int(max(int64_t(0), int64_t(n) - a.L + row0 - a.window + 1));
+    const int start = s.first_seen & ~(a.box_rows - 1);
+    const bool apart = start > a.sinks;
+    s.sink_tiles = apart ? (a.sinks + kKeys - 1) / kKeys : 0;
+    s.start = apart ? start : 0;
+    s.tiles = keys <= 0 ? 0 : s.sink_tiles + (keys - s.start + kKeys - 1) / kKeys;
+    return s;
+}
+
 // kOdd: the group size is odd and the last pair of each group repeats its
 // last head (a separate instantiation, so that even groups keep their code).
 // kD: head_dim (128, or 64: one 64-column half per Q, K and V row, four
@@ -363,7 +386,7 @@ __device__ __forceinline__ void piece_arrive_receiver(const uint4* state, const 
 // context zero-filled). Each loader warp waits for its own copies of a stage
 // once it has issued the next stage's, fences them to the tensor cores'
 // proxy and then arrives.
-template <bool kOdd, int kD, bool kPieces, bool kSmall>
+template <bool kOdd, int kD, bool kPieces, bool kSmall, bool kWin = false>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_pairs_kernel(const __grid_constant__ CUtensorMap q_map,
                          const __grid_constant__ CUtensorMap key_map,
@@ -418,6 +441,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         int nk = a.causal ? min(nn, pl + 1) : nn;
         nk = nk < 0 ? 0 : nk;
         *n_out = nn;
+        if constexpr (kWin)
+            return window_span(a, nn, r0, nk).tiles;
         return (nk + kKeys - 1) / kKeys;
     };
     // scratch until the epilogues: the ranking, and the tiles and context
@@ -507,7 +532,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             e[kENT] = nt;
             e[kERole] = kWhole;
         }
+        if constexpr (kWin) {
+            const WindowSpan ws = window_span(a, n, t * kRows, n);
+            e[kEK0] = ws.sink_tiles;
+            e[kESlot] = ws.start;
+        }
     }
+    // First key of tile j of an item (k0, slot: its entries kEK0, kESlot), and
+    // the end of the keys that the tile's run holds.
+    auto tile_key0 = [&](int k0, int slot, int j) {
+        if constexpr (kWin)
+            return j < k0 ? j * kKeys : slot + (j - k0) * kKeys;
+        return (k0 + j) * kKeys;
+    };
+    auto tile_end = [&](int k0, int n, int j) { return kWin && j < k0 ? a.sinks : n; };
 
     const uint32_t sQ = smem_u32(smem + Layout::kQ);
     const uint32_t sK = smem_u32(smem + Layout::kK);
@@ -590,28 +628,29 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int it = 0; it < n_items; ++it) {
                 const int32_t* e = items + it * kEntry;
                 const int nt = e[kENT], k0 = e[kEK0];
+                const int slot = kWin ? e[kESlot] : 0;
                 if (nt == 0)
                     continue;
                 const int b = e[kEB], n = e[kEN], hk = e[kEHK];
                 const int32_t* bt = a.block_table + int64_t(b) * a.max_pages;
                 // tile j of the piece is the item's K/V tile k0 + j
                 auto n_boxes = [&](int j) {
-                    const int key0 = (k0 + j) * kKeys;
-                    return (min(n, key0 + kKeys) - key0 + box - 1) / box;
+                    const int key0 = tile_key0(k0, slot, j);
+                    return (min(tile_end(k0, n, j), key0 + kKeys) - key0 + box - 1) / box;
                 };
                 // Raw block-table entry of this lane's box in tile j, loaded
                 // ahead of use and checked at use (entry 0 when the box does
                 // not exist, so that nothing waits for it before use).
                 auto fetch_page = [&](int j) -> int {
                     const bool live = j < nt && my_box < n_boxes(j);
-                    return bt[live ? ((k0 + j) * kKeys + my_box * box) / a.ps : 0];
+                    return bt[live ? (tile_key0(k0, slot, j) + my_box * box) / a.ps : 0];
                 };
                 auto pool_row = [&](int j, int phys) -> int {
                     if (unsigned(phys) >= unsigned(a.num_pages)) {
                         atomicOr(a.err, PA_DEVERR_PAGE_ID_BIT);
                         phys = 0;
                     }
-                    const int tok = (k0 + j) * kKeys + my_box * box;
+                    const int tok = tile_key0(k0, slot, j) + my_box * box;
                     return (phys * a.H_kv + hk) * a.ps + (tok - (tok / a.ps) * a.ps);
                 };
                 // Pages of fewer than 8 tokens: row r of tile j (row r of
@@ -641,12 +680,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int empty = (is_v ? kVEmpty : kKEmpty) + s;
                     const bool ok = mbar_wait_warp(&bar[empty], ((gj >> 1) & 1) ^ 1u, misc, a.err);
                     if (ok) {
-                        const int key0 = (k0 + j) * kKeys;
+                        const int key0 = tile_key0(k0, slot, j);
+                        const int end = tile_end(k0, n, j);
                         uint8_t* dst = smem + (is_v ? Layout::kV : Layout::kK) + s * Layout::kMat;
                         const uint16_t* pool = is_v ? a.value_pages : a.key_pages;
                         for (int r = li * 32 + lane; r < kKeys; r += 96) {
                             const int key = key0 + r;
-                            const bool live = key < n;
+                            const bool live = key < end;
                             int64_t row = 0;
                             if (live) {
                                 int phys = bt[key / a.ps];
@@ -909,6 +949,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int rows = min(kRows, a.L - row0);
             const int i = row0 + r;
             const int lim = a.causal ? min(n - a.L + i, n - 1) : n - 1;  // last visible key
+            const int slot0 = kWin ? e[kESlot] : 0;
+            const int low = lim - a.window + 1;          // kWin: the window's first key
+            // kWin: the first key that a row of the tile sees through the window
+            const int first_seen = int(max(int64_t(0), int64_t(n) - a.L + row0 - a.window + 1));
             float m_used = -INFINITY;
             float l = 0.f;
 
@@ -922,8 +966,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // P overwrites any). Reading the two 64-column halves one after
                 // the other, the lower half twice, was 0.9 us per call slower on
                 // the 512-row batch.
-                const int key0 = (k0 + j) * kKeys;
-                const bool edge = key0 + kKeys - 1 > lim;
+                const int key0 = tile_key0(k0, slot0, j);
+                const bool first_run = kWin && j < k0;
+                const bool edge = key0 + kKeys - 1 > lim || (kWin && key0 < low);
                 uint32_t sv[128];
                 float* s = reinterpret_cast<float*>(sv);
 #pragma unroll
@@ -935,7 +980,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int w = 0; w < 4; ++w) {
                         const int nv = lim - (key0 + 32 * w) + 1;   // visible keys
-                        const uint32_t vis = nv >= 32 ? 0xffffffffu : nv <= 0 ? 0u : (1u << nv) - 1u;
+                        uint32_t vis = nv >= 32 ? 0xffffffffu : nv <= 0 ? 0u : (1u << nv) - 1u;
+                        if constexpr (kWin) {
+                            // behind the window, unless among the first keys
+                            const int nl = low - (key0 + 32 * w), nf = a.sinks - (key0 + 32 * w);
+                            const uint32_t past = nl >= 32 ? 0xffffffffu : nl <= 0 ? 0u : (1u << nl) - 1u;
+                            const uint32_t sink = nf >= 32 ? 0xffffffffu : nf <= 0 ? 0u : (1u << nf) - 1u;
+                            vis &= first_run ? sink : ~past | sink;
+                        }
 #pragma unroll
                         for (int k = 0; k < 32; ++k)
                             s[32 * w + k] = (vis >> k) & 1u ? s[32 * w + k] : -INFINITY;
@@ -1003,7 +1055,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tmem_wait_st();
                 // V rows past the context hold stale bytes: zero them (P is 0
                 // there, but 0 * NaN is not) before either head's P V.
-                if (head == 0 && n < key0 + kKeys) {
+                const int end = tile_end(k0, n, j);
+                if (kWin && head == 0 && (end < key0 + kKeys || (key0 < first_seen && a.sinks < first_seen))) {
+                    // also those between the sinks and what the tile's rows see
+                    mbar_wait_bounded(&bar[kVFull + (gj & 1)], (gj >> 1) & 1, misc, a.err);
+                    constexpr int kRowChunks = kD / 8;
+                    uint8_t* vb = smem + Layout::kV + (gj & 1) * Layout::kMat;
+                    for (int idx = r; idx < kKeys * kRowChunks; idx += 128) {
+                        const int zr = idx / kRowChunks, ch = idx % kRowChunks;
+                        const int key = key0 + zr;
+                        if (key >= end || (key >= a.sinks && key < first_seen))
+                            *reinterpret_cast<uint4*>(vb + (ch >> 3) * Layout::kHalf + zr * 128 +
+                                                      (((ch & 7) ^ (zr & 7)) << 4)) = make_uint4(0, 0, 0, 0);
+                    }
+                    fence_proxy_async_smem();
+                }
+                if (!kWin && head == 0 && n < key0 + kKeys) {
                     mbar_wait_bounded(&bar[kVFull + (gj & 1)], (gj >> 1) & 1, misc, a.err);
                     const int z0 = max(0, n - key0);
                     constexpr int kRowChunks = kD / 8;    // 16-byte chunks per V row
@@ -1227,7 +1294,7 @@ namespace {
 
 // Register split and shared-memory limit checked once per device and
 // instantiation, then the launch.
-template <bool kOdd, int kD, bool kPieces, bool kSmall>
+template <bool kOdd, int kD, bool kPieces, bool kSmall, bool kWin = false>
 cudaError_t launch_pairs(const cudaLaunchConfig_t& cfg_in, const CUtensorMap& q_map,
                          const CUtensorMap& key_map, const CUtensorMap& value_map,
                          const CUtensorMap& out_map, const PrefillArgs& a, int device)
@@ -1237,7 +1304,7 @@ cudaError_t launch_pairs(const cudaLaunchConfig_t& cfg_in, const CUtensorMap& q_
     static std::atomic<int> regs_ok[kMaxDev];
     if (device < 0 || device >= kMaxDev)
         return cudaErrorInvalidDevice;
-    const void* fn = reinterpret_cast<const void*>(prefill_pairs_kernel<kOdd, kD, kPieces, kSmall>);
+    const void* fn = reinterpret_cast<const void*>(prefill_pairs_kernel<kOdd, kD, kPieces, kSmall, kWin>);
     const int smem = Layout<kD>::kBytes;
     // The register split needs 128 x kRegsProducer + 256 x kRegsSoftmax
     // registers out of the launch's own 384 x numRegs, a launch count no
@@ -1264,7 +1331,7 @@ cudaError_t launch_pairs(const cudaLaunchConfig_t& cfg_in, const CUtensorMap& q_
     }
     cudaLaunchConfig_t cfg = cfg_in;
     cfg.dynamicSmemBytes = size_t(smem);
-    return cudaLaunchKernelEx(&cfg, prefill_pairs_kernel<kOdd, kD, kPieces, kSmall>, q_map, key_map, value_map,
+    return cudaLaunchKernelEx(&cfg, prefill_pairs_kernel<kOdd, kD, kPieces, kSmall, kWin>, q_map, key_map, value_map,
                               out_map, a);
 }
 
@@ -1307,6 +1374,14 @@ cudaError_t launch_prefill_pairs(const CUtensorMap& q_map, const CUtensorMap& ke
     const bool odd = a.G % 2 != 0;
     const bool small = a.ps < 8;
     auto launch = [&]() {
+        if (a.window > 0) {
+            auto go = [&](auto fn) { return fn(cfg, q_map, key_map, value_map, out_map, a, device); };
+            if (small)
+                return a.D == 64 ? (odd ? go(launch_pairs<true, 64, false, true, true>) : go(launch_pairs<false, 64, false, true, true>))
+                                 : (odd ? go(launch_pairs<true, 128, false, true, true>) : go(launch_pairs<false, 128, false, true, true>));
+            return a.D == 64 ? (odd ? go(launch_pairs<true, 64, false, false, true>) : go(launch_pairs<false, 64, false, false, true>))
+                             : (odd ? go(launch_pairs<true, 128, false, false, true>) : go(launch_pairs<false, 128, false, false, true>));
+        }
         if (small) {
             if (a.D == 64)
                 return odd ? launch_pairs<true, 64, false, true>(cfg, q_map, key_map, value_map, out_map, a, device)
@@ -1327,7 +1402,7 @@ cudaError_t launch_prefill_pairs(const CUtensorMap& q_map, const CUtensorMap& ke
     // ranking in shared memory; otherwise whole items. No block waits for
     // another (the second to arrive merges), so the launch is an ordinary one.
     const int64_t M = int64_t(a.B) * a.n_qtiles;
-    if (workspace && !small && a.D == 128 && M <= kThreads && n_items > grid && n_items <= 2 * grid &&
+    if (workspace && a.window == 0 && !small && a.D == 128 && M <= kThreads && n_items > grid && n_items <= 2 * grid &&
         workspace_bytes >= prefill_pairs_workspace_bytes(int(grid)) &&
         (reinterpret_cast<uintptr_t>(workspace) & 255u) == 0) {
         uint8_t* w = static_cast<uint8_t*>(workspace);

@@ -153,3 +153,134 @@ def test_two_calls_on_two_streams_and_a_replayed_graph():
             assert torch.equal(o, w)
             o.zero_()
         torch.cuda.synchronize()
+
+
+# ---- the prefill kernel and the dispatch ------------------------------------
+
+def run_prefill(c, W, S):
+    return _pa().pa_prefill_window(**c, window=W, sinks=S)
+
+
+def check_prefill(lens, H_q, H_kv, L, D, ps, W, S, seed):
+    c = make(lens, H_q, H_kv, L, D, ps, seed, W, S)
+    out = run_prefill(c, W, S)
+    check_no_device_error()
+    check_out(out, reference(c, W, S), False, W + S + 1)
+
+
+PREFILL_LENS = [0, 1, 60, 128, 129, 300, 1000]
+
+
+@pytest.mark.parametrize("ps", [1, 2, 4, 8, 16, 64, 128, 256])
+@pytest.mark.parametrize("W,S", [(1, 0), (1, 2), (64, 4), (128, 128), (129, 0), (200, 130), (513, 17)])
+def test_prefill_pages_and_windows(ps, W, S):
+    check_prefill(PREFILL_LENS, 4, 2, 60, 128, ps, W, S, seed=ps + W)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("L", [1, 2, 127, 128, 129, 257, 700])
+@pytest.mark.parametrize("W,S", [(40, 4), (300, 0)])
+def test_prefill_lengths(L, W, S, D):
+    check_prefill([0, 3, L, L + 1, L + 200, L + 999], 4, 2, L, D, 16, W, S, seed=L + D)
+
+
+@pytest.mark.parametrize("ps", [4, 16])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("H_q,H_kv", [(1, 1), (3, 1), (7, 1), (28, 4), (8, 8), (32, 8)])
+def test_prefill_head_layouts(H_q, H_kv, D, ps):
+    check_prefill([100, 431], H_q, H_kv, 100, D, ps, 90, 5, seed=H_q + D)
+
+
+def test_prefill_many_items_per_block_and_many_tiles():
+    check_prefill([40 + (13 * i) % 700 for i in range(90)], 8, 2, 40, 64, 16, 64, 4, seed=30)
+    check_prefill([6000, 5500], 32, 8, 5000, 128, 16, 257, 4, seed=31)
+
+
+@pytest.mark.parametrize("W", [100000, 2**31 - 1])
+def test_prefill_window_past_every_context_is_full_attention(W):
+    pa = _pa()
+    c = make([130, 64, 777, 2100], 8, 2, 130, 128, 16, seed=32, poison=False)
+    assert torch.equal(run_prefill(c, W, 3), pa.pa_prefill(**c))
+
+
+@pytest.mark.parametrize("L", [1, 24, 25, 32, 33, 200])
+@pytest.mark.parametrize("mcl", [0, 4200])
+def test_dispatch(L, mcl):
+    pa = _pa()
+    c = make([L, L + 300, 4200], 8, 2, L, 128, 16, 33, W=200, S=4)
+    got = pa.pa_attention_window(**c, window=200, sinks=4, max_context_len=mcl)
+    check_no_device_error()
+    check_out(got, reference(c, 200, 4), False, 300)
+    want = run_decode(c, 200, 4, max_context_len=mcl) if L <= 24 else run_prefill(c, 200, 4)
+    assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("ps", [1, 16, 128, 256])
+@pytest.mark.parametrize("L", [3, 9, 130, 300])
+@pytest.mark.parametrize("W,S", [(1, 0), (100, 4), (300, 130), (5000, 4)])
+def test_dispatch_e4m3(L, W, S, ps):
+    pa = _pa()
+    lens = [0, 2, L, L + 77, L + 1500]
+    c = make(lens, 7, 1, L, 128, ps, 34, W, S, fp8=True)
+    got = pa.pa_attention_window_fp8(**c, k_scale=SCALES[0], v_scale=SCALES[1], window=W, sinks=S,
+                                     max_context_len=max(lens))
+    check_no_device_error()
+    # the second route rounds P to bf16
+    ref = reference(c, W, S, fp8=True)
+    check_out(got, ref, L <= 8, min(W, 3000) + S + L)
+
+
+def test_e4m3_copies_hold_the_seen_tokens_alone():
+    """The workspace of a short window over a long context is small, and the
+    longest context a bound allows works with it."""
+    pa = _pa()
+    c = make([60000, 59993], 4, 1, 100, 128, 16, 35, W=256, S=4, fp8=True)
+    shape = pa.make_shape(c["query"].shape, c["key_pages"].shape, c["block_table"].shape[1])
+    need = pa.pa_attention_window_fp8_workspace_bytes(shape, 16, 60000, 256, 4)
+    assert need < 2 * 6 * 128 * 128 * 2 * 2 + 2 * 469 * 4
+    ws = torch.full((need,), 0xFF, dtype=torch.uint8, device="cuda")
+    got = pa.pa_attention_window_fp8(**c, k_scale=SCALES[0], v_scale=SCALES[1], window=256, sinks=4,
+                                     max_context_len=60000, workspace=ws)
+    check_no_device_error()
+    check_out(got, reference(c, 256, 4, fp8=True), False, 400)
+
+
+def test_prefill_and_dispatch_refusals():
+    pa = _pa()
+    c = make([300, 200], 4, 2, 100, 128, 16, seed=36)
+    for kw, err in ((dict(window=0), pa.PagedAttentionError), (dict(sinks=-1), pa.PagedAttentionError),
+                    (dict(scale=float("inf")), pa.PagedAttentionError), (dict(page_size=8), ValueError)):
+        with pytest.raises(err):
+            pa.pa_prefill_window(**{**dict(c, window=8), **kw})
+        with pytest.raises(err):
+            pa.pa_attention_window(**{**dict(c, window=8), **kw})
+    with pytest.raises(pa.PagedAttentionError):
+        pa.pa_attention_window(**c, window=8, max_context_len=-1)
+    c = make([300, 200], 4, 2, 100, 128, 16, seed=36, fp8=True)
+    ok = dict(c, k_scale=1.0, v_scale=1.0, window=8, max_context_len=300)
+    for kw in (dict(k_scale=0.0), dict(v_scale=float("nan")), dict(window=-1), dict(sinks=-1),
+               dict(workspace=torch.empty(4096, dtype=torch.uint8, device="cuda"))):
+        with pytest.raises(pa.PagedAttentionError):
+            pa.pa_attention_window_fp8(**{**ok, **kw})
+
+
+def test_prefill_bad_page_is_recorded():
+    pa = _pa()
+    c = make([300, 200], 4, 2, 100, 64, 16, seed=37, W=64, S=4, poison=False)
+    c["block_table"][0, 300 // 16] = 1 << 20
+    run_prefill(c, 64, 4)
+    assert pa.pa_get_device_error() == (pa.PA_ERR_DEVICE_BOUNDS, pa.PA_DEVERR_PAGE_ID)
+
+
+def test_prefill_replayed_graph_on_another_stream():
+    c = make([300, 700], 8, 2, 200, 128, 16, seed=38, W=128, S=4)
+    want = run_prefill(c, 128, 4)
+    out = torch.empty_like(want)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        _pa().pa_prefill_window(**c, window=128, sinks=4, out=out)
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
