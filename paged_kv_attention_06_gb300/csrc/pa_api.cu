@@ -1060,7 +1060,9 @@ pa_status run_evict(void* key_pages, void* value_pages, float* weight_pages,
     a.keep = keep;
     a.sinks = sinks;
     a.recent = recent;
-    return launch_evict(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+    return launch_evict(a, dev->id, dev->sm_count, static_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? PA_OK
+               : PA_ERR_CUDA;
 }
 
 }  // namespace
