@@ -552,12 +552,13 @@ pa_status pa_decode_weights_fp8(const void *query, const void *key_pages, const 
  * request of `keep` tokens or fewer keeps all of them.
  *   key_pages, value_pages  [P, H_kv, page_size, D] bf16 (_fp8: e4m3 codes,
  *                    head_dim 128); weight_pages [P, H_kv, page_size] fp32.
- *   dst_block_table  [B, dst_max_pages] int32. The block table itself: in
- *                    place; slots behind the kept ones keep their contents.
- *                    Another table: entry i of a request is either entry i of
- *                    its own block_table row, or a page that no request of the
- *                    call reads and no other entry names (pages shared by
- *                    requests are evicted into fresh ones). At least
+ *   dst_block_table  [B, dst_max_pages] int32. The block table itself (the same
+ *                    address): in place; slots behind the kept ones keep their
+ *                    contents. Another table: pages that no request of the call
+ *                    reads and no other entry names (pages shared by requests
+ *                    are evicted into fresh ones); an entry that is the
+ *                    request's own page of the same place records
+ *                    PA_DEVERR_PAGE_ID, and rows around it are not written. At least
  *                    min(keep, max_pages * page_size) tokens wide; entries
  *                    behind the kept rows are not read.
  *   kept             [B, H_kv, keep] int32 out: the kept positions, ascending,

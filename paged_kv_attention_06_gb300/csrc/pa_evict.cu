@@ -6,9 +6,9 @@
 //
 // Two kernels, chained by programmatic dependent launch:
 //   * select, one block per (request, KV head): the k-th largest weight by a
-//     radix search over order-preserving 32-bit keys (four histograms of eight
-//     bits, from the top; the histogram of each holds the keys that share the
-//     bits found so far), then one ordered pass that writes the positions of
+//     radix search over order-preserving 32-bit keys (histograms of 11, 11 and
+//     10 bits, from the top; each counts the keys that share the bits found so
+//     far), then one ordered pass that writes the positions of
 //     the keys above it and of the first ones equal to it. No sort, no atomics
 //     whose order could show: the histogram counts are sums, the positions come
 //     from a prefix sum.
@@ -70,30 +70,49 @@ __device__ __forceinline__ int slot_row(const EvictArgs& a, const int32_t* bt, i
 constexpr int kSelThreads = 512;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kMaxCluster = 8;
-constexpr int kFly = 8;                      // weights in flight per thread
+constexpr int kFly = 8;                      // keys of a batch per thread
+constexpr int kBatch = kSelThreads * kFly;
 // Keys that a block holds in shared memory after the one read of the weights;
 // what lies behind them is read again in every pass.
-constexpr int kSelKeys = 19 * 1024;
-constexpr int kHistInts = 256 * 32;
+constexpr int kSelKeys = 4 * kBatch;
+// Digits of a key, from the top: shift and bins. The first holds the sign, the
+// exponent and two bits of the mantissa, so that weights of like size spread
+// over bins; after it few keys are left to count.
+constexpr int kPasses = 3;
+__host__ __device__ constexpr int digit_shift(int pass) { return pass == 0 ? 21 : pass == 1 ? 10 : 0; }
+__host__ __device__ constexpr int digit_bins(int pass) { return pass == 2 ? 1024 : 2048; }
+__host__ __device__ constexpr int digit_offset(int pass) { return 2048 * pass; }
+constexpr int kBins = 2048 + 2048 + 1024;
 
-// One cluster of `cluster_dim` blocks per (request, KV head), each with a run of the
-// candidate positions. Histograms have a copy per lane, so that neither equal
-// digits (most weights share a few exponents) nor banks collide: 32k keys took
-// 45 us with one copy and one block.
+// One cluster of C blocks per (request, KV head), each with a run of the
+// candidate positions and a histogram of its own. A block adds its bins that
+// are not empty (few) to the totals of every block of the cluster, so after one
+// cluster barrier a pass each block scans the totals itself; reading the
+// others' histograms instead took 12 us a pass at C = 8.
 __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const EvictArgs a, int cached)
 {
-    extern __shared__ uint32_t smem_keys[];  // [256][32] histogram copies, then [cached] keys
-    __shared__ int sums[2][256];             // this block's histogram of a pass (by parity)
-    __shared__ int counts[2];                // this block's keys above and equal
+    extern __shared__ uint32_t smem_keys[];  // own bins, totals, then [cached] keys
+    __shared__ int2 before[kMaxCluster];     // keys above and equal in each block of the cluster
     __shared__ int found[3];                 // digit, keys above it within the prefix, keys of it
-    __shared__ int2 warp_sum[kSelWarps];
-    int* hist = reinterpret_cast<int*>(smem_keys);
-    uint32_t* keys = smem_keys + kHistInts;
-    grid_dependency_wait();
-    grid_launch_dependents();
+    __shared__ int scan[kSelWarps];
+    __shared__ alignas(16) int tally[kFly * kSelWarps];   // above | equal << 16, by (u, warp)
+    __shared__ int2 mine;                    // this block's keys above and equal
+    int* own = reinterpret_cast<int*>(smem_keys);
+    int* totals = own + kBins;
+    uint32_t* keys = smem_keys + 2 * kBins;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    for (int i = tid; i < 2 * kBins / 4; i += kSelThreads)
+        reinterpret_cast<int4*>(own)[i] = make_int4(0, 0, 0, 0);
+    if (tid == 0)
+        mine = make_int2(0, 0);
     cg::cluster_group cluster = cg::this_cluster();
     const int C = int(cluster.num_blocks()), rank = int(cluster.block_rank());
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    // The totals are clear in every block: waited for before the first addition.
+    if (C > 1)
+        cluster.barrier_arrive();
+    __syncthreads();
+    grid_dependency_wait();
+    grid_launch_dependents();
     const int bh = blockIdx.x / C;
     const int b = bh / a.H_kv, h = bh - b * a.H_kv;
     const bool first = tid == 0 && h == 0 && rank == 0;
@@ -101,112 +120,140 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const Evic
     int32_t* kept = a.kept + int64_t(bh) * a.keep;
     if (first)
         a.new_lens[b] = n < a.keep ? n : a.keep;
-    // All blocks of a cluster take the same way out, before any of them
-    // reads another's shared memory.
     const int all = rank * kSelThreads + tid, step = C * kSelThreads;
+    const int k = a.keep - a.sinks - a.recent;       // to choose among [sinks, n - recent)
     if (n <= a.keep) {
         for (int j = all; j < a.keep; j += step)
             kept[j] = j < n ? j : -1;
+    } else {
+        for (int j = all; j < a.sinks; j += step)
+            kept[j] = j;
+        for (int j = all; j < a.recent; j += step)
+            kept[a.keep - a.recent + j] = n - a.recent + j;
+    }
+    if (n <= a.keep || k == 0) {                     // the same in every block of the cluster
+        if (C > 1)
+            cluster.barrier_wait();
         return;
     }
-    for (int j = all; j < a.sinks; j += step)
-        kept[j] = j;
-    for (int j = all; j < a.recent; j += step)
-        kept[a.keep - a.recent + j] = n - a.recent + j;
-    const int k = a.keep - a.sinks - a.recent;       // to choose among [sinks, n - recent)
-    if (k == 0)
-        return;
     const int total = n - a.recent - a.sinks;
     const int part = ((total + C - 1) / C + 31) & ~31;
     const int lo = a.sinks + rank * part;            // this block's candidates: [lo, lo + m)
     const int m = max(0, min(part, total - rank * part));
     const int32_t* bt = a.block_table + int64_t(b) * a.max_pages;
-    // The one read of the weights: kFly page ids, then kFly weights in flight.
-    const int held = m < cached ? m : cached;
-    for (int p0 = tid; p0 < held; p0 += kSelThreads * kFly) {
+    // A batch of keys: thread tid holds positions q0 + u * kSelThreads + tid. From
+    // memory, the page ids are in flight together, then the weights.
+    auto read_batch = [&](int q0, uint32_t* key) {
         int row[kFly];
         float w[kFly];
 #pragma unroll
         for (int u = 0; u < kFly; ++u) {
-            const int p = p0 + u * kSelThreads;
-            row[u] = p < held ? slot_row(a, bt, h, lo + p) : -1;
+            const int p = q0 + u * kSelThreads + tid;
+            row[u] = p < m ? slot_row(a, bt, h, lo + p) : -1;
         }
 #pragma unroll
         for (int u = 0; u < kFly; ++u)
             w[u] = row[u] >= 0 ? a.weight_pages[row[u]] : NAN;
 #pragma unroll
         for (int u = 0; u < kFly; ++u)
-            if (p0 + u * kSelThreads < held)
-                keys[p0 + u * kSelThreads] = weight_key(w[u]);
-    }
-    auto key_at = [&](int p) -> uint32_t {
-        if (p < held)
-            return keys[p];
-        const int row = slot_row(a, bt, h, lo + p);
-        return row < 0 ? 0u : weight_key(a.weight_pages[row]);
+            key[u] = weight_key(w[u]);
+    };
+    auto batch = [&](int q0, uint32_t* key) {
+        if (q0 + kBatch <= cached) {
+#pragma unroll
+            for (int u = 0; u < kFly; ++u)
+                key[u] = keys[q0 + u * kSelThreads + tid];
+        } else {
+            read_batch(q0, key);
+        }
+    };
+    auto live = [&](int q0, int u) { return q0 + u * kSelThreads + tid < m; };
+    // A key into a histogram; a warp whose keys share the digit adds once.
+    auto count = [&](int* to, int digit, bool counts) {
+        const unsigned who = __ballot_sync(0xffffffffu, counts);
+        if (who == 0)
+            return;
+        const int lead = __shfl_sync(0xffffffffu, digit, __ffs(who) - 1);
+        if (__all_sync(0xffffffffu, !counts || digit == lead)) {
+            if (lane == __ffs(who) - 1)
+                atomicAdd(&to[lead], __popc(who));
+        } else if (counts) {
+            atomicAdd(&to[digit], 1);
+        }
     };
 
-    // The k-th largest key, eight bits at a time from the top; done as soon as
-    // all keys that share the bits found are wanted.
+    // The k-th largest key, from the top digit down; done as soon as all keys
+    // that share the bits found are wanted.
     uint32_t prefix = 0;
     int want = k;                                    // rank among the keys that share the prefix
     bool all_equal = false;
-    for (int shift = 24; shift >= 0 && !all_equal; shift -= 8) {
-        const int buf = (shift >> 3) & 1;
-        for (int i = tid; i < kHistInts; i += kSelThreads)
-            hist[i] = 0;
-        __syncthreads();
-        const uint32_t mask = shift == 24 ? 0u : 0xffffffffu << (shift + 8);
-        for (int p = tid; p < m; p += kSelThreads) {
-            const uint32_t key = key_at(p);
-            if ((key & mask) == prefix)
-                atomicAdd(&hist[((key >> shift) & 255u) * 32 + lane], 1);
-        }
-        __syncthreads();
-        {
-            // two threads a bin, each half of the copies, rotated over the banks
-            const int bin = tid >> 1;
-            int c = 0;
+#pragma unroll 1
+    for (int pass = 0; pass < kPasses && !all_equal; ++pass) {
+        const int shift = digit_shift(pass), bins = digit_bins(pass);
+        int* bin = own + digit_offset(pass);
+        int* tot = totals + digit_offset(pass);
+        const uint32_t mask = pass == 0 ? 0u : 0xffffffffu << digit_shift(pass - 1);
+        for (int q0 = 0; q0 < m; q0 += kBatch) {
+            uint32_t key[kFly];
+            if (pass == 0) {                         // the one read of the weights
+                read_batch(q0, key);
+                if (q0 + kBatch <= cached) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-                c += hist[bin * 32 + (tid & 1) * 16 + ((i + bin) & 15)];
-            c += __shfl_xor_sync(0xffffffffu, c, 1);
-            if ((tid & 1) == 0)
-                sums[buf][bin] = c;
-        }
-        cluster.sync();
-        if (warp == 0) {
-            // bins 255 - 8 lane down to 248 - 8 lane, counted from the top
-            int c[8], sum = 0;
-#pragma unroll
-            for (int u = 0; u < 8; ++u)
-                c[u] = 0;
-            for (int r = 0; r < C; ++r) {
-                const int* from = cluster.map_shared_rank(&sums[buf][0], r);
-#pragma unroll
-                for (int u = 0; u < 8; ++u)
-                    c[u] += from[255 - 8 * lane - u];
-            }
-#pragma unroll
-            for (int u = 0; u < 8; ++u)
-                sum += c[u];
-            int incl = sum;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int v = __shfl_up_sync(0xffffffffu, incl, o);
-                if (lane >= o)
-                    incl += v;
-            }
-            int above = incl - sum;
-#pragma unroll
-            for (int u = 0; u < 8; ++u) {
-                if (above < want && want <= above + c[u]) {
-                    found[0] = 255 - 8 * lane - u;
-                    found[1] = above;
-                    found[2] = c[u];
+                    for (int u = 0; u < kFly; ++u)
+                        keys[q0 + u * kSelThreads + tid] = key[u];
                 }
-                above += c[u];
+            } else {
+                batch(q0, key);
             }
+#pragma unroll
+            for (int u = 0; u < kFly; ++u)
+                if (q0 + u * kSelThreads < m)
+                    count(bin, int(key[u] >> shift) & (bins - 1), live(q0, u) && (key[u] & mask) == prefix);
+        }
+        __syncthreads();
+        const int* sum_of = bin;
+        if (C > 1) {
+            if (pass == 0)
+                cluster.barrier_wait();              // every block's totals are clear
+            for (int i = tid; i < bins; i += kSelThreads) {
+                const int c = bin[i];
+                if (c != 0)
+                    for (int r = 0; r < C; ++r)
+                        atomicAdd(cluster.map_shared_rank(tot, r) + i, c);
+            }
+            cluster.sync();
+            sum_of = tot;
+        }
+        // Bins from the top, four a thread (in the last pass the upper half of
+        // the threads has none).
+        const int base = bins - 4 * (tid + 1);
+        int4 c = make_int4(0, 0, 0, 0);
+        if (base >= 0)
+            c = *reinterpret_cast<const int4*>(sum_of + base);
+        const int sum = c.x + c.y + c.z + c.w;
+        int incl = sum;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o)
+                incl += v;
+        }
+        if (lane == 31)
+            scan[warp] = incl;
+        __syncthreads();
+        int above = incl - sum;
+#pragma unroll
+        for (int w = 0; w < kSelWarps; ++w)
+            above += w < warp ? scan[w] : 0;
+        const int each[4] = {c.w, c.z, c.y, c.x};
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            if (above < want && want <= above + each[u]) {
+                found[0] = base + 3 - u;
+                found[1] = above;
+                found[2] = each[u];
+            }
+            above += each[u];
         }
         __syncthreads();
         prefix |= uint32_t(found[0]) << shift;
@@ -215,74 +262,100 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const Evic
     }
     // Kept: the keys above prefix, and the first `want` of those equal to it;
     // where all that share the found bits are wanted, the keys from prefix up.
-    // Each warp takes a run of positions: counts first, then the places.
-    const int run = ((m + kSelWarps - 1) / kSelWarps + 31) & ~31;
-    const int r0 = warp * run, r1 = min(m, r0 + run);
-    auto judge = [&](int p, uint32_t* g, uint32_t* e, bool* gg, bool* ee) {
-        const uint32_t key = p < r1 ? key_at(p) : 0u;
-        *gg = p < r1 && (all_equal ? key >= prefix : key > prefix);
-        *ee = p < r1 && !all_equal && key == prefix;
-        *g = __ballot_sync(0xffffffffu, *gg);
-        *e = __ballot_sync(0xffffffffu, *ee);
-    };
-    uint32_t g, e;
-    bool gg, ee;
-    int gt = 0, eq = 0;
-    for (int p0 = r0; p0 < r1; p0 += 32) {
-        judge(p0 + lane, &g, &e, &gg, &ee);
-        gt += __popc(g);
-        eq += __popc(e);
-    }
-    if (lane == 0)
-        warp_sum[warp] = make_int2(gt, eq);
-    __syncthreads();
-    int above = 0, equal = 0;                        // kept-above and equal keys before this warp's
-    for (int w = 0; w < warp; ++w) {
-        above += warp_sum[w].x;
-        equal += warp_sum[w].y;
-    }
-    if (warp == kSelWarps - 1 && lane == 0) {
-        counts[0] = above + gt;
-        counts[1] = equal + eq;
-    }
-    cluster.sync();
-    for (int r = 0; r < rank; ++r) {
-        const int* from = cluster.map_shared_rank(&counts[0], r);
-        above += from[0];
-        equal += from[1];
+    auto above_it = [&](uint32_t key) { return all_equal ? key >= prefix : key > prefix; };
+    auto equal_it = [&](uint32_t key) { return !all_equal && key == prefix; };
+    int above = 0, equal = 0;                        // in the blocks and batches before
+    if (C > 1) {
+        int g = 0, e = 0;
+        for (int q0 = 0; q0 < m; q0 += kBatch) {
+            uint32_t key[kFly];
+            batch(q0, key);
+#pragma unroll
+            for (int u = 0; u < kFly; ++u)
+                if (live(q0, u)) {
+                    g += above_it(key[u]) ? 1 : 0;
+                    e += equal_it(key[u]) ? 1 : 0;
+                }
+        }
+        g = __reduce_add_sync(0xffffffffu, g);
+        e = __reduce_add_sync(0xffffffffu, e);
+        if (lane == 0) {
+            atomicAdd(&mine.x, g);
+            atomicAdd(&mine.y, e);
+        }
+        __syncthreads();
+        if (tid < C)
+            cluster.map_shared_rank(before, tid)[rank] = mine;
+        cluster.sync();                              // the last access to another block's memory
+        for (int r = 0; r < rank; ++r) {
+            above += before[r].x;
+            equal += before[r].y;
+        }
     }
     const uint32_t below = (1u << lane) - 1u;
-    for (int p0 = r0; p0 < r1; p0 += 32) {
-        judge(p0 + lane, &g, &e, &gg, &ee);
-        const int ga = above + __popc(g & below);
-        const int ea = equal + __popc(e & below);
-        if (gg || (ee && ea < want))
-            kept[a.sinks + ga + (ea < want ? ea : want)] = lo + p0 + lane;
-        above += __popc(g);
-        equal += __popc(e);
+    for (int q0 = 0; q0 < m; q0 += kBatch) {
+        uint32_t key[kFly], g[kFly], e[kFly];
+        batch(q0, key);
+        __syncthreads();                             // the batch before has read tally
+#pragma unroll
+        for (int u = 0; u < kFly; ++u) {
+            g[u] = __ballot_sync(0xffffffffu, live(q0, u) && above_it(key[u]));
+            e[u] = __ballot_sync(0xffffffffu, live(q0, u) && equal_it(key[u]));
+            if (lane == 0)
+                tally[u * kSelWarps + warp] = __popc(g[u]) | (__popc(e[u]) << 16);
+        }
+        __syncthreads();
+        // Every warp sums all tallies, four a lane (4096 keys: each half fits).
+        const int4 t = reinterpret_cast<const int4*>(tally)[lane];
+        const int sum = t.x + t.y + t.z + t.w;
+        int incl = sum;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o)
+                incl += v;
+        }
+        const int excl = incl - sum;
+        const int entry = warp & 3;                  // of the four of lane u * 4 + warp / 4
+        const int mid = excl + (entry > 0 ? t.x : 0) + (entry > 1 ? t.y : 0) + (entry > 2 ? t.z : 0);
+#pragma unroll
+        for (int u = 0; u < kFly; ++u) {
+            const int at = __shfl_sync(0xffffffffu, mid, u * (kSelWarps / 4) + (warp >> 2));
+            const int ga = above + (at & 0xffff) + __popc(g[u] & below);
+            const int ea = equal + (at >> 16) + __popc(e[u] & below);
+            const bool eq = e[u] >> lane & 1u;
+            if ((g[u] >> lane & 1u) || (eq && ea < want))
+                kept[a.sinks + ga + (ea < want ? ea : want)] = lo + q0 + u * kSelThreads + tid;
+        }
+        const int sums = __shfl_sync(0xffffffffu, incl, 31);
+        above += sums & 0xffff;
+        equal += sums >> 16;
     }
-    cluster.sync();                                  // no block ends while another reads its counts
 }
 
 constexpr int kMoveThreads = 256;
 constexpr int kSlice = 64;                   // bytes of a row per block
 constexpr int kUnroll = 4;                   // rows of a tile per thread
-constexpr int kChunkRows = 2048;             // rows per block where order does not matter
 constexpr int kTableInts = 6 * 1024;         // page ids staged in shared memory
+constexpr int kMinChunk = kMoveThreads / (kSlice / 16) * kUnroll;   // rows: one tile
+
+// How a move kernel's blocks take the rows of their (request, KV head): all of
+// them in order (in place), a chunk of them, or one tile of them.
+enum MoveKind : int { kInPlace, kChunk, kTile };
 
 // Rows [j_begin, j_end) of the kept ones. T: uint4 with four threads per row
-// slice, or float with one (the weights). bt, dt: the request's page ids
-// (shared memory, or global where they are many). One tile is in registers
-// while the next one's rows are read: a row's source is never a destination of
-// an earlier tile, so reading ahead is safe; the barrier keeps a tile's writes
-// behind every thread's reads of it.
-template <typename T, int kPerRow>
+// slice, or float with one (the weights). bt, dt: the request's page ids. One
+// tile is in registers while the next one's rows are read, and the positions of
+// the one after are on their way. A row's source is never a destination of an
+// earlier tile, so reading ahead is safe; in place, the barrier keeps a tile's
+// writes behind every thread's reads of it.
+template <typename T, int kPerRow, MoveKind kKind>
 __device__ __forceinline__ void move_rows(const EvictArgs& a, T* pool, int64_t row_units, int unit,
                                           const int32_t* bt, const int32_t* dt, int h, int j_begin,
                                           int j_end, const int32_t* kept)
 {
     constexpr int kRows = kMoveThreads / kPerRow;
-    constexpr int kTile = kRows * kUnroll;
+    constexpr int kStep = kRows * kUnroll;
     const int r0 = threadIdx.x / kPerRow;
     T* col = pool + unit;
     int pos[kUnroll];                        // kept positions of the tile to be read next
@@ -316,76 +389,84 @@ __device__ __forceinline__ void move_rows(const EvictArgs& a, T* pool, int64_t r
     };
     fetch(j_begin);
     read(j_begin, 0);
-    fetch(j_begin + kTile);
-    for (int j0 = j_begin; j0 < j_end; j0 += 2 * kTile) {
-        read(j0 + kTile, 1);
-        fetch(j0 + 2 * kTile);
-        __syncthreads();
+    if constexpr (kKind == kTile) {          // no more rows than a step of either type
+        write(j_begin, 0);
+        return;
+    }
+    fetch(j_begin + kStep);
+    for (int j0 = j_begin; j0 < j_end; j0 += 2 * kStep) {
+        read(j0 + kStep, 1);
+        fetch(j0 + 2 * kStep);
+        if (kKind == kInPlace)
+            __syncthreads();
         write(j0, 0);
-        read(j0 + 2 * kTile, 0);
-        fetch(j0 + 3 * kTile);
-        __syncthreads();
-        write(j0 + kTile, 1);
+        read(j0 + 2 * kStep, 0);
+        fetch(j0 + 3 * kStep);
+        if (kKind == kInPlace)
+            __syncthreads();
+        write(j0 + kStep, 1);
     }
 }
 
+// Blocks of a (request, KV head): a 64-byte column slice of K or of V, or the
+// weights.
+template <MoveKind kKind>
 __global__ void __launch_bounds__(kMoveThreads, 4) evict_move_kernel(const EvictArgs a)
 {
-    __shared__ int32_t table[kTableInts];
+    __shared__ int32_t table[kKind == kTile ? 2 : kTableInts];
     grid_dependency_wait();
     grid_launch_dependents();
     const int per = 2 * a.slices + 1;                // K slices, V slices, the weights
     int64_t blk = blockIdx.x;
     const int part = int(blk % per);
     blk /= per;
-    const int chunk = int(blk % a.chunks);
-    const int64_t bh = blk / a.chunks;
+    const int chunk = kKind == kInPlace ? 0 : int(blk % a.chunks);
+    const int64_t bh = kKind == kInPlace ? blk : blk / a.chunks;
     const int b = int(bh / a.H_kv), h = int(bh - int64_t(b) * a.H_kv);
     const int n = evict_context(a, b, false);
     const int len = n < a.keep ? n : a.keep;
     const int32_t* kept = a.kept + bh * a.keep;
     const int32_t* bt = a.block_table + int64_t(b) * a.max_pages;
     const int32_t* dt = a.dst_table + int64_t(b) * a.dst_max_pages;
-    const int dst_ids = (len + (1 << a.ps_shift) - 1) >> a.ps_shift;
-    // Chunks of rows in any order where no destination page is one of the
-    // request's own; otherwise its rows in order, in the first chunk's block.
-    int j_begin = chunk * kChunkRows, j_end = min(len, j_begin + kChunkRows);
-    if (a.chunks > 1) {
-        int own = 0;
-        for (int i = threadIdx.x; i < dst_ids; i += kMoveThreads)
-            own |= dt[i] == bt[i];
-        if (__syncthreads_or(own)) {
-            if (chunk > 0)
-                return;
-            j_end = len;
-        }
-    } else {
-        j_end = len;
-    }
+    const int j_begin = chunk * a.chunk_rows;
+    const int j_end = kKind == kInPlace ? len : min(len, j_begin + a.chunk_rows);
     if (j_begin >= j_end)
         return;
-    // The page ids that these rows need.
-    const int s0 = kept[j_begin] >> a.ps_shift, s1 = kept[j_end - 1] >> a.ps_shift;
     const int d0 = j_begin >> a.ps_shift, d1 = (j_end - 1) >> a.ps_shift;
-    const int ns = s1 - s0 + 1, nd = d1 - d0 + 1;
-    if (ns + nd <= kTableInts) {
-        for (int i = threadIdx.x; i < ns; i += kMoveThreads)
-            table[i] = bt[s0 + i];
-        for (int i = threadIdx.x; i < nd; i += kMoveThreads)
-            table[ns + i] = dt[d0 + i];
-        bt = table - s0;
-        dt = table + ns - d0;
-        __syncthreads();
+    if constexpr (kKind != kInPlace) {
+        // A destination that the request still reads: recorded, and the block's
+        // rows are not written.
+        int own = 0;
+        for (int i = d0 + int(threadIdx.x); i <= d1; i += kMoveThreads)
+            own |= dt[i] == bt[i];
+        if (__syncthreads_or(own)) {
+            if (threadIdx.x == 0)
+                atomicOr(a.err, PA_DEVERR_PAGE_ID_BIT);
+            return;
+        }
+    }
+    if constexpr (kKind != kTile) {
+        // The page ids of these rows in shared memory, where they fit.
+        const int s0 = kept[j_begin] >> a.ps_shift, s1 = kept[j_end - 1] >> a.ps_shift;
+        const int ns = s1 - s0 + 1, nd = d1 - d0 + 1;
+        if (ns + nd <= kTableInts) {
+            for (int i = threadIdx.x; i < ns; i += kMoveThreads)
+                table[i] = bt[s0 + i];
+            for (int i = threadIdx.x; i < nd; i += kMoveThreads)
+                table[ns + i] = dt[d0 + i];
+            bt = table - s0;
+            dt = table + ns - d0;
+            __syncthreads();
+        }
     }
     if (part == 2 * a.slices) {
-        move_rows<float, 1>(a, a.weight_pages, 1, 0, bt, dt, h, j_begin, j_end, kept);
+        move_rows<float, 1, kKind>(a, a.weight_pages, 1, 0, bt, dt, h, j_begin, j_end, kept);
     } else {
         const bool is_v = part >= a.slices;
         const int slice = part - (is_v ? a.slices : 0);
-        move_rows<uint4, kSlice / 16>(a, reinterpret_cast<uint4*>(is_v ? a.value_pages : a.key_pages),
-                                      a.row_bytes / 16,
-                                      slice * (kSlice / 16) + int(threadIdx.x % (kSlice / 16)), bt, dt, h,
-                                      j_begin, j_end, kept);
+        move_rows<uint4, kSlice / 16, kKind>(
+            a, static_cast<uint4*>(is_v ? a.value_pages : a.key_pages), a.row_bytes / 16,
+            slice * (kSlice / 16) + int(threadIdx.x % (kSlice / 16)), bt, dt, h, j_begin, j_end, kept);
     }
 }
 
@@ -393,20 +474,27 @@ __global__ void __launch_bounds__(kMoveThreads, 4) evict_move_kernel(const Evict
 
 cudaError_t launch_evict(EvictArgs a, int device, int sm_count, cudaStream_t stream)
 {
-    a.slices = a.row_bytes / kSlice;
     const int64_t heads = int64_t(a.B) * a.H_kv;
     const int64_t cap = int64_t(a.max_pages) << a.ps_shift;
     const int64_t rows = cap < a.keep ? cap : a.keep;
-    a.chunks = a.dst_table == a.block_table ? 1 : int((rows + kChunkRows - 1) / kChunkRows);
-    const int64_t moves = heads * (2 * a.slices + 1) * a.chunks;
+    const bool in_place = a.dst_table == a.block_table;
+    a.slices = a.row_bytes / kSlice;
+    const int64_t parts = heads * (2 * a.slices + 1);
+    // Chunks of 2048 rows, of fewer while that leaves the GPU short of blocks.
+    a.chunk_rows = 2048;
+    while (a.chunk_rows > kMinChunk && parts * ((rows + a.chunk_rows - 1) / a.chunk_rows) < 3 * int64_t(sm_count))
+        a.chunk_rows /= 2;
+    a.chunks = in_place ? 1 : int((rows + a.chunk_rows - 1) / a.chunk_rows);
+    const int64_t moves = parts * a.chunks;
     // Blocks per (request, KV head) for the choice: more while the GPU has room
-    // for them (two per SM) and each still has a few keys per thread.
+    // for them (two per SM) and each still has more than a batch of keys.
     int C = 1;
-    while (C < kMaxCluster && heads * C * 2 <= 2 * int64_t(sm_count) && cap > 4 * kSelThreads * C)
+    while (C < kMaxCluster && heads * C * 2 <= 2 * int64_t(sm_count) && cap > int64_t(kBatch) * C)
         C *= 2;
     if (moves >= (int64_t(1) << 31) || heads * C >= (int64_t(1) << 31))
         return cudaErrorInvalidValue;
-    const int64_t share = (cap + C - 1) / C + 31;
+    // whole batches of keys in shared memory
+    const int64_t share = ((cap + C - 1) / C + 31 + kBatch - 1) / kBatch * kBatch;
     const int cached = int(share < kSelKeys ? share : kSelKeys);
     constexpr int kMaxDev = 64;
     static std::atomic<bool> raised[kMaxDev];
@@ -415,7 +503,7 @@ cudaError_t launch_evict(EvictArgs a, int device, int sm_count, cudaStream_t str
     cudaError_t e;
     if (!raised[device].load(std::memory_order_relaxed)) {
         e = cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 (kHistInts + kSelKeys) * int(sizeof(uint32_t)));
+                                 (2 * kBins + kSelKeys) * int(sizeof(uint32_t)));
         if (e != cudaSuccess)
             return e;
         raised[device].store(true, std::memory_order_relaxed);
@@ -430,7 +518,7 @@ cudaError_t launch_evict(EvictArgs a, int device, int sm_count, cudaStream_t str
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(unsigned(heads * C));
     cfg.blockDim = dim3(kSelThreads);
-    cfg.dynamicSmemBytes = size_t(kHistInts + cached) * sizeof(uint32_t);
+    cfg.dynamicSmemBytes = size_t(2 * kBins + cached) * sizeof(uint32_t);
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
@@ -441,7 +529,8 @@ cudaError_t launch_evict(EvictArgs a, int device, int sm_count, cudaStream_t str
     cfg.blockDim = dim3(kMoveThreads);
     cfg.dynamicSmemBytes = 0;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, evict_move_kernel, a);
+    return cudaLaunchKernelEx(&cfg, in_place ? evict_move_kernel<kInPlace>
+                                    : a.chunk_rows == kMinChunk ? evict_move_kernel<kTile> : evict_move_kernel<kChunk>, a);
 }
 
 }  // namespace pa

@@ -87,7 +87,7 @@ struct EvictArgs {
     unsigned* err;
     int32_t B, H_kv, row_bytes, ps_shift, num_pages, max_pages, dst_max_pages;
     int32_t keep, sinks, recent;
-    int32_t slices, chunks;       // set by the launcher: column slices of a row, chunks of rows
+    int32_t slices, chunks, chunk_rows;   // set by the launcher: column slices of a row, chunks of rows
 };
 
 cudaError_t launch_evict(EvictArgs a, int device, int sm_count, cudaStream_t stream);

@@ -35,9 +35,6 @@ def make(lens, H_kv, D, ps, keep, seed, fp8=False, dst="same", weights="spread",
         for b, k in enumerate(dcount):
             dt[b, :k] = perm[at:at + k]
             at += k
-            if dst == "mixed":            # every second page is the request's own
-                own = np.arange(k) % 2 == 1
-                dt[b, :k][own] = bt[b, :k][own]
     shape = (P, H_kv, ps, D)
     if fp8:
         k, v = (rng.integers(0, 256, shape).astype(np.uint8) for _ in "kv")
@@ -114,7 +111,7 @@ def check(c, keep, S=0, R=0):
 LENS = [0, 1, 7, 63, 64, 65, 200, 201, 1030, 1500]
 
 
-@pytest.mark.parametrize("dst", ["same", "other", "mixed"])
+@pytest.mark.parametrize("dst", ["same", "other"])
 @pytest.mark.parametrize("ps", [1, 4, 16, 256])
 @pytest.mark.parametrize("D,fp8", [(64, False), (128, False), (128, True)])
 def test_matches_the_definition(D, fp8, ps, dst):
@@ -171,6 +168,20 @@ def test_bad_lengths_and_pages_are_recorded():
     for old, t in zip(before, (d["key_pages"], d["value_pages"], d["weight_pages"])):
         a, b = (x[page, :, :8].contiguous().view(torch.uint8) for x in (old, t))
         assert torch.equal(a, b)
+
+
+def test_own_page_in_another_table_is_recorded_and_not_written():
+    pa = _pa()
+    c = make([200], 2, 64, 16, 64, seed=17, dst="other")
+    d = device(c)
+    before = d["key_pages"].clone()
+    d["dst_block_table"][0, 1] = d["block_table"][0, 1]
+    kept, _ = pa.pa_kv_evict(**d, keep=64)
+    assert pa.pa_get_device_error() == (pa.PA_ERR_DEVICE_BOUNDS, pa.PA_DEVERR_PAGE_ID)
+    want, _, _ = plain(c, 64, 0, 0)
+    assert np.array_equal(kept.cpu().numpy(), want)
+    page = int(d["block_table"][0, 1])
+    assert torch.equal(before[page].view(torch.int16), d["key_pages"][page].view(torch.int16))
 
 
 def test_offsets_past_32_bits():
