@@ -305,15 +305,20 @@ def pa_append_kv_fp8(key: torch.Tensor, value: torch.Tensor, key_pages: torch.Te
     _check(st, "pa_append_kv_fp8")
 
 
-def _on_device(device: torch.device, stream, tensors):
-    """(raw stream, guard or None) of a call whose tensors all live on
-    `device`: the given stream or the device's current one, and a guard that
-    makes the device current where it is not."""
-    for name, t in tensors:
-        if t is not None and t.device != device:
-            raise ValueError(f"{name} is on {t.device}, expected {device}")
-    raw = torch._C._cuda_getCurrentRawStream(device.index) if stream is None else _stream(stream)
-    guard = None if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+def _ptr(t: torch.Tensor, dtype: torch.dtype, device_index: int, name: str) -> int:
+    """_dev_ptr, and on the device of the call."""
+    if t.dtype is not dtype or t.get_device() != device_index or not t.is_contiguous():
+        if t.is_cuda and t.get_device() != device_index:
+            raise ValueError(f"{name} is on {t.device}, expected cuda:{device_index}")
+        return _dev_ptr(t, dtype, name)
+    return t.data_ptr()
+
+
+def _on_device(device_index: int, stream):
+    """(raw stream, guard or None): the given stream or the device's current
+    one, and a guard that makes the device current where it is not."""
+    raw = torch._C._cuda_getCurrentRawStream(device_index) if stream is None else _stream(stream)
+    guard = None if torch.cuda.current_device() == device_index else torch.cuda.device(device_index)
     return raw, guard
 
 
@@ -360,7 +365,7 @@ def _qk_norm_rope_append(qkv, q_weight, k_weight, cos_sin, positions, key_pages,
     H_q = width // D - 2 * H_kv
     if H_q <= 0 or (H_q + 2 * H_kv) * D != width:
         raise ValueError("qkv's rows are not (H_q + 2 H_kv) heads of the pools' head_dim")
-    if tuple(slot_mapping.shape) != (B, L):
+    if slot_mapping.shape != (B, L):
         raise ValueError("slot_mapping must be [B, L]")
     if not qkv.is_cuda:
         raise ValueError("qkv must be a CUDA tensor")
@@ -368,41 +373,39 @@ def _qk_norm_rope_append(qkv, q_weight, k_weight, cos_sin, positions, key_pages,
         raise TypeError(f"qkv must be torch.bfloat16, got {qkv.dtype}")
     if qkv.stride(2) != 1:
         raise ValueError("qkv's rows must be contiguous")
-    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
-        if w is not None and tuple(w.shape) != (D,):
-            raise ValueError(f"{name} must be [D]")
+    if q_weight is not None and q_weight.shape != (D,):
+        raise ValueError("q_weight must be [D]")
+    if k_weight is not None and k_weight.shape != (D,):
+        raise ValueError("k_weight must be [D]")
     R = table_len = 0
     if cos_sin is not None:
-        if positions is None or tuple(positions.shape) != (B, L):
+        if positions is None or positions.shape != (B, L):
             raise ValueError("positions must be [B, L]")
         if cos_sin.dim() != 2:
             raise ValueError("cos_sin must be [table_len, rotary_dim]")
         table_len, R = cos_sin.shape
-    device = qkv.device
-    raw, guard = _on_device(device, stream, (
-        ("q_weight", q_weight), ("k_weight", k_weight), ("cos_sin", cos_sin),
-        ("positions", positions), ("key_pages", key_pages), ("value_pages", value_pages),
-        ("slot_mapping", slot_mapping), ("query", query)))
+    dev = qkv.get_device()
+    raw, guard = _on_device(dev, stream)
     if query is None:
-        query = torch.empty((B, H_q, L, D), dtype=torch.bfloat16, device=device)
+        query = torch.empty((B, H_q, L, D), dtype=torch.bfloat16, device=qkv.device)
         _keep_for(query, stream)
-    elif tuple(query.shape) != (B, H_q, L, D):
+    elif query.shape != (B, H_q, L, D):
         raise ValueError("query must be [B, H_q, L, D]")
     if B == 0 or L == 0:
         return query
-    shape = pa_shape(B, H_q, H_kv, D, L, P, 0)
     # the strides of an axis of one element say nothing
     bs = qkv.stride(0) if B > 1 else L * width
     ts = qkv.stride(1) if L > 1 else width
     _launch(getattr(_lib, what), what, guard, qkv.data_ptr(), bs, ts,
-            None if q_weight is None else _dev_ptr(q_weight, torch.bfloat16, "q_weight"),
-            None if k_weight is None else _dev_ptr(k_weight, torch.bfloat16, "k_weight"),
-            float(eps), None if cos_sin is None else _dev_ptr(cos_sin, torch.float32, "cos_sin"),
-            R, table_len, int(bool(interleaved)),
-            None if cos_sin is None else _dev_ptr(positions, torch.int32, "positions"),
-            _dev_ptr(query, torch.bfloat16, "query"), _dev_ptr(key_pages, pool_dtype, "key_pages"),
-            _dev_ptr(value_pages, pool_dtype, "value_pages"),
-            _dev_ptr(slot_mapping, torch.int32, "slot_mapping"), int(page_size), *scales, shape, raw)
+            None if q_weight is None else _ptr(q_weight, torch.bfloat16, dev, "q_weight"),
+            None if k_weight is None else _ptr(k_weight, torch.bfloat16, dev, "k_weight"), eps,
+            None if cos_sin is None else _ptr(cos_sin, torch.float32, dev, "cos_sin"), R, table_len,
+            1 if interleaved else 0,
+            None if cos_sin is None else _ptr(positions, torch.int32, dev, "positions"),
+            _ptr(query, torch.bfloat16, dev, "query"), _ptr(key_pages, pool_dtype, dev, "key_pages"),
+            _ptr(value_pages, pool_dtype, dev, "value_pages"),
+            _ptr(slot_mapping, torch.int32, dev, "slot_mapping"), page_size, *scales,
+            pa_shape(B, H_q, H_kv, D, L, P, 0), raw)
     return query
 
 
@@ -429,7 +432,7 @@ def pa_qk_norm_rope_append_fp8(qkv, q_weight, k_weight, cos_sin, positions, key_
     """pa_qk_norm_rope_append into uint8 e4m3 pools, code = e4m3(x / scale)."""
     return _qk_norm_rope_append(qkv, q_weight, k_weight, cos_sin, positions, key_pages,
                                 value_pages, slot_mapping, page_size,
-                                (float(k_scale), float(v_scale)), eps, interleaved, query, stream)
+                                (k_scale, v_scale), eps, interleaved, query, stream)
 
 
 def _kv_evict(what, pool_dtype, key_pages, value_pages, weight_pages, block_table, context_lens,
@@ -437,42 +440,38 @@ def _kv_evict(what, pool_dtype, key_pages, value_pages, weight_pages, block_tabl
     P, H_kv, ps, D = key_pages.shape
     if ps != page_size or value_pages.shape != key_pages.shape:
         raise ValueError("page pool shape does not match page_size")
-    if tuple(weight_pages.shape) != (P, H_kv, ps):
+    if weight_pages.shape != (P, H_kv, ps):
         raise ValueError("weight_pages must be [P, H_kv, page_size]")
     B = block_table.shape[0]
-    if block_table.dim() != 2 or tuple(context_lens.shape) != (B,):
+    if block_table.dim() != 2 or context_lens.shape != (B,):
         raise ValueError("block_table must be [B, max_pages] and context_lens [B]")
     dst = block_table if dst_block_table is None else dst_block_table
     if dst.dim() != 2 or dst.shape[0] != B:
         raise ValueError("dst_block_table must be [B, dst_max_pages]")
-    device = key_pages.device
-    if device.type != "cuda":
+    if not key_pages.is_cuda:
         raise ValueError("key_pages must be a CUDA tensor")
-    raw, guard = _on_device(device, stream, (
-        ("value_pages", value_pages), ("weight_pages", weight_pages), ("block_table", block_table),
-        ("context_lens", context_lens), ("dst_block_table", dst), ("kept", kept),
-        ("new_lens", new_lens)))
+    dev = key_pages.get_device()
+    raw, guard = _on_device(dev, stream)
     if kept is None:
-        kept = torch.empty((B, H_kv, max(int(keep), 0)), dtype=torch.int32, device=device)
+        kept = torch.empty((B, H_kv, max(int(keep), 0)), dtype=torch.int32, device=key_pages.device)
         _keep_for(kept, stream)
-    elif tuple(kept.shape) != (B, H_kv, keep):
+    elif kept.shape != (B, H_kv, keep):
         raise ValueError("kept must be [B, H_kv, keep]")
     if new_lens is None:
-        new_lens = torch.empty((B,), dtype=torch.int32, device=device)
+        new_lens = torch.empty((B,), dtype=torch.int32, device=key_pages.device)
         _keep_for(new_lens, stream)
-    elif tuple(new_lens.shape) != (B,):
+    elif new_lens.shape != (B,):
         raise ValueError("new_lens must be [B]")
     if B == 0:
         return kept, new_lens
-    shape = pa_shape(B, H_kv, H_kv, D, 1, P, block_table.shape[1])
-    _launch(getattr(_lib, what), what, guard, _dev_ptr(key_pages, pool_dtype, "key_pages"),
-            _dev_ptr(value_pages, pool_dtype, "value_pages"),
-            _dev_ptr(weight_pages, torch.float32, "weight_pages"),
-            _dev_ptr(block_table, torch.int32, "block_table"),
-            _dev_ptr(context_lens, torch.int32, "context_lens"), int(page_size), int(keep),
-            int(sinks), int(recent), _dev_ptr(dst, torch.int32, "dst_block_table"), dst.shape[1],
-            _dev_ptr(kept, torch.int32, "kept"), _dev_ptr(new_lens, torch.int32, "new_lens"), shape,
-            raw)
+    _launch(getattr(_lib, what), what, guard, _ptr(key_pages, pool_dtype, dev, "key_pages"),
+            _ptr(value_pages, pool_dtype, dev, "value_pages"),
+            _ptr(weight_pages, torch.float32, dev, "weight_pages"),
+            _ptr(block_table, torch.int32, dev, "block_table"),
+            _ptr(context_lens, torch.int32, dev, "context_lens"), page_size, keep, sinks, recent,
+            _ptr(dst, torch.int32, dev, "dst_block_table"), dst.shape[1],
+            _ptr(kept, torch.int32, dev, "kept"), _ptr(new_lens, torch.int32, dev, "new_lens"),
+            pa_shape(B, H_kv, H_kv, D, 1, P, block_table.shape[1]), raw)
     return kept, new_lens
 
 
@@ -502,53 +501,61 @@ def pa_kv_evict_fp8(key_pages, value_pages, weight_pages, block_table, context_l
 
 
 def _paged(query, key_pages, value_pages, block_table, context_lens, page_size, scale, out,
-           workspace, pool_dtype, stream, more=()):
-    """Checks shared by the attention calls below: (shape, the five leading
-    pointers, scale, out, raw stream, device guard)."""
-    B, H_q, L, D = query.shape
+           pool_dtype, stream):
+    """Checks shared by the attention calls below: (shape, the pointers of
+    query and pools, those of the tables, scale, out, its pointer, device index,
+    raw stream, device guard)."""
     if not query.is_cuda:
         raise ValueError("query must be a CUDA tensor")
-    if key_pages.dim() != 4 or key_pages.shape[2] != page_size or value_pages.shape != key_pages.shape:
+    B, H_q, L, D = query.shape
+    if key_pages.dim() != 4 or value_pages.shape != key_pages.shape:
+        raise ValueError("page pools must be [P, H_kv, page_size, D]")
+    P, H_kv, ps, D_pool = key_pages.shape
+    if ps != page_size:
         raise ValueError("page pool shape does not match page_size")
-    if block_table.dim() != 2 or block_table.shape[0] != B or tuple(context_lens.shape) != (B,):
+    if D_pool != D:
+        raise ValueError("query and pages disagree on head_dim")
+    if block_table.dim() != 2 or block_table.shape[0] != B or context_lens.shape != (B,):
         raise ValueError("block_table must be [B, max_pages] and context_lens [B]")
-    if scale is None:
-        scale = 1.0 / math.sqrt(D)
-    shape = make_shape(query.shape, key_pages.shape, block_table.shape[1])
-    device = query.device
-    raw, guard = _on_device(device, stream, (
-        ("key_pages", key_pages), ("value_pages", value_pages), ("block_table", block_table),
-        ("context_lens", context_lens), ("out", out), ("workspace", workspace)) + more)
-    ptrs = (_dev_ptr(query, torch.bfloat16, "query"), _dev_ptr(key_pages, pool_dtype, "key_pages"),
-            _dev_ptr(value_pages, pool_dtype, "value_pages"))
-    tables = (_dev_ptr(block_table, torch.int32, "block_table"),
-              _dev_ptr(context_lens, torch.int32, "context_lens"))
+    dev = query.get_device()
+    raw, guard = _on_device(dev, stream)
+    ptrs = (_ptr(query, torch.bfloat16, dev, "query"), _ptr(key_pages, pool_dtype, dev, "key_pages"),
+            _ptr(value_pages, pool_dtype, dev, "value_pages"))
+    tables = (_ptr(block_table, torch.int32, dev, "block_table"),
+              _ptr(context_lens, torch.int32, dev, "context_lens"))
     if out is None:
         out = torch.empty_like(query)
         _keep_for(out, stream)
     elif out.shape != query.shape:
         raise ValueError("out must have the query's shape")
-    return shape, ptrs, tables, float(scale), out, _dev_ptr(out, torch.bfloat16, "out"), raw, guard
+    return (pa_shape(B, H_q, H_kv, D, L, P, block_table.shape[1]), ptrs, tables,
+            1.0 / math.sqrt(D) if scale is None else scale, out,
+            _ptr(out, torch.bfloat16, dev, "out"), dev, raw, guard)
 
 
-def _sized(fn, guard, *args) -> int:
-    """A workspace size, asked of the library with the call's device current."""
-    if guard is None:
-        return int(fn(*args))
-    with guard:
-        return int(fn(*args))
-
-
-def _window(what, query, key_pages, value_pages, block_table, context_lens, page_size, scales,
-            window, sinks, scale, out, max_context_len, workspace, stream, size):
-    shape, ptrs, tables, scale, out, out_ptr, raw, guard = _paged(
-        query, key_pages, value_pages, block_table, context_lens, page_size, scale, out, workspace,
-        torch.uint8 if scales else torch.bfloat16, stream)
+def _workspace(workspace, size, guard, sizes, query, stream):
+    """(pointer, bytes, tensor) of the caller's workspace, or of one made for
+    this call with the bytes that the library's `size(*sizes)` names."""
     if workspace is None:
-        workspace = _scratch(size(shape, guard), query.device, stream)
-    _launch(getattr(_lib, what), what, guard, *ptrs, *tables, int(page_size), scale, *scales,
-            int(window), int(sinks), out_ptr, shape, int(max_context_len), workspace.data_ptr(),
-            workspace.numel() * workspace.element_size(), raw)
+        if guard is None:
+            need = size(*sizes)
+        else:
+            with guard:
+                need = size(*sizes)
+        workspace = _scratch(need, query.device, stream)
+    elif workspace.get_device() != query.get_device():
+        raise ValueError(f"workspace is on {workspace.device}, expected {query.device}")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
+
+
+def _window(fn, size, size_args, query, key_pages, value_pages, block_table, context_lens,
+            page_size, scales, window, sinks, scale, out, max_context_len, workspace, stream):
+    shape, ptrs, tables, scale, out, out_ptr, _, raw, guard = _paged(
+        query, key_pages, value_pages, block_table, context_lens, page_size, scale, out,
+        torch.uint8 if scales else torch.bfloat16, stream)
+    ws, ws_bytes, keep = _workspace(workspace, size, guard, (shape,) + size_args, query, stream)
+    _launch(fn, fn.__name__, guard, *ptrs, *tables, page_size, scale, *scales, window, sinks,
+            out_ptr, shape, max_context_len, ws, ws_bytes, raw)
     return out
 
 
@@ -559,9 +566,9 @@ def pa_decode_window(query: torch.Tensor, key_pages: torch.Tensor, value_pages: 
                      workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """pa_decode where the row at position p sees keys j <= p with
     j > p - window or j < sinks; pages that no row sees are not touched."""
-    return _window("pa_decode_window", query, key_pages, value_pages, block_table, context_lens,
-                   page_size, (), window, sinks, scale, out, max_context_len, workspace, stream,
-                   lambda shape, guard: _sized(_lib.pa_decode_workspace_bytes, guard, shape))
+    return _window(_lib.pa_decode_window, _lib.pa_decode_workspace_bytes, (), query, key_pages,
+                   value_pages, block_table, context_lens, page_size, (), window, sinks, scale, out,
+                   max_context_len, workspace, stream)
 
 
 def pa_decode_window_fp8(query, key_pages, value_pages, block_table, context_lens, page_size: int,
@@ -569,10 +576,9 @@ def pa_decode_window_fp8(query, key_pages, value_pages, block_table, context_len
                          scale: Optional[float] = None, out=None, max_context_len: int = 0,
                          workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """pa_decode_window over uint8 e4m3 pools."""
-    return _window("pa_decode_window_fp8", query, key_pages, value_pages, block_table,
-                   context_lens, page_size, (float(k_scale), float(v_scale)), window, sinks, scale,
-                   out, max_context_len, workspace, stream,
-                   lambda shape, guard: _sized(_lib.pa_decode_workspace_bytes, guard, shape))
+    return _window(_lib.pa_decode_window_fp8, _lib.pa_decode_workspace_bytes, (), query, key_pages,
+                   value_pages, block_table, context_lens, page_size, (k_scale, v_scale), window,
+                   sinks, scale, out, max_context_len, workspace, stream)
 
 
 def pa_prefill_window(query: torch.Tensor, key_pages: torch.Tensor, value_pages: torch.Tensor,
@@ -580,11 +586,11 @@ def pa_prefill_window(query: torch.Tensor, key_pages: torch.Tensor, value_pages:
                       window: int, sinks: int = 0, scale: Optional[float] = None,
                       out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """pa_decode_window's result on the tensor-core prefill kernel."""
-    shape, ptrs, tables, scale, out, out_ptr, raw, guard = _paged(
-        query, key_pages, value_pages, block_table, context_lens, page_size, scale, out, None,
+    shape, ptrs, tables, scale, out, out_ptr, _, raw, guard = _paged(
+        query, key_pages, value_pages, block_table, context_lens, page_size, scale, out,
         torch.bfloat16, stream)
-    _launch(_lib.pa_prefill_window, "pa_prefill_window", guard, *ptrs, *tables, int(page_size),
-            scale, int(window), int(sinks), out_ptr, shape, raw)
+    _launch(_lib.pa_prefill_window, "pa_prefill_window", guard, *ptrs, *tables, page_size, scale,
+            window, sinks, out_ptr, shape, raw)
     return out
 
 
@@ -613,11 +619,10 @@ def pa_attention_window(query: torch.Tensor, key_pages: torch.Tensor, value_page
                         workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """The dispatch: pa_decode_window for short queries, pa_prefill_window
     beyond."""
-    return _window("pa_attention_window", query, key_pages, value_pages, block_table, context_lens,
-                   page_size, (), window, sinks, scale, out, max_context_len, workspace, stream,
-                   lambda shape, guard: _sized(_lib.pa_attention_window_workspace_bytes, guard,
-                                               shape, int(page_size), int(max_context_len),
-                                               int(window), int(sinks)))
+    return _window(_lib.pa_attention_window, _lib.pa_attention_window_workspace_bytes,
+                   (page_size, max_context_len, window, sinks), query, key_pages, value_pages,
+                   block_table, context_lens, page_size, (), window, sinks, scale, out,
+                   max_context_len, workspace, stream)
 
 
 def pa_attention_window_fp8(query, key_pages, value_pages, block_table, context_lens,
@@ -629,12 +634,10 @@ def pa_attention_window_fp8(query, key_pages, value_pages, block_table, context_
     None reads context_lens.max() (a device-to-host copy)."""
     if max_context_len is None:
         max_context_len = int(context_lens.max().item())
-    return _window("pa_attention_window_fp8", query, key_pages, value_pages, block_table,
-                   context_lens, page_size, (float(k_scale), float(v_scale)), window, sinks, scale,
-                   out, max_context_len, workspace, stream,
-                   lambda shape, guard: _sized(_lib.pa_attention_window_fp8_workspace_bytes, guard,
-                                               shape, int(page_size), int(max_context_len),
-                                               int(window), int(sinks)))
+    return _window(_lib.pa_attention_window_fp8, _lib.pa_attention_window_fp8_workspace_bytes,
+                   (page_size, max_context_len, window, sinks), query, key_pages, value_pages,
+                   block_table, context_lens, page_size, (k_scale, v_scale), window, sinks, scale,
+                   out, max_context_len, workspace, stream)
 
 
 def pa_decode_weights_workspace_bytes(shape: pa_shape, max_context_len: int,
@@ -643,20 +646,18 @@ def pa_decode_weights_workspace_bytes(shape: pa_shape, max_context_len: int,
         return int(_lib.pa_decode_weights_workspace_bytes(shape, int(max_context_len)))
 
 
-def _weights(what, query, key_pages, value_pages, weight_pages, block_table, context_lens,
+def _weights(fn, query, key_pages, value_pages, weight_pages, block_table, context_lens,
              page_size, scales, max_context_len, decay, scale, causal, out, workspace, stream):
-    if tuple(weight_pages.shape) != tuple(key_pages.shape[:3]):
+    if weight_pages.shape != key_pages.shape[:3]:
         raise ValueError("weight_pages must be [P, H_kv, page_size]")
-    shape, ptrs, tables, scale, out, out_ptr, raw, guard = _paged(
-        query, key_pages, value_pages, block_table, context_lens, page_size, scale, out, workspace,
-        torch.uint8 if scales else torch.bfloat16, stream, (("weight_pages", weight_pages),))
-    if workspace is None:
-        workspace = _scratch(_sized(_lib.pa_decode_weights_workspace_bytes, guard, shape,
-                                    int(max_context_len)), query.device, stream)
-    _launch(getattr(_lib, what), what, guard, *ptrs,
-            _dev_ptr(weight_pages, torch.float32, "weight_pages"), *tables, int(page_size), scale,
-            *scales, int(bool(causal)), float(decay), out_ptr, shape, int(max_context_len),
-            workspace.data_ptr(), workspace.numel() * workspace.element_size(), raw)
+    shape, ptrs, tables, scale, out, out_ptr, dev, raw, guard = _paged(
+        query, key_pages, value_pages, block_table, context_lens, page_size, scale, out,
+        torch.uint8 if scales else torch.bfloat16, stream)
+    weights = _ptr(weight_pages, torch.float32, dev, "weight_pages")
+    ws, ws_bytes, keep = _workspace(workspace, _lib.pa_decode_weights_workspace_bytes, guard,
+                                    (shape, max_context_len), query, stream)
+    _launch(fn, fn.__name__, guard, *ptrs, weights, *tables, page_size, scale, *scales,
+            1 if causal else 0, decay, out_ptr, shape, max_context_len, ws, ws_bytes, raw)
     return out
 
 
@@ -671,7 +672,7 @@ def pa_decode_weights(query: torch.Tensor, key_pages: torch.Tensor, value_pages:
     got, summed over the group's heads and the rows (old: 0 for the L newest
     positions, and everywhere when decay is 0). max_context_len bounds
     context_lens."""
-    return _weights("pa_decode_weights", query, key_pages, value_pages, weight_pages, block_table,
+    return _weights(_lib.pa_decode_weights, query, key_pages, value_pages, weight_pages, block_table,
                     context_lens, page_size, (), max_context_len, decay, scale, causal, out,
                     workspace, stream)
 
@@ -682,9 +683,9 @@ def pa_decode_weights_fp8(query, key_pages, value_pages, weight_pages, block_tab
                           out=None, workspace: Optional[torch.Tensor] = None,
                           stream=None) -> torch.Tensor:
     """pa_decode_weights over uint8 e4m3 pools."""
-    return _weights("pa_decode_weights_fp8", query, key_pages, value_pages, weight_pages,
-                    block_table, context_lens, page_size, (float(k_scale), float(v_scale)),
-                    max_context_len, decay, scale, causal, out, workspace, stream)
+    return _weights(_lib.pa_decode_weights_fp8, query, key_pages, value_pages, weight_pages,
+                    block_table, context_lens, page_size, (k_scale, v_scale), max_context_len,
+                    decay, scale, causal, out, workspace, stream)
 
 
 def pa_decode_fp8(query, key_pages, value_pages, block_table, context_lens, page_size: int,

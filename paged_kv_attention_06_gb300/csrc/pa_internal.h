@@ -66,7 +66,7 @@ struct NormRopeArgs {
     unsigned* err;
     int32_t B, L, H_q, H_kv, D, ps_shift, num_pages;
     int32_t rotary_dim, table_len, interleaved;
-    int32_t gpt;                  // set by the launcher: lane groups per token
+    int32_t q_groups, kv_groups;  // set by the launcher: lane groups per token and kind
     int32_t fp8;
     float eps, k_scale, v_scale;
 };

@@ -15,12 +15,13 @@
 // code nearest to value / scale).
 //
 // Bound by memory: every element is read once and written once, ten
-// operations in between. A row (token, head) is held by D / 8 lanes, 16 bytes
-// each, so loads and stores are whole 32-byte sectors and the mean is a
-// shuffle tree; a group of lanes takes U heads of one token, all loads issued
-// before the first is used, and the token's angles are read once for the U
-// heads. In the half form an element's partner sits R / 16 lanes away: its raw
-// bf16 words come by shuffle.
+// operations in between. A row (token, head) is held by D / 8 lanes; in the
+// half form a lane holds four elements and their four partners, so the
+// rotation needs no exchange and half the angles that eight neighbours would
+// (8 bytes a load, each group of lanes still covering whole 128-byte lines). A
+// group of lanes takes U heads of one kind of one token: all loads are issued
+// before the first is used, and the products of weights and angles are made once
+// for the U heads, two elements to an instruction.
 #include <stdint.h>
 
 #include "pa_device.cuh"
@@ -29,41 +30,44 @@
 namespace pa {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 
-__device__ __forceinline__ float2 bf16x2_to_f32(uint32_t w)
+// Four bf16 -> two fp32 pairs, and back.
+__device__ __forceinline__ void unpack4(uint2 v, float2* x)
 {
-    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+    x[0] = make_float2(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xffff0000u));
+    x[1] = make_float2(__uint_as_float(v.y << 16), __uint_as_float(v.y & 0xffff0000u));
 }
-
-__device__ __forceinline__ void unpack8(uint4 v, float* x)
+__device__ __forceinline__ uint2 pack4(const float2* x)
 {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        const float2 f = bf16x2_to_f32(w[k]);
-        x[2 * k] = f.x;
-        x[2 * k + 1] = f.y;
+    return make_uint2(pack_bf16x2(x[0].x, x[0].y), pack_bf16x2(x[1].x, x[1].y));
+}
+// The e4m3 codes of four quotients x / scale (each rounded to fp32 first).
+// x * recip (recip = 1 / scale) is within 3 * 2^-24 of the quotient: where the
+// numbers 2^-21 below and above it have the same codes, so has the quotient,
+// and the division is not needed (it took a quarter of the kernel's time). recip
+// = 0: always divide.
+__device__ __forceinline__ uint32_t quantise4(const float2* x, float scale, float recip)
+{
+    if (recip != 0.f) {
+        const float2 r = make_float2(recip, recip);
+        const float2 q0 = __fmul2_rn(x[0], r), q1 = __fmul2_rn(x[1], r);
+        const float2 dn = make_float2(1.f - 0x1p-21f, 1.f - 0x1p-21f);
+        const float2 up = make_float2(1.f + 0x1p-21f, 1.f + 0x1p-21f);
+        const float2 d0 = __fmul2_rn(q0, dn), d1 = __fmul2_rn(q1, dn);
+        const float2 u0 = __fmul2_rn(q0, up), u1 = __fmul2_rn(q1, up);
+        const uint32_t lo = f32x2_to_e4m3x2(d0.x, d0.y) | (f32x2_to_e4m3x2(d1.x, d1.y) << 16);
+        const uint32_t hi = f32x2_to_e4m3x2(u0.x, u0.y) | (f32x2_to_e4m3x2(u1.x, u1.y) << 16);
+        if (lo == hi)
+            return lo;
     }
+    return f32x2_to_e4m3x2(__fdiv_rn(x[0].x, scale), __fdiv_rn(x[0].y, scale)) |
+           (f32x2_to_e4m3x2(__fdiv_rn(x[1].x, scale), __fdiv_rn(x[1].y, scale)) << 16);
 }
 
-__device__ __forceinline__ uint4 pack8(const float* x)
-{
-    return make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
-                      pack_bf16x2(x[6], x[7]));
-}
-
-__device__ __forceinline__ uint2 quantise8(const float* x, float scale)
-{
-    uint32_t c[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-        c[k] = f32x2_to_e4m3x2(__fdiv_rn(x[2 * k], scale), __fdiv_rn(x[2 * k + 1], scale));
-    return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
-}
-
-// One group of D / 8 lanes: heads j, j + gpt, ... (U of them at most) of one
-// token, gpt groups per token.
+// One group of D / 8 lanes: up to U neighbouring heads of one kind (queries,
+// keys or values) of one token; a.q_groups groups for the queries, a.kv_groups
+// each for keys and values.
 template <int D, int U, bool kInter, bool kF8>
 __global__ void __launch_bounds__(kThreads) norm_rope_append_kernel(const NormRopeArgs a)
 {
@@ -73,32 +77,53 @@ __global__ void __launch_bounds__(kThreads) norm_rope_append_kernel(const NormRo
     grid_launch_dependents();
     const int64_t group = (int64_t(blockIdx.x) * kThreads + threadIdx.x) / kLanes;
     const int c = threadIdx.x & (kLanes - 1);
-    const int H = a.H_q + 2 * a.H_kv;
-    const int64_t tok_u = udiv64(group, a.gpt);
-    const int j = int(group - tok_u * a.gpt);
+    const int per_token = a.q_groups + 2 * a.kv_groups;
+    const int64_t tok_u = udiv64(group, per_token);
+    const int j = int(group - tok_u * per_token);
+    const int kind = j < a.q_groups ? 0 : j < a.q_groups + a.kv_groups ? 1 : 2;   // q, k, v
+    const int h0 = (kind == 0 ? j : j - a.q_groups - (kind == 2 ? a.kv_groups : 0)) * U;
     // Groups past the last token stay for the shuffles and write nothing.
     const bool live = tok_u < int64_t(a.B) * a.L;
+    const int heads = live ? min(U, (kind == 0 ? a.H_q : a.H_kv) - h0) : 0;
     const int64_t tok = live ? tok_u : 0;
     const int b = int(udiv64(tok, a.L));
     const int i = int(tok - int64_t(b) * a.L);
-    const uint16_t* src = a.qkv + int64_t(b) * a.batch_stride + int64_t(i) * a.token_stride + c * 8;
+    // This lane's two runs of four elements, starting at e0 and e1. Half form:
+    // a run and its partners R / 2 further on, or two runs behind R.
+    // Interleaved form: eight neighbours.
+    const int R = a.rotary_dim;
+    const bool turns = kind < 2 && 8 * c < R;
+    const bool apart = !kInter && 8 * c < R;
+    const int e0 = apart ? 4 * c : 8 * c;
+    const int e1 = apart ? 4 * c + R / 2 : 8 * c + 4;
 
-    uint4 raw[U];
+    const uint16_t* src = a.qkv + int64_t(b) * a.batch_stride + int64_t(i) * a.token_stride +
+                          ((kind == 0 ? 0 : kind == 1 ? a.H_q : a.H_q + a.H_kv) + h0) * D;
+    uint2 raw[U][2];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-        const int h = j + u * a.gpt;
-        raw[u] = live && h < H ? *reinterpret_cast<const uint4*>(src + int64_t(h) * D)
-                               : make_uint4(0, 0, 0, 0);
+        raw[u][0] = raw[u][1] = make_uint2(0, 0);
+        if (u < heads) {
+            raw[u][0] = *reinterpret_cast<const uint2*>(src + u * D + e0);
+            raw[u][1] = *reinterpret_cast<const uint2*>(src + u * D + e1);
+        }
     }
     const int64_t slot = a.slot_mapping[tok];
-
-    // This lane's 8 angles: elements [8 c, 8 c + 8) of the row.
-    float cs[8], sn[8];
-    const int R = a.rotary_dim;
-    const bool turns = 8 * c < R;
-    const int half_lanes = R / 16;                       // lanes of half a rotation (half form)
-    const bool upper = !kInter && c >= half_lanes;       // holds the second elements of its pairs
-    if (R > 0) {
+    // The row is y = inv * (x A + p B), p the partners: with the weights w and
+    // the angles, A = w cos and B = +- w' sin, made once for the U heads.
+    // Half form: x[0..1] and x[2..3] are partners; interleaved form: the two of
+    // each pair.
+    float2 A[4], B[4];
+    const uint16_t* w = kind == 0 ? a.q_weight : kind == 1 ? a.k_weight : nullptr;
+    if (w != nullptr) {
+        unpack4(*reinterpret_cast<const uint2*>(w + e0), A);
+        unpack4(*reinterpret_cast<const uint2*>(w + e1), A + 2);
+    } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            A[k] = make_float2(1.f, 1.f);
+    }
+    if (R > 0 && kind < 2) {
         int pos = a.positions[tok];
         if (pos < 0 || pos >= a.table_len) {
             if (live && slot >= 0 && c == 0 && j == 0)
@@ -106,106 +131,97 @@ __global__ void __launch_bounds__(kThreads) norm_rope_append_kernel(const NormRo
             pos = pos < 0 ? 0 : a.table_len - 1;
         }
         if (turns) {
-            const float* row = a.cos_sin + int64_t(pos) * R;
-            if constexpr (kInter) {                      // angles 4 c .. 4 c + 3
-                const float4 p = *reinterpret_cast<const float4*>(row + 4 * c);
-                const float4 q = *reinterpret_cast<const float4*>(row + R / 2 + 4 * c);
-                cs[0] = p.x; cs[1] = p.y; cs[2] = p.z; cs[3] = p.w;
-                sn[0] = q.x; sn[1] = q.y; sn[2] = q.z; sn[3] = q.w;
+            const float* row = a.cos_sin + int64_t(pos) * R + 4 * c;    // angles 4 c .. 4 c + 3
+            const float4 cs = *reinterpret_cast<const float4*>(row);
+            const float4 sn = *reinterpret_cast<const float4*>(row + R / 2);
+            if constexpr (kInter) {
+                const float cc[4] = {cs.x, cs.y, cs.z, cs.w}, ss[4] = {sn.x, sn.y, sn.z, sn.w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    B[k] = make_float2(-A[k].y * ss[k], A[k].x * ss[k]);
+                    A[k] = make_float2(A[k].x * cc[k], A[k].y * cc[k]);
+                }
             } else {
-                const float* at = row + 8 * (upper ? c - half_lanes : c);
+                const float2 cc[2] = {make_float2(cs.x, cs.y), make_float2(cs.z, cs.w)};
+                const float2 ss[2] = {make_float2(sn.x, sn.y), make_float2(sn.z, sn.w)};
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
-                    const float4 p = *reinterpret_cast<const float4*>(at + 4 * k);
-                    const float4 q = *reinterpret_cast<const float4*>(at + R / 2 + 4 * k);
-                    cs[4 * k] = p.x; cs[4 * k + 1] = p.y; cs[4 * k + 2] = p.z; cs[4 * k + 3] = p.w;
-                    sn[4 * k] = q.x; sn[4 * k + 1] = q.y; sn[4 * k + 2] = q.z; sn[4 * k + 3] = q.w;
+                    B[k] = make_float2(-A[2 + k].x * ss[k].x, -A[2 + k].y * ss[k].y);
+                    B[2 + k] = make_float2(A[k].x * ss[k].x, A[k].y * ss[k].y);
+                    A[k] = make_float2(A[k].x * cc[k].x, A[k].y * cc[k].y);
+                    A[2 + k] = make_float2(A[2 + k].x * cc[k].x, A[2 + k].y * cc[k].y);
                 }
             }
         }
     }
-    // The slot's row offset in the pools (element of head 0), or -1.
-    int64_t dst = -1;
-    if (live && slot >= 0) {
+    // Where head h0's row goes (elements), and the step from head to head.
+    uint16_t* to = a.query;
+    int64_t at = ((int64_t(b) * a.H_q + h0) * a.L + i) * D, head_step = int64_t(a.L) * D;
+    int stored = heads;
+    if (kind > 0) {
+        to = kind == 1 ? a.key_pages : a.value_pages;
+        head_step = int64_t(D) << a.ps_shift;
         const int64_t page = slot >> a.ps_shift;
-        if (page >= a.num_pages) {
-            if (c == 0 && j == 0)
+        if (slot < 0 || page >= a.num_pages) {
+            if (slot >= 0 && live && c == 0 && h0 == 0)
                 atomicOr(a.err, PA_DEVERR_SLOT_BIT);
+            stored = 0;
         } else {
-            dst = ((page * a.H_kv << a.ps_shift) + (slot & ((1 << a.ps_shift) - 1))) * D + c * 8;
+            at = (((page * a.H_kv + h0) << a.ps_shift) + (slot & ((1 << a.ps_shift) - 1))) * D;
         }
     }
-    const int partner = !turns ? c : upper ? c - half_lanes : c + half_lanes;   // half form
+    const bool quantised = kF8 && kind > 0;
+    const float scale = kind == 1 ? a.k_scale : a.v_scale;
+    // (scales far out, where 1 / scale is not a normal number, divide)
+    const float recip = quantised && scale > 0x1p-100f && scale < 0x1p100f ? __fdiv_rn(1.f, scale) : 0.f;
+    const bool normed = __any_sync(0xffffffffu, w != nullptr);
 
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-        const int h = j + u * a.gpt;
-        const int kind = h < a.H_q ? 0 : h < a.H_q + a.H_kv ? 1 : 2;   // q, k, v
-        float x[8];
-        unpack8(raw[u], x);
-        float sum = 0.f;
+        float2 x[4];
+        unpack4(raw[u][0], x);
+        unpack4(raw[u][1], x + 2);
+        float inv = 1.f;
+        if (normed) {
+            float2 s2 = __fmul2_rn(x[0], x[0]);
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-            sum = fmaf(x[k], x[k], sum);
+            for (int k = 1; k < 4; ++k)
+                s2 = __ffma2_rn(x[k], x[k], s2);
+            float sum = s2.x + s2.y;
 #pragma unroll
-        for (int o = kLanes / 2; o > 0; o >>= 1)
-            sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        uint4 other = make_uint4(0, 0, 0, 0);
-        if constexpr (!kInter) {
-            other.x = __shfl_sync(0xffffffffu, raw[u].x, partner, kLanes);
-            other.y = __shfl_sync(0xffffffffu, raw[u].y, partner, kLanes);
-            other.z = __shfl_sync(0xffffffffu, raw[u].z, partner, kLanes);
-            other.w = __shfl_sync(0xffffffffu, raw[u].w, partner, kLanes);
+            for (int o = kLanes / 2; o > 0; o >>= 1)
+                sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            if (w != nullptr)
+                inv = rsqrtf(sum * (1.f / D) + a.eps);
         }
-        if (!live || h >= H)
+        if (u >= stored)
             continue;
+        uint2 out[2] = {raw[u][0], raw[u][1]};       // values of bf16 pools: as they are
         if (kind < 2) {
-            const uint16_t* w = kind == 0 ? a.q_weight : a.k_weight;
-            float y[8];                                  // the partners, normed
-            if constexpr (!kInter)
-                unpack8(other, y);
-            if (w != nullptr) {
-                const float inv = rsqrtf(sum * (1.f / D) + a.eps);
-                float wx[8];
-                unpack8(*reinterpret_cast<const uint4*>(w + 8 * c), wx);
+            const float2 inv2 = make_float2(inv, inv);
+            float2 y[4];
 #pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    x[k] = x[k] * inv * wx[k];
-                if constexpr (!kInter) {
-                    unpack8(*reinterpret_cast<const uint4*>(w + 8 * partner), wx);
-#pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        y[k] = y[k] * inv * wx[k];
-                }
-            }
+            for (int k = 0; k < 4; ++k)
+                y[k] = __fmul2_rn(x[k], A[k]);
             if (turns) {
-                if constexpr (kInter) {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const float p = x[2 * k], q = x[2 * k + 1];
-                        x[2 * k] = p * cs[k] - q * sn[k];
-                        x[2 * k + 1] = q * cs[k] + p * sn[k];
-                    }
-                } else {
-#pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        x[k] = upper ? x[k] * cs[k] + y[k] * sn[k] : x[k] * cs[k] - y[k] * sn[k];
-                }
+                for (int k = 0; k < 4; ++k)
+                    y[k] = __ffma2_rn(kInter ? make_float2(x[k].y, x[k].x) : x[k ^ 2], B[k], y[k]);
             }
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                x[k] = __fmul2_rn(y[k], inv2);
+            out[0] = pack4(x);
+            out[1] = pack4(x + 2);
         }
-        if (kind == 0) {
-            uint16_t* q = a.query + ((int64_t(b) * a.H_q + h) * a.L + i) * D + c * 8;
-            *reinterpret_cast<uint4*>(q) = pack8(x);
-        } else if (dst >= 0) {
-            const int hk = h - a.H_q - (kind == 2 ? a.H_kv : 0);
-            const int64_t at = dst + (int64_t(hk) << a.ps_shift) * D;
-            if constexpr (kF8) {
-                uint8_t* pool = reinterpret_cast<uint8_t*>(kind == 1 ? a.key_pages : a.value_pages);
-                *reinterpret_cast<uint2*>(pool + at) = quantise8(x, kind == 1 ? a.k_scale : a.v_scale);
-            } else {
-                uint16_t* pool = kind == 1 ? a.key_pages : a.value_pages;
-                *reinterpret_cast<uint4*>(pool + at) = kind == 2 ? raw[u] : pack8(x);
-            }
+        if (quantised) {
+            uint8_t* row = reinterpret_cast<uint8_t*>(to) + at + u * head_step;
+            *reinterpret_cast<uint32_t*>(row + e0) = quantise4(x, scale, recip);
+            *reinterpret_cast<uint32_t*>(row + e1) = quantise4(x + 2, scale, recip);
+        } else {
+            uint16_t* row = to + at + u * head_step;
+            *reinterpret_cast<uint2*>(row + e0) = out[0];
+            *reinterpret_cast<uint2*>(row + e1) = out[1];
         }
     }
 }
@@ -233,8 +249,9 @@ cudaError_t launch_norm_rope_append(NormRopeArgs a, cudaStream_t stream)
     // One head per group while that still leaves the GPU short of threads.
     const bool few = tokens * H * lanes < int64_t(256) * 1024;
     const int U = few ? 1 : kHeads;
-    a.gpt = (H + U - 1) / U;
-    const int64_t blocks = (tokens * a.gpt * lanes + kThreads - 1) / kThreads;
+    a.q_groups = (a.H_q + U - 1) / U;
+    a.kv_groups = (a.H_kv + U - 1) / U;
+    const int64_t blocks = (tokens * (a.q_groups + 2 * a.kv_groups) * lanes + kThreads - 1) / kThreads;
     if (blocks >= (int64_t(1) << 31))
         return cudaErrorInvalidValue;
     const void* fn = a.D == 64 ? (few ? kernel_for<64, 1>(a.interleaved, a.fp8) : kernel_for<64, kHeads>(a.interleaved, a.fp8))
