@@ -24,7 +24,9 @@ _API = ("pa_append_kv", "pa_decode", "pa_prefill", "pa_attention", "pa_attention
 def __getattr__(name):
     if name in _API or name.startswith("PA_"):
         from . import binding
-        return getattr(binding, name)
+        value = getattr(binding, name)
+        globals()[name] = value      # found directly from now on
+        return value
     raise AttributeError(name)
 
 

@@ -318,7 +318,7 @@ def _on_device(device_index: int, stream):
     """(raw stream, guard or None): the given stream or the device's current
     one, and a guard that makes the device current where it is not."""
     raw = torch._C._cuda_getCurrentRawStream(device_index) if stream is None else _stream(stream)
-    guard = None if torch.cuda.current_device() == device_index else torch.cuda.device(device_index)
+    guard = None if torch._C._cuda_getDevice() == device_index else torch.cuda.device(device_index)
     return raw, guard
 
 
@@ -328,7 +328,7 @@ def _launch(fn, what: str, guard, *args) -> None:
     else:
         with guard:
             st = fn(*args)
-    if st != PA_OK:
+    if st:
         raise PagedAttentionError(st, what)
 
 
