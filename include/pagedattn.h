@@ -443,9 +443,13 @@ pa_status pa_attention(const void *query, const void *key_pages,
  * back the pages between the sinks and the window. Within the pages that are
  * read, slots that no row of the call sees may hold any bytes; a slot that one
  * row sees and another does not has to hold numbers (0 * NaN in P . V).
- * Other arguments, the workspace (pa_decode_workspace_bytes) and the errors as
- * for pa_decode / pa_decode_fp8.
+ * workspace: pa_decode_window_workspace_bytes(shape) bytes (0: invalid shape),
+ * 16-byte aligned, any contents; calls that share one must not overlap on the
+ * GPU. Other arguments and the errors as for pa_decode / pa_decode_fp8.
+ * Up to 16 rows per request and KV head (G * L) take a kernel of their own,
+ * in one launch; more take pa_decode's.
  */
+size_t pa_decode_window_workspace_bytes(pa_shape shape);
 pa_status pa_decode_window(const void *query, const void *key_pages, const void *value_pages,
                            const int32_t *block_table, const int32_t *context_lens,
                            int32_t page_size, float scale, int32_t window, int32_t sinks,

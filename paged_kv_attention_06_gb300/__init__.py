@@ -16,7 +16,7 @@ _API = ("pa_append_kv", "pa_decode", "pa_prefill", "pa_attention", "pa_attention
         "pa_prefill_fp8_workspace_bytes", "pa_attention_fp8",
         "pa_qk_norm_rope_append", "pa_qk_norm_rope_append_fp8",
         "pa_kv_evict", "pa_kv_evict_fp8", "pa_decode_window", "pa_decode_window_fp8",
-        "pa_prefill_window", "pa_attention_window", "pa_attention_window_fp8",
+        "pa_decode_window_workspace_bytes", "pa_prefill_window", "pa_attention_window", "pa_attention_window_fp8",
         "pa_attention_window_workspace_bytes", "pa_attention_window_fp8_workspace_bytes",
         "pa_decode_weights", "pa_decode_weights_fp8", "pa_decode_weights_workspace_bytes")
 

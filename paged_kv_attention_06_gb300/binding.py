@@ -143,6 +143,8 @@ def _load() -> ctypes.CDLL:
     lib.pa_decode_window.restype = ctypes.c_int
     lib.pa_decode_window_fp8.argtypes = tables + [f32, f32, i32, i32] + tail
     lib.pa_decode_window_fp8.restype = ctypes.c_int
+    lib.pa_decode_window_workspace_bytes.argtypes = [pa_shape]
+    lib.pa_decode_window_workspace_bytes.restype = sz
     lib.pa_prefill_window.argtypes = tables + [i32, i32, vp, pa_shape, vp]
     lib.pa_prefill_window.restype = ctypes.c_int
     lib.pa_attention_window.argtypes = tables + [i32, i32] + tail
@@ -566,7 +568,7 @@ def pa_decode_window(query: torch.Tensor, key_pages: torch.Tensor, value_pages: 
                      workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """pa_decode where the row at position p sees keys j <= p with
     j > p - window or j < sinks; pages that no row sees are not touched."""
-    return _window(_lib.pa_decode_window, _lib.pa_decode_workspace_bytes, (), query, key_pages,
+    return _window(_lib.pa_decode_window, _lib.pa_decode_window_workspace_bytes, (), query, key_pages,
                    value_pages, block_table, context_lens, page_size, (), window, sinks, scale, out,
                    max_context_len, workspace, stream)
 
@@ -576,9 +578,14 @@ def pa_decode_window_fp8(query, key_pages, value_pages, block_table, context_len
                          scale: Optional[float] = None, out=None, max_context_len: int = 0,
                          workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """pa_decode_window over uint8 e4m3 pools."""
-    return _window(_lib.pa_decode_window_fp8, _lib.pa_decode_workspace_bytes, (), query, key_pages,
+    return _window(_lib.pa_decode_window_fp8, _lib.pa_decode_window_workspace_bytes, (), query, key_pages,
                    value_pages, block_table, context_lens, page_size, (k_scale, v_scale), window,
                    sinks, scale, out, max_context_len, workspace, stream)
+
+
+def pa_decode_window_workspace_bytes(shape: pa_shape, device: Optional[torch.device] = None) -> int:
+    with torch.cuda.device(device if device is not None else torch.cuda.current_device()):
+        return int(_lib.pa_decode_window_workspace_bytes(shape))
 
 
 def pa_prefill_window(query: torch.Tensor, key_pages: torch.Tensor, value_pages: torch.Tensor,

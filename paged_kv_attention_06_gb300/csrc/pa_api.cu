@@ -132,6 +132,7 @@ struct MapCacheEntry {
     const void* pool;
     uint64_t rows;
     int32_t D, ps;
+    int box_rows;
     bool fp8;
     bool valid;
 };
@@ -140,23 +141,25 @@ thread_local MapCacheEntry t_map_cache[kMapCache];
 thread_local int t_map_next = 0;
 
 pa_status encode_pool_map_uncached(CUtensorMap* map, const void* pool, const pa_shape& s,
-                                   int32_t ps, bool fp8);
+                                   int32_t ps, bool fp8, int box_rows);
 
 // 2-D view of a page pool: rows = P * H_kv * page_size, columns = D (bf16
 // elements, or e4m3 codes of one byte when fp8).
 pa_status encode_pool_map(CUtensorMap* map, const void* pool, const pa_shape& s, int32_t ps,
-                          bool fp8 = false)
+                          bool fp8 = false, int box_rows = 0)
 {
+    if (box_rows == 0)
+        box_rows = ps < kDecodeTokens ? ps : kDecodeTokens;
     const uint64_t rows = uint64_t(s.num_pages) * s.num_kv_heads * ps;
     for (int i = 0; i < kMapCache; ++i) {
         const MapCacheEntry& e = t_map_cache[i];
         if (e.valid && e.pool == pool && e.rows == rows && e.D == s.head_dim && e.ps == ps &&
-            e.fp8 == fp8) {
+            e.fp8 == fp8 && e.box_rows == box_rows) {
             *map = e.map;
             return PA_OK;
         }
     }
-    pa_status st = encode_pool_map_uncached(map, pool, s, ps, fp8);
+    pa_status st = encode_pool_map_uncached(map, pool, s, ps, fp8, box_rows);
     if (st == PA_OK) {
         MapCacheEntry& e = t_map_cache[t_map_next];
         t_map_next = (t_map_next + 1) % kMapCache;
@@ -166,13 +169,14 @@ pa_status encode_pool_map(CUtensorMap* map, const void* pool, const pa_shape& s,
         e.D = s.head_dim;
         e.ps = ps;
         e.fp8 = fp8;
+        e.box_rows = box_rows;
         e.valid = true;
     }
     return st;
 }
 
 pa_status encode_pool_map_uncached(CUtensorMap* map, const void* pool, const pa_shape& s,
-                                   int32_t ps, bool fp8)
+                                   int32_t ps, bool fp8, int box_rows)
 {
     PFN_cuTensorMapEncodeTiled_v12000 enc;
     pa_status st = get_encoder(&enc);
@@ -181,7 +185,6 @@ pa_status encode_pool_map_uncached(CUtensorMap* map, const void* pool, const pa_
     const cuuint64_t dims[2] = {cuuint64_t(s.head_dim),
                                 cuuint64_t(s.num_pages) * s.num_kv_heads * ps};
     const cuuint64_t strides[1] = {cuuint64_t(s.head_dim) * (fp8 ? 1 : 2)};
-    const int box_rows = ps < kDecodeTokens ? ps : kDecodeTokens;
     // a box row is 128 bytes: 64 bf16 or 128 e4m3 codes
     const cuuint32_t box[2] = {fp8 ? 128u : 64u, cuuint32_t(box_rows)};
     const cuuint32_t estr[2] = {1u, 1u};
@@ -511,6 +514,7 @@ pa_status run_split_kv(const void* query, const void* key_pages, const void* val
 
     const int grid_max = decode_max_grid(dev->sm_count);
     int64_t grid = grid_max;
+    int64_t granules = 0;                  // of 64 keys, at most
     if (whole_segments) {
         grid = nseg < grid_max ? nseg : grid_max;
     } else if (max_context_len > 0) {
@@ -522,27 +526,27 @@ pa_status run_split_kv(const void* query, const void* key_pages, const void* val
                 (int64_t(extra.window) + s.q_len + 2 * kDecodeTokens - 3) / kDecodeTokens;
             gran = std::min(gran, runs);
         }
-        const int64_t bound = nseg * (gran > 0 ? gran : 1);
-        if (bound < grid)
-            grid = bound;
+        granules = nseg * (gran > 0 ? gran : 1);
+        if (granules < grid)
+            grid = granules;
     }
     if (grid < 1)
         grid = 1;
 
+    const bool rows = extra.mode != kFull && !whole_segments &&
+                      decode_rows_takes(s, dev->max_smem_optin);
     DecodeArgs a;
     memset(&a, 0, sizeof a);
-    if (!whole_segments) {
+    if (rows) {
+        if (!workspace || workspace_bytes < decode_rows_workspace_bytes(s, dev->sm_count) ||
+            (reinterpret_cast<uintptr_t>(workspace) & 15u))
+            return PA_ERR_WORKSPACE;
+    } else if (!whole_segments) {
         const size_t need = decode_workspace_bytes(nseg, grid_max, s.head_dim, plan.TG);
         if (!workspace || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 15u))
             return PA_ERR_WORKSPACE;
         a.partials = static_cast<float*>(workspace);
     }
-    CUtensorMap kmap, vmap;
-    if ((st = encode_pool_map(&kmap, key_pages, s, page_size, fp8 != 0)) != PA_OK)
-        return st;
-    if ((st = encode_pool_map(&vmap, value_pages, s, page_size, fp8 != 0)) != PA_OK)
-        return st;
-
     a.q = static_cast<const uint16_t*>(query);
     a.out = static_cast<uint16_t*>(out);
     a.block_table = block_table;
@@ -577,8 +581,27 @@ pa_status run_split_kv(const void* query, const void* key_pages, const void* val
     a.row_state = extra.row_state;
     a.score_stride = extra.score_stride;
     a.score_cap = extra.score_cap;
+    if (rows) {
+        CUtensorMap kmap, vmap;
+        a.box_rows = decode_rows_box(s, fp8 != 0, page_size);
+        a.swz = a.box_rows >= 8 ? 7 : 0;
+        if ((st = encode_pool_map(&kmap, key_pages, s, page_size, fp8 != 0, a.box_rows)) != PA_OK ||
+            (st = encode_pool_map(&vmap, value_pages, s, page_size, fp8 != 0, a.box_rows)) != PA_OK)
+            return st;
+        while ((1 << a.ps_shift) < page_size)
+            ++a.ps_shift;
+        return launch_decode_rows(kmap, vmap, a, s, max_context_len > 0 ? granules : 0, workspace, dev->id,
+                                  dev->sm_count, stream) == cudaSuccess
+                   ? PA_OK
+                   : PA_ERR_CUDA;
+    }
     a.debug_unset_wait = t_arm_unset_wait ? 1 : 0;
     t_arm_unset_wait = false;
+    CUtensorMap kmap, vmap;
+    if ((st = encode_pool_map(&kmap, key_pages, s, page_size, fp8 != 0)) != PA_OK)
+        return st;
+    if ((st = encode_pool_map(&vmap, value_pages, s, page_size, fp8 != 0)) != PA_OK)
+        return st;
     CUtensorMap qmap;
     const uint64_t q_rows = uint64_t(s.batch) * s.num_q_heads * s.q_len;
     if ((st = encode_rows_map(&qmap, query, q_rows, uint32_t(kDecodeRows), uint32_t(s.head_dim))) !=
@@ -1213,7 +1236,7 @@ pa_status plan_weights(const pa_shape& s, int32_t max_context_len, WeightPlan* p
 {
     if (max_context_len <= 0)
         return PA_ERR_INVALID_ARG;
-    const size_t decode = pa_decode_workspace_bytes(s);
+    const size_t decode = pa_decode_window_workspace_bytes(s);   // the same kernels
     if (decode == 0)
         return PA_ERR_UNSUPPORTED;
     p->stride = (int64_t(max_context_len) + 63) / 64 * 64;
@@ -1290,6 +1313,16 @@ pa_status run_decode_weights(const void* query, const void* key_pages, const voi
 
 }  // namespace
 
+size_t pa_decode_window_workspace_bytes(pa_shape shape)
+{
+    const size_t many = pa_decode_workspace_bytes(shape);
+    DeviceInfo* dev;
+    if (many == 0 || device_info(&dev) != PA_OK)
+        return 0;
+    return decode_rows_takes(shape, dev->max_smem_optin) ? decode_rows_workspace_bytes(shape, dev->sm_count)
+                                                         : many;
+}
+
 pa_status pa_decode_window(const void* query, const void* key_pages, const void* value_pages,
                            const int32_t* block_table, const int32_t* context_lens,
                            int32_t page_size, float scale, int32_t window, int32_t sinks, void* out,
@@ -1345,7 +1378,7 @@ size_t pa_attention_window_workspace_bytes(pa_shape shape, int32_t page_size,
     if (!pow2_in(page_size, 1, 256) || window <= 0 || sinks < 0 || max_context_len < 0)
         return 0;
     return pa_attention_route(shape, window_reach(shape, max_context_len, window, sinks)) == 0
-               ? pa_decode_workspace_bytes(shape)
+               ? pa_decode_window_workspace_bytes(shape)
                : 0;
 }
 
@@ -1377,7 +1410,7 @@ size_t pa_attention_window_fp8_workspace_bytes(pa_shape shape, int32_t page_size
     if (!pow2_in(page_size, 1, 256) || route < 0 || shape.head_dim != 128 || window <= 0 || sinks < 0 || max_context_len < 0)
         return 0;
     if (route == 0)
-        return pa_decode_workspace_bytes(shape);
+        return pa_decode_window_workspace_bytes(shape);
     WindowCopyPlan p;
     return plan_window_copy(shape, max_context_len, std::min(window, 1 << 30),
                             std::min(sinks, 1 << 30), &p) == PA_OK

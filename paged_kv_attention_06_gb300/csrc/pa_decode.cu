@@ -49,6 +49,7 @@
 
 #include "pa_device.cuh"
 #include "pa_internal.h"
+#include "pa_split.cuh"
 
 namespace pa {
 namespace {
@@ -88,15 +89,6 @@ struct Layout {
     static constexpr int kPrefix = kMisc + 32;
     static size_t bytes(int B) { return kPrefix + size_t(2 * B + 1) * 4 + 1024; }
 };
-
-__device__ __forceinline__ int clamp_context(int n, int cap, unsigned* err)
-{
-    if (n < 0 || n > cap) {
-        atomicOr(err, PA_DEVERR_CONTEXT_LEN_BIT);
-        n = n < 0 ? 0 : cap;
-    }
-    return n;
-}
 
 // Longest context: what the block table holds, and with kScores the rows of
 // scores too.
@@ -160,37 +152,6 @@ __device__ __forceinline__ bool hidden(const DecodeArgs& a, int tok, int low, bo
     return false;
 }
 
-struct SegmentPos {
-    int b, h, ms, seg;  // request, KV head, segment within the (b, h) rows
-    int64_t seg_start;  // first granule of the segment in the stream
-    int seg_len;        // granules in the segment
-};
-
-// The segment hm (0 <= hm < per_req) of request b. pre[b] = first granule of
-// request b, gbr[b] = granules in each of its segments.
-__device__ __forceinline__ SegmentPos segment_at(const int32_t* pre, const int32_t* gbr,
-                                                 int per_req, int MS, int b, int hm)
-{
-    SegmentPos s;
-    s.b = b;
-    s.h = MS == 1 ? hm : hm / MS;
-    s.ms = hm - s.h * MS;
-    s.seg = b * per_req + hm;
-    s.seg_len = gbr[b];
-    s.seg_start = pre[b] + int64_t(hm) * s.seg_len;
-    return s;
-}
-
-// The segment after s in the stream (segments are in (request, KV head, row
-// tile group) order and none is empty).
-__device__ __forceinline__ SegmentPos next_segment(const int32_t* pre, const int32_t* gbr,
-                                                   int per_req, int MS, const SegmentPos& s)
-{
-    const int hm = s.seg - s.b * per_req + 1;
-    return hm < per_req ? segment_at(pre, gbr, per_req, MS, s.b, hm)
-                        : segment_at(pre, gbr, per_req, MS, s.b + 1, 0);
-}
-
 // The split over blocks weighs each segment as its granules plus pu units
 // (DecodeArgs::piece_units): a piece costs a block more than its granules (the
 // first granule's Q tile, the partial tail granule, the epilogue; for e4m3
@@ -204,62 +165,6 @@ __device__ __forceinline__ SegmentPos next_segment(const int32_t* pre, const int
 // three on e4m3 pools (measured on 128-token pages: 79.9 us with 1, 63.4
 // with 3).
 __host__ __device__ constexpr int piece_units(bool f8) { return f8 ? 3 : 1; }
-
-// Block index that processes the granule at unit position u.
-__device__ __forceinline__ int64_t block_of_unit(int64_t u, int64_t units, int64_t grid)
-{
-    return udiv64((u + 1) * grid - 1, units);
-}
-
-// First granule whose unit position is >= u (the granule count if none),
-// and the request b and segment hm within it that hold that granule (b = B
-// if none), for the two unit positions u0 <= u1 at once (the two searches
-// and their divisions interleave). Called by whole warps.
-struct StreamPoint {
-    int64_t x;
-    int b, hm;
-};
-__device__ __forceinline__ void granules_at_units(const int32_t* pre, const int32_t* gbr, int B,
-                                                  int per_req, int64_t u0, int64_t u1,
-                                                  int64_t units, int pu, StreamPoint& p0,
-                                                  StreamPoint& p1)
-{
-    const int lane = threadIdx.x & 31;
-    const int64_t per_b = int64_t(pu) * per_req;
-    auto pre_u = [&](int b) { return int64_t(pre[b]) + per_b * b; };
-    // largest b with pre_u(b) <= u, for both u (pre_u(0) = 0 <= u); each
-    // round samples 32 evenly spaced candidates of the remaining range, so
-    // B <= 32 takes one round of one shared-memory read per lane
-    int lo0 = 0, n0 = B, lo1 = 0, n1 = B;
-    while (n0 > 32 || n1 > 32) {
-        const int s0 = (n0 + 31) >> 5, s1 = (n1 + 31) >> 5;
-        const bool ok0 = lane * s0 < n0 && pre_u(lo0 + lane * s0) <= u0;
-        const bool ok1 = lane * s1 < n1 && pre_u(lo1 + lane * s1) <= u1;
-        const int l0 = 31 - __clz(__ballot_sync(0xffffffffu, ok0));
-        const int l1 = 31 - __clz(__ballot_sync(0xffffffffu, ok1));
-        lo0 += l0 * s0;
-        n0 = min(s0, n0 - l0 * s0);
-        lo1 += l1 * s1;
-        n1 = min(s1, n1 - l1 * s1);
-    }
-    const bool ok0 = lane < n0 && pre_u(lo0 + lane) <= u0;
-    const bool ok1 = lane < n1 && pre_u(lo1 + lane) <= u1;
-    lo0 += 31 - __clz(__ballot_sync(0xffffffffu, ok0));
-    lo1 += 31 - __clz(__ballot_sync(0xffffffffu, ok1));
-    auto finish = [&](int lo, int64_t u, StreamPoint& p) {
-        if (u >= units) {
-            p = StreamPoint{pre[B], B, 0};
-            return;
-        }
-        const int gb = gbr[lo];
-        const int64_t r = u - pre_u(lo);
-        const int64_t hm = udiv64(r, gb + pu);
-        const int64_t in = r - hm * (gb + pu) - pu;
-        p = StreamPoint{pre[lo] + hm * gb + (in > 0 ? in : 0), lo, int(hm)};
-    };
-    finish(lo0, u0, p0);
-    finish(lo1, u1, p1);
-}
 
 // kMode: kFull, kWindow (Span above), or kScores (the scores of every row and
 // the row states go to the workspace too, for the accumulation of weights).
@@ -1418,6 +1323,7 @@ using DecodeKernel = void (*)(CUtensorMap, CUtensorMap, CUtensorMap, DecodeArgs)
 
 // The instantiation for (head_dim, e4m3 pages, row tiles per segment), with
 // its index in the table of raised shared-memory limits.
+// One bf16 row tile is the few-row kernel's with a window or scores.
 template <int kMode>
 DecodeKernel decode_kernel_of(int D, bool fp8, int TG, int* index)
 {
@@ -1427,11 +1333,12 @@ DecodeKernel decode_kernel_of(int D, bool fp8, int TG, int* index)
     }
     const int t = TG == 4 ? 2 : TG == 2 ? 1 : 0;
     *index = 1 + (D == 64 ? 0 : 3) + t;
-    if (D == 64)
-        return t == 2 ? decode_kernel<64, false, 4, kMode> : t == 1 ? decode_kernel<64, false, 2, kMode>
-                                                                     : decode_kernel<64, false, 1, kMode>;
-    return t == 2 ? decode_kernel<128, false, 4, kMode> : t == 1 ? decode_kernel<128, false, 2, kMode>
-                                                                  : decode_kernel<128, false, 1, kMode>;
+    if (t > 0)
+        return D == 64 ? (t == 2 ? decode_kernel<64, false, 4, kMode> : decode_kernel<64, false, 2, kMode>)
+                       : (t == 2 ? decode_kernel<128, false, 4, kMode> : decode_kernel<128, false, 2, kMode>);
+    if constexpr (kMode == kFull)
+        return D == 64 ? decode_kernel<64, false, 1, kFull> : decode_kernel<128, false, 1, kFull>;
+    return nullptr;
 }
 
 DecodeKernel decode_kernel_for(int mode, int D, bool fp8, int TG, int* index)
@@ -1470,6 +1377,8 @@ cudaError_t launch_decode(const CUtensorMap& key_map, const CUtensorMap& value_m
     const DecodeKernel kern = decode_kernel_for(a.mode, a.D, fp8, a.TG, &di);
     if (device < 0 || device >= kMaxDev)
         return cudaErrorInvalidDevice;
+    if (kern == nullptr)
+        return cudaErrorInvalidValue;
     if (smem_set[device][di].load(std::memory_order_relaxed) < smem) {
         cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(kern),
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, smem);

@@ -168,6 +168,11 @@ struct DecodeArgs {
     float2* row_state;  // kScores: [B * H_kv][R] (max, sum)
     int64_t score_stride;      // a multiple of 64, at least score_cap
     int32_t score_cap;         // kScores: longest context
+    // The few-row kernel: log2 of the page size, and one arrival word per segment
+    // with the launch's stamp.
+    int32_t ps_shift;
+    unsigned long long* arrive;
+    uint64_t stamp;
     int32_t debug_unset_wait;  // test support: block 0 first waits on a barrier
                                // that nothing arrives at (times out, flags)
 };
@@ -178,6 +183,17 @@ size_t decode_workspace_bytes(int64_t nseg, int grid_max, int D, int TG);
 cudaError_t launch_decode(const CUtensorMap& key_map, const CUtensorMap& value_map,
                           const CUtensorMap& q_map, const DecodeArgs& a, int grid, int device,
                           cudaStream_t stream);
+
+// The few-row kernel (at most 16 rows per request and KV head; kWindow and
+// kScores): whether it takes a shape on a device with max_smem bytes of shared
+// memory a block, its workspace, and the launch (granule_bound: an upper bound of the
+// 4-tile granules, 0 unknown).
+bool decode_rows_takes(const pa_shape& s, int max_smem);
+size_t decode_rows_workspace_bytes(const pa_shape& s, int sm_count);
+int decode_rows_box(const pa_shape& s, bool fp8, int page_size);   // keys per TMA box (DecodeArgs::box_rows)
+cudaError_t launch_decode_rows(const CUtensorMap& key_map, const CUtensorMap& value_map, DecodeArgs a,
+                               const pa_shape& s, int64_t granule_bound, void* workspace,
+                               int device, int sm_count, cudaStream_t stream);
 
 // Accumulation of attention weights: weight_pages[slot of j] = decay * old (0
 // for the L newest positions, or where decay is 0) + sum over the R rows of

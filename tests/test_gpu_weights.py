@@ -92,8 +92,14 @@ def test_long_contexts(fp8):
 
 
 def test_output_is_pa_decodes():
+    """The few-row kernel's output is that of pa_decode_window with a window
+    past every context, the many-row kernel's that of pa_decode."""
     pa = _pa()
     c = make([300, 4000, 1], 28, 4, 1, 128, 16, seed=4)
+    got = run(c, pool_like(c), 1.0)
+    check_out(got, reference(c), False, 4000)
+    assert torch.equal(got, pa.pa_decode_window(**c, window=4000, max_context_len=4000))
+    c = make([300, 4000, 1], 28, 4, 3, 128, 16, seed=4)
     got = run(c, pool_like(c), 1.0)
     assert torch.equal(got, pa.pa_decode(**c, max_context_len=4000))
 

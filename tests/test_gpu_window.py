@@ -61,10 +61,13 @@ def test_head_layouts(H_q, H_kv, D):
 @pytest.mark.parametrize("W", [5000, 1 << 30, 2**31 - 1])
 def test_window_past_every_context_is_full_attention(W):
     pa = _pa()
+    # 12 rows a group: the few-row kernel, which rounds P less than pa_decode's
     c = make([1, 64, 777, 2100], 8, 2, 3, 128, 16, seed=3, poison=False)
     got = pa.pa_decode_window(**c, window=W, sinks=7)
-    want = pa.pa_decode(**c)
-    assert torch.equal(got, want)
+    check_out(got, reference(c), False, 2100)
+    # 20 rows: pa_decode's kernel, the same bits
+    c = make([1, 64, 777, 2100], 8, 2, 5, 128, 16, seed=3, poison=False)
+    assert torch.equal(pa.pa_decode_window(**c, window=W, sinks=7), pa.pa_decode(**c))
 
 
 @pytest.mark.parametrize("S", [90, 5000, 2**31 - 1])
