@@ -16,7 +16,7 @@
 //     a row are the very words that a lane's instructions want: K with four
 //     lanes a row, V with eight, V's pairs of keys joined by byte permutes.
 //   * Each warp has a ring of its own, two tiles (16 KiB) deep, that it fills by
-//     TMA (whole page slices, 128-byte swizzle) and empties itself: 192 KiB on
+//     TMA (whole page slices, 128-byte swizzle) and empties itself: 128 KiB on
 //     their way per SM, across the ends of pieces, and no barrier between the
 //     warps but at the end of a piece. (Copies by the lanes themselves, into
 //     registers or shared memory, came to 4.1-4.6 TB/s however many were
@@ -30,13 +30,14 @@
 //   * The tiles of all (request, KV head) form one stream of granules (one tile
 //     for each of a block's four warps) that the grid splits evenly, as the
 //     many-row kernel does; a piece that does not hold its whole segment leaves
-//     its state in the workspace, and the last block to arrive at the segment's
-//     word merges the pieces, in their order: no second launch, and bits that do
-//     not depend on who was last. The word carries the launch's stamp, so it
-//     needs no clearing beforehand, and is cleared by the merge, so a replayed
-//     graph finds it empty.
+//     its state in the workspace, and a second, small kernel merges the pieces
+//     in their order.
 //
-// Bound by memory: every K and V byte that a row sees is read once.
+// Bound by memory: every K and V byte that a row sees is read once. Measured (one
+// call of a replayed graph): 64 bf16 requests, window 2048, 510 MB in 82 us
+// (6.2 TB/s, of 6.8 measured for a copy); e4m3, 255 MB in 49 us; 32 requests of
+// a window of 1024 in groups of 7, 51 MB in 16 us; one request, window 512, 8.4
+// us, of which the second kernel is about 3.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <math.h>
@@ -55,7 +56,11 @@ constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr float kMoveLog2 = 8.f;      // scores may exceed the maximum in use by this much
 constexpr int kPieceUnits = 1;        // a piece's cost beyond its granules
-constexpr int kBlocksPerSM[3] = {0, 3, 2};   // by row tiles
+// Two blocks of two tiles a warp: with three the second kernel's blocks and the
+// next call's find no room until the last block of this one ends (64 e4m3
+// requests, window 2048: 62 us against 49; 8 bf16 requests of 16k-32k: 160
+// against 142), with four tiles a warp likewise (75 and 189 us).
+constexpr int kBlocksPerSM = 2;
 
 // kTok keys per step and warp: 16 rows of 256 bytes or 32 of 128.
 template <int D, bool F8>
@@ -72,8 +77,7 @@ constexpr int kStages = 2;            // tiles on their way per warp
 constexpr int kTileBytes = 4096;      // K (or V) of one tile: [128-byte column block][key][128 bytes]
 template <int D, int NT>
 struct Smem {
-    static constexpr int kRegs = D / 16 * NT * 4;                     // of O^T per lane
-    static constexpr int kSlab = (kRegs + 4 * NT) * 32 * 4;           // one warp's state: O^T, m, l
+    static constexpr int kSlab = (D / 16 * NT * 4 + 4 * NT) * 32 * 4; // one warp's state: O^T, m, l
     static constexpr int kRing = 0;                                   // [warp][stage][K, V]
     static constexpr int kSlabs = kRing + kWarps * kStages * 2 * kTileBytes;
     static constexpr int kBars = kSlabs + 2 * kSlab;                  // [warp][stage][K, V]
@@ -125,23 +129,125 @@ __device__ __forceinline__ int context_cap(const DecodeArgs& a)
     return kMode == kScores ? min(cap, a.score_cap) : cap;
 }
 
-// Arrivals before this one at a segment's word in this launch: the stamp in the
-// upper 48 bits, the arrivals in the lower 16 (a word of another launch, or
-// whatever the workspace held, counts as none).
-__device__ __forceinline__ unsigned arrive(unsigned long long* w, uint64_t stamp)
-{
-    unsigned long long old = 0;          // what the launch before left, usually
-    for (;;) {
-        const bool mine = (old >> 16) == stamp;
-        const unsigned long long got = atomicCAS(w, old, mine ? old + 1 : (stamp << 16) | 1ull);
-        if (got == old)
-            return mine ? unsigned(old & 0xffffu) : 0u;
-        old = got;
+// The softmax state of up to 8 NT rows in one warp's lanes: O^T as the tensor
+// core leaves it (rows 8 nt + 2 q + (k & 1)), and m and l of the lane's rows.
+template <int D, int NT>
+struct RowState {
+    static constexpr int kKS = D / 16;
+    static constexpr int kRegs = kKS * NT * 4;
+    static constexpr int kPlaces = kRegs + 4 * NT;
+    float o[kKS][NT][4], m[NT][2], l[NT][2];
+
+    __device__ __forceinline__ void clear()
+    {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            m[nt][0] = m[nt][1] = -INFINITY;
+            l[nt][0] = l[nt][1] = 0.f;
+#pragma unroll
+            for (int t = 0; t < kKS; ++t)
+                o[t][nt][0] = o[t][nt][1] = o[t][nt][2] = o[t][nt][3] = 0.f;
+        }
     }
-}
+    // To and from kPlaces x 32 floats, lane by lane.
+    __device__ __forceinline__ void put(float* to, int lane) const
+    {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+            for (int t = 0; t < kKS; ++t)
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    to[((nt * kKS + t) * 4 + k) * 32 + lane] = o[t][nt][k];
+#pragma unroll
+            for (int rr = 0; rr < 2; ++rr) {
+                to[(kRegs + 4 * nt + rr) * 32 + lane] = m[nt][rr];
+                to[(kRegs + 4 * nt + 2 + rr) * 32 + lane] = l[nt][rr];
+            }
+        }
+    }
+    // M = max, l = l 2^(m - M) + l' 2^(m' - M), likewise O.
+    __device__ __forceinline__ void fold(const float* v)
+    {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            float f1[2], f2[2];
+#pragma unroll
+            for (int rr = 0; rr < 2; ++rr) {
+                const float m2 = v[kRegs + 4 * nt + rr], l2 = v[kRegs + 4 * nt + 2 + rr];
+                const float M = fmaxf(m[nt][rr], m2);
+                f1[rr] = m[nt][rr] == -INFINITY ? 0.f : fast_exp2(m[nt][rr] - M);
+                f2[rr] = m2 == -INFINITY ? 0.f : fast_exp2(m2 - M);
+                m[nt][rr] = M;
+                l[nt][rr] = l[nt][rr] * f1[rr] + l2 * f2[rr];
+            }
+#pragma unroll
+            for (int t = 0; t < kKS; ++t)
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    o[t][nt][k] = o[t][nt][k] * f1[k & 1] + v[(nt * kKS + t) * 4 + k] * f2[k & 1];
+        }
+    }
+    __device__ __forceinline__ void take(const float* from, int lane)
+    {
+        float v[kPlaces];
+#pragma unroll
+        for (int i = 0; i < kPlaces; ++i)
+            v[i] = from[i * 32 + lane];
+        fold(v);
+    }
+    // Four warps' states into warp 0's: 2 and 3 into 0 and 1, then 1 into 0.
+    // slabs: two states; free when the block comes here. By the whole block.
+    __device__ __forceinline__ void gather(float* slabs, int warp, int lane)
+    {
+        if (warp >= 2)
+            put(slabs + (warp - 2) * kPlaces * 32, lane);
+        __syncthreads();
+        if (warp < 2)
+            take(slabs + warp * kPlaces * 32, lane);
+        if (warp == 1)
+            put(slabs + kPlaces * 32, lane);
+        __syncthreads();
+        if (warp == 0)
+            take(slabs + kPlaces * 32, lane);
+    }
+    // The output rows of (request, KV head) bh, from q_row0 on: each lane holds
+    // runs of neighbouring elements of D.
+    template <bool F8, int kMode>
+    __device__ __forceinline__ void write(const DecodeArgs& a, int64_t bh, int64_t q_row0, int lane) const
+    {
+        const int g = lane >> 2, q = lane & 3;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int rr = 0; rr < 2; ++rr) {
+                const int r = 8 * nt + 2 * q + rr;
+                if (r >= a.R)
+                    continue;
+                if constexpr (kMode == kScores) {
+                    if (g == 0)
+                        a.row_state[bh * a.R + r] = make_float2(m[nt][rr], l[nt][rr]);
+                }
+                const float inv = l[nt][rr] > 0.f ? a.v_scale / l[nt][rr] : 0.f;
+                uint16_t* dst = a.out + (q_row0 + r) * D;
+                auto pair = [&](int t, int k) { return pack_bf16x2(o[t][nt][k] * inv, o[t + 1][nt][k] * inv); };
+                if constexpr (D == 64) {             // element 8 g + t + 4 half
+                    *reinterpret_cast<uint4*>(dst + 8 * g) =
+                        make_uint4(pair(0, rr), pair(2, rr), pair(0, 2 + rr), pair(2, 2 + rr));
+                } else {                             // e4m3: 16 g + t + 8 half; bf16: 64 half + 8 g + t
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        const int k = 2 * half + rr;
+                        *reinterpret_cast<uint4*>(dst + (F8 ? 16 * g + 8 * half : 64 * half + 8 * g)) =
+                            make_uint4(pair(0, k), pair(2, k), pair(4, k), pair(6, k));
+                    }
+                }
+            }
+    }
+};
 
 template <int D, bool F8, int NT, int kMode>
-__global__ void __launch_bounds__(kThreads, kBlocksPerSM[NT])
+__global__ void __launch_bounds__(kThreads, kBlocksPerSM)
     decode_rows_kernel(const __grid_constant__ CUtensorMap key_map,
                        const __grid_constant__ CUtensorMap value_map, const DecodeArgs a)
 {
@@ -149,7 +255,6 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSM[NT])
     using Lay = Smem<D, NT>;
     constexpr int kTok = Sh::kTok, kSub = Sh::kSub, kKL = Sh::kKLoads, kVL = Sh::kVLoads, kKS = Sh::kSteps;
     constexpr int kSlot = Lay::kSlab / 4;             // floats of a piece's state
-    constexpr int kRegs = Lay::kRegs;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     volatile int* misc = reinterpret_cast<volatile int*>(smem + Lay::kMisc);
@@ -167,7 +272,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSM[NT])
         for (int i = 0; i < kStages * 2; ++i)
             mbar_init(&bars[i], 1);
         if (warp == 0) {
-            misc[1] = 0;                              // a wait ran out
+            misc[0] = 0;                              // a wait ran out
             prefetch_tensormap(&key_map);
             prefetch_tensormap(&value_map);
         }
@@ -366,15 +471,11 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSM[NT])
         if constexpr (kMode == kWindow)
             low_max = __reduce_max_sync(0xffffffffu, low_max);
 
-        float m[NT][2], l[NT][2], o[kKS][NT][4];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            m[nt][0] = m[nt][1] = -INFINITY;
-            l[nt][0] = l[nt][1] = 0.f;
-#pragma unroll
-            for (int t = 0; t < kKS; ++t)
-                o[t][nt][0] = o[t][nt][1] = o[t][nt][2] = o[t][nt][3] = 0.f;
-        }
+        RowState<D, NT> st;
+        st.clear();
+        auto& m = st.m;
+        auto& l = st.l;
+        auto& o = st.o;
 
         for (; at.x < piece_end; ++at.x) {
             int end;
@@ -384,7 +485,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSM[NT])
                 kMode == kWindow && int(at.x - sp.seg_start) * kWarps + warp < span.sink_tiles;
             const uint8_t* kt = ring + stage * (2 * kTileBytes);
             const uint8_t* vt = kt + kTileBytes;
-            mbar_wait_warp(&bars[stage * 2], phase, misc + 1, a.err);
+            mbar_wait_warp(&bars[stage * 2], phase, misc, a.err);
             // ---- S^T = K Q^T: tokens 16 s + g (+ 8), rows 2 q + {0, 1}
             // (even and odd k-steps apart: half the chain of dependent products)
             float sc[kSub][NT][4], odd[kSub][NT][4];
@@ -547,7 +648,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSM[NT])
             }
             // ---- O^T += V^T P^T; tile t of O^T holds the elements of D that the
             // lanes' words give to it (out_element below)
-            mbar_wait_warp(&bars[stage * 2 + 1], phase, misc + 1, a.err);
+            mbar_wait_warp(&bars[stage * 2 + 1], phase, misc, a.err);
 #pragma unroll
             for (int s = 0; s < kSub; ++s) {
                 uint4 vr[4][kVL];
@@ -625,7 +726,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSM[NT])
                 }
             }
             } else {
-                mbar_wait_warp(&bars[stage * 2 + 1], phase, misc + 1, a.err);   // nothing was copied
+                mbar_wait_warp(&bars[stage * 2 + 1], phase, misc, a.err);   // nothing was copied
             }
             if (more) {
                 __syncwarp();
@@ -637,8 +738,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSM[NT])
             }
         }
 
-        // ---- end of a piece: the four warps' states, all in the same lanes'
-        // places, meet in warp 0: 2 and 3 in 0 and 1, then 1 in 0.
+        // ---- end of a piece ---------------------------------------------------
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -646,142 +746,13 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSM[NT])
 #pragma unroll
                 for (int off = 4; off < 32; off <<= 1)
                     l[nt][rr] += __shfl_xor_sync(0xffffffffu, l[nt][rr], off);
-        // A state's place i of this lane: O^T, then m, then l.
-        auto put = [&](float* to) {
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-                for (int t = 0; t < kKS; ++t)
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        to[((nt * kKS + t) * 4 + k) * 32 + lane] = o[t][nt][k];
-#pragma unroll
-                for (int rr = 0; rr < 2; ++rr) {
-                    to[(kRegs + 4 * nt + rr) * 32 + lane] = m[nt][rr];
-                    to[(kRegs + 4 * nt + 2 + rr) * 32 + lane] = l[nt][rr];
-                }
-            }
-        };
-        auto take = [&](const float* from, bool global) {
-            auto get = [&](int i) { return global ? __ldcg(from + i * 32 + lane) : from[i * 32 + lane]; };
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                float v[kKS * 4], m2[2], l2[2];
-#pragma unroll
-                for (int i = 0; i < kKS * 4; ++i)
-                    v[i] = get(nt * kKS * 4 + i);
-#pragma unroll
-                for (int rr = 0; rr < 2; ++rr) {
-                    m2[rr] = get(kRegs + 4 * nt + rr);
-                    l2[rr] = get(kRegs + 4 * nt + 2 + rr);
-                }
-                float f1[2], f2[2];
-#pragma unroll
-                for (int rr = 0; rr < 2; ++rr) {
-                    const float M = fmaxf(m[nt][rr], m2[rr]);
-                    f1[rr] = m[nt][rr] == -INFINITY ? 0.f : fast_exp2(m[nt][rr] - M);
-                    f2[rr] = m2[rr] == -INFINITY ? 0.f : fast_exp2(m2[rr] - M);
-                    m[nt][rr] = M;
-                    l[nt][rr] = l[nt][rr] * f1[rr] + l2[rr] * f2[rr];
-                }
-#pragma unroll
-                for (int t = 0; t < kKS; ++t)
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        o[t][nt][k] = o[t][nt][k] * f1[k & 1] + v[t * 4 + k] * f2[k & 1];
-            }
-        };
-        float* slabs = reinterpret_cast<float*>(smem + Lay::kSlabs);
-        auto gather = [&]() {
-            if (warp >= 2)
-                put(slabs + (warp - 2) * kSlot);
-            __syncthreads();
-            if (warp < 2)
-                take(slabs + warp * kSlot, false);
-            if (warp == 1)
-                put(slabs + kSlot);
-            __syncthreads();
-            if (warp == 0)
-                take(slabs + kSlot, false);
-        };
-        // Output row r = 8 nt + 2 q + rr from warp 0's lanes: runs of the
-        // elements of D that a lane holds.
-        auto write_out = [&]() {
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int rr = 0; rr < 2; ++rr) {
-                    const int r = 8 * nt + 2 * q + rr;
-                    if (r >= a.R)
-                        continue;
-                    if constexpr (kMode == kScores) {
-                        if (g == 0)
-                            a.row_state[(int64_t(sp.b) * a.H_kv + sp.h) * a.R + r] =
-                                make_float2(m[nt][rr], l[nt][rr]);
-                    }
-                    const float inv = l[nt][rr] > 0.f ? a.v_scale / l[nt][rr] : 0.f;
-                    uint16_t* dst = a.out + (q_row0 + r) * D;
-                    if constexpr (D == 64) {         // 8 g + t + 4 half
-                        *reinterpret_cast<uint4*>(dst + 8 * g) =
-                            make_uint4(pack_bf16x2(o[0][nt][rr] * inv, o[1][nt][rr] * inv),
-                                       pack_bf16x2(o[2][nt][rr] * inv, o[3][nt][rr] * inv),
-                                       pack_bf16x2(o[0][nt][2 + rr] * inv, o[1][nt][2 + rr] * inv),
-                                       pack_bf16x2(o[2][nt][2 + rr] * inv, o[3][nt][2 + rr] * inv));
-                    } else {
-                        // e4m3: 16 g + t + 8 half; bf16: 64 half + 8 g + t
-#pragma unroll
-                        for (int half = 0; half < 2; ++half) {
-                            const int k = 2 * half + rr;
-                            *reinterpret_cast<uint4*>(dst + (F8 ? 16 * g + 8 * half : 64 * half + 8 * g)) =
-                                make_uint4(pack_bf16x2(o[0][nt][k] * inv, o[1 % kKS][nt][k] * inv),
-                                           pack_bf16x2(o[2 % kKS][nt][k] * inv, o[3 % kKS][nt][k] * inv),
-                                           pack_bf16x2(o[4 % kKS][nt][k] * inv, o[5 % kKS][nt][k] * inv),
-                                           pack_bf16x2(o[6 % kKS][nt][k] * inv, o[7 % kKS][nt][k] * inv));
-                        }
-                    }
-                }
-        };
         __syncthreads();                             // the piece before has read the slabs
-        gather();
-        if (sp.seg_start >= p0.x && sp.seg_start + sp.seg_len <= x_end) {
-            if (warp == 0 && !misc[1])
-                write_out();                         // the whole segment was here
-        } else {
-            // The segment's pieces are those of blocks first .. last.
-            const int64_t u0 = sp.seg_start + int64_t(kPieceUnits) * (sp.seg + 1);
-            const int64_t first = block_of_unit(u0, units, grid);
-            const int np = int(block_of_unit(u0 + sp.seg_len - 1, units, grid) - first) + 1;
-            float* slots = a.partials + int64_t(sp.seg) * kSlot;     // of the segment, by block
-            if (warp == 0) {
-                put(slots + cta * kSlot);
-                __threadfence();
-                __syncwarp();
-                if (lane == 0)
-                    misc[0] = arrive(a.arrive + sp.seg, a.stamp) + 1 == unsigned(np);
-            }
-            __syncthreads();
-            if (misc[0]) {
-                // Last to arrive: warp w merges pieces w, w + 4, ... in order.
-                __threadfence();
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    m[nt][0] = m[nt][1] = -INFINITY;
-                    l[nt][0] = l[nt][1] = 0.f;
-#pragma unroll
-                    for (int t = 0; t < kKS; ++t)
-                        o[t][nt][0] = o[t][nt][1] = o[t][nt][2] = o[t][nt][3] = 0.f;
-                }
-#pragma unroll 2
-                for (int k = warp; k < np; k += kWarps)
-                    take(slots + (first + k) * kSlot, true);
-                gather();
-                if (warp == 0) {
-                    if (!misc[1])
-                        write_out();
-                    if (lane == 0)
-                        *reinterpret_cast<volatile unsigned long long*>(a.arrive + sp.seg) = 0ull;
-                }
-            }
+        st.gather(reinterpret_cast<float*>(smem + Lay::kSlabs), warp, lane);
+        if (warp == 0 && !misc[0]) {
+            if (sp.seg_start >= p0.x && sp.seg_start + sp.seg_len <= x_end)
+                st.template write<F8, kMode>(a, int64_t(sp.b) * a.H_kv + sp.h, q_row0, lane);
+            else                                     // a slot of its own: segment and block
+                st.put(a.partials + (int64_t(sp.seg) + cta) * kSlot, lane);
         }
         // on to the next segment
         if (at.x < x_end) {
@@ -791,16 +762,104 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSM[NT])
     }
 }
 
-using RowsKernel = void (*)(CUtensorMap, CUtensorMap, DecodeArgs);
-template <int kMode>
-RowsKernel rows_kernel_of(int D, bool fp8, int NT, int* index)
+// The segments that straddle blocks: one block each (the others return once the
+// first kernel is done). Warp w folds pieces w, w + 4, ... in order, one on its
+// way while the one before is folded in.
+template <int D, bool F8, int NT, int kMode>
+__global__ void __launch_bounds__(kThreads) decode_rows_merge_kernel(const DecodeArgs a, int decode_grid)
 {
-    *index = (fp8 ? 0 : D == 64 ? 2 : 4) + NT - 1;
+    using Sh = Shape<D, F8>;
+    using State = RowState<D, NT>;
+    constexpr int kSlot = State::kPlaces * 32;
+    __shared__ float slabs[2 * kSlot];
+    __shared__ int red[2][kWarps];
+    grid_launch_dependents();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int seg = blockIdx.x;
+    const int b = seg / a.H_kv, h = seg - b * a.H_kv;
+    const int cap = context_cap<kMode>(a);
+    auto granules = [&](int r) {
+        const int n = a.context_lens[r];
+        return tile_span<Sh::kTok, kMode>(a, n < 0 ? 0 : n > cap ? cap : n).granules;
+    };
+    // The split of the first kernel, from its inputs (which were complete before
+    // it let this one start).
+    int before = 0, total = 0;
+    for (int r = threadIdx.x; r < a.B; r += kThreads) {
+        const int gs = granules(r) * a.H_kv;
+        total += gs;
+        before += r < b ? gs : 0;
+    }
+    total = __reduce_add_sync(0xffffffffu, total);
+    before = __reduce_add_sync(0xffffffffu, before);
+    if (lane == 0) {
+        red[0][warp] = total;
+        red[1][warp] = before;
+    }
+    __syncthreads();
+    total = before = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+        total += red[0][w];
+        before += red[1][w];
+    }
+    const int len = granules(b);
+    const int64_t units = total + int64_t(kPieceUnits) * a.B * a.H_kv;
+    const int64_t grid = int64_t(decode_grid) < units ? int64_t(decode_grid) : units;
+    const int64_t u0 = before + int64_t(h) * len + int64_t(kPieceUnits) * (seg + 1);
+    const int64_t first = block_of_unit(u0, units, grid);
+    const int np = int(block_of_unit(u0 + len - 1, units, grid) - first) + 1;
+    // Every block waits, so that this grid does not end before the one it
+    // follows.
+    grid_dependency_wait();
+    if (np == 1)
+        return;
+    const float* slots = a.partials + (int64_t(seg) + first) * kSlot + lane;
+    State st;
+    st.clear();
+    float v[2][State::kPlaces];
+    auto fetch = [&](int k, float* to) {
+#pragma unroll
+        for (int i = 0; i < State::kPlaces; ++i)
+            to[i] = __ldcg(slots + int64_t(k) * kSlot + i * 32);
+    };
+    if (warp < np)
+        fetch(warp, v[0]);
+    for (int k = warp; k < np; k += 2 * kWarps) {
+        if (k + kWarps < np)
+            fetch(k + kWarps, v[1]);
+        st.fold(v[0]);
+        if (k + 2 * kWarps < np)
+            fetch(k + 2 * kWarps, v[0]);
+        if (k + kWarps < np)
+            st.fold(v[1]);
+    }
+    st.gather(slabs, warp, lane);
+    if (warp == 0)
+        st.template write<F8, kMode>(a, seg, (int64_t(b) * a.H_q + h * a.G) * a.L, lane);
+}
+
+using RowsKernel = void (*)(CUtensorMap, CUtensorMap, DecodeArgs);
+using RowsMerge = void (*)(DecodeArgs, int);
+struct RowsKernels {
+    RowsKernel main;
+    RowsMerge merge;
+};
+template <int D, bool F8, int NT>
+RowsKernels rows_kernels(int mode)
+{
+    if (mode == kWindow)
+        return {decode_rows_kernel<D, F8, NT, kWindow>, decode_rows_merge_kernel<D, F8, NT, kWindow>};
+    return {decode_rows_kernel<D, F8, NT, kScores>, decode_rows_merge_kernel<D, F8, NT, kScores>};
+}
+RowsKernels rows_kernels_for(int D, bool fp8, int NT, int mode, int* index)
+{
+    *index = ((fp8 ? 0 : D == 64 ? 2 : 4) + NT - 1) * 2 + (mode == kWindow ? 0 : 1);
     if (fp8)
-        return NT == 1 ? decode_rows_kernel<128, true, 1, kMode> : decode_rows_kernel<128, true, 2, kMode>;
+        return NT == 1 ? rows_kernels<128, true, 1>(mode) : rows_kernels<128, true, 2>(mode);
     if (D == 64)
-        return NT == 1 ? decode_rows_kernel<64, false, 1, kMode> : decode_rows_kernel<64, false, 2, kMode>;
-    return NT == 1 ? decode_rows_kernel<128, false, 1, kMode> : decode_rows_kernel<128, false, 2, kMode>;
+        return NT == 1 ? rows_kernels<64, false, 1>(mode) : rows_kernels<64, false, 2>(mode);
+    return NT == 1 ? rows_kernels<128, false, 1>(mode) : rows_kernels<128, false, 2>(mode);
 }
 
 size_t rows_smem_bytes(int D, int NT, int B)
@@ -819,14 +878,7 @@ bool decode_rows_takes(const pa_shape& s, int max_smem)
     return R <= 16 && rows_smem_bytes(s.head_dim, row_tiles(s), s.batch) <= size_t(max_smem);
 }
 
-int decode_rows_grid(const pa_shape& s, int sm_count)
-{
-    // one wave: what the shared memory of an SM (228 KiB, 1 KiB of it each
-    // block's own) holds
-    const int NT = row_tiles(s);
-    const int fit = int(228 * 1024 / (rows_smem_bytes(s.head_dim, NT, s.batch) + 1024));
-    return sm_count * (fit < kBlocksPerSM[NT] ? (fit < 1 ? 1 : fit) : kBlocksPerSM[NT]);
-}
+int decode_rows_grid(int sm_count) { return sm_count * kBlocksPerSM; }
 
 int decode_rows_box(const pa_shape& s, bool fp8, int page_size)
 {
@@ -836,12 +888,10 @@ int decode_rows_box(const pa_shape& s, bool fp8, int page_size)
 
 size_t decode_rows_workspace_bytes(const pa_shape& s, int sm_count)
 {
-    const size_t segs = size_t(s.batch) * s.num_kv_heads;
-    const size_t words = (segs * sizeof(unsigned long long) + 15) & ~size_t(15);
     const int NT = row_tiles(s);
     const size_t slot = s.head_dim == 64 ? (NT == 1 ? Smem<64, 1>::kSlab : Smem<64, 2>::kSlab)
                                          : (NT == 1 ? Smem<128, 1>::kSlab : Smem<128, 2>::kSlab);
-    return words + (segs + size_t(decode_rows_grid(s, sm_count))) * slot;
+    return (size_t(s.batch) * s.num_kv_heads + size_t(decode_rows_grid(sm_count))) * slot;
 }
 
 cudaError_t launch_decode_rows(const CUtensorMap& key_map, const CUtensorMap& value_map, DecodeArgs a,
@@ -849,27 +899,21 @@ cudaError_t launch_decode_rows(const CUtensorMap& key_map, const CUtensorMap& va
                                int device, int sm_count, cudaStream_t stream)
 {
     const int NT = row_tiles(s);
-    const size_t segs = size_t(s.batch) * s.num_kv_heads;
-    int64_t grid = decode_rows_grid(s, sm_count);
-    // Few granules: 4 of them a block at least, so that a segment's pieces stay
-    // few (each costs its merge).
-    if (granule_bound > 0 && granule_bound < 4 * grid)
-        grid = (granule_bound + 4 - 1) / 4;
-    a.arrive = static_cast<unsigned long long*>(workspace);
-    a.partials = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) +
-                                          ((segs * sizeof(unsigned long long) + 15) & ~size_t(15)));
-    a.stamp = next_launch_stamp();
+    int64_t grid = decode_rows_grid(sm_count);
+    // Few granules: two of them a block at least, so that a segment's pieces stay
+    // few (one request, window 4096: 11.3 us, 14.0 with one; window 512: 8.4 and 8.2).
+    if (granule_bound > 0 && granule_bound < 2 * grid)
+        grid = (granule_bound + 2 - 1) / 2;
+    a.partials = static_cast<float*>(workspace);
     int index = 0;
-    const RowsKernel kern = a.mode == kWindow ? rows_kernel_of<kWindow>(a.D, a.fp8 != 0, NT, &index)
-                                              : rows_kernel_of<kScores>(a.D, a.fp8 != 0, NT, &index);
-    index += a.mode == kWindow ? 0 : 6;
+    const RowsKernels kern = rows_kernels_for(a.D, a.fp8 != 0, NT, a.mode, &index);
     constexpr int kMaxDev = 64;
     static std::atomic<int> smem_set[kMaxDev][12];
     if (device < 0 || device >= kMaxDev)
         return cudaErrorInvalidDevice;
     const int smem = int(rows_smem_bytes(a.D, NT, a.B));
     if (smem_set[device][index].load(std::memory_order_relaxed) < smem) {
-        const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(kern),
+        const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(kern.main),
                                                    cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess)
             return e;
@@ -885,7 +929,12 @@ cudaError_t launch_decode_rows(const CUtensorMap& key_map, const CUtensorMap& va
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, key_map, value_map, a);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern.main, key_map, value_map, a);
+    if (e != cudaSuccess)
+        return e;
+    cfg.gridDim = dim3(unsigned(int64_t(a.B) * a.H_kv));
+    cfg.dynamicSmemBytes = 0;
+    return cudaLaunchKernelEx(&cfg, kern.merge, a, int(grid));
 }
 
 }  // namespace pa

@@ -168,11 +168,7 @@ struct DecodeArgs {
     float2* row_state;  // kScores: [B * H_kv][R] (max, sum)
     int64_t score_stride;      // a multiple of 64, at least score_cap
     int32_t score_cap;         // kScores: longest context
-    // The few-row kernel: log2 of the page size, and one arrival word per segment
-    // with the launch's stamp.
-    int32_t ps_shift;
-    unsigned long long* arrive;
-    uint64_t stamp;
+    int32_t ps_shift;   // the few-row kernel: log2 of the page size
     int32_t debug_unset_wait;  // test support: block 0 first waits on a barrier
                                // that nothing arrives at (times out, flags)
 };

@@ -10,8 +10,10 @@
 // set-up). All in fp32; the rows are added in order.
 //
 // Bound by memory: 4 R bytes of scores a position (mostly still in L2) and 8 of
-// weights. A thread holds one position, so the score rows and the page rows are
-// read in whole sectors; the R row states are staged in shared memory.
+// weights. A thread holds four neighbouring positions: 16 bytes of each score
+// row, and of the page row where pages hold at least four slots and the pool
+// is aligned to 16 bytes (otherwise four single slots). The page id and the old
+// weights are requested before the scores.
 #include <stdint.h>
 
 #include "pa_device.cuh"
@@ -20,8 +22,11 @@
 namespace pa {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
+constexpr int kEach = 4;                             // positions per thread
+constexpr int kSpan = kThreads * kEach;
 
+template <bool kVector>
 __global__ void __launch_bounds__(kThreads) accumulate_weights_kernel(const WeightArgs a)
 {
     __shared__ float2 state[kThreads];               // (max, 1 / sum) of up to kThreads rows
@@ -33,11 +38,48 @@ __global__ void __launch_bounds__(kThreads) accumulate_weights_kernel(const Weig
     int n = a.context_lens[b];
     const int cap = min(a.max_pages << a.ps_shift, a.score_cap);
     n = n < 0 ? 0 : n > cap ? cap : n;               // recorded by the decode pass
-    if (chunk * kThreads >= n)
+    if (chunk * kSpan >= n)
         return;
-    const int pos = chunk * kThreads + int(threadIdx.x);
+    const int pos = chunk * kSpan + int(threadIdx.x) * kEach;
+    const int32_t* bt = a.block_table + int64_t(b) * a.max_pages;
+    const int fresh = a.decay != 0.f ? n - a.L : 0;  // positions from here on start at 0
+    float* to[kEach];
+    float old[kEach] = {0.f, 0.f, 0.f, 0.f};
+    if constexpr (kVector) {
+        to[0] = nullptr;
+        if (pos < n) {
+            const int phys = bt[pos >> a.ps_shift];
+            if (unsigned(phys) < unsigned(a.num_pages)) {    // otherwise recorded by the decode pass
+                to[0] = a.weight_pages + ((int64_t(phys) * a.H_kv + h) << a.ps_shift) +
+                        (pos & ((1 << a.ps_shift) - 1));
+                if (pos < fresh) {
+                    const float4 v = *reinterpret_cast<const float4*>(to[0]);
+                    old[0] = v.x;
+                    old[1] = v.y;
+                    old[2] = v.z;
+                    old[3] = v.w;
+                }
+            }
+        }
+    } else {
+#pragma unroll
+        for (int u = 0; u < kEach; ++u) {
+            to[u] = nullptr;
+            if (pos + u < n) {
+                const int phys = bt[(pos + u) >> a.ps_shift];
+                if (unsigned(phys) < unsigned(a.num_pages)) {
+                    to[u] = a.weight_pages + ((int64_t(phys) * a.H_kv + h) << a.ps_shift) +
+                            ((pos + u) & ((1 << a.ps_shift) - 1));
+                    if (pos + u < fresh)
+                        old[u] = *to[u];
+                }
+            }
+        }
+    }
+    // A row of scores is a whole number of 64 positions: 16 bytes at pos < n lie
+    // within it.
     const float* s = a.scores + bh * a.R * a.score_stride + pos;
-    float w = 0.f;
+    float w[kEach] = {0.f, 0.f, 0.f, 0.f};
     for (int r0 = 0; r0 < a.R; r0 += kThreads) {
         __syncthreads();
         const int rows = min(kThreads, a.R - r0);
@@ -48,26 +90,48 @@ __global__ void __launch_bounds__(kThreads) accumulate_weights_kernel(const Weig
         }
         __syncthreads();
         if (pos < n)
-            for (int r = 0; r < rows; ++r)
-                w = fmaf(fast_exp2(s[(r0 + r) * a.score_stride] - state[r].x), state[r].y, w);
+#pragma unroll 4
+            for (int r = 0; r < rows; ++r) {
+                const float4 v = __ldcg(reinterpret_cast<const float4*>(s + (r0 + r) * a.score_stride));
+                const float2 st = state[r];
+                w[0] = fmaf(fast_exp2(v.x - st.x), st.y, w[0]);
+                w[1] = fmaf(fast_exp2(v.y - st.x), st.y, w[1]);
+                w[2] = fmaf(fast_exp2(v.z - st.x), st.y, w[2]);
+                w[3] = fmaf(fast_exp2(v.w - st.x), st.y, w[3]);
+            }
     }
-    if (pos >= n)
-        return;
-    const int phys = a.block_table[int64_t(b) * a.max_pages + (pos >> a.ps_shift)];
-    if (unsigned(phys) >= unsigned(a.num_pages))
-        return;                                      // recorded by the decode pass
-    float* to = a.weight_pages + ((int64_t(phys) * a.H_kv + h) << a.ps_shift) + (pos & ((1 << a.ps_shift) - 1));
-    *to = a.decay != 0.f && pos < n - a.L ? fmaf(a.decay, *to, w) : w;
+#pragma unroll
+    for (int u = 0; u < kEach; ++u)
+        if (pos + u < fresh)
+            w[u] = fmaf(a.decay, old[u], w[u]);
+    if constexpr (kVector) {
+        if (to[0] != nullptr) {
+            if (pos + kEach <= n) {
+                *reinterpret_cast<float4*>(to[0]) = make_float4(w[0], w[1], w[2], w[3]);
+            } else {
+#pragma unroll
+                for (int u = 0; u < kEach; ++u)      // slots behind the context stay
+                    if (pos + u < n)
+                        to[0][u] = w[u];
+            }
+        }
+    } else {
+#pragma unroll
+        for (int u = 0; u < kEach; ++u)
+            if (to[u] != nullptr)
+                *to[u] = w[u];
+    }
 }
 
 }  // namespace
 
 cudaError_t launch_accumulate_weights(WeightArgs a, cudaStream_t stream)
 {
-    a.chunks = (a.score_cap + kThreads - 1) / kThreads;
+    a.chunks = (a.score_cap + kSpan - 1) / kSpan;
     const int64_t blocks = int64_t(a.B) * a.H_kv * a.chunks;
     if (blocks < 1 || blocks >= (int64_t(1) << 31))
         return cudaErrorInvalidValue;
+    const bool vector = a.ps_shift >= 2 && (reinterpret_cast<uintptr_t>(a.weight_pages) & 15u) == 0;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -77,7 +141,7 @@ cudaError_t launch_accumulate_weights(WeightArgs a, cudaStream_t stream)
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, accumulate_weights_kernel, a);
+    return cudaLaunchKernelEx(&cfg, vector ? accumulate_weights_kernel<true> : accumulate_weights_kernel<false>, a);
 }
 
 }  // namespace pa
