@@ -1,4 +1,5 @@
-"""ctypes binding of libpagedattn.so, with the C entry points' names.
+"""Binding of libpagedattn.so, with the C entry points' names: ctypes, and for the
+newer calls the compiled module _pagedattn_calls (pa_python.cpp).
 
 Argument marshalling only: every step of the computation runs in the CUDA
 kernels behind the C ABI. Torch tensors supply device pointers and the
@@ -124,43 +125,15 @@ def _load() -> ctypes.CDLL:
     lib.pa_status_string.restype = ctypes.c_char_p
     lib.pa_version.argtypes = []
     lib.pa_version.restype = ctypes.c_char_p
-    i64 = ctypes.c_int64
-    qk = [vp, i64, i64, vp, vp, f32, vp, i32, i32, ctypes.c_int, vp, vp, vp, vp, vp, i32]
-    lib.pa_qk_norm_rope_append.argtypes = qk + [pa_shape, vp]
-    lib.pa_qk_norm_rope_append.restype = ctypes.c_int
-    lib.pa_qk_norm_rope_append_fp8.argtypes = qk + [f32, f32, pa_shape, vp]
-    lib.pa_qk_norm_rope_append_fp8.restype = ctypes.c_int
-    ev = [vp, vp, vp, vp, vp, i32, i32, i32, i32, vp, i32, vp, vp, pa_shape, vp]
-    lib.pa_kv_evict.argtypes = ev
-    lib.pa_kv_evict.restype = ctypes.c_int
-    lib.pa_kv_evict_fp8.argtypes = ev
-    lib.pa_kv_evict_fp8.restype = ctypes.c_int
-    lib.pa_kv_cache_truncate.argtypes = [vp, i64, i32]
+    lib.pa_kv_cache_truncate.argtypes = [vp, ctypes.c_int64, i32]
     lib.pa_kv_cache_truncate.restype = ctypes.c_int
-    tables = [vp, vp, vp, vp, vp, i32, f32]
-    tail = [vp, pa_shape, i32, vp, sz, vp]
-    lib.pa_decode_window.argtypes = tables + [i32, i32] + tail
-    lib.pa_decode_window.restype = ctypes.c_int
-    lib.pa_decode_window_fp8.argtypes = tables + [f32, f32, i32, i32] + tail
-    lib.pa_decode_window_fp8.restype = ctypes.c_int
     lib.pa_decode_window_workspace_bytes.argtypes = [pa_shape]
     lib.pa_decode_window_workspace_bytes.restype = sz
-    lib.pa_prefill_window.argtypes = tables + [i32, i32, vp, pa_shape, vp]
-    lib.pa_prefill_window.restype = ctypes.c_int
-    lib.pa_attention_window.argtypes = tables + [i32, i32] + tail
-    lib.pa_attention_window.restype = ctypes.c_int
-    lib.pa_attention_window_fp8.argtypes = tables + [f32, f32, i32, i32] + tail
-    lib.pa_attention_window_fp8.restype = ctypes.c_int
     for f in (lib.pa_attention_window_workspace_bytes, lib.pa_attention_window_fp8_workspace_bytes):
         f.argtypes = [pa_shape, i32, i32, i32, i32]
         f.restype = sz
     lib.pa_decode_weights_workspace_bytes.argtypes = [pa_shape, i32]
     lib.pa_decode_weights_workspace_bytes.restype = sz
-    wtables = [vp, vp, vp, vp, vp, vp, i32, f32]
-    lib.pa_decode_weights.argtypes = wtables + [ctypes.c_int, f32] + tail
-    lib.pa_decode_weights.restype = ctypes.c_int
-    lib.pa_decode_weights_fp8.argtypes = wtables + [f32, f32, ctypes.c_int, f32] + tail
-    lib.pa_decode_weights_fp8.restype = ctypes.c_int
     lib.pa_debug_arm_wait_timeout.argtypes = []
     lib.pa_debug_arm_wait_timeout.restype = None
     lib.pa_debug_prefill_variant.argtypes = [ctypes.c_int]
@@ -169,6 +142,24 @@ def _load() -> ctypes.CDLL:
 
 
 _lib = _load()
+
+
+def _load_calls():
+    import importlib.machinery
+    import importlib.util
+    if not os.path.exists(_build.PYTHON_LIB):
+        raise ImportError(
+            f"{_build.PYTHON_LIB} is not built; run "
+            "`python -c 'import __graft_entry__ as g; g.build()'`")
+    loader = importlib.machinery.ExtensionFileLoader("_pagedattn_calls", _build.PYTHON_LIB)
+    module = importlib.util.module_from_spec(
+        importlib.util.spec_from_loader("_pagedattn_calls", loader))
+    loader.exec_module(module)
+    module.set_error(PagedAttentionError)
+    return module
+
+
+_calls = _load_calls()
 
 
 def status_string(status: int) -> str:
@@ -307,108 +298,9 @@ def pa_append_kv_fp8(key: torch.Tensor, value: torch.Tensor, key_pages: torch.Te
     _check(st, "pa_append_kv_fp8")
 
 
-def _ptr(t: torch.Tensor, dtype: torch.dtype, device_index: int, name: str) -> int:
-    """_dev_ptr, and on the device of the call."""
-    if t.dtype is not dtype or t.get_device() != device_index or not t.is_contiguous():
-        if t.is_cuda and t.get_device() != device_index:
-            raise ValueError(f"{name} is on {t.device}, expected cuda:{device_index}")
-        return _dev_ptr(t, dtype, name)
-    return t.data_ptr()
-
-
-def _on_device(device_index: int, stream):
-    """(raw stream, guard or None): the given stream or the device's current
-    one, and a guard that makes the device current where it is not."""
-    raw = torch._C._cuda_getCurrentRawStream(device_index) if stream is None else _stream(stream)
-    guard = None if torch._C._cuda_getDevice() == device_index else torch.cuda.device(device_index)
-    return raw, guard
-
-
-def _launch(fn, what: str, guard, *args) -> None:
-    if guard is None:
-        st = fn(*args)
-    else:
-        with guard:
-            st = fn(*args)
-    if st:
-        raise PagedAttentionError(st, what)
-
-
-def _scratch(need: int, device: torch.device, stream) -> torch.Tensor:
-    """A workspace of this call alone: the allocator orders its reuse on the
-    stream that the call runs on (a capture's lives in the graph's pool)."""
-    buf = torch.empty(max(int(need), 16), dtype=torch.uint8, device=device)
-    _keep_for(buf, stream)
-    return buf
-
-
-def _keep_for(t: torch.Tensor, stream) -> None:
-    """Memory allocated on the current stream for a call on `stream`."""
-    if stream is None:
-        return
-    if not isinstance(stream, torch.cuda.Stream):
-        if int(stream) == torch.cuda.current_stream(t.device).cuda_stream:
-            return
-        stream = torch.cuda.ExternalStream(int(stream), device=t.device)
-    t.record_stream(stream)
-
-
-def _qk_norm_rope_append(qkv, q_weight, k_weight, cos_sin, positions, key_pages, value_pages,
-                         slot_mapping, page_size, scales, eps, interleaved, query, stream):
-    fp8 = bool(scales)
-    what = "pa_qk_norm_rope_append_fp8" if fp8 else "pa_qk_norm_rope_append"
-    pool_dtype = torch.uint8 if fp8 else torch.bfloat16
-    if qkv.dim() != 3:
-        raise ValueError("qkv must be [B, L, (H_q + 2 H_kv) * D]")
-    B, L, width = qkv.shape
-    P, H_kv, ps, D = key_pages.shape
-    if ps != page_size or value_pages.shape != key_pages.shape:
-        raise ValueError("page pool shape does not match page_size")
-    H_q = width // D - 2 * H_kv
-    if H_q <= 0 or (H_q + 2 * H_kv) * D != width:
-        raise ValueError("qkv's rows are not (H_q + 2 H_kv) heads of the pools' head_dim")
-    if slot_mapping.shape != (B, L):
-        raise ValueError("slot_mapping must be [B, L]")
-    if not qkv.is_cuda:
-        raise ValueError("qkv must be a CUDA tensor")
-    if qkv.dtype != torch.bfloat16:
-        raise TypeError(f"qkv must be torch.bfloat16, got {qkv.dtype}")
-    if qkv.stride(2) != 1:
-        raise ValueError("qkv's rows must be contiguous")
-    if q_weight is not None and q_weight.shape != (D,):
-        raise ValueError("q_weight must be [D]")
-    if k_weight is not None and k_weight.shape != (D,):
-        raise ValueError("k_weight must be [D]")
-    R = table_len = 0
-    if cos_sin is not None:
-        if positions is None or positions.shape != (B, L):
-            raise ValueError("positions must be [B, L]")
-        if cos_sin.dim() != 2:
-            raise ValueError("cos_sin must be [table_len, rotary_dim]")
-        table_len, R = cos_sin.shape
-    dev = qkv.get_device()
-    raw, guard = _on_device(dev, stream)
-    if query is None:
-        query = torch.empty((B, H_q, L, D), dtype=torch.bfloat16, device=qkv.device)
-        _keep_for(query, stream)
-    elif query.shape != (B, H_q, L, D):
-        raise ValueError("query must be [B, H_q, L, D]")
-    if B == 0 or L == 0:
-        return query
-    # the strides of an axis of one element say nothing
-    bs = qkv.stride(0) if B > 1 else L * width
-    ts = qkv.stride(1) if L > 1 else width
-    _launch(getattr(_lib, what), what, guard, qkv.data_ptr(), bs, ts,
-            None if q_weight is None else _ptr(q_weight, torch.bfloat16, dev, "q_weight"),
-            None if k_weight is None else _ptr(k_weight, torch.bfloat16, dev, "k_weight"), eps,
-            None if cos_sin is None else _ptr(cos_sin, torch.float32, dev, "cos_sin"), R, table_len,
-            1 if interleaved else 0,
-            None if cos_sin is None else _ptr(positions, torch.int32, dev, "positions"),
-            _ptr(query, torch.bfloat16, dev, "query"), _ptr(key_pages, pool_dtype, dev, "key_pages"),
-            _ptr(value_pages, pool_dtype, dev, "value_pages"),
-            _ptr(slot_mapping, torch.int32, dev, "slot_mapping"), page_size, *scales,
-            pa_shape(B, H_q, H_kv, D, L, P, 0), raw)
-    return query
+def _raw(stream):
+    """None (the device's current stream), or the raw handle of a stream."""
+    return None if stream is None else _stream(stream)
 
 
 def pa_qk_norm_rope_append(qkv: torch.Tensor, q_weight: Optional[torch.Tensor],
@@ -422,9 +314,8 @@ def pa_qk_norm_rope_append(qkv: torch.Tensor, q_weight: Optional[torch.Tensor],
     no norm), rotation by cos_sin [table_len, R] fp32 at positions [B, L]
     (None: no rotation), k and v rows into the pages at slot_mapping [B, L].
     Returns the queries [B, H_q, L, D]."""
-    return _qk_norm_rope_append(qkv, q_weight, k_weight, cos_sin, positions, key_pages,
-                                value_pages, slot_mapping, page_size, (), eps, interleaved, query,
-                                stream)
+    return _calls.append(qkv, q_weight, k_weight, cos_sin, positions, key_pages, value_pages,
+                         slot_mapping, page_size, None, None, eps, interleaved, query, _raw(stream))
 
 
 def pa_qk_norm_rope_append_fp8(qkv, q_weight, k_weight, cos_sin, positions, key_pages, value_pages,
@@ -432,49 +323,9 @@ def pa_qk_norm_rope_append_fp8(qkv, q_weight, k_weight, cos_sin, positions, key_
                                eps: float = 1e-6, interleaved: bool = False, query=None,
                                stream=None) -> torch.Tensor:
     """pa_qk_norm_rope_append into uint8 e4m3 pools, code = e4m3(x / scale)."""
-    return _qk_norm_rope_append(qkv, q_weight, k_weight, cos_sin, positions, key_pages,
-                                value_pages, slot_mapping, page_size,
-                                (k_scale, v_scale), eps, interleaved, query, stream)
-
-
-def _kv_evict(what, pool_dtype, key_pages, value_pages, weight_pages, block_table, context_lens,
-              page_size, keep, sinks, recent, dst_block_table, kept, new_lens, stream):
-    P, H_kv, ps, D = key_pages.shape
-    if ps != page_size or value_pages.shape != key_pages.shape:
-        raise ValueError("page pool shape does not match page_size")
-    if weight_pages.shape != (P, H_kv, ps):
-        raise ValueError("weight_pages must be [P, H_kv, page_size]")
-    B = block_table.shape[0]
-    if block_table.dim() != 2 or context_lens.shape != (B,):
-        raise ValueError("block_table must be [B, max_pages] and context_lens [B]")
-    dst = block_table if dst_block_table is None else dst_block_table
-    if dst.dim() != 2 or dst.shape[0] != B:
-        raise ValueError("dst_block_table must be [B, dst_max_pages]")
-    if not key_pages.is_cuda:
-        raise ValueError("key_pages must be a CUDA tensor")
-    dev = key_pages.get_device()
-    raw, guard = _on_device(dev, stream)
-    if kept is None:
-        kept = torch.empty((B, H_kv, max(int(keep), 0)), dtype=torch.int32, device=key_pages.device)
-        _keep_for(kept, stream)
-    elif kept.shape != (B, H_kv, keep):
-        raise ValueError("kept must be [B, H_kv, keep]")
-    if new_lens is None:
-        new_lens = torch.empty((B,), dtype=torch.int32, device=key_pages.device)
-        _keep_for(new_lens, stream)
-    elif new_lens.shape != (B,):
-        raise ValueError("new_lens must be [B]")
-    if B == 0:
-        return kept, new_lens
-    _launch(getattr(_lib, what), what, guard, _ptr(key_pages, pool_dtype, dev, "key_pages"),
-            _ptr(value_pages, pool_dtype, dev, "value_pages"),
-            _ptr(weight_pages, torch.float32, dev, "weight_pages"),
-            _ptr(block_table, torch.int32, dev, "block_table"),
-            _ptr(context_lens, torch.int32, dev, "context_lens"), page_size, keep, sinks, recent,
-            _ptr(dst, torch.int32, dev, "dst_block_table"), dst.shape[1],
-            _ptr(kept, torch.int32, dev, "kept"), _ptr(new_lens, torch.int32, dev, "new_lens"),
-            pa_shape(B, H_kv, H_kv, D, 1, P, block_table.shape[1]), raw)
-    return kept, new_lens
+    return _calls.append(qkv, q_weight, k_weight, cos_sin, positions, key_pages, value_pages,
+                         slot_mapping, page_size, k_scale, v_scale, eps, interleaved, query,
+                         _raw(stream))
 
 
 def pa_kv_evict(key_pages: torch.Tensor, value_pages: torch.Tensor, weight_pages: torch.Tensor,
@@ -487,9 +338,8 @@ def pa_kv_evict(key_pages: torch.Tensor, value_pages: torch.Tensor, weight_pages
     weight_pages [P, H_kv, page_size] fp32; their rows move, in order, to the
     front of dst_block_table's pages (None: in place). Returns (kept [B, H_kv,
     keep] int32 positions, new_lens [B] int32)."""
-    return _kv_evict("pa_kv_evict", torch.bfloat16, key_pages, value_pages, weight_pages,
-                     block_table, context_lens, page_size, keep, sinks, recent, dst_block_table,
-                     kept, new_lens, stream)
+    return _calls.evict(key_pages, value_pages, weight_pages, block_table, context_lens, page_size,
+                        keep, sinks, recent, dst_block_table, kept, new_lens, False, _raw(stream))
 
 
 def pa_kv_evict_fp8(key_pages, value_pages, weight_pages, block_table, context_lens,
@@ -497,68 +347,8 @@ def pa_kv_evict_fp8(key_pages, value_pages, weight_pages, block_table, context_l
                     dst_block_table=None, kept=None, new_lens=None,
                     stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
     """pa_kv_evict over uint8 e4m3 pools (the codes move as they are)."""
-    return _kv_evict("pa_kv_evict_fp8", torch.uint8, key_pages, value_pages, weight_pages,
-                     block_table, context_lens, page_size, keep, sinks, recent, dst_block_table,
-                     kept, new_lens, stream)
-
-
-def _paged(query, key_pages, value_pages, block_table, context_lens, page_size, scale, out,
-           pool_dtype, stream):
-    """Checks shared by the attention calls below: (shape, the pointers of
-    query and pools, those of the tables, scale, out, its pointer, device index,
-    raw stream, device guard)."""
-    if not query.is_cuda:
-        raise ValueError("query must be a CUDA tensor")
-    B, H_q, L, D = query.shape
-    if key_pages.dim() != 4 or value_pages.shape != key_pages.shape:
-        raise ValueError("page pools must be [P, H_kv, page_size, D]")
-    P, H_kv, ps, D_pool = key_pages.shape
-    if ps != page_size:
-        raise ValueError("page pool shape does not match page_size")
-    if D_pool != D:
-        raise ValueError("query and pages disagree on head_dim")
-    if block_table.dim() != 2 or block_table.shape[0] != B or context_lens.shape != (B,):
-        raise ValueError("block_table must be [B, max_pages] and context_lens [B]")
-    dev = query.get_device()
-    raw, guard = _on_device(dev, stream)
-    ptrs = (_ptr(query, torch.bfloat16, dev, "query"), _ptr(key_pages, pool_dtype, dev, "key_pages"),
-            _ptr(value_pages, pool_dtype, dev, "value_pages"))
-    tables = (_ptr(block_table, torch.int32, dev, "block_table"),
-              _ptr(context_lens, torch.int32, dev, "context_lens"))
-    if out is None:
-        out = torch.empty_like(query)
-        _keep_for(out, stream)
-    elif out.shape != query.shape:
-        raise ValueError("out must have the query's shape")
-    return (pa_shape(B, H_q, H_kv, D, L, P, block_table.shape[1]), ptrs, tables,
-            1.0 / math.sqrt(D) if scale is None else scale, out,
-            _ptr(out, torch.bfloat16, dev, "out"), dev, raw, guard)
-
-
-def _workspace(workspace, size, guard, sizes, query, stream):
-    """(pointer, bytes, tensor) of the caller's workspace, or of one made for
-    this call with the bytes that the library's `size(*sizes)` names."""
-    if workspace is None:
-        if guard is None:
-            need = size(*sizes)
-        else:
-            with guard:
-                need = size(*sizes)
-        workspace = _scratch(need, query.device, stream)
-    elif workspace.get_device() != query.get_device():
-        raise ValueError(f"workspace is on {workspace.device}, expected {query.device}")
-    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
-
-
-def _window(fn, size, size_args, query, key_pages, value_pages, block_table, context_lens,
-            page_size, scales, window, sinks, scale, out, max_context_len, workspace, stream):
-    shape, ptrs, tables, scale, out, out_ptr, _, raw, guard = _paged(
-        query, key_pages, value_pages, block_table, context_lens, page_size, scale, out,
-        torch.uint8 if scales else torch.bfloat16, stream)
-    ws, ws_bytes, keep = _workspace(workspace, size, guard, (shape,) + size_args, query, stream)
-    _launch(fn, fn.__name__, guard, *ptrs, *tables, page_size, scale, *scales, window, sinks,
-            out_ptr, shape, max_context_len, ws, ws_bytes, raw)
-    return out
+    return _calls.evict(key_pages, value_pages, weight_pages, block_table, context_lens, page_size,
+                        keep, sinks, recent, dst_block_table, kept, new_lens, True, _raw(stream))
 
 
 def pa_decode_window(query: torch.Tensor, key_pages: torch.Tensor, value_pages: torch.Tensor,
@@ -568,9 +358,9 @@ def pa_decode_window(query: torch.Tensor, key_pages: torch.Tensor, value_pages: 
                      workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """pa_decode where the row at position p sees keys j <= p with
     j > p - window or j < sinks; pages that no row sees are not touched."""
-    return _window(_lib.pa_decode_window, _lib.pa_decode_window_workspace_bytes, (), query, key_pages,
-                   value_pages, block_table, context_lens, page_size, (), window, sinks, scale, out,
-                   max_context_len, workspace, stream)
+    return _calls.window(0, query, key_pages, value_pages, block_table, context_lens, page_size,
+                         None, None, window, sinks, scale, out, max_context_len, workspace,
+                         _raw(stream))
 
 
 def pa_decode_window_fp8(query, key_pages, value_pages, block_table, context_lens, page_size: int,
@@ -578,9 +368,9 @@ def pa_decode_window_fp8(query, key_pages, value_pages, block_table, context_len
                          scale: Optional[float] = None, out=None, max_context_len: int = 0,
                          workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """pa_decode_window over uint8 e4m3 pools."""
-    return _window(_lib.pa_decode_window_fp8, _lib.pa_decode_window_workspace_bytes, (), query, key_pages,
-                   value_pages, block_table, context_lens, page_size, (k_scale, v_scale), window,
-                   sinks, scale, out, max_context_len, workspace, stream)
+    return _calls.window(0, query, key_pages, value_pages, block_table, context_lens, page_size,
+                         k_scale, v_scale, window, sinks, scale, out, max_context_len, workspace,
+                         _raw(stream))
 
 
 def pa_decode_window_workspace_bytes(shape: pa_shape, device: Optional[torch.device] = None) -> int:
@@ -593,12 +383,8 @@ def pa_prefill_window(query: torch.Tensor, key_pages: torch.Tensor, value_pages:
                       window: int, sinks: int = 0, scale: Optional[float] = None,
                       out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """pa_decode_window's result on the tensor-core prefill kernel."""
-    shape, ptrs, tables, scale, out, out_ptr, _, raw, guard = _paged(
-        query, key_pages, value_pages, block_table, context_lens, page_size, scale, out,
-        torch.bfloat16, stream)
-    _launch(_lib.pa_prefill_window, "pa_prefill_window", guard, *ptrs, *tables, page_size, scale,
-            window, sinks, out_ptr, shape, raw)
-    return out
+    return _calls.window(1, query, key_pages, value_pages, block_table, context_lens, page_size,
+                         None, None, window, sinks, scale, out, 0, None, _raw(stream))
 
 
 def pa_attention_window_workspace_bytes(shape: pa_shape, page_size: int, max_context_len: int,
@@ -626,10 +412,9 @@ def pa_attention_window(query: torch.Tensor, key_pages: torch.Tensor, value_page
                         workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """The dispatch: pa_decode_window for short queries, pa_prefill_window
     beyond."""
-    return _window(_lib.pa_attention_window, _lib.pa_attention_window_workspace_bytes,
-                   (page_size, max_context_len, window, sinks), query, key_pages, value_pages,
-                   block_table, context_lens, page_size, (), window, sinks, scale, out,
-                   max_context_len, workspace, stream)
+    return _calls.window(2, query, key_pages, value_pages, block_table, context_lens, page_size,
+                         None, None, window, sinks, scale, out, max_context_len, workspace,
+                         _raw(stream))
 
 
 def pa_attention_window_fp8(query, key_pages, value_pages, block_table, context_lens,
@@ -641,31 +426,15 @@ def pa_attention_window_fp8(query, key_pages, value_pages, block_table, context_
     None reads context_lens.max() (a device-to-host copy)."""
     if max_context_len is None:
         max_context_len = int(context_lens.max().item())
-    return _window(_lib.pa_attention_window_fp8, _lib.pa_attention_window_fp8_workspace_bytes,
-                   (page_size, max_context_len, window, sinks), query, key_pages, value_pages,
-                   block_table, context_lens, page_size, (k_scale, v_scale), window, sinks, scale,
-                   out, max_context_len, workspace, stream)
+    return _calls.window(2, query, key_pages, value_pages, block_table, context_lens, page_size,
+                         k_scale, v_scale, window, sinks, scale, out, max_context_len, workspace,
+                         _raw(stream))
 
 
 def pa_decode_weights_workspace_bytes(shape: pa_shape, max_context_len: int,
                                       device: Optional[torch.device] = None) -> int:
     with torch.cuda.device(device if device is not None else torch.cuda.current_device()):
         return int(_lib.pa_decode_weights_workspace_bytes(shape, int(max_context_len)))
-
-
-def _weights(fn, query, key_pages, value_pages, weight_pages, block_table, context_lens,
-             page_size, scales, max_context_len, decay, scale, causal, out, workspace, stream):
-    if weight_pages.shape != key_pages.shape[:3]:
-        raise ValueError("weight_pages must be [P, H_kv, page_size]")
-    shape, ptrs, tables, scale, out, out_ptr, dev, raw, guard = _paged(
-        query, key_pages, value_pages, block_table, context_lens, page_size, scale, out,
-        torch.uint8 if scales else torch.bfloat16, stream)
-    weights = _ptr(weight_pages, torch.float32, dev, "weight_pages")
-    ws, ws_bytes, keep = _workspace(workspace, _lib.pa_decode_weights_workspace_bytes, guard,
-                                    (shape, max_context_len), query, stream)
-    _launch(fn, fn.__name__, guard, *ptrs, weights, *tables, page_size, scale, *scales,
-            1 if causal else 0, decay, out_ptr, shape, max_context_len, ws, ws_bytes, raw)
-    return out
 
 
 def pa_decode_weights(query: torch.Tensor, key_pages: torch.Tensor, value_pages: torch.Tensor,
@@ -679,9 +448,9 @@ def pa_decode_weights(query: torch.Tensor, key_pages: torch.Tensor, value_pages:
     got, summed over the group's heads and the rows (old: 0 for the L newest
     positions, and everywhere when decay is 0). max_context_len bounds
     context_lens."""
-    return _weights(_lib.pa_decode_weights, query, key_pages, value_pages, weight_pages, block_table,
-                    context_lens, page_size, (), max_context_len, decay, scale, causal, out,
-                    workspace, stream)
+    return _calls.weights(query, key_pages, value_pages, weight_pages, block_table, context_lens,
+                          page_size, None, None, max_context_len, decay, scale, causal, out,
+                          workspace, _raw(stream))
 
 
 def pa_decode_weights_fp8(query, key_pages, value_pages, weight_pages, block_table, context_lens,
@@ -690,9 +459,9 @@ def pa_decode_weights_fp8(query, key_pages, value_pages, weight_pages, block_tab
                           out=None, workspace: Optional[torch.Tensor] = None,
                           stream=None) -> torch.Tensor:
     """pa_decode_weights over uint8 e4m3 pools."""
-    return _weights(_lib.pa_decode_weights_fp8, query, key_pages, value_pages, weight_pages,
-                    block_table, context_lens, page_size, (k_scale, v_scale), max_context_len,
-                    decay, scale, causal, out, workspace, stream)
+    return _calls.weights(query, key_pages, value_pages, weight_pages, block_table, context_lens,
+                          page_size, k_scale, v_scale, max_context_len, decay, scale, causal, out,
+                          workspace, _raw(stream))
 
 
 def pa_decode_fp8(query, key_pages, value_pages, block_table, context_lens, page_size: int,

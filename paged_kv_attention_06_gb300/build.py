@@ -2,7 +2,8 @@
 
 Every .cu file under csrc/ is compiled in parallel (one -gencode, no other
 architecture), then linked into ``_build/libpagedattn.so`` against the shared
-CUDA runtime. Re-running is cheap: nothing is rebuilt when the library is
+CUDA runtime; ``_build/_pagedattn_calls.so`` is the Python side of the newer
+calls. Re-running is cheap: nothing is rebuilt when the library is
 newer than every source and header.
 """
 from __future__ import annotations
@@ -22,6 +23,11 @@ LIB = os.path.join(BUILD, "libpagedattn.so")
 ROOT = os.path.dirname(HERE)
 BENCH_SRC = os.path.join(ROOT, "bench_loop.cpp")
 BENCH_LIB = os.path.join(BUILD, "libpabench.so")
+
+# The Python side of the newer calls (pa_python.cpp): a CPython module that
+# reads torch tensors directly.
+PYTHON_SRC = os.path.join(CSRC, "pa_python.cpp")
+PYTHON_LIB = os.path.join(BUILD, "_pagedattn_calls.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
@@ -43,14 +49,14 @@ def _sources():
 def _deps():
     return (_sources() + glob.glob(os.path.join(CSRC, "*.h")) +
             glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(INCLUDE, "*.h")) +
-            [os.path.abspath(__file__)])
+            [PYTHON_SRC, os.path.abspath(__file__)])
 
 
 def up_to_date() -> bool:
-    for lib in (LIB, BENCH_LIB):
-        if not os.path.exists(lib):
-            return False
-    t = min(os.path.getmtime(LIB), os.path.getmtime(BENCH_LIB))
+    libs = (LIB, BENCH_LIB, PYTHON_LIB)
+    if not all(os.path.exists(lib) for lib in libs):
+        return False
+    t = min(os.path.getmtime(lib) for lib in libs)
     return all(os.path.getmtime(p) <= t for p in _deps() + [BENCH_SRC])
 
 
@@ -72,9 +78,30 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
             raise RuntimeError(f"nvcc failed on {os.path.basename(src)}")
         return obj
 
+    def compile_python() -> str:
+        import sysconfig
+        import torch
+        root = os.path.dirname(torch.__file__)
+        obj = os.path.join(BUILD, "pa_python.o")
+        cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-I", INCLUDE,
+               "-I", sysconfig.get_paths()["include"],
+               "-I", os.path.join(root, "include"),
+               "-I", os.path.join(root, "include", "torch", "csrc", "api", "include"),
+               "-I", os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc))), "include"),
+               f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+               "-c", PYTHON_SRC, "-o", obj]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if verbose or r.returncode:
+            sys.stderr.write(r.stdout + r.stderr)
+        if r.returncode:
+            raise RuntimeError("compiling pa_python.cpp failed")
+        return obj
+
     srcs = _sources()
-    with ThreadPoolExecutor(max_workers=max(1, min(len(srcs), os.cpu_count() or 1))) as ex:
+    with ThreadPoolExecutor(max_workers=max(2, min(len(srcs) + 1, os.cpu_count() or 1))) as ex:
+        python_obj = ex.submit(compile_python)
         objs = list(ex.map(compile_one, srcs))
+        python_obj = python_obj.result()
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = [nvcc, *ARCH, "-shared", "-cudart", "shared", "-o", tmp, *objs,
            "-Xlinker", "-soname=libpagedattn.so", "-Xlinker", "-rpath=/usr/local/cuda/lib64"]
@@ -83,6 +110,17 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
         sys.stderr.write(r.stdout + r.stderr)
         raise RuntimeError("nvcc link failed")
     os.replace(tmp, LIB)
+    import torch
+    torch_lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = PYTHON_LIB + f".tmp{os.getpid()}"
+    cmd = ["g++", "-shared", "-o", tmp, python_obj, "-L", BUILD, "-lpagedattn", "-L", torch_lib,
+           "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN",
+           f"-Wl,-rpath,{torch_lib}"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode:
+        sys.stderr.write(r.stdout + r.stderr)
+        raise RuntimeError("linking _pagedattn_calls failed")
+    os.replace(tmp, PYTHON_LIB)
     # The benchmark's native step loops (bench_loop.cpp, beside bench.py):
     # host code only, linked against the library above.
     if os.path.exists(BENCH_SRC):
