@@ -623,10 +623,25 @@ pa_status pa_kv_cache_release(pa_kv_cache *cache, int64_t seq_id);
  * back the pages behind them, last page first: the host side of pa_kv_evict in
  * place, whose new length min(context length, keep) the host knows without
  * reading the device. The pages may be handed out to work that follows on the
- * same stream. PA_ERR_INVALID_ARG (nothing changed) for an unknown seq_id or
- * another new_len.
+ * same stream. PA_ERR_INVALID_ARG (nothing changed) for an unknown seq_id,
+ * another new_len, or one that ends inside a page given back by
+ * pa_kv_cache_trim_window.
  */
 pa_status pa_kv_cache_truncate(pa_kv_cache *cache, int64_t seq_id, int32_t new_len);
+
+/*
+ * Gives back the full pages of seq_id that no later row sees through a sliding
+ * window of `window` keys and the first `sinks` keys (pa_decode_window's mask, for
+ * query rows at positions from the current length on): the host side of the
+ * window calls. The pages' block-table entries are -1 from then on; the length
+ * and all other positions stay. Call it after the step whose rows still saw
+ * them was issued; the pages may be handed out to work that follows on the same
+ * stream. A sequence trimmed for one window must not be attended to with a larger
+ * one. PA_ERR_INVALID_ARG (nothing changed) for an unknown seq_id, window < 1 or
+ * sinks < 0.
+ */
+pa_status pa_kv_cache_trim_window(pa_kv_cache *cache, int64_t seq_id, int32_t window,
+                                  int32_t sinks);
 
 /* Pages not held by any request; -1 on a null cache. */
 int32_t pa_kv_cache_free_pages(const pa_kv_cache *cache);

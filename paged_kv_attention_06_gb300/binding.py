@@ -127,6 +127,8 @@ def _load() -> ctypes.CDLL:
     lib.pa_version.restype = ctypes.c_char_p
     lib.pa_kv_cache_truncate.argtypes = [vp, ctypes.c_int64, i32]
     lib.pa_kv_cache_truncate.restype = ctypes.c_int
+    lib.pa_kv_cache_trim_window.argtypes = [vp, ctypes.c_int64, i32, i32]
+    lib.pa_kv_cache_trim_window.restype = ctypes.c_int
     lib.pa_decode_window_workspace_bytes.argtypes = [pa_shape]
     lib.pa_decode_window_workspace_bytes.restype = sz
     for f in (lib.pa_attention_window_workspace_bytes, lib.pa_attention_window_fp8_workspace_bytes):
@@ -810,6 +812,12 @@ class KVCache:
         them (after pa_kv_evict in place: min(context length, keep))."""
         _check(_lib.pa_kv_cache_truncate(self._h, int(seq_id), int(new_len)),
                "pa_kv_cache_truncate")
+
+    def trim_window(self, seq_id: int, window: int, sinks: int = 0) -> None:
+        """Free the full pages that no later row sees through the window (their
+        table entries become -1)."""
+        _check(_lib.pa_kv_cache_trim_window(self._h, int(seq_id), int(window), int(sinks)),
+               "pa_kv_cache_trim_window")
 
     @property
     def free_pages(self) -> int:

@@ -30,7 +30,7 @@
 namespace {
 
 struct Sequence {
-    std::vector<int32_t> pages;
+    std::vector<int32_t> pages;   // -1: given back by pa_kv_cache_trim_window
     int32_t len = 0;       // tokens cached
 };
 
@@ -80,6 +80,27 @@ void undo(pa_kv_cache* c, const std::vector<Taken>& log)
     }
 }
 
+// Room on the free list for n more pages; false (nothing changed) without
+// host memory.
+bool reserve_free(pa_kv_cache* c, size_t n)
+{
+    try {
+        c->free_list.reserve(c->free_list.size() + n);
+    } catch (const std::bad_alloc&) {
+        return false;
+    }
+    return true;
+}
+
+// A page (or -1, given back before) onto the free list.
+void give_back(pa_kv_cache* c, int32_t page)
+{
+    if (page < 0)
+        return;
+    c->free_list.push_back(page);
+    --c->held;
+}
+
 }  // namespace
 
 struct pa_kv_cache_snapshot {
@@ -122,8 +143,10 @@ pa_status pa_kv_cache_release(pa_kv_cache* cache, int64_t seq_id)
     if (it == cache->seqs.end())
         return PA_ERR_INVALID_ARG;   // unknown, or released already
     for (int32_t p : it->second.pages)
-        cache->free_list.push_back(p);
-    cache->held -= int32_t(it->second.pages.size());
+        if (p >= 0) {
+            cache->free_list.push_back(p);
+            --cache->held;
+        }
     cache->seqs.erase(it);
     return PA_OK;
 }
@@ -137,18 +160,42 @@ pa_status pa_kv_cache_truncate(pa_kv_cache* cache, int64_t seq_id, int32_t new_l
         return PA_ERR_INVALID_ARG;
     Sequence& s = it->second;
     const size_t held = (size_t(new_len) + cache->page_size - 1) / size_t(cache->page_size);
-    const size_t give = s.pages.size() - held;
-    try {
-        cache->free_list.reserve(cache->free_list.size() + give);
-    } catch (const std::bad_alloc&) {
+    // the next token would go into a page that was given back
+    if (new_len % cache->page_size != 0 && s.pages[held - 1] < 0)
+        return PA_ERR_INVALID_ARG;
+    if (!reserve_free(cache, s.pages.size() - held))
         return PA_ERR_NO_PAGES;   // no host memory; nothing changed
-    }
-    for (size_t k = 0; k < give; ++k) {
-        cache->free_list.push_back(s.pages.back());
+    while (s.pages.size() > held) {
+        give_back(cache, s.pages.back());
         s.pages.pop_back();
     }
-    cache->held -= int32_t(give);
     s.len = new_len;
+    return PA_OK;
+}
+
+pa_status pa_kv_cache_trim_window(pa_kv_cache* cache, int64_t seq_id, int32_t window, int32_t sinks)
+{
+    if (!cache || window <= 0 || sinks < 0)
+        return PA_ERR_INVALID_ARG;
+    auto it = cache->seqs.find(seq_id);
+    if (it == cache->seqs.end())
+        return PA_ERR_INVALID_ARG;
+    Sequence& s = it->second;
+    // The next token sits at position len and sees len - window + 1 and on. The
+    // page it goes into stays.
+    const int64_t ps = cache->page_size;
+    const int64_t seen = int64_t(s.len) - window + 1;
+    const int64_t full = s.len / ps;
+    const int64_t end = seen > 0 ? (seen / ps < full ? seen / ps : full) : 0;
+    const int64_t begin = (int64_t(sinks) + ps - 1) / ps;
+    if (begin >= end)
+        return PA_OK;
+    if (!reserve_free(cache, size_t(end - begin)))
+        return PA_ERR_NO_PAGES;
+    for (int64_t j = end - 1; j >= begin; --j) {
+        give_back(cache, s.pages[size_t(j)]);
+        s.pages[size_t(j)] = -1;
+    }
     return PA_OK;
 }
 

@@ -1,5 +1,5 @@
-"""pa_kv_evict's argument checks through the C ABI and pa_kv_cache_truncate,
-without a GPU."""
+"""pa_kv_evict's argument checks through the C ABI, pa_kv_cache_truncate and
+pa_kv_cache_trim_window, without a GPU."""
 import ctypes
 
 import numpy as np
@@ -110,3 +110,58 @@ def test_truncate_refusals_and_snapshot():
     assert c.context_len(1) == 10 and c.free_pages == 5
     bt, cl, sm = c.plan([1], [1], 8, 1)
     assert cl[0] == 11 and np.all(bt[0, :3] >= 0)
+
+
+@pytest.mark.parametrize("ps", [1, 4, 16])
+@pytest.mark.parametrize("window,sinks", [(1, 0), (5, 0), (20, 3), (20, 16), (33, 1), (1000, 4)])
+def test_trim_window_keeps_what_later_rows_see(ps, window, sinks):
+    import paged_kv_attention_06_gb300 as pa
+    c = pa.KVCache(200, ps)
+    c.add(1)
+    rows = {}
+    n = 0
+    for step in (1, 7, 30, 1, 1, 45, 1):
+        bt, cl, sm = c.plan([1], [step], 120, 45)
+        n += step
+        assert cl[0] == n
+        # every key that the step's rows see is in a page the request holds, in
+        # the slot it was written to
+        for t in range(n - step, n):
+            rows[t] = sm[0, t - (n - step)]
+        for p in range(n - step, n):
+            for j in range(n):
+                if j <= p and (j > p - window or j < sinks):
+                    assert bt[0, j // ps] * ps + j % ps == rows[j]
+        c.trim_window(1, window, sinks)
+        held = 200 - c.free_pages
+        seen = [j for j in range(n) if j > n - window or j < sinks]
+        need = {j // ps for j in seen} | ({n // ps} if n % ps else set())
+        assert held == len(need)
+        c.trim_window(1, window, sinks)              # again: nothing more
+        assert held == 200 - c.free_pages
+    snap = c.snapshot()
+    c.release(1)
+    assert c.free_pages == 200
+    c.restore(snap)
+    assert c.free_pages == 200 - held and c.context_len(1) == n
+
+
+def test_trim_window_refusals_and_truncate_after_it():
+    import paged_kv_attention_06_gb300 as pa
+    c = pa.KVCache(16, 4)
+    c.add(1)
+    c.plan([1], [30], 16, 30)
+    for args in ((2, 4, 0), (1, 0, 0), (1, -1, 0), (1, 4, -1)):
+        with pytest.raises(pa.PagedAttentionError) as e:
+            c.trim_window(*args)
+        assert e.value.status == pa.PA_ERR_INVALID_ARG
+    assert c.free_pages == 8
+    c.trim_window(1, 6, 4)                           # pages 1 .. 5 (positions 4 .. 23) go
+    assert c.free_pages == 13
+    with pytest.raises(pa.PagedAttentionError):      # would go on inside a freed page
+        c.truncate(1, 10)
+    assert c.context_len(1) == 30 and c.free_pages == 13
+    c.truncate(1, 8)                                 # at a page border
+    assert c.free_pages == 15
+    bt, cl, sm = c.plan([1], [1], 16, 1)
+    assert cl[0] == 9 and list(bt[0, :3] >= 0) == [True, False, True]
