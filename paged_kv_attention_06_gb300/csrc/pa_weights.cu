@@ -14,6 +14,7 @@
 // row, and of the page row where pages hold at least four slots and the pool
 // is aligned to 16 bytes (otherwise four single slots). The page id and the old
 // weights are requested before the scores.
+#include <math.h>
 #include <stdint.h>
 
 #include "pa_device.cuh"
@@ -30,16 +31,19 @@ template <bool kVector>
 __global__ void __launch_bounds__(kThreads) accumulate_weights_kernel(const WeightArgs a)
 {
     __shared__ float2 state[kThreads];               // (max, 1 / sum) of up to kThreads rows
-    grid_dependency_wait();
     grid_launch_dependents();
+    // Lengths, tables and weights are inputs of the whole call: complete before
+    // the decode pass began, and read before this kernel waits for it.
     const int64_t bh = blockIdx.x / a.chunks;
     const int chunk = int(blockIdx.x - bh * a.chunks);
     const int b = int(bh / a.H_kv), h = int(bh - int64_t(b) * a.H_kv);
     int n = a.context_lens[b];
     const int cap = min(a.max_pages << a.ps_shift, a.score_cap);
     n = n < 0 ? 0 : n > cap ? cap : n;               // recorded by the decode pass
-    if (chunk * kSpan >= n)
+    if (chunk * kSpan >= n) {
+        grid_dependency_wait();                      // no block of the call ends before its first kernels
         return;
+    }
     const int pos = chunk * kSpan + int(threadIdx.x) * kEach;
     const int32_t* bt = a.block_table + int64_t(b) * a.max_pages;
     const int fresh = a.decay != 0.f ? n - a.L : 0;  // positions from here on start at 0
@@ -80,25 +84,38 @@ __global__ void __launch_bounds__(kThreads) accumulate_weights_kernel(const Weig
     // within it.
     const float* s = a.scores + bh * a.R * a.score_stride + pos;
     float w[kEach] = {0.f, 0.f, 0.f, 0.f};
+    grid_dependency_wait();
     for (int r0 = 0; r0 < a.R; r0 += kThreads) {
         __syncthreads();
         const int rows = min(kThreads, a.R - r0);
+        // the first scores come with the states
+        constexpr int kAhead = 4;
+        float4 v[kAhead];
+#pragma unroll
+        for (int r = 0; r < kAhead; ++r)
+            v[r] = pos < n && r < rows ? __ldcg(reinterpret_cast<const float4*>(s + (r0 + r) * a.score_stride))
+                                       : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
         if (int(threadIdx.x) < rows) {
             const float2 st = a.row_state[bh * a.R + r0 + threadIdx.x];
             // a row that sees nothing: every score is -inf and weighs 0
             state[threadIdx.x] = make_float2(st.x == -INFINITY ? 0.f : st.x, st.y > 0.f ? 1.f / st.y : 0.f);
         }
         __syncthreads();
+        auto add = [&](int r, float4 x) {
+            const float2 st = state[r];
+            w[0] = fmaf(fast_exp2(x.x - st.x), st.y, w[0]);
+            w[1] = fmaf(fast_exp2(x.y - st.x), st.y, w[1]);
+            w[2] = fmaf(fast_exp2(x.z - st.x), st.y, w[2]);
+            w[3] = fmaf(fast_exp2(x.w - st.x), st.y, w[3]);
+        };
+#pragma unroll
+        for (int r = 0; r < kAhead; ++r)
+            if (r < rows)
+                add(r, v[r]);
         if (pos < n)
 #pragma unroll 4
-            for (int r = 0; r < rows; ++r) {
-                const float4 v = __ldcg(reinterpret_cast<const float4*>(s + (r0 + r) * a.score_stride));
-                const float2 st = state[r];
-                w[0] = fmaf(fast_exp2(v.x - st.x), st.y, w[0]);
-                w[1] = fmaf(fast_exp2(v.y - st.x), st.y, w[1]);
-                w[2] = fmaf(fast_exp2(v.z - st.x), st.y, w[2]);
-                w[3] = fmaf(fast_exp2(v.w - st.x), st.y, w[3]);
-            }
+            for (int r = kAhead; r < rows; ++r)
+                add(r, __ldcg(reinterpret_cast<const float4*>(s + (r0 + r) * a.score_stride)));
     }
 #pragma unroll
     for (int u = 0; u < kEach; ++u)
