@@ -260,6 +260,13 @@ __device__ __forceinline__ unsigned arrive_piece(unsigned long long* w, uint32_t
     }
 }
 
+// Whoever merges clears the word: a replayed graph launches with the same stamp
+// and has to find it empty.
+__device__ __forceinline__ void clear_piece(unsigned long long* w)
+{
+    *reinterpret_cast<volatile unsigned long long*>(w) = 0ull;
+}
+
 // The merge of an item's two parts, each held as O / l (bf16) with its (m, l):
 // out = w0 (O_0 / l_0) + w1 (O_1 / l_1), w_k = l_k 2^(m_k - M) out_scale / l,
 // M = max(m_0, m_1), l = l_0 2^(m_0 - M) + l_1 2^(m_1 - M). Whichever block
@@ -330,6 +337,8 @@ __device__ __forceinline__ void piece_arrive_receiver(const uint4* state, const 
     old = __shfl_sync(0xffffffffu, old, 0);
     if (old == 0)
         return;                                // the donor merges
+    if (lane == 0)
+        clear_piece(arrive + (int64_t(slot) * 2 + head) * 4 + w4);
     __threadfence();                           // the donor's state, stored before its arrival
     __syncwarp();
     const int r = w4 * 32 + lane;
@@ -1138,6 +1147,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                             skip = old == 0;
                             __threadfence();
                         }
+                        if (!skip && lane == 0)
+                            clear_piece(w);
                         __syncwarp();
                         const int64_t i0 = piece_state(slot, 0, head);
                         w_m = merge_weights(__ldcg(a.state_ml + i0 * 128 + r), make_float2(m_used, l),
