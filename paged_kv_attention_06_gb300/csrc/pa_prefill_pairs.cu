@@ -120,9 +120,7 @@ static_assert(kMmaDone < Layout<128>::kNumBars, "barrier count");
 // head 0, the first K/V tile run here, the role (below), the tail piece's
 // state slot (its donor block).
 enum { kEB = 0, kET, kEH0, kEH1, kEHK, kEN, kENT, kEDup, kEK0, kERole, kESlot, kEntry = 12 };
-// With a sliding window (kWin) an item's tiles are those of the sinks, then
-// those from the window's first page on: kEK0 holds the number of the first,
-// kESlot the first key of the second (there are no pieces then).
+// With a sliding window (kWin) an item visits runs of keys (window_span).
 // Item roles: the whole item here; the item's last tiles here, state left
 // for its first block (run first on the receiving block); the item's first
 // tiles here, merged at the end with the state its last tiles left.
@@ -362,23 +360,27 @@ __device__ __forceinline__ void piece_arrive_receiver(const uint4* state, const 
     }
 }
 
-// The keys of an item with a sliding window: tiles of 128 keys over [0,
-// sinks), then from `start`, the first key that the item's first row sees
-// through the window (first_seen) rounded down to a page (or 128 keys within a
-// larger page), so that no page is touched that no row sees; one run from 0
-// where the two would meet. `keys`: one past the last key that a row sees.
+// The keys of an item with a sliding window: those of [0, sinks), rounded up to
+// whole boxes (`sink_keys`), then those from `start` on, the first key that the
+// item's first row sees through the window rounded down to a box; one run
+// from 0 where the two would meet. Boxes lie within a page and none is touched
+// that no row sees. The two runs are laid end to end and cut into tiles of 128
+// places, so the sinks rarely cost a tile of their own: key j is place j before
+// sink_keys and place j + shift from there on.
 struct WindowSpan {
-    int sink_tiles, start, first_seen, tiles;
+    int sink_keys, start, shift;
+    int first_seen;      // place of the first key that a row sees through the window
 };
-__device__ __forceinline__ WindowSpan window_span(const PrefillArgs& a, int n, int row0, int keys)
+__device__ __forceinline__ WindowSpan window_span(const PrefillArgs& a, int n, int row0)
 {
     WindowSpan s;
-    s.first_seen = int(max(int64_t(0), int64_t(n) - a.L + row0 - a.window + 1));
-    const int start = s.first_seen & ~(a.box_rows - 1);
+    const int first = int(max(int64_t(0), int64_t(n) - a.L + row0 - a.window + 1));
+    const int start = first & ~(a.box_rows - 1);
     const bool apart = start > a.sinks;
-    s.sink_tiles = apart ? (a.sinks + kKeys - 1) / kKeys : 0;
+    s.sink_keys = apart ? (a.sinks + a.box_rows - 1) & ~(a.box_rows - 1) : 0;
     s.start = apart ? start : 0;
-    s.tiles = keys <= 0 ? 0 : s.sink_tiles + (keys - s.start + kKeys - 1) / kKeys;
+    s.shift = s.sink_keys - s.start;
+    s.first_seen = first + s.shift;
     return s;
 }
 
@@ -451,7 +453,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         nk = nk < 0 ? 0 : nk;
         *n_out = nn;
         if constexpr (kWin)
-            return window_span(a, nn, r0, nk).tiles;
+            return nk <= 0 ? 0 : (nk + window_span(a, nn, r0).shift + kKeys - 1) / kKeys;
         return (nk + kKeys - 1) / kKeys;
     };
     // scratch until the epilogues: the ranking, and the tiles and context
@@ -541,20 +543,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             e[kENT] = nt;
             e[kERole] = kWhole;
         }
-        if constexpr (kWin) {
-            const WindowSpan ws = window_span(a, n, t * kRows, n);
-            e[kEK0] = ws.sink_tiles;
-            e[kESlot] = ws.start;
-        }
     }
-    // First key of tile j of an item (k0, slot: its entries kEK0, kESlot), and
-    // the end of the keys that the tile's run holds.
-    auto tile_key0 = [&](int k0, int slot, int j) {
-        if constexpr (kWin)
-            return j < k0 ? j * kKeys : slot + (j - k0) * kKeys;
-        return (k0 + j) * kKeys;
+    auto span_of_item = [&](int n, int t) {
+        return kWin ? window_span(a, n, t * kRows) : WindowSpan{0, 0, 0, 0};
     };
-    auto tile_end = [&](int k0, int n, int j) { return kWin && j < k0 ? a.sinks : n; };
+    // The key at a place of the item's runs.
+    auto key_of = [&](const WindowSpan& ws, int place) {
+        return kWin && place >= ws.sink_keys ? place - ws.shift : place;
+    };
 
     const uint32_t sQ = smem_u32(smem + Layout::kQ);
     const uint32_t sK = smem_u32(smem + Layout::kK);
@@ -637,29 +633,30 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int it = 0; it < n_items; ++it) {
                 const int32_t* e = items + it * kEntry;
                 const int nt = e[kENT], k0 = e[kEK0];
-                const int slot = kWin ? e[kESlot] : 0;
                 if (nt == 0)
                     continue;
                 const int b = e[kEB], n = e[kEN], hk = e[kEHK];
+                const WindowSpan ws = span_of_item(n, e[kET]);
+                const int end = kWin ? n + ws.shift : n;     // places
                 const int32_t* bt = a.block_table + int64_t(b) * a.max_pages;
                 // tile j of the piece is the item's K/V tile k0 + j
                 auto n_boxes = [&](int j) {
-                    const int key0 = tile_key0(k0, slot, j);
-                    return (min(tile_end(k0, n, j), key0 + kKeys) - key0 + box - 1) / box;
+                    const int key0 = (k0 + j) * kKeys;
+                    return (min(end, key0 + kKeys) - key0 + box - 1) / box;
                 };
                 // Raw block-table entry of this lane's box in tile j, loaded
                 // ahead of use and checked at use (entry 0 when the box does
                 // not exist, so that nothing waits for it before use).
                 auto fetch_page = [&](int j) -> int {
                     const bool live = j < nt && my_box < n_boxes(j);
-                    return bt[live ? (tile_key0(k0, slot, j) + my_box * box) / a.ps : 0];
+                    return bt[live ? key_of(ws, (k0 + j) * kKeys + my_box * box) / a.ps : 0];
                 };
                 auto pool_row = [&](int j, int phys) -> int {
                     if (unsigned(phys) >= unsigned(a.num_pages)) {
                         atomicOr(a.err, PA_DEVERR_PAGE_ID_BIT);
                         phys = 0;
                     }
-                    const int tok = tile_key0(k0, slot, j) + my_box * box;
+                    const int tok = key_of(ws, (k0 + j) * kKeys + my_box * box);
                     return (phys * a.H_kv + hk) * a.ps + (tok - (tok / a.ps) * a.ps);
                 };
                 // Pages of fewer than 8 tokens: row r of tile j (row r of
@@ -689,13 +686,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int empty = (is_v ? kVEmpty : kKEmpty) + s;
                     const bool ok = mbar_wait_warp(&bar[empty], ((gj >> 1) & 1) ^ 1u, misc, a.err);
                     if (ok) {
-                        const int key0 = tile_key0(k0, slot, j);
-                        const int end = tile_end(k0, n, j);
+                        const int key0 = (k0 + j) * kKeys;
                         uint8_t* dst = smem + (is_v ? Layout::kV : Layout::kK) + s * Layout::kMat;
                         const uint16_t* pool = is_v ? a.value_pages : a.key_pages;
                         for (int r = li * 32 + lane; r < kKeys; r += 96) {
-                            const int key = key0 + r;
-                            const bool live = key < end;
+                            const int key = key_of(ws, key0 + r);
+                            const bool live = key0 + r < end;
                             int64_t row = 0;
                             if (live) {
                                 int phys = bt[key / a.ps];
@@ -957,11 +953,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int row0 = e[kET] * kRows;
             const int rows = min(kRows, a.L - row0);
             const int i = row0 + r;
-            const int lim = a.causal ? min(n - a.L + i, n - 1) : n - 1;  // last visible key
-            const int slot0 = kWin ? e[kESlot] : 0;
-            const int low = lim - a.window + 1;          // kWin: the window's first key
-            // kWin: the first key that a row of the tile sees through the window
-            const int first_seen = int(max(int64_t(0), int64_t(n) - a.L + row0 - a.window + 1));
+            const WindowSpan ws = span_of_item(n, e[kET]);
+            const int last = a.causal ? min(n - a.L + i, n - 1) : n - 1;  // last visible key
+            const int lim = kWin ? last + ws.shift : last;                // and its place
+            // kWin: place of the window's first key, behind the sinks
+            const int low = kWin ? max(last - a.window + 1 + ws.shift, ws.sink_keys) : 0;
+            const int end = kWin ? n + ws.shift : n;
             float m_used = -INFINITY;
             float l = 0.f;
 
@@ -975,9 +972,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // P overwrites any). Reading the two 64-column halves one after
                 // the other, the lower half twice, was 0.9 us per call slower on
                 // the 512-row batch.
-                const int key0 = tile_key0(k0, slot0, j);
-                const bool first_run = kWin && j < k0;
-                const bool edge = key0 + kKeys - 1 > lim || (kWin && key0 < low);
+                const int key0 = (k0 + j) * kKeys;
+                bool edge = key0 + kKeys - 1 > lim || (kWin && key0 < low);
+                if constexpr (kWin)
+                    edge = __any_sync(0xffffffffu, edge);    // the votes below are the whole warp's
                 uint32_t sv[128];
                 float* s = reinterpret_cast<float*>(sv);
 #pragma unroll
@@ -995,7 +993,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                             const int nl = low - (key0 + 32 * w), nf = a.sinks - (key0 + 32 * w);
                             const uint32_t past = nl >= 32 ? 0xffffffffu : nl <= 0 ? 0u : (1u << nl) - 1u;
                             const uint32_t sink = nf >= 32 ? 0xffffffffu : nf <= 0 ? 0u : (1u << nf) - 1u;
-                            vis &= first_run ? sink : ~past | sink;
+                            vis &= ~past | sink;
+                            // a warp's 32 rows share most of a window's edge
+                            if (__all_sync(0xffffffffu, vis == 0xffffffffu))
+                                continue;
                         }
 #pragma unroll
                         for (int k = 0; k < 32; ++k)
@@ -1064,18 +1065,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tmem_wait_st();
                 // V rows past the context hold stale bytes: zero them (P is 0
                 // there, but 0 * NaN is not) before either head's P V.
-                const int end = tile_end(k0, n, j);
-                if (kWin && head == 0 && (end < key0 + kKeys || (key0 < first_seen && a.sinks < first_seen))) {
-                    // also those between the sinks and what the tile's rows see
+                if (kWin && head == 0 &&
+                    (end < key0 + kKeys || (key0 < ws.first_seen && a.sinks < ws.first_seen))) {
+                    // also those between the sinks and what the item's rows see:
+                    // places [z0, z1) and [z2, 128) of the tile
                     mbar_wait_bounded(&bar[kVFull + (gj & 1)], (gj >> 1) & 1, misc, a.err);
+                    const int z2 = max(min(end - key0, kKeys), 0);
+                    const int z0 = min(max(a.sinks - key0, 0), z2);
+                    const int z1 = min(max(ws.first_seen - key0, z0), z2);
                     constexpr int kRowChunks = kD / 8;
                     uint8_t* vb = smem + Layout::kV + (gj & 1) * Layout::kMat;
-                    for (int idx = r; idx < kKeys * kRowChunks; idx += 128) {
-                        const int zr = idx / kRowChunks, ch = idx % kRowChunks;
-                        const int key = key0 + zr;
-                        if (key >= end || (key >= a.sinks && key < first_seen))
-                            *reinterpret_cast<uint4*>(vb + (ch >> 3) * Layout::kHalf + zr * 128 +
-                                                      (((ch & 7) ^ (zr & 7)) << 4)) = make_uint4(0, 0, 0, 0);
+                    for (int idx = r; idx < (z1 - z0 + kKeys - z2) * kRowChunks; idx += 128) {
+                        int zr = z0 + idx / kRowChunks;
+                        if (zr >= z1)
+                            zr += z2 - z1;
+                        const int ch = idx % kRowChunks;
+                        *reinterpret_cast<uint4*>(vb + (ch >> 3) * Layout::kHalf + zr * 128 +
+                                                  (((ch & 7) ^ (zr & 7)) << 4)) = make_uint4(0, 0, 0, 0);
                     }
                     fence_proxy_async_smem();
                 }
