@@ -334,16 +334,18 @@ __global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const Evic
 }
 
 constexpr int kMoveThreads = 256;
-constexpr int kSlice = 64;                   // bytes of a row per block
+constexpr int kInPlaceSlice = 64;            // bytes of a row per block, in place
 constexpr int kUnroll = 4;                   // rows of a tile per thread
 constexpr int kTableInts = 6 * 1024;         // page ids staged in shared memory
-constexpr int kMinChunk = kMoveThreads / (kSlice / 16) * kUnroll;   // rows: one tile
+constexpr int kChunkBytes = 256 * 1024;      // of K or V per block, where the order is free
+// Rows of one tile, for slices of `slice` bytes.
+__host__ __device__ constexpr int tile_rows(int slice) { return kMoveThreads / (slice / 16) * kUnroll; }
 
 // How a move kernel's blocks take the rows of their (request, KV head): all of
 // them in order (in place), a chunk of them, or one tile of them.
 enum MoveKind : int { kInPlace, kChunk, kTile };
 
-// Rows [j_begin, j_end) of the kept ones. T: uint4 with four threads per row
+// Rows [j_begin, j_end) of the kept ones. T: uint4 with kPerRow threads per row
 // slice, or float with one (the weights). bt, dt: the request's page ids. One
 // tile is in registers while the next one's rows are read, and the positions of
 // the one after are on their way. A row's source is never a destination of an
@@ -408,9 +410,11 @@ __device__ __forceinline__ void move_rows(const EvictArgs& a, T* pool, int64_t r
     }
 }
 
-// Blocks of a (request, KV head): a 64-byte column slice of K or of V, or the
-// weights.
-template <MoveKind kKind>
+// Blocks of a (request, KV head): a column slice of K or of V, or the weights. In
+// place the slices are narrow, since a block takes all rows and only the slices
+// spread the work (8192 rows of 64 heads: 122 us with 64 bytes, 154 with 128);
+// where the order is free they are whole rows (113 us, 124 with 64 bytes).
+template <MoveKind kKind, int kSlice>
 __global__ void __launch_bounds__(kMoveThreads, 4) evict_move_kernel(const EvictArgs a)
 {
     __shared__ int32_t table[kKind == kTile ? 2 : kTableInts];
@@ -478,11 +482,14 @@ cudaError_t launch_evict(EvictArgs a, int device, int sm_count, cudaStream_t str
     const int64_t cap = int64_t(a.max_pages) << a.ps_shift;
     const int64_t rows = cap < a.keep ? cap : a.keep;
     const bool in_place = a.dst_table == a.block_table;
-    a.slices = a.row_bytes / kSlice;
+    const int slice = in_place ? kInPlaceSlice : a.row_bytes;
+    a.slices = a.row_bytes / slice;
     const int64_t parts = heads * (2 * a.slices + 1);
-    // Chunks of 2048 rows, of fewer while that leaves the GPU short of blocks.
-    a.chunk_rows = 2048;
-    while (a.chunk_rows > kMinChunk && parts * ((rows + a.chunk_rows - 1) / a.chunk_rows) < 3 * int64_t(sm_count))
+    // Chunks of kChunkBytes, of less (down to a tile) while that leaves the GPU
+    // short of blocks.
+    a.chunk_rows = kChunkBytes / slice;
+    while (a.chunk_rows > tile_rows(slice) &&
+           parts * ((rows + a.chunk_rows - 1) / a.chunk_rows) < 3 * int64_t(sm_count))
         a.chunk_rows /= 2;
     a.chunks = in_place ? 1 : int((rows + a.chunk_rows - 1) / a.chunk_rows);
     const int64_t moves = parts * a.chunks;
@@ -529,8 +536,12 @@ cudaError_t launch_evict(EvictArgs a, int device, int sm_count, cudaStream_t str
     cfg.blockDim = dim3(kMoveThreads);
     cfg.dynamicSmemBytes = 0;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, in_place ? evict_move_kernel<kInPlace>
-                                    : a.chunk_rows == kMinChunk ? evict_move_kernel<kTile> : evict_move_kernel<kChunk>, a);
+    const bool tile = a.chunk_rows == tile_rows(slice), wide = slice == 256;
+    return cudaLaunchKernelEx(&cfg,
+                              in_place ? evict_move_kernel<kInPlace, kInPlaceSlice>
+                              : tile   ? (wide ? evict_move_kernel<kTile, 256> : evict_move_kernel<kTile, 128>)
+                                       : (wide ? evict_move_kernel<kChunk, 256> : evict_move_kernel<kChunk, 128>),
+                              a);
 }
 
 }  // namespace pa
