@@ -1057,6 +1057,8 @@ pa_status run_evict(void* key_pages, void* value_pages, float* weight_pages,
             ranges_overlap(out, bytes, dst_block_table, uint64_t(s.batch) * dst_max_pages * 4))
             return PA_ERR_INVALID_ARG;
     }
+    if (ranges_overlap(kept, kept_bytes, new_lens, len_bytes))
+        return PA_ERR_INVALID_ARG;
     DeviceInfo* dev;
     pa_status st = device_info(&dev);
     if (st != PA_OK)

@@ -779,7 +779,7 @@ __global__ void __launch_bounds__(kThreads) decode_rows_merge_kernel(const Decod
     const int b = seg / a.H_kv, h = seg - b * a.H_kv;
     const int cap = context_cap<kMode>(a);
     auto granules = [&](int r) {
-        const int n = a.context_lens[r];
+        const int n = __ldcg(a.context_lens + r);
         return tile_span<Sh::kTok, kMode>(a, n < 0 ? 0 : n > cap ? cap : n).granules;
     };
     // The split of the first kernel, from its inputs (which were complete before

@@ -150,6 +150,8 @@ struct Call {
         const at::Tensor& t = tensor(o, "workspace");
         if (!t.is_cuda() || t.get_device() != device)
             value_error("workspace must be on the query's device");
+        if (!t.is_contiguous())
+            value_error("workspace must be contiguous");
         return t;
     }
 };

@@ -33,11 +33,11 @@ __global__ void __launch_bounds__(kThreads) accumulate_weights_kernel(const Weig
     __shared__ float2 state[kThreads];               // (max, 1 / sum) of up to kThreads rows
     grid_launch_dependents();
     // Lengths, tables and weights are inputs of the whole call: complete before
-    // the decode pass began, and read before this kernel waits for it.
+    // the decode pass began, and read (from L2) before this kernel waits for it.
     const int64_t bh = blockIdx.x / a.chunks;
     const int chunk = int(blockIdx.x - bh * a.chunks);
     const int b = int(bh / a.H_kv), h = int(bh - int64_t(b) * a.H_kv);
-    int n = a.context_lens[b];
+    int n = __ldcg(a.context_lens + b);
     const int cap = min(a.max_pages << a.ps_shift, a.score_cap);
     n = n < 0 ? 0 : n > cap ? cap : n;               // recorded by the decode pass
     if (chunk * kSpan >= n) {
@@ -52,12 +52,12 @@ __global__ void __launch_bounds__(kThreads) accumulate_weights_kernel(const Weig
     if constexpr (kVector) {
         to[0] = nullptr;
         if (pos < n) {
-            const int phys = bt[pos >> a.ps_shift];
+            const int phys = __ldcg(bt + (pos >> a.ps_shift));
             if (unsigned(phys) < unsigned(a.num_pages)) {    // otherwise recorded by the decode pass
                 to[0] = a.weight_pages + ((int64_t(phys) * a.H_kv + h) << a.ps_shift) +
                         (pos & ((1 << a.ps_shift) - 1));
                 if (pos < fresh) {
-                    const float4 v = *reinterpret_cast<const float4*>(to[0]);
+                    const float4 v = __ldcg(reinterpret_cast<const float4*>(to[0]));
                     old[0] = v.x;
                     old[1] = v.y;
                     old[2] = v.z;
@@ -70,12 +70,12 @@ __global__ void __launch_bounds__(kThreads) accumulate_weights_kernel(const Weig
         for (int u = 0; u < kEach; ++u) {
             to[u] = nullptr;
             if (pos + u < n) {
-                const int phys = bt[(pos + u) >> a.ps_shift];
+                const int phys = __ldcg(bt + ((pos + u) >> a.ps_shift));
                 if (unsigned(phys) < unsigned(a.num_pages)) {
                     to[u] = a.weight_pages + ((int64_t(phys) * a.H_kv + h) << a.ps_shift) +
                             ((pos + u) & ((1 << a.ps_shift) - 1));
                     if (pos + u < fresh)
-                        old[u] = *to[u];
+                        old[u] = __ldcg(to[u]);
                 }
             }
         }

@@ -37,7 +37,7 @@ SHAPE = dict(batch=2, num_q_heads=4, num_kv_heads=2, head_dim=128, q_len=1, num_
     (dict(sinks=33), 1), (dict(recent=37), 1), (dict(sinks=2**31 - 1, recent=2**31 - 1), 1),
     (dict(dmp=2), 1), (dict(dmp=0), 1), (dict(ps=24), 2), (dict(ps=512), 2),
     (dict(nl=0x50000), 1), (dict(nl=0x40000), 1), (dict(kept=0x50000 - 300), 1),
-    (dict(kept=0x60008), 1),
+    (dict(kept=0x60008), 1), (dict(kept=0x80000 - 4), 1),
     (dict(shape=dict(batch=0)), 1), (dict(shape=dict(num_kv_heads=0)), 1),
     (dict(shape=dict(max_pages=0)), 1), (dict(shape=dict(head_dim=96)), 2),
     (dict(shape=dict(num_pages=1 << 30)), 2),

@@ -123,6 +123,8 @@ def test_refusals():
                     (dict(query=c["query"].cpu()), ValueError),
                     (dict(out=c["query"][:1]), ValueError),
                     (dict(block_table=c["block_table"].cpu()), ValueError),
+                    (dict(workspace=torch.empty(1, dtype=torch.uint8, device="cuda").expand(1 << 24)), ValueError),
+                    (dict(workspace=torch.empty(16, dtype=torch.uint8)), ValueError),
                     (dict(workspace=torch.empty(16, dtype=torch.uint8, device="cuda")), pa.PagedAttentionError)):
         with pytest.raises(err):
             pa.pa_decode_window(**{**dict(c, window=8), **kw})
