@@ -56,10 +56,10 @@ constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr float kMoveLog2 = 8.f;      // scores may exceed the maximum in use by this much
 constexpr int kPieceUnits = 1;        // a piece's cost beyond its granules
-// Two blocks of two tiles a warp: with three the second kernel's blocks and the
-// next call's find no room until the last block of this one ends (64 e4m3
-// requests, window 2048: 62 us against 49; 8 bf16 requests of 16k-32k: 160
-// against 142), with four tiles a warp likewise (75 and 189 us).
+// Two blocks of two tiles a warp. 64 e4m3 requests, window 2048: 49 us, with three
+// blocks 62, with four tiles a warp 75; 8 bf16 requests of 16k-32k: 142, 160 and
+// 189. (Presumably the second kernel's blocks and the next call's then find no
+// room until the last block of this one ends.)
 constexpr int kBlocksPerSM = 2;
 
 // kTok keys per step and warp: 16 rows of 256 bytes or 32 of 128.

@@ -367,6 +367,10 @@ __device__ __forceinline__ void piece_arrive_receiver(const uint4* state, const 
 // that no row sees. The two runs are laid end to end and cut into tiles of 128
 // places, so the sinks rarely cost a tile of their own: key j is place j before
 // sink_keys and place j + shift from there on.
+// Bound by the tiles (18 of them an item at a window of 2048, of which a row sees
+// 16) and about 4 us an item beyond them. Measured (one call of a replayed graph,
+// 32 heads on 8): 8191 rows, window 2048, 197 us (1223 TFLOP/s); 4 x 512 rows,
+// window 1024, 36 us.
 struct WindowSpan {
     int sink_keys, start, shift;
     int first_seen;      // place of the first key that a row sees through the window

@@ -13,7 +13,9 @@
 // weights. A thread holds four neighbouring positions: 16 bytes of each score
 // row, and of the page row where pages hold at least four slots and the pool
 // is aligned to 16 bytes (otherwise four single slots). The page id and the old
-// weights are requested before the scores.
+// weights are requested before the scores. 8 requests of 16k-32k tokens, 32 heads on
+// 8: 12 us by itself; in a call whose scores are small it is latency, of which the
+// early requests hide a part (32 requests up to 4096 tokens: 24.4 -> 22.9 us a call).
 #include <math.h>
 #include <stdint.h>
 
