@@ -446,8 +446,8 @@ pa_status pa_attention(const void *query, const void *key_pages,
  * workspace: pa_decode_window_workspace_bytes(shape) bytes (0: invalid shape),
  * 16-byte aligned, any contents; calls that share one must not overlap on the
  * GPU. Other arguments and the errors as for pa_decode / pa_decode_fp8.
- * Up to 16 rows per request and KV head (G * L) take a kernel of their own,
- * in one launch; more take pa_decode's.
+ * Up to 16 rows per request and KV head (G * L) take kernels of their own; more
+ * take pa_decode's. Two kernels on `stream`.
  */
 size_t pa_decode_window_workspace_bytes(pa_shape shape);
 pa_status pa_decode_window(const void *query, const void *key_pages, const void *value_pages,

@@ -2,9 +2,9 @@
 // the evicted cache (pa_qk_norm_rope_append, the window and weight calls,
 // pa_kv_evict): argument checks, the tensors that a call makes where none are
 // given (outputs, a workspace of this call alone, both made on the device of the
-// call and kept for its stream), and the call of the C ABI on that device and
-// stream. A call of one token takes about 2 us on the GPU; the same checks written
-// in Python took 8.
+// call and for its stream), and the call of the C ABI on that device and stream. An
+// append of one token takes 2.1 us on the GPU; a call of it 3.4 us, 10.7 with these
+// checks written in Python.
 //
 // Module _pagedattn_calls; binding.py declares the signatures and documents them.
 #include <Python.h>
@@ -15,7 +15,6 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <ATen/ops/empty.h>
-#include <ATen/ops/empty_like.h>
 
 #include <cmath>
 #include <limits>
@@ -66,6 +65,14 @@ int32_t integer(PyObject* o, const char* name)
     if (v < std::numeric_limits<int32_t>::min() || v > std::numeric_limits<int32_t>::max())
         value_error(std::string(name) + " does not fit 32 bits");
     return int32_t(v);
+}
+
+// A size of a tensor as the C ABI takes it.
+int32_t size32(int64_t n, const char* what)
+{
+    if (n > std::numeric_limits<int32_t>::max())
+        value_error(std::string(what) + " does not fit 32 bits");
+    return int32_t(n);
 }
 
 double number(PyObject* o)
@@ -130,16 +137,17 @@ struct Call {
         return o == Py_None ? nullptr : check(tensor(o, name), type, name);
     }
 
-    // Memory made on the current stream for a call on another one.
-    const at::Tensor& kept(const at::Tensor& t) const
-    {
-        if (other_stream)
-            t.record_stream(c10::cuda::getStreamFromExternal(stream, device).unwrap());
-        return t;
-    }
+    // Memory for the call, of its stream's own: what was freed on the current one
+    // may still be in use there. The caller reads it on the current stream.
     at::Tensor make(at::IntArrayRef sizes, at::ScalarType type) const
     {
-        return kept(at::empty(sizes, at::TensorOptions().dtype(type).device(c10::Device(c10::kCUDA, device))));
+        const auto options = at::TensorOptions().dtype(type).device(c10::Device(c10::kCUDA, device));
+        if (!other_stream)
+            return at::empty(sizes, options);
+        const c10::cuda::CUDAStreamGuard on(c10::cuda::getStreamFromExternal(stream, device));
+        const at::Tensor t = at::empty(sizes, options);
+        t.record_stream(current.unwrap());
+        return t;
     }
     // The caller's workspace, or one of this call: the allocator orders its reuse
     // (a capture's lives in the graph's pool).
@@ -215,7 +223,7 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n)
             if (cs.dim() != 2 || cs.size(0) > std::numeric_limits<int32_t>::max())
                 value_error("cos_sin must be [table_len, rotary_dim]");
             table = cs.size(0);
-            R = cs.size(1);
+            R = size32(cs.size(1), "rotary_dim");
         }
         at::Tensor query;
         if (a[13] == Py_None) {
@@ -236,7 +244,8 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n)
         if (B > 0 && L > 0) {
             // the strides of an axis of one element say nothing
             const int64_t bs = B > 1 ? qkv.stride(0) : L * width, ts = L > 1 ? qkv.stride(1) : width;
-            const pa_shape shape{int32_t(B), int32_t(H_q), int32_t(H_kv), int32_t(D), int32_t(L), int32_t(P), 0};
+            const pa_shape shape{size32(B, "B"), size32(H_q, "H_q"), size32(H_kv, "H_kv"), size32(D, "D"),
+                                 size32(L, "L"), size32(P, "the number of pages"), 0};
             const float eps = float(number(a[11]));
             const int inter = truth(a[12]);
             const pa_status st =
@@ -289,15 +298,16 @@ struct Paged {
         cl = call.check(lens, at::kInt, "context_lens");
         scale = scale_arg == Py_None ? float(1.0 / std::sqrt(double(query.size(3)))) : float(number(scale_arg));
         if (out_arg == Py_None) {
-            out = call.kept(at::empty_like(query));
+            out = call.make(query.sizes(), at::kBFloat16);
         } else {
             out = tensor(out_arg, "out");
             if (out.sizes() != query.sizes())
                 value_error("out must have the query's shape");
             call.check(out, at::kBFloat16, "out");
         }
-        shape = pa_shape{int32_t(query.size(0)), int32_t(query.size(1)), int32_t(kp.size(1)), int32_t(query.size(3)),
-                         int32_t(query.size(2)), int32_t(kp.size(0)), int32_t(table.size(1))};
+        shape = pa_shape{size32(query.size(0), "B"), size32(query.size(1), "H_q"), size32(kp.size(1), "H_kv"),
+                         size32(query.size(3), "D"), size32(query.size(2), "L"),
+                         size32(kp.size(0), "the number of pages"), size32(table.size(1), "max_pages")};
     }
     const int32_t* table() const { return static_cast<const int32_t*>(bt); }
     const int32_t* lens() const { return static_cast<const int32_t*>(cl); }
@@ -424,10 +434,11 @@ PyObject* evict(PyObject*, PyObject* const* a, Py_ssize_t n)
         int32_t* kept_ptr = static_cast<int32_t*>(call.check(kept, at::kInt, "kept"));
         int32_t* fresh_ptr = static_cast<int32_t*>(call.check(fresh, at::kInt, "new_lens"));
         if (B > 0) {
-            const pa_shape shape{int32_t(B), int32_t(H), int32_t(H), int32_t(kp.size(3)), 1, int32_t(kp.size(0)),
-                                 int32_t(table.size(1))};
+            const int32_t heads = size32(H, "H_kv");
+            const pa_shape shape{size32(B, "B"), heads, heads, size32(kp.size(3), "D"), 1,
+                                 size32(kp.size(0), "the number of pages"), size32(table.size(1), "max_pages")};
             const pa_status st = (fp8 ? pa_kv_evict_fp8 : pa_kv_evict)(k, v, w, bt, cl, ps, keep, sinks, recent, dt,
-                                                                       int32_t(dst.size(1)), kept_ptr, fresh_ptr, shape,
+                                                                       size32(dst.size(1), "dst_max_pages"), kept_ptr, fresh_ptr, shape,
                                                                        call.stream);
             if (raised(st, what))
                 return nullptr;

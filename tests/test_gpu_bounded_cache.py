@@ -212,3 +212,48 @@ def test_a_step_captured_and_replayed():
         check_no_device_error()
         for x, y in zip(got, want):
             assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("call", ["append", "window", "workspace", "evict"])
+def test_memory_made_for_another_stream_is_not_in_use_on_this_one(call):
+    """A tensor freed on the current stream while a copy of it is still to run
+    there: the memory that a call on another stream makes is not that one."""
+    pa = _pa()
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    n, L = 64, 64 if call == "append" else 1
+    kp, vp = (torch.randn((8, H_KV, PS, D), generator=gen, device="cuda").to(torch.bfloat16) for _ in range(2))
+    wp = torch.rand((8, H_KV, PS), generator=gen, device="cuda")
+    ids = torch.arange(8, dtype=torch.int32, device="cuda")[None]
+    lens = torch.tensor([n], dtype=torch.int32, device="cuda")
+    q = torch.randn((1, H_Q, L, D), generator=gen, device="cuda").to(torch.bfloat16)
+    qkv = torch.randn((1, L, (H_Q + 2 * H_KV) * D), generator=gen, device="cuda").to(torch.bfloat16)
+    slots = torch.arange(L, dtype=torch.int32, device="cuda")[None]
+    side = torch.cuda.Stream()
+    ws = torch.empty(1 << 24, dtype=torch.uint8, device="cuda")
+    out = torch.empty_like(q)
+    raw = side.cuda_stream
+    if call == "append":
+        run = lambda: pa.pa_qk_norm_rope_append(qkv, None, None, None, None, kp, vp, slots, PS, stream=raw)
+        size = q.nbytes
+    elif call == "window":
+        run = lambda: pa.pa_decode_window(q, kp, vp, ids, lens, PS, 32, 2, max_context_len=n, workspace=ws,
+                                          stream=raw)
+        size = q.nbytes
+    elif call == "workspace":
+        run = lambda: pa.pa_decode_weights(q, kp, vp, wp, ids, lens, PS, n, decay=0.0, out=out, stream=raw)
+        shape = pa.make_shape(q.shape, kp.shape, ids.shape[1])
+        size = pa.pa_decode_weights_workspace_bytes(shape, n)
+    else:
+        run = lambda: pa.pa_kv_evict(kp, vp, wp, ids, lens, PS, 32, 2, 8, stream=raw)
+        size = H_KV * 32 * 4
+    run()                                            # loads the kernels
+    torch.cuda.synchronize()
+    held = torch.full((size,), 7, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    torch.cuda._sleep(200_000_000)                   # about 0.1 s
+    copy = held.clone()
+    del held
+    run()
+    torch.cuda.synchronize()
+    check_no_device_error()
+    assert torch.all(copy == 7)
