@@ -45,7 +45,8 @@
 // item started in an earlier block, per head O as [32 column quads][128
 // rows][4 floats] (a warp's stores and loads contiguous) and (m, l) per row;
 // and per head and softmax warp one 64-bit flag that holds the launch's stamp
-// once that warp's rows are written (so the workspace needs no clearing).
+// once that warp's rows are written (so the workspace needs no clearing) and
+// that its reader sets to 0.
 // The wait for a flag is bounded; the launch is cooperative, so every block
 // is resident and the wait normally ends at once.
 #include <cuda.h>
@@ -903,6 +904,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     }
                     ready = __all_sync(0xffffffffu, got);
+                    // Each flag has this one reader, which clears it: a replayed
+                    // graph launches with the same stamp and has to find it unset.
+                    if (ready && lane == 0)
+                        *const_cast<volatile unsigned long long*>(f) = 0ull;
                 }
                 if (!ready) {
                     if (lane == 0 && !misc[0]) {

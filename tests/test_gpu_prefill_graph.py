@@ -1,6 +1,7 @@
-"""pa_attention's prefill with tail pieces, captured and replayed on other
-inputs: the launch's stamp is the same in every replay, so the states that the
-replay before left must not be taken for this one's."""
+"""The prefills that hand states from block to block (pa_attention's tail pieces,
+pa_prefill_split), captured and replayed on other inputs: the launch's stamp is
+the same in every replay, so the states that the replay before left must not be
+taken for this one's."""
 import pytest
 import torch
 
@@ -38,3 +39,30 @@ def test_tail_pieces_in_a_replayed_graph_see_new_inputs(setting):
             assert torch.equal(out, want)
     finally:
         pa.pa_debug_prefill_variant(0)
+
+
+@pytest.mark.parametrize("lens, L", [([3000], 129), ([2600, 900], 200), ([9000], 64), ([700, 300, 2900], 130)])
+def test_split_prefill_in_a_replayed_graph_sees_new_inputs(lens, L):
+    import paged_kv_attention_06_gb300 as pa
+    c = make(lens, 4, 2, L, 128, 16, 62, poison=False)
+    fresh = make(lens, 4, 2, L, 128, 16, 63, poison=False)
+    out = torch.empty_like(c["query"])
+    ws, _ = pa.prefill_workspace(pa.make_shape(c["query"].shape, c["key_pages"].shape, c["block_table"].shape[1]), 16,
+                                 c["query"].device)
+
+    def call(c, out, ws):
+        return pa.pa_prefill_split(**c, out=out, workspace=ws)
+
+    call(c, out, ws)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call(c, out, ws)
+    graph.replay()
+    want = call(fresh, torch.empty_like(out), torch.zeros_like(ws))
+    for k in ("query", "key_pages", "value_pages", "block_table"):
+        c[k].copy_(fresh[k])
+    for _ in range(3):
+        out.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
