@@ -477,9 +477,13 @@ pa_status pa_prefill_window(const void *query, const void *key_pages, const void
 /*
  * The dispatch of the two: pa_decode_window or pa_prefill_window, by
  * pa_attention_route's rule on the keys a row can reach (the smaller of
- * max_context_len, where known, and sinks + window + L). The workspace is
- * needed on the decode route only: pa_attention_window_workspace_bytes bytes (0
- * also for invalid sizes), 16-byte aligned, any contents.
+ * max_context_len, where known, and sinks + window + L). workspace:
+ * pa_attention_window_workspace_bytes bytes (0: none needed, or invalid sizes), any
+ * contents; calls that share one must not overlap on the GPU. The decode route
+ * needs it, 16-byte aligned. On the prefill route it is for head_dim 128, pages of
+ * at least 8 tokens and groups of at least 2 where whole query tiles would leave
+ * SMs idle for long: with it (256-byte aligned) the tiles of keys are spread
+ * evenly, as pa_prefill_split does; without it the call is pa_prefill_window.
  */
 size_t pa_attention_window_workspace_bytes(pa_shape shape, int32_t page_size,
                                            int32_t max_context_len, int32_t window, int32_t sinks);

@@ -50,7 +50,10 @@ void pa_debug_arm_wait_timeout(void);
  *   5  as 4, with the receiving blocks running the piece after their own
  *      item, so that the donors usually finish first and the receiving
  *      blocks write the merged rows (the path taken when a receiving block
- *      starts late).
+ *      starts late);
+ *   6  as 2; pa_attention_window and its e4m3 form take the split kernel
+ *      wherever it can run and the workspace has room, in pieces of about two
+ *      tiles (the workspace function follows the setting).
  * Settings 1 and 2 also hold for pa_prefill_split and for pa_attention given
  * a prefill workspace (the workspace is then not used). Any other value is
  * taken as 0. Returns the previous setting. Results agree

@@ -264,6 +264,46 @@ size_t split_prefill_need(const pa_shape& s, int32_t page_size, const DeviceInfo
     return split > pieces ? split : pieces;
 }
 
+// The split kernel. cudaErrorNotSupported: its register split is not available, or
+// not every block could be resident (another client holds SMs); the other
+// kernels take the call then.
+cudaError_t run_split(const CUtensorMap& qmap, const CUtensorMap& kmap, const CUtensorMap& vmap,
+                      const PrefillArgs& a, const DeviceInfo* dev, int grid, void* workspace,
+                      cudaStream_t stream)
+{
+    SplitPrefillArgs sa;
+    memset(&sa, 0, sizeof sa);
+    sa.out = a.out;
+    sa.block_table = a.block_table;
+    sa.context_lens = a.context_lens;
+    sa.err = a.err;
+    sa.B = a.B;
+    sa.H_q = a.H_q;
+    sa.H_kv = a.H_kv;
+    sa.L = a.L;
+    sa.ps = a.ps;
+    sa.max_pages = a.max_pages;
+    sa.num_pages = a.num_pages;
+    sa.G = a.G;
+    sa.n_qtiles = a.n_qtiles;
+    sa.box_rows = a.box_rows;
+    sa.scale_log2 = a.scale_log2;
+    sa.causal = a.causal;
+    sa.out_scale = a.out_scale;
+    sa.window = a.window;
+    sa.sinks = a.sinks;
+    // An error the caller left pending is not ours to clear: note it, so
+    // that only a refused cooperative launch of this call is cleared.
+    const bool pending = cudaPeekAtLastError() != cudaSuccess;
+    const cudaError_t e = launch_prefill_split(qmap, kmap, vmap, sa, grid, workspace,
+                                               dev->id, stream);
+    if (e != cudaErrorCooperativeLaunchTooLarge)
+        return e;
+    if (!pending)
+        (void)cudaGetLastError();
+    return cudaErrorNotSupported;
+}
+
 // Prefill on tcgen05 (D = 128 or 64; pages of fewer than 8 tokens on the
 // pairs kernel, whose loaders then copy K/V row by row). With a workspace of at least split_prefill_need
 // bytes: the split kernel (K/V tiles spread evenly over one block per SM);
@@ -346,38 +386,9 @@ pa_status run_prefill_tc(const void* query, const void* key_pages, const void* v
     a.value_pages = static_cast<const uint16_t*>(value_pages);
     a.piece_last = t_prefill_variant == 5 ? 1 : 0;
     if (split) {
-        SplitPrefillArgs sa;
-        memset(&sa, 0, sizeof sa);
-        sa.out = a.out;
-        sa.block_table = a.block_table;
-        sa.context_lens = a.context_lens;
-        sa.err = a.err;
-        sa.B = a.B;
-        sa.H_q = a.H_q;
-        sa.H_kv = a.H_kv;
-        sa.L = a.L;
-        sa.ps = a.ps;
-        sa.max_pages = a.max_pages;
-        sa.num_pages = a.num_pages;
-        sa.G = a.G;
-        sa.n_qtiles = a.n_qtiles;
-        sa.box_rows = a.box_rows;
-        sa.scale_log2 = a.scale_log2;
-        sa.causal = a.causal;
-        sa.out_scale = a.out_scale;
-        // An error the caller left pending is not ours to clear: note it, so
-        // that only a refused cooperative launch of this call is cleared.
-        const bool pending = cudaPeekAtLastError() != cudaSuccess;
-        cudaError_t e = launch_prefill_split(qmap, kmap, vmap, sa, dev->sm_count, workspace,
-                                             dev->id, stream);
-        if (e == cudaSuccess)
-            return PA_OK;
-        if (e != cudaErrorNotSupported && e != cudaErrorCooperativeLaunchTooLarge)
-            return PA_ERR_CUDA;
-        // The register split is not available, or not every block could be
-        // resident (another client holds SMs): the kernels below.
-        if (e == cudaErrorCooperativeLaunchTooLarge && !pending)
-            (void)cudaGetLastError();
+        const cudaError_t e = run_split(qmap, kmap, vmap, a, dev, dev->sm_count, workspace, stream);
+        if (e != cudaErrorNotSupported)
+            return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
     }
     // The pairs kernel's tail pieces use the caller's workspace (pa_attention's).
     // Test setting 4: a grid of two thirds of the items, so that small shapes
@@ -396,13 +407,47 @@ pa_status run_prefill_tc(const void* query, const void* key_pages, const void* v
     return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
-// Prefill with a sliding window on the pairs kernel (every head_dim, page size
-// and group size; whole items). PA_ERR_UNSUPPORTED where its register split is
-// not available.
+// Blocks of the split kernel for a windowed prefill, or 0: the pairs kernel. With t
+// tiles an item, whole items take the time of R t tiles, R = ceil(items / SMs); the
+// split kernel that of a block's share of all tiles (two more an item) and about
+// ten for what it adds (a launch that overlaps no other, the merges). Measured, 32
+// heads on 8, one request, pairs and split in us: 64 items, window 2048 37 and 35,
+// 4096 63 and 47, 16384 216 and 122; 96 items, 4096 63 and 60; 128 items, 4096 64
+// and 72, 16384 218 and 222; 160 items, 1024 40 and 36, 2048 66 and 50, 4096 117
+// and 80; 1024 items, 4096 306 and 358. Blocks of fewer than 8 tiles merge too many
+// states (16 items, window 4096: 45 against 40). max_context_len 0: unknown.
+int window_split_grid(const pa_shape& s, int32_t page_size, int32_t max_context_len, int32_t window,
+                      int32_t sinks, const DeviceInfo* dev)
+{
+    if (split_prefill_need(s, page_size, dev) == 0)
+        return 0;
+    const int64_t context = max_context_len > 0 ? max_context_len : int64_t(s.max_pages) * page_size;
+    const int64_t keys = std::min(context, int64_t(window) + sinks + 127);
+    const int64_t t = (keys + 127) / 128, items = prefill_pair_items(s), sms = dev->sm_count;
+    const int64_t tiles = items * (t + 2);
+    if (t_prefill_variant == 6)            // test setting: always, in small pieces
+        return int(std::max<int64_t>(1, std::min(sms, tiles / 2)));
+    const int64_t grid = std::max<int64_t>(1, std::min(sms, tiles / 8));
+    const int64_t whole = (items + sms - 1) / sms * t, share = (tiles + grid - 1) / grid;
+    return 10 * whole > 11 * (share + 10) ? int(grid) : 0;
+}
+size_t window_split_need(const pa_shape& s, int32_t page_size, int32_t max_context_len,
+                         int32_t window, int32_t sinks, const DeviceInfo* dev)
+{
+    const int grid = window_split_grid(s, page_size, max_context_len, window, sinks, dev);
+    return grid > 0 ? prefill_split_workspace_bytes(grid) : 0;
+}
+
+// Prefill with a sliding window: the split kernel where window_split_grid says so
+// and the workspace is large enough, otherwise the pairs kernel (every head_dim, page size
+// and group size; whole items). PA_ERR_UNSUPPORTED where the register split is not
+// available.
 pa_status run_prefill_window(const void* query, const void* key_pages, const void* value_pages,
                              const int32_t* block_table, const int32_t* context_lens,
                              int32_t page_size, float scale, int32_t window, int32_t sinks,
-                             float out_scale, void* out, const pa_shape& s, cudaStream_t stream)
+                             float out_scale, void* out, const pa_shape& s,
+                             int32_t max_context_len, void* workspace, size_t workspace_bytes,
+                             cudaStream_t stream)
 {
     DeviceInfo* dev;
     pa_status st = device_info(&dev);
@@ -449,6 +494,13 @@ pa_status run_prefill_window(const void* query, const void* key_pages, const voi
     a.value_pages = static_cast<const uint16_t*>(value_pages);
     a.window = window;
     a.sinks = sinks;
+    const int grid = workspace ? window_split_grid(s, page_size, max_context_len, window, sinks, dev) : 0;
+    if (grid > 0 && workspace_bytes >= prefill_split_workspace_bytes(grid) &&
+        (reinterpret_cast<uintptr_t>(workspace) & 255u) == 0) {
+        const cudaError_t e = run_split(qmap, kmap, vmap, a, dev, grid, workspace, stream);
+        if (e != cudaErrorNotSupported)
+            return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+    }
     const cudaError_t e = launch_prefill_pairs(qmap, kmap, vmap, omap, a, dev->id, dev->sm_count,
                                                nullptr, 0, stream);
     return e == cudaSuccess ? PA_OK : e == cudaErrorNotSupported ? PA_ERR_UNSUPPORTED : PA_ERR_CUDA;
@@ -1194,7 +1246,7 @@ pa_status run_decode_window(const void* query, const void* key_pages, const void
 struct WindowCopyPlan {
     int64_t P1 = 0, P2 = 0;
     pa_shape copy{};
-    size_t kv_bytes = 0, table_off = 0, total = 0;
+    size_t kv_bytes = 0, table_off = 0, split_off = 0, split_bytes = 0, total = 0;
 };
 
 pa_status plan_window_copy(const pa_shape& s, int32_t max_context_len, int32_t window,
@@ -1214,7 +1266,13 @@ pa_status plan_window_copy(const pa_shape& s, int32_t max_context_len, int32_t w
     p->copy.max_pages = int32_t(p->P2);
     p->kv_bytes = size_t(pages) * s.num_kv_heads * 128 * 128 * 2;
     p->table_off = 2 * p->kv_bytes;
-    p->total = p->table_off + size_t(s.batch) * size_t(p->P2) * 4;
+    p->split_off = (p->table_off + size_t(s.batch) * size_t(p->P2) * 4 + 255) & ~size_t(255);
+    DeviceInfo* dev;
+    const pa_status st = device_info(&dev);
+    if (st != PA_OK)
+        return st;
+    p->split_bytes = window_split_need(s, 128, max_context_len, window, sinks, dev);
+    p->total = p->split_off + p->split_bytes;
     return PA_OK;
 }
 
@@ -1348,10 +1406,13 @@ pa_status pa_decode_window_fp8(const void* query, const void* key_pages, const v
                              max_context_len, workspace, workspace_bytes, stream);
 }
 
-pa_status pa_prefill_window(const void* query, const void* key_pages, const void* value_pages,
-                            const int32_t* block_table, const int32_t* context_lens,
-                            int32_t page_size, float scale, int32_t window, int32_t sinks,
-                            void* out, pa_shape shape, void* stream)
+namespace {
+
+pa_status run_window_prefill(const void* query, const void* key_pages, const void* value_pages,
+                             const int32_t* block_table, const int32_t* context_lens,
+                             int32_t page_size, float scale, int32_t window, int32_t sinks,
+                             void* out, const pa_shape& shape, int32_t max_context_len,
+                             void* workspace, size_t workspace_bytes, void* stream)
 {
     pa_status st = check_attention(query, key_pages, value_pages, block_table, context_lens,
                                    page_size, scale, out, shape);
@@ -1363,8 +1424,8 @@ pa_status pa_prefill_window(const void* query, const void* key_pages, const void
         return st;
     extra.sinks = std::min(sinks, 1 << 30);
     st = run_prefill_window(query, key_pages, value_pages, block_table, context_lens, page_size,
-                            scale, extra.window, extra.sinks, 1.f, out, shape,
-                            static_cast<cudaStream_t>(stream));
+                            scale, extra.window, extra.sinks, 1.f, out, shape, max_context_len,
+                            workspace, workspace_bytes, static_cast<cudaStream_t>(stream));
     if (st != PA_ERR_UNSUPPORTED)
         return st;
     // Without the pairs kernel's register split: the split-KV kernel with
@@ -1374,13 +1435,30 @@ pa_status pa_prefill_window(const void* query, const void* key_pages, const void
                         1.f, 1.f, extra);
 }
 
+}  // namespace
+
+pa_status pa_prefill_window(const void* query, const void* key_pages, const void* value_pages,
+                            const int32_t* block_table, const int32_t* context_lens,
+                            int32_t page_size, float scale, int32_t window, int32_t sinks,
+                            void* out, pa_shape shape, void* stream)
+{
+    return run_window_prefill(query, key_pages, value_pages, block_table, context_lens, page_size,
+                              scale, window, sinks, out, shape, 0, nullptr, 0, stream);
+}
+
 size_t pa_attention_window_workspace_bytes(pa_shape shape, int32_t page_size,
                                            int32_t max_context_len, int32_t window, int32_t sinks)
 {
     if (!pow2_in(page_size, 1, 256) || window <= 0 || sinks < 0 || max_context_len < 0)
         return 0;
-    return pa_attention_route(shape, window_reach(shape, max_context_len, window, sinks)) == 0
-               ? pa_decode_window_workspace_bytes(shape)
+    const int32_t route =
+        pa_attention_route(shape, window_reach(shape, max_context_len, window, sinks));
+    if (route == 0)
+        return pa_decode_window_workspace_bytes(shape);
+    DeviceInfo* dev;
+    return route > 0 && device_info(&dev) == PA_OK
+               ? window_split_need(shape, page_size, max_context_len, std::min(window, 1 << 30),
+                                   std::min(sinks, 1 << 30), dev)
                : 0;
 }
 
@@ -1400,8 +1478,9 @@ pa_status pa_attention_window(const void* query, const void* key_pages, const vo
         return pa_decode_window(query, key_pages, value_pages, block_table, context_lens,
                                 page_size, scale, window, sinks, out, shape, max_context_len,
                                 workspace, workspace_bytes, stream);
-    return pa_prefill_window(query, key_pages, value_pages, block_table, context_lens, page_size,
-                             scale, window, sinks, out, shape, stream);
+    return run_window_prefill(query, key_pages, value_pages, block_table, context_lens, page_size,
+                              scale, window, sinks, out, shape, max_context_len, workspace,
+                              workspace_bytes, stream);
 }
 
 size_t pa_attention_window_fp8_workspace_bytes(pa_shape shape, int32_t page_size,
@@ -1479,7 +1558,8 @@ pa_status pa_attention_window_fp8(const void* query, const void* key_pages,
     if (launch_fp8_pages_to_bf16(c, s) != cudaSuccess)
         return PA_ERR_CUDA;
     return run_prefill_window(query, c.key_out, c.value_out, c.table_out, context_lens, 128,
-                              scale * k_scale, cut, first, v_scale, out, p.copy, s);
+                              scale * k_scale, cut, first, v_scale, out, p.copy, max_context_len,
+                              w + p.split_off, p.split_bytes, s);
 }
 
 size_t pa_decode_weights_workspace_bytes(pa_shape shape, int32_t max_context_len)
@@ -1751,7 +1831,10 @@ void pa_debug_arm_wait_timeout(void) { t_arm_unset_wait = true; }
 int pa_debug_prefill_variant(int variant)
 {
     const int prev = t_prefill_variant;
-    t_prefill_variant = (variant == 1 || variant == 2 || variant == 4 || variant == 5) ? variant : 0;
+    t_prefill_variant = (variant == 1 || variant == 2 || variant == 4 || variant == 5 ||
+                         variant == 6)
+                            ? variant
+                            : 0;
     return prev;
 }
 

@@ -293,6 +293,7 @@ struct SplitPrefillArgs {
     float scale_log2;
     int32_t causal;
     float out_scale;    // the output is out_scale * softmax . V (e4m3 copies: v_scale)
+    int32_t window, sinks;   // window > 0: a sliding window, first keys that stay visible
 };
 
 size_t prefill_split_smem_bytes();

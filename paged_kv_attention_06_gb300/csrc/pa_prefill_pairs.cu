@@ -62,6 +62,7 @@
 #include "pa_device.cuh"
 #include "pa_internal.h"
 #include "pa_tcgen05.cuh"
+#include "pa_window.cuh"
 
 namespace pa {
 namespace {
@@ -120,7 +121,11 @@ static_assert(kMmaDone < Layout<128>::kNumBars, "barrier count");
 // head 0, the first K/V tile run here, the role (below), the tail piece's
 // state slot (its donor block).
 enum { kEB = 0, kET, kEH0, kEH1, kEHK, kEN, kENT, kEDup, kEK0, kERole, kESlot, kEntry = 12 };
-// With a sliding window (kWin) an item visits runs of keys (window_span).
+// With a sliding window (kWin) an item visits runs of keys (window_span). Bound
+// by the tiles (18 of them an item at a window of 2048, of which a row sees 16)
+// and about 4 us an item beyond them. Measured (one call of a replayed graph, 32
+// heads on 8): 8191 rows, window 2048, 197 us (1223 TFLOP/s); 4 x 512 rows, window
+// 1024, 36 us.
 // Item roles: the whole item here; the item's last tiles here, state left
 // for its first block (run first on the receiving block); the item's first
 // tiles here, merged at the end with the state its last tiles left.
@@ -358,34 +363,6 @@ __device__ __forceinline__ void piece_arrive_receiver(const uint4* state, const 
         if (write)
             *reinterpret_cast<uint4*>(out_row + ch * 8) = make_uint4(o[0], o[1], o[2], o[3]);
     }
-}
-
-// The keys of an item with a sliding window: those of [0, sinks), rounded up to
-// whole boxes (`sink_keys`), then those from `start` on, the first key that the
-// item's first row sees through the window rounded down to a box; one run
-// from 0 where the two would meet. Boxes lie within a page and none is touched
-// that no row sees. The two runs are laid end to end and cut into tiles of 128
-// places, so the sinks rarely cost a tile of their own: key j is place j before
-// sink_keys and place j + shift from there on.
-// Bound by the tiles (18 of them an item at a window of 2048, of which a row sees
-// 16) and about 4 us an item beyond them. Measured (one call of a replayed graph,
-// 32 heads on 8): 8191 rows, window 2048, 197 us (1223 TFLOP/s); 4 x 512 rows,
-// window 1024, 36 us.
-struct WindowSpan {
-    int sink_keys, start, shift;
-    int first_seen;      // place of the first key that a row sees through the window
-};
-__device__ __forceinline__ WindowSpan window_span(const PrefillArgs& a, int n, int row0)
-{
-    WindowSpan s;
-    const int first = int(max(int64_t(0), int64_t(n) - a.L + row0 - a.window + 1));
-    const int start = first & ~(a.box_rows - 1);
-    const bool apart = start > a.sinks;
-    s.sink_keys = apart ? (a.sinks + a.box_rows - 1) & ~(a.box_rows - 1) : 0;
-    s.start = apart ? start : 0;
-    s.shift = s.sink_keys - s.start;
-    s.first_seen = first + s.shift;
-    return s;
 }
 
 // kOdd: the group size is odd and the last pair of each group repeats its

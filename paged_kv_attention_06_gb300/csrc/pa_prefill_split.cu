@@ -27,6 +27,10 @@
 // combination of the pages' decode schedule, "Choose a Schedule for Each
 // Query Shape", applied to the long-query tiles), in a fixed order.
 //
+// With a sliding window (kWin) an item's tiles are those of its runs of keys
+// (pa_window.cuh); the rest is the same. One call of a replayed graph, 32 heads on
+// 8, one request of 512 rows: window 4096 47 us (whole items 63), 16384 122 (216).
+//
 // Per block (384 threads, as the pairs kernel):
 //   * warps 0, 2, 3: TMA loads of the K and V tiles of 128 keys page by page
 //     (two K and two V stages, the stream running on across pieces); warps 0
@@ -60,6 +64,7 @@
 #include "pa_device.cuh"
 #include "pa_internal.h"
 #include "pa_tcgen05.cuh"
+#include "pa_window.cuh"
 
 namespace pa {
 namespace {
@@ -124,8 +129,9 @@ __device__ __forceinline__ uint64_t mnmajor_base(uint32_t saddr)
 }
 
 // K/V tiles visited by query tile t of request b (and its clamped context
-// length). Every role of every block evaluates the same function, so all of
+// length); with a sliding window (kWin) those of its runs of keys. Every role of every block evaluates the same function, so all of
 // them see the same item stream.
+template <bool kWin>
 __device__ __forceinline__ int combo_tiles(const SplitPrefillArgs& a, int m, int* n_out)
 {
     const int b = m / a.n_qtiles;
@@ -139,6 +145,8 @@ __device__ __forceinline__ int combo_tiles(const SplitPrefillArgs& a, int m, int
     int nk = a.causal ? min(n, p_last + 1) : n;
     nk = nk < 0 ? 0 : nk;
     *n_out = n;
+    if (kWin && nk > 0)
+        nk += window_span(a, n, row0).shift;
     return (nk + kKeys - 1) / kKeys;
 }
 
@@ -185,13 +193,14 @@ struct Piece {
 struct Cursor {
     int m, hp;
     int64_t us;
+    template <bool kWin>
     __device__ __forceinline__ bool next(const SplitPrefillArgs& a, int pairs, int64_t s, int64_t e,
                                          Piece& p)
     {
         if (us >= e)
             return false;
         int n;
-        const int nt = combo_tiles(a, m, &n);
+        const int nt = combo_tiles<kWin>(a, m, &n);
         p.b = m / a.n_qtiles;
         p.t = m - p.b * a.n_qtiles;
         p.hp = hp;
@@ -228,6 +237,7 @@ struct TileIter {
     Piece p;
     int k;               // next tile of p
     bool have;           // p is loaded
+    template <bool kWin>
     __device__ __forceinline__ TileDesc next(const SplitPrefillArgs& a, int pairs, int64_t s,
                                              int64_t e)
     {
@@ -246,7 +256,7 @@ struct TileIter {
                 ++k;
                 return d;
             }
-            if (!cur.next(a, pairs, s, e, p))
+            if (!cur.next<kWin>(a, pairs, s, e, p))
                 return d;
             have = true;
             k = p.k0;
@@ -265,7 +275,9 @@ __device__ __forceinline__ int block_of_unit(int64_t x, int64_t U, int64_t G)
 // kOdd: the group size is odd; the last head pair of each group holds its
 // last head twice (computed by both softmax warpgroups, written by the
 // first only), a separate instantiation so that even groups keep their code.
-template <bool kOdd>
+// kWin: a sliding window; an item's tiles are those of its runs of keys laid end
+// to end (WindowSpan), and `place` is a key's number among them.
+template <bool kOdd, bool kWin>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_split_kernel(const __grid_constant__ CUtensorMap q_map,
                          const __grid_constant__ CUtensorMap key_map,
@@ -315,7 +327,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     long long mine = 0;
     for (int m = m_lo; m < m_hi; ++m) {
         int n;
-        const int nt = combo_tiles(a, m, &n);
+        const int nt = combo_tiles<kWin>(a, m, &n);
         mine += item_units(nt);
         if (blockIdx.x == 0 && m % a.n_qtiles == 0) {
             const int raw = a.context_lens[m / a.n_qtiles];
@@ -352,7 +364,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         long long pre = excl;
         for (int m = m_lo; m < m_hi; ++m) {
             int n;
-            const int nt = combo_tiles(a, m, &n);
+            const int nt = combo_tiles<kWin>(a, m, &n);
             const int64_t w = item_units(nt);
             if ((pre + w) * pairs > s) {
                 const int64_t hp = (s - pre * pairs) / w;
@@ -427,7 +439,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // waits for an L2 read rather than a DRAM one.
                 Cursor pc = start;
                 Piece pp;
-                while (pc.next(a, pairs, s, e, pp)) {
+                while (pc.next<kWin>(a, pairs, s, e, pp)) {
                     if (pp.k1 > pp.k0) {
                         for (int h = 0; h < 2; ++h) {
                             const int qrow = (pp.b * a.H_q + head_of(pp.hp, h)) * a.L + pp.t * kRows;
@@ -444,9 +456,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             it.have = false;
             it.k = 0;
             int qp = 0;                                  // pieces whose Q this warp loaded
-            auto n_boxes = [&](const TileDesc& d) {
+            auto n_boxes = [&](const TileDesc& d, const WindowSpan& ws) {
                 const int key0 = d.k * kKeys;
-                return (min(d.n, key0 + kKeys) - key0 + box - 1) / box;
+                return (min(d.n + ws.shift, key0 + kKeys) - key0 + box - 1) / box;
             };
             auto load_q = [&](const TileDesc& d, int h) {
                 // Head h's Q tile of a new piece, once head h's last S of the
@@ -467,18 +479,21 @@ __global__ void __launch_bounds__(kThreads, 1)
             // are loaded just before the wait for its K stage, which hides the
             // load (consecutive tiles' entries share cache lines).
             int n_tiles = 0;
-            for (TileDesc d = it.next(a, pairs, s, e); d.valid; d = it.next(a, pairs, s, e)) {
+            for (TileDesc d = it.next<kWin>(a, pairs, s, e); d.valid; d = it.next<kWin>(a, pairs, s, e)) {
                 const int g = n_tiles++;
                 // Head 0's Q is needed with the first K, head 1's only after
                 // both heads' work on the previous tile: loader 1 issues its K/V
                 // boxes before it waits to refill Q_1.
                 if (d.first && li == 0)
                     load_q(d, 0);
-                const int nbox = n_boxes(d);
+                const WindowSpan ws = kWin ? window_span(a, d.n, d.t * kRows) : WindowSpan{0, 0, 0, 0};
+                const int nbox = n_boxes(d, ws);
                 const int mine_boxes = nbox > li ? (nbox - li + 2) / 3 : 0;
                 const bool live = my_box < nbox;
-                int phys = live ? a.block_table[int64_t(d.b) * a.max_pages + (d.k * kKeys + my_box * box) / a.ps]
-                                : 0;
+                // this lane's box: its first key
+                const int place = d.k * kKeys + my_box * box;
+                const int tok = kWin && place >= ws.sink_keys ? place - ws.shift : place;
+                int phys = live ? a.block_table[int64_t(d.b) * a.max_pages + tok / a.ps] : 0;
                 const int st = g & 1;
     #pragma unroll 1
                 for (int is_v = 0; is_v < 2; ++is_v) {
@@ -494,7 +509,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 atomicOr(a.err, PA_DEVERR_PAGE_ID_BIT);
                                 phys = 0;
                             }
-                            const int tok = d.k * kKeys + my_box * box;
                             const int hk = d.hp / per_group;
                             const int row = (phys * a.H_kv + hk) * a.ps + (tok - (tok / a.ps) * a.ps);
                             uint8_t* dst = smem + (is_v ? Layout::kV : Layout::kK) + st * Layout::kMat +
@@ -563,7 +577,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             TileDesc cur, nxt;
     #pragma unroll 1
             for (int u = 0; u < 2; ++u) {
-                const TileDesc d = it.next(a, pairs, s, e);
+                const TileDesc d = it.next<kWin>(a, pairs, s, e);
                 if (u == 0)
                     cur = d;
                 else
@@ -622,7 +636,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     break;
                 if (nxt.first)
                     ++qp;
-                const TileDesc nn = it.next(a, pairs, s, e);   // tile g + 2
+                const TileDesc nn = it.next<kWin>(a, pairs, s, e);   // tile g + 2
                 tc_fence_after();
                 s_mmas(1, g + 1);
                 if (nxt.last)
@@ -693,7 +707,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0) {
                 Cursor cur = warp_cursor[w8];
                 Piece pc;
-                more = cur.next(a, pairs, vr[0], vr[1], pc) ? 1 : 0;
+                more = cur.next<kWin>(a, pairs, vr[0], vr[1], pc) ? 1 : 0;
                 warp_piece[w8] = pc;
                 warp_cursor[w8] = cur;
             }
@@ -704,8 +718,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (vp->k1 <= vp->k0 && !vp->zero)
                 continue;                            // none of this item's tiles is here
             const int i = vp->t * kRows + r;
-            const int n = vp->n;
-            const int lim = a.causal ? min(n - a.L + i, n - 1) : n - 1;
+            // Places: this row's last visible key, the end of the keys; kWin: the
+            // window's first key, behind the sinks, and the first that some row
+            // of the item sees (0: none between it and the sinks).
+            int n = vp->n;
+            int lim = a.causal ? min(n - a.L + i, n - 1) : n - 1;
+            int low = 0, seen = 0;
+            if constexpr (kWin) {
+                const WindowSpan ws = window_span(a, n, vp->t * kRows);
+                low = max(lim - a.window + 1 + ws.shift, ws.sink_keys);
+                seen = a.sinks < ws.first_seen ? ws.first_seen : 0;
+                n += ws.shift;
+                lim += ws.shift;
+            }
             const int k_first = vp->k0, k_end = vp->k1;
             // The first piece of an item cut at this block's end reads the
             // next block's flag now and tests it at the end, so that the
@@ -719,7 +744,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mbar_wait_warp(&bar[kSFull + head], g & 1, misc, a.err);
                 tc_fence_after();
                 const int key0 = k * kKeys;
-                const bool edge = key0 + kKeys - 1 > lim;
+                bool edge = key0 + kKeys - 1 > lim || (kWin && key0 < low);
+                if constexpr (kWin)
+                    edge = __any_sync(0xffffffffu, edge);    // the votes below are the whole warp's
                 // All 128 scores of the row in registers (four loads, one wait).
                 uint32_t sv[128];
                 float* sc = reinterpret_cast<float*>(sv);
@@ -731,7 +758,17 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int w = 0; w < 4; ++w) {
                         const int nv = lim - (key0 + 32 * w) + 1;
-                        const uint32_t vis = nv >= 32 ? 0xffffffffu : nv <= 0 ? 0u : (1u << nv) - 1u;
+                        uint32_t vis = nv >= 32 ? 0xffffffffu : nv <= 0 ? 0u : (1u << nv) - 1u;
+                        if constexpr (kWin) {
+                            // behind the window, unless among the first keys
+                            const int nl = low - (key0 + 32 * w), nf = a.sinks - (key0 + 32 * w);
+                            const uint32_t past = nl >= 32 ? 0xffffffffu : nl <= 0 ? 0u : (1u << nl) - 1u;
+                            const uint32_t sink = nf >= 32 ? 0xffffffffu : nf <= 0 ? 0u : (1u << nf) - 1u;
+                            vis &= ~past | sink;
+                            // a warp's 32 rows share most of a window's edge
+                            if (__all_sync(0xffffffffu, vis == 0xffffffffu))
+                                continue;
+                        }
 #pragma unroll
                         for (int kq = 0; kq < 32; ++kq)
                             sc[32 * w + kq] = (vis >> kq) & 1u ? sc[32 * w + kq] : -INFINITY;
@@ -796,14 +833,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 tmem_wait_st();
                 // V rows past the context hold stale bytes: zero them before
-                // either head's P V.
-                if (head == 0 && n < key0 + kKeys) {
+                // either head's P V; kWin: also those between the sinks and what
+                // the item's rows see (places [z0, z1) and [z2, 128) of the tile).
+                if (head == 0 && (n < key0 + kKeys || (kWin && key0 < seen))) {
                     mbar_wait_bounded(&bar[kVFull + (g & 1)], (g >> 1) & 1, misc, a.err);
-                    const int z0 = max(0, n - key0);
-                    const int nz = (kKeys - z0) * 16;
+                    const int z2 = min(max(n - key0, 0), kKeys);
+                    const int z0 = kWin ? min(max(a.sinks - key0, 0), z2) : z2;
+                    const int z1 = kWin ? min(max(seen - key0, z0), z2) : z2;
+                    const int nz = (z1 - z0 + kKeys - z2) * 16;
                     uint8_t* vb = smem + Layout::kV + (g & 1) * Layout::kMat;
                     for (int idx = r; idx < nz; idx += 128) {
-                        const int zr = z0 + idx / 16, ch = idx % 16;
+                        int zr = z0 + idx / 16;
+                        const int ch = idx % 16;
+                        if (kWin && zr >= z1)
+                            zr += z2 - z1;
                         *reinterpret_cast<uint4*>(vb + (ch >> 3) * Layout::kHalf + zr * 128 +
                                                   (((ch & 7) ^ (zr & 7)) << 4)) = make_uint4(0, 0, 0, 0);
                     }
@@ -1041,14 +1084,18 @@ cudaError_t launch_prefill_split(const CUtensorMap& q_map, const CUtensorMap& ke
                                  void* workspace, int device, cudaStream_t stream)
 {
     constexpr int kMaxDev = 64;
-    static std::atomic<int> smem_set[kMaxDev][2];
-    static std::atomic<int> regs_ok[kMaxDev][2];
+    static std::atomic<int> smem_set[kMaxDev][4];
+    static std::atomic<int> regs_ok[kMaxDev][4];
     if (device < 0 || device >= kMaxDev)
         return cudaErrorInvalidDevice;
     const bool odd = a.G % 2 != 0;
-    const void* fn = odd ? reinterpret_cast<const void*>(prefill_split_kernel<true>)
-                         : reinterpret_cast<const void*>(prefill_split_kernel<false>);
-    int rk = regs_ok[device][odd].load(std::memory_order_relaxed);
+    const int which = (odd ? 1 : 0) + (a.window > 0 ? 2 : 0);
+    using Kernel = void (*)(const CUtensorMap, const CUtensorMap, const CUtensorMap, const SplitPrefillArgs);
+    static const Kernel kernels[4] = {prefill_split_kernel<false, false>, prefill_split_kernel<true, false>,
+                                      prefill_split_kernel<false, true>, prefill_split_kernel<true, true>};
+    const Kernel kernel = kernels[which];
+    const void* fn = reinterpret_cast<const void*>(kernel);
+    int rk = regs_ok[device][which].load(std::memory_order_relaxed);
     if (rk == 0) {
         cudaFuncAttributes fa;
         cudaError_t e = cudaFuncGetAttributes(&fa, fn);
@@ -1057,16 +1104,16 @@ cudaError_t launch_prefill_split(const CUtensorMap& q_map, const CUtensorMap& ke
         const bool fits = fa.numRegs >= kRegsProducer && fa.numRegs <= kRegsSoftmax &&
                           128 * kRegsProducer + 256 * kRegsSoftmax <= kThreads * fa.numRegs;
         rk = fits ? 1 : 2;
-        regs_ok[device][odd].store(rk, std::memory_order_relaxed);
+        regs_ok[device][which].store(rk, std::memory_order_relaxed);
     }
     if (rk != 1)
         return cudaErrorNotSupported;
     const int smem = Layout::kBytes;
-    if (smem_set[device][odd].load(std::memory_order_relaxed) < smem) {
+    if (smem_set[device][which].load(std::memory_order_relaxed) < smem) {
         cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess)
             return e;
-        smem_set[device][odd].store(smem, std::memory_order_relaxed);
+        smem_set[device][which].store(smem, std::memory_order_relaxed);
     }
     const uint64_t st = next_launch_stamp();
     uint8_t* w = static_cast<uint8_t*>(workspace);
@@ -1089,8 +1136,7 @@ cudaError_t launch_prefill_split(const CUtensorMap& q_map, const CUtensorMap& ke
     attr[0].val.cooperative = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return odd ? cudaLaunchKernelEx(&cfg, prefill_split_kernel<true>, q_map, key_map, value_map, a)
-               : cudaLaunchKernelEx(&cfg, prefill_split_kernel<false>, q_map, key_map, value_map, a);
+    return cudaLaunchKernelEx(&cfg, kernel, q_map, key_map, value_map, a);
 }
 
 }  // namespace pa

@@ -216,8 +216,13 @@ def test_dispatch(L, mcl):
     got = pa.pa_attention_window(**c, window=200, sinks=4, max_context_len=mcl)
     check_no_device_error()
     check_out(got, reference(c, 200, 4), False, 300)
-    want = run_decode(c, 200, 4, max_context_len=mcl) if L <= 24 else run_prefill(c, 200, 4)
-    assert torch.equal(got, want)
+    if L <= 24:
+        assert torch.equal(got, run_decode(c, 200, 4, max_context_len=mcl))
+    else:
+        # without room for the split kernel: pa_prefill_window
+        none = torch.empty(16, dtype=torch.uint8, device="cuda")
+        got = pa.pa_attention_window(**c, window=200, sinks=4, max_context_len=mcl, workspace=none)
+        assert torch.equal(got, run_prefill(c, 200, 4))
 
 
 @pytest.mark.parametrize("ps", [1, 16, 128, 256])
@@ -289,3 +294,91 @@ def test_prefill_replayed_graph_on_another_stream():
         graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(out, want)
+
+
+# ---- the prefill with its tiles spread over the SMs ---------------------------
+
+@pytest.fixture
+def split_always():
+    """Test setting 6: the split kernel for every windowed prefill that it can
+    take, in pieces of about two tiles."""
+    pa = _pa()
+    pa.pa_debug_prefill_variant(6)
+    yield
+    pa.pa_debug_prefill_variant(0)
+
+
+def check_split(lens, H_q, H_kv, L, ps, W, S, seed, fp8=False):
+    pa = _pa()
+    c = make(lens, H_q, H_kv, L, 128, ps, seed, W, S, fp8)
+    mcl = max(max(lens), 1)
+    shape = pa.make_shape(c["query"].shape, c["key_pages"].shape, c["block_table"].shape[1])
+    ref = reference(c, W, S, fp8)
+    if fp8:
+        c.update(k_scale=SCALES[0], v_scale=SCALES[1])
+        need = pa.pa_attention_window_fp8_workspace_bytes(shape, ps, mcl, W, S)
+        call = pa.pa_attention_window_fp8
+    else:
+        need = pa.pa_attention_window_workspace_bytes(shape, ps, mcl, W, S)
+        assert need > 0
+        call = pa.pa_attention_window
+    ws = torch.full((need,), 0xFF, dtype=torch.uint8, device="cuda")
+    out = call(**c, window=W, sinks=S, max_context_len=mcl, workspace=ws)
+    check_no_device_error()
+    check_out(out, ref, False, W + S + 1)
+    again = call(**c, window=W, sinks=S, max_context_len=mcl, workspace=ws)
+    assert torch.equal(out, again)
+
+
+@pytest.mark.parametrize("ps", [8, 16, 64, 128, 256])
+@pytest.mark.parametrize("W,S", [(1, 0), (1, 2), (64, 4), (128, 128), (129, 0), (200, 130), (513, 17), (5000, 4)])
+def test_split_pages_and_windows(split_always, ps, W, S):
+    check_split(PREFILL_LENS, 4, 2, 60, ps, W, S, seed=ps + W)
+
+
+@pytest.mark.parametrize("L", [40, 127, 128, 129, 257, 700])
+@pytest.mark.parametrize("W,S", [(40, 4), (300, 0), (900, 20)])
+def test_split_lengths(split_always, L, W, S):
+    check_split([0, 3, L, L + 1, L + 200, L + 999], 4, 2, L, 16, W, S, seed=L + W)
+
+
+@pytest.mark.parametrize("H_q,H_kv", [(2, 1), (3, 1), (7, 1), (28, 4), (32, 8)])
+def test_split_head_layouts(split_always, H_q, H_kv):
+    check_split([100, 1431], H_q, H_kv, 100, 16, 490, 5, seed=H_q)
+
+
+@pytest.mark.parametrize("L", [9, 130])
+@pytest.mark.parametrize("W,S", [(100, 4), (300, 130), (1000, 0)])
+def test_split_e4m3(split_always, L, W, S):
+    check_split([0, 2, L, L + 77, L + 1500], 8, 2, L, 16, W, S, seed=34, fp8=True)
+
+
+def test_split_of_few_items_and_long_windows():
+    """Shapes that the call itself spreads over the SMs: many pieces an item,
+    and two items a block short of two rounds."""
+    check_split([6000], 8, 2, 100, 16, 4096, 4, seed=50)
+    check_split([4500, 5200], 32, 8, 600, 16, 2048, 20, seed=51)
+
+
+def test_split_in_a_replayed_graph_sees_new_inputs():
+    pa = _pa()
+    c, fresh = (make([6000], 8, 2, 100, 128, 16, s, 4096, 4, poison=False) for s in (52, 53))
+    kw = dict(window=4096, sinks=4, max_context_len=6000)
+    shape = pa.make_shape(c["query"].shape, c["key_pages"].shape, c["block_table"].shape[1])
+    need = pa.pa_attention_window_workspace_bytes(shape, 16, 6000, 4096, 4)
+    assert need > 0
+    ws = torch.zeros(need, dtype=torch.uint8, device="cuda")
+    out = torch.empty_like(c["query"])
+    pa.pa_attention_window(**c, **kw, out=out, workspace=ws)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        pa.pa_attention_window(**c, **kw, out=out, workspace=ws)
+    graph.replay()
+    want = pa.pa_attention_window(**fresh, **kw, workspace=torch.zeros_like(ws))
+    for k in ("query", "key_pages", "value_pages", "block_table"):
+        c[k].copy_(fresh[k])
+    for _ in range(3):
+        out.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
