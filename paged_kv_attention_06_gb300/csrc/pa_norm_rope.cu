@@ -22,9 +22,14 @@
 // group of lanes takes U heads of one kind of one token: all loads are issued
 // before the first is used, and the products of weights and angles are made once
 // for the U heads, two elements to an instruction. Measured (one call of a
-// replayed graph): 8188 tokens of 32 + 2 x 8 heads of 128, 204.6 MB, 39.1 us (5.2
-// TB/s, of 6.8 for a copy; 62.8 before the pairs of one lane), e4m3 pools 48 us;
+// replayed graph): 8188 tokens of 32 + 2 x 8 heads of 128, 204.6 MB, 34.8 us (5.9
+// TB/s, of 6.8 for a copy; 62.8 before the pairs of one lane), e4m3 pools 42 us;
 // one token 2.1 us. What is left is the latency of a block's loads.
+//
+// Loads and bf16 stores are marked as streamed (evict first), both or neither: 38.7
+// us without, 38.8 with the stores' alone, 40 with the loads' alone. The attention that
+// follows does not pay for it: qkv written, appended and attended to (window 1024),
+// 8188 tokens 178 us against 181, 4094 tokens 97 against 98, 1024 tokens 33.4 both.
 #include <stdint.h>
 
 #include "pa_device.cuh"
@@ -107,8 +112,8 @@ __global__ void __launch_bounds__(kThreads) norm_rope_append_kernel(const NormRo
     for (int u = 0; u < U; ++u) {
         raw[u][0] = raw[u][1] = make_uint2(0, 0);
         if (u < heads) {
-            raw[u][0] = *reinterpret_cast<const uint2*>(src + u * D + e0);
-            raw[u][1] = *reinterpret_cast<const uint2*>(src + u * D + e1);
+            raw[u][0] = __ldcs(reinterpret_cast<const uint2*>(src + u * D + e0));
+            raw[u][1] = __ldcs(reinterpret_cast<const uint2*>(src + u * D + e1));
         }
     }
     const int64_t slot = a.slot_mapping[tok];
@@ -223,8 +228,8 @@ __global__ void __launch_bounds__(kThreads) norm_rope_append_kernel(const NormRo
             *reinterpret_cast<uint32_t*>(row + e1) = quantise4(x + 2, scale, recip);
         } else {
             uint16_t* row = to + at + u * head_step;
-            *reinterpret_cast<uint2*>(row + e0) = out[0];
-            *reinterpret_cast<uint2*>(row + e1) = out[1];
+            __stcs(reinterpret_cast<uint2*>(row + e0), out[0]);
+            __stcs(reinterpret_cast<uint2*>(row + e1), out[1]);
         }
     }
 }
