@@ -561,8 +561,9 @@ pa_status pa_decode_weights_fp8(const void *query, const void *key_pages, const 
  *   key_pages, value_pages  [P, H_kv, page_size, D] bf16 (_fp8: e4m3 codes,
  *                    head_dim 128); weight_pages [P, H_kv, page_size] fp32.
  *   dst_block_table  [B, dst_max_pages] int32. The block table itself (the same
- *                    address): in place; slots behind the kept ones keep their
- *                    contents. Another table: pages that no request of the call
+ *                    address; dst_max_pages is max_pages then, or B is 1): in
+ *                    place; slots behind the kept ones keep their contents.
+ *                    Another table: pages that no request of the call
  *                    reads and no other entry names (pages shared by requests
  *                    are evicted into fresh ones); an entry that is the
  *                    request's own page of the same place records

@@ -1099,6 +1099,9 @@ pa_status run_evict(void* key_pages, void* value_pages, float* weight_pages,
     const int64_t most = std::min(int64_t(keep), int64_t(s.max_pages) * page_size);
     if (int64_t(dst_max_pages) * page_size < most)
         return PA_ERR_INVALID_ARG;
+    // In place the two tables are one: rows of another width would be other requests'.
+    if (dst_block_table == block_table && s.batch > 1 && dst_max_pages != s.max_pages)
+        return PA_ERR_INVALID_ARG;
     // The kernels read the lengths and the table after new_lens and kept are written.
     const uint64_t heads = uint64_t(s.batch) * s.num_kv_heads;
     const uint64_t kept_bytes = heads * keep * 4, len_bytes = uint64_t(s.batch) * 4;
