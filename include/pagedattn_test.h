@@ -53,7 +53,9 @@ void pa_debug_arm_wait_timeout(void);
  *      starts late);
  *   6  as 2; pa_attention_window and its e4m3 form take the split kernel
  *      wherever it can run and the workspace has room, in pieces of about two
- *      tiles (the workspace function follows the setting).
+ *      tiles (the workspace function follows the setting);
+ *   7  as 2; pa_prefill_window runs on the split-KV kernel with whole segments,
+ *      as where the tensor-core kernel's register split is not available.
  * Settings 1 and 2 also hold for pa_prefill_split and for pa_attention given
  * a prefill workspace (the workspace is then not used). Any other value is
  * taken as 0. Returns the previous setting. Results agree

@@ -453,7 +453,7 @@ pa_status run_prefill_window(const void* query, const void* key_pages, const voi
     pa_status st = device_info(&dev);
     if (st != PA_OK)
         return st;
-    if (prefill_pairs_smem_bytes(s.head_dim) > size_t(dev->max_smem_optin))
+    if (prefill_pairs_smem_bytes(s.head_dim) > size_t(dev->max_smem_optin) || t_prefill_variant == 7)
         return PA_ERR_UNSUPPORTED;
     const int64_t n_qtiles = (int64_t(s.q_len) + 127) / 128;
     const int64_t q_rows = int64_t(s.batch) * s.num_q_heads * s.q_len;
@@ -1835,7 +1835,7 @@ int pa_debug_prefill_variant(int variant)
 {
     const int prev = t_prefill_variant;
     t_prefill_variant = (variant == 1 || variant == 2 || variant == 4 || variant == 5 ||
-                         variant == 6)
+                         variant == 6 || variant == 7)
                             ? variant
                             : 0;
     return prev;

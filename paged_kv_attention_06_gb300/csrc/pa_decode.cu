@@ -1322,8 +1322,9 @@ namespace {
 using DecodeKernel = void (*)(CUtensorMap, CUtensorMap, CUtensorMap, DecodeArgs);
 
 // The instantiation for (head_dim, e4m3 pages, row tiles per segment), with
-// its index in the table of raised shared-memory limits.
-// One bf16 row tile is the few-row kernel's with a window or scores.
+// its index in the table of raised shared-memory limits. One bf16 row tile with a
+// window or scores is the few-row kernel's, but for batches whose table of requests
+// does not fit beside that kernel's rings, and for whole segments.
 template <int kMode>
 DecodeKernel decode_kernel_of(int D, bool fp8, int TG, int* index)
 {
@@ -1333,12 +1334,11 @@ DecodeKernel decode_kernel_of(int D, bool fp8, int TG, int* index)
     }
     const int t = TG == 4 ? 2 : TG == 2 ? 1 : 0;
     *index = 1 + (D == 64 ? 0 : 3) + t;
-    if (t > 0)
-        return D == 64 ? (t == 2 ? decode_kernel<64, false, 4, kMode> : decode_kernel<64, false, 2, kMode>)
-                       : (t == 2 ? decode_kernel<128, false, 4, kMode> : decode_kernel<128, false, 2, kMode>);
-    if constexpr (kMode == kFull)
-        return D == 64 ? decode_kernel<64, false, 1, kFull> : decode_kernel<128, false, 1, kFull>;
-    return nullptr;
+    if (D == 64)
+        return t == 2 ? decode_kernel<64, false, 4, kMode> : t == 1 ? decode_kernel<64, false, 2, kMode>
+                                                                    : decode_kernel<64, false, 1, kMode>;
+    return t == 2 ? decode_kernel<128, false, 4, kMode> : t == 1 ? decode_kernel<128, false, 2, kMode>
+                                                                 : decode_kernel<128, false, 1, kMode>;
 }
 
 DecodeKernel decode_kernel_for(int mode, int D, bool fp8, int TG, int* index)
@@ -1377,8 +1377,6 @@ cudaError_t launch_decode(const CUtensorMap& key_map, const CUtensorMap& value_m
     const DecodeKernel kern = decode_kernel_for(a.mode, a.D, fp8, a.TG, &di);
     if (device < 0 || device >= kMaxDev)
         return cudaErrorInvalidDevice;
-    if (kern == nullptr)
-        return cudaErrorInvalidValue;
     if (smem_set[device][di].load(std::memory_order_relaxed) < smem) {
         cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(kern),
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
