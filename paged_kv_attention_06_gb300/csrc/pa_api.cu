@@ -93,6 +93,25 @@ pa_status get_encoder(PFN_cuTensorMapEncodeTiled_v12000* fn)
     return PA_OK;
 }
 
+// Encodes a tensor map. The driver wants a current context: a host thread whose first
+// CUDA call this is has none until the runtime binds its device's.
+template <typename... Args>
+pa_status encode_map(Args... args)
+{
+    PFN_cuTensorMapEncodeTiled_v12000 enc;
+    const pa_status st = get_encoder(&enc);
+    if (st != PA_OK)
+        return st;
+    CUresult r = enc(args...);
+    if (r == CUDA_ERROR_INVALID_CONTEXT || r == CUDA_ERROR_NOT_INITIALIZED) {
+        int dev = 0;
+        if (cudaGetDevice(&dev) != cudaSuccess || cudaSetDevice(dev) != cudaSuccess)
+            return PA_ERR_CUDA;
+        r = enc(args...);
+    }
+    return r == CUDA_SUCCESS ? PA_OK : PA_ERR_CUDA;
+}
+
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 bool pow2_in(int v, int lo, int hi) { return v >= lo && v <= hi && (v & (v - 1)) == 0; }
@@ -178,10 +197,6 @@ pa_status encode_pool_map(CUtensorMap* map, const void* pool, const pa_shape& s,
 pa_status encode_pool_map_uncached(CUtensorMap* map, const void* pool, const pa_shape& s,
                                    int32_t ps, bool fp8, int box_rows)
 {
-    PFN_cuTensorMapEncodeTiled_v12000 enc;
-    pa_status st = get_encoder(&enc);
-    if (st != PA_OK)
-        return st;
     const cuuint64_t dims[2] = {cuuint64_t(s.head_dim),
                                 cuuint64_t(s.num_pages) * s.num_kv_heads * ps};
     const cuuint64_t strides[1] = {cuuint64_t(s.head_dim) * (fp8 ? 1 : 2)};
@@ -193,11 +208,10 @@ pa_status encode_pool_map_uncached(CUtensorMap* map, const void* pool, const pa_
     // 128-byte aligned).
     const CUtensorMapSwizzle swz =
         box_rows >= 8 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE;
-    CUresult r = enc(map, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
+    return encode_map(map, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
                      const_cast<void*>(pool), dims, strides, box, estr,
                      CU_TENSOR_MAP_INTERLEAVE_NONE, swz, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    return r == CUDA_SUCCESS ? PA_OK : PA_ERR_CUDA;
 }
 
 // 2-D bf16 tensor map over `rows` rows of `cols` columns, boxes of 64 columns
@@ -205,19 +219,14 @@ pa_status encode_pool_map_uncached(CUtensorMap* map, const void* pool, const pa_
 pa_status encode_rows_map(CUtensorMap* map, const void* base, uint64_t rows, uint32_t box_rows,
                           uint32_t cols = 128)
 {
-    PFN_cuTensorMapEncodeTiled_v12000 enc;
-    pa_status st = get_encoder(&enc);
-    if (st != PA_OK)
-        return st;
     const cuuint64_t dims[2] = {cuuint64_t(cols), cuuint64_t(rows)};
     const cuuint64_t strides[1] = {cuuint64_t(cols) * 2};
     const cuuint32_t box[2] = {64u, box_rows};
     const cuuint32_t estr[2] = {1u, 1u};
-    CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims,
+    return encode_map(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims,
                      strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                      CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    return r == CUDA_SUCCESS ? PA_OK : PA_ERR_CUDA;
 }
 
 // 3-D bf16 tensor map over the attention output [B * H_q, L, cols]: boxes of
@@ -225,18 +234,13 @@ pa_status encode_rows_map(CUtensorMap* map, const void* base, uint64_t rows, uin
 // prefill kernel's output stores; rows past L are outside the map).
 pa_status encode_out_map(CUtensorMap* map, void* base, uint64_t heads, uint64_t L, uint32_t cols)
 {
-    PFN_cuTensorMapEncodeTiled_v12000 enc;
-    pa_status st = get_encoder(&enc);
-    if (st != PA_OK)
-        return st;
     const cuuint64_t dims[3] = {cuuint64_t(cols), cuuint64_t(L), cuuint64_t(heads)};
     const cuuint64_t strides[2] = {cuuint64_t(cols) * 2, cuuint64_t(cols) * 2 * L};
     const cuuint32_t box[3] = {64u, 32u, 1u};
     const cuuint32_t estr[3] = {1u, 1u, 1u};
-    CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, base, dims, strides, box, estr,
+    return encode_map(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, base, dims, strides, box, estr,
                      CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                      CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    return r == CUDA_SUCCESS ? PA_OK : PA_ERR_CUDA;
 }
 
 // Workspace the split prefill kernel needs for this shape on this device, or
