@@ -27,6 +27,18 @@ namespace {
 
 PyObject* g_error = nullptr;   // PagedAttentionError
 
+// The C call without the interpreter lock: a launch may wait for room in its stream's
+// queue, and what would make room may need the lock. Nothing in it touches Python. (The
+// tensors stay alive: the caller's frame holds them.)
+template <typename F>
+pa_status unlocked(F call)
+{
+    PyThreadState* const state = PyEval_SaveThread();
+    const pa_status st = call();
+    PyEval_RestoreThread(state);
+    return st;
+}
+
 // Thrown with a Python error set.
 struct Raised {};
 
@@ -248,14 +260,17 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n)
                                  size32(L, "L"), size32(P, "the number of pages"), 0};
             const float eps = float(number(a[11]));
             const int inter = truth(a[12]);
-            const pa_status st =
-                fp8 ? pa_qk_norm_rope_append_fp8(qkv.data_ptr(), bs, ts, qw, kw, eps, static_cast<float*>(cs),
-                                                 int32_t(R), int32_t(table), inter, static_cast<int32_t*>(pos), q_ptr,
-                                                 k_ptr, v_ptr, static_cast<int32_t*>(slot), ps, float(number(a[9])),
-                                                 float(number(a[10])), shape, call.stream)
-                    : pa_qk_norm_rope_append(qkv.data_ptr(), bs, ts, qw, kw, eps, static_cast<float*>(cs), int32_t(R),
-                                             int32_t(table), inter, static_cast<int32_t*>(pos), q_ptr, k_ptr, v_ptr,
-                                             static_cast<int32_t*>(slot), ps, shape, call.stream);
+            const float ks = fp8 ? float(number(a[9])) : 1.f, vs = fp8 ? float(number(a[10])) : 1.f;
+            const void* rows = qkv.data_ptr();
+            const pa_status st = unlocked([&] {
+                return fp8 ? pa_qk_norm_rope_append_fp8(rows, bs, ts, qw, kw, eps, static_cast<float*>(cs), int32_t(R),
+                                                        int32_t(table), inter, static_cast<int32_t*>(pos), q_ptr, k_ptr,
+                                                        v_ptr, static_cast<int32_t*>(slot), ps, ks, vs, shape,
+                                                        call.stream)
+                           : pa_qk_norm_rope_append(rows, bs, ts, qw, kw, eps, static_cast<float*>(cs), int32_t(R),
+                                                    int32_t(table), inter, static_cast<int32_t*>(pos), q_ptr, k_ptr,
+                                                    v_ptr, static_cast<int32_t*>(slot), ps, shape, call.stream);
+            });
             if (raised(st, what))
                 return nullptr;
         }
@@ -331,32 +346,33 @@ PyObject* window(PyObject*, PyObject* const* a, Py_ssize_t n)
         const char* what;
         if (which == 1) {
             what = "pa_prefill_window";
-            st = pa_prefill_window(p.q, p.k, p.v, p.table(), p.lens(), p.ps, p.scale, win, sinks, out, p.shape,
-                                   p.call.stream);
+            st = unlocked([&] {
+                return pa_prefill_window(p.q, p.k, p.v, p.table(), p.lens(), p.ps, p.scale, win, sinks, out, p.shape,
+                                         p.call.stream);
+            });
         } else {
             size_t need = 0;
             if (a[14] == Py_None)
                 need = which == 0 ? pa_decode_window_workspace_bytes(p.shape)
                        : fp8      ? pa_attention_window_fp8_workspace_bytes(p.shape, p.ps, longest, win, sinks)
                                   : pa_attention_window_workspace_bytes(p.shape, p.ps, longest, win, sinks);
-            const at::Tensor ws = p.call.workspace(a[14], need);
-            const size_t bytes = ws.nbytes();
-            if (which == 0 && fp8) {
-                what = "pa_decode_window_fp8";
-                st = pa_decode_window_fp8(p.q, p.k, p.v, p.table(), p.lens(), p.ps, p.scale, ks, vs, win, sinks, out,
-                                          p.shape, longest, ws.data_ptr(), bytes, p.call.stream);
-            } else if (which == 0) {
-                what = "pa_decode_window";
-                st = pa_decode_window(p.q, p.k, p.v, p.table(), p.lens(), p.ps, p.scale, win, sinks, out, p.shape,
-                                      longest, ws.data_ptr(), bytes, p.call.stream);
-            } else if (fp8) {
-                what = "pa_attention_window_fp8";
-                st = pa_attention_window_fp8(p.q, p.k, p.v, p.table(), p.lens(), p.ps, p.scale, ks, vs, win, sinks, out,
-                                             p.shape, longest, ws.data_ptr(), bytes, p.call.stream);
+            const at::Tensor workspace = p.call.workspace(a[14], need);
+            const size_t bytes = workspace.nbytes();
+            void* ws = workspace.data_ptr();
+            if (fp8) {
+                what = which == 0 ? "pa_decode_window_fp8" : "pa_attention_window_fp8";
+                const auto f = which == 0 ? pa_decode_window_fp8 : pa_attention_window_fp8;
+                st = unlocked([&] {
+                    return f(p.q, p.k, p.v, p.table(), p.lens(), p.ps, p.scale, ks, vs, win, sinks, out, p.shape,
+                             longest, ws, bytes, p.call.stream);
+                });
             } else {
-                what = "pa_attention_window";
-                st = pa_attention_window(p.q, p.k, p.v, p.table(), p.lens(), p.ps, p.scale, win, sinks, out, p.shape,
-                                         longest, ws.data_ptr(), bytes, p.call.stream);
+                what = which == 0 ? "pa_decode_window" : "pa_attention_window";
+                const auto f = which == 0 ? pa_decode_window : pa_attention_window;
+                st = unlocked([&] {
+                    return f(p.q, p.k, p.v, p.table(), p.lens(), p.ps, p.scale, win, sinks, out, p.shape, longest, ws,
+                             bytes, p.call.stream);
+                });
             }
         }
         if (raised(st, what))
@@ -380,15 +396,17 @@ PyObject* weights(PyObject*, PyObject* const* a, Py_ssize_t n)
         const int32_t longest = integer(a[9], "max_context_len");
         const float decay = float(number(a[10]));
         const int causal = truth(a[12]);
-        const at::Tensor ws = p.call.workspace(
+        const float ks = fp8 ? float(number(a[7])) : 1.f, vs = fp8 ? float(number(a[8])) : 1.f;
+        const at::Tensor workspace = p.call.workspace(
             a[14], a[14] == Py_None ? pa_decode_weights_workspace_bytes(p.shape, longest) : 0);
-        void* out = p.out.data_ptr();
-        const pa_status st =
-            fp8 ? pa_decode_weights_fp8(p.q, p.k, p.v, w, p.table(), p.lens(), p.ps, p.scale, float(number(a[7])),
-                                        float(number(a[8])), causal, decay, out, p.shape, longest, ws.data_ptr(),
-                                        ws.nbytes(), p.call.stream)
-                : pa_decode_weights(p.q, p.k, p.v, w, p.table(), p.lens(), p.ps, p.scale, causal, decay, out, p.shape,
-                                    longest, ws.data_ptr(), ws.nbytes(), p.call.stream);
+        void *out = p.out.data_ptr(), *ws = workspace.data_ptr();
+        const size_t bytes = workspace.nbytes();
+        const pa_status st = unlocked([&] {
+            return fp8 ? pa_decode_weights_fp8(p.q, p.k, p.v, w, p.table(), p.lens(), p.ps, p.scale, ks, vs, causal,
+                                               decay, out, p.shape, longest, ws, bytes, p.call.stream)
+                       : pa_decode_weights(p.q, p.k, p.v, w, p.table(), p.lens(), p.ps, p.scale, causal, decay, out,
+                                           p.shape, longest, ws, bytes, p.call.stream);
+        });
         if (raised(st, fp8 ? "pa_decode_weights_fp8" : "pa_decode_weights"))
             return nullptr;
         return THPVariable_Wrap(p.out);
@@ -437,9 +455,11 @@ PyObject* evict(PyObject*, PyObject* const* a, Py_ssize_t n)
             const int32_t heads = size32(H, "H_kv");
             const pa_shape shape{size32(B, "B"), heads, heads, size32(kp.size(3), "D"), 1,
                                  size32(kp.size(0), "the number of pages"), size32(table.size(1), "max_pages")};
-            const pa_status st = (fp8 ? pa_kv_evict_fp8 : pa_kv_evict)(k, v, w, bt, cl, ps, keep, sinks, recent, dt,
-                                                                       size32(dst.size(1), "dst_max_pages"), kept_ptr, fresh_ptr, shape,
-                                                                       call.stream);
+            const int32_t dst_pages = size32(dst.size(1), "dst_max_pages");
+            const pa_status st = unlocked([&] {
+                return (fp8 ? pa_kv_evict_fp8 : pa_kv_evict)(k, v, w, bt, cl, ps, keep, sinks, recent, dt, dst_pages,
+                                                             kept_ptr, fresh_ptr, shape, call.stream);
+            });
             if (raised(st, what))
                 return nullptr;
         }
