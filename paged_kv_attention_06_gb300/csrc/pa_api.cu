@@ -75,6 +75,23 @@ pa_status device_info(DeviceInfo** out)
     return PA_OK;
 }
 
+cudaError_t raise_smem_limit(const void* kernel, std::atomic<bool>* raised)
+{
+    if (raised->load(std::memory_order_relaxed))
+        return cudaSuccess;
+    DeviceInfo* dev;
+    if (device_info(&dev) != PA_OK)
+        return cudaErrorInvalidDevice;
+    cudaFuncAttributes fa;
+    cudaError_t e = cudaFuncGetAttributes(&fa, kernel);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 dev->max_smem_optin - int(fa.sharedSizeBytes));
+    if (e == cudaSuccess)
+        raised->store(true, std::memory_order_relaxed);
+    return e;
+}
+
 namespace {
 
 pa_status get_encoder(PFN_cuTensorMapEncodeTiled_v12000* fn)

@@ -1365,10 +1365,8 @@ cudaError_t launch_decode(const CUtensorMap& key_map, const CUtensorMap& value_m
                           const CUtensorMap& q_map, const DecodeArgs& a, int grid, int device,
                           cudaStream_t stream)
 {
-    // The dynamic shared-memory limit is raised once per (device, kernel)
-    // and only grows.
     constexpr int kMaxDev = 64;
-    static std::atomic<int> smem_set[kMaxDev][7 * kDecodeModes];
+    static std::atomic<bool> raised[kMaxDev][7 * kDecodeModes];
     const bool fp8 = a.fp8 != 0;
     if ((fp8 && (a.D != 128 || a.TG != 1)) || (a.TG != 1 && a.TG != 2 && a.TG != 4))
         return cudaErrorInvalidValue;
@@ -1377,13 +1375,9 @@ cudaError_t launch_decode(const CUtensorMap& key_map, const CUtensorMap& value_m
     const DecodeKernel kern = decode_kernel_for(a.mode, a.D, fp8, a.TG, &di);
     if (device < 0 || device >= kMaxDev)
         return cudaErrorInvalidDevice;
-    if (smem_set[device][di].load(std::memory_order_relaxed) < smem) {
-        cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(kern),
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-        if (e != cudaSuccess)
-            return e;
-        smem_set[device][di].store(smem, std::memory_order_relaxed);
-    }
+    cudaError_t e = raise_smem_limit(reinterpret_cast<const void*>(kern), &raised[device][di]);
+    if (e != cudaSuccess)
+        return e;
     // Both kernels are launched with programmatic stream serialization: each
     // may be scheduled before its predecessor in the stream has finished and
     // waits for it (griddepcontrol.wait) before touching its data.
@@ -1397,7 +1391,7 @@ cudaError_t launch_decode(const CUtensorMap& key_map, const CUtensorMap& value_m
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    cudaError_t e = cudaLaunchKernelEx(&cfg, kern, key_map, value_map, q_map, a);
+    e = cudaLaunchKernelEx(&cfg, kern, key_map, value_map, q_map, a);
     if (e != cudaSuccess || a.whole_segments)
         return e;
     DecodeArgs ma = a;

@@ -908,17 +908,13 @@ cudaError_t launch_decode_rows(const CUtensorMap& key_map, const CUtensorMap& va
     int index = 0;
     const RowsKernels kern = rows_kernels_for(a.D, a.fp8 != 0, NT, a.mode, &index);
     constexpr int kMaxDev = 64;
-    static std::atomic<int> smem_set[kMaxDev][12];
+    static std::atomic<bool> raised[kMaxDev][12];
     if (device < 0 || device >= kMaxDev)
         return cudaErrorInvalidDevice;
     const int smem = int(rows_smem_bytes(a.D, NT, a.B));
-    if (smem_set[device][index].load(std::memory_order_relaxed) < smem) {
-        const cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(kern.main),
-                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-        if (e != cudaSuccess)
-            return e;
-        smem_set[device][index].store(smem, std::memory_order_relaxed);
-    }
+    cudaError_t e = raise_smem_limit(reinterpret_cast<const void*>(kern.main), &raised[device][index]);
+    if (e != cudaSuccess)
+        return e;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -929,7 +925,7 @@ cudaError_t launch_decode_rows(const CUtensorMap& key_map, const CUtensorMap& va
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern.main, key_map, value_map, a);
+    e = cudaLaunchKernelEx(&cfg, kern.main, key_map, value_map, a);
     if (e != cudaSuccess)
         return e;
     cfg.gridDim = dim3(unsigned(int64_t(a.B) * a.H_kv));

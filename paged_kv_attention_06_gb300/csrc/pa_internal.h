@@ -7,6 +7,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "../../include/pagedattn.h"
 
 namespace pa {
@@ -32,6 +34,11 @@ struct DeviceInfo {
     unsigned* err = nullptr;  // device address of the error word
 };
 pa_status device_info(DeviceInfo** out);
+
+// Raises a kernel's limit of dynamic shared memory, once per device (*raised), to all
+// that a block can have there: the same number whatever the call's batch, so that host
+// threads whose first calls meet do not lower each other's.
+cudaError_t raise_smem_limit(const void* kernel, std::atomic<bool>* raised);
 
 // ---------------------------------------------------------------------------
 // Write path
