@@ -581,7 +581,8 @@ pa_status run_split_kv(const void* query, const void* key_pages, const void* val
         return PA_ERR_UNSUPPORTED;
     const DecodePlan plan = decode_plan(s, fp8 != 0);
     const int64_t nseg = plan.nseg;
-    const size_t smem = decode_smem_bytes(s.head_dim, s.batch, fp8 != 0, plan.TG);
+    const size_t smem = decode_smem_bytes(s.head_dim, s.batch, fp8 != 0, plan.TG) +
+                        decode_static_smem_bytes(fp8 != 0);
     if (smem > size_t(dev->max_smem_optin))
         return PA_ERR_UNSUPPORTED;  // batch too large for the per-block prefix table
 

@@ -1309,6 +1309,12 @@ size_t decode_smem_bytes(int D, int B, bool fp8, int TG)
          : TG == 2 ? Layout<128, false, 2>::bytes(B) : Layout<128>::bytes(B);
 }
 
+// Shared memory beside that: the e4m3 kernel's row states.
+size_t decode_static_smem_bytes(bool fp8)
+{
+    return fp8 ? size_t(kConsumerWarps) * 2 * kDecodeRows * sizeof(float) : 0;
+}
+
 int decode_max_grid(int sm_count) { return 2 * sm_count; }
 
 size_t decode_workspace_bytes(int64_t nseg, int grid_max, int D, int TG)

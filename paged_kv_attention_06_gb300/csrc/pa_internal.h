@@ -180,7 +180,8 @@ struct DecodeArgs {
                                // that nothing arrives at (times out, flags)
 };
 
-size_t decode_smem_bytes(int D, int B, bool fp8 = false, int TG = 1);
+size_t decode_smem_bytes(int D, int B, bool fp8 = false, int TG = 1);   // dynamic
+size_t decode_static_smem_bytes(bool fp8);
 int decode_max_grid(int sm_count);
 size_t decode_workspace_bytes(int64_t nseg, int grid_max, int D, int TG);
 cudaError_t launch_decode(const CUtensorMap& key_map, const CUtensorMap& value_map,

@@ -144,3 +144,29 @@ def test_window_prefill_without_the_tensor_core_kernel(D, H_q, H_kv, L, W, S):
         pa.pa_debug_prefill_variant(0)
     check_no_device_error()
     check(c, out, False, W, S)
+
+
+def test_the_largest_e4m3_batches_run_or_are_unsupported():
+    """The table of requests, up to the last that fits beside the e4m3 kernel's own arrays."""
+    pa = _pa()
+    c = batch(32000, 1, 1, 1, 128, True, seed=7, n_max=16)
+    ws = torch.empty(512 << 20, dtype=torch.uint8, device="cuda")
+    out = torch.empty_like(c["query"])
+
+    def runs(B):
+        part = {k: x[:B] if k in ("query", "block_table", "context_lens") else x for k, x in c.items()}
+        try:
+            pa.pa_decode_fp8(**part, k_scale=1.0, v_scale=1.0, out=out[:B], max_context_len=16, workspace=ws)
+        except pa.PagedAttentionError as e:
+            assert e.status == pa.PA_ERR_UNSUPPORTED, (B, e)
+            return False
+        return True
+
+    lo, hi = 1, 32000                                # runs, does not
+    assert runs(lo) and not runs(hi)
+    while hi - lo > 1:
+        mid = (lo + hi) // 2
+        lo, hi = (mid, hi) if runs(mid) else (lo, mid)
+    for B in range(lo - 40, lo + 100):
+        assert runs(B) == (B <= lo)
+    check_no_device_error()
