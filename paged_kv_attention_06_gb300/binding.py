@@ -146,22 +146,28 @@ def _load() -> ctypes.CDLL:
 _lib = _load()
 
 
-def _load_calls():
-    import importlib.machinery
-    import importlib.util
-    if not os.path.exists(_build.PYTHON_LIB):
-        raise ImportError(
-            f"{_build.PYTHON_LIB} is not built; run "
-            "`python -c 'import __graft_entry__ as g; g.build()'`")
-    loader = importlib.machinery.ExtensionFileLoader("_pagedattn_calls", _build.PYTHON_LIB)
-    module = importlib.util.module_from_spec(
-        importlib.util.spec_from_loader("_pagedattn_calls", loader))
-    loader.exec_module(module)
-    module.set_error(PagedAttentionError)
-    return module
+class _Calls:
+    """The compiled module, loaded with the first of its calls: the calls through ctypes
+    need neither it nor the torch that it was built for."""
+
+    def __getattr__(self, name):
+        global _calls
+        import importlib.machinery
+        import importlib.util
+        if not os.path.exists(_build.PYTHON_LIB):
+            raise ImportError(
+                f"{_build.PYTHON_LIB} is not built; run "
+                "`python -c 'import __graft_entry__ as g; g.build()'`")
+        loader = importlib.machinery.ExtensionFileLoader("_pagedattn_calls", _build.PYTHON_LIB)
+        module = importlib.util.module_from_spec(
+            importlib.util.spec_from_loader("_pagedattn_calls", loader))
+        loader.exec_module(module)
+        module.set_error(PagedAttentionError)
+        _calls = module              # called directly from now on
+        return getattr(module, name)
 
 
-_calls = _load_calls()
+_calls = _Calls()
 
 
 def status_string(status: int) -> str:
