@@ -101,7 +101,6 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
     with ThreadPoolExecutor(max_workers=max(2, min(len(srcs) + 1, os.cpu_count() or 1))) as ex:
         python_obj = ex.submit(compile_python)
         objs = list(ex.map(compile_one, srcs))
-        python_obj = python_obj.result()
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = [nvcc, *ARCH, "-shared", "-cudart", "shared", "-o", tmp, *objs,
            "-Xlinker", "-soname=libpagedattn.so", "-Xlinker", "-rpath=/usr/local/cuda/lib64"]
@@ -110,17 +109,6 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
         sys.stderr.write(r.stdout + r.stderr)
         raise RuntimeError("nvcc link failed")
     os.replace(tmp, LIB)
-    import torch
-    torch_lib = os.path.join(os.path.dirname(torch.__file__), "lib")
-    tmp = PYTHON_LIB + f".tmp{os.getpid()}"
-    cmd = ["g++", "-shared", "-o", tmp, python_obj, "-L", BUILD, "-lpagedattn", "-L", torch_lib,
-           "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN",
-           f"-Wl,-rpath,{torch_lib}"]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode:
-        sys.stderr.write(r.stdout + r.stderr)
-        raise RuntimeError("linking _pagedattn_calls failed")
-    os.replace(tmp, PYTHON_LIB)
     # The benchmark's native step loops (bench_loop.cpp, beside bench.py):
     # host code only, linked against the library above.
     if os.path.exists(BENCH_SRC):
@@ -133,6 +121,19 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
             sys.stderr.write(r.stdout + r.stderr)
             raise RuntimeError("bench loop build failed")
         os.replace(tmp, BENCH_LIB)
+    # Last: what it lacks (torch's headers, a compiler that takes them) keeps nothing
+    # else from being built.
+    import torch
+    torch_lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = PYTHON_LIB + f".tmp{os.getpid()}"
+    cmd = ["g++", "-shared", "-o", tmp, python_obj.result(), "-L", BUILD, "-lpagedattn", "-L", torch_lib,
+           "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN",
+           f"-Wl,-rpath,{torch_lib}"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode:
+        sys.stderr.write(r.stdout + r.stderr)
+        raise RuntimeError("linking _pagedattn_calls failed")
+    os.replace(tmp, PYTHON_LIB)
     return LIB
 
 

@@ -4,6 +4,8 @@ import os
 import subprocess
 import sys
 
+import pytest
+
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 SCRIPT = """
@@ -40,3 +42,43 @@ def test_with_a_module_that_does_not_load(tmp_path):
     bad = tmp_path / "_pagedattn_calls.so"
     bad.write_bytes(b"another torch's")
     assert "refused:" in run(str(bad))
+
+
+@pytest.fixture
+def fake_build(monkeypatch, tmp_path):
+    """build.build() into tmp_path, with compilers that only make their output file.
+    .fails: a text; the commands that contain it fail. .ran: the commands."""
+    from paged_kv_attention_06_gb300 import build
+
+    class Fake:
+        fails = "\0"
+        ran = []
+
+    def run(cmd, **kw):
+        fake.ran.append(cmd)
+        failed = any(fake.fails in str(x) for x in cmd)
+        if not failed:
+            with open(cmd[cmd.index("-o") + 1], "w") as f:
+                f.write("made")
+        return subprocess.CompletedProcess(cmd, int(failed), "", "")
+
+    fake = Fake()
+    fake.build, fake.ran = build, []
+    for name in ("LIB", "BENCH_LIB", "PYTHON_LIB"):
+        monkeypatch.setattr(build, name, str(tmp_path / os.path.basename(getattr(build, name))))
+    monkeypatch.setattr(build, "BUILD", str(tmp_path))
+    monkeypatch.setattr(build, "_nvcc", lambda: sys.executable)
+    monkeypatch.setattr(build.subprocess, "run", run)
+    return fake
+
+
+@pytest.mark.parametrize("what", ["pa_python.cpp", "-ltorch_python"])
+def test_the_library_is_built_where_the_module_cannot_be(fake_build, what):
+    fake_build.fails = what
+    with pytest.raises(RuntimeError):
+        fake_build.build.build()
+    assert os.path.exists(fake_build.build.LIB) and os.path.exists(fake_build.build.BENCH_LIB)
+    assert not os.path.exists(fake_build.build.PYTHON_LIB)
+    fake_build.fails = "\0"
+    fake_build.build.build()
+    assert os.path.exists(fake_build.build.PYTHON_LIB) and fake_build.build.up_to_date()
