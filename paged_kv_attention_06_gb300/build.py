@@ -52,9 +52,22 @@ def _deps():
             [PYTHON_SRC, os.path.abspath(__file__)])
 
 
+def _python_built_for() -> str:
+    """The torch and Python that _pagedattn_calls.so is compiled against, in a file
+    beside it: their headers are not among the sources."""
+    import torch
+    return f"torch {torch.__version__}, {sys.implementation.cache_tag}"
+
+
 def up_to_date() -> bool:
     libs = (LIB, BENCH_LIB, PYTHON_LIB)
     if not all(os.path.exists(lib) for lib in libs):
+        return False
+    try:
+        with open(PYTHON_LIB + ".for") as f:
+            if f.read() != _python_built_for():
+                return False
+    except OSError:
         return False
     t = min(os.path.getmtime(lib) for lib in libs)
     return all(os.path.getmtime(p) <= t for p in _deps() + [BENCH_SRC])
@@ -134,6 +147,8 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
         sys.stderr.write(r.stdout + r.stderr)
         raise RuntimeError("linking _pagedattn_calls failed")
     os.replace(tmp, PYTHON_LIB)
+    with open(PYTHON_LIB + ".for", "w") as f:
+        f.write(_python_built_for())
     return LIB
 
 

@@ -82,3 +82,14 @@ def test_the_library_is_built_where_the_module_cannot_be(fake_build, what):
     fake_build.fails = "\0"
     fake_build.build.build()
     assert os.path.exists(fake_build.build.PYTHON_LIB) and fake_build.build.up_to_date()
+
+
+def test_another_torch_means_another_build(fake_build, monkeypatch):
+    import torch
+    fake_build.build.build()
+    assert fake_build.build.up_to_date()
+    n = len(fake_build.ran)
+    monkeypatch.setattr(torch, "__version__", "0.0.1")
+    assert not fake_build.build.up_to_date()
+    fake_build.build.build()
+    assert len(fake_build.ran) > n and fake_build.build.up_to_date()
