@@ -447,7 +447,9 @@ pa_status pa_attention(const void *query, const void *key_pages,
  * 16-byte aligned, any contents; calls that share one must not overlap on the
  * GPU. Other arguments and the errors as for pa_decode / pa_decode_fp8.
  * Up to 16 rows per request and KV head (G * L) take kernels of their own; more
- * take pa_decode's. Two kernels on `stream`.
+ * take pa_decode's. Two kernels on `stream`. The e4m3 form takes the query and the
+ * softmax weights in f16, as pa_decode_fp8 (query elements below 65504 in
+ * magnitude; below 2^-14 they keep fewer bits).
  */
 size_t pa_decode_window_workspace_bytes(pa_shape shape);
 pa_status pa_decode_window(const void *query, const void *key_pages, const void *value_pages,
@@ -500,7 +502,8 @@ pa_status pa_attention_window(const void *query, const void *key_pages, const vo
  * attends over the copies (k_scale in the softmax scale, v_scale in the output),
  * as pa_prefill_fp8 does for full attention. max_context_len bounds
  * context_lens; on the second route a longer entry records
- * PA_DEVERR_CONTEXT_LEN and is cut to the next multiple of 128.
+ * PA_DEVERR_CONTEXT_LEN and is cut to the next multiple of 128. On the first
+ * route the query is taken in f16, as pa_decode_fp8.
  *   workspace  pa_attention_window_fp8_workspace_bytes bytes (0: invalid
  *              sizes), 256-byte aligned, any contents.
  */
@@ -532,7 +535,7 @@ pa_status pa_attention_window_fp8(const void *query, const void *key_pages,
  *                    must not overlap on the GPU.
  * Pages shared by requests of one call must not be used here (two requests
  * would update one slot). Weights are summed in fp32, rows in order. Three
- * kernels on `stream`.
+ * kernels on `stream`. The e4m3 form takes the query in f16, as pa_decode_fp8.
  */
 size_t pa_decode_weights_workspace_bytes(pa_shape shape, int32_t max_context_len);
 pa_status pa_decode_weights(const void *query, const void *key_pages, const void *value_pages,
@@ -630,7 +633,11 @@ pa_status pa_kv_cache_release(pa_kv_cache *cache, int64_t seq_id);
  * reading the device. The pages may be handed out to work that follows on the
  * same stream. PA_ERR_INVALID_ARG (nothing changed) for an unknown seq_id,
  * another new_len, or one that ends inside a page given back by
- * pa_kv_cache_trim_window.
+ * pa_kv_cache_trim_window. Other pages given back behind the new length stay gone
+ * (table entries of -1), and the call does not know the window of the rows to come:
+ * a row whose window reaches into such a page reads the entry, which is recorded
+ * (PA_DEVERR_PAGE_ID). Where t tokens may be cut again (a draft that is not taken),
+ * trim for a window of at least the rows' window + t.
  */
 pa_status pa_kv_cache_truncate(pa_kv_cache *cache, int64_t seq_id, int32_t new_len);
 

@@ -815,7 +815,9 @@ class KVCache:
 
     def truncate(self, seq_id: int, new_len: int) -> None:
         """Cut a request to its first new_len tokens and free the pages behind
-        them (after pa_kv_evict in place: min(context length, keep))."""
+        them (after pa_kv_evict in place: min(context length, keep)). Pages that
+        trim_window freed stay free: where t tokens may be cut again, trim for a
+        window of at least the rows' window + t."""
         _check(_lib.pa_kv_cache_truncate(self._h, int(seq_id), int(new_len)),
                "pa_kv_cache_truncate")
 
