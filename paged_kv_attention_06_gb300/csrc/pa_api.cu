@@ -260,9 +260,6 @@ pa_status encode_out_map(CUtensorMap* map, void* base, uint64_t heads, uint64_t 
                      CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
-// Workspace the split prefill kernel needs for this shape on this device, or
-// 0 when the shape takes another prefill kernel (head_dim 64, pages of fewer
-// than 8 tokens, one query head per KV group, or shared memory too small).
 // (request, pair of query heads of one KV group, 128-row query tile) items of a
 // prefill: ceil(G / 2) pairs per group (an odd group's last pair repeats its
 // last head).
@@ -272,6 +269,9 @@ int64_t prefill_pair_items(const pa_shape& s)
     return int64_t(s.batch) * ((int64_t(s.q_len) + 127) / 128) * s.num_kv_heads * ((g + 1) / 2);
 }
 
+// Workspace the split prefill kernel needs for this shape on this device, or
+// 0 when the shape takes another prefill kernel (head_dim 64, pages of fewer
+// than 8 tokens, one query head per KV group, or shared memory too small).
 size_t split_prefill_need(const pa_shape& s, int32_t page_size, const DeviceInfo* dev)
 {
     if (s.head_dim != 128 || page_size < 8 || s.num_kv_heads <= 0 ||
@@ -1375,7 +1375,6 @@ pa_status run_decode_weights(const void* query, const void* key_pages, const voi
     a.weight_pages = weight_pages;
     a.block_table = block_table;
     a.context_lens = context_lens;
-    a.err = dev->err;
     a.score_stride = p.stride;
     a.B = shape.batch;
     a.H_kv = shape.num_kv_heads;

@@ -554,22 +554,22 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSM)
             }
             const bool edge = t0 + kTok - 1 > lim_min || t0 + kTok > end || (kMode == kWindow && t0 < low_max);
             if (busy) {
-            if (edge) {
+                if (edge) {
 #pragma unroll
-                for (int s = 0; s < kSub; ++s)
+                    for (int s = 0; s < kSub; ++s)
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
+                        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const int tok = t0 + 16 * s + g + 8 * (j >> 1);
-                            bool seen = tok < end && tok <= lim[nt][j & 1];
-                            if constexpr (kMode == kWindow)
-                                seen = seen && (tok < a.sinks || (!first_run && tok >= low[nt][j & 1]));
-                            if (!seen)
-                                sc[s][nt][j] = -INFINITY;
-                        }
-            }
-            if constexpr (kMode == kScores) {
+                            for (int j = 0; j < 4; ++j) {
+                                const int tok = t0 + 16 * s + g + 8 * (j >> 1);
+                                bool seen = tok < end && tok <= lim[nt][j & 1];
+                                if constexpr (kMode == kWindow)
+                                    seen = seen && (tok < a.sinks || (!first_run && tok >= low[nt][j & 1]));
+                                if (!seen)
+                                    sc[s][nt][j] = -INFINITY;
+                            }
+                }
+                if constexpr (kMode == kScores) {
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -585,146 +585,147 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSM)
                                 }
                             }
                         }
-            }
-            // ---- the maximum in use
-            float mx[NT][2];
-            bool moves = false;
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int rr = 0; rr < 2; ++rr) {
-                    float v = fmaxf(sc[0][nt][rr], sc[0][nt][2 + rr]);
-#pragma unroll
-                    for (int s = 1; s < kSub; ++s)
-                        v = fmaxf(v, fmaxf(sc[s][nt][rr], sc[s][nt][2 + rr]));
-                    mx[nt][rr] = v * c;
-                    moves |= mx[nt][rr] > m[nt][rr] + kMoveLog2 ||
-                             (m[nt][rr] == -INFINITY && mx[nt][rr] > -INFINITY);
                 }
-            if (__any_sync(0xffffffffu, moves)) {
+                // ---- the maximum in use
+                float mx[NT][2];
+                bool moves = false;
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int rr = 0; rr < 2; ++rr) {
-                        float v = mx[nt][rr];
+                        float v = fmaxf(sc[0][nt][rr], sc[0][nt][2 + rr]);
 #pragma unroll
-                        for (int off = 4; off < 32; off <<= 1)
-                            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, off));
-                        if (v > m[nt][rr]) {
-                            const float f = m[nt][rr] == -INFINITY ? 0.f : fast_exp2(m[nt][rr] - v);
-                            m[nt][rr] = v;
-                            l[nt][rr] *= f;
+                        for (int s = 1; s < kSub; ++s)
+                            v = fmaxf(v, fmaxf(sc[s][nt][rr], sc[s][nt][2 + rr]));
+                        mx[nt][rr] = v * c;
+                        moves |= mx[nt][rr] > m[nt][rr] + kMoveLog2 ||
+                                 (m[nt][rr] == -INFINITY && mx[nt][rr] > -INFINITY);
+                    }
+                if (__any_sync(0xffffffffu, moves)) {
 #pragma unroll
-                            for (int t = 0; t < kKS; ++t) {
-                                o[t][nt][rr] *= f;
-                                o[t][nt][2 + rr] *= f;
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int rr = 0; rr < 2; ++rr) {
+                            float v = mx[nt][rr];
+#pragma unroll
+                            for (int off = 4; off < 32; off <<= 1)
+                                v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, off));
+                            if (v > m[nt][rr]) {
+                                const float f = m[nt][rr] == -INFINITY ? 0.f : fast_exp2(m[nt][rr] - v);
+                                m[nt][rr] = v;
+                                l[nt][rr] *= f;
+#pragma unroll
+                                for (int t = 0; t < kKS; ++t) {
+                                    o[t][nt][rr] *= f;
+                                    o[t][nt][2 + rr] *= f;
+                                }
                             }
                         }
-                    }
-            }
-            // ---- P^T: two keys of one row a register, after the transpose
-            uint32_t ph[kSub][NT][2], pl[kSub][NT][2];
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                const float mu[2] = {m[nt][0] == -INFINITY ? 0.f : m[nt][0],
-                                     m[nt][1] == -INFINITY ? 0.f : m[nt][1]};
-#pragma unroll
-                for (int s = 0; s < kSub; ++s)
-#pragma unroll
-                    for (int hh = 0; hh < 2; ++hh) {
-                        const float p0v = fast_exp2(fmaf(sc[s][nt][2 * hh], c, -mu[0]));
-                        const float p1v = fast_exp2(fmaf(sc[s][nt][2 * hh + 1], c, -mu[1]));
-                        l[nt][0] += p0v;
-                        l[nt][1] += p1v;
-                        if constexpr (F8) {
-                            ph[s][nt][hh] = transpose8x8(pack_f16x2(p0v, p1v));
-                        } else {
-                            const uint32_t hi = pack_bf16x2(p0v, p1v);
-                            ph[s][nt][hh] = transpose8x8(hi);
-                            pl[s][nt][hh] = transpose8x8(pack_bf16x2(p0v - __uint_as_float(hi << 16),
-                                                                     p1v - __uint_as_float(hi & 0xffff0000u)));
-                        }
-                    }
-            }
-            // ---- O^T += V^T P^T; tile t of O^T holds the elements of D that the
-            // lanes' words give to it (out_element below)
-            mbar_wait_warp(&bars[stage * 2 + 1], phase, misc, a.err);
-#pragma unroll
-            for (int s = 0; s < kSub; ++s) {
-                uint4 vr[4][kVL];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const int r = 16 * s + 2 * q + (k & 1) + 8 * (k >> 1);
-#pragma unroll
-                    for (int i = 0; i < kVL; ++i)
-                        vr[k][i] = *reinterpret_cast<const uint4*>(vt + i * kHalfBytes + r * 128 + ((g ^ (r & swz)) << 4));
                 }
-                if (edge) {
-                    // Keys that no row sees: zeros, whatever the page holds (P is 0
-                    // there, but 0 * NaN is not).
+                // ---- P^T: two keys of one row a register, after the transpose
+                uint32_t ph[kSub][NT][2], pl[kSub][NT][2];
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    const float mu[2] = {m[nt][0] == -INFINITY ? 0.f : m[nt][0],
+                                         m[nt][1] == -INFINITY ? 0.f : m[nt][1]};
+#pragma unroll
+                    for (int s = 0; s < kSub; ++s)
+#pragma unroll
+                        for (int hh = 0; hh < 2; ++hh) {
+                            const float p0v = fast_exp2(fmaf(sc[s][nt][2 * hh], c, -mu[0]));
+                            const float p1v = fast_exp2(fmaf(sc[s][nt][2 * hh + 1], c, -mu[1]));
+                            l[nt][0] += p0v;
+                            l[nt][1] += p1v;
+                            if constexpr (F8) {
+                                ph[s][nt][hh] = transpose8x8(pack_f16x2(p0v, p1v));
+                            } else {
+                                const uint32_t hi = pack_bf16x2(p0v, p1v);
+                                ph[s][nt][hh] = transpose8x8(hi);
+                                pl[s][nt][hh] = transpose8x8(pack_bf16x2(p0v - __uint_as_float(hi << 16),
+                                                                         p1v - __uint_as_float(hi & 0xffff0000u)));
+                            }
+                        }
+                }
+                // ---- O^T += V^T P^T; tile t of O^T holds the elements of D that the
+                // lanes' words give to it (RowState::write has them in order)
+                mbar_wait_warp(&bars[stage * 2 + 1], phase, misc, a.err);
+#pragma unroll
+                for (int s = 0; s < kSub; ++s) {
+                    uint4 vr[4][kVL];
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        const int tok = t0 + 16 * s + 2 * q + (k & 1) + 8 * (k >> 1);
-                        if (tok >= end || (kMode == kWindow && tok >= a.sinks && tok < span.first_seen))
+                        const int r = 16 * s + 2 * q + (k & 1) + 8 * (k >> 1);
 #pragma unroll
-                            for (int i = 0; i < kVL; ++i)
-                                vr[k][i] = make_uint4(0, 0, 0, 0);
+                        for (int i = 0; i < kVL; ++i)
+                            vr[k][i] = *reinterpret_cast<const uint4*>(vt + i * kHalfBytes + r * 128 +
+                                                                       ((g ^ (r & swz)) << 4));
                     }
-                }
-                auto product = [&](int t, const uint32_t* A) {
+                    if (edge) {
+                        // Keys that no row sees: zeros, whatever the page holds (P is 0
+                        // there, but 0 * NaN is not).
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        if constexpr (F8) {
-                            mma_f16_16816(o[t][nt], A, ph[s][nt][0], ph[s][nt][1]);
-                        } else {
-                            mma_bf16_16816(o[t][nt], A, ph[s][nt][0], ph[s][nt][1]);
-                            mma_bf16_16816(o[t][nt], A, pl[s][nt][0], pl[s][nt][1]);
+                        for (int k = 0; k < 4; ++k) {
+                            const int tok = t0 + 16 * s + 2 * q + (k & 1) + 8 * (k >> 1);
+                            if (tok >= end || (kMode == kWindow && tok >= a.sinks && tok < span.first_seen))
+#pragma unroll
+                                for (int i = 0; i < kVL; ++i)
+                                    vr[k][i] = make_uint4(0, 0, 0, 0);
                         }
                     }
-                };
-                if constexpr (F8) {
-                    // word w: codes 4 w .. 4 w + 3 (rows g of tiles), w + 2: rows g + 8
+                    auto product = [&](int t, const uint32_t* A) {
 #pragma unroll
-                    for (int w = 0; w < 2; ++w) {
-                        uint32_t f[2][2][4];      // [keys 2 q / 2 q + 8][half][element of the word]
-#pragma unroll
-                        for (int kk = 0; kk < 2; ++kk)
-#pragma unroll
-                            for (int hh = 0; hh < 2; ++hh) {
-                                const uint32_t x0 = word(vr[2 * kk][0], w + 2 * hh);
-                                const uint32_t x1 = word(vr[2 * kk + 1][0], w + 2 * hh);
-                                const uint32_t e01 = __byte_perm(x0, x1, 0x5140);
-                                const uint32_t e23 = __byte_perm(x0, x1, 0x7362);
-                                f[kk][hh][0] = e4m3x2_to_f16x2(e01);
-                                f[kk][hh][1] = e4m3x2_hi_to_f16x2(e01);
-                                f[kk][hh][2] = e4m3x2_to_f16x2(e23);
-                                f[kk][hh][3] = e4m3x2_hi_to_f16x2(e23);
+                        for (int nt = 0; nt < NT; ++nt) {
+                            if constexpr (F8) {
+                                mma_f16_16816(o[t][nt], A, ph[s][nt][0], ph[s][nt][1]);
+                            } else {
+                                mma_bf16_16816(o[t][nt], A, ph[s][nt][0], ph[s][nt][1]);
+                                mma_bf16_16816(o[t][nt], A, pl[s][nt][0], pl[s][nt][1]);
                             }
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const uint32_t A[4] = {f[0][0][e], f[0][1][e], f[1][0][e], f[1][1][e]};
-                            product(4 * w + e, A);
                         }
-                    }
-                } else {
+                    };
+                    if constexpr (F8) {
+                        // word w: codes 4 w .. 4 w + 3 (rows g of tiles), w + 2: rows g + 8
 #pragma unroll
-                    for (int t = 0; t < kKS; ++t) {
-                        // elements e0 (rows g) and e1 (rows g + 8) of a lane's words
-                        constexpr bool kTwo = D == 128;
-                        const int e0 = t, e1 = kTwo ? t : t + 4;
-                        uint32_t A[4];
+                        for (int w = 0; w < 2; ++w) {
+                            uint32_t f[2][2][4];      // [keys 2 q / 2 q + 8][half][element of the word]
 #pragma unroll
-                        for (int kk = 0; kk < 2; ++kk) {
-                            A[2 * kk] = __byte_perm(word(vr[2 * kk][0], e0 >> 1), word(vr[2 * kk + 1][0], e0 >> 1),
-                                                    e0 & 1 ? 0x7632 : 0x5410);
-                            A[2 * kk + 1] =
-                                __byte_perm(word(vr[2 * kk][kTwo ? 1 : 0], e1 >> 1),
-                                            word(vr[2 * kk + 1][kTwo ? 1 : 0], e1 >> 1), e1 & 1 ? 0x7632 : 0x5410);
+                            for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+                                for (int hh = 0; hh < 2; ++hh) {
+                                    const uint32_t x0 = word(vr[2 * kk][0], w + 2 * hh);
+                                    const uint32_t x1 = word(vr[2 * kk + 1][0], w + 2 * hh);
+                                    const uint32_t e01 = __byte_perm(x0, x1, 0x5140);
+                                    const uint32_t e23 = __byte_perm(x0, x1, 0x7362);
+                                    f[kk][hh][0] = e4m3x2_to_f16x2(e01);
+                                    f[kk][hh][1] = e4m3x2_hi_to_f16x2(e01);
+                                    f[kk][hh][2] = e4m3x2_to_f16x2(e23);
+                                    f[kk][hh][3] = e4m3x2_hi_to_f16x2(e23);
+                                }
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const uint32_t A[4] = {f[0][0][e], f[0][1][e], f[1][0][e], f[1][1][e]};
+                                product(4 * w + e, A);
+                            }
                         }
-                        product(t, A);
+                    } else {
+#pragma unroll
+                        for (int t = 0; t < kKS; ++t) {
+                            // elements e0 (rows g) and e1 (rows g + 8) of a lane's words
+                            constexpr bool kTwo = D == 128;
+                            const int e0 = t, e1 = kTwo ? t : t + 4;
+                            uint32_t A[4];
+#pragma unroll
+                            for (int kk = 0; kk < 2; ++kk) {
+                                A[2 * kk] = __byte_perm(word(vr[2 * kk][0], e0 >> 1), word(vr[2 * kk + 1][0], e0 >> 1),
+                                                        e0 & 1 ? 0x7632 : 0x5410);
+                                A[2 * kk + 1] =
+                                    __byte_perm(word(vr[2 * kk][kTwo ? 1 : 0], e1 >> 1),
+                                                word(vr[2 * kk + 1][kTwo ? 1 : 0], e1 >> 1), e1 & 1 ? 0x7632 : 0x5410);
+                            }
+                            product(t, A);
+                        }
                     }
                 }
-            }
             } else {
                 mbar_wait_warp(&bars[stage * 2 + 1], phase, misc, a.err);   // nothing was copied
             }

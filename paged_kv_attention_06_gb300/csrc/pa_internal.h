@@ -157,7 +157,7 @@ struct DecodeArgs {
     int32_t MS;         // segments per (request, KV head): ceil(ceil(R / 16) / TG)
     int32_t TG;         // 16-row tiles per segment (1, 2 or 4); tile t of segment
                         // ms holds rows [16 (ms TG + t), 16 (ms TG + t) + 16) of R
-    int32_t box_rows;   // rows per TMA box: min(ps, 64)
+    int32_t box_rows;   // rows per TMA box: min(ps, 64); the few-row kernel min(ps, its tile of 16 or 32)
     int32_t swz;        // 7: 128B-swizzled stage layout (box_rows >= 8); 0: linear
     int32_t whole_segments;  // 1: every block takes whole segments (no partials)
     int32_t piece_units;     // split weight of a piece beyond its granules (set by
@@ -208,7 +208,6 @@ struct WeightArgs {
     float* weight_pages;          // [P, H_kv, ps]
     const int32_t* block_table;
     const int32_t* context_lens;
-    unsigned* err;
     int64_t score_stride;
     int32_t B, H_kv, R, L, ps_shift, max_pages, num_pages, score_cap;
     int32_t chunks;               // set by the launcher: blocks per (request, KV head)
@@ -251,22 +250,25 @@ struct PrefillArgs {
     int32_t window, sinks;
 };
 
-// Prefill over e4m3 pools: bf16 copies of the visible K/V tokens, in pages
-// of 128 tokens; copy page b * P2 + p holds tokens [128 p, 128 p + 128) of
-// request b.
+// Prefill over e4m3 pools: bf16 copies of the K/V tokens that some row sees, in
+// pages of 128 tokens, P1 a request, and a table of P2 entries a request that leads
+// to them: entry p is the copy page of tokens [128 p, 128 p + 128). Without a window
+// P1 = P2 and entry p of request b is b * P2 + p. With one, copy page b * P1 + i is
+// that of the sinks' i-th 128 tokens, and behind the sinks' pages of the i-th from
+// the first token on that some row sees through the window; entries of tokens
+// that no row sees are not written.
 struct Fp8PagesArgs {
     const uint8_t* key_pages;     // [P, H_kv, ps, 128] e4m3 codes
     const uint8_t* value_pages;
     const int32_t* block_table;   // [B, max_pages]
     const int32_t* context_lens;  // [B]
-    uint16_t* key_out;            // [B * P2, H_kv, 128, 128] bf16
+    uint16_t* key_out;            // [B * P1, H_kv, 128, 128] bf16
     uint16_t* value_out;
-    int32_t* table_out;           // [B, P2]: b * P2 + p
+    int32_t* table_out;           // [B, P2]
     unsigned* err;
     int32_t B, H_kv, ps, max_pages, num_pages;
-    int32_t P2;                   // table entries per request: ceil(max_context_len / 128)
-    // A sliding window (0: none) over rows of length L: only the tokens that
-    // some row sees are copied, P1 copy pages per request (P2 without a window).
+    int32_t P2;                   // ceil(max_context_len / 128)
+    // A sliding window (0: none, and P1 is not read) over L query rows.
     int32_t window, sinks, L;
     int32_t P1;
 };
