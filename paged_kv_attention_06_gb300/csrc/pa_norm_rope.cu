@@ -22,14 +22,16 @@
 // group of lanes takes U heads of one kind of one token: all loads are issued
 // before the first is used, and the products of weights and angles are made once
 // for the U heads, two elements to an instruction. Measured (one call of a
-// replayed graph): 8188 tokens of 32 + 2 x 8 heads of 128, 204.6 MB, 34.8 us (5.9
-// TB/s, of 6.8 for a copy; 62.8 before the pairs of one lane), e4m3 pools 42 us;
-// one token 2.1 us. What is left is the latency of a block's loads.
+// replayed graph): 8188 tokens of 32 + 2 x 8 heads of 128, 204.6 MB, 35 us (5.8
+// TB/s, of 6.8 for a copy), e4m3 pools 42 us (188.7 MB, 4.5 TB/s: presumably the division
+// and the narrow stores of the codes); one token 2.0 us. What is left is the
+// latency of a block's loads.
 //
-// Loads and bf16 stores are marked as streamed (evict first), both or neither: 38.7
-// us without, 38.8 with the stores' alone, 40 with the loads' alone. The attention that
-// follows does not pay for it: qkv written, appended and attended to (window 1024),
-// 8188 tokens 178 us against 181, 4094 tokens 97 against 98, 1024 tokens 33.4 both.
+// Loads and bf16 stores are marked as streamed (evict first): 39.2 us without. Marking
+// one side alone gained nothing when it was measured (38.7 us without, 38.8 with the
+// stores' alone, 40 with the loads' alone, 34.7 with both). The attention that follows does not
+// pay for it: qkv written, appended and attended to (window 1024), 8188 tokens 178 us
+// against 181, 4094 tokens 97 against 98, 1024 tokens 33.4 both.
 #include <stdint.h>
 
 #include "pa_device.cuh"
@@ -38,7 +40,8 @@
 namespace pa {
 namespace {
 
-constexpr int kThreads = 128;      // 64: 38.6 us, but 64 e4m3 tokens 2.7 against 2.5
+// 8188 tokens 35.1 us, e4m3 pools 42.3; 256 threads 35.9 and 48.4, 64 threads 35.3 us.
+constexpr int kThreads = 128;
 
 // Four bf16 -> two fp32 pairs, and back.
 __device__ __forceinline__ void unpack4(uint2 v, float2* x)
@@ -50,25 +53,11 @@ __device__ __forceinline__ uint2 pack4(const float2* x)
 {
     return make_uint2(pack_bf16x2(x[0].x, x[0].y), pack_bf16x2(x[1].x, x[1].y));
 }
-// The e4m3 codes of four quotients x / scale (each rounded to fp32 first).
-// x * recip (recip = 1 / scale) is within 3 * 2^-24 of the quotient: where the
-// numbers 2^-21 below and above it have the same codes, so has the quotient,
-// and the division is not needed (8188 tokens, 256 threads a block:
-// 51.2 us, 53.2 with it for every code). recip = 0: always divide.
-__device__ __forceinline__ uint32_t quantise4(const float2* x, float scale, float recip)
+// The e4m3 codes of four quotients x / scale, each rounded to fp32 first. (A product
+// with 1 / scale, and the division only where the code could differ, is slower with
+// 128 threads a block: 8188 tokens 43.7 us, 42.3 with the division alone.)
+__device__ __forceinline__ uint32_t quantise4(const float2* x, float scale)
 {
-    if (recip != 0.f) {
-        const float2 r = make_float2(recip, recip);
-        const float2 q0 = __fmul2_rn(x[0], r), q1 = __fmul2_rn(x[1], r);
-        const float2 dn = make_float2(1.f - 0x1p-21f, 1.f - 0x1p-21f);
-        const float2 up = make_float2(1.f + 0x1p-21f, 1.f + 0x1p-21f);
-        const float2 d0 = __fmul2_rn(q0, dn), d1 = __fmul2_rn(q1, dn);
-        const float2 u0 = __fmul2_rn(q0, up), u1 = __fmul2_rn(q1, up);
-        const uint32_t lo = f32x2_to_e4m3x2(d0.x, d0.y) | (f32x2_to_e4m3x2(d1.x, d1.y) << 16);
-        const uint32_t hi = f32x2_to_e4m3x2(u0.x, u0.y) | (f32x2_to_e4m3x2(u1.x, u1.y) << 16);
-        if (lo == hi)
-            return lo;
-    }
     return f32x2_to_e4m3x2(__fdiv_rn(x[0].x, scale), __fdiv_rn(x[0].y, scale)) |
            (f32x2_to_e4m3x2(__fdiv_rn(x[1].x, scale), __fdiv_rn(x[1].y, scale)) << 16);
 }
@@ -180,8 +169,6 @@ __global__ void __launch_bounds__(kThreads) norm_rope_append_kernel(const NormRo
     }
     const bool quantised = kF8 && kind > 0;
     const float scale = kind == 1 ? a.k_scale : a.v_scale;
-    // (scales far out, where 1 / scale is not a normal number, divide)
-    const float recip = quantised && scale > 0x1p-100f && scale < 0x1p100f ? __fdiv_rn(1.f, scale) : 0.f;
     const bool normed = __any_sync(0xffffffffu, w != nullptr);
 
 #pragma unroll
@@ -224,8 +211,8 @@ __global__ void __launch_bounds__(kThreads) norm_rope_append_kernel(const NormRo
         }
         if (quantised) {
             uint8_t* row = reinterpret_cast<uint8_t*>(to) + at + u * head_step;
-            *reinterpret_cast<uint32_t*>(row + e0) = quantise4(x, scale, recip);
-            *reinterpret_cast<uint32_t*>(row + e1) = quantise4(x + 2, scale, recip);
+            *reinterpret_cast<uint32_t*>(row + e0) = quantise4(x, scale);
+            *reinterpret_cast<uint32_t*>(row + e1) = quantise4(x + 2, scale);
         } else {
             uint16_t* row = to + at + u * head_step;
             __stcs(reinterpret_cast<uint2*>(row + e0), out[0]);
@@ -255,7 +242,7 @@ cudaError_t launch_norm_rope_append(NormRopeArgs a, cudaStream_t stream)
     const int64_t tokens = int64_t(a.B) * a.L;
     const int lanes = a.D / 8;
     // One head per group while that still leaves the GPU short of threads. Four
-    // otherwise: 8188 tokens 39.8 us, 48.7 with two, 41.5 with six, 40.4 with eight.
+    // otherwise: 8188 tokens 35.1 us, 43.3 with two, 37.3 with six, 35.6 with eight.
     const bool few = tokens * H * lanes < int64_t(256) * 1024;
     const int U = few ? 1 : kHeads;
     a.q_groups = (a.H_q + U - 1) / U;
