@@ -34,9 +34,9 @@
 //     in their order.
 //
 // Bound by memory: every K and V byte that a row sees is read once. Measured (one
-// call of a replayed graph): 64 bf16 requests, window 2048, 510 MB in 82 us
-// (6.2 TB/s, of 6.8 measured for a copy); e4m3, 255 MB in 49 us; 32 requests of
-// a window of 1024 in groups of 7, 51 MB in 16 us; one request, window 512, 8.4
+// call of a replayed graph): 64 bf16 requests, window 2048, 508 MB in 85 us
+// (6.0 TB/s, of 6.8 measured for a copy); e4m3, 255 MB in 49 us; 32 requests of
+// a window of 1024 in groups of 7, 51 MB in 16 us; one request, window 512, 8.2
 // us, of which the second kernel is about 3.
 #include <cuda.h>
 #include <cuda_bf16.h>

@@ -22,8 +22,9 @@
 //
 // The move is bound by memory (each kept row read and written once), the choice
 // by the latency of its passes. Measured (one call of a replayed graph): 8
-// requests of 16k-32k tokens to 8192 per head, 549 MB, 113 us (122 in place); with
-// 16 rows kept, nearly the choice alone, 23 us; one request of 1280 to 1024, 8.8.
+// requests of 16k-32k tokens to 8192 per head, 549 MB, 114 us (131 in place; e4m3 pools,
+// 281 MB, 73 and 108); with 16 rows kept, nearly the choice alone, 23 us; one request of
+// 1280 to 1024, 8.6.
 #include <cooperative_groups.h>
 #include <math.h>
 #include <stdint.h>
@@ -417,8 +418,9 @@ __device__ __forceinline__ void move_rows(const EvictArgs& a, T* pool, int64_t r
 
 // Blocks of a (request, KV head): a column slice of K or of V, or the weights. In
 // place the slices are narrow, since a block takes all rows and only the slices
-// spread the work (8192 rows of 64 heads: 122 us with 64 bytes, 154 with 128);
-// where the order is free they are whole rows (113 us, 124 with 64 bytes).
+// spread the work (8192 rows of 64 heads: 131 us with 64 bytes, 159 with 128, 152 with
+// 32; e4m3 rows of 128 bytes 108, 150 and 91); where the order is free they are whole
+// rows (113 us, 124 with 64 bytes).
 template <MoveKind kKind, int kSlice>
 __global__ void __launch_bounds__(kMoveThreads, 4) evict_move_kernel(const EvictArgs a)
 {
