@@ -595,6 +595,81 @@ pa_status pa_kv_evict_fp8(void *key_pages, void *value_pages, float *weight_page
                           int32_t *kept, int32_t *new_lens, pa_shape shape, void *stream);
 
 /*
+ * 4-bit page pools, with a step of their own for every 32 elements of a row (Reading
+ * vLLM's PagedAttention Kernel, 3.2: the write path takes the cache dtype; here the
+ * scales follow the data, so none are passed). head_dim 128 only. A pool is
+ * [P, H_kv, page_size, 80] bytes; a row's first 64 bytes are its codes (element d in
+ * byte d / 2, even d in the low half), then for each group of 32 elements its step s and
+ * its least value m as f16: s0 m0 s1 m1 s2 m2 s3 m3. A code c stands for m + s c.
+ */
+
+/*
+ * pa_append_kv for 4-bit pools. Of each group of 32 elements of a new row:
+ *   y = f16(min(max(x, -448), 448)),  m = min y,  s = f16(fp32(max y - m) / 15),
+ *   code = the integer nearest to (y - m) / s, ties to even, at most 15 (0 where s
+ *   is 0). A NaN makes its group's m and s NaN.
+ * Same slots, checks and error reporting as pa_append_kv.
+ */
+pa_status pa_append_kv_q4(const void *key, const void *value, void *key_pages, void *value_pages,
+                          const int32_t *slot_mapping, int32_t page_size, pa_shape shape,
+                          void *stream);
+
+/*
+ * pa_gather_kv from 4-bit pools: every request's rows as the bf16 nearest to m + s c
+ * (fp32 first) in key_dense, value_dense [B, H_kv, dense_len, 128]. The same table,
+ * checks and errors; one kernel on `stream`.
+ */
+pa_status pa_gather_kv_q4(const void *key_pages, const void *value_pages,
+                          const int32_t *block_table, const int32_t *context_lens,
+                          int32_t page_size, pa_shape shape, int32_t dense_len, void *key_dense,
+                          void *value_dense, void *stream);
+
+/*
+ * pa_decode over 4-bit pools, straight from the codes: s c is rounded to f16 (and s / 16
+ * too, for the codes in the high halves, which shows where s is below 2^-10), m is added
+ * in the products' fp32 sums. The query and the softmax weights are taken in f16 (query
+ * elements below 65504 in magnitude; below 2^-14 they keep fewer bits). A group whose m
+ * and s are NaN gives NaN in a visible slot; slots past a request's context are never
+ * read. Any L; K and V are read once per 16 rows (G * L) of a request and KV head.
+ *   workspace  pa_decode_q4_workspace_bytes(shape) bytes (0: invalid or unsupported
+ *              shape), 16-byte aligned, any contents; calls that share one must
+ *              not overlap on the GPU.
+ * Other arguments and errors as for pa_decode. Two kernels on `stream`.
+ */
+size_t pa_decode_q4_workspace_bytes(pa_shape shape);
+pa_status pa_decode_q4(const void *query, const void *key_pages, const void *value_pages,
+                       const int32_t *block_table, const int32_t *context_lens, int32_t page_size,
+                       float scale, int causal, void *out, pa_shape shape, int32_t max_context_len,
+                       void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Prefill over 4-bit pools, as pa_prefill_fp8: the tokens that the requests have cached
+ * are copied into bf16 pages of 128 tokens in the workspace (m + s c rounded to bf16),
+ * and pa_attention's prefill kernels attend over the copies. max_context_len bounds
+ * context_lens; a longer entry records PA_DEVERR_CONTEXT_LEN and is cut to the next
+ * multiple of 128. workspace: pa_prefill_q4_workspace_bytes bytes (0: invalid sizes),
+ * 256-byte aligned, any contents; calls that share one must not overlap on the GPU.
+ */
+size_t pa_prefill_q4_workspace_bytes(pa_shape shape, int32_t max_context_len);
+pa_status pa_prefill_q4(const void *query, const void *key_pages, const void *value_pages,
+                        const int32_t *block_table, const int32_t *context_lens, int32_t page_size,
+                        float scale, int causal, void *out, pa_shape shape,
+                        int32_t max_context_len, void *workspace, size_t workspace_bytes,
+                        void *stream);
+
+/*
+ * The dispatch of the two: pa_decode_q4 for L <= 8, pa_prefill_q4 otherwise, with the
+ * same arguments. workspace: the one that call takes, at least
+ * pa_attention_q4_workspace_bytes bytes (0: invalid sizes), 256-byte aligned.
+ */
+size_t pa_attention_q4_workspace_bytes(pa_shape shape, int32_t max_context_len);
+pa_status pa_attention_q4(const void *query, const void *key_pages, const void *value_pages,
+                          const int32_t *block_table, const int32_t *context_lens,
+                          int32_t page_size, float scale, int causal, void *out, pa_shape shape,
+                          int32_t max_context_len, void *workspace, size_t workspace_bytes,
+                          void *stream);
+
+/*
  * Synchronises `stream`, then reads and clears the device error word of the
  * current device. *flags (may be NULL) receives the PA_DEVERR_* bits seen
  * since the last call. Returns PA_OK when no bit was set,

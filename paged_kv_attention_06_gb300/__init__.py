@@ -18,7 +18,10 @@ _API = ("pa_append_kv", "pa_decode", "pa_prefill", "pa_attention", "pa_attention
         "pa_kv_evict", "pa_kv_evict_fp8", "pa_decode_window", "pa_decode_window_fp8",
         "pa_decode_window_workspace_bytes", "pa_prefill_window", "pa_attention_window", "pa_attention_window_fp8",
         "pa_attention_window_workspace_bytes", "pa_attention_window_fp8_workspace_bytes",
-        "pa_decode_weights", "pa_decode_weights_fp8", "pa_decode_weights_workspace_bytes")
+        "pa_decode_weights", "pa_decode_weights_fp8", "pa_decode_weights_workspace_bytes",
+        "pa_append_kv_q4", "pa_gather_kv_q4", "pa_decode_q4", "pa_prefill_q4", "pa_attention_q4",
+        "pa_decode_q4_workspace_bytes", "pa_prefill_q4_workspace_bytes",
+        "pa_attention_q4_workspace_bytes")
 
 
 def __getattr__(name):

@@ -136,6 +136,11 @@ def _load() -> ctypes.CDLL:
         f.restype = sz
     lib.pa_decode_weights_workspace_bytes.argtypes = [pa_shape, i32]
     lib.pa_decode_weights_workspace_bytes.restype = sz
+    lib.pa_decode_q4_workspace_bytes.argtypes = [pa_shape]
+    lib.pa_decode_q4_workspace_bytes.restype = sz
+    for f in (lib.pa_prefill_q4_workspace_bytes, lib.pa_attention_q4_workspace_bytes):
+        f.argtypes = [pa_shape, i32]
+        f.restype = sz
     lib.pa_debug_arm_wait_timeout.argtypes = []
     lib.pa_debug_arm_wait_timeout.restype = None
     lib.pa_debug_prefill_variant.argtypes = [ctypes.c_int]
@@ -470,6 +475,79 @@ def pa_decode_weights_fp8(query, key_pages, value_pages, weight_pages, block_tab
     return _calls.weights(query, key_pages, value_pages, weight_pages, block_table, context_lens,
                           page_size, k_scale, v_scale, max_context_len, decay, scale, causal, out,
                           workspace, _raw(stream))
+
+
+def pa_append_kv_q4(key: torch.Tensor, value: torch.Tensor, key_pages: torch.Tensor,
+                    value_pages: torch.Tensor, slot_mapping: torch.Tensor, page_size: int,
+                    stream=None) -> None:
+    """key/value [B, H_kv, L_new, 128] bf16 -> uint8 4-bit pages [P, H_kv,
+    page_size, 80] at slot_mapping [B, L_new]: codes of 4 bits, and a step and a
+    least value as f16 for every 32 elements."""
+    _calls.append_q4(key, value, key_pages, value_pages, slot_mapping, page_size, _raw(stream))
+
+
+def pa_gather_kv_q4(key_pages: torch.Tensor, value_pages: torch.Tensor, block_table: torch.Tensor,
+                    context_lens: torch.Tensor, page_size: int, dense_len: int,
+                    key_dense: Optional[torch.Tensor] = None,
+                    value_dense: Optional[torch.Tensor] = None,
+                    stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """What the requests have cached in 4-bit pages, as bf16 [B, H_kv, dense_len,
+    128]; rows at or past a request's context are not written. Returns (key_dense,
+    value_dense)."""
+    return _calls.gather_q4(key_pages, value_pages, block_table, context_lens, page_size, dense_len,
+                            key_dense, value_dense, _raw(stream))
+
+
+def pa_decode_q4_workspace_bytes(shape: pa_shape, device: Optional[torch.device] = None) -> int:
+    with torch.cuda.device(device if device is not None else torch.cuda.current_device()):
+        return int(_lib.pa_decode_q4_workspace_bytes(shape))
+
+
+def pa_prefill_q4_workspace_bytes(shape: pa_shape, max_context_len: int,
+                                  device: Optional[torch.device] = None) -> int:
+    with torch.cuda.device(device if device is not None else torch.cuda.current_device()):
+        return int(_lib.pa_prefill_q4_workspace_bytes(shape, int(max_context_len)))
+
+
+def pa_attention_q4_workspace_bytes(shape: pa_shape, max_context_len: int,
+                                    device: Optional[torch.device] = None) -> int:
+    with torch.cuda.device(device if device is not None else torch.cuda.current_device()):
+        return int(_lib.pa_attention_q4_workspace_bytes(shape, int(max_context_len)))
+
+
+def pa_decode_q4(query: torch.Tensor, key_pages: torch.Tensor, value_pages: torch.Tensor,
+                 block_table: torch.Tensor, context_lens: torch.Tensor, page_size: int,
+                 scale: Optional[float] = None, causal: bool = True,
+                 out: Optional[torch.Tensor] = None, max_context_len: int = 0,
+                 workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """pa_decode over uint8 4-bit pools [P, H_kv, page_size, 80]."""
+    return _calls.attention_q4(0, query, key_pages, value_pages, block_table, context_lens, page_size,
+                               scale, causal, out, max_context_len, workspace, _raw(stream))
+
+
+def pa_prefill_q4(query, key_pages, value_pages, block_table, context_lens, page_size: int,
+                  scale: Optional[float] = None, causal: bool = True, out=None,
+                  max_context_len: Optional[int] = None,
+                  workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Tensor-core prefill over uint8 4-bit pools. max_context_len bounds
+    context_lens and sizes the bf16 copy in the workspace; None reads
+    context_lens.max() (a device-to-host copy)."""
+    if max_context_len is None:
+        max_context_len = int(context_lens.max().item())
+    return _calls.attention_q4(1, query, key_pages, value_pages, block_table, context_lens, page_size,
+                               scale, causal, out, max_context_len, workspace, _raw(stream))
+
+
+def pa_attention_q4(query, key_pages, value_pages, block_table, context_lens, page_size: int,
+                    scale: Optional[float] = None, causal: bool = True, out=None,
+                    max_context_len: Optional[int] = None,
+                    workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """The dispatch for 4-bit pools: pa_decode_q4 for short queries,
+    pa_prefill_q4 beyond. max_context_len as for pa_prefill_q4."""
+    if max_context_len is None:
+        max_context_len = int(context_lens.max().item())
+    return _calls.attention_q4(2, query, key_pages, value_pages, block_table, context_lens, page_size,
+                               scale, causal, out, max_context_len, workspace, _raw(stream))
 
 
 def pa_decode_fp8(query, key_pages, value_pages, block_table, context_lens, page_size: int,

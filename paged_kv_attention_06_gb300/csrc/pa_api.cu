@@ -612,7 +612,8 @@ pa_status run_split_kv(const void* query, const void* key_pages, const void* val
     DecodeArgs a;
     memset(&a, 0, sizeof a);
     if (rows) {
-        if (!workspace || workspace_bytes < decode_rows_workspace_bytes(s, dev->sm_count) ||
+        if (!workspace ||
+            workspace_bytes < decode_rows_workspace_bytes(s, fp8 ? kE4m3Pool : kBf16Pool, extra.mode, dev->sm_count) ||
             (reinterpret_cast<uintptr_t>(workspace) & 15u))
             return PA_ERR_WORKSPACE;
     } else if (!whole_segments) {
@@ -657,15 +658,16 @@ pa_status run_split_kv(const void* query, const void* key_pages, const void* val
     a.score_cap = extra.score_cap;
     if (rows) {
         CUtensorMap kmap, vmap;
-        a.box_rows = decode_rows_box(s, fp8 != 0, page_size);
+        const int kind = fp8 ? kE4m3Pool : kBf16Pool;
+        a.box_rows = decode_rows_box(s, kind, page_size);
         a.swz = a.box_rows >= 8 ? 7 : 0;
         if ((st = encode_pool_map(&kmap, key_pages, s, page_size, fp8 != 0, a.box_rows)) != PA_OK ||
             (st = encode_pool_map(&vmap, value_pages, s, page_size, fp8 != 0, a.box_rows)) != PA_OK)
             return st;
         while ((1 << a.ps_shift) < page_size)
             ++a.ps_shift;
-        return launch_decode_rows(kmap, vmap, a, s, max_context_len > 0 ? granules : 0, workspace, dev->id,
-                                  dev->sm_count, stream) == cudaSuccess
+        const int rows_grid = decode_rows_launch_grid(s, kind, max_context_len > 0 ? granules : 0, dev->sm_count);
+        return launch_decode_rows(kmap, vmap, a, s, kind, rows_grid, workspace, dev->id, stream) == cudaSuccess
                    ? PA_OK
                    : PA_ERR_CUDA;
     }
@@ -1403,8 +1405,9 @@ size_t pa_decode_window_workspace_bytes(pa_shape shape)
     DeviceInfo* dev;
     if (many == 0 || device_info(&dev) != PA_OK)
         return 0;
-    return decode_rows_takes(shape, dev->max_smem_optin) ? decode_rows_workspace_bytes(shape, dev->sm_count)
-                                                         : many;
+    return decode_rows_takes(shape, dev->max_smem_optin)
+               ? decode_rows_workspace_bytes(shape, kBf16Pool, kWindow, dev->sm_count)
+               : many;
 }
 
 pa_status pa_decode_window(const void* query, const void* key_pages, const void* value_pages,
@@ -1658,6 +1661,295 @@ pa_status pa_gather_kv(const void* key_pages, const void* value_pages, const int
     a.dense_len = dense_len;
     return launch_gather(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? PA_OK
                                                                                : PA_ERR_CUDA;
+}
+
+namespace {
+
+// Checks of a read-back's sizes.
+pa_status check_q4_pools(const pa_shape& s, int32_t page_size)
+{
+    if (s.batch <= 0 || s.num_kv_heads <= 0 || s.num_pages <= 0 || s.max_pages <= 0 || s.head_dim <= 0)
+        return PA_ERR_INVALID_ARG;
+    if (s.head_dim != 128 || !pow2_in(page_size, 1, 256))
+        return PA_ERR_UNSUPPORTED;
+    if (int64_t(s.num_pages) * s.num_kv_heads * page_size >= (int64_t(1) << 31) ||
+        int64_t(s.max_pages) * page_size >= (int64_t(1) << 30))
+        return PA_ERR_UNSUPPORTED;
+    return PA_OK;
+}
+
+Q4ReadArgs q4_read_args(const void* key_pages, const void* value_pages, const int32_t* block_table,
+                        const int32_t* context_lens, int32_t page_size, const pa_shape& s,
+                        const DeviceInfo* dev)
+{
+    Q4ReadArgs a;
+    memset(&a, 0, sizeof a);
+    a.key_pages = static_cast<const uint8_t*>(key_pages);
+    a.value_pages = static_cast<const uint8_t*>(value_pages);
+    a.block_table = block_table;
+    a.context_lens = context_lens;
+    a.err = dev->err;
+    a.B = s.batch;
+    a.H_kv = s.num_kv_heads;
+    a.ps = page_size;
+    a.num_pages = s.num_pages;
+    a.max_pages = s.max_pages;
+    return a;
+}
+
+}  // namespace
+
+pa_status pa_append_kv_q4(const void* key, const void* value, void* key_pages, void* value_pages,
+                          const int32_t* slot_mapping, int32_t page_size, pa_shape shape,
+                          void* stream)
+{
+    if (!key || !value || !key_pages || !value_pages || !slot_mapping)
+        return PA_ERR_INVALID_ARG;
+    if (shape.batch <= 0 || shape.num_kv_heads <= 0 || shape.q_len < 0 || shape.num_pages <= 0 ||
+        shape.head_dim <= 0)
+        return PA_ERR_INVALID_ARG;
+    if (!aligned16(key) || !aligned16(value) || !aligned16(key_pages) || !aligned16(value_pages))
+        return PA_ERR_INVALID_ARG;
+    if (shape.head_dim != 128 || !pow2_in(page_size, 1, 256))
+        return PA_ERR_UNSUPPORTED;
+    if (int64_t(shape.num_pages) * shape.num_kv_heads * page_size >= (int64_t(1) << 31) ||
+        int64_t(shape.batch) * shape.q_len * shape.num_kv_heads >= (int64_t(1) << 35))
+        return PA_ERR_UNSUPPORTED;
+    DeviceInfo* dev;
+    pa_status st = device_info(&dev);
+    if (st != PA_OK)
+        return st;
+    if (shape.q_len == 0)
+        return PA_OK;
+    AppendArgs a;
+    memset(&a, 0, sizeof a);
+    a.key = static_cast<const uint16_t*>(key);
+    a.value = static_cast<const uint16_t*>(value);
+    a.key_pages = static_cast<uint16_t*>(key_pages);     // byte pages; the kernel casts back
+    a.value_pages = static_cast<uint16_t*>(value_pages);
+    a.slot_mapping = slot_mapping;
+    a.err = dev->err;
+    a.B = shape.batch;
+    a.L_new = shape.q_len;
+    a.H_kv = shape.num_kv_heads;
+    a.D = 128;
+    a.ps = page_size;
+    a.num_pages = shape.num_pages;
+    return launch_append_q4(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? PA_OK
+                                                                                  : PA_ERR_CUDA;
+}
+
+pa_status pa_gather_kv_q4(const void* key_pages, const void* value_pages,
+                          const int32_t* block_table, const int32_t* context_lens,
+                          int32_t page_size, pa_shape shape, int32_t dense_len, void* key_dense,
+                          void* value_dense, void* stream)
+{
+    if (!key_pages || !value_pages || !block_table || !context_lens || !key_dense || !value_dense ||
+        dense_len <= 0)
+        return PA_ERR_INVALID_ARG;
+    if (!aligned16(key_pages) || !aligned16(value_pages) || !aligned16(key_dense) ||
+        !aligned16(value_dense))
+        return PA_ERR_INVALID_ARG;
+    pa_status st = check_q4_pools(shape, page_size);
+    if (st != PA_OK)
+        return st;
+    if (int64_t(shape.batch) * shape.num_kv_heads * ((int64_t(dense_len) + 63) / 64) >=
+        (int64_t(1) << 31))
+        return PA_ERR_UNSUPPORTED;
+    DeviceInfo* dev;
+    if ((st = device_info(&dev)) != PA_OK)
+        return st;
+    Q4ReadArgs a = q4_read_args(key_pages, value_pages, block_table, context_lens, page_size, shape, dev);
+    a.key_out = static_cast<uint16_t*>(key_dense);
+    a.value_out = static_cast<uint16_t*>(value_dense);
+    a.head_stride = int64_t(dense_len) * 128;
+    a.batch_stride = a.head_stride * shape.num_kv_heads;
+    a.block_stride = int64_t(kQ4CopyRows) * 128;
+    a.max_len = dense_len;
+    return launch_read_q4(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+namespace {
+
+// The bf16 copies of what the requests have cached in a 4-bit pool, with their table,
+// at the front of a workspace laid out by plan_prefill_fp8.
+pa_status copy_q4(const void* key_pages, const void* value_pages, const int32_t* block_table,
+                  const int32_t* context_lens, int32_t page_size, const pa_shape& s,
+                  const Fp8PrefillPlan& p, const DeviceInfo* dev, uint8_t* w, cudaStream_t stream)
+{
+    Q4ReadArgs a = q4_read_args(key_pages, value_pages, block_table, context_lens, page_size, s, dev);
+    a.key_out = reinterpret_cast<uint16_t*>(w);
+    a.value_out = reinterpret_cast<uint16_t*>(w + p.kv_bytes);
+    a.table_out = reinterpret_cast<int32_t*>(w + p.table_off);
+    a.head_stride = int64_t(kQ4CopyRows) * 128;
+    a.block_stride = a.head_stride * s.num_kv_heads;
+    a.batch_stride = a.block_stride * p.P2;
+    a.max_len = int32_t(p.P2 * kQ4CopyRows);
+    a.copy_pages = int32_t(p.P2);
+    return launch_read_q4(a, stream) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+}  // namespace
+
+namespace {
+
+// What the few-row kernel takes of a call (no tensor maps, no outputs of its modes).
+DecodeArgs rows_args(const void* query, const int32_t* block_table, const int32_t* context_lens,
+                     int32_t page_size, float scale, int causal, void* out, const pa_shape& s, int kind,
+                     DecodeMode mode, const DeviceInfo* dev)
+{
+    DecodeArgs a;
+    memset(&a, 0, sizeof a);
+    a.q = static_cast<const uint16_t*>(query);
+    a.out = static_cast<uint16_t*>(out);
+    a.block_table = block_table;
+    a.context_lens = context_lens;
+    a.err = dev->err;
+    a.B = s.batch;
+    a.H_q = s.num_q_heads;
+    a.H_kv = s.num_kv_heads;
+    a.L = s.q_len;
+    a.D = s.head_dim;
+    a.ps = page_size;
+    a.max_pages = s.max_pages;
+    a.num_pages = s.num_pages;
+    a.G = s.num_q_heads / s.num_kv_heads;
+    a.R = a.G * s.q_len;
+    a.box_rows = decode_rows_box(s, kind, page_size);
+    a.swz = a.box_rows >= 8 ? 7 : 0;
+    while ((1 << a.ps_shift) < page_size)
+        ++a.ps_shift;
+    a.scale_log2 = scale * 1.4426950408889634f;
+    a.causal = causal ? 1 : 0;
+    a.fp8 = kind == kE4m3Pool ? 1 : 0;
+    a.v_scale = 1.f;
+    a.mode = mode;
+    return a;
+}
+
+// Tiles of keys by four, at most, of all segments of the few-row kernel.
+int64_t rows_granules(const pa_shape& s, int kind, int64_t keys)
+{
+    const int64_t MS = (int64_t(s.num_q_heads / s.num_kv_heads) * s.q_len + kSegmentRows - 1) / kSegmentRows;
+    const int64_t tile = kind == kBf16Pool && s.head_dim == 128 ? 64 : 128;
+    return int64_t(s.batch) * s.num_kv_heads * MS * std::max<int64_t>(1, (keys + tile - 1) / tile);
+}
+
+bool rows_shape_ok(const pa_shape& s)
+{
+    return s.batch > 0 && s.num_q_heads > 0 && s.num_kv_heads > 0 && s.q_len > 0 &&
+           s.num_q_heads % s.num_kv_heads == 0 &&
+           int64_t(s.num_q_heads / s.num_kv_heads) * s.q_len < (int64_t(1) << 30);
+}
+
+}  // namespace
+
+size_t pa_decode_q4_workspace_bytes(pa_shape shape)
+{
+    DeviceInfo* dev;
+    if (!rows_shape_ok(shape) || shape.head_dim != 128 || device_info(&dev) != PA_OK ||
+        !decode_rows_fits(shape, kQ4Pool, kFull, dev->max_smem_optin))
+        return 0;
+    return decode_rows_workspace_bytes(shape, kQ4Pool, kFull, dev->sm_count);
+}
+
+pa_status pa_decode_q4(const void* query, const void* key_pages, const void* value_pages,
+                       const int32_t* block_table, const int32_t* context_lens, int32_t page_size,
+                       float scale, int causal, void* out, pa_shape shape, int32_t max_context_len,
+                       void* workspace, size_t workspace_bytes, void* stream)
+{
+    pa_status st = check_attention(query, key_pages, value_pages, block_table, context_lens,
+                                   page_size, scale, out, shape);
+    if (st != PA_OK)
+        return st;
+    if (shape.head_dim != 128 || !rows_shape_ok(shape))
+        return PA_ERR_UNSUPPORTED;
+    DeviceInfo* dev;
+    if ((st = device_info(&dev)) != PA_OK)
+        return st;
+    if (!decode_rows_fits(shape, kQ4Pool, kFull, dev->max_smem_optin))
+        return PA_ERR_UNSUPPORTED;
+    if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 15u) ||
+        workspace_bytes < decode_rows_workspace_bytes(shape, kQ4Pool, kFull, dev->sm_count))
+        return PA_ERR_WORKSPACE;
+    DecodeArgs a = rows_args(query, block_table, context_lens, page_size, scale, causal, out, shape, kQ4Pool,
+                             kFull, dev);
+    a.key_rows = static_cast<const uint8_t*>(key_pages);
+    a.value_rows = static_cast<const uint8_t*>(value_pages);
+    const int grid = decode_rows_launch_grid(
+        shape, kQ4Pool, max_context_len > 0 ? rows_granules(shape, kQ4Pool, max_context_len) : 0, dev->sm_count);
+    const CUtensorMap none = {};
+    return launch_decode_rows(none, none, a, shape, kQ4Pool, grid, workspace, dev->id,
+                              static_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? PA_OK
+               : PA_ERR_CUDA;
+}
+
+size_t pa_prefill_q4_workspace_bytes(pa_shape shape, int32_t max_context_len)
+{
+    return pa_prefill_fp8_workspace_bytes(shape, max_context_len);
+}
+
+pa_status pa_prefill_q4(const void* query, const void* key_pages, const void* value_pages,
+                        const int32_t* block_table, const int32_t* context_lens, int32_t page_size,
+                        float scale, int causal, void* out, pa_shape shape,
+                        int32_t max_context_len, void* workspace, size_t workspace_bytes,
+                        void* stream)
+{
+    pa_status st = check_attention(query, key_pages, value_pages, block_table, context_lens,
+                                   page_size, scale, out, shape);
+    if (st != PA_OK)
+        return st;
+    if (shape.head_dim != 128)
+        return PA_ERR_UNSUPPORTED;
+    DeviceInfo* dev;
+    if ((st = device_info(&dev)) != PA_OK)
+        return st;
+    Fp8PrefillPlan p;
+    if ((st = plan_prefill_fp8(shape, max_context_len, dev, &p)) != PA_OK)
+        return st;
+    if (!workspace || workspace_bytes < p.total || (reinterpret_cast<uintptr_t>(workspace) & 255u))
+        return PA_ERR_WORKSPACE;
+    uint8_t* w = static_cast<uint8_t*>(workspace);
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if ((st = copy_q4(key_pages, value_pages, block_table, context_lens, page_size, shape, p, dev, w,
+                      s)) != PA_OK)
+        return st;
+    return run_prefill_tc(query, w, w + p.kv_bytes, reinterpret_cast<int32_t*>(w + p.table_off),
+                          context_lens, 128, scale, causal, out, p.copy, s,
+                          p.split_bytes ? w + p.split_off : nullptr, p.split_bytes, 1.f,
+                          p.piece_bytes ? w + p.split_off : nullptr, p.piece_bytes);
+}
+
+namespace {
+
+// Route of pa_attention_q4: the few-row kernel reads K and V once per 16 rows of a
+// (request, KV head), the prefill copies them to bf16 first.
+int32_t route_q4(const pa_shape& shape) { return shape.q_len <= 0 ? -1 : shape.q_len <= 8 ? 0 : 1; }
+
+}  // namespace
+
+size_t pa_attention_q4_workspace_bytes(pa_shape shape, int32_t max_context_len)
+{
+    const int32_t route = route_q4(shape);
+    if (route < 0)
+        return 0;
+    return route == 0 ? pa_decode_q4_workspace_bytes(shape)
+                      : pa_prefill_q4_workspace_bytes(shape, max_context_len);
+}
+
+pa_status pa_attention_q4(const void* query, const void* key_pages, const void* value_pages,
+                          const int32_t* block_table, const int32_t* context_lens, int32_t page_size,
+                          float scale, int causal, void* out, pa_shape shape,
+                          int32_t max_context_len, void* workspace, size_t workspace_bytes,
+                          void* stream)
+{
+    const int32_t route = route_q4(shape);
+    if (route < 0)
+        return PA_ERR_INVALID_ARG;
+    return (route == 0 ? pa_decode_q4 : pa_prefill_q4)(
+        query, key_pages, value_pages, block_table, context_lens, page_size, scale, causal, out, shape,
+        max_context_len, workspace, workspace_bytes, stream);
 }
 
 pa_status pa_decode_dense(const void* query, const void* key_dense, const void* value_dense,

@@ -112,6 +112,30 @@ struct GatherArgs {
 
 cudaError_t launch_gather(const GatherArgs& a, cudaStream_t stream);
 
+// 4-bit pools (pa_q4.cuh): the quantising append (AppendArgs, pages of 80-byte rows,
+// D 128), and the read-back of every request's rows as bf16. Row t of (request b,
+// KV head h) goes to element b * batch_stride + h * head_stride + (t / 128) * block_stride
+// + (t % 128) * 128: dense rows, or pages of 128 tokens with a table (table_out
+// [B, copy_pages], page b * copy_pages + t / 128; rows of a bad page are zeros there).
+constexpr int kQ4CopyRows = 128;
+struct Q4ReadArgs {
+    const uint8_t* key_pages;     // [P, H_kv, ps, 80]
+    const uint8_t* value_pages;
+    const int32_t* block_table;   // [B, max_pages]
+    const int32_t* context_lens;  // [B]
+    uint16_t* key_out;
+    uint16_t* value_out;
+    int32_t* table_out;           // null: dense rows
+    unsigned* err;
+    int64_t batch_stride, head_stride, block_stride;
+    int32_t B, H_kv, ps, num_pages, max_pages;
+    int32_t max_len;              // rows a request has room for
+    int32_t copy_pages;
+    int32_t chunks;               // set by the launcher
+};
+cudaError_t launch_append_q4(const AppendArgs& a, cudaStream_t stream);
+cudaError_t launch_read_q4(Q4ReadArgs a, cudaStream_t stream);
+
 // ---------------------------------------------------------------------------
 // Split-KV attention (decode schedule)
 
@@ -142,7 +166,23 @@ DecodePlan decode_plan(const pa_shape& s, bool fp8);
 
 // What a decode kernel attends to and leaves: everything; a sliding window and
 // the first keys; everything, with the scores and row states kept.
-enum DecodeMode : int { kFull = 0, kWindow = 1, kScores = 2, kDecodeModes = 3 };
+// The few-row kernel also: the keys behind a shared prefix, states left as rows.
+enum DecodeMode : int { kFull = 0, kWindow = 1, kScores = 2, kDecodeModes = 3, kSuffix = 3 };
+
+// What a pool's rows hold.
+enum PoolKind : int { kBf16Pool = 0, kE4m3Pool = 1, kQ4Pool = 2 };
+
+// Query rows of a segment of the few-row kernel, where a call has more.
+constexpr int kSegmentRows = 16;
+
+// The prefixes that requests of a batch share (pa_prefix.cuh).
+struct PrefixArgs {
+    const int32_t* table;         // [count, pages]
+    const int32_t* lens;          // [count]
+    const int32_t* starts;        // [count + 1]
+    int32_t count, pages;
+    int32_t cap;                  // longest prefix
+};
 
 struct DecodeArgs {
     const uint16_t* q;            // [B, H_q, L, D]
@@ -176,6 +216,9 @@ struct DecodeArgs {
     int64_t score_stride;      // a multiple of 64, at least score_cap
     int32_t score_cap;         // kScores: longest context
     int32_t ps_shift;   // the few-row kernel: log2 of the page size
+    const uint8_t* key_rows;      // 4-bit pools
+    const uint8_t* value_rows;
+    PrefixArgs prefix;            // kSuffix
     int32_t debug_unset_wait;  // test support: block 0 first waits on a barrier
                                // that nothing arrives at (times out, flags)
 };
@@ -188,16 +231,19 @@ cudaError_t launch_decode(const CUtensorMap& key_map, const CUtensorMap& value_m
                           const CUtensorMap& q_map, const DecodeArgs& a, int grid, int device,
                           cudaStream_t stream);
 
-// The few-row kernel (at most 16 rows per request and KV head; kWindow and
-// kScores): whether it takes a shape on a device with max_smem bytes of shared
-// memory a block, its workspace, and the launch (granule_bound: an upper bound of the
-// 4-tile granules, 0 unknown).
+// The few-row kernel: whether it takes a window or weight call (at most 16 rows per
+// request and KV head) on a device with max_smem bytes of shared memory a block;
+// whether the modes that cut more rows into segments fit (kFull over 4-bit pools,
+// kSuffix); the keys per TMA box (DecodeArgs::box_rows); its workspace; its blocks
+// (granule_bound: an upper bound of the 4-tile granules, 0 unknown) and the launch.
 bool decode_rows_takes(const pa_shape& s, int max_smem);
-size_t decode_rows_workspace_bytes(const pa_shape& s, int sm_count);
-int decode_rows_box(const pa_shape& s, bool fp8, int page_size);   // keys per TMA box (DecodeArgs::box_rows)
+bool decode_rows_fits(const pa_shape& s, int kind, int mode, int max_smem);
+int decode_rows_box(const pa_shape& s, int kind, int page_size);
+size_t decode_rows_workspace_bytes(const pa_shape& s, int kind, int mode, int sm_count);
+int decode_rows_launch_grid(const pa_shape& s, int kind, int64_t granule_bound, int sm_count);
 cudaError_t launch_decode_rows(const CUtensorMap& key_map, const CUtensorMap& value_map, DecodeArgs a,
-                               const pa_shape& s, int64_t granule_bound, void* workspace,
-                               int device, int sm_count, cudaStream_t stream);
+                               const pa_shape& s, int kind, int grid, void* workspace, int device,
+                               cudaStream_t stream);
 
 // Accumulation of attention weights: weight_pages[slot of j] = decay * old (0
 // for the L newest positions, or where decay is 0) + sum over the R rows of

@@ -1,6 +1,6 @@
 // The Python side of the calls that take a model's step from the projection to
 // the evicted cache (pa_qk_norm_rope_append, the window and weight calls,
-// pa_kv_evict): argument checks, the tensors that a call makes where none are
+// pa_kv_evict) and of the 4-bit pools' calls: argument checks, the tensors that a call makes where none are
 // given (outputs, a workspace of this call alone, both made on the device of the
 // call and for its stream), and the call of the C ABI on that device and stream. An
 // append of one token takes 2.1 us on the GPU; a call of it 3.4 us, 10.7 with these
@@ -278,6 +278,11 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n)
     });
 }
 
+// Bytes of a 4-bit pool's row, and the elements that it holds.
+constexpr int64_t kQ4Row = 80, kQ4Elements = 128;
+
+enum class Pool { kBf16, kE4m3, kQ4 };
+
 // What the attention calls share: query, pools, tables, page size, scale, out.
 struct Paged {
     Call call;
@@ -288,6 +293,11 @@ struct Paged {
     at::Tensor out;
 
     Paged(PyObject* const* a, PyObject* bt_arg, PyObject* cl_arg, PyObject* ps_arg, bool fp8, PyObject* scale_arg,
+          PyObject* out_arg, PyObject* stream_arg)
+        : Paged(a, bt_arg, cl_arg, ps_arg, fp8 ? Pool::kE4m3 : Pool::kBf16, scale_arg, out_arg, stream_arg)
+    {
+    }
+    Paged(PyObject* const* a, PyObject* bt_arg, PyObject* cl_arg, PyObject* ps_arg, Pool kind, PyObject* scale_arg,
           PyObject* out_arg, PyObject* stream_arg)
         : call(tensor(a[0], "query"), "query", stream_arg)
     {
@@ -301,11 +311,12 @@ struct Paged {
             value_error("page pools must be [P, H_kv, page_size, D]");
         if (kp.size(2) != ps)
             value_error("page pool shape does not match page_size");
-        if (kp.size(3) != query.size(3))
-            value_error("query and pages disagree on head_dim");
+        if (kind == Pool::kQ4 ? kp.size(3) != kQ4Row || query.size(3) != kQ4Elements : kp.size(3) != query.size(3))
+            value_error(kind == Pool::kQ4 ? "4-bit pools hold rows of 80 bytes for a head_dim of 128"
+                                          : "query and pages disagree on head_dim");
         if (table.dim() != 2 || table.size(0) != query.size(0) || !shape_is(lens, {query.size(0)}))
             value_error("block_table must be [B, max_pages] and context_lens [B]");
-        const at::ScalarType pool = fp8 ? at::kByte : at::kBFloat16;
+        const at::ScalarType pool = kind == Pool::kBf16 ? at::kBFloat16 : at::kByte;
         q = call.check(query, at::kBFloat16, "query");
         k = call.check(kp, pool, "key_pages");
         v = call.check(vp, pool, "value_pages");
@@ -376,6 +387,113 @@ PyObject* window(PyObject*, PyObject* const* a, Py_ssize_t n)
             }
         }
         if (raised(st, what))
+            return nullptr;
+        return THPVariable_Wrap(p.out);
+    });
+}
+
+// The pools of a 4-bit call, [P, H_kv, page_size, 80].
+pa_shape q4_pools(const at::Tensor& kp, const at::Tensor& vp, int32_t ps)
+{
+    if (kp.dim() != 4 || kp.size(2) != ps || kp.size(3) != kQ4Row || vp.sizes() != kp.sizes())
+        value_error("4-bit page pools must be [P, H_kv, page_size, 80]");
+    const int32_t heads = size32(kp.size(1), "H_kv");
+    return pa_shape{0, heads, heads, int32_t(kQ4Elements), 0, size32(kp.size(0), "the number of pages"), 0};
+}
+
+// key, value, key_pages, value_pages, slot_mapping, page_size, stream
+PyObject* append_q4(PyObject*, PyObject* const* a, Py_ssize_t n)
+{
+    return guarded([&]() -> PyObject* {
+        check_args(n, 7);
+        const at::Tensor &key = tensor(a[0], "key"), &value = tensor(a[1], "value");
+        const at::Tensor &kp = tensor(a[2], "key_pages"), &vp = tensor(a[3], "value_pages");
+        const at::Tensor& slots = tensor(a[4], "slot_mapping");
+        const int32_t ps = integer(a[5], "page_size");
+        pa_shape shape = q4_pools(kp, vp, ps);
+        if (key.dim() != 4 || key.size(1) != kp.size(1) || key.size(3) != kQ4Elements || value.sizes() != key.sizes())
+            value_error("key and value must be [B, H_kv, L_new, 128], with the pools' H_kv");
+        if (!shape_is(slots, {key.size(0), key.size(2)}))
+            value_error("slot_mapping must be [B, L_new]");
+        Call call(key, "key", a[6]);
+        void *k = call.check(key, at::kBFloat16, "key"), *v = call.check(value, at::kBFloat16, "value");
+        void *kpp = call.check(kp, at::kByte, "key_pages"), *vpp = call.check(vp, at::kByte, "value_pages");
+        const int32_t* slot = static_cast<int32_t*>(call.check(slots, at::kInt, "slot_mapping"));
+        shape.batch = size32(key.size(0), "B");
+        shape.q_len = size32(key.size(2), "L_new");
+        if (shape.batch > 0 && shape.q_len > 0) {
+            const pa_status st = unlocked([&] { return pa_append_kv_q4(k, v, kpp, vpp, slot, ps, shape, call.stream); });
+            if (raised(st, "pa_append_kv_q4"))
+                return nullptr;
+        }
+        Py_RETURN_NONE;
+    });
+}
+
+// key_pages, value_pages, block_table, context_lens, page_size, dense_len, key_dense, value_dense, stream
+PyObject* gather_q4(PyObject*, PyObject* const* a, Py_ssize_t n)
+{
+    return guarded([&]() -> PyObject* {
+        check_args(n, 9);
+        const at::Tensor &kp = tensor(a[0], "key_pages"), &vp = tensor(a[1], "value_pages");
+        const at::Tensor &table = tensor(a[2], "block_table"), &lens = tensor(a[3], "context_lens");
+        const int32_t ps = integer(a[4], "page_size"), len = integer(a[5], "dense_len");
+        pa_shape shape = q4_pools(kp, vp, ps);
+        const int64_t B = table.dim() == 2 ? table.size(0) : -1, H = kp.size(1);
+        if (B < 0 || !shape_is(lens, {B}))
+            value_error("block_table must be [B, max_pages] and context_lens [B]");
+        if (len < 0)
+            value_error("dense_len must not be negative");
+        Call call(kp, "key_pages", a[8]);
+        void *k = call.check(kp, at::kByte, "key_pages"), *v = call.check(vp, at::kByte, "value_pages");
+        const int32_t* bt = static_cast<int32_t*>(call.check(table, at::kInt, "block_table"));
+        const int32_t* cl = static_cast<int32_t*>(call.check(lens, at::kInt, "context_lens"));
+        const at::Tensor kd = a[6] == Py_None ? call.make({B, H, len, kQ4Elements}, at::kBFloat16) : tensor(a[6], "key_dense");
+        const at::Tensor vd = a[7] == Py_None ? call.make({B, H, len, kQ4Elements}, at::kBFloat16) : tensor(a[7], "value_dense");
+        if (!shape_is(kd, {B, H, len, kQ4Elements}) || !shape_is(vd, {B, H, len, kQ4Elements}))
+            value_error("dense buffers must be [B, H_kv, dense_len, 128]");
+        void *ko = call.check(kd, at::kBFloat16, "key_dense"), *vo = call.check(vd, at::kBFloat16, "value_dense");
+        shape.batch = size32(B, "B");
+        shape.max_pages = size32(table.size(1), "max_pages");
+        if (B > 0 && len > 0) {
+            const pa_status st =
+                unlocked([&] { return pa_gather_kv_q4(k, v, bt, cl, ps, shape, len, ko, vo, call.stream); });
+            if (raised(st, "pa_gather_kv_q4"))
+                return nullptr;
+        }
+        PyObject* x = THPVariable_Wrap(kd);
+        PyObject* y = x ? THPVariable_Wrap(vd) : nullptr;
+        PyObject* both = y ? PyTuple_Pack(2, x, y) : nullptr;
+        Py_XDECREF(x);
+        Py_XDECREF(y);
+        return both;
+    });
+}
+
+// which (0 decode, 1 prefill, 2 dispatch), query, key_pages, value_pages, block_table, context_lens,
+// page_size, scale, causal, out, max_context_len, workspace, stream
+PyObject* attention_q4(PyObject*, PyObject* const* a, Py_ssize_t n)
+{
+    return guarded([&]() -> PyObject* {
+        check_args(n, 13);
+        const int32_t which = integer(a[0], "which");
+        Paged p(a + 1, a[4], a[5], a[6], Pool::kQ4, a[7], a[9], a[12]);
+        const int causal = truth(a[8]);
+        const int32_t longest = integer(a[10], "max_context_len");
+        size_t need = 0;
+        if (a[11] == Py_None)
+            need = which == 0   ? pa_decode_q4_workspace_bytes(p.shape)
+                   : which == 1 ? pa_prefill_q4_workspace_bytes(p.shape, longest)
+                                : pa_attention_q4_workspace_bytes(p.shape, longest);
+        const at::Tensor workspace = p.call.workspace(a[11], need);
+        const size_t bytes = workspace.nbytes();
+        void *out = p.out.data_ptr(), *ws = workspace.data_ptr();
+        const auto f = which == 0 ? pa_decode_q4 : which == 1 ? pa_prefill_q4 : pa_attention_q4;
+        const pa_status st = unlocked([&] {
+            return f(p.q, p.k, p.v, p.table(), p.lens(), p.ps, p.scale, causal, out, p.shape, longest, ws, bytes,
+                     p.call.stream);
+        });
+        if (raised(st, which == 0 ? "pa_decode_q4" : which == 1 ? "pa_prefill_q4" : "pa_attention_q4"))
             return nullptr;
         return THPVariable_Wrap(p.out);
     });
@@ -490,6 +608,9 @@ PyMethodDef g_methods[] = {
     {"window", fast(window), METH_FASTCALL, "the sliding-window calls"},
     {"weights", fast(weights), METH_FASTCALL, "pa_decode_weights and its e4m3 form"},
     {"evict", fast(evict), METH_FASTCALL, "pa_kv_evict and its e4m3 form"},
+    {"append_q4", fast(append_q4), METH_FASTCALL, "pa_append_kv_q4"},
+    {"gather_q4", fast(gather_q4), METH_FASTCALL, "pa_gather_kv_q4"},
+    {"attention_q4", fast(attention_q4), METH_FASTCALL, "the attention calls over 4-bit pools"},
     {"set_error", set_error, METH_O, "the class raised for a pa_status"},
     {nullptr, nullptr, 0, nullptr},
 };
