@@ -68,6 +68,7 @@ typedef enum pa_status {
 #define PA_DEVERR_CONTEXT_LEN  0x4u  /* context_lens entry < 0 or > max_pages*ps    */
 #define PA_DEVERR_TIMEOUT      0x8u  /* pipeline wait gave up                       */
 #define PA_DEVERR_POSITION     0x10u /* positions entry outside [0, table_len)      */
+#define PA_DEVERR_PREFIX       0x20u /* prefix_starts that do not ascend in the batch */
 
 /* Problem sizes shared by every call. */
 typedef struct pa_shape {
@@ -668,6 +669,66 @@ pa_status pa_attention_q4(const void *query, const void *key_pages, const void *
                           int32_t page_size, float scale, int causal, void *out, pa_shape shape,
                           int32_t max_context_len, void *workspace, size_t workspace_bytes,
                           void *stream);
+
+/*
+ * Decode of a batch whose requests share long prefixes, each prefix attended to once for
+ * all of them: what pa_decode gives (causal) where request b's positions before
+ * prefix_lens[p] lie in prefix p's pages. The rows of all requests of a prefix go through
+ * the tensor cores together, so its K and V are read once per 256 of their rows; the
+ * few-row kernel reads each request's own keys, and a merge joins the two.
+ *   prefix_table   [num_prefixes, prefix_pages] int32, the pages of each prefix.
+ *   prefix_lens    [num_prefixes] int32, tokens, 0 .. min(prefix_pages * page_size,
+ *                  max_prefix_len) (a longer one records PA_DEVERR_CONTEXT_LEN and
+ *                  is cut). They need not end a page: a request's own copy of the
+ *                  last page holds its tokens behind the prefix.
+ *   prefix_starts  [num_prefixes + 1] int32, ascending, within 0 .. B: prefix p belongs
+ *                  to requests prefix_starts[p] .. prefix_starts[p + 1] - 1; requests
+ *                  before the first or from the last on have none. Where they do not
+ *                  ascend PA_DEVERR_PREFIX is recorded and the outputs are numbers
+ *                  without meaning.
+ *   block_table    entries of pages that lie wholly before a request's prefix_len are
+ *                  not read and may hold anything.
+ *   context_lens   positions in all, prefix included; a request may be shorter than its
+ *                  prefix (or empty): its rows see what they see.
+ *   num_prefixes   1 .. 1024;  max_prefix_len > 0 bounds prefix_lens and sizes the
+ *                  workspace.
+ *   workspace      ..._workspace_bytes(shape, page_size, num_prefixes, max_prefix_len)
+ *                  bytes (0: invalid or unsupported sizes), 256-byte aligned, any
+ *                  contents; calls that share one must not overlap on the GPU.
+ * Other arguments and errors as for pa_decode / pa_decode_fp8 / pa_decode_q4. Built for
+ * few rows a request; any L is computed. Three kernels on `stream`; one more
+ * before them copies the prefixes into bf16 pages of 128 tokens in the workspace where
+ * the pool is not bf16 (e4m3 exactly, 4-bit values rounded to bf16) or its pages hold
+ * fewer than 8 tokens.
+ */
+size_t pa_decode_prefix_workspace_bytes(pa_shape shape, int32_t page_size, int32_t num_prefixes,
+                                        int32_t max_prefix_len);
+pa_status pa_decode_prefix(const void *query, const void *key_pages, const void *value_pages,
+                           const int32_t *block_table, const int32_t *context_lens,
+                           int32_t page_size, float scale, const int32_t *prefix_table,
+                           const int32_t *prefix_lens, const int32_t *prefix_starts,
+                           int32_t num_prefixes, int32_t prefix_pages, int32_t max_prefix_len,
+                           void *out, pa_shape shape, int32_t max_context_len, void *workspace,
+                           size_t workspace_bytes, void *stream);
+size_t pa_decode_prefix_fp8_workspace_bytes(pa_shape shape, int32_t page_size,
+                                            int32_t num_prefixes, int32_t max_prefix_len);
+pa_status pa_decode_prefix_fp8(const void *query, const void *key_pages, const void *value_pages,
+                               const int32_t *block_table, const int32_t *context_lens,
+                               int32_t page_size, float scale, float k_scale, float v_scale,
+                               const int32_t *prefix_table, const int32_t *prefix_lens,
+                               const int32_t *prefix_starts, int32_t num_prefixes,
+                               int32_t prefix_pages, int32_t max_prefix_len, void *out,
+                               pa_shape shape, int32_t max_context_len, void *workspace,
+                               size_t workspace_bytes, void *stream);
+size_t pa_decode_prefix_q4_workspace_bytes(pa_shape shape, int32_t page_size,
+                                           int32_t num_prefixes, int32_t max_prefix_len);
+pa_status pa_decode_prefix_q4(const void *query, const void *key_pages, const void *value_pages,
+                              const int32_t *block_table, const int32_t *context_lens,
+                              int32_t page_size, float scale, const int32_t *prefix_table,
+                              const int32_t *prefix_lens, const int32_t *prefix_starts,
+                              int32_t num_prefixes, int32_t prefix_pages, int32_t max_prefix_len,
+                              void *out, pa_shape shape, int32_t max_context_len, void *workspace,
+                              size_t workspace_bytes, void *stream);
 
 /*
  * Synchronises `stream`, then reads and clears the device error word of the

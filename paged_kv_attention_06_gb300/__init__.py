@@ -21,7 +21,9 @@ _API = ("pa_append_kv", "pa_decode", "pa_prefill", "pa_attention", "pa_attention
         "pa_decode_weights", "pa_decode_weights_fp8", "pa_decode_weights_workspace_bytes",
         "pa_append_kv_q4", "pa_gather_kv_q4", "pa_decode_q4", "pa_prefill_q4", "pa_attention_q4",
         "pa_decode_q4_workspace_bytes", "pa_prefill_q4_workspace_bytes",
-        "pa_attention_q4_workspace_bytes")
+        "pa_attention_q4_workspace_bytes", "pa_decode_prefix", "pa_decode_prefix_fp8",
+        "pa_decode_prefix_q4", "pa_decode_prefix_workspace_bytes",
+        "pa_decode_prefix_fp8_workspace_bytes", "pa_decode_prefix_q4_workspace_bytes")
 
 
 def __getattr__(name):

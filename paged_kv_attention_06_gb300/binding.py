@@ -34,6 +34,7 @@ PA_DEVERR_SLOT = 0x2
 PA_DEVERR_CONTEXT_LEN = 0x4
 PA_DEVERR_TIMEOUT = 0x8
 PA_DEVERR_POSITION = 0x10
+PA_DEVERR_PREFIX = 0x20
 
 LIB_PATH = _build.LIB
 
@@ -140,6 +141,10 @@ def _load() -> ctypes.CDLL:
     lib.pa_decode_q4_workspace_bytes.restype = sz
     for f in (lib.pa_prefill_q4_workspace_bytes, lib.pa_attention_q4_workspace_bytes):
         f.argtypes = [pa_shape, i32]
+        f.restype = sz
+    for f in (lib.pa_decode_prefix_workspace_bytes, lib.pa_decode_prefix_fp8_workspace_bytes,
+              lib.pa_decode_prefix_q4_workspace_bytes):
+        f.argtypes = [pa_shape, i32, i32, i32]
         f.restype = sz
     lib.pa_debug_arm_wait_timeout.argtypes = []
     lib.pa_debug_arm_wait_timeout.restype = None
@@ -548,6 +553,70 @@ def pa_attention_q4(query, key_pages, value_pages, block_table, context_lens, pa
         max_context_len = int(context_lens.max().item())
     return _calls.attention_q4(2, query, key_pages, value_pages, block_table, context_lens, page_size,
                                scale, causal, out, max_context_len, workspace, _raw(stream))
+
+
+def _prefix_workspace(f, shape, page_size, num_prefixes, max_prefix_len, device) -> int:
+    with torch.cuda.device(device if device is not None else torch.cuda.current_device()):
+        return int(f(shape, int(page_size), int(num_prefixes), int(max_prefix_len)))
+
+
+def pa_decode_prefix_workspace_bytes(shape: pa_shape, page_size: int, num_prefixes: int,
+                                     max_prefix_len: int,
+                                     device: Optional[torch.device] = None) -> int:
+    return _prefix_workspace(_lib.pa_decode_prefix_workspace_bytes, shape, page_size, num_prefixes,
+                             max_prefix_len, device)
+
+
+def pa_decode_prefix_fp8_workspace_bytes(shape: pa_shape, page_size: int, num_prefixes: int,
+                                         max_prefix_len: int,
+                                         device: Optional[torch.device] = None) -> int:
+    return _prefix_workspace(_lib.pa_decode_prefix_fp8_workspace_bytes, shape, page_size,
+                             num_prefixes, max_prefix_len, device)
+
+
+def pa_decode_prefix_q4_workspace_bytes(shape: pa_shape, page_size: int, num_prefixes: int,
+                                        max_prefix_len: int,
+                                        device: Optional[torch.device] = None) -> int:
+    return _prefix_workspace(_lib.pa_decode_prefix_q4_workspace_bytes, shape, page_size,
+                             num_prefixes, max_prefix_len, device)
+
+
+def pa_decode_prefix(query: torch.Tensor, key_pages: torch.Tensor, value_pages: torch.Tensor,
+                     block_table: torch.Tensor, context_lens: torch.Tensor, page_size: int,
+                     prefix_table: torch.Tensor, prefix_lens: torch.Tensor,
+                     prefix_starts: torch.Tensor, max_prefix_len: Optional[int] = None,
+                     scale: Optional[float] = None, out: Optional[torch.Tensor] = None,
+                     max_context_len: int = 0, workspace: Optional[torch.Tensor] = None,
+                     stream=None) -> torch.Tensor:
+    """pa_decode of requests that share prefixes: requests prefix_starts[p] ..
+    prefix_starts[p + 1] - 1 have their first prefix_lens[p] positions in the pages
+    prefix_table[p], which are attended to once for all of them; block_table leads to the
+    positions behind. max_prefix_len bounds prefix_lens (None: the table's width)."""
+    return _calls.prefix(0, query, key_pages, value_pages, block_table, context_lens, page_size,
+                         None, None, prefix_table, prefix_lens, prefix_starts, max_prefix_len,
+                         scale, out, max_context_len, workspace, _raw(stream))
+
+
+def pa_decode_prefix_fp8(query, key_pages, value_pages, block_table, context_lens, page_size: int,
+                         k_scale: float, v_scale: float, prefix_table, prefix_lens, prefix_starts,
+                         max_prefix_len: Optional[int] = None, scale: Optional[float] = None,
+                         out=None, max_context_len: int = 0,
+                         workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """pa_decode_prefix over uint8 e4m3 pools."""
+    return _calls.prefix(1, query, key_pages, value_pages, block_table, context_lens, page_size,
+                         k_scale, v_scale, prefix_table, prefix_lens, prefix_starts,
+                         max_prefix_len, scale, out, max_context_len, workspace, _raw(stream))
+
+
+def pa_decode_prefix_q4(query, key_pages, value_pages, block_table, context_lens, page_size: int,
+                        prefix_table, prefix_lens, prefix_starts,
+                        max_prefix_len: Optional[int] = None, scale: Optional[float] = None,
+                        out=None, max_context_len: int = 0,
+                        workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """pa_decode_prefix over uint8 4-bit pools [P, H_kv, page_size, 80]."""
+    return _calls.prefix(2, query, key_pages, value_pages, block_table, context_lens, page_size,
+                         None, None, prefix_table, prefix_lens, prefix_starts, max_prefix_len,
+                         scale, out, max_context_len, workspace, _raw(stream))
 
 
 def pa_decode_fp8(query, key_pages, value_pages, block_table, context_lens, page_size: int,

@@ -1678,11 +1678,11 @@ pa_status check_q4_pools(const pa_shape& s, int32_t page_size)
     return PA_OK;
 }
 
-Q4ReadArgs q4_read_args(const void* key_pages, const void* value_pages, const int32_t* block_table,
+PageReadArgs page_read_args(const void* key_pages, const void* value_pages, const int32_t* block_table,
                         const int32_t* context_lens, int32_t page_size, const pa_shape& s,
                         const DeviceInfo* dev)
 {
-    Q4ReadArgs a;
+    PageReadArgs a;
     memset(&a, 0, sizeof a);
     a.key_pages = static_cast<const uint8_t*>(key_pages);
     a.value_pages = static_cast<const uint8_t*>(value_pages);
@@ -1759,34 +1759,54 @@ pa_status pa_gather_kv_q4(const void* key_pages, const void* value_pages,
     DeviceInfo* dev;
     if ((st = device_info(&dev)) != PA_OK)
         return st;
-    Q4ReadArgs a = q4_read_args(key_pages, value_pages, block_table, context_lens, page_size, shape, dev);
+    PageReadArgs a = page_read_args(key_pages, value_pages, block_table, context_lens, page_size, shape, dev);
     a.key_out = static_cast<uint16_t*>(key_dense);
     a.value_out = static_cast<uint16_t*>(value_dense);
     a.head_stride = int64_t(dense_len) * 128;
     a.batch_stride = a.head_stride * shape.num_kv_heads;
     a.block_stride = int64_t(kQ4CopyRows) * 128;
     a.max_len = dense_len;
-    return launch_read_q4(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+    return launch_read_pages(a, kQ4Pool, 128, static_cast<cudaStream_t>(stream)) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
 namespace {
 
-// The bf16 copies of what the requests have cached in a 4-bit pool, with their table,
-// at the front of a workspace laid out by plan_prefill_fp8.
-pa_status copy_q4(const void* key_pages, const void* value_pages, const int32_t* block_table,
-                  const int32_t* context_lens, int32_t page_size, const pa_shape& s,
-                  const Fp8PrefillPlan& p, const DeviceInfo* dev, uint8_t* w, cudaStream_t stream)
+// bf16 copies, in pages of 128 tokens, of what `s.batch` tables lead to: K and V (kv_bytes
+// each), then the copies' table (P2 entries each) table_off bytes into w.
+pa_status copy_pages(const void* key_pages, const void* value_pages, const int32_t* block_table,
+                     const int32_t* context_lens, int32_t page_size, const pa_shape& s, int kind,
+                     int64_t P2, size_t kv_bytes, size_t table_off, const DeviceInfo* dev, uint8_t* w,
+                     cudaStream_t stream)
 {
-    Q4ReadArgs a = q4_read_args(key_pages, value_pages, block_table, context_lens, page_size, s, dev);
+    if (kind == kE4m3Pool) {
+        Fp8PagesArgs c;
+        memset(&c, 0, sizeof c);
+        c.key_pages = static_cast<const uint8_t*>(key_pages);
+        c.value_pages = static_cast<const uint8_t*>(value_pages);
+        c.block_table = block_table;
+        c.context_lens = context_lens;
+        c.key_out = reinterpret_cast<uint16_t*>(w);
+        c.value_out = reinterpret_cast<uint16_t*>(w + kv_bytes);
+        c.table_out = reinterpret_cast<int32_t*>(w + table_off);
+        c.err = dev->err;
+        c.B = s.batch;
+        c.H_kv = s.num_kv_heads;
+        c.ps = page_size;
+        c.max_pages = s.max_pages;
+        c.num_pages = s.num_pages;
+        c.P2 = int32_t(P2);
+        return launch_fp8_pages_to_bf16(c, stream) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+    }
+    PageReadArgs a = page_read_args(key_pages, value_pages, block_table, context_lens, page_size, s, dev);
     a.key_out = reinterpret_cast<uint16_t*>(w);
-    a.value_out = reinterpret_cast<uint16_t*>(w + p.kv_bytes);
-    a.table_out = reinterpret_cast<int32_t*>(w + p.table_off);
-    a.head_stride = int64_t(kQ4CopyRows) * 128;
+    a.value_out = reinterpret_cast<uint16_t*>(w + kv_bytes);
+    a.table_out = reinterpret_cast<int32_t*>(w + table_off);
+    a.head_stride = int64_t(kQ4CopyRows) * s.head_dim;
     a.block_stride = a.head_stride * s.num_kv_heads;
-    a.batch_stride = a.block_stride * p.P2;
-    a.max_len = int32_t(p.P2 * kQ4CopyRows);
-    a.copy_pages = int32_t(p.P2);
-    return launch_read_q4(a, stream) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+    a.batch_stride = a.block_stride * P2;
+    a.max_len = int32_t(P2 * kQ4CopyRows);
+    a.copy_pages = int32_t(P2);
+    return launch_read_pages(a, kind, s.head_dim, stream) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
 }  // namespace
@@ -1831,7 +1851,7 @@ DecodeArgs rows_args(const void* query, const int32_t* block_table, const int32_
 int64_t rows_granules(const pa_shape& s, int kind, int64_t keys)
 {
     const int64_t MS = (int64_t(s.num_q_heads / s.num_kv_heads) * s.q_len + kSegmentRows - 1) / kSegmentRows;
-    const int64_t tile = kind == kBf16Pool && s.head_dim == 128 ? 64 : 128;
+    const int64_t tile = 4 * decode_rows_tile(s, kind);
     return int64_t(s.batch) * s.num_kv_heads * MS * std::max<int64_t>(1, (keys + tile - 1) / tile);
 }
 
@@ -1912,8 +1932,8 @@ pa_status pa_prefill_q4(const void* query, const void* key_pages, const void* va
         return PA_ERR_WORKSPACE;
     uint8_t* w = static_cast<uint8_t*>(workspace);
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if ((st = copy_q4(key_pages, value_pages, block_table, context_lens, page_size, shape, p, dev, w,
-                      s)) != PA_OK)
+    if ((st = copy_pages(key_pages, value_pages, block_table, context_lens, page_size, shape, kQ4Pool, p.P2,
+                         p.kv_bytes, p.table_off, dev, w, s)) != PA_OK)
         return st;
     return run_prefill_tc(query, w, w + p.kv_bytes, reinterpret_cast<int32_t*>(w + p.table_off),
                           context_lens, 128, scale, causal, out, p.copy, s,
@@ -1950,6 +1970,236 @@ pa_status pa_attention_q4(const void* query, const void* key_pages, const void* 
     return (route == 0 ? pa_decode_q4 : pa_prefill_q4)(
         query, key_pages, value_pages, block_table, context_lens, page_size, scale, causal, out, shape,
         max_context_len, workspace, workspace_bytes, stream);
+}
+
+namespace {
+
+// A decode behind shared prefixes: whether the prefixes are attended to on copies (pools
+// that the prefix kernel cannot read by TMA, and those that are not bf16), and the
+// workspace: copies with their table, the prefixes' states, the few-row kernel's.
+struct PrefixPlan {
+    bool copies = false;
+    int64_t P2 = 0;
+    int prefix_grid = 0;
+    size_t kv_bytes = 0, table_off = 0, state_off = 0, ml_off = 0, rows_off = 0, total = 0;
+};
+
+constexpr int32_t kMaxPrefixes = 1024;   // their table lies in shared memory
+
+pa_status plan_prefix(const pa_shape& s, int32_t page_size, int kind, int32_t count, int32_t max_prefix_len,
+                      const DeviceInfo* dev, PrefixPlan* p)
+{
+    if (s.batch <= 0 || s.num_q_heads <= 0 || s.num_kv_heads <= 0 || s.q_len <= 0 || s.head_dim <= 0 ||
+        count <= 0 || max_prefix_len <= 0)
+        return PA_ERR_INVALID_ARG;
+    if ((s.head_dim != 128 && (kind != kBf16Pool || s.head_dim != 64)) || !pow2_in(page_size, 1, 256) ||
+        !rows_shape_ok(s) || count > kMaxPrefixes || max_prefix_len >= (1 << 30))
+        return PA_ERR_UNSUPPORTED;
+    const int64_t R = int64_t(s.num_q_heads / s.num_kv_heads) * s.q_len;
+    if (!decode_rows_fits(s, kind, kSuffix, dev->max_smem_optin) || s.batch * R >= (int64_t(1) << 30) ||
+        s.batch * R * s.num_kv_heads >= (int64_t(1) << 31) ||
+        prefix_smem_bytes(s.head_dim, count) > size_t(dev->max_smem_optin))
+        return PA_ERR_UNSUPPORTED;
+    p->copies = kind != kBf16Pool || page_size < 8;
+    p->P2 = (int64_t(max_prefix_len) + kQ4CopyRows - 1) / kQ4CopyRows;
+    if (p->copies) {
+        const int64_t pages = count * p->P2;
+        if (pages * s.num_kv_heads * kQ4CopyRows >= (int64_t(1) << 31))
+            return PA_ERR_UNSUPPORTED;
+        p->kv_bytes = size_t(pages) * s.num_kv_heads * kQ4CopyRows * s.head_dim * 2;
+        p->table_off = 2 * p->kv_bytes;
+        p->state_off = (p->table_off + size_t(pages) * 4 + 255) & ~size_t(255);
+    }
+    // blocks: one an SM, two tiles each at least
+    const int64_t items = s.num_kv_heads * (s.batch * R / 256 + count);
+    const int64_t tiles = items * p->P2;
+    p->prefix_grid = int(std::min<int64_t>(dev->sm_count, tiles));
+    size_t ml = 0;
+    const size_t states = prefix_state_bytes(s, count, p->prefix_grid, &ml);
+    p->ml_off = p->state_off + ml;
+    p->rows_off = (p->state_off + states + 255) & ~size_t(255);
+    p->total = p->rows_off + decode_rows_workspace_bytes(s, kind, kSuffix, dev->sm_count);
+    return PA_OK;
+}
+
+size_t prefix_workspace(const pa_shape& s, int32_t page_size, int kind, int32_t count, int32_t max_prefix_len)
+{
+    DeviceInfo* dev;
+    PrefixPlan p;
+    if (device_info(&dev) != PA_OK || plan_prefix(s, page_size, kind, count, max_prefix_len, dev, &p) != PA_OK)
+        return 0;
+    return p.total;
+}
+
+pa_status run_decode_prefix(const void* query, const void* key_pages, const void* value_pages,
+                            const int32_t* block_table, const int32_t* context_lens, int32_t page_size,
+                            float scale, int kind, float k_scale, float v_scale, const int32_t* prefix_table,
+                            const int32_t* prefix_lens, const int32_t* prefix_starts, int32_t num_prefixes,
+                            int32_t prefix_pages, int32_t max_prefix_len, void* out, const pa_shape& shape,
+                            int32_t max_context_len, void* workspace, size_t workspace_bytes, void* stream)
+{
+    pa_status st = check_attention(query, key_pages, value_pages, block_table, context_lens, page_size, scale,
+                                   out, shape);
+    if (st != PA_OK)
+        return st;
+    if (!prefix_table || !prefix_lens || !prefix_starts || prefix_pages <= 0 ||
+        (kind == kE4m3Pool && bad_scales(k_scale, v_scale)))
+        return PA_ERR_INVALID_ARG;
+    if (int64_t(prefix_pages) * page_size >= (int64_t(1) << 30))
+        return PA_ERR_UNSUPPORTED;
+    DeviceInfo* dev;
+    if ((st = device_info(&dev)) != PA_OK)
+        return st;
+    PrefixPlan p;
+    if ((st = plan_prefix(shape, page_size, kind, num_prefixes, max_prefix_len, dev, &p)) != PA_OK)
+        return st;
+    if (!workspace || workspace_bytes < p.total || (reinterpret_cast<uintptr_t>(workspace) & 255u))
+        return PA_ERR_WORKSPACE;
+    uint8_t* w = static_cast<uint8_t*>(workspace);
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const int D = shape.head_dim;
+
+    PrefixKernelArgs a;
+    memset(&a, 0, sizeof a);
+    a.q = static_cast<const uint16_t*>(query);
+    a.context_lens = context_lens;
+    a.state = reinterpret_cast<float*>(w + p.state_off);
+    a.state_ml = reinterpret_cast<float2*>(w + p.ml_off);
+    a.err = dev->err;
+    a.prefix.table = prefix_table;
+    a.prefix.lens = prefix_lens;
+    a.prefix.starts = prefix_starts;
+    a.prefix.count = num_prefixes;
+    a.prefix.pages = prefix_pages;
+    a.prefix.cap = int32_t(std::min<int64_t>(int64_t(prefix_pages) * page_size, max_prefix_len));
+    a.B = shape.batch;
+    a.H_q = shape.num_q_heads;
+    a.H_kv = shape.num_kv_heads;
+    a.L = shape.q_len;
+    a.G = shape.num_q_heads / shape.num_kv_heads;
+    a.R = a.G * shape.q_len;
+    a.ps = page_size;
+    a.num_pages = shape.num_pages;
+    a.block_ps = page_size;
+    a.max_pages = shape.max_pages;
+    a.scale_log2 = scale * 1.4426950408889634f * k_scale;
+    const PrefixArgs own_table = a.prefix;
+    const void *kp = key_pages, *vp = value_pages;
+    pa_shape pool = shape;
+    if (p.copies) {
+        pa_shape tables = shape;
+        tables.batch = num_prefixes;
+        tables.max_pages = prefix_pages;
+        if ((st = copy_pages(key_pages, value_pages, prefix_table, prefix_lens, page_size, tables, kind, p.P2,
+                             p.kv_bytes, p.table_off, dev, w, s)) != PA_OK)
+            return st;
+        kp = w;
+        vp = w + p.kv_bytes;
+        a.prefix.table = reinterpret_cast<const int32_t*>(w + p.table_off);
+        a.prefix.pages = int32_t(p.P2);
+        a.ps = kQ4CopyRows;
+        a.num_pages = pool.num_pages = int32_t(num_prefixes * p.P2);
+    }
+    a.box_rows = std::min(a.ps, 128);
+    const uint64_t pool_rows = uint64_t(pool.num_pages) * shape.num_kv_heads * a.ps;
+    CUtensorMap kmap, vmap;
+    if ((st = encode_rows_map(&kmap, kp, pool_rows, uint32_t(a.box_rows), uint32_t(D))) != PA_OK ||
+        (st = encode_rows_map(&vmap, vp, pool_rows, uint32_t(a.box_rows), uint32_t(D))) != PA_OK)
+        return st;
+    cudaError_t e = launch_prefix(kmap, vmap, a, D, p.prefix_grid, dev->id, s);
+    if (e != cudaSuccess)
+        return e == cudaErrorNotSupported ? PA_ERR_UNSUPPORTED : PA_ERR_CUDA;
+
+    DecodeArgs d = rows_args(query, block_table, context_lens, page_size, scale * k_scale, 1, out, shape, kind,
+                             kSuffix, dev);
+    d.key_rows = static_cast<const uint8_t*>(key_pages);
+    d.value_rows = static_cast<const uint8_t*>(value_pages);
+    d.prefix = own_table;
+    CUtensorMap skmap = {}, svmap = {};
+    if (kind != kQ4Pool &&
+        ((st = encode_pool_map(&skmap, key_pages, shape, page_size, kind == kE4m3Pool, d.box_rows)) != PA_OK ||
+         (st = encode_pool_map(&svmap, value_pages, shape, page_size, kind == kE4m3Pool, d.box_rows)) != PA_OK))
+        return st;
+    const int grid = decode_rows_launch_grid(
+        shape, kind, max_context_len > 0 ? rows_granules(shape, kind, max_context_len) : 0, dev->sm_count);
+    if (launch_decode_rows(skmap, svmap, d, shape, kind, grid, w + p.rows_off, dev->id, s) != cudaSuccess)
+        return PA_ERR_CUDA;
+
+    PrefixMergeArgs m;
+    memset(&m, 0, sizeof m);
+    m.prefix_args = a;
+    m.prefix_args.prefix = own_table;
+    m.suffix_state = reinterpret_cast<const float*>(w + p.rows_off);
+    m.out = static_cast<uint16_t*>(out);
+    m.out_scale = v_scale;
+    m.prefix_grid = p.prefix_grid;
+    m.suffix_grid = grid;
+    m.MS = (a.R + kSegmentRows - 1) / kSegmentRows;
+    m.per_req = shape.num_kv_heads * m.MS;
+    m.row_tiles = decode_rows_row_tiles(shape);
+    m.tile_keys = decode_rows_tile(shape, kind);
+    m.box_rows = d.box_rows;
+    return launch_prefix_merge(m, D, s) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+}  // namespace
+
+size_t pa_decode_prefix_workspace_bytes(pa_shape shape, int32_t page_size, int32_t num_prefixes,
+                                        int32_t max_prefix_len)
+{
+    return prefix_workspace(shape, page_size, kBf16Pool, num_prefixes, max_prefix_len);
+}
+
+size_t pa_decode_prefix_fp8_workspace_bytes(pa_shape shape, int32_t page_size, int32_t num_prefixes,
+                                            int32_t max_prefix_len)
+{
+    return prefix_workspace(shape, page_size, kE4m3Pool, num_prefixes, max_prefix_len);
+}
+
+size_t pa_decode_prefix_q4_workspace_bytes(pa_shape shape, int32_t page_size, int32_t num_prefixes,
+                                           int32_t max_prefix_len)
+{
+    return prefix_workspace(shape, page_size, kQ4Pool, num_prefixes, max_prefix_len);
+}
+
+pa_status pa_decode_prefix(const void* query, const void* key_pages, const void* value_pages,
+                           const int32_t* block_table, const int32_t* context_lens, int32_t page_size,
+                           float scale, const int32_t* prefix_table, const int32_t* prefix_lens,
+                           const int32_t* prefix_starts, int32_t num_prefixes, int32_t prefix_pages,
+                           int32_t max_prefix_len, void* out, pa_shape shape, int32_t max_context_len,
+                           void* workspace, size_t workspace_bytes, void* stream)
+{
+    return run_decode_prefix(query, key_pages, value_pages, block_table, context_lens, page_size, scale,
+                             kBf16Pool, 1.f, 1.f, prefix_table, prefix_lens, prefix_starts, num_prefixes,
+                             prefix_pages, max_prefix_len, out, shape, max_context_len, workspace,
+                             workspace_bytes, stream);
+}
+
+pa_status pa_decode_prefix_fp8(const void* query, const void* key_pages, const void* value_pages,
+                               const int32_t* block_table, const int32_t* context_lens, int32_t page_size,
+                               float scale, float k_scale, float v_scale, const int32_t* prefix_table,
+                               const int32_t* prefix_lens, const int32_t* prefix_starts,
+                               int32_t num_prefixes, int32_t prefix_pages, int32_t max_prefix_len, void* out,
+                               pa_shape shape, int32_t max_context_len, void* workspace,
+                               size_t workspace_bytes, void* stream)
+{
+    return run_decode_prefix(query, key_pages, value_pages, block_table, context_lens, page_size, scale,
+                             kE4m3Pool, k_scale, v_scale, prefix_table, prefix_lens, prefix_starts,
+                             num_prefixes, prefix_pages, max_prefix_len, out, shape, max_context_len, workspace,
+                             workspace_bytes, stream);
+}
+
+pa_status pa_decode_prefix_q4(const void* query, const void* key_pages, const void* value_pages,
+                              const int32_t* block_table, const int32_t* context_lens, int32_t page_size,
+                              float scale, const int32_t* prefix_table, const int32_t* prefix_lens,
+                              const int32_t* prefix_starts, int32_t num_prefixes, int32_t prefix_pages,
+                              int32_t max_prefix_len, void* out, pa_shape shape, int32_t max_context_len,
+                              void* workspace, size_t workspace_bytes, void* stream)
+{
+    return run_decode_prefix(query, key_pages, value_pages, block_table, context_lens, page_size, scale,
+                             kQ4Pool, 1.f, 1.f, prefix_table, prefix_lens, prefix_starts, num_prefixes,
+                             prefix_pages, max_prefix_len, out, shape, max_context_len, workspace,
+                             workspace_bytes, stream);
 }
 
 pa_status pa_decode_dense(const void* query, const void* key_dense, const void* value_dense,

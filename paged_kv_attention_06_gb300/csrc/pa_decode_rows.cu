@@ -78,7 +78,7 @@ int decode_rows_grid(const pa_shape& s, int kind, int sm_count)
 
 int decode_rows_box(const pa_shape& s, int kind, int page_size)
 {
-    const int tok = kind == kBf16Pool && s.head_dim == 128 ? 16 : 32;
+    const int tok = decode_rows_tile(s, kind);
     return page_size < tok ? page_size : tok;
 }
 
@@ -88,6 +88,10 @@ size_t decode_rows_workspace_bytes(const pa_shape& s, int kind, int mode, int sm
     return (size_t(s.batch) * s.num_kv_heads * size_t(MS) + size_t(decode_rows_grid(s, kind, sm_count))) *
            rows::facts(s.head_dim, kind, rows::row_tiles(s), 1, mode).slab;
 }
+
+int decode_rows_tile(const pa_shape& s, int kind) { return kind == kBf16Pool && s.head_dim == 128 ? 16 : 32; }
+
+int decode_rows_row_tiles(const pa_shape& s) { return rows::row_tiles(s); }
 
 int decode_rows_launch_grid(const pa_shape& s, int kind, int64_t granule_bound, int sm_count)
 {

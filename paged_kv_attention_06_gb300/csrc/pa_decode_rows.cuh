@@ -370,7 +370,7 @@ __global__ void __launch_bounds__(kThreads, (Smem<D, KIND, NT>::kBlocksPerSM))
                 const int n = clamp_context(a.context_lens[b], cap, a.err);
                 int first = 0;
                 if constexpr (kMode == kSuffix)
-                    firsts[b] = first = min(prefix_of(a.prefix, b), n);
+                    firsts[b] = first = min(prefix_len_of(a.prefix, b), n);
                 gs = tile_span<kTok, kMode>(a, n, first).granules;
                 gbr[b] = gs;
                 len[b] = n;
@@ -389,7 +389,8 @@ __global__ void __launch_bounds__(kThreads, (Smem<D, KIND, NT>::kBlocksPerSM))
     }
     __syncthreads();
     const int64_t units = pre[a.B] + int64_t(kPieceUnits) * a.B * per_req;
-    const int64_t grid = int64_t(gridDim.x) < units ? int64_t(gridDim.x) : units;
+    const int64_t grid = kMode == kSuffix ? suffix_blocks(units, int(gridDim.x))
+                                          : int64_t(gridDim.x) < units ? int64_t(gridDim.x) : units;
     const int64_t cta = blockIdx.x;
     if (cta >= grid) {
         if constexpr (kMode == kSuffix)

@@ -19,6 +19,7 @@ constexpr unsigned PA_DEVERR_SLOT_BIT = 0x2u;
 constexpr unsigned PA_DEVERR_CONTEXT_LEN_BIT = 0x4u;
 constexpr unsigned PA_DEVERR_TIMEOUT_BIT = 0x8u;
 constexpr unsigned PA_DEVERR_POSITION_BIT = 0x10u;
+constexpr unsigned PA_DEVERR_PREFIX_BIT = 0x20u;
 
 // Longest a kernel waits for one pipeline phase before giving up, and the
 // limit of every later wait of a block that already gave up once.
@@ -113,13 +114,14 @@ struct GatherArgs {
 cudaError_t launch_gather(const GatherArgs& a, cudaStream_t stream);
 
 // 4-bit pools (pa_q4.cuh): the quantising append (AppendArgs, pages of 80-byte rows,
-// D 128), and the read-back of every request's rows as bf16. Row t of (request b,
+// D 128), and the read-back of every request's rows as bf16 (kind; bf16 pools also with
+// head_dim 64: rows of D elements then). Row t of (request b,
 // KV head h) goes to element b * batch_stride + h * head_stride + (t / 128) * block_stride
-// + (t % 128) * 128: dense rows, or pages of 128 tokens with a table (table_out
+// + (t % 128) * D: dense rows, or pages of 128 tokens with a table (table_out
 // [B, copy_pages], page b * copy_pages + t / 128; rows of a bad page are zeros there).
 constexpr int kQ4CopyRows = 128;
-struct Q4ReadArgs {
-    const uint8_t* key_pages;     // [P, H_kv, ps, 80]
+struct PageReadArgs {
+    const uint8_t* key_pages;     // [P, H_kv, ps, row bytes]
     const uint8_t* value_pages;
     const int32_t* block_table;   // [B, max_pages]
     const int32_t* context_lens;  // [B]
@@ -134,7 +136,7 @@ struct Q4ReadArgs {
     int32_t chunks;               // set by the launcher
 };
 cudaError_t launch_append_q4(const AppendArgs& a, cudaStream_t stream);
-cudaError_t launch_read_q4(Q4ReadArgs a, cudaStream_t stream);
+cudaError_t launch_read_pages(PageReadArgs a, int kind, int D, cudaStream_t stream);
 
 // ---------------------------------------------------------------------------
 // Split-KV attention (decode schedule)
@@ -240,10 +242,42 @@ bool decode_rows_takes(const pa_shape& s, int max_smem);
 bool decode_rows_fits(const pa_shape& s, int kind, int mode, int max_smem);
 int decode_rows_box(const pa_shape& s, int kind, int page_size);
 size_t decode_rows_workspace_bytes(const pa_shape& s, int kind, int mode, int sm_count);
+int decode_rows_tile(const pa_shape& s, int kind);     // keys of a tile
+int decode_rows_row_tiles(const pa_shape& s);          // 8-row tiles of a segment
 int decode_rows_launch_grid(const pa_shape& s, int kind, int64_t granule_bound, int sm_count);
 cudaError_t launch_decode_rows(const CUtensorMap& key_map, const CUtensorMap& value_map, DecodeArgs a,
                                const pa_shape& s, int kind, int grid, void* workspace, int device,
                                cudaStream_t stream);
+
+// Decode behind shared prefixes: the prefixes' part for all their requests' rows, and
+// the merge of it with the few-row kernel's (kSuffix).
+struct PrefixKernelArgs {
+    const uint16_t* q;            // [B, H_q, L, D]
+    const int32_t* context_lens;  // [B]
+    float* state;                 // [slot][256 rows][D]
+    float2* state_ml;             // [slot][256] (max, sum)
+    unsigned* err;
+    PrefixArgs prefix;            // table of the pages that the maps lead to
+    int32_t B, H_q, H_kv, L, G, R;
+    int32_t ps, num_pages;        // of those pages
+    int32_t box_rows;             // min(ps, 128), at least 8
+    int32_t block_ps, max_pages;  // of the requests' own tables
+    float scale_log2;
+};
+struct PrefixMergeArgs {
+    PrefixKernelArgs prefix_args;
+    const float* suffix_state;    // [slot][row_tiles * 8 * (D + 2)]
+    uint16_t* out;                // [B, H_q, L, D]
+    float out_scale;
+    int32_t prefix_grid, suffix_grid;
+    int32_t MS, per_req, row_tiles, tile_keys, box_rows;   // of the few-row kernel
+};
+size_t prefix_smem_bytes(int D, int count);
+// The states' workspace, and where (m, l) start in it.
+size_t prefix_state_bytes(const pa_shape& s, int count, int grid, size_t* ml_off);
+cudaError_t launch_prefix(const CUtensorMap& key_map, const CUtensorMap& value_map, const PrefixKernelArgs& a,
+                          int D, int grid, int device, cudaStream_t stream);
+cudaError_t launch_prefix_merge(const PrefixMergeArgs& a, int D, cudaStream_t stream);
 
 // Accumulation of attention weights: weight_pages[slot of j] = decay * old (0
 // for the L newest positions, or where decay is 0) + sum over the R rows of

@@ -6,26 +6,17 @@
 
 namespace pa {
 
-// Prefix p belongs to the requests starts[p] .. starts[p + 1] - 1. Where the starts do
-// not ascend within the batch (PA_DEVERR_PREFIX), each is taken as the largest so
-// far, so that both kernels see the same division.
-__device__ __forceinline__ int prefix_start(const PrefixArgs& x, int p, int B)
-{
-    const int s = __ldg(x.starts + p);
-    return s < 0 ? 0 : s > B ? B : s;
-}
-
 __device__ __forceinline__ int prefix_len(const PrefixArgs& x, int p)
 {
     const int n = __ldg(x.lens + p);
     return n < 0 ? 0 : n > x.cap ? x.cap : n;
 }
 
-// Tokens of request b's prefix; 0 where it has none.
+// The prefix of request b: starts[p] <= b < starts[p + 1]; -1 where it has none.
 __device__ __forceinline__ int prefix_of(const PrefixArgs& x, int b)
 {
     if (x.count == 0 || b < __ldg(x.starts) || b >= __ldg(x.starts + x.count))
-        return 0;
+        return -1;
     int lo = 0, hi = x.count;              // starts[lo] <= b < starts[hi]
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
@@ -34,7 +25,28 @@ __device__ __forceinline__ int prefix_of(const PrefixArgs& x, int b)
         else
             hi = mid;
     }
-    return prefix_len(x, lo);
+    return lo;
+}
+
+__device__ __forceinline__ int prefix_len_of(const PrefixArgs& x, int b)
+{
+    const int p = prefix_of(x, b);
+    return p < 0 ? 0 : prefix_len(x, p);
+}
+
+// The few-row kernel behind a prefix: granules (four tiles of tile_keys) of the keys
+// first .. n - 1, from the box that holds the first; and the blocks that share units of
+// work, two units a block at least.
+__device__ __forceinline__ int suffix_granules(int n, int first, int box_rows, int tile_keys)
+{
+    const int start = first < n ? first & ~(box_rows - 1) : n;
+    const int tiles = (n - start + tile_keys - 1) / tile_keys;
+    return max(1, (tiles + 3) / 4);
+}
+__device__ __forceinline__ int64_t suffix_blocks(int64_t units, int grid)
+{
+    const int64_t most = (units + 1) / 2;
+    return most < grid ? most : grid;
 }
 
 // Floats of a few-row state left as rows: O [8 NT][D], then (m, l) of each row.

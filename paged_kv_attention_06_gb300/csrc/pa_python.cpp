@@ -1,6 +1,6 @@
 // The Python side of the calls that take a model's step from the projection to
 // the evicted cache (pa_qk_norm_rope_append, the window and weight calls,
-// pa_kv_evict) and of the 4-bit pools' calls: argument checks, the tensors that a call makes where none are
+// pa_kv_evict), of the 4-bit pools' calls and of the decode behind shared prefixes: argument checks, the tensors that a call makes where none are
 // given (outputs, a workspace of this call alone, both made on the device of the
 // call and for its stream), and the call of the C ABI on that device and stream. An
 // append of one token takes 2.1 us on the GPU; a call of it 3.4 us, 10.7 with these
@@ -499,6 +499,51 @@ PyObject* attention_q4(PyObject*, PyObject* const* a, Py_ssize_t n)
     });
 }
 
+// kind (0 bf16, 1 e4m3, 2 4-bit pools), query, key_pages, value_pages, block_table, context_lens,
+// page_size, k_scale, v_scale, prefix_table, prefix_lens, prefix_starts, max_prefix_len (None: the
+// table's width), scale, out, max_context_len, workspace, stream
+PyObject* prefix(PyObject*, PyObject* const* a, Py_ssize_t n)
+{
+    return guarded([&]() -> PyObject* {
+        check_args(n, 18);
+        const int32_t which = integer(a[0], "kind");
+        const Pool kind = which == 0 ? Pool::kBf16 : which == 1 ? Pool::kE4m3 : Pool::kQ4;
+        Paged p(a + 1, a[4], a[5], a[6], kind, a[13], a[14], a[17]);
+        const at::Tensor &table = tensor(a[9], "prefix_table"), &lens = tensor(a[10], "prefix_lens"),
+                         &starts = tensor(a[11], "prefix_starts");
+        if (table.dim() != 2 || !shape_is(lens, {table.size(0)}) || !shape_is(starts, {table.size(0) + 1}))
+            value_error("prefix_table must be [num_prefixes, prefix_pages], prefix_lens [num_prefixes] and "
+                        "prefix_starts [num_prefixes + 1]");
+        const int32_t* pt = static_cast<int32_t*>(p.call.check(table, at::kInt, "prefix_table"));
+        const int32_t* pl = static_cast<int32_t*>(p.call.check(lens, at::kInt, "prefix_lens"));
+        const int32_t* pst = static_cast<int32_t*>(p.call.check(starts, at::kInt, "prefix_starts"));
+        const int32_t count = size32(table.size(0), "num_prefixes"), pages = size32(table.size(1), "prefix_pages");
+        const int32_t most = a[12] == Py_None ? size32(int64_t(pages) * p.ps, "max_prefix_len")
+                                              : integer(a[12], "max_prefix_len");
+        const int32_t longest = integer(a[15], "max_context_len");
+        const float ks = which == 1 ? float(number(a[7])) : 1.f, vs = which == 1 ? float(number(a[8])) : 1.f;
+        size_t need = 0;
+        if (a[16] == Py_None)
+            need = (which == 0   ? pa_decode_prefix_workspace_bytes
+                    : which == 1 ? pa_decode_prefix_fp8_workspace_bytes
+                                 : pa_decode_prefix_q4_workspace_bytes)(p.shape, p.ps, count, most);
+        const at::Tensor workspace = p.call.workspace(a[16], need);
+        const size_t bytes = workspace.nbytes();
+        void *out = p.out.data_ptr(), *ws = workspace.data_ptr();
+        const pa_status st = unlocked([&] {
+            return which == 1 ? pa_decode_prefix_fp8(p.q, p.k, p.v, p.table(), p.lens(), p.ps, p.scale, ks, vs, pt, pl,
+                                                     pst, count, pages, most, out, p.shape, longest, ws, bytes,
+                                                     p.call.stream)
+                              : (which == 0 ? pa_decode_prefix : pa_decode_prefix_q4)(
+                                    p.q, p.k, p.v, p.table(), p.lens(), p.ps, p.scale, pt, pl, pst, count, pages, most,
+                                    out, p.shape, longest, ws, bytes, p.call.stream);
+        });
+        if (raised(st, which == 0 ? "pa_decode_prefix" : which == 1 ? "pa_decode_prefix_fp8" : "pa_decode_prefix_q4"))
+            return nullptr;
+        return THPVariable_Wrap(p.out);
+    });
+}
+
 // query, key_pages, value_pages, weight_pages, block_table, context_lens, page_size, k_scale,
 // v_scale (None: bf16 pools), max_context_len, decay, scale, causal, out, workspace, stream
 PyObject* weights(PyObject*, PyObject* const* a, Py_ssize_t n)
@@ -611,6 +656,7 @@ PyMethodDef g_methods[] = {
     {"append_q4", fast(append_q4), METH_FASTCALL, "pa_append_kv_q4"},
     {"gather_q4", fast(gather_q4), METH_FASTCALL, "pa_gather_kv_q4"},
     {"attention_q4", fast(attention_q4), METH_FASTCALL, "the attention calls over 4-bit pools"},
+    {"prefix", fast(prefix), METH_FASTCALL, "pa_decode_prefix and its e4m3 and 4-bit forms"},
     {"set_error", set_error, METH_O, "the class raised for a pa_status"},
     {nullptr, nullptr, 0, nullptr},
 };

@@ -151,11 +151,16 @@ __device__ __forceinline__ uint4 values8(uint32_t codes, uint32_t params)
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// One block per (request, KV head, kReadTokens tokens), 16 lanes a row.
+// One block per (request, KV head, kReadTokens tokens), 16 lanes a row (8 where D is
+// 64). bf16 pools (kQ4 false): rows as they are, for pages that the kernels above them
+// cannot read by TMA.
 constexpr int kReadTokens = 64;
 
-__global__ void __launch_bounds__(256) read_q4_kernel(const Q4ReadArgs a)
+template <bool kQ4, int D>
+__global__ void __launch_bounds__(256) read_pages_kernel(const PageReadArgs a)
 {
+    constexpr int kLanes = D / 8, kRowsAtOnce = 256 / kLanes;
+    constexpr int kRowBytes = kQ4 ? kQ4RowBytes : 2 * D;
     grid_dependency_wait();
     grid_launch_dependents();
     const int chunks = a.chunks;
@@ -175,15 +180,15 @@ __global__ void __launch_bounds__(256) read_q4_kernel(const Q4ReadArgs a)
     if (t0 >= n)
         return;
     const int32_t* bt = a.block_table + int64_t(b) * a.max_pages;
-    const int c = threadIdx.x & 15, row = threadIdx.x >> 4;
-    constexpr int kRounds = kReadTokens / 16;
-    uint32_t kc[kRounds], vc[kRounds], kpar[kRounds], vpar[kRounds];
+    const int c = threadIdx.x % kLanes, row = threadIdx.x / kLanes;
+    constexpr int kRounds = kReadTokens / kRowsAtOnce;
+    uint4 kx[kRounds], vx[kRounds];         // 4-bit rows: x the codes, y the parameters
     bool live[kRounds];
 #pragma unroll
     for (int k = 0; k < kRounds; ++k) {
-        const int t = t0 + 16 * k + row;
+        const int t = t0 + kRowsAtOnce * k + row;
         live[k] = t < n;
-        kc[k] = vc[k] = kpar[k] = vpar[k] = 0;
+        kx[k] = vx[k] = make_uint4(0, 0, 0, 0);
         if (live[k]) {
             const int lp = t / a.ps;
             const int phys = bt[lp];
@@ -193,11 +198,16 @@ __global__ void __launch_bounds__(256) read_q4_kernel(const Q4ReadArgs a)
                 live[k] = a.table_out != nullptr;      // a copy's row: zeros; a dense row: left
                 continue;
             }
-            const int64_t src = ((int64_t(phys) * a.H_kv + h) * a.ps + (t - lp * a.ps)) * kQ4RowBytes;
-            kc[k] = *reinterpret_cast<const uint32_t*>(a.key_pages + src + c * 4);
-            vc[k] = *reinterpret_cast<const uint32_t*>(a.value_pages + src + c * 4);
-            kpar[k] = *reinterpret_cast<const uint32_t*>(a.key_pages + src + kQ4CodeBytes + (c & 12));
-            vpar[k] = *reinterpret_cast<const uint32_t*>(a.value_pages + src + kQ4CodeBytes + (c & 12));
+            const int64_t src = ((int64_t(phys) * a.H_kv + h) * a.ps + (t - lp * a.ps)) * kRowBytes;
+            if constexpr (kQ4) {
+                kx[k].x = *reinterpret_cast<const uint32_t*>(a.key_pages + src + c * 4);
+                vx[k].x = *reinterpret_cast<const uint32_t*>(a.value_pages + src + c * 4);
+                kx[k].y = *reinterpret_cast<const uint32_t*>(a.key_pages + src + kQ4CodeBytes + (c & 12));
+                vx[k].y = *reinterpret_cast<const uint32_t*>(a.value_pages + src + kQ4CodeBytes + (c & 12));
+            } else {
+                kx[k] = *reinterpret_cast<const uint4*>(a.key_pages + src + c * 16);
+                vx[k] = *reinterpret_cast<const uint4*>(a.value_pages + src + c * 16);
+            }
         }
     }
     // rows from a pointer of their 128-token block: dense rows follow on, copy pages
@@ -207,10 +217,10 @@ __global__ void __launch_bounds__(256) read_q4_kernel(const Q4ReadArgs a)
     for (int k = 0; k < kRounds; ++k) {
         if (!live[k])
             continue;
-        const int t = t0 + 16 * k + row;
-        const int64_t dst = base + int64_t(t / kQ4CopyRows) * a.block_stride + int64_t(t % kQ4CopyRows) * 128;
-        *reinterpret_cast<uint4*>(a.key_out + dst) = values8(kc[k], kpar[k]);
-        *reinterpret_cast<uint4*>(a.value_out + dst) = values8(vc[k], vpar[k]);
+        const int t = t0 + kRowsAtOnce * k + row;
+        const int64_t dst = base + int64_t(t / kQ4CopyRows) * a.block_stride + int64_t(t % kQ4CopyRows) * D;
+        *reinterpret_cast<uint4*>(a.key_out + dst) = kQ4 ? values8(kx[k].x, kx[k].y) : kx[k];
+        *reinterpret_cast<uint4*>(a.value_out + dst) = kQ4 ? values8(vx[k].x, vx[k].y) : vx[k];
     }
 }
 
@@ -236,7 +246,7 @@ cudaError_t launch_append_q4(const AppendArgs& a, cudaStream_t stream)
     return cudaLaunchKernelEx(&cfg, append_q4_kernel, a);
 }
 
-cudaError_t launch_read_q4(Q4ReadArgs a, cudaStream_t stream)
+cudaError_t launch_read_pages(PageReadArgs a, int kind, int D, cudaStream_t stream)
 {
     a.chunks = int32_t((int64_t(a.max_len) + kReadTokens - 1) / kReadTokens);
     const int64_t blocks = int64_t(a.B) * a.H_kv * a.chunks;
@@ -251,7 +261,11 @@ cudaError_t launch_read_q4(Q4ReadArgs a, cudaStream_t stream)
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, read_q4_kernel, a);
+    return cudaLaunchKernelEx(&cfg,
+                              kind == kQ4Pool ? read_pages_kernel<true, 128>
+                              : D == 64       ? read_pages_kernel<false, 64>
+                                              : read_pages_kernel<false, 128>,
+                              a);
 }
 
 }  // namespace pa
