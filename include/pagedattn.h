@@ -690,16 +690,16 @@ pa_status pa_attention_q4(const void *query, const void *key_pages, const void *
  *                  not read and may hold anything.
  *   context_lens   positions in all, prefix included; a request may be shorter than its
  *                  prefix (or empty): its rows see what they see.
- *   num_prefixes   1 .. 1024;  max_prefix_len > 0 bounds prefix_lens and sizes the
+ *   num_prefixes   1 .. 256;  max_prefix_len > 0 bounds prefix_lens and sizes the
  *                  workspace.
  *   workspace      ..._workspace_bytes(shape, page_size, num_prefixes, max_prefix_len)
  *                  bytes (0: invalid or unsupported sizes), 256-byte aligned, any
  *                  contents; calls that share one must not overlap on the GPU.
- * Other arguments and errors as for pa_decode / pa_decode_fp8 / pa_decode_q4. Built for
- * few rows a request; any L is computed. Three kernels on `stream`; one more
- * before them copies the prefixes into bf16 pages of 128 tokens in the workspace where
- * the pool is not bf16 (e4m3 exactly, 4-bit values rounded to bf16) or its pages hold
- * fewer than 8 tokens.
+ * Other arguments and errors as for pa_decode / pa_decode_fp8 / pa_decode_q4. Codes are
+ * turned into f16 (e4m3 exactly; a prefix's 4-bit values m + s c rounded once), as are the
+ * query and the softmax weights over them. Built for few rows a request; any L is
+ * computed. Three kernels on `stream`; where a bf16 pool's pages hold fewer than 8
+ * tokens, one more before them copies the prefixes into pages of 128 in the workspace.
  */
 size_t pa_decode_prefix_workspace_bytes(pa_shape shape, int32_t page_size, int32_t num_prefixes,
                                         int32_t max_prefix_len);

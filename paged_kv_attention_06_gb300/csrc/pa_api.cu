@@ -17,6 +17,7 @@
 #include "../../include/pagedattn.h"
 #include "../../include/pagedattn_test.h"
 #include "pa_internal.h"
+#include "pa_q4.cuh"
 
 namespace pa {
 
@@ -1778,25 +1779,6 @@ pa_status copy_pages(const void* key_pages, const void* value_pages, const int32
                      int64_t P2, size_t kv_bytes, size_t table_off, const DeviceInfo* dev, uint8_t* w,
                      cudaStream_t stream)
 {
-    if (kind == kE4m3Pool) {
-        Fp8PagesArgs c;
-        memset(&c, 0, sizeof c);
-        c.key_pages = static_cast<const uint8_t*>(key_pages);
-        c.value_pages = static_cast<const uint8_t*>(value_pages);
-        c.block_table = block_table;
-        c.context_lens = context_lens;
-        c.key_out = reinterpret_cast<uint16_t*>(w);
-        c.value_out = reinterpret_cast<uint16_t*>(w + kv_bytes);
-        c.table_out = reinterpret_cast<int32_t*>(w + table_off);
-        c.err = dev->err;
-        c.B = s.batch;
-        c.H_kv = s.num_kv_heads;
-        c.ps = page_size;
-        c.max_pages = s.max_pages;
-        c.num_pages = s.num_pages;
-        c.P2 = int32_t(P2);
-        return launch_fp8_pages_to_bf16(c, stream) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
-    }
     PageReadArgs a = page_read_args(key_pages, value_pages, block_table, context_lens, page_size, s, dev);
     a.key_out = reinterpret_cast<uint16_t*>(w);
     a.value_out = reinterpret_cast<uint16_t*>(w + kv_bytes);
@@ -1981,10 +1963,12 @@ struct PrefixPlan {
     bool copies = false;
     int64_t P2 = 0;
     int prefix_grid = 0;
-    size_t kv_bytes = 0, table_off = 0, state_off = 0, ml_off = 0, rows_off = 0, total = 0;
+    int32_t items = 0;
+    size_t kv_bytes = 0, table_off = 0, state_off = 0, ml_off = 0, pieces_off = 0, note_off = 0, rows_off = 0,
+           total = 0;
 };
 
-constexpr int32_t kMaxPrefixes = 1024;   // their table lies in shared memory
+constexpr int32_t kMaxPrefixes = 256;    // their table lies in shared memory
 
 pa_status plan_prefix(const pa_shape& s, int32_t page_size, int kind, int32_t count, int32_t max_prefix_len,
                       const DeviceInfo* dev, PrefixPlan* p)
@@ -1998,9 +1982,9 @@ pa_status plan_prefix(const pa_shape& s, int32_t page_size, int kind, int32_t co
     const int64_t R = int64_t(s.num_q_heads / s.num_kv_heads) * s.q_len;
     if (!decode_rows_fits(s, kind, kSuffix, dev->max_smem_optin) || s.batch * R >= (int64_t(1) << 30) ||
         s.batch * R * s.num_kv_heads >= (int64_t(1) << 31) ||
-        prefix_smem_bytes(s.head_dim, count) > size_t(dev->max_smem_optin))
+        prefix_smem_bytes(s.head_dim, kind, count) > size_t(dev->max_smem_optin))
         return PA_ERR_UNSUPPORTED;
-    p->copies = kind != kBf16Pool || page_size < 8;
+    p->copies = kind == kBf16Pool && page_size < 8;
     p->P2 = (int64_t(max_prefix_len) + kQ4CopyRows - 1) / kQ4CopyRows;
     if (p->copies) {
         const int64_t pages = count * p->P2;
@@ -2012,12 +1996,18 @@ pa_status plan_prefix(const pa_shape& s, int32_t page_size, int kind, int32_t co
     }
     // blocks: one an SM, two tiles each at least
     const int64_t items = s.num_kv_heads * (s.batch * R / 256 + count);
-    const int64_t tiles = items * p->P2;
-    p->prefix_grid = int(std::min<int64_t>(dev->sm_count, tiles));
-    size_t ml = 0;
-    const size_t states = prefix_state_bytes(s, count, p->prefix_grid, &ml);
+    p->prefix_grid = int(std::min<int64_t>(dev->sm_count, items * p->P2));
+    if (items * prefix_item_units(p->P2) >= (int64_t(1) << 31))   // units are 32-bit numbers
+        return PA_ERR_UNSUPPORTED;
+    p->items = int32_t(items);
+    size_t ml = 0, pieces = 0;
+    const size_t states = prefix_state_bytes(s, items, p->prefix_grid, &ml, &pieces);
     p->ml_off = p->state_off + ml;
-    p->rows_off = (p->state_off + states + 255) & ~size_t(255);
+    p->pieces_off = p->state_off + pieces;
+    // notes for the merge: an int4 a request, an int2 an item and a segment
+    const int64_t segments = int64_t(s.batch) * s.num_kv_heads * ((R + kSegmentRows - 1) / kSegmentRows);
+    p->note_off = (p->state_off + states + 255) & ~size_t(255);
+    p->rows_off = (p->note_off + size_t(s.batch) * 16 + size_t(items + segments) * 8 + 255) & ~size_t(255);
     p->total = p->rows_off + decode_rows_workspace_bytes(s, kind, kSuffix, dev->sm_count);
     return PA_OK;
 }
@@ -2065,6 +2055,10 @@ pa_status run_decode_prefix(const void* query, const void* key_pages, const void
     a.context_lens = context_lens;
     a.state = reinterpret_cast<float*>(w + p.state_off);
     a.state_ml = reinterpret_cast<float2*>(w + p.ml_off);
+    a.more_pieces = w + p.pieces_off;
+    a.most_items = p.items;
+    a.note_request = reinterpret_cast<int4*>(w + p.note_off);
+    a.note_item = reinterpret_cast<int2*>(a.note_request + shape.batch);
     a.err = dev->err;
     a.prefix.table = prefix_table;
     a.prefix.lens = prefix_lens;
@@ -2102,11 +2096,18 @@ pa_status run_decode_prefix(const void* query, const void* key_pages, const void
     }
     a.box_rows = std::min(a.ps, 128);
     const uint64_t pool_rows = uint64_t(pool.num_pages) * shape.num_kv_heads * a.ps;
-    CUtensorMap kmap, vmap;
-    if ((st = encode_rows_map(&kmap, kp, pool_rows, uint32_t(a.box_rows), uint32_t(D))) != PA_OK ||
-        (st = encode_rows_map(&vmap, vp, pool_rows, uint32_t(a.box_rows), uint32_t(D))) != PA_OK)
+    CUtensorMap kmap = {}, vmap = {};
+    if (kind == kBf16Pool &&
+        ((st = encode_rows_map(&kmap, kp, pool_rows, uint32_t(a.box_rows), uint32_t(D))) != PA_OK ||
+         (st = encode_rows_map(&vmap, vp, pool_rows, uint32_t(a.box_rows), uint32_t(D))) != PA_OK))
         return st;
-    cudaError_t e = launch_prefix(kmap, vmap, a, D, p.prefix_grid, dev->id, s);
+    a.key_rows = static_cast<const uint8_t*>(key_pages);
+    a.value_rows = static_cast<const uint8_t*>(value_pages);
+    while ((1 << a.ps_shift) < a.ps)
+        ++a.ps_shift;
+    a.by_R.set(a.R);
+    a.by_L.set(a.L);
+    cudaError_t e = launch_prefix(kmap, vmap, a, D, kind, p.prefix_grid, dev->id, s);
     if (e != cudaSuccess)
         return e == cudaErrorNotSupported ? PA_ERR_UNSUPPORTED : PA_ERR_CUDA;
 
@@ -2115,6 +2116,7 @@ pa_status run_decode_prefix(const void* query, const void* key_pages, const void
     d.key_rows = static_cast<const uint8_t*>(key_pages);
     d.value_rows = static_cast<const uint8_t*>(value_pages);
     d.prefix = own_table;
+    d.note_segment = a.note_item + p.items;
     CUtensorMap skmap = {}, svmap = {};
     if (kind != kQ4Pool &&
         ((st = encode_pool_map(&skmap, key_pages, shape, page_size, kind == kE4m3Pool, d.box_rows)) != PA_OK ||
@@ -2128,18 +2130,14 @@ pa_status run_decode_prefix(const void* query, const void* key_pages, const void
     PrefixMergeArgs m;
     memset(&m, 0, sizeof m);
     m.prefix_args = a;
-    m.prefix_args.prefix = own_table;
     m.suffix_state = reinterpret_cast<const float*>(w + p.rows_off);
     m.out = static_cast<uint16_t*>(out);
     m.out_scale = v_scale;
-    m.prefix_grid = p.prefix_grid;
-    m.suffix_grid = grid;
+    m.note_segment = d.note_segment;
+    m.by_H.set(shape.num_kv_heads);
     m.MS = (a.R + kSegmentRows - 1) / kSegmentRows;
-    m.per_req = shape.num_kv_heads * m.MS;
     m.row_tiles = decode_rows_row_tiles(shape);
-    m.tile_keys = decode_rows_tile(shape, kind);
-    m.box_rows = d.box_rows;
-    return launch_prefix_merge(m, D, s) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+    return launch_prefix_merge(m, D, dev->sm_count, s) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
 }  // namespace

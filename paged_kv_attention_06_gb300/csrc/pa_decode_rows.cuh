@@ -967,9 +967,15 @@ __global__ void __launch_bounds__(kThreads, (Smem<D, KIND, NT>::kBlocksPerSM))
         __syncthreads();                             // the piece before has read the slabs
         st.gather(reinterpret_cast<float*>(smem + Lay::kSlabs), warp, lane);
         if (warp == 0 && !misc[0]) {
-            if constexpr (kMode == kSuffix)
+            if constexpr (kMode == kSuffix) {
                 st.template put_rows<KIND>(a.partials + (int64_t(sp.seg) + cta) * kSlot, rows, lane);
-            else if (sp.seg_start >= p0.x && sp.seg_start + sp.seg_len <= x_end)
+                if (lane == 0) {
+                    if (sp.seg_start >= p0.x)
+                        a.note_segment[sp.seg].x = int(cta);
+                    if (sp.seg_start + sp.seg_len <= x_end)
+                        a.note_segment[sp.seg].y = int(cta);
+                }
+            } else if (sp.seg_start >= p0.x && sp.seg_start + sp.seg_len <= x_end)
                 st.template write<KIND, kMode>(a, int64_t(sp.b) * a.H_kv + sp.h, q_row0, rows, lane);
             else                                     // a slot of its own: segment and block
                 st.put(a.partials + (int64_t(sp.seg) + cta) * kSlot, lane);

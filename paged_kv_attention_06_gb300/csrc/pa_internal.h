@@ -221,6 +221,7 @@ struct DecodeArgs {
     const uint8_t* key_rows;      // 4-bit pools
     const uint8_t* value_rows;
     PrefixArgs prefix;            // kSuffix
+    int2* note_segment;           // kSuffix: for the merge (PrefixMergeArgs)
     int32_t debug_unset_wait;  // test support: block 0 first waits on a barrier
                                // that nothing arrives at (times out, flags)
 };
@@ -249,6 +250,23 @@ cudaError_t launch_decode_rows(const CUtensorMap& key_map, const CUtensorMap& va
                                const pa_shape& s, int kind, int grid, void* workspace, int device,
                                cudaStream_t stream);
 
+// Division of 0 .. 2^31 - 1 by a fixed number: with s = ceil(log2 d), m = floor(2^32 (2^s - d)
+// / d) + 1 the quotient is (umulhi(m, n) + n) >> s.
+struct FixedDivisor {
+    uint32_t mul;
+    int32_t shift;
+    void set(int32_t d)
+    {
+        shift = 0;
+        while ((int64_t(1) << shift) < d)
+            ++shift;
+        mul = uint32_t((((uint64_t(1) << shift) - uint64_t(d)) << 32) / uint64_t(d) + 1);
+    }
+#ifdef __CUDACC__
+    __device__ __forceinline__ int of(int n) const { return int((__umulhi(mul, uint32_t(n)) + uint32_t(n)) >> shift); }
+#endif
+};
+
 // Decode behind shared prefixes: the prefixes' part for all their requests' rows, and
 // the merge of it with the few-row kernel's (kSuffix).
 struct PrefixKernelArgs {
@@ -262,6 +280,15 @@ struct PrefixKernelArgs {
     int32_t ps, num_pages;        // of those pages
     int32_t box_rows;             // min(ps, 128), at least 8
     int32_t block_ps, max_pages;  // of the requests' own tables
+    const uint8_t* key_rows;      // e4m3 and 4-bit pools
+    const uint8_t* value_rows;
+    int32_t ps_shift;             // log2 of ps
+    FixedDivisor by_R, by_L;
+    int4* note_request;           // [B] first item (-1: none), its row 0 among them, items a KV
+                                  // head, 1: both halves of a state hold the rows
+    int2* note_item;              // [most_items] first and last block
+    void* more_pieces;            // [grid][most_items]
+    int32_t most_items;
     float scale_log2;
 };
 struct PrefixMergeArgs {
@@ -269,15 +296,21 @@ struct PrefixMergeArgs {
     const float* suffix_state;    // [slot][row_tiles * 8 * (D + 2)]
     uint16_t* out;                // [B, H_q, L, D]
     float out_scale;
-    int32_t prefix_grid, suffix_grid;
-    int32_t MS, per_req, row_tiles, tile_keys, box_rows;   // of the few-row kernel
+    const int2* note_segment;     // [B * H_kv * MS] first and last block
+    FixedDivisor by_H;            // H_kv
+    int32_t MS, row_tiles;        // of the few-row kernel
+    int32_t share;                // set by the launcher: warps a row
 };
-size_t prefix_smem_bytes(int D, int count);
-// The states' workspace, and where (m, l) start in it.
-size_t prefix_state_bytes(const pa_shape& s, int count, int grid, size_t* ml_off);
+// A block's pieces of items that lie in shared memory; an item's units of work.
+constexpr int kPrefixMaxPieces = 64;
+inline int64_t prefix_item_units(int64_t tiles) { return tiles * 4 + 8; }
+size_t prefix_smem_bytes(int D, int kind, int count);
+// The workspace of the states of `items` items, and where (m, l) and the pieces behind
+// kPrefixMaxPieces start in it.
+size_t prefix_state_bytes(const pa_shape& s, int64_t items, int grid, size_t* ml_off, size_t* pieces_off);
 cudaError_t launch_prefix(const CUtensorMap& key_map, const CUtensorMap& value_map, const PrefixKernelArgs& a,
-                          int D, int grid, int device, cudaStream_t stream);
-cudaError_t launch_prefix_merge(const PrefixMergeArgs& a, int D, cudaStream_t stream);
+                          int D, int kind, int grid, int device, cudaStream_t stream);
+cudaError_t launch_prefix_merge(PrefixMergeArgs a, int D, int sm_count, cudaStream_t stream);
 
 // Accumulation of attention weights: weight_pages[slot of j] = decay * old (0
 // for the L newest positions, or where decay is 0) + sum over the R rows of

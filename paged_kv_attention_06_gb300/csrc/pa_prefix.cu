@@ -21,7 +21,12 @@
 // between the warpgroups:
 //   S(j) = Q K^T,  softmax (lazy rescale at 2^8),  O += P V(j),  S(j + 2) over P(j).
 //
-//   * warp 0: K tiles, warp 2: V tiles by TMA, page by page, two stages each;
+//   * bf16 pools, warp 0: K tiles, warp 2: V tiles by TMA, page by page, two stages each;
+//   * e4m3 and 4-bit pools, warp 0: tiles of codes by TMA into a ring, warps 12-15: codes
+//     into f16 (K two stages, V one); Q and P are f16 then. (A copy of the prefixes as
+//     bf16 pages before this kernel took 42 of 107 us for 64 e4m3 requests over 31000
+//     shared keys; three converting warps that asked for their codes themselves took 2.3
+//     us a tile, register loads 4.);
 //   * warp 1 (one elected thread): the tcgen05.mma chain;
 //   * warps 4-7 and 8-11: the query rows of a piece into shared memory, the softmax
 //     (P over the upper half of the scores' columns in TMEM, rounded to bf16: its error,
@@ -38,6 +43,7 @@
 #include "pa_device.cuh"
 #include "pa_internal.h"
 #include "pa_prefix.cuh"
+#include "pa_q4.cuh"
 #include "pa_split.cuh"
 #include "pa_tcgen05.cuh"
 
@@ -45,29 +51,44 @@ namespace pa {
 namespace {
 
 constexpr int kKeys = 128;            // keys per tile
-constexpr int kThreads = 384;
+constexpr int kMaxPieces = kPrefixMaxPieces;
 constexpr uint32_t kTmemCols = 512;
 constexpr float kRescaleLog2 = 8.f;
-constexpr int kRegsProducer = 128;
-constexpr int kRegsSoftmax = 184;
-static_assert(128 * kRegsProducer + 256 * kRegsSoftmax <= 65536, "register split");
 
 __host__ __device__ constexpr uint32_t col_s(int half) { return uint32_t(half * 128); }
 __host__ __device__ constexpr uint32_t col_o(int half) { return uint32_t(256 + half * 128); }
 constexpr uint32_t kPCol = 64;
 
-template <int D>
+// Pools of codes: each of four warps turns kRunKeys keys of every K and V tile into f16;
+// kRing tiles of codes are on their way to them.
+constexpr int kRunKeys = 32, kConverters = kKeys / kRunKeys, kRing = 3;
+
+template <int D, int KIND>
 struct Layout {
-    static constexpr int kBlock = 128 * 128;            // 128 rows x 64 bf16 (128 B)
-    static constexpr int kMat = D / 64 * kBlock;        // 128 x D bf16, [column block][row][128 B]
+    static constexpr bool kCodes = KIND != kBf16Pool;
+    static constexpr int kVStages = kCodes ? 1 : 2;     // the ring takes the second one's place
+    static constexpr int kRowBytes = KIND == kQ4Pool ? kQ4RowBytes : D;   // of codes
+    static constexpr int kCodeTile = kKeys * kRowBytes;
+    static constexpr int kThreads = kCodes ? 512 : 384;
+    // Registers a thread: warps 0-3, the two softmax warpgroups, the converters.
+    static constexpr int kRegsFirst = kCodes ? 64 : 128;
+    static constexpr int kRegsSoftmax = kCodes ? 176 : 184;
+    static constexpr int kRegsConvert = kCodes ? 88 : 0;
+    static constexpr int kRegsSum = 128 * (kRegsFirst + 2 * kRegsSoftmax + kRegsConvert);
+    static_assert(kRegsSum <= 65536, "register split");
+    static constexpr int kBlock = 128 * 128;            // 128 rows x 64 elements (128 B)
+    static constexpr int kMat = D / 64 * kBlock;        // 128 x D, [column block][row][128 B]
     static constexpr int kQ = 0;                        // [half]
     static constexpr int kK = kQ + 2 * kMat;            // 2 stages
-    static constexpr int kV = kK + 2 * kMat;            // 2 stages
-    static constexpr int kBar = kV + 2 * kMat;
-    static constexpr int kNumBars = 16;
+    static constexpr int kV = kK + 2 * kMat;
+    static constexpr int kCodeRing = kV + kVStages * kMat;   // [slot][key][row bytes]
+    static constexpr int kBar = kCodeRing + (kCodes ? kRing * kCodeTile : 0);
+    static constexpr int kNumBars = 16 + (kCodes ? 2 * kRing : 0);
     static constexpr int kTmemSlot = kBar + kNumBars * 8;
     static constexpr int kMisc = kTmemSlot + 16;
-    static constexpr int kGroups = kMisc + 16;          // Group[count]
+    static constexpr int kSlotInfo = kMisc + 16;        // [slot] (tile and matrix, keys)
+    static constexpr int kPieces = kSlotInfo + (kCodes ? kRing * 8 : 0);   // Piece[kMaxPieces]
+    static constexpr int kGroups = kPieces + kMaxPieces * 36;              // Group[count]
 };
 
 // Barrier indices.
@@ -79,7 +100,8 @@ constexpr int kVEmpty = 8;
 constexpr int kSFull = 10;    // + half (2)
 constexpr int kPFull = 12;    // + half
 constexpr int kPVDone = 14;   // + half
-static_assert(kPVDone + 1 < Layout<128>::kNumBars, "barrier count");
+constexpr int kCodeFull = 16; // + slot (kRing)
+constexpr int kCodeEmpty = kCodeFull + kRing;
 
 // A tile weighs kTileUnits, an item kItemUnits more (its rows, its state: about two
 // tiles' time); a tile belongs to the block whose range holds its first unit. A block has
@@ -88,11 +110,13 @@ constexpr int kTileUnits = 4;
 constexpr int kItemUnits = 8;
 constexpr int kLeastUnits = 8;
 
-// One prefix: where its units and items start, its keys, its rows for one KV head.
+// One prefix: its keys, its first request, its rows for one KV head; where its units and
+// items start in the stream.
 struct Group {
-    long long us;
-    int item, items, len, first, rows, tiles;
-    __device__ __forceinline__ long long item_units() const { return (long long)tiles * kTileUnits + kItemUnits; }
+    int len, first, rows, items, us, item;
+    __device__ __forceinline__ int tiles() const { return (len + kKeys - 1) / kKeys; }
+    __device__ __forceinline__ int item_units() const { return tiles() * kTileUnits + kItemUnits; }
+    __device__ __forceinline__ int units() const { return items * item_units(); }
 };
 
 // *bad: the starts do not ascend within the batch.
@@ -103,62 +127,48 @@ __device__ __forceinline__ Group group_at(const PrefixKernelArgs& a, int p, bool
     const int end = __ldg(a.prefix.starts + p + 1);
     *bad = g.first < 0 || end < g.first || end > a.B;
     g.len = prefix_len(a.prefix, p);
-    g.tiles = (g.len + kKeys - 1) / kKeys;
     g.rows = *bad ? 0 : (end - g.first) * a.R;
-    g.items = g.tiles > 0 ? a.H_kv * ((g.rows + 255) / 256) : 0;
-    g.us = 0;
-    g.item = 0;
+    g.items = g.len > 0 ? a.H_kv * ((g.rows + 255) / 256) : 0;
+    g.us = g.item = 0;
     return g;
 }
 
-// Blocks that take part, of U units.
-__device__ __forceinline__ long long working_blocks(long long U, int grid)
-{
-    const long long most = U / kLeastUnits;
-    return most < 1 ? 1 : most < grid ? most : grid;
-}
-__device__ __forceinline__ long long range_start(long long c, long long U, long long G) { return c * U / G; }
-__device__ __forceinline__ int block_of(long long x, long long U, long long G) { return int(((x + 1) * G - 1) / U); }
+// The ranges of U units that G blocks take: U / G each, the first U % G one more.
+struct Ranges {
+    int G, per, rem;
+    __device__ __forceinline__ Ranges(int U, int grid)
+    {
+        G = max(1, min(grid, U / kLeastUnits));
+        per = U / G;
+        rem = U - per * G;
+    }
+    __device__ __forceinline__ int start(int c) const { return c * per + min(c, rem); }
+};
 
 // The part of an item in a block's range of units.
 struct Piece {
-    int p, item, h, rb;      // prefix, item of all, KV head, block of 256 rows
-    int k0, k1;              // tiles
+    int p, len, k0, k1;      // prefix, its keys; tiles
+    int h, rb, rows, first;  // KV head, block of 256 rows; the prefix's rows and first request
+    int item;                // of all
 };
-struct Cursor {
-    int p, i;                // the next item: the i-th of prefix p
-    __device__ __forceinline__ bool next(const Group* groups, int count, long long s, long long e, Piece& out)
+
+// A block's pieces: the first kMaxPieces in shared memory, what there may be more (many
+// short prefixes beside a long one) in the workspace.
+struct Pieces {
+    Piece* near;
+    Piece* far;
+    __device__ __forceinline__ Piece& operator[](int i) const
     {
-        for (;;) {
-            if (p >= count)
-                return false;
-            const Group& g = groups[p];
-            if (i >= g.items) {
-                ++p;
-                i = 0;
-                continue;
-            }
-            const long long us = g.us + i * g.item_units();
-            if (us >= e)
-                return false;
-            auto first_at = [&](long long x) {
-                const long long d = x - us - kItemUnits;
-                const long long k = d <= 0 ? 0 : (d + kTileUnits - 1) / kTileUnits;
-                return int(k > g.tiles ? g.tiles : k);
-            };
-            out.k0 = first_at(s);
-            out.k1 = first_at(e);
-            const int blocks = (g.rows + 255) / 256;
-            out.p = p;
-            out.item = g.item + i;
-            out.h = i / blocks;
-            out.rb = i - out.h * blocks;
-            ++i;
-            if (out.k0 < out.k1)
-                return true;
-        }
+        return *(i < kMaxPieces ? near + i : far + (i - kMaxPieces));
     }
 };
+
+// The first tile of an item (first unit us) that starts at or after unit x.
+__device__ __forceinline__ int tile_at(int x, int us, int tiles)
+{
+    const int d = x - us - kItemUnits;
+    return d <= 0 ? 0 : min(tiles, (d + kTileUnits - 1) / kTileUnits);
+}
 
 // The products' steps, in order: a step is one warpgroup's (half's) work on one tile.
 // Half j & 1 takes step j; `first` / `last` of its piece for that half, `opens` /
@@ -168,21 +178,20 @@ struct Step {
     bool first, opens, closes, valid;
 };
 struct StepIter {
-    Cursor cur;
-    Piece piece;
-    int k, g, sub, done;     // next tile of the piece, of the stream; steps of the tile; of the piece
-    bool have, pair;
-    __device__ __forceinline__ Step next(const Group* groups, int count, long long s, long long e)
+    int i, k, k1, g, sub, done;   // next piece; next tile of this one, its end, of the stream; steps of the tile, of the piece
+    bool pair;
+    __device__ __forceinline__ Step next(const Pieces& pieces, int count)
     {
         Step st;
         st.valid = false;
-        if (!have || k >= piece.k1) {
-            if (!cur.next(groups, count, s, e, piece))
+        if (k >= k1) {
+            if (i >= count)
                 return st;
-            have = true;
-            k = piece.k0;
+            k = pieces[i].k0;
+            k1 = pieces[i].k1;
+            pair = pieces[i].rows > 128;
             sub = done = 0;
-            pair = groups[piece.p].rows > 128;
+            ++i;
         }
         st.valid = true;
         st.g = g;
@@ -201,104 +210,110 @@ struct StepIter {
     }
 };
 
-template <int D>
-__global__ void __launch_bounds__(kThreads, 1)
+// A run's codes at `from` as f16 into a [column block][key][128 bytes] matrix, swizzled; the
+// first `live` keys of it, zeros behind them. Of every 8 elements of 4-bit rows the order
+// is 0 4 1 5 2 6 3 7, as their codes come apart: Q has it too, and the states are put
+// right as they are written.
+// kEnds: fewer than kRunKeys of them.
+template <int KIND, bool kEnds>
+__device__ __forceinline__ void convert_run(uint8_t* mat, int block_bytes, const uint8_t* from, int key0, int live,
+                                            int lane)
+{
+    constexpr bool kQ4 = KIND == kQ4Pool;
+    constexpr int kRowBytes = kQ4 ? kQ4RowBytes : 128;
+    constexpr int kChunks = kQ4 ? 4 : 8;                         // 16-byte pieces of a row's codes
+    constexpr int kOut = kQ4 ? 4 : 2;                            // 16-byte pieces of f16 from each
+    const int c = lane % kChunks;
+    // Lanes whose pieces go to the second column block start with the other half of
+    // them: the eight lanes of a store then meet eight different bank groups.
+    const bool turned = c >= kChunks / 2;
+    uint4 codes[kChunks];                                        // all read before the first is stored
+    uint32_t params[kQ4 ? kChunks : 1];
+#pragma unroll
+    for (int i = 0; i < kChunks; ++i) {
+        const uint8_t* row = from + (i * (32 / kChunks) + lane / kChunks) * kRowBytes;
+        codes[i] = *(reinterpret_cast<const uint4*>(row) + c);
+        if constexpr (kQ4)
+            params[i] = *(reinterpret_cast<const uint32_t*>(row + kQ4CodeBytes) + c);
+    }
+#pragma unroll
+    for (int i = 0; i < kChunks; ++i) {
+        const int r = i * (32 / kChunks) + lane / kChunks;
+        const uint4 x = codes[i];
+        const uint32_t w[4] = {turned ? x.z : x.x, turned ? x.w : x.y, turned ? x.x : x.z, turned ? x.y : x.w};
+        uint32_t v[4 * kOut];
+        if constexpr (kQ4) {
+            const uint32_t s = __byte_perm(params[i], 0, 0x1010), m = __byte_perm(params[i], 0, 0x3232);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    // c exactly (1024 + c - 1024, (1024 + 16 c) / 16 - 64), then m + s c
+                    const uint32_t y = w[k] >> (8 * j);
+                    const uint32_t lo = add_f16x2((y & 0x000f000fu) | 0x64006400u, 0xe400e400u);
+                    const uint32_t hi = fma_f16x2((y & 0x00f000f0u) | 0x64006400u, 0x2c002c00u, 0xd400d400u);
+                    v[4 * k + 2 * j] = fma_f16x2(lo, s, m);
+                    v[4 * k + 2 * j + 1] = fma_f16x2(hi, s, m);
+                }
+        } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                v[2 * k] = e4m3x2_to_f16x2(w[k]);
+                v[2 * k + 1] = e4m3x2_hi_to_f16x2(w[k]);
+            }
+        }
+        const int key = key0 + r;
+#pragma unroll
+        for (int k = 0; k < kOut; ++k) {
+            const int ch = c * kOut + (turned ? k ^ (kOut / 2) : k);   // 16-byte piece of the f16 row
+            *reinterpret_cast<uint4*>(mat + (ch >> 3) * block_bytes + key * 128 + (((ch & 7) ^ (key & 7)) << 4)) =
+                !kEnds || r < live ? make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3])
+                                   : make_uint4(0, 0, 0, 0);
+        }
+    }
+}
+
+// Two f16 pairs of neighbours (elements 2 i, 2 i + 1 of 8) as 4-bit rows have them.
+__device__ __forceinline__ uint4 apart(uint4 v)
+{
+    return make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632), __byte_perm(v.y, v.w, 0x5410),
+                      __byte_perm(v.y, v.w, 0x7632));
+}
+
+template <int D, int KIND>
+__global__ void __launch_bounds__((Layout<D, KIND>::kThreads), 1)
     prefix_kernel(const __grid_constant__ CUtensorMap key_map, const __grid_constant__ CUtensorMap value_map,
                   const PrefixKernelArgs a)
 {
-    using Lay = Layout<D>;
+    using Lay = Layout<D, KIND>;
+    constexpr int kVStages = Lay::kVStages;
+    constexpr bool kCodes = KIND != kBf16Pool;
     constexpr int kBlocks = D / 64;                      // 128-byte column blocks of a row
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t* bar = reinterpret_cast<uint64_t*>(smem + Lay::kBar);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Lay::kTmemSlot);
     volatile int* misc = reinterpret_cast<volatile int*>(smem + Lay::kMisc);
-    Group* groups = reinterpret_cast<Group*>(smem + Lay::kGroups);
-    __shared__ long long total_units;
+    const Pieces pieces = {reinterpret_cast<Piece*>(smem + Lay::kPieces),
+                           static_cast<Piece*>(a.more_pieces) + int64_t(blockIdx.x) * a.most_items};
+    static_assert(sizeof(Piece) == 36, "as laid out");
+    __shared__ int piece_count;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int count = a.prefix.count;
-
-    grid_dependency_wait();
-    grid_launch_dependents();
-    // ---- the prefixes' places in the stream ---------------------------------------
-    if (warp == 0) {
-        long long us = 0;
-        int item = 0;
-        bool bad = false;
-        for (int base = 0; base < count; base += 32) {
-            const int p = base + lane;
-            Group g;
-            g.items = 0;
-            g.tiles = 0;
-            if (p < count) {
-                bool no;
-                g = group_at(a, p, &no);
-                bad |= no;
-                const int n = __ldg(a.prefix.lens + p);
-                if (blockIdx.x == 0 && (n < 0 || n > a.prefix.cap))
-                    atomicOr(a.err, PA_DEVERR_CONTEXT_LEN_BIT);
-            }
-            const long long units = g.items * g.item_units();
-            long long incl_u = units;
-            int incl_i = g.items;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const long long u = __shfl_up_sync(0xffffffffu, incl_u, o);
-                const int v = __shfl_up_sync(0xffffffffu, incl_i, o);
-                if (lane >= o) {
-                    incl_u += u;
-                    incl_i += v;
-                }
-            }
-            if (p < count) {
-                g.us = us + incl_u - units;
-                g.item = item + incl_i - g.items;
-                groups[p] = g;
-            }
-            us += __shfl_sync(0xffffffffu, incl_u, 31);
-            item += __shfl_sync(0xffffffffu, incl_i, 31);
-        }
-        // Rows counted twice would have more states than there is room for: none then.
-        bad = __any_sync(0xffffffffu, bad);
-        if (lane == 0) {
-            total_units = bad ? 0 : us;
-            if (bad && blockIdx.x == 0)
-                atomicOr(a.err, PA_DEVERR_PREFIX_BIT);
-        }
-    }
-    __syncthreads();
-    const long long U = total_units;
-    const long long G = working_blocks(U, int(gridDim.x));
-    const int c = int(blockIdx.x);
-    if (U == 0 || c >= G)
-        return;
-    const long long s = range_start(c, U, G), e = range_start(c + 1, U, G);
-    Cursor start;
-    {
-        int lo = 0, hi = count;                          // the last prefix that starts at or before s
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (groups[mid].us <= s)
-                lo = mid;
-            else
-                hi = mid;
-        }
-        start.p = lo;
-        start.i = groups[lo].items > 0 ? int((s - groups[lo].us) / groups[lo].item_units()) : 0;
-    }
-
-    const uint32_t sQ = smem_u32(smem + Lay::kQ), sK = smem_u32(smem + Lay::kK), sV = smem_u32(smem + Lay::kV);
     if (threadIdx.x == 0) {
         misc[0] = 0;
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bar[kQFull + i], 4);              // one arrival per warp
-            mbar_init(&bar[kKFull + i], 1);
+            mbar_init(&bar[kKFull + i], kCodes ? kConverters : 1);
             mbar_init(&bar[kKEmpty + i], 1);
-            mbar_init(&bar[kVFull + i], 1);
+            mbar_init(&bar[kVFull + i], kCodes ? kConverters : 1);
             mbar_init(&bar[kVEmpty + i], 1);
             mbar_init(&bar[kSFull + i], 1);
             mbar_init(&bar[kPFull + i], 4);
             mbar_init(&bar[kPVDone + i], 1);
+        }
+        for (int i = 0; i < kRing && kCodes; ++i) {
+            mbar_init(&bar[kCodeFull + i], 1);
+            mbar_init(&bar[kCodeEmpty + i], kConverters);
         }
         fence_barrier_init();
     }
@@ -307,13 +322,230 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_relinquish();
     }
     tc_fence_before();
+    grid_dependency_wait();
+    grid_launch_dependents();
+    // The queries into L2, before the keys queue up in front of them (a block's rows came
+    // in 4 us after they were asked for).
+    {
+        const int64_t lines = (int64_t(a.B) * a.H_q * a.L * D * 2 + 127) / 128;
+        for (int64_t i = int64_t(blockIdx.x) * Lay::kThreads + threadIdx.x; i < lines;
+             i += int64_t(gridDim.x) * Lay::kThreads)
+            prefetch_l2(reinterpret_cast<const uint8_t*>(a.q) + i * 128);
+    }
+    // ---- the prefixes' places in the stream, and this block's pieces ---------------
+    const int c = int(blockIdx.x);
+    if (warp == 0) {
+        Group* groups = reinterpret_cast<Group*>(smem + Lay::kGroups);
+        const int prefixes = a.prefix.count;
+        int us = 0, item = 0;
+        bool bad = false;
+        for (int base = 0; base < prefixes; base += 32) {
+            const int p = base + lane;
+            Group g;
+            g.len = g.items = 0;
+            if (p < prefixes) {
+                bool no;
+                g = group_at(a, p, &no);
+                bad |= no;
+                if (c == 0) {
+                    const int n = __ldg(a.prefix.lens + p);
+                    if (n < 0 || n > a.prefix.cap)
+                        atomicOr(a.err, PA_DEVERR_CONTEXT_LEN_BIT);
+                }
+            }
+            int incl_u = g.units(), incl_i = g.items;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int u = __shfl_up_sync(0xffffffffu, incl_u, o), v = __shfl_up_sync(0xffffffffu, incl_i, o);
+                if (lane >= o) {
+                    incl_u += u;
+                    incl_i += v;
+                }
+            }
+            if (p < prefixes) {
+                g.us = us + incl_u - g.units();
+                g.item = item + incl_i - g.items;
+                groups[p] = g;
+            }
+            us += __shfl_sync(0xffffffffu, incl_u, 31);
+            item += __shfl_sync(0xffffffffu, incl_i, 31);
+        }
+        // Rows counted twice would have more states than there is room for: none then.
+        bad = __any_sync(0xffffffffu, bad);
+        if (bad && c == 0 && lane == 0)
+            atomicOr(a.err, PA_DEVERR_PREFIX_BIT);
+        const int U = bad ? 0 : us;
+        const Ranges ranges(U, int(gridDim.x));
+        int found = 0;
+        if (U > 0 && c < ranges.G) {
+            const int s = ranges.start(c), e = ranges.start(c + 1);
+            for (int base = 0; base < prefixes; base += 32) {
+                const int p = base + lane;
+                int i0 = 0, n = 0;
+                Group g;
+                if (p < prefixes) {
+                    g = groups[p];
+                    const int w = g.item_units(), end = g.us + g.units();
+                    if (g.items > 0 && g.us < e && s < end) {
+                        i0 = (max(s, g.us) - g.us) / w;
+                        int i1 = (min(e, end) - 1 - g.us) / w;
+                        // an item whose tiles all start before the range, or behind it
+                        if (tile_at(s, g.us + i0 * w, g.tiles()) == g.tiles())
+                            ++i0;
+                        if (tile_at(e, g.us + i1 * w, g.tiles()) == 0)
+                            --i1;
+                        n = max(0, i1 - i0 + 1);
+                    }
+                }
+                int incl = n;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int v = __shfl_up_sync(0xffffffffu, incl, o);
+                    if (lane >= o)
+                        incl += v;
+                }
+                const int blocks = n > 0 ? (g.rows + 255) / 256 : 1;
+                for (int x = 0; x < n; ++x) {
+                    const int at = found + incl - n + x, i = i0 + x;
+                    Piece& pc = pieces[at];
+                    const int h = i / blocks;
+                    pc.p = p;
+                    pc.len = g.len;
+                    pc.k0 = tile_at(s, g.us + i * g.item_units(), g.tiles());
+                    pc.k1 = tile_at(e, g.us + i * g.item_units(), g.tiles());
+                    pc.h = h;
+                    pc.rb = i - h * blocks;
+                    pc.rows = g.rows;
+                    pc.first = g.first;
+                    pc.item = g.item + i;
+                }
+                found += __shfl_sync(0xffffffffu, incl, 31);
+            }
+        }
+        if (lane == 0)
+            piece_count = bad ? -1 : found;
+    }
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
+    const int count = max(piece_count, 0);
+    // ---- notes for the merge: where a request's rows are among the items' (row 0 of
+    // the first one's KV head 0), and the blocks that hold each item's first and last tile
+    if (warp == 3) {
+        const Group* groups = reinterpret_cast<const Group*>(smem + Lay::kGroups);
+        for (int b = c * 32 + lane; b < a.B; b += int(gridDim.x) * 32) {
+            const int p = piece_count < 0 ? -1 : prefix_of(a.prefix, b);
+            int4 note = make_int4(-1, 0, 0, 0);
+            if (p >= 0 && groups[p].items > 0)
+                note = make_int4(groups[p].item, (b - groups[p].first) * a.R, (groups[p].rows + 255) / 256,
+                                 groups[p].rows > 128 ? 0 : 1);
+            a.note_request[b] = note;
+        }
+        for (int i = lane; i < count; i += 32) {
+            const Piece& pc = pieces[i];
+            if (pc.k0 == 0)
+                a.note_item[pc.item].x = c;
+            if (pc.k1 * kKeys >= pc.len)
+                a.note_item[pc.item].y = c;
+        }
+    }
+    if (count == 0) {
+        if (warp == 1)
+            tmem_dealloc(tmem, kTmemCols);
+        return;
+    }
 
+    const uint32_t sQ = smem_u32(smem + Lay::kQ), sK = smem_u32(smem + Lay::kK), sV = smem_u32(smem + Lay::kV);
     if (warp < 4) {
-        setmaxnreg_dec<kRegsProducer>();
-        if (warp == 0 || warp == 2) {
+        setmaxnreg_dec<Lay::kRegsFirst>();
+        if (kCodes && warp == 0) {
+            // ===================== tiles of codes ====================================
+            if constexpr (kCodes) {
+                const uint64_t policy = l2_policy_evict_last();  // the item's other row blocks read it too
+                const int box = min(a.ps, kKeys);
+                const int box_shift = min(a.ps_shift, 7);
+                int2* info = reinterpret_cast<int2*>(smem + Lay::kSlotInfo);
+                // The order: K of tile 0, then K of tile g + 1 and V of tile g in turn, so that
+                // the wait for V's one stage (the product before) keeps no K from the scores
+                // ahead.
+                struct Tile {                            // tile k of a piece, g of the block's stream
+                    int i, k, k1, g;
+                };
+                auto pass = [&](Tile& t) {
+                    ++t.g;
+                    if (++t.k >= t.k1 && ++t.i < count) {
+                        t.k = pieces[t.i].k0;
+                        t.k1 = pieces[t.i].k1;
+                    }
+                };
+                Tile kt = {0, pieces[0].k0, pieces[0].k1, 0};
+                Tile vt = kt;
+                const uint32_t ps_mask = (1u << a.ps_shift) - 1u;
+                int u = 0;                               // tiles of codes asked for
+                auto slot_free = [&](int slot) {
+                    return mbar_wait_warp(&bar[kCodeEmpty + slot], ((u / kRing) & 1) ^ 1u, misc, a.err);
+                };
+                auto request = [&](const Tile& t, bool is_v) {
+                    const int slot = u % kRing;
+                    const int first = t.k * kKeys;
+                    const Piece& pc = pieces[t.i];
+                    const int live = min(kKeys, pc.len - first);
+                    const int boxes = (live + box - 1) >> box_shift;
+                    const int32_t* table = a.prefix.table + int64_t(pc.p) * a.prefix.pages;
+                    int pages[kKeys / 32];
+#pragma unroll
+                    for (int i = 0; i < kKeys / 32; ++i)
+                        if (32 * i + lane < boxes)
+                            pages[i] = __ldg(table + ((first + ((32 * i + lane) << box_shift)) >> a.ps_shift));
+                    const bool ok = slot_free(slot);
+                    if (ok) {
+                        if (lane == 0) {
+                            info[slot] = make_int2(2 * t.g + (is_v ? 1 : 0), live);
+                            mbar_arrive_expect_tx(&bar[kCodeFull + slot], uint32_t(boxes * box * Lay::kRowBytes));
+                        }
+                        __syncwarp();
+#pragma unroll
+                        for (int i = 0; i < kKeys / 32; ++i) {
+                            const int at = (32 * i + lane) << box_shift;
+                            if (32 * i + lane < boxes) {
+                                if (unsigned(pages[i]) >= unsigned(a.num_pages)) {
+                                    atomicOr(a.err, PA_DEVERR_PAGE_ID_BIT);
+                                    pages[i] = 0;
+                                }
+                                const uint32_t row = (uint32_t(pages[i] * a.H_kv + pc.h) << a.ps_shift) +
+                                                     (uint32_t(first + at) & ps_mask);
+                                bulk_load(smem + Lay::kCodeRing + slot * Lay::kCodeTile + at * Lay::kRowBytes,
+                                          (is_v ? a.value_rows : a.key_rows) + uint64_t(row) * Lay::kRowBytes,
+                                          uint32_t(box * Lay::kRowBytes), &bar[kCodeFull + slot], policy);
+                            }
+                        }
+                    }
+                    __syncwarp();
+                    ++u;
+                };
+                request(kt, false);
+                while (vt.i < count) {
+                    if (kt.i < count) {
+                        pass(kt);
+                        if (kt.i < count)
+                            request(kt, false);
+                    }
+                    request(vt, true);
+                    pass(vt);
+                }
+                // The end, and no copy still landing: the converters have waited for each.
+                const int slot = u % kRing;
+                slot_free(slot);
+                if (lane == 0) {
+                    info[slot] = make_int2(-1, 0);
+                    mbar_arrive(&bar[kCodeFull + slot]);
+                }
+                for (int i = 1; i < kRing; ++i) {
+                    ++u;
+                    slot_free(u % kRing);
+                }
+            }
+        } else if (!kCodes && (warp == 0 || warp == 2)) {
             // ===================== K (warp 0) and V (warp 2) tiles ===================
             const bool is_v = warp == 2;
             const CUtensorMap* map = is_v ? &value_map : &key_map;
@@ -323,16 +555,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0)
                 prefetch_tensormap(map);
             const int box = a.box_rows;                  // min(page size, 128), at least 8
-            Cursor cur = start;
-            Piece pc;
             int g = 0;
-            while (cur.next(groups, count, s, e, pc)) {
-                const int n = groups[pc.p].len;
-                for (int k = pc.k0; k < pc.k1; ++k, ++g) {
+            for (int i = 0; i < count; ++i) {
+                const int n = pieces[i].len, k1 = pieces[i].k1, head = pieces[i].h;
+                const int32_t* table = a.prefix.table + int64_t(pieces[i].p) * a.prefix.pages;
+                for (int k = pieces[i].k0; k < k1; ++k, ++g) {
                     const int key0 = k * kKeys;
                     const int boxes = (min(n, key0 + kKeys) - key0 + box - 1) / box;
                     const int tok = key0 + lane * box;
-                    int phys = lane < boxes ? __ldg(a.prefix.table + int64_t(pc.p) * a.prefix.pages + tok / a.ps) : 0;
+                    int phys = lane < boxes ? __ldg(table + (tok >> a.ps_shift)) : 0;
                     const int st = g & 1;
                     const bool ok = mbar_wait_warp(&bar[empty + st], ((g >> 1) & 1) ^ 1u, misc, a.err);
                     if (ok) {
@@ -344,7 +575,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 atomicOr(a.err, PA_DEVERR_PAGE_ID_BIT);
                                 phys = 0;
                             }
-                            const int row = (phys * a.H_kv + pc.h) * a.ps + tok % a.ps;
+                            const int row = ((phys * a.H_kv + head) << a.ps_shift) + (tok & (a.ps - 1));
                             uint8_t* dst = to + st * Lay::kMat + lane * box * 128;
 #pragma unroll
                             for (int x = 0; x < kBlocks; ++x)
@@ -360,8 +591,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else if (warp == 1) {
             // ===================== MMA issue (one elected thread) =====================
             const bool leader = elect_one();
-            const uint32_t idesc_s = idesc_bf16_f32(128, kKeys, 0);
-            const uint32_t idesc_pv = idesc_bf16_f32(128, D, 1);
+            const uint32_t idesc_s = kCodes ? idesc_f16_f32(128, kKeys, 0) : idesc_bf16_f32(128, kKeys, 0);
+            const uint32_t idesc_pv = kCodes ? idesc_f16_f32(128, D, 1) : idesc_bf16_f32(128, D, 1);
             const uint64_t dq = smem_desc_sw128(sQ, 16u, 1024u), dk = smem_desc_sw128(sK, 16u, 1024u);
             const uint64_t dv = smem_desc_sw128(sV, uint32_t(Lay::kBlock), 1024u);
             auto k_major = [](int kk) { return uint32_t(kk >> 2) * Lay::kBlock + uint32_t(kk & 3) * 32u; };
@@ -373,13 +604,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tc_commit(&bar[bi]);
                 __syncwarp();
             };
-            int pieces[2] = {0, 0};                      // query tiles waited for, by half
+            int rounds[2] = {0, 0};                      // query tiles waited for, by half
             auto scores = [&](int j, const Step& st) {
                 const int h = j & 1, stage = st.g & 1;
                 if (st.first) {
-                    if (!wait(kQFull + h, pieces[h] & 1))
+                    if (!wait(kQFull + h, rounds[h] & 1))
                         return false;
-                    ++pieces[h];
+                    ++rounds[h];
                 }
                 if (!wait(kKFull + stage, (st.g >> 1) & 1))
                     return false;
@@ -397,16 +628,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 return true;
             };
             StepIter it;
-            it.cur = start;
-            it.have = false;
-            it.g = 0;
-            Step now = it.next(groups, count, s, e), next = it.next(groups, count, s, e);
+            it.i = it.k = it.k1 = it.g = 0;
+            Step now = it.next(pieces, count), next = it.next(pieces, count);
             bool ok = now.valid && scores(0, now) && (!next.valid || scores(1, next));
             int j = 0;
             for (; ok && now.valid; ++j) {
-                const int h = j & 1, stage = now.g & 1;
+                const int h = j & 1, stage = kVStages == 1 ? 0 : now.g & 1;
                 const uint32_t phase = (j >> 1) & 1;
-                if (!wait(kPFull + h, phase) || !wait(kVFull + stage, (now.g >> 1) & 1))
+                if (!wait(kPFull + h, phase) || !wait(kVFull + stage, (kVStages == 1 ? now.g : now.g >> 1) & 1))
                     break;
                 tc_fence_after();
                 if (leader) {
@@ -420,7 +649,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 commit(kPVDone + h);
                 if (now.closes)
                     commit(kVEmpty + stage);
-                const Step after = next.valid ? it.next(groups, count, s, e) : next;
+                const Step after = next.valid ? it.next(pieces, count) : next;
                 // S(j + 2) overwrites P(j); the wait is also this block's last
                 if (!wait(kPVDone + h, phase))
                     break;
@@ -430,9 +659,41 @@ __global__ void __launch_bounds__(kThreads, 1)
                 next = after;
             }
         }
+    } else if (kCodes && warp >= 12) {
+        setmaxnreg_dec<(kCodes ? Lay::kRegsConvert : 24)>();
+        // ===================== codes into f16: keys 32 w .. of every tile ===============
+        if constexpr (kCodes) {
+            const int key0 = (warp - 12) * kRunKeys;
+            const int2* info = reinterpret_cast<const int2*>(smem + Lay::kSlotInfo);
+            for (int u = 0;; ++u) {
+                const int slot = u % kRing;
+                if (!mbar_wait_warp(&bar[kCodeFull + slot], (u / kRing) & 1, misc, a.err))
+                    break;
+                const int2 what = info[slot];
+                if (what.x < 0)
+                    break;
+                const int v = what.x & 1, tile = what.x >> 1;
+                const int st = v ? 0 : tile & 1;
+                const uint32_t turn = v ? tile : tile >> 1;
+                const bool ok = mbar_wait_warp(&bar[(v ? kVEmpty : kKEmpty) + st], (turn & 1) ^ 1u, misc, a.err);
+                if (ok) {
+                    uint8_t* mat = smem + (v ? Lay::kV : Lay::kK) + st * Lay::kMat;
+                    const uint8_t* from = smem + Lay::kCodeRing + slot * Lay::kCodeTile + key0 * Lay::kRowBytes;
+                    if (what.y >= key0 + kRunKeys)
+                        convert_run<KIND, false>(mat, Lay::kBlock, from, key0, kRunKeys, lane);
+                    else
+                        convert_run<KIND, true>(mat, Lay::kBlock, from, key0, what.y - key0, lane);
+                    fence_proxy_async_smem();
+                }
+                __syncwarp();
+                if (lane == 0) {
+                    if (ok)
+                        mbar_arrive(&bar[(v ? kVFull : kKFull) + st]);
+                    mbar_arrive(&bar[kCodeEmpty + slot]);
+                }
+            }
+        }
     } else {
-        setmaxnreg_inc<kRegsSoftmax>();
-        // ===================== softmax: one warpgroup per half =====================
         const int half = (warp - 4) >> 2;
         const int w4 = warp & 3;
         const int r = w4 * 32 + lane;
@@ -440,61 +701,65 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t ts = trow + col_s(half), to = trow + col_o(half);
         const float c2l = a.scale_log2;
         uint8_t* mat = smem + Lay::kQ + half * Lay::kMat;
-        Cursor cur = start;
-        Piece pc;
-        int j0 = 0;                                      // the block's steps before this piece
-        int g0 = 0;                                      // and tiles
-        while (cur.next(groups, count, s, e, pc)) {
-            const Group& gr = groups[pc.p];
-            const int n = gr.len;
-            const bool pair = gr.rows > 128;
-            const int tiles = pc.k1 - pc.k0;
-            const int steps = pair ? 2 * tiles : tiles;
+        // ===================== softmax: one warpgroup per half =====================
+        setmaxnreg_inc<Lay::kRegsSoftmax>();
+        // (What a piece needs again at its end is read again from shared memory: the fold
+        // needs every register it has.)
+        int j0 = 0, g0 = 0;                              // the block's steps and tiles before this piece
+        for (int i = 0, tiles, steps; i < count; ++i, j0 += steps, g0 += tiles) {
+            const volatile Piece& pc = pieces[i];
+            const int n = pc.len, tile0 = pc.k0;
+            const bool pair = pc.rows > 128;
+            tiles = pc.k1 - tile0;
+            steps = pair ? 2 * tiles : tiles;
             // region 0: the half that takes the piece's first step
             const int region = half ^ (j0 & 1);
             const int mine = (steps - region + 1) >> 1;
             // this thread's row
             const int f = pair ? pc.rb * 256 + region * 128 + r : r;
-            const bool live = f < gr.rows;
-            const int b = live ? gr.first + f / a.R : 0, x = live ? f % a.R : 0;
-            int lim = -1;                                // its last visible key
-            int64_t q_at = 0;
-            if (live) {
-                const int cap = a.max_pages * a.block_ps;
-                int ctx = __ldg(a.context_lens + b);
-                ctx = ctx < 0 ? 0 : ctx > cap ? cap : ctx;
-                lim = min(n, ctx - a.L + x % a.L + 1) - 1;
-                q_at = ((int64_t(b) * a.H_q + pc.h * a.G) * a.L + x) * D;
-            }
-            const int64_t slot = int64_t(pc.item) + c;
-            float2* ml = a.state_ml + slot * 256 + region * 128;
+            const bool live = f < pc.rows;
+            // (Rows behind the last take another's query: they see nothing, and a branch around
+            // the loads would have each wait for the one before, 6 us.)
+            const int fr = live ? f : 0;
+            const int in = a.by_R.of(fr), x = fr - in * a.R, b = pc.first + in;
+            const int64_t q_at = ((int64_t(b) * a.H_q + pc.h * a.G) * a.L + x) * D;
+            const int ctx = __ldg(a.context_lens + b);
             if (mine == 0) {
                 if (live)
-                    __stcg(ml + r, make_float2(-INFINITY, 0.f));
-                j0 += steps;
-                g0 += tiles;
+                    __stcg(a.state_ml + (int64_t(pc.item) + c) * 256 + region * 128 + r, make_float2(-INFINITY, 0.f));
                 continue;
             }
             // ---- the rows of Q, 16 bytes a lane, swizzled as TMA would
             {
                 constexpr int kChunks = D / 8;           // 16-byte chunks of a row
                 constexpr int kPer = 32 / kChunks;       // rows a round
+                constexpr int kRounds = 32 / kPer;
+                uint4 v[kRounds];                        // all on their way before the first is stored
+                const int ch = lane % kChunks;
 #pragma unroll
-                for (int i = 0; i < 32 / kPer; ++i) {
-                    const int row = i * kPer + lane / kChunks, ch = lane % kChunks;
-                    const int64_t at = __shfl_sync(0xffffffffu, q_at, row);
-                    const bool there = __shfl_sync(0xffffffffu, int(live), row) != 0;
-                    uint4 v = make_uint4(0, 0, 0, 0);
-                    if (there)
-                        v = *reinterpret_cast<const uint4*>(a.q + at + ch * 8);
-                    const int rr = w4 * 32 + row;
-                    *reinterpret_cast<uint4*>(mat + (ch >> 3) * Lay::kBlock + rr * 128 + (((ch & 7) ^ (rr & 7)) << 4)) = v;
+                for (int i = 0; i < kRounds; ++i) {
+                    const int64_t at = __shfl_sync(0xffffffffu, q_at, i * kPer + lane / kChunks);
+                    v[i] = __ldg(reinterpret_cast<const uint4*>(a.q + at + ch * 8));
+                }
+#pragma unroll
+                for (int i = 0; i < kRounds; ++i) {
+                    const int rr = w4 * 32 + i * kPer + lane / kChunks;
+                    if constexpr (kCodes)
+                        v[i] = make_uint4(bf16x2_to_f16x2(v[i].x), bf16x2_to_f16x2(v[i].y), bf16x2_to_f16x2(v[i].z),
+                                          bf16x2_to_f16x2(v[i].w));
+                    if constexpr (KIND == kQ4Pool)
+                        v[i] = apart(v[i]);
+                    *reinterpret_cast<uint4*>(mat + (ch >> 3) * Lay::kBlock + rr * 128 + (((ch & 7) ^ (rr & 7)) << 4)) =
+                        v[i];
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0)
                     mbar_arrive(&bar[kQFull + half]);
             }
+            const int cap = a.max_pages * a.block_ps;
+            int lim = (ctx < 0 ? 0 : ctx > cap ? cap : ctx) - a.L + x - a.by_L.of(x) * a.L;
+            lim = live ? min(n - 1, lim) : -1;
             float m_used = -INFINITY, l = 0.f;
             for (int u = 0; u < mine; ++u) {
                 const int j = j0 + 2 * u + region;       // step of the block: j & 1 == half
@@ -505,7 +770,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint32_t phase = (j >> 1) & 1;
                 mbar_wait_warp(&bar[kSFull + half], phase, misc, a.err);
                 tc_fence_after();
-                const int key0 = (pc.k0 + tile) * kKeys;
+                const int key0 = (tile0 + tile) * kKeys;
                 uint32_t sv[128];
                 float* sc = reinterpret_cast<float*>(sv);
 #pragma unroll
@@ -553,7 +818,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             __ffma2_rn(make_float2(sc[64 * hf + 2 * kq], sc[64 * hf + 2 * kq + 1]), cc, nmu2);
                         const float2 pp = make_float2(fast_exp2(v.x), fast_exp2(v.y));
                         lsum[kq & 3] = __fadd2_rn(lsum[kq & 3], pp);
-                        pk[kq] = pack_bf16x2(pp.x, pp.y);
+                        pk[kq] = kCodes ? pack_f16x2(pp.x, pp.y) : pack_bf16x2(pp.x, pp.y);
                     }
                     tmem_st32(ts + kPCol + 32u * hf, pk);
                 };
@@ -579,8 +844,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 tmem_wait_st();
                 // V rows past the prefix hold whatever the page or the stage held: zeros
-                // before either half's product with them
-                if (opens && n < key0 + kKeys) {
+                // before either half's product with them (codes: written as zeros)
+                if (!kCodes && opens && n < key0 + kKeys) {
                     mbar_wait_bounded(&bar[kVFull + (g & 1)], (g >> 1) & 1, misc, a.err);
                     const int z = n - key0;
                     uint8_t* vb = smem + Lay::kV + (g & 1) * Lay::kMat;
@@ -601,19 +866,24 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_wait_warp(&bar[kPVDone + half], ((j0 + 2 * (mine - 1) + region) >> 1) & 1, misc, a.err);
             tc_fence_after();
             const bool good = misc[0] == 0;
+            const int64_t place = (int64_t(pc.item) + c) * 256 + region * 128;
             if (live && good)
-                __stcg(ml + r, make_float2(m_used, l));
+                __stcg(a.state_ml + place + r, make_float2(m_used, l));
             uint8_t* stage = mat + w4 * 32 * 128;
-            float* rows_out = a.state + (slot * 256 + region * 128 + w4 * 32) * D;
+            float* rows_out = a.state + (place + w4 * 32) * D;
 #pragma unroll
             for (int q4 = 0; q4 < D / 32; ++q4) {
                 uint32_t ov[32];
                 tmem_ld32(to + 32u * q4, ov);
                 tmem_wait_ld();
 #pragma unroll
-                for (int cq = 0; cq < 8; ++cq)
+                for (int cq = 0; cq < 8; ++cq) {
+                    // elements 4 cq .. 4 cq + 3; 4-bit rows: places 2 i or 2 i + 1 of the 8
+                    constexpr bool kApart = KIND == kQ4Pool;
+                    const int at = kApart ? 8 * (cq >> 1) + (cq & 1) : 4 * cq, by = kApart ? 2 : 1;
                     *reinterpret_cast<uint4*>(stage + lane * 128 + ((cq ^ (lane & 7)) << 4)) =
-                        make_uint4(ov[4 * cq], ov[4 * cq + 1], ov[4 * cq + 2], ov[4 * cq + 3]);
+                        make_uint4(ov[at], ov[at + by], ov[at + 2 * by], ov[at + 3 * by]);
+                }
                 __syncwarp();
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
@@ -626,8 +896,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
             }
             tc_fence_before();
-            j0 += steps;
-            g0 += tiles;
         }
     }
 
@@ -638,191 +906,134 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-// The last step: one block per query row joins the states that the prefix's pieces and
-// the row's own segment left. Everything before the wait is from the call's inputs, so
-// it runs while the kernels before are at work.
-constexpr int kMergeThreads = 128;
+// The last step joins the states that the prefix's pieces and the segment behind it left
+// for a row: by a.share warps of a block (a power of two), each some of the pieces. Where
+// they lie is read from what the two kernels before noted down: found again from the
+// call's tables, by every warp, it took 2 to 6 us (few of these blocks fit beside the
+// few-row kernel's, so it was not hidden before the wait).
+constexpr int kMergeWarps = 8, kMergeThreads = 32 * kMergeWarps;
 
 template <int D>
-__global__ void __launch_bounds__(kMergeThreads) prefix_merge_kernel(const PrefixMergeArgs a)
+__global__ void __launch_bounds__(kMergeThreads, 6) prefix_merge_kernel(const PrefixMergeArgs a)
 {
-    extern __shared__ float weights[];                   // [pieces]
-    __shared__ float4 sums[kMergeThreads / 32][32];
-    __shared__ float red[2][kMergeThreads / 32];
-    __shared__ long long red_units[2][kMergeThreads / 32];
-    __shared__ int red_items[kMergeThreads / 32];
-    grid_launch_dependents();
+    __shared__ float4 sums[kMergeWarps][32];
+    __shared__ float2 row_ml[kMergeWarps];               // (max, sum) of each warp's pieces
     const PrefixKernelArgs& k = a.prefix_args;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t row = blockIdx.x;                      // of [B, H_kv, R]
-    const int bh = int(row / k.R), x = int(row - int64_t(bh) * k.R);
-    const int b = bh / k.H_kv, h = bh - b * k.H_kv;
-
-    // ---- the prefix's pieces
-    long long U = 0, us = 0;
-    int item = 0;
-    bool bad = false;
-    for (int p = threadIdx.x; p < k.prefix.count; p += kMergeThreads) {
-        bool no;
-        const Group g = group_at(k, p, &no);
-        bad |= no;
-        const long long units = g.items * g.item_units();
-        // the prefixes before b's end at or before it
-        const bool before = g.items > 0 && g.first + g.rows / k.R <= b;
-        U += units;
-        us += before ? units : 0;
-        item += before ? g.items : 0;
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        U += __shfl_xor_sync(0xffffffffu, U, o);
-        us += __shfl_xor_sync(0xffffffffu, us, o);
-        item += __shfl_xor_sync(0xffffffffu, item, o);
-    }
-    if (lane == 0) {
-        red_units[0][warp] = U;
-        red_units[1][warp] = us;
-        red_items[warp] = item;
-    }
-    // ---- the segment's pieces behind it
-    const int cap = k.max_pages * k.block_ps;
-    auto granules = [&](int q) {
-        int n = __ldcg(k.context_lens + q);
-        n = n < 0 ? 0 : n > cap ? cap : n;
-        return suffix_granules(n, min(prefix_len_of(k.prefix, q), n), a.box_rows, a.tile_keys);
-    };
-    int total = 0, ahead = 0;
-    for (int q = threadIdx.x; q < k.B; q += kMergeThreads) {
-        const int gs = granules(q) * a.per_req;
-        total += gs;
-        ahead += q < b ? gs : 0;
-    }
-    total = __reduce_add_sync(0xffffffffu, total);
-    ahead = __reduce_add_sync(0xffffffffu, ahead);
-    __shared__ int red_gran[2][kMergeThreads / 32];
-    if (lane == 0) {
-        red_gran[0][warp] = total;
-        red_gran[1][warp] = ahead;
-    }
-    bad = __syncthreads_or(bad);
-    U = us = 0;
-    item = total = ahead = 0;
-#pragma unroll
-    for (int w = 0; w < kMergeThreads / 32; ++w) {
-        U += red_units[0][w];
-        us += red_units[1][w];
-        item += red_items[w];
-        total += red_gran[0][w];
-        ahead += red_gran[1][w];
-    }
-    int np = 0, regions = 1;
-    const float* p_o = nullptr;
-    const float2* p_ml = nullptr;
-    {
-        const int p = bad ? -1 : prefix_of(k.prefix, b);
-        if (p >= 0) {
-            bool no;
-            const Group g = group_at(k, p, &no);
-            const int f = (b - g.first) * k.R + x;
-            if (g.items > 0) {
-                const int blocks = (g.rows + 255) / 256;
-                const int i = h * blocks + (f >> 8);
-                const long long at = us + i * g.item_units() + kItemUnits;
-                const long long G = working_blocks(U, a.prefix_grid);
-                const int c0 = block_of(at, U, G);
-                np = block_of(at + (long long)(g.tiles - 1) * kTileUnits, U, G) - c0 + 1;
-                regions = g.rows > 128 ? 1 : 2;
-                const int64_t place = (int64_t(item) + i + c0) * 256 + (f & 255);
-                p_o = k.state + place * D;
-                p_ml = k.state_ml + place;
-            }
-        }
-    }
-    const int mine = np * regions;
-    const int seg_rows = 8 * a.row_tiles;                // rows of a segment's slot
-    const int ms = x / kSegmentRows, xr = x - ms * kSegmentRows;
-    const int hm = h * a.MS + ms;
-    const int seg = b * a.per_req + hm;
-    const int len = granules(b);
-    const int64_t units = total + int64_t(k.B) * a.per_req;
-    const int64_t grid = suffix_blocks(units, a.suffix_grid);
-    const int64_t u0 = ahead + int64_t(hm) * len + (seg + 1);
-    const int64_t first = block_of_unit(u0, units, grid);
-    const int ns = int(block_of_unit(u0 + len - 1, units, grid) - first) + 1;
+    const int share = a.share, sub = warp & (share - 1);
+    const int row = (int(blockIdx.x) * kMergeWarps + warp) / share;   // of [B, H_kv, R]
+    const bool live = row < k.B * k.H_kv * k.R;
+    const int bh = live ? k.by_R.of(row) : 0, x = live ? row - bh * k.R : 0;
+    const int b = a.by_H.of(bh), h = bh - b * k.H_kv;
+    int np = 0, ns = 0, twice = 0;                       // pieces of the prefix, of the segment
+    int64_t p_row = 0;                                   // the row's in the prefix's first state
     const int slot = suffix_slot_floats(D, a.row_tiles);
-    const float* s_at = a.suffix_state + (int64_t(seg) + first) * slot;
-    const int pieces = mine + ns;
-    auto state_of = [&](int t) -> const float* {
-        if (t < mine) {
-            const int c = regions == 2 ? t >> 1 : t;
-            return p_o + (int64_t(c) * 256 + (regions == 2 ? (t & 1) * 128 : 0)) * D;
-        }
-        return s_at + int64_t(t - mine) * slot + xr * D;
-    };
-    auto ml_of = [&](int t) -> const float2* {
-        if (t < mine) {
-            const int c = regions == 2 ? t >> 1 : t;
-            return p_ml + int64_t(c) * 256 + (regions == 2 ? (t & 1) * 128 : 0);
-        }
-        return reinterpret_cast<const float2*>(s_at + int64_t(t - mine) * slot + seg_rows * D + 2 * xr);
-    };
-
+    const int xr = x % kSegmentRows;
+    const int seg = (b * k.H_kv + h) * a.MS + x / kSegmentRows;
+    const float* s_at = a.suffix_state;
     grid_dependency_wait();
-    // ---- the largest maximum, each piece's factor, the sum
-    float top = -INFINITY;
-    for (int t = threadIdx.x; t < pieces; t += kMergeThreads)
-        top = fmaxf(top, __ldcg(ml_of(t)).x);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    if (lane == 0)
-        red[0][warp] = top;
-    __syncthreads();
-    top = fmaxf(fmaxf(red[0][0], red[0][1]), fmaxf(red[0][2], red[0][3]));
-    float sum = 0.f;
-    for (int t = threadIdx.x; t < pieces; t += kMergeThreads) {
-        const float2 v = __ldcg(ml_of(t));
-        const float w = v.x == -INFINITY ? 0.f : fast_exp2(v.x - top);
-        weights[t] = w;
-        sum += w * v.y;
+    grid_launch_dependents();
+    if (live) {
+        const int4 note = __ldcg(k.note_request + b);
+        const int2 blocks = __ldcg(a.note_segment + seg);
+        if (note.x >= 0) {
+            const int f = note.y + x, item = note.x + h * note.z + (f >> 8);
+            const int2 where = __ldcg(k.note_item + item);
+            twice = note.w;                              // both halves hold the rows
+            np = (where.y - where.x + 1) << twice;
+            p_row = (int64_t(item) + where.x) * 256 + (f & 255);
+        }
+        ns = blocks.y - blocks.x + 1;
+        s_at += (int64_t(seg) + blocks.x) * slot;
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-        sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (lane == 0)
-        red[1][warp] = sum;
-    __syncthreads();
-    sum = (red[1][0] + red[1][1]) + (red[1][2] + red[1][3]);
-    // ---- the outputs: warp w takes pieces w, w + 4, ...
+    const int pieces = np + ns;
+    auto p_place = [&](int t) { return p_row + int64_t(t >> twice) * 256 + ((t & twice) << 7); };
+
+    // ---- this warp's pieces sub, sub + share, ...: 32 at a time, their (m, l) a lane
+    float top = -INFINITY, sum = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int t = warp; t < pieces; t += kMergeThreads / 32) {
-        const float w = weights[t];
-        if (w > 0.f) {                                   // nothing seen: the state was not written
-            if constexpr (D == 128) {
-                const float4 v = __ldcg(reinterpret_cast<const float4*>(state_of(t)) + lane);
-                o.x = fmaf(w, v.x, o.x);
-                o.y = fmaf(w, v.y, o.y);
-                o.z = fmaf(w, v.z, o.z);
-                o.w = fmaf(w, v.w, o.w);
-            } else {
-                const float2 v = __ldcg(reinterpret_cast<const float2*>(state_of(t)) + lane);
-                o.x = fmaf(w, v.x, o.x);
-                o.y = fmaf(w, v.y, o.y);
+    for (int t0 = sub; t0 < pieces; t0 += 32 * share) {
+        const int mine = t0 + lane * share;
+        float2 ml = make_float2(-INFINITY, 0.f);
+        if (mine < pieces)
+            ml = __ldcg(mine < np ? k.state_ml + p_place(mine)
+                                  : reinterpret_cast<const float2*>(s_at + int64_t(mine - np) * slot +
+                                                                    8 * a.row_tiles * D) + xr);
+        float m = fmaxf(top, ml.x);
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1)
+            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+        // nothing seen: the state was not written, and counts for nothing
+        const float w = ml.x == -INFINITY ? 0.f : fast_exp2(ml.x - m);
+        const float old = top == -INFINITY ? 0.f : fast_exp2(top - m);
+        float add = w * ml.y;
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1)
+            add += __shfl_xor_sync(0xffffffffu, add, off);
+        sum = sum * old + add;
+        o.x *= old;
+        o.y *= old;
+        o.z *= old;
+        o.w *= old;
+        top = m;
+        const int n = min(32, (pieces - t0 + share - 1) / share);
+        constexpr int kAtOnce = 4;                       // on their way
+        for (int i0 = 0; i0 < n; i0 += kAtOnce) {
+            float4 v[kAtOnce];
+            float wi[kAtOnce];
+#pragma unroll
+            for (int i = 0; i < kAtOnce; ++i) {
+                wi[i] = __shfl_sync(0xffffffffu, w, i0 + i);     // 0 behind the last
+                v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (wi[i] > 0.f) {
+                    const int t = t0 + (i0 + i) * share;
+                    const float* at = t < np ? k.state + p_place(t) * D : s_at + int64_t(t - np) * slot + xr * D;
+                    if constexpr (D == 128) {
+                        v[i] = __ldcg(reinterpret_cast<const float4*>(at) + lane);
+                    } else {
+                        const float2 x2 = __ldcg(reinterpret_cast<const float2*>(at) + lane);
+                        v[i].x = x2.x;
+                        v[i].y = x2.y;
+                    }
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < kAtOnce; ++i) {
+                o.x = fmaf(wi[i], v[i].x, o.x);
+                o.y = fmaf(wi[i], v[i].y, o.y);
+                o.z = fmaf(wi[i], v[i].z, o.z);
+                o.w = fmaf(wi[i], v[i].w, o.w);
             }
         }
     }
-    sums[warp][lane] = o;
-    __syncthreads();
-    if (warp == 0) {
-#pragma unroll
-        for (int w = 1; w < kMergeThreads / 32; ++w) {
-            const float4 v = sums[w][lane];
-            o.x += v.x;
-            o.y += v.y;
-            o.z += v.z;
-            o.w += v.w;
+    if (share > 1) {
+        sums[warp][lane] = o;
+        if (lane == 0)
+            row_ml[warp] = make_float2(top, sum);
+        __syncthreads();
+        if (sub != 0)
+            return;
+        float m = top;
+        for (int w = 1; w < share; ++w)
+            m = fmaxf(m, row_ml[warp + w].x);
+        const float f = top == -INFINITY ? 0.f : fast_exp2(top - m);
+        sum *= f;
+        o.x *= f;
+        o.y *= f;
+        o.z *= f;
+        o.w *= f;
+        for (int w = 1; w < share; ++w) {
+            const float2 ml = row_ml[warp + w];
+            const float fw = ml.x == -INFINITY ? 0.f : fast_exp2(ml.x - m);
+            const float4 v = sums[warp + w][lane];
+            sum = fmaf(fw, ml.y, sum);
+            o.x = fmaf(fw, v.x, o.x);
+            o.y = fmaf(fw, v.y, o.y);
+            o.z = fmaf(fw, v.z, o.z);
+            o.w = fmaf(fw, v.w, o.w);
         }
+    }
+    if (live) {
         const float inv = sum > 0.f ? a.out_scale / sum : 0.f;
         uint16_t* dst = a.out + ((int64_t(b) * k.H_q + h * k.G) * k.L + x) * D;
         if constexpr (D == 128)
@@ -835,32 +1046,41 @@ __global__ void __launch_bounds__(kMergeThreads) prefix_merge_kernel(const Prefi
 
 }  // namespace
 
-size_t prefix_smem_bytes(int D, int count)
+size_t prefix_smem_bytes(int D, int kind, int count)
 {
-    return size_t(D == 64 ? Layout<64>::kGroups : Layout<128>::kGroups) + size_t(count) * sizeof(Group) + 1024;
+    const int fixed = kind == kE4m3Pool ? Layout<128, kE4m3Pool>::kGroups
+                      : kind == kQ4Pool ? Layout<128, kQ4Pool>::kGroups
+                      : D == 64         ? Layout<64, kBf16Pool>::kGroups
+                                        : Layout<128, kBf16Pool>::kGroups;
+    return size_t(fixed) + size_t(count) * sizeof(Group) + 1024;
 }
 
-size_t prefix_state_bytes(const pa_shape& s, int count, int grid, size_t* ml_off)
+size_t prefix_state_bytes(const pa_shape& s, int64_t items, int grid, size_t* ml_off, size_t* pieces_off)
 {
-    const int64_t R = int64_t(s.num_q_heads / s.num_kv_heads) * s.q_len;
-    const int64_t items = s.num_kv_heads * (int64_t(s.batch) * R / 256 + count);
     const size_t slots = size_t(items + grid);
     *ml_off = slots * 256 * size_t(s.head_dim) * sizeof(float);
-    return *ml_off + slots * 256 * sizeof(float2);
+    *pieces_off = *ml_off + slots * 256 * sizeof(float2);
+    return *pieces_off + (items > kMaxPieces ? size_t(items) * size_t(grid) * sizeof(Piece) : 0);
 }
 
 cudaError_t launch_prefix(const CUtensorMap& key_map, const CUtensorMap& value_map, const PrefixKernelArgs& a,
-                          int D, int grid, int device, cudaStream_t stream)
+                          int D, int kind, int grid, int device, cudaStream_t stream)
 {
     using Kernel = void (*)(CUtensorMap, CUtensorMap, PrefixKernelArgs);
     constexpr int kMaxDev = 64;
-    static std::atomic<bool> raised[kMaxDev][2];
-    static std::atomic<int> regs_ok[kMaxDev][2];
+    static std::atomic<bool> raised[kMaxDev][4];
+    static std::atomic<int> regs_ok[kMaxDev][4];
     if (device < 0 || device >= kMaxDev)
         return cudaErrorInvalidDevice;
-    const int which = D == 64 ? 0 : 1;
-    const Kernel kernel = D == 64 ? prefix_kernel<64> : prefix_kernel<128>;
+    const int which = kind == kE4m3Pool ? 2 : kind == kQ4Pool ? 3 : D == 64 ? 0 : 1;
+    static const Kernel kernels[4] = {prefix_kernel<64, kBf16Pool>, prefix_kernel<128, kBf16Pool>,
+                                      prefix_kernel<128, kE4m3Pool>, prefix_kernel<128, kQ4Pool>};
+    const Kernel kernel = kernels[which];
     const void* fn = reinterpret_cast<const void*>(kernel);
+    const int threads = kind == kBf16Pool ? Layout<128, kBf16Pool>::kThreads : Layout<128, kE4m3Pool>::kThreads;
+    const int first = kind == kBf16Pool ? Layout<128, kBf16Pool>::kRegsFirst : Layout<128, kE4m3Pool>::kRegsFirst;
+    const int most = kind == kBf16Pool ? Layout<128, kBf16Pool>::kRegsSoftmax : Layout<128, kE4m3Pool>::kRegsSoftmax;
+    const int sum = kind == kBf16Pool ? Layout<128, kBf16Pool>::kRegsSum : Layout<128, kE4m3Pool>::kRegsSum;
     // setmaxnreg draws on the registers that the block was launched with
     int rk = regs_ok[device][which].load(std::memory_order_relaxed);
     if (rk == 0) {
@@ -868,10 +1088,7 @@ cudaError_t launch_prefix(const CUtensorMap& key_map, const CUtensorMap& value_m
         const cudaError_t e = cudaFuncGetAttributes(&fa, fn);
         if (e != cudaSuccess)
             return e;
-        rk = fa.numRegs >= kRegsProducer && fa.numRegs <= kRegsSoftmax &&
-                     128 * kRegsProducer + 256 * kRegsSoftmax <= kThreads * fa.numRegs
-                 ? 1
-                 : 2;
+        rk = fa.numRegs >= first && fa.numRegs <= most && sum <= threads * fa.numRegs ? 1 : 2;
         regs_ok[device][which].store(rk, std::memory_order_relaxed);
     }
     if (rk != 1)
@@ -884,18 +1101,23 @@ cudaError_t launch_prefix(const CUtensorMap& key_map, const CUtensorMap& value_m
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(unsigned(grid));
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = prefix_smem_bytes(D, a.prefix.count);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = prefix_smem_bytes(D, kind, a.prefix.count);
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kernel, key_map, value_map, a);
 }
 
-cudaError_t launch_prefix_merge(const PrefixMergeArgs& a, int D, cudaStream_t stream)
+cudaError_t launch_prefix_merge(PrefixMergeArgs a, int D, int sm_count, cudaStream_t stream)
 {
     const PrefixKernelArgs& k = a.prefix_args;
-    const int64_t blocks = int64_t(k.B) * k.H_kv * k.R;
+    // as many warps a row as the device holds of them at once
+    const int64_t rows = int64_t(k.B) * k.H_kv * k.R;
+    a.share = kMergeWarps;
+    while (a.share > 1 && rows * a.share > int64_t(sm_count) * 6 * kMergeWarps)
+        a.share /= 2;
+    const int64_t blocks = (rows * a.share + kMergeWarps - 1) / kMergeWarps;
     if (blocks <= 0 || blocks >= (int64_t(1) << 31))
         return cudaErrorInvalidValue;
     cudaLaunchAttribute attr[1];
@@ -904,7 +1126,6 @@ cudaError_t launch_prefix_merge(const PrefixMergeArgs& a, int D, cudaStream_t st
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(unsigned(blocks));
     cfg.blockDim = dim3(kMergeThreads);
-    cfg.dynamicSmemBytes = size_t(2 * a.prefix_grid + a.suffix_grid + 2) * sizeof(float);
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;

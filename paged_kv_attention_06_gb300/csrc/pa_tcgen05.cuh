@@ -62,8 +62,8 @@ __device__ __forceinline__ uint64_t desc_advance(uint64_t desc, uint32_t bytes)
     return desc + uint64_t(bytes >> 4);
 }
 
-// Instruction descriptor of tcgen05.mma kind::f16: fp32 accumulator, bf16 A
-// and B, A K-major, B K-major (b_mn_major = 0) or MN-major (1), N >> 3 in
+// Instruction descriptor of tcgen05.mma kind::f16: fp32 accumulator, bf16 (or, below,
+// f16) A and B, A K-major, B K-major (b_mn_major = 0) or MN-major (1), N >> 3 in
 // bits 17-22, M >> 4 in bits 24-28.
 __host__ __device__ constexpr uint32_t idesc_bf16_f32(int M, int N, int b_mn_major)
 {
@@ -76,7 +76,12 @@ __host__ __device__ constexpr uint32_t idesc_bf16_f32(int M, int N, int b_mn_maj
            | (uint32_t(M >> 4) << 24);    // M
 }
 
-// D[tmem] (+)= A[smem] * B[smem]^T, issued by one thread.
+__host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, int b_mn_major)
+{
+    return idesc_bf16_f32(M, N, b_mn_major) & ~((1u << 7) | (1u << 10));
+}
+
+// D[tmem] (+)= A[smem] * B[smem]^T, issued by one thread. (Either type: the descriptor says.)
 __device__ __forceinline__ void tc_mma_bf16(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
                                             uint32_t idesc, uint32_t accumulate)
 {

@@ -55,7 +55,7 @@ def make(prefixes, lens, H_q, H_kv, L, D, ps, seed, pool="bf16", poison=True):
                 prefix_table=pt.cuda(), prefix_lens=i32([n for n, _ in prefixes]), prefix_starts=i32(starts))
 
 
-def _rows(pool, kind, page, off, copied):
+def _rows(pool, kind, page, off, shared):
     """Values [H, n, D] and the sizes of what is summed for them, as the calls round them."""
     x = pool[page, :, off].transpose(0, 1)
     if kind == "bf16":
@@ -63,10 +63,10 @@ def _rows(pool, kind, page, off, copied):
     if kind == "e4m3":
         return x.view(F8).float().double(), x.view(F8).float().double().abs()
     rows = x.cpu().numpy()
-    if copied:
-        v = torch.from_numpy(q4_ref.dense_values(rows)).cuda()
-        return v, v.abs()
     c, s, m = q4_ref.parts(rows)
+    if shared:
+        v = torch.from_numpy((m + s * c).astype(np.float16).astype(np.float64)).cuda()
+        return v, v.abs()
     sc = torch.from_numpy((s * c).astype(np.float16).astype(np.float64)).cuda()
     m = torch.from_numpy(m).cuda()
     return sc + m, sc.abs() + m.abs()
@@ -94,9 +94,9 @@ def reference(c, kind="bf16", group=None):
         out, mag, size = torch.zeros_like(q), torch.zeros_like(q), 0.0
         if parts:
             k, v, ka, va = [], [], [], []
-            for page, off, copied in parts:
+            for page, off, shared in parts:
                 for pool, vals, sizes in ((c["key_pages"], k, ka), (c["value_pages"], v, va)):
-                    x, a = _rows(pool, kind, page, off, copied)
+                    x, a = _rows(pool, kind, page, off, shared)
                     vals.append(x)
                     sizes.append(a)
             k, v, ka, va = (torch.cat(x, 1).repeat_interleave(H_q // H_kv, 0) for x in (k, v, ka, va))
@@ -113,7 +113,7 @@ def reference(c, kind="bf16", group=None):
 def check(out, ref, kind, n_max, vmax):
     """Output rounding: half a step of bf16, 2^-8 of the value. The prefix's weights are
     rounded to bf16 for P . V, 2^-8 of each term (the others finer: two bf16, or f16 for
-    codes, with 2^-25 a key where f16 is subnormal). Scores: D fp32 additions of
+    codes, there in the prefix too, with 2^-25 a key where f16 is subnormal). Scores: D fp32 additions of
     truncated size, 2^-16 of scale * sum |q| |k|, on both sides of the quotient. The sums:
     n roundings; the merge: three more of 2^-22 each (ex2)."""
     for b, (r, mag, size) in enumerate(ref):

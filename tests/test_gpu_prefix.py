@@ -71,6 +71,14 @@ def test_many_prefixes():
     run(prefixes, lens, 4, 2, 1, 128, 16, seed=4)
 
 
+def test_short_prefixes_beside_long_ones():
+    """A block's share of the work is over 64 short prefixes (more than it lists in shared
+    memory)."""
+    prefixes = [(250000, 1), (250000, 1)] + [(5 + i % 3, 1) for i in range(100)]
+    lens = [n + 1 + i % 5 for i, (n, _) in enumerate(prefixes)]
+    run(prefixes, lens, 8, 8, 1, 64, 256, seed=13)
+
+
 def test_requests_shorter_than_their_prefix():
     """Rows that see a part of the prefix, one key of it, or nothing."""
     run([(600, 8)], [600, 599, 300, 129, 128, 1, 0, 700], 8, 2, 1, 128, 16, seed=5)

@@ -69,5 +69,5 @@ def test_workspace_of_invalid_sizes_is_zero(lib):
               lib.pa_decode_prefix_q4_workspace_bytes):
         for bad in (dict(head_dim=96), dict(batch=0), dict(num_q_heads=5), dict(q_len=0)):
             assert f(Shape(**dict(SHAPE, **bad)), 16, 1, 60) == 0
-        for ps, count, longest in ((12, 1, 60), (16, 0, 60), (16, 1025, 60), (16, 1, 0), (16, 1, 1 << 30)):
+        for ps, count, longest in ((12, 1, 60), (16, 0, 60), (16, 257, 60), (16, 1, 0), (16, 1, 1 << 30)):
             assert f(Shape(**SHAPE), ps, count, longest) == 0
