@@ -1714,7 +1714,7 @@ pa_status pa_append_kv_q4(const void* key, const void* value, void* key_pages, v
     if (shape.head_dim != 128 || !pow2_in(page_size, 1, 256))
         return PA_ERR_UNSUPPORTED;
     if (int64_t(shape.num_pages) * shape.num_kv_heads * page_size >= (int64_t(1) << 31) ||
-        int64_t(shape.batch) * shape.q_len * shape.num_kv_heads >= (int64_t(1) << 35))
+        int64_t(shape.batch) * shape.q_len * shape.num_kv_heads >= (int64_t(1) << 31) - 65536 * 16)
         return PA_ERR_UNSUPPORTED;
     DeviceInfo* dev;
     pa_status st = device_info(&dev);
@@ -1754,7 +1754,7 @@ pa_status pa_gather_kv_q4(const void* key_pages, const void* value_pages,
     pa_status st = check_q4_pools(shape, page_size);
     if (st != PA_OK)
         return st;
-    if (int64_t(shape.batch) * shape.num_kv_heads * ((int64_t(dense_len) + 63) / 64) >=
+    if (int64_t(shape.batch) * shape.num_kv_heads * ((int64_t(dense_len) + 127) / 128) >=
         (int64_t(1) << 31))
         return PA_ERR_UNSUPPORTED;
     DeviceInfo* dev;

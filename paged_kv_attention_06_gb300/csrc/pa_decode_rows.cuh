@@ -71,7 +71,7 @@ struct Shape {
     static constexpr int kKLoads = kRowBytes / 64;    // 16-byte loads per lane and K row
     static constexpr int kVLoads = (kRowBytes + 127) / 128;   // and V row
     static constexpr int kSteps = D / 16;             // k-steps of S, 16-row tiles of O^T
-    static constexpr int kStages = 2;                 // tiles on their way per warp
+    static constexpr int kStages = KIND == kQ4Pool ? 1 : 2;   // tiles on their way per warp
     // K (or V) of one tile: [128-byte column block][key][128 bytes], or [key][80 bytes]
     static constexpr int kTileBytes = kTok * kRowBytes;
 };
@@ -79,6 +79,10 @@ struct Shape {
 template <int D, int KIND, int NT>
 struct Smem {
     using Sh = Shape<D, KIND>;
+    // 4-bit rows, 32 requests of up to 4096 keys, 64 of up to 8192, 8 of 16k-32k (us): three
+    // blocks and two tiles of 32 keys on their way 21.1, 48.3, 72.2, one 16.4, 47.0, 70.2;
+    // two blocks and two tiles 17.5, 53.1, 79.7; four 23.4, 58.5, 76.0; three blocks and one
+    // tile of 64 keys 18.3, 50.1, 67.5.
     static constexpr int kBlocksPerSM = KIND == kQ4Pool && NT == 1 ? 3 : 2;
     static constexpr int kSlab = (D / 16 * NT * 4 + 4 * NT) * 32 * 4; // one warp's state: O^T, m, l
     static constexpr int kRing = 0;                                   // [warp][stage][K, V]
@@ -437,12 +441,10 @@ __global__ void __launch_bounds__(kThreads, (Smem<D, KIND, NT>::kBlocksPerSM))
                           !(kMode == kWindow && t >= a.sinks && t + a.box_rows <= p.span.first_seen);
         return live ? t : -1;
     };
-    auto page_of = [&](const Place& p) {
-        const int t = box_token(p);
+    auto page_of = [&](const Place& p, int t) {
         return t < 0 ? 0 : __ldg(a.block_table + int64_t(p.sp.b) * a.max_pages + (t >> a.ps_shift));
     };
-    auto row_of = [&](const Place& p, int phys) {
-        const int t = box_token(p);
+    auto row_of = [&](const Place& p, int t, int phys) {
         if (t < 0)
             return -1;
         if (unsigned(phys) >= unsigned(a.num_pages)) {
@@ -486,15 +488,18 @@ __global__ void __launch_bounds__(kThreads, (Smem<D, KIND, NT>::kBlocksPerSM))
             enter(p);
         }
     };
-    int page = page_of(ahead);
+    int tok = box_token(ahead);                      // the lane's box of the next tile, and its page
+    int page = page_of(ahead, tok);
 #pragma unroll
     for (int st = 0; st < kStages; ++st) {
         const bool live = ahead.x < x_end;
         if (live) {
-            const int row = row_of(ahead, page);
+            const int row = row_of(ahead, tok, page);
             step(ahead);
-            if (ahead.x < x_end)
-                page = page_of(ahead);
+            if (ahead.x < x_end) {
+                tok = box_token(ahead);
+                page = page_of(ahead, tok);
+            }
             copy(row, st, 0);
             copy(row, st, 1);
         }
@@ -694,12 +699,14 @@ __global__ void __launch_bounds__(kThreads, (Smem<D, KIND, NT>::kBlocksPerSM))
             int row_v = -1;
             const bool more = ahead.x < x_end;
             if (more) {
-                row_v = row_of(ahead, page);
+                row_v = row_of(ahead, tok, page);
                 __syncwarp();                        // every lane has read the place
                 copy(row_v, stage, 0);
                 step(ahead);
-                if (ahead.x < x_end)
-                    page = page_of(ahead);
+                if (ahead.x < x_end) {
+                    tok = box_token(ahead);
+                    page = page_of(ahead, tok);
+                }
             }
             const bool edge = t0 + kTok - 1 > lim_min || t0 + kTok > end || (kMode == kWindow && t0 < low_max) ||
                               (kMode == kSuffix && t0 < span.first_seen);

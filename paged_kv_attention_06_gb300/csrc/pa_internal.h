@@ -41,6 +41,23 @@ pa_status device_info(DeviceInfo** out);
 // threads whose first calls meet do not lower each other's.
 cudaError_t raise_smem_limit(const void* kernel, std::atomic<bool>* raised);
 
+// Division of 0 .. 2^31 - 1 by a fixed number: with s = ceil(log2 d), m = floor(2^32 (2^s - d)
+// / d) + 1 the quotient is (umulhi(m, n) + n) >> s.
+struct FixedDivisor {
+    uint32_t mul;
+    int32_t shift;
+    void set(int32_t d)
+    {
+        shift = 0;
+        while ((int64_t(1) << shift) < d)
+            ++shift;
+        mul = uint32_t((((uint64_t(1) << shift) - uint64_t(d)) << 32) / uint64_t(d) + 1);
+    }
+#ifdef __CUDACC__
+    __device__ __forceinline__ int of(int n) const { return int((__umulhi(mul, uint32_t(n)) + uint32_t(n)) >> shift); }
+#endif
+};
+
 // ---------------------------------------------------------------------------
 // Write path
 
@@ -133,7 +150,8 @@ struct PageReadArgs {
     int32_t B, H_kv, ps, num_pages, max_pages;
     int32_t max_len;              // rows a request has room for
     int32_t copy_pages;
-    int32_t chunks;               // set by the launcher
+    int32_t chunks;               // set by the launcher, like the divisors
+    FixedDivisor by_chunks, by_H;
 };
 cudaError_t launch_append_q4(const AppendArgs& a, cudaStream_t stream);
 cudaError_t launch_read_pages(PageReadArgs a, int kind, int D, cudaStream_t stream);
@@ -249,23 +267,6 @@ int decode_rows_launch_grid(const pa_shape& s, int kind, int64_t granule_bound, 
 cudaError_t launch_decode_rows(const CUtensorMap& key_map, const CUtensorMap& value_map, DecodeArgs a,
                                const pa_shape& s, int kind, int grid, void* workspace, int device,
                                cudaStream_t stream);
-
-// Division of 0 .. 2^31 - 1 by a fixed number: with s = ceil(log2 d), m = floor(2^32 (2^s - d)
-// / d) + 1 the quotient is (umulhi(m, n) + n) >> s.
-struct FixedDivisor {
-    uint32_t mul;
-    int32_t shift;
-    void set(int32_t d)
-    {
-        shift = 0;
-        while ((int64_t(1) << shift) < d)
-            ++shift;
-        mul = uint32_t((((uint64_t(1) << shift) - uint64_t(d)) << 32) / uint64_t(d) + 1);
-    }
-#ifdef __CUDACC__
-    __device__ __forceinline__ int of(int n) const { return int((__umulhi(mul, uint32_t(n)) + uint32_t(n)) >> shift); }
-#endif
-};
 
 // Decode behind shared prefixes: the prefixes' part for all their requests' rows, and
 // the merge of it with the few-row kernel's (kSuffix).

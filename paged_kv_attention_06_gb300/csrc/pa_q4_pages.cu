@@ -24,28 +24,31 @@
 namespace pa {
 namespace {
 
-// Minimum and maximum that keep a NaN.
-__device__ __forceinline__ float min_nan(float a, float b)
+// Minimum and maximum of f16 pairs that keep a NaN.
+__device__ __forceinline__ uint32_t min2(uint32_t a, uint32_t b)
 {
-    float r;
-    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    uint32_t r;
+    asm("min.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
-__device__ __forceinline__ float max_nan(float a, float b)
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b)
 {
-    float r;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    uint32_t r;
+    asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
+__device__ __forceinline__ float2 widen(uint32_t v) { return __half22float2(*reinterpret_cast<const __half2*>(&v)); }
 
-// The code of y = m + t, where the quotient by fp32 arithmetic lies too near a half
-// to say on which side it is: in 64 bits, where t and (k + 1/2) s are exact.
-__device__ __noinline__ int code_near_half(float y, float m, float s, float q)
+// The code of y where the quotient q by fp32 arithmetic may lie too near a half to say on
+// which side it is. With t + e = y - m exactly (t rounded, e what that lost), k = floor(q):
+// (k + 1/2) s has 16 bits, so t - (k + 1/2) s is exact near the half, and its sum with e
+// has the sign of y - m - (k + 1/2) s.
+__device__ __forceinline__ float code_near_half(float y, float m, float s, float q)
 {
-    const double t = double(y) - double(m);
-    const int k = int(floorf(q));
-    const double half = (double(k) + 0.5) * double(s);
-    return k + (t > half || (t == half && (k & 1)) ? 1 : 0);
+    const float t = y - m, back = t - y, e = (y - (t - back)) - (m + back);
+    const float k = floorf(q);
+    const float d = fmaf(-(k + 0.5f), s, t) + e;
+    return fminf(d > 0.f || (d == 0.f && (int(k) & 1)) ? k + 1.f : k, 15.f);
 }
 
 // One lane's 8 elements of a row (the group's other 24 are in the lanes that differ in
@@ -53,74 +56,83 @@ __device__ __noinline__ int code_near_half(float y, float m, float s, float q)
 __device__ __forceinline__ uint32_t quantise8(const uint4& x, uint32_t* params)
 {
     const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-    float y[8];
+    uint32_t y[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        y[2 * i] = __uint_as_float(w[i] << 16);
-        y[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
+    for (int i = 0; i < 4; ++i)      // f16 first: what is past 448 is cut the same way
+        y[i] = min2(max2(bf16x2_to_f16x2(w[i]), 0xdf00df00u), 0x5f005f00u);
+    static_assert(kQ4Max == 448.f, "0x5f00");
+    uint32_t lo = min2(min2(y[0], y[1]), min2(y[2], y[3])), hi = max2(max2(y[0], y[1]), max2(y[2], y[3]));
+    // (least, negated largest) of the pair, then of the four lanes
+    lo = min2(__byte_perm(lo, hi ^ 0x80008000u, 0x5410), __byte_perm(lo, hi ^ 0x80008000u, 0x7632));
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-        y[i] = __half2float(__float2half_rn(min_nan(max_nan(y[i], -kQ4Max), kQ4Max)));
-    float lo = y[0], hi = y[0];
-#pragma unroll
-    for (int i = 1; i < 8; ++i) {
-        lo = min_nan(lo, y[i]);
-        hi = max_nan(hi, y[i]);
-    }
-#pragma unroll
-    for (int o = 1; o < 4; o <<= 1) {
-        lo = min_nan(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-        hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, o));
-    }
-    const __half sh = __float2half_rn(__fdiv_rn(hi - lo, 15.f));
+    for (int o = 1; o < 4; o <<= 1)
+        lo = min2(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+    const float2 ends = widen(lo);
+    const float m = ends.x;
+    const __half sh = __float2half_rn(__fdiv_rn(-ends.y - m, 15.f));
     const float s = __half2float(sh);
-    *params = uint32_t(__half_as_ushort(sh)) | uint32_t(__half_as_ushort(__float2half_rn(lo))) << 16;
-    // t / s to within 2^-19 of a step, times what a half allows for the rounding of t
-    const float inv = s > 0.f ? __frcp_rn(s) : 0.f;
-    uint32_t codes = 0;
+    *params = uint32_t(__half_as_ushort(sh)) | lo << 16;
+    // t / s to within 2^-18 of a step, a quarter of what a half is given for it
+    const float inv = s > 0.f ? __fdividef(1.f, s) : 0.f;
+    const float2 m2 = make_float2(-m, -m), inv2 = make_float2(inv, inv);
+    const float2 round2 = make_float2(12582912.f, 12582912.f);      // 1.5 * 2^23: q + that is rounded to a whole
+    const float2 back2 = make_float2(-12582912.f, -12582912.f), minus2 = make_float2(-1.f, -1.f);
+    float worst = 0.f;
+    float2 sum = make_float2(0.f, 0.f);                  // c0 + 16 c2 + 256 c4 + 4096 c6, and c1 + ...
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const float q = (y[i] - lo) * inv;
-        const float r = rintf(q);
-        int c = int(r);
-        if (fabsf(q - r) > 0.5f - 0x1p-16f)
-            c = code_near_half(y[i], lo, s, q);
-        codes |= uint32_t(min(max(c, 0), 15)) << (4 * i);
+    for (int i = 3; i >= 0; --i) {
+        const float2 q = __fmul2_rn(__fadd2_rn(widen(y[i]), m2), inv2);
+        const float2 r = __fadd2_rn(__fadd2_rn(q, round2), back2);
+        const float2 d = __ffma2_rn(r, minus2, q);
+        worst = fmaxf(worst, fmaxf(fabsf(d.x), fabsf(d.y)));
+        sum = __ffma2_rn(sum, make_float2(16.f, 16.f), r);
     }
-    return codes;
+    // Near a half (one group in 50: bf16 values are coarse), and where s is so small that
+    // its own rounding may put a quotient past 15.
+    if (worst > 0.5f - 0x1p-16f || s < 0x1p-14f) {
+        sum = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int i = 3; i >= 0; --i) {
+            const float2 v = widen(y[i]);
+            sum.x = fmaf(sum.x, 16.f, code_near_half(v.x, m, s, (v.x - m) * inv));
+            sum.y = fmaf(sum.y, 16.f, code_near_half(v.y, m, s, (v.y - m) * inv));
+        }
+    }
+    // the codes of even elements in bits 0-3, 8-11, ..., of odd ones 4 bits on
+    auto spread = [](float c) {
+        const uint32_t x = __float_as_uint(c + 8388608.f) & 0xffffu;
+        const uint32_t y2 = (x | x << 8) & 0x00ff00ffu;
+        return (y2 | y2 << 4) & 0x0f0f0f0fu;
+    };
+    const uint32_t all = spread(sum.x) | spread(sum.y) << 4;
+    return s > 0.f ? all : 0u;                           // one value, or a NaN
 }
 
 // Lane group of 16 per (request, KV head, token) row, K then V.
-__global__ void __launch_bounds__(256) append_q4_kernel(const AppendArgs a)
+__global__ void __launch_bounds__(256) append_q4_kernel(const AppendArgs a, const FixedDivisor by_L, const FixedDivisor by_H)
 {
     grid_dependency_wait();
     grid_launch_dependents();
     uint8_t* const kp = reinterpret_cast<uint8_t*>(a.key_pages);
     uint8_t* const vp = reinterpret_cast<uint8_t*>(a.value_pages);
-    const int64_t rows = int64_t(a.B) * a.H_kv * a.L_new;
+    const int rows = a.B * a.H_kv * a.L_new;
     const int c = threadIdx.x & 15;
-    const int64_t step = int64_t(gridDim.x) * (blockDim.x >> 4);
-    const int64_t first = int64_t(blockIdx.x) * (blockDim.x >> 4) + (threadIdx.x >> 4);
+    const int shift = __ffs(a.ps) - 1;
     // whole warps stay in the loop: the extremes are found by shuffles
-    const int64_t rounds = (rows + step - 1) / step;
-    for (int64_t k = 0; k < rounds; ++k) {
-        const int64_t r = first + k * step;
+    for (int r0 = int(blockIdx.x) * 16; r0 < rows; r0 += int(gridDim.x) * 16) {
+        const int r = r0 + int(threadIdx.x >> 4);
         const bool live = r < rows;
         uint4 kx = make_uint4(0, 0, 0, 0), vx = kx;
         int64_t dst = -1;
         if (live) {
-            kx = *reinterpret_cast<const uint4*>(a.key + r * 128 + c * 8);
-            vx = *reinterpret_cast<const uint4*>(a.value + r * 128 + c * 8);
-            const int64_t bh = udiv64(r, a.L_new);
-            const int i = int(r - bh * a.L_new);
-            const int b = int(udiv64(bh, a.H_kv));
-            const int h = int(bh - int64_t(b) * a.H_kv);
-            const int64_t slot = a.slot_mapping[int64_t(b) * a.L_new + i];
+            kx = *reinterpret_cast<const uint4*>(a.key + int64_t(r) * 128 + c * 8);
+            vx = *reinterpret_cast<const uint4*>(a.value + int64_t(r) * 128 + c * 8);
+            const int bh = by_L.of(r), b = by_H.of(bh), h = bh - b * a.H_kv;
+            const int slot = a.slot_mapping[b * a.L_new + (r - bh * a.L_new)];
             if (slot >= 0) {
-                const int64_t page = udiv64(slot, a.ps);
+                const int page = slot >> shift;
                 if (page < a.num_pages)
-                    dst = ((page * a.H_kv + h) * a.ps + (slot - page * a.ps)) * kQ4RowBytes;
+                    dst = ((int64_t(page) * a.H_kv + h) * a.ps + (slot & (a.ps - 1))) * kQ4RowBytes;
                 else if (c == 0 && h == 0)
                     atomicOr(a.err, PA_DEVERR_SLOT_BIT);
             }
@@ -145,16 +157,20 @@ __device__ __forceinline__ uint4 values8(uint32_t codes, uint32_t params)
     const float m = __half2float(__ushort_as_half(uint16_t(params >> 16)));
     uint32_t w[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-        w[i] = pack_bf16x2(fmaf(float((codes >> (8 * i)) & 15u), s, m),
-                           fmaf(float((codes >> (8 * i + 4)) & 15u), s, m));
+    for (int i = 0; i < 4; ++i) {                        // 2^23 + c, c, m + s c
+        const float2 c = __fadd2_rn(make_float2(__uint_as_float(((codes >> (8 * i)) & 15u) | 0x4b000000u),
+                                                __uint_as_float(((codes >> (8 * i + 4)) & 15u) | 0x4b000000u)),
+                                    make_float2(-8388608.f, -8388608.f));
+        const float2 v = __ffma2_rn(c, make_float2(s, s), make_float2(m, m));
+        w[i] = pack_bf16x2(v.x, v.y);
+    }
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 // One block per (request, KV head, kReadTokens tokens), 16 lanes a row (8 where D is
 // 64). bf16 pools (kQ4 false): rows as they are, for pages that the kernels above them
 // cannot read by TMA.
-constexpr int kReadTokens = 64;
+constexpr int kReadTokens = 128;
 
 template <bool kQ4, int D>
 __global__ void __launch_bounds__(256) read_pages_kernel(const PageReadArgs a)
@@ -163,42 +179,44 @@ __global__ void __launch_bounds__(256) read_pages_kernel(const PageReadArgs a)
     constexpr int kRowBytes = kQ4 ? kQ4RowBytes : 2 * D;
     grid_dependency_wait();
     grid_launch_dependents();
-    const int chunks = a.chunks;
-    const int64_t bh = udiv64(blockIdx.x, chunks);
-    const int t0 = int(blockIdx.x - bh * chunks) * kReadTokens;
-    const int b = int(udiv64(bh, a.H_kv));
-    const int h = int(bh - int64_t(b) * a.H_kv);
+    const int bh = a.by_chunks.of(int(blockIdx.x));
+    const int first = (int(blockIdx.x) - bh * a.chunks) * kReadTokens;
+    const int b = a.by_H.of(bh), h = bh - b * a.H_kv;
     const int cap = int(min(int64_t(a.max_pages) * a.ps, int64_t(a.max_len)));
     int n = a.context_lens[b];
     if (n < 0 || n > cap) {
-        if (h == 0 && t0 == 0 && threadIdx.x == 0)
+        if (h == 0 && first == 0 && threadIdx.x == 0)
             atomicOr(a.err, PA_DEVERR_CONTEXT_LEN_BIT);
         n = n < 0 ? 0 : cap;
     }
-    if (a.table_out && h == 0 && threadIdx.x == 0 && t0 % kQ4CopyRows == 0)
-        a.table_out[int64_t(b) * a.copy_pages + t0 / kQ4CopyRows] = int32_t(b * a.copy_pages + t0 / kQ4CopyRows);
-    if (t0 >= n)
+    if (a.table_out && h == 0 && threadIdx.x == 0)
+        a.table_out[int64_t(b) * a.copy_pages + first / kQ4CopyRows] = b * a.copy_pages + first / kQ4CopyRows;
+    static_assert(kReadTokens == kQ4CopyRows, "a block writes one page of a copy");
+    if (first >= n)
         return;
     const int32_t* bt = a.block_table + int64_t(b) * a.max_pages;
+    const int shift = __ffs(a.ps) - 1;
     const int c = threadIdx.x % kLanes, row = threadIdx.x / kLanes;
     constexpr int kRounds = kReadTokens / kRowsAtOnce;
     uint4 kx[kRounds], vx[kRounds];         // 4-bit rows: x the codes, y the parameters
     bool live[kRounds];
+    int phys[kRounds];
 #pragma unroll
     for (int k = 0; k < kRounds; ++k) {
-        const int t = t0 + kRowsAtOnce * k + row;
+        const int t = first + kRowsAtOnce * k + row;
         live[k] = t < n;
+        phys[k] = live[k] ? __ldg(bt + (t >> shift)) : 0;
+    }
+#pragma unroll
+    for (int k = 0; k < kRounds; ++k) {
+        const int t = first + kRowsAtOnce * k + row;
         kx[k] = vx[k] = make_uint4(0, 0, 0, 0);
-        if (live[k]) {
-            const int lp = t / a.ps;
-            const int phys = bt[lp];
-            if (unsigned(phys) >= unsigned(a.num_pages)) {
-                if (c == 0 && h == 0)
-                    atomicOr(a.err, PA_DEVERR_PAGE_ID_BIT);
-                live[k] = a.table_out != nullptr;      // a copy's row: zeros; a dense row: left
-                continue;
-            }
-            const int64_t src = ((int64_t(phys) * a.H_kv + h) * a.ps + (t - lp * a.ps)) * kRowBytes;
+        if (unsigned(phys[k]) >= unsigned(a.num_pages)) {
+            if (c == 0 && h == 0)
+                atomicOr(a.err, PA_DEVERR_PAGE_ID_BIT);
+            live[k] = a.table_out != nullptr;            // a copy's row: zeros; a dense row: left
+        } else if (live[k]) {
+            const int64_t src = ((int64_t(phys[k]) * a.H_kv + h) * a.ps + (t & (a.ps - 1))) * kRowBytes;
             if constexpr (kQ4) {
                 kx[k].x = *reinterpret_cast<const uint32_t*>(a.key_pages + src + c * 4);
                 vx[k].x = *reinterpret_cast<const uint32_t*>(a.value_pages + src + c * 4);
@@ -210,15 +228,15 @@ __global__ void __launch_bounds__(256) read_pages_kernel(const PageReadArgs a)
             }
         }
     }
-    // rows from a pointer of their 128-token block: dense rows follow on, copy pages
-    // are apart by the other heads' pages
-    const int64_t base = int64_t(b) * a.batch_stride + int64_t(h) * a.head_stride + c * 8;
+    // (128-token blocks of dense rows follow on, copy pages are apart by the other heads'
+    // pages)
+    const int64_t base = int64_t(b) * a.batch_stride + int64_t(h) * a.head_stride +
+                         int64_t(first / kQ4CopyRows) * a.block_stride + c * 8;
 #pragma unroll
     for (int k = 0; k < kRounds; ++k) {
         if (!live[k])
             continue;
-        const int t = t0 + kRowsAtOnce * k + row;
-        const int64_t dst = base + int64_t(t / kQ4CopyRows) * a.block_stride + int64_t(t % kQ4CopyRows) * D;
+        const int64_t dst = base + (kRowsAtOnce * k + row) * D;
         *reinterpret_cast<uint4*>(a.key_out + dst) = kQ4 ? values8(kx[k].x, kx[k].y) : kx[k];
         *reinterpret_cast<uint4*>(a.value_out + dst) = kQ4 ? values8(vx[k].x, vx[k].y) : vx[k];
     }
@@ -243,13 +261,18 @@ cudaError_t launch_append_q4(const AppendArgs& a, cudaStream_t stream)
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, append_q4_kernel, a);
+    FixedDivisor by_L, by_H;
+    by_L.set(a.L_new);
+    by_H.set(a.H_kv);
+    return cudaLaunchKernelEx(&cfg, append_q4_kernel, a, by_L, by_H);
 }
 
 cudaError_t launch_read_pages(PageReadArgs a, int kind, int D, cudaStream_t stream)
 {
     a.chunks = int32_t((int64_t(a.max_len) + kReadTokens - 1) / kReadTokens);
     const int64_t blocks = int64_t(a.B) * a.H_kv * a.chunks;
+    a.by_chunks.set(a.chunks);
+    a.by_H.set(a.H_kv);
     if (blocks <= 0 || blocks >= (int64_t(1) << 31))
         return cudaErrorInvalidValue;
     cudaLaunchAttribute attr[1];
