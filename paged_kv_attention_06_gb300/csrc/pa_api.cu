@@ -2081,12 +2081,6 @@ pa_status run_decode_prefix(const void* query, const void* key_pages, const void
     const void *kp = key_pages, *vp = value_pages;
     pa_shape pool = shape;
     if (p.copies) {
-        pa_shape tables = shape;
-        tables.batch = num_prefixes;
-        tables.max_pages = prefix_pages;
-        if ((st = copy_pages(key_pages, value_pages, prefix_table, prefix_lens, page_size, tables, kind, p.P2,
-                             p.kv_bytes, p.table_off, dev, w, s)) != PA_OK)
-            return st;
         kp = w;
         vp = w + p.kv_bytes;
         a.prefix.table = reinterpret_cast<const int32_t*>(w + p.table_off);
@@ -2107,9 +2101,6 @@ pa_status run_decode_prefix(const void* query, const void* key_pages, const void
         ++a.ps_shift;
     a.by_R.set(a.R);
     a.by_L.set(a.L);
-    cudaError_t e = launch_prefix(kmap, vmap, a, D, kind, p.prefix_grid, dev->id, s);
-    if (e != cudaSuccess)
-        return e == cudaErrorNotSupported ? PA_ERR_UNSUPPORTED : PA_ERR_CUDA;
 
     DecodeArgs d = rows_args(query, block_table, context_lens, page_size, scale * k_scale, 1, out, shape, kind,
                              kSuffix, dev);
@@ -2122,6 +2113,20 @@ pa_status run_decode_prefix(const void* query, const void* key_pages, const void
         ((st = encode_pool_map(&skmap, key_pages, shape, page_size, kind == kE4m3Pool, d.box_rows)) != PA_OK ||
          (st = encode_pool_map(&svmap, value_pages, shape, page_size, kind == kE4m3Pool, d.box_rows)) != PA_OK))
         return st;
+    // From here on only a launch can fail.
+    const cudaError_t e = prepare_prefix(D, kind, dev->id);
+    if (e != cudaSuccess)
+        return e == cudaErrorNotSupported ? PA_ERR_UNSUPPORTED : PA_ERR_CUDA;
+    if (p.copies) {
+        pa_shape tables = shape;
+        tables.batch = num_prefixes;
+        tables.max_pages = prefix_pages;
+        if ((st = copy_pages(key_pages, value_pages, prefix_table, prefix_lens, page_size, tables, kind, p.P2,
+                             p.kv_bytes, p.table_off, dev, w, s)) != PA_OK)
+            return st;
+    }
+    if (launch_prefix(kmap, vmap, a, D, kind, p.prefix_grid, s) != cudaSuccess)
+        return PA_ERR_CUDA;
     const int grid = decode_rows_launch_grid(
         shape, kind, max_context_len > 0 ? rows_granules(shape, kind, max_context_len) : 0, dev->sm_count);
     if (launch_decode_rows(skmap, svmap, d, shape, kind, grid, w + p.rows_off, dev->id, s) != cudaSuccess)

@@ -973,8 +973,9 @@ __global__ void __launch_bounds__(kThreads, (Smem<D, KIND, NT>::kBlocksPerSM))
                     l[nt][rr] += __shfl_xor_sync(0xffffffffu, l[nt][rr], off);
         __syncthreads();                             // the piece before has read the slabs
         st.gather(reinterpret_cast<float*>(smem + Lay::kSlabs), warp, lane);
-        if (warp == 0 && !misc[0]) {
+        if (warp == 0 && (kMode == kSuffix || !misc[0])) {
             if constexpr (kMode == kSuffix) {
+                // (after a wait that ran out too: what follows finds its places by these notes)
                 st.template put_rows<KIND>(a.partials + (int64_t(sp.seg) + cta) * kSlot, rows, lane);
                 if (lane == 0) {
                     if (sp.seg_start >= p0.x)

@@ -309,8 +309,11 @@ size_t prefix_smem_bytes(int D, int kind, int count);
 // The workspace of the states of `items` items, and where (m, l) and the pieces behind
 // kPrefixMaxPieces start in it.
 size_t prefix_state_bytes(const pa_shape& s, int64_t items, int grid, size_t* ml_off, size_t* pieces_off);
+// What can fail before the launch: the limits of the device. cudaErrorNotSupported: a
+// build whose registers the kernel cannot split.
+cudaError_t prepare_prefix(int D, int kind, int device);
 cudaError_t launch_prefix(const CUtensorMap& key_map, const CUtensorMap& value_map, const PrefixKernelArgs& a,
-                          int D, int kind, int grid, int device, cudaStream_t stream);
+                          int D, int kind, int grid, cudaStream_t stream);
 cudaError_t launch_prefix_merge(PrefixMergeArgs a, int D, int sm_count, cudaStream_t stream);
 
 // Accumulation of attention weights: weight_pages[slot of j] = decay * old (0

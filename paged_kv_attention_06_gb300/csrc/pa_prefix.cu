@@ -1063,21 +1063,35 @@ size_t prefix_state_bytes(const pa_shape& s, int64_t items, int grid, size_t* ml
     return *pieces_off + (items > kMaxPieces ? size_t(items) * size_t(grid) * sizeof(Piece) : 0);
 }
 
-cudaError_t launch_prefix(const CUtensorMap& key_map, const CUtensorMap& value_map, const PrefixKernelArgs& a,
-                          int D, int kind, int grid, int device, cudaStream_t stream)
+namespace {
+
+using PrefixKernel = void (*)(CUtensorMap, CUtensorMap, PrefixKernelArgs);
+
+int prefix_instance(int D, int kind) { return kind == kE4m3Pool ? 2 : kind == kQ4Pool ? 3 : D == 64 ? 0 : 1; }
+
+PrefixKernel prefix_kernel_of(int which)
 {
-    using Kernel = void (*)(CUtensorMap, CUtensorMap, PrefixKernelArgs);
+    static const PrefixKernel kernels[4] = {prefix_kernel<64, kBf16Pool>, prefix_kernel<128, kBf16Pool>,
+                                            prefix_kernel<128, kE4m3Pool>, prefix_kernel<128, kQ4Pool>};
+    return kernels[which];
+}
+
+int prefix_threads(int kind)
+{
+    return kind == kBf16Pool ? Layout<128, kBf16Pool>::kThreads : Layout<128, kE4m3Pool>::kThreads;
+}
+
+}  // namespace
+
+cudaError_t prepare_prefix(int D, int kind, int device)
+{
     constexpr int kMaxDev = 64;
     static std::atomic<bool> raised[kMaxDev][4];
     static std::atomic<int> regs_ok[kMaxDev][4];
     if (device < 0 || device >= kMaxDev)
         return cudaErrorInvalidDevice;
-    const int which = kind == kE4m3Pool ? 2 : kind == kQ4Pool ? 3 : D == 64 ? 0 : 1;
-    static const Kernel kernels[4] = {prefix_kernel<64, kBf16Pool>, prefix_kernel<128, kBf16Pool>,
-                                      prefix_kernel<128, kE4m3Pool>, prefix_kernel<128, kQ4Pool>};
-    const Kernel kernel = kernels[which];
-    const void* fn = reinterpret_cast<const void*>(kernel);
-    const int threads = kind == kBf16Pool ? Layout<128, kBf16Pool>::kThreads : Layout<128, kE4m3Pool>::kThreads;
+    const int which = prefix_instance(D, kind), threads = prefix_threads(kind);
+    const void* fn = reinterpret_cast<const void*>(prefix_kernel_of(which));
     const int first = kind == kBf16Pool ? Layout<128, kBf16Pool>::kRegsFirst : Layout<128, kE4m3Pool>::kRegsFirst;
     const int most = kind == kBf16Pool ? Layout<128, kBf16Pool>::kRegsSoftmax : Layout<128, kE4m3Pool>::kRegsSoftmax;
     const int sum = kind == kBf16Pool ? Layout<128, kBf16Pool>::kRegsSum : Layout<128, kE4m3Pool>::kRegsSum;
@@ -1093,20 +1107,23 @@ cudaError_t launch_prefix(const CUtensorMap& key_map, const CUtensorMap& value_m
     }
     if (rk != 1)
         return cudaErrorNotSupported;
-    cudaError_t e = raise_smem_limit(fn, &raised[device][which]);
-    if (e != cudaSuccess)
-        return e;
+    return raise_smem_limit(fn, &raised[device][which]);
+}
+
+cudaError_t launch_prefix(const CUtensorMap& key_map, const CUtensorMap& value_map, const PrefixKernelArgs& a,
+                          int D, int kind, int grid, cudaStream_t stream)
+{
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(unsigned(grid));
-    cfg.blockDim = dim3(threads);
+    cfg.blockDim = dim3(prefix_threads(kind));
     cfg.dynamicSmemBytes = prefix_smem_bytes(D, kind, a.prefix.count);
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, key_map, value_map, a);
+    return cudaLaunchKernelEx(&cfg, prefix_kernel_of(prefix_instance(D, kind)), key_map, value_map, a);
 }
 
 cudaError_t launch_prefix_merge(PrefixMergeArgs a, int D, int sm_count, cudaStream_t stream)
