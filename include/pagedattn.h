@@ -645,8 +645,9 @@ pa_status pa_decode_q4(const void *query, const void *key_pages, const void *val
 
 /*
  * Prefill over 4-bit pools, as pa_prefill_fp8: the tokens that the requests have cached
- * are copied into bf16 pages of 128 tokens in the workspace (m + s c rounded to bf16),
- * and pa_attention's prefill kernels attend over the copies. max_context_len bounds
+ * are copied into pages of 128 tokens in the workspace (m + s c, of K rounded to bf16, of
+ * V and of the softmax's weights to f16), and pa_attention's prefill kernels attend over
+ * the copies. max_context_len bounds
  * context_lens; a longer entry records PA_DEVERR_CONTEXT_LEN and is cut to the next
  * multiple of 128. workspace: pa_prefill_q4_workspace_bytes bytes (0: invalid sizes),
  * 256-byte aligned, any contents; calls that share one must not overlap on the GPU.

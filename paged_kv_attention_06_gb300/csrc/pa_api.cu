@@ -314,6 +314,7 @@ cudaError_t run_split(const CUtensorMap& qmap, const CUtensorMap& kmap, const CU
     sa.out_scale = a.out_scale;
     sa.window = a.window;
     sa.sinks = a.sinks;
+    sa.f16_values = a.f16_values;
     // An error the caller left pending is not ours to clear: note it, so
     // that only a refused cooperative launch of this call is cleared.
     const bool pending = cudaPeekAtLastError() != cudaSuccess;
@@ -336,7 +337,7 @@ pa_status run_prefill_tc(const void* query, const void* key_pages, const void* v
                          int32_t page_size, float scale, int causal, void* out,
                          const pa_shape& s, cudaStream_t stream, void* workspace = nullptr,
                          size_t workspace_bytes = 0, float out_scale = 1.f,
-                         void* piece_ws = nullptr, size_t piece_ws_bytes = 0)
+                         void* piece_ws = nullptr, size_t piece_ws_bytes = 0, bool f16_values = false)
 {
     DeviceInfo* dev;
     pa_status st = device_info(&dev);
@@ -404,6 +405,7 @@ pa_status run_prefill_tc(const void* query, const void* key_pages, const void* v
     a.causal = causal ? 1 : 0;
     a.out_scale = out_scale;
     a.D = s.head_dim;
+    a.f16_values = f16_values ? 1 : 0;
     a.key_pages = static_cast<const uint16_t*>(key_pages);
     a.value_pages = static_cast<const uint16_t*>(value_pages);
     a.piece_last = t_prefill_variant == 5 ? 1 : 0;
@@ -1773,7 +1775,8 @@ pa_status pa_gather_kv_q4(const void* key_pages, const void* value_pages,
 namespace {
 
 // bf16 copies, in pages of 128 tokens, of what `s.batch` tables lead to: K and V (kv_bytes
-// each), then the copies' table (P2 entries each) table_off bytes into w.
+// each; V of 4-bit pools in f16), then the copies' table (P2 entries each) table_off bytes
+// into w.
 pa_status copy_pages(const void* key_pages, const void* value_pages, const int32_t* block_table,
                      const int32_t* context_lens, int32_t page_size, const pa_shape& s, int kind,
                      int64_t P2, size_t kv_bytes, size_t table_off, const DeviceInfo* dev, uint8_t* w,
@@ -1788,6 +1791,7 @@ pa_status copy_pages(const void* key_pages, const void* value_pages, const int32
     a.batch_stride = a.block_stride * P2;
     a.max_len = int32_t(P2 * kQ4CopyRows);
     a.copy_pages = int32_t(P2);
+    a.f16_values = kind == kQ4Pool;
     return launch_read_pages(a, kind, s.head_dim, stream) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
@@ -1920,13 +1924,13 @@ pa_status pa_prefill_q4(const void* query, const void* key_pages, const void* va
     return run_prefill_tc(query, w, w + p.kv_bytes, reinterpret_cast<int32_t*>(w + p.table_off),
                           context_lens, 128, scale, causal, out, p.copy, s,
                           p.split_bytes ? w + p.split_off : nullptr, p.split_bytes, 1.f,
-                          p.piece_bytes ? w + p.split_off : nullptr, p.piece_bytes);
+                          p.piece_bytes ? w + p.split_off : nullptr, p.piece_bytes, true);
 }
 
 namespace {
 
 // Route of pa_attention_q4: the few-row kernel reads K and V once per 16 rows of a
-// (request, KV head), the prefill copies them to bf16 first.
+// (request, KV head), the prefill copies them first.
 int32_t route_q4(const pa_shape& shape) { return shape.q_len <= 0 ? -1 : shape.q_len <= 8 ? 0 : 1; }
 
 }  // namespace

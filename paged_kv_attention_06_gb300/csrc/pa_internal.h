@@ -150,6 +150,7 @@ struct PageReadArgs {
     int32_t B, H_kv, ps, num_pages, max_pages;
     int32_t max_len;              // rows a request has room for
     int32_t copy_pages;
+    int32_t f16_values;           // the values leave as f16 (4-bit rows; else bf16)
     int32_t chunks;               // set by the launcher, like the divisors
     FixedDivisor by_chunks, by_H;
 };
@@ -365,6 +366,7 @@ struct PrefillArgs {
     // Pairs kernel: a sliding window of `window` keys (0: none; causal) and the
     // first `sinks` keys.
     int32_t window, sinks;
+    int32_t f16_values;           // V holds f16 (head_dim 128, pages of 8 tokens or more, no window)
 };
 
 // Prefill over e4m3 pools: bf16 copies of the K/V tokens that some row sees, in
@@ -421,6 +423,7 @@ struct SplitPrefillArgs {
     int32_t causal;
     float out_scale;    // the output is out_scale * softmax . V (e4m3 copies: v_scale)
     int32_t window, sinks;   // window > 0: a sliding window, first keys that stay visible
+    int32_t f16_values;      // V holds f16 (no window)
 };
 
 size_t prefill_split_smem_bytes();

@@ -81,6 +81,8 @@ __device__ __forceinline__ uint64_t mnmajor_base(uint32_t saddr)
     return smem_desc_sw128(saddr, uint32_t(Layout::kHalf), 1024u);
 }
 
+// kF16: V holds f16 (copies of 4-bit rows) and P is written in f16.
+template <bool kF16>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_kernel(const __grid_constant__ CUtensorMap q_map,
                    const __grid_constant__ CUtensorMap key_map,
@@ -245,7 +247,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ===================== MMA issue (one thread) ======================
         if (lane == 0) {
             const uint32_t idesc_s = idesc_bf16_f32(kTile, kTile, 0);
-            const uint32_t idesc_pv = idesc_bf16_f32(kTile, 128, 1);
+            const uint32_t idesc_pv = kF16 ? idesc_f16_f32(kTile, 128, 1) : idesc_bf16_f32(kTile, 128, 1);
             // Base descriptors built once; every k-step is one add.
             const uint64_t dq = kmajor_base(sQ);
             const uint64_t dk0 = kmajor_base(sK), dk1 = desc_advance(dk0, Layout::kMat);
@@ -351,7 +353,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const float p0 = fast_exp2(fmaf(s[2 * k], c, -mu));
                 const float p1 = fast_exp2(fmaf(s[2 * k + 1], c, -mu));
                 l += p0 + p1;
-                pk[k] = pack_bf16x2(p0, p1);
+                pk[k] = pack_p<kF16>(p0, p1);
             }
             // P buffer and O are free once the previous P V has completed.
             if (j >= 1)
@@ -443,16 +445,16 @@ cudaError_t launch_prefill(const CUtensorMap& q_map, const CUtensorMap& key_map,
                            cudaStream_t stream)
 {
     constexpr int kMaxDev = 64;
-    static std::atomic<int> smem_set[kMaxDev];
+    static std::atomic<int> smem_set[kMaxDev][2];
     if (device < 0 || device >= kMaxDev)
         return cudaErrorInvalidDevice;
-    const int smem = Layout::kBytes;
-    if (smem_set[device].load(std::memory_order_relaxed) < smem) {
-        cudaError_t e = cudaFuncSetAttribute(prefill_kernel,
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    const int smem = Layout::kBytes, which = a.f16_values ? 1 : 0;
+    const auto kernel = a.f16_values ? prefill_kernel<true> : prefill_kernel<false>;
+    if (smem_set[device][which].load(std::memory_order_relaxed) < smem) {
+        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess)
             return e;
-        smem_set[device].store(smem, std::memory_order_relaxed);
+        smem_set[device][which].store(smem, std::memory_order_relaxed);
     }
     const int64_t grid = int64_t(a.B) * a.H_q * a.n_qtiles;
     // Programmatic stream serialization: the blocks may be scheduled while the
@@ -468,7 +470,7 @@ cudaError_t launch_prefill(const CUtensorMap& q_map, const CUtensorMap& key_map,
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, prefill_kernel, q_map, key_map, value_map, a);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, q_map, key_map, value_map, a);
     return e;
 }
 

@@ -378,7 +378,9 @@ __device__ __forceinline__ void piece_arrive_receiver(const uint4* state, const 
 // context zero-filled). Each loader warp waits for its own copies of a stage
 // once it has issued the next stage's, fences them to the tensor cores'
 // proxy and then arrives.
-template <bool kOdd, int kD, bool kPieces, bool kSmall, bool kWin = false>
+//
+// kF16: V holds f16 (copies of 4-bit rows) and P is written in f16.
+template <bool kOdd, int kD, bool kPieces, bool kSmall, bool kWin = false, bool kF16 = false>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_pairs_kernel(const __grid_constant__ CUtensorMap q_map,
                          const __grid_constant__ CUtensorMap key_map,
@@ -789,7 +791,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // (the next K and V tiles) are taken after the commits of a tile.
             const bool leader = elect_one();
             const uint32_t idesc_s = idesc_bf16_f32(kRows, kKeys, 0);
-            const uint32_t idesc_pv = idesc_bf16_f32(kRows, kD, 1);
+            const uint32_t idesc_pv = kF16 ? idesc_f16_f32(kRows, kD, 1) : idesc_bf16_f32(kRows, kD, 1);
             // Base descriptors built once; every k-step is one add.
             const uint64_t dq0 = kmajor_base(sQ), dq1 = desc_advance(dq0, Layout::kMat);
             const uint64_t dk0 = kmajor_base(sK), dk1 = desc_advance(dk0, Layout::kMat);
@@ -1017,7 +1019,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const float2 x = __ffma2_rn(make_float2(s[64 * hf + 2 * k], s[64 * hf + 2 * k + 1]), c2, nmu2);
                         const float2 pp = make_float2(fast_exp2(x.x), fast_exp2(x.y));
                         lsum[k & 3] = __fadd2_rn(lsum[k & 3], pp);
-                        pk[k] = pack_bf16x2(pp.x, pp.y);
+                        pk[k] = pack_p<kF16>(pp.x, pp.y);
                     }
                     tmem_st32(ts + kPCol + 32u * hf, pk);
                 };
@@ -1292,7 +1294,7 @@ namespace {
 
 // Register split and shared-memory limit checked once per device and
 // instantiation, then the launch.
-template <bool kOdd, int kD, bool kPieces, bool kSmall, bool kWin = false>
+template <bool kOdd, int kD, bool kPieces, bool kSmall, bool kWin = false, bool kF16 = false>
 cudaError_t launch_pairs(const cudaLaunchConfig_t& cfg_in, const CUtensorMap& q_map,
                          const CUtensorMap& key_map, const CUtensorMap& value_map,
                          const CUtensorMap& out_map, const PrefillArgs& a, int device)
@@ -1302,7 +1304,7 @@ cudaError_t launch_pairs(const cudaLaunchConfig_t& cfg_in, const CUtensorMap& q_
     static std::atomic<int> regs_ok[kMaxDev];
     if (device < 0 || device >= kMaxDev)
         return cudaErrorInvalidDevice;
-    const void* fn = reinterpret_cast<const void*>(prefill_pairs_kernel<kOdd, kD, kPieces, kSmall, kWin>);
+    const void* fn = reinterpret_cast<const void*>(prefill_pairs_kernel<kOdd, kD, kPieces, kSmall, kWin, kF16>);
     const int smem = Layout<kD>::kBytes;
     // The register split needs 128 x kRegsProducer + 256 x kRegsSoftmax
     // registers out of the launch's own 384 x numRegs, a launch count no
@@ -1329,8 +1331,8 @@ cudaError_t launch_pairs(const cudaLaunchConfig_t& cfg_in, const CUtensorMap& q_
     }
     cudaLaunchConfig_t cfg = cfg_in;
     cfg.dynamicSmemBytes = size_t(smem);
-    return cudaLaunchKernelEx(&cfg, prefill_pairs_kernel<kOdd, kD, kPieces, kSmall, kWin>, q_map, key_map, value_map,
-                              out_map, a);
+    return cudaLaunchKernelEx(&cfg, prefill_pairs_kernel<kOdd, kD, kPieces, kSmall, kWin, kF16>, q_map, key_map,
+                              value_map, out_map, a);
 }
 
 }  // namespace
@@ -1372,8 +1374,17 @@ cudaError_t launch_prefill_pairs(const CUtensorMap& q_map, const CUtensorMap& ke
     const bool odd = a.G % 2 != 0;
     const bool small = a.ps < 8;
     auto launch = [&]() {
+        auto go = [&](auto fn) { return fn(cfg, q_map, key_map, value_map, out_map, a, device); };
+        if (a.f16_values) {
+            if (small || a.D != 128 || a.window > 0)
+                return cudaErrorInvalidValue;
+            if (a.state != nullptr)
+                return odd ? go(launch_pairs<true, 128, true, false, false, true>)
+                           : go(launch_pairs<false, 128, true, false, false, true>);
+            return odd ? go(launch_pairs<true, 128, false, false, false, true>)
+                       : go(launch_pairs<false, 128, false, false, false, true>);
+        }
         if (a.window > 0) {
-            auto go = [&](auto fn) { return fn(cfg, q_map, key_map, value_map, out_map, a, device); };
             if (small)
                 return a.D == 64 ? (odd ? go(launch_pairs<true, 64, false, true, true>) : go(launch_pairs<false, 64, false, true, true>))
                                  : (odd ? go(launch_pairs<true, 128, false, true, true>) : go(launch_pairs<false, 128, false, true, true>));

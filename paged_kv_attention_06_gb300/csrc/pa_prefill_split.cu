@@ -277,7 +277,8 @@ __device__ __forceinline__ int block_of_unit(int64_t x, int64_t U, int64_t G)
 // first only), a separate instantiation so that even groups keep their code.
 // kWin: a sliding window; an item's tiles are those of its runs of keys laid end
 // to end (WindowSpan), and `place` is a key's number among them.
-template <bool kOdd, bool kWin>
+// kF16: V holds f16 (copies of 4-bit rows) and P is written in f16.
+template <bool kOdd, bool kWin, bool kF16 = false>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_split_kernel(const __grid_constant__ CUtensorMap q_map,
                          const __grid_constant__ CUtensorMap key_map,
@@ -534,7 +535,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // ===================== MMA issue (one elected thread) ==============
             const bool leader = elect_one();
             const uint32_t idesc_s = idesc_bf16_f32(kRows, kKeys, 0);
-            const uint32_t idesc_pv = idesc_bf16_f32(kRows, 128, 1);
+            const uint32_t idesc_pv = kF16 ? idesc_f16_f32(kRows, 128, 1) : idesc_bf16_f32(kRows, 128, 1);
             const uint64_t dq0 = kmajor_base(sQ), dq1 = desc_advance(dq0, Layout::kMat);
             const uint64_t dk0 = kmajor_base(sK), dk1 = desc_advance(dk0, Layout::kMat);
             const uint64_t dv0 = mnmajor_base(sV), dv1 = desc_advance(dv0, Layout::kMat);
@@ -806,7 +807,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             __ffma2_rn(make_float2(sc[64 * hf + 2 * kq], sc[64 * hf + 2 * kq + 1]), cc, nmu2);
                         const float2 pp = make_float2(fast_exp2(x.x), fast_exp2(x.y));
                         lsum[kq & 3] = __fadd2_rn(lsum[kq & 3], pp);
-                        pk[kq] = pack_bf16x2(pp.x, pp.y);
+                        pk[kq] = pack_p<kF16>(pp.x, pp.y);
                     }
                     tmem_st32(ts + kPCol + 32u * hf, pk);
                 };
@@ -1088,15 +1089,18 @@ cudaError_t launch_prefill_split(const CUtensorMap& q_map, const CUtensorMap& ke
                                  void* workspace, int device, cudaStream_t stream)
 {
     constexpr int kMaxDev = 64;
-    static std::atomic<int> smem_set[kMaxDev][4];
-    static std::atomic<int> regs_ok[kMaxDev][4];
+    static std::atomic<int> smem_set[kMaxDev][6];
+    static std::atomic<int> regs_ok[kMaxDev][6];
     if (device < 0 || device >= kMaxDev)
         return cudaErrorInvalidDevice;
     const bool odd = a.G % 2 != 0;
-    const int which = (odd ? 1 : 0) + (a.window > 0 ? 2 : 0);
+    if (a.f16_values && a.window > 0)
+        return cudaErrorInvalidValue;
+    const int which = (odd ? 1 : 0) + (a.f16_values ? 4 : a.window > 0 ? 2 : 0);
     using Kernel = void (*)(const CUtensorMap, const CUtensorMap, const CUtensorMap, const SplitPrefillArgs);
-    static const Kernel kernels[4] = {prefill_split_kernel<false, false>, prefill_split_kernel<true, false>,
-                                      prefill_split_kernel<false, true>, prefill_split_kernel<true, true>};
+    static const Kernel kernels[6] = {prefill_split_kernel<false, false>, prefill_split_kernel<true, false>,
+                                      prefill_split_kernel<false, true>, prefill_split_kernel<true, true>,
+                                      prefill_split_kernel<false, false, true>, prefill_split_kernel<true, false, true>};
     const Kernel kernel = kernels[which];
     const void* fn = reinterpret_cast<const void*>(kernel);
     int rk = regs_ok[device][which].load(std::memory_order_relaxed);

@@ -150,7 +150,8 @@ __global__ void __launch_bounds__(256) append_q4_kernel(const AppendArgs a, cons
     }
 }
 
-// 8 codes and their group's params -> 8 bf16.
+// 8 codes and their group's params -> 8 bf16 or f16.
+template <bool kF16>
 __device__ __forceinline__ uint4 values8(uint32_t codes, uint32_t params)
 {
     const float s = __half2float(__ushort_as_half(uint16_t(params & 0xffffu)));
@@ -162,17 +163,18 @@ __device__ __forceinline__ uint4 values8(uint32_t codes, uint32_t params)
                                                 __uint_as_float(((codes >> (8 * i + 4)) & 15u) | 0x4b000000u)),
                                     make_float2(-8388608.f, -8388608.f));
         const float2 v = __ffma2_rn(c, make_float2(s, s), make_float2(m, m));
-        w[i] = pack_bf16x2(v.x, v.y);
+        w[i] = kF16 ? pack_f16x2(v.x, v.y) : pack_bf16x2(v.x, v.y);
     }
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 // One block per (request, KV head, kReadTokens tokens), 16 lanes a row (8 where D is
 // 64). bf16 pools (kQ4 false): rows as they are, for pages that the kernels above them
-// cannot read by TMA.
+// cannot read by TMA. kF16: the values in f16, whose step is an eighth of bf16's (all
+// that a row can hold lies within f16's range).
 constexpr int kReadTokens = 128;
 
-template <bool kQ4, int D>
+template <bool kQ4, int D, bool kF16 = false>
 __global__ void __launch_bounds__(256) read_pages_kernel(const PageReadArgs a)
 {
     constexpr int kLanes = D / 8, kRowsAtOnce = 256 / kLanes;
@@ -237,8 +239,8 @@ __global__ void __launch_bounds__(256) read_pages_kernel(const PageReadArgs a)
         if (!live[k])
             continue;
         const int64_t dst = base + (kRowsAtOnce * k + row) * D;
-        *reinterpret_cast<uint4*>(a.key_out + dst) = kQ4 ? values8(kx[k].x, kx[k].y) : kx[k];
-        *reinterpret_cast<uint4*>(a.value_out + dst) = kQ4 ? values8(vx[k].x, vx[k].y) : vx[k];
+        *reinterpret_cast<uint4*>(a.key_out + dst) = kQ4 ? values8<false>(kx[k].x, kx[k].y) : kx[k];
+        *reinterpret_cast<uint4*>(a.value_out + dst) = kQ4 ? values8<kF16>(vx[k].x, vx[k].y) : vx[k];
     }
 }
 
@@ -285,7 +287,8 @@ cudaError_t launch_read_pages(PageReadArgs a, int kind, int D, cudaStream_t stre
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg,
-                              kind == kQ4Pool ? read_pages_kernel<true, 128>
+                              kind == kQ4Pool ? (a.f16_values ? read_pages_kernel<true, 128, true>
+                                                              : read_pages_kernel<true, 128>)
                               : D == 64       ? read_pages_kernel<false, 64>
                                               : read_pages_kernel<false, 128>,
                               a);

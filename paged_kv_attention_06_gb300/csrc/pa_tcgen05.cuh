@@ -81,6 +81,14 @@ __host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, int b_mn_majo
     return idesc_bf16_f32(M, N, b_mn_major) & ~((1u << 7) | (1u << 10));
 }
 
+// P of softmax . V, two columns of a row: in f16 where V is (both operands of a product
+// have one type), else bf16. (P is at most 2^8, which f16 holds with three bits more.)
+template <bool kF16>
+__device__ __forceinline__ uint32_t pack_p(float lo, float hi)
+{
+    return kF16 ? pack_f16x2(lo, hi) : pack_bf16x2(lo, hi);
+}
+
 // D[tmem] (+)= A[smem] * B[smem]^T, issued by one thread. (Either type: the descriptor says.)
 __device__ __forceinline__ void tc_mma_bf16(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
                                             uint32_t idesc, uint32_t accumulate)
