@@ -669,7 +669,7 @@ pa_status run_split_kv(const void* query, const void* key_pages, const void* val
             return st;
         while ((1 << a.ps_shift) < page_size)
             ++a.ps_shift;
-        const int rows_grid = decode_rows_launch_grid(s, kind, max_context_len > 0 ? granules : 0, dev->sm_count);
+        const int rows_grid = decode_rows_launch_grid(s, kind, extra.mode, max_context_len > 0 ? granules : 0, dev->sm_count);
         return launch_decode_rows(kmap, vmap, a, s, kind, rows_grid, workspace, dev->id, stream) == cudaSuccess
                    ? PA_OK
                    : PA_ERR_CUDA;
@@ -1883,7 +1883,7 @@ pa_status pa_decode_q4(const void* query, const void* key_pages, const void* val
     a.key_rows = static_cast<const uint8_t*>(key_pages);
     a.value_rows = static_cast<const uint8_t*>(value_pages);
     const int grid = decode_rows_launch_grid(
-        shape, kQ4Pool, max_context_len > 0 ? rows_granules(shape, kQ4Pool, max_context_len) : 0, dev->sm_count);
+        shape, kQ4Pool, kFull, max_context_len > 0 ? rows_granules(shape, kQ4Pool, max_context_len) : 0, dev->sm_count);
     const CUtensorMap none = {};
     return launch_decode_rows(none, none, a, shape, kQ4Pool, grid, workspace, dev->id,
                               static_cast<cudaStream_t>(stream)) == cudaSuccess
@@ -2008,10 +2008,10 @@ pa_status plan_prefix(const pa_shape& s, int32_t page_size, int kind, int32_t co
     const size_t states = prefix_state_bytes(s, items, p->prefix_grid, &ml, &pieces);
     p->ml_off = p->state_off + ml;
     p->pieces_off = p->state_off + pieces;
-    // notes for the merge: an int4 a request, an int2 an item and a segment
+    // notes for the merge: an int4 a row, an int2 a segment
     const int64_t segments = int64_t(s.batch) * s.num_kv_heads * ((R + kSegmentRows - 1) / kSegmentRows);
     p->note_off = (p->state_off + states + 255) & ~size_t(255);
-    p->rows_off = (p->note_off + size_t(s.batch) * 16 + size_t(items + segments) * 8 + 255) & ~size_t(255);
+    p->rows_off = (p->note_off + size_t(s.batch * R) * s.num_kv_heads * 16 + size_t(segments) * 8 + 255) & ~size_t(255);
     p->total = p->rows_off + decode_rows_workspace_bytes(s, kind, kSuffix, dev->sm_count);
     return PA_OK;
 }
@@ -2061,8 +2061,7 @@ pa_status run_decode_prefix(const void* query, const void* key_pages, const void
     a.state_ml = reinterpret_cast<float2*>(w + p.ml_off);
     a.more_pieces = w + p.pieces_off;
     a.most_items = p.items;
-    a.note_request = reinterpret_cast<int4*>(w + p.note_off);
-    a.note_item = reinterpret_cast<int2*>(a.note_request + shape.batch);
+    a.note_row = reinterpret_cast<int4*>(w + p.note_off);
     a.err = dev->err;
     a.prefix.table = prefix_table;
     a.prefix.lens = prefix_lens;
@@ -2105,13 +2104,14 @@ pa_status run_decode_prefix(const void* query, const void* key_pages, const void
         ++a.ps_shift;
     a.by_R.set(a.R);
     a.by_L.set(a.L);
+    a.by_H.set(a.H_kv);
 
     DecodeArgs d = rows_args(query, block_table, context_lens, page_size, scale * k_scale, 1, out, shape, kind,
                              kSuffix, dev);
     d.key_rows = static_cast<const uint8_t*>(key_pages);
     d.value_rows = static_cast<const uint8_t*>(value_pages);
     d.prefix = own_table;
-    d.note_segment = a.note_item + p.items;
+    d.note_segment = reinterpret_cast<int2*>(a.note_row + int64_t(a.B) * a.H_kv * a.R);
     CUtensorMap skmap = {}, svmap = {};
     if (kind != kQ4Pool &&
         ((st = encode_pool_map(&skmap, key_pages, shape, page_size, kind == kE4m3Pool, d.box_rows)) != PA_OK ||
@@ -2132,7 +2132,7 @@ pa_status run_decode_prefix(const void* query, const void* key_pages, const void
     if (launch_prefix(kmap, vmap, a, D, kind, p.prefix_grid, s) != cudaSuccess)
         return PA_ERR_CUDA;
     const int grid = decode_rows_launch_grid(
-        shape, kind, max_context_len > 0 ? rows_granules(shape, kind, max_context_len) : 0, dev->sm_count);
+        shape, kind, kSuffix, max_context_len > 0 ? rows_granules(shape, kind, max_context_len) : 0, dev->sm_count);
     if (launch_decode_rows(skmap, svmap, d, shape, kind, grid, w + p.rows_off, dev->id, s) != cudaSuccess)
         return PA_ERR_CUDA;
 
@@ -2143,7 +2143,6 @@ pa_status run_decode_prefix(const void* query, const void* key_pages, const void
     m.out = static_cast<uint16_t*>(out);
     m.out_scale = v_scale;
     m.note_segment = d.note_segment;
-    m.by_H.set(shape.num_kv_heads);
     m.MS = (a.R + kSegmentRows - 1) / kSegmentRows;
     m.row_tiles = decode_rows_row_tiles(shape);
     return launch_prefix_merge(m, D, dev->sm_count, s) == cudaSuccess ? PA_OK : PA_ERR_CUDA;

@@ -36,9 +36,11 @@ struct Facts {
 template <int D, int KIND, int NT>
 Facts facts_of(int B, int mode)
 {
-    using Lay = Smem<D, KIND, NT>;
-    return {mode == kSuffix ? size_t(suffix_slot_floats(D, NT)) * 4 : size_t(Lay::kSlab), Lay::bytes(B, mode),
-            Lay::kBlocksPerSM};
+    using Suffix = Smem<D, KIND, NT, kSuffix>;
+    using Other = Smem<D, KIND, NT, kFull>;
+    if (mode == kSuffix)
+        return {size_t(suffix_slot_floats(D, NT)) * 4, Suffix::bytes(B), Suffix::kBlocksPerSM};
+    return {size_t(Other::kSlab), Other::bytes(B), Other::kBlocksPerSM};
 }
 Facts facts(int D, int kind, int NT, int B, int mode)
 {
@@ -71,9 +73,9 @@ bool decode_rows_fits(const pa_shape& s, int kind, int mode, int max_smem)
            rows::facts(s.head_dim, kind, rows::row_tiles(s), s.batch, mode).smem <= size_t(max_smem);
 }
 
-int decode_rows_grid(const pa_shape& s, int kind, int sm_count)
+int decode_rows_grid(const pa_shape& s, int kind, int mode, int sm_count)
 {
-    return sm_count * rows::facts(s.head_dim, kind, rows::row_tiles(s), 1, kFull).blocks_per_sm;
+    return sm_count * rows::facts(s.head_dim, kind, rows::row_tiles(s), 1, mode).blocks_per_sm;
 }
 
 int decode_rows_box(const pa_shape& s, int kind, int page_size)
@@ -85,7 +87,7 @@ int decode_rows_box(const pa_shape& s, int kind, int page_size)
 size_t decode_rows_workspace_bytes(const pa_shape& s, int kind, int mode, int sm_count)
 {
     const int64_t MS = (rows::rows_of(s) + kSegmentRows - 1) / kSegmentRows;
-    return (size_t(s.batch) * s.num_kv_heads * size_t(MS) + size_t(decode_rows_grid(s, kind, sm_count))) *
+    return (size_t(s.batch) * s.num_kv_heads * size_t(MS) + size_t(decode_rows_grid(s, kind, mode, sm_count))) *
            rows::facts(s.head_dim, kind, rows::row_tiles(s), 1, mode).slab;
 }
 
@@ -93,9 +95,9 @@ int decode_rows_tile(const pa_shape& s, int kind) { return kind == kBf16Pool && 
 
 int decode_rows_row_tiles(const pa_shape& s) { return rows::row_tiles(s); }
 
-int decode_rows_launch_grid(const pa_shape& s, int kind, int64_t granule_bound, int sm_count)
+int decode_rows_launch_grid(const pa_shape& s, int kind, int mode, int64_t granule_bound, int sm_count)
 {
-    int64_t grid = decode_rows_grid(s, kind, sm_count);
+    int64_t grid = decode_rows_grid(s, kind, mode, sm_count);
     // Few granules: two of them a block at least, so that a segment's pieces stay
     // few (one request, window 4096: 11.3 us, 14.0 with one; window 512: 8.4 and 8.2).
     if (granule_bound > 0 && granule_bound < 2 * grid)

@@ -58,7 +58,7 @@ constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr float kMoveLog2 = 8.f;      // scores may exceed the maximum in use by this much
 constexpr int kPieceUnits = 1;        // a piece's cost beyond its granules
-// Two blocks (Smem::kBlocksPerSM) of two tiles a warp. 64 e4m3 requests, window 2048: 49 us, with three
+// Two blocks an SM of two tiles a warp (Smem: not for 4-bit pools, nor behind a prefix). 64 e4m3 requests, window 2048: 49 us, with three
 // blocks 62, with four tiles a warp 75; 8 bf16 requests of 16k-32k: 142, 160 and
 // 189. (Presumably the second kernel's blocks and the next call's then find no
 // room until the last block of this one ends.)
@@ -71,28 +71,32 @@ struct Shape {
     static constexpr int kKLoads = kRowBytes / 64;    // 16-byte loads per lane and K row
     static constexpr int kVLoads = (kRowBytes + 127) / 128;   // and V row
     static constexpr int kSteps = D / 16;             // k-steps of S, 16-row tiles of O^T
-    static constexpr int kStages = KIND == kQ4Pool ? 1 : 2;   // tiles on their way per warp
     // K (or V) of one tile: [128-byte column block][key][128 bytes], or [key][80 bytes]
     static constexpr int kTileBytes = kTok * kRowBytes;
 };
 
-template <int D, int KIND, int NT>
+template <int D, int KIND, int NT, int kMode>
 struct Smem {
     using Sh = Shape<D, KIND>;
     // 4-bit rows, 32 requests of up to 4096 keys, 64 of up to 8192, 8 of 16k-32k (us): three
     // blocks and two tiles of 32 keys on their way 21.1, 48.3, 72.2, one 16.4, 47.0, 70.2;
     // two blocks and two tiles 17.5, 53.1, 79.7; four 23.4, 58.5, 76.0; three blocks and one
     // tile of 64 keys 18.3, 50.1, 67.5.
-    static constexpr int kBlocksPerSM = KIND == kQ4Pool && NT == 1 ? 3 : 2;
+    // Behind a prefix, whose kernel leaves the SMs one by one and whose merge follows: 8
+    // bf16 requests, 32 of them, 64 e4m3 requests with two blocks of two tiles 16.4, 37.6,
+    // 72.3; three of two 15.8, 38.2, 76.7; three of one 15.7, 36.8, 68.7; four of one 16.9,
+    // 39.4, 70.1; two of three 16.3, 38.3, 75.2.
+    static constexpr int kStages = KIND == kQ4Pool || (kMode == kSuffix && NT == 1) ? 1 : 2;  // tiles on their way
+    static constexpr int kBlocksPerSM = kStages == 1 && NT == 1 ? 3 : 2;
     static constexpr int kSlab = (D / 16 * NT * 4 + 4 * NT) * 32 * 4; // one warp's state: O^T, m, l
     static constexpr int kRing = 0;                                   // [warp][stage][K, V]
-    static constexpr int kSlabs = kRing + kWarps * Sh::kStages * 2 * Sh::kTileBytes;
+    static constexpr int kSlabs = kRing + kWarps * kStages * 2 * Sh::kTileBytes;
     static constexpr int kBars = kSlabs + 2 * kSlab;                  // [warp][stage][K, V]
-    static constexpr int kMisc = kBars + kWarps * Sh::kStages * 2 * 8;
+    static constexpr int kMisc = kBars + kWarps * kStages * 2 * 8;
     static constexpr int kPrefix = kMisc + 16;   // [B + 1] granules before, [B] granules, [B] lengths, kSuffix: [B] firsts
-    static size_t bytes(int B, int mode)
+    static size_t bytes(int B)
     {
-        return kPrefix + size_t((mode == kSuffix ? 4 : 3) * B + 1) * 4 + 1024;
+        return kPrefix + size_t((kMode == kSuffix ? 4 : 3) * B + 1) * 4 + 1024;
     }
 };
 
@@ -317,14 +321,14 @@ struct Q4Step {
 };
 
 template <int D, int KIND, int NT, int kMode>
-__global__ void __launch_bounds__(kThreads, (Smem<D, KIND, NT>::kBlocksPerSM))
+__global__ void __launch_bounds__(kThreads, (Smem<D, KIND, NT, kMode>::kBlocksPerSM))
     decode_rows_kernel(const __grid_constant__ CUtensorMap key_map,
                        const __grid_constant__ CUtensorMap value_map, const DecodeArgs a)
 {
     constexpr bool F8 = KIND == kE4m3Pool, Q4 = KIND == kQ4Pool, kP16 = F8 || Q4;
     using Sh = Shape<D, KIND>;
-    using Lay = Smem<D, KIND, NT>;
-    constexpr int kStages = Sh::kStages, kTileBytes = Sh::kTileBytes;
+    using Lay = Smem<D, KIND, NT, kMode>;
+    constexpr int kStages = Lay::kStages, kTileBytes = Sh::kTileBytes;
     constexpr int kTok = Sh::kTok, kSub = Sh::kSub, kKL = Sh::kKLoads, kVL = Sh::kVLoads, kKS = Sh::kSteps;
     // floats of a piece's state
     constexpr int kSlot = kMode == kSuffix ? suffix_slot_floats(D, NT) : Lay::kSlab / 4;

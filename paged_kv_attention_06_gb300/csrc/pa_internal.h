@@ -264,7 +264,7 @@ int decode_rows_box(const pa_shape& s, int kind, int page_size);
 size_t decode_rows_workspace_bytes(const pa_shape& s, int kind, int mode, int sm_count);
 int decode_rows_tile(const pa_shape& s, int kind);     // keys of a tile
 int decode_rows_row_tiles(const pa_shape& s);          // 8-row tiles of a segment
-int decode_rows_launch_grid(const pa_shape& s, int kind, int64_t granule_bound, int sm_count);
+int decode_rows_launch_grid(const pa_shape& s, int kind, int mode, int64_t granule_bound, int sm_count);
 cudaError_t launch_decode_rows(const CUtensorMap& key_map, const CUtensorMap& value_map, DecodeArgs a,
                                const pa_shape& s, int kind, int grid, void* workspace, int device,
                                cudaStream_t stream);
@@ -285,10 +285,9 @@ struct PrefixKernelArgs {
     const uint8_t* key_rows;      // e4m3 and 4-bit pools
     const uint8_t* value_rows;
     int32_t ps_shift;             // log2 of ps
-    FixedDivisor by_R, by_L;
-    int4* note_request;           // [B] first item (-1: none), its row 0 among them, items a KV
-                                  // head, 1: both halves of a state hold the rows
-    int2* note_item;              // [most_items] first and last block
+    FixedDivisor by_R, by_L, by_H;   // by_H: H_kv
+    int4* note_row;               // [B * H_kv * R] its first state in the prefix, states, place in
+                                  // them, 1: both halves of a state hold the rows
     void* more_pieces;            // [grid][most_items]
     int32_t most_items;
     float scale_log2;
@@ -299,7 +298,6 @@ struct PrefixMergeArgs {
     uint16_t* out;                // [B, H_q, L, D]
     float out_scale;
     const int2* note_segment;     // [B * H_kv * MS] first and last block
-    FixedDivisor by_H;            // H_kv
     int32_t MS, row_tiles;        // of the few-row kernel
     int32_t share;                // set by the launcher: warps a row
 };

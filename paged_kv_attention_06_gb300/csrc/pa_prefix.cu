@@ -143,6 +143,11 @@ struct Ranges {
         rem = U - per * G;
     }
     __device__ __forceinline__ int start(int c) const { return c * per + min(c, rem); }
+    __device__ __forceinline__ int of(int u) const       // the block whose range holds unit u
+    {
+        const int longer = rem * (per + 1);
+        return u < longer ? u / (per + 1) : rem + (u - longer) / per;
+    }
 };
 
 // The part of an item in a block's range of units.
@@ -297,7 +302,7 @@ __global__ void __launch_bounds__((Layout<D, KIND>::kThreads), 1)
     const Pieces pieces = {reinterpret_cast<Piece*>(smem + Lay::kPieces),
                            static_cast<Piece*>(a.more_pieces) + int64_t(blockIdx.x) * a.most_items};
     static_assert(sizeof(Piece) == 36, "as laid out");
-    __shared__ int piece_count;
+    __shared__ int piece_count, all_units;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         misc[0] = 0;
@@ -422,31 +427,43 @@ __global__ void __launch_bounds__((Layout<D, KIND>::kThreads), 1)
                 found += __shfl_sync(0xffffffffu, incl, 31);
             }
         }
-        if (lane == 0)
-            piece_count = bad ? -1 : found;
+        if (lane == 0) {
+            piece_count = found;
+            all_units = U;
+        }
     }
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    const int count = max(piece_count, 0);
-    // ---- notes for the merge: where a request's rows are among the items' (row 0 of
-    // the first one's KV head 0), and the blocks that hold each item's first and last tile
+    const int count = piece_count;
+    // ---- notes for the merge: where each row's states are
     if (warp == 3) {
         const Group* groups = reinterpret_cast<const Group*>(smem + Lay::kGroups);
-        for (int b = c * 32 + lane; b < a.B; b += int(gridDim.x) * 32) {
-            const int p = piece_count < 0 ? -1 : prefix_of(a.prefix, b);
-            int4 note = make_int4(-1, 0, 0, 0);
-            if (p >= 0 && groups[p].items > 0)
-                note = make_int4(groups[p].item, (b - groups[p].first) * a.R, (groups[p].rows + 255) / 256,
-                                 groups[p].rows > 128 ? 0 : 1);
-            a.note_request[b] = note;
-        }
-        for (int i = lane; i < count; i += 32) {
-            const Piece& pc = pieces[i];
-            if (pc.k0 == 0)
-                a.note_item[pc.item].x = c;
-            if (pc.k1 * kKeys >= pc.len)
-                a.note_item[pc.item].y = c;
+        const Ranges ranges(all_units, int(gridDim.x));
+        const int rows = a.B * a.H_kv * a.R;
+        for (int row = c * 32 + lane; row < rows; row += int(gridDim.x) * 32) {
+            const int bh = a.by_R.of(row), x = row - bh * a.R, b = a.by_H.of(bh), h = bh - b * a.H_kv;
+            int4 note = make_int4(0, 0, 0, 0);
+            if (all_units > 0 && b >= groups[0].first) {
+                int p = 0;                               // the last prefix that starts at b or before
+                for (int hi = a.prefix.count; hi - p > 1;) {
+                    const int mid = (p + hi) >> 1;
+                    if (groups[mid].first <= b)
+                        p = mid;
+                    else
+                        hi = mid;
+                }
+                const Group g = groups[p];
+                const int f = (b - g.first) * a.R + x;
+                if (f < g.rows && g.items > 0) {
+                    const int i = h * ((g.rows + 255) >> 8) + (f >> 8);
+                    const int u = g.us + i * g.item_units() + kItemUnits;
+                    const int from = ranges.of(u), to = ranges.of(u + (g.tiles() - 1) * kTileUnits);
+                    const int twice = g.rows > 128 ? 0 : 1;
+                    note = make_int4(g.item + i + from, (to - from + 1) << twice, f & 255, twice);
+                }
+            }
+            a.note_row[row] = note;
         }
     }
     if (count == 0) {
@@ -485,18 +502,28 @@ __global__ void __launch_bounds__((Layout<D, KIND>::kThreads), 1)
                 auto slot_free = [&](int slot) {
                     return mbar_wait_warp(&bar[kCodeEmpty + slot], ((u / kRing) & 1) ^ 1u, misc, a.err);
                 };
-                auto request = [&](const Tile& t, bool is_v) {
+                struct Pages {                           // of a tile's boxes 32 i + lane
+                    int id[kKeys / 32];
+                };
+                auto lookup = [&](const Tile& t) {
+                    Pages pages;
+                    const int first = t.k * kKeys;
+                    const Piece& pc = pieces[t.i];
+                    const int boxes = (min(kKeys, pc.len - first) + box - 1) >> box_shift;
+                    const int32_t* table = a.prefix.table + int64_t(pc.p) * a.prefix.pages;
+#pragma unroll
+                    for (int i = 0; i < kKeys / 32; ++i)
+                        pages.id[i] =
+                            32 * i + lane < boxes
+                                ? __ldg(table + ((first + ((32 * i + lane) << box_shift)) >> a.ps_shift)) : 0;
+                    return pages;
+                };
+                auto request = [&](const Tile& t, bool is_v, const Pages& pages) {
                     const int slot = u % kRing;
                     const int first = t.k * kKeys;
                     const Piece& pc = pieces[t.i];
                     const int live = min(kKeys, pc.len - first);
                     const int boxes = (live + box - 1) >> box_shift;
-                    const int32_t* table = a.prefix.table + int64_t(pc.p) * a.prefix.pages;
-                    int pages[kKeys / 32];
-#pragma unroll
-                    for (int i = 0; i < kKeys / 32; ++i)
-                        if (32 * i + lane < boxes)
-                            pages[i] = __ldg(table + ((first + ((32 * i + lane) << box_shift)) >> a.ps_shift));
                     const bool ok = slot_free(slot);
                     if (ok) {
                         if (lane == 0) {
@@ -508,11 +535,12 @@ __global__ void __launch_bounds__((Layout<D, KIND>::kThreads), 1)
                         for (int i = 0; i < kKeys / 32; ++i) {
                             const int at = (32 * i + lane) << box_shift;
                             if (32 * i + lane < boxes) {
-                                if (unsigned(pages[i]) >= unsigned(a.num_pages)) {
+                                int page = pages.id[i];
+                                if (unsigned(page) >= unsigned(a.num_pages)) {
                                     atomicOr(a.err, PA_DEVERR_PAGE_ID_BIT);
-                                    pages[i] = 0;
+                                    page = 0;
                                 }
-                                const uint32_t row = (uint32_t(pages[i] * a.H_kv + pc.h) << a.ps_shift) +
+                                const uint32_t row = (uint32_t(page * a.H_kv + pc.h) << a.ps_shift) +
                                                      (uint32_t(first + at) & ps_mask);
                                 bulk_load(smem + Lay::kCodeRing + slot * Lay::kCodeTile + at * Lay::kRowBytes,
                                           (is_v ? a.value_rows : a.key_rows) + uint64_t(row) * Lay::kRowBytes,
@@ -523,15 +551,23 @@ __global__ void __launch_bounds__((Layout<D, KIND>::kThreads), 1)
                     __syncwarp();
                     ++u;
                 };
-                request(kt, false);
+                // Pages are looked up a request ahead; V's are those that K had.
+                Pages next = lookup(kt), now = next, held = next;
+                auto request_k = [&]() {
+                    now = next;
+                    request(kt, false, now);
+                    pass(kt);
+                    if (kt.i < count)
+                        next = lookup(kt);
+                };
+                request_k();
+                held = now;
                 while (vt.i < count) {
-                    if (kt.i < count) {
-                        pass(kt);
-                        if (kt.i < count)
-                            request(kt, false);
-                    }
-                    request(vt, true);
+                    if (kt.i < count)
+                        request_k();
+                    request(vt, true, held);
                     pass(vt);
+                    held = now;
                 }
                 // The end, and no copy still landing: the converters have waited for each.
                 const int slot = u % kRing;
@@ -555,15 +591,24 @@ __global__ void __launch_bounds__((Layout<D, KIND>::kThreads), 1)
             if (lane == 0)
                 prefetch_tensormap(map);
             const int box = a.box_rows;                  // min(page size, 128), at least 8
-            int g = 0;
+            // (a tile's pages are looked up while the tile before is waited for)
+            auto page_at = [&](int i, int k) {
+                const int key0 = k * kKeys + lane * box;
+                return lane * box < kKeys && key0 < pieces[i].len
+                           ? __ldg(a.prefix.table + int64_t(pieces[i].p) * a.prefix.pages + (key0 >> a.ps_shift)) : 0;
+            };
+            int g = 0, next = page_at(0, pieces[0].k0);
             for (int i = 0; i < count; ++i) {
                 const int n = pieces[i].len, k1 = pieces[i].k1, head = pieces[i].h;
-                const int32_t* table = a.prefix.table + int64_t(pieces[i].p) * a.prefix.pages;
                 for (int k = pieces[i].k0; k < k1; ++k, ++g) {
                     const int key0 = k * kKeys;
                     const int boxes = (min(n, key0 + kKeys) - key0 + box - 1) / box;
                     const int tok = key0 + lane * box;
-                    int phys = lane < boxes ? __ldg(table + (tok >> a.ps_shift)) : 0;
+                    int phys = next;
+                    if (k + 1 < k1)
+                        next = page_at(i, k + 1);
+                    else if (i + 1 < count)
+                        next = page_at(i + 1, pieces[i + 1].k0);
                     const int st = g & 1;
                     const bool ok = mbar_wait_warp(&bar[empty + st], ((g >> 1) & 1) ^ 1u, misc, a.err);
                     if (ok) {
@@ -908,13 +953,17 @@ __global__ void __launch_bounds__((Layout<D, KIND>::kThreads), 1)
 
 // The last step joins the states that the prefix's pieces and the segment behind it left
 // for a row: by a.share warps of a block (a power of two), each some of the pieces. Where
-// they lie is read from what the two kernels before noted down: found again from the
-// call's tables, by every warp, it took 2 to 6 us (few of these blocks fit beside the
-// few-row kernel's, so it was not hidden before the wait).
-constexpr int kMergeWarps = 8, kMergeThreads = 32 * kMergeWarps;
+// they lie is read from what the two kernels before noted down, row by row: found again
+// from the call's tables, by every warp, it took 2 to 6 us (few of these blocks fit beside
+// the few-row kernel's, so it was not hidden before the wait). A chain of two reads: the
+// notes, then the states' (m, l) together with the first states.
+// kMergeWarpsPerSM bounds the warps a row gets. 32 bf16 requests behind 16384 keys, 64
+// e4m3 requests (us, whole calls), 40 warps: 34.0, 63.9; 24: 34.4, 67.7; 48: 35.8, 65.2;
+// 64 warps of fewer registers 43.9, 76.2.
+constexpr int kMergeWarps = 8, kMergeThreads = 32 * kMergeWarps, kMergeWarpsPerSM = 40;
 
 template <int D>
-__global__ void __launch_bounds__(kMergeThreads, 6) prefix_merge_kernel(const PrefixMergeArgs a)
+__global__ void __launch_bounds__(kMergeThreads, 4) prefix_merge_kernel(const PrefixMergeArgs a)
 {
     __shared__ float4 sums[kMergeWarps][32];
     __shared__ float2 row_ml[kMergeWarps];               // (max, sum) of each warp's pieces
@@ -924,25 +973,21 @@ __global__ void __launch_bounds__(kMergeThreads, 6) prefix_merge_kernel(const Pr
     const int row = (int(blockIdx.x) * kMergeWarps + warp) / share;   // of [B, H_kv, R]
     const bool live = row < k.B * k.H_kv * k.R;
     const int bh = live ? k.by_R.of(row) : 0, x = live ? row - bh * k.R : 0;
-    const int b = a.by_H.of(bh), h = bh - b * k.H_kv;
-    int np = 0, ns = 0, twice = 0;                       // pieces of the prefix, of the segment
+    const int b = k.by_H.of(bh), h = bh - b * k.H_kv;
+    int np = 0, ns = 0, twice = 0;                       // states of the prefix, of the segment
     int64_t p_row = 0;                                   // the row's in the prefix's first state
     const int slot = suffix_slot_floats(D, a.row_tiles);
     const int xr = x % kSegmentRows;
-    const int seg = (b * k.H_kv + h) * a.MS + x / kSegmentRows;
+    const int seg = bh * a.MS + x / kSegmentRows;
     const float* s_at = a.suffix_state;
     grid_dependency_wait();
     grid_launch_dependents();
     if (live) {
-        const int4 note = __ldcg(k.note_request + b);
+        const int4 note = __ldcg(k.note_row + row);
         const int2 blocks = __ldcg(a.note_segment + seg);
-        if (note.x >= 0) {
-            const int f = note.y + x, item = note.x + h * note.z + (f >> 8);
-            const int2 where = __ldcg(k.note_item + item);
-            twice = note.w;                              // both halves hold the rows
-            np = (where.y - where.x + 1) << twice;
-            p_row = (int64_t(item) + where.x) * 256 + (f & 255);
-        }
+        np = note.y;
+        twice = note.w;                                  // both halves hold the rows
+        p_row = int64_t(note.x) * 256 + note.z;
         ns = blocks.y - blocks.x + 1;
         s_at += (int64_t(seg) + blocks.x) * slot;
     }
@@ -952,6 +997,23 @@ __global__ void __launch_bounds__(kMergeThreads, 6) prefix_merge_kernel(const Pr
     // ---- this warp's pieces sub, sub + share, ...: 32 at a time, their (m, l) a lane
     float top = -INFINITY, sum = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    constexpr int kAtOnce = 4;                           // states on their way
+    auto fetch = [&](int t, float4* v) {                 // of pieces t, t + share, ...
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i, t += share) {
+            v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (t < pieces) {
+                const float* at = t < np ? k.state + p_place(t) * D : s_at + int64_t(t - np) * slot + xr * D;
+                if constexpr (D == 128) {
+                    v[i] = __ldcg(reinterpret_cast<const float4*>(at) + lane);
+                } else {
+                    const float2 x2 = __ldcg(reinterpret_cast<const float2*>(at) + lane);
+                    v[i].x = x2.x;
+                    v[i].y = x2.y;
+                }
+            }
+        }
+    };
     for (int t0 = sub; t0 < pieces; t0 += 32 * share) {
         const int mine = t0 + lane * share;
         float2 ml = make_float2(-INFINITY, 0.f);
@@ -959,6 +1021,8 @@ __global__ void __launch_bounds__(kMergeThreads, 6) prefix_merge_kernel(const Pr
             ml = __ldcg(mine < np ? k.state_ml + p_place(mine)
                                   : reinterpret_cast<const float2*>(s_at + int64_t(mine - np) * slot +
                                                                     8 * a.row_tiles * D) + xr);
+        float4 v[kAtOnce];
+        fetch(t0, v);
         float m = fmaxf(top, ml.x);
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1)
@@ -977,32 +1041,18 @@ __global__ void __launch_bounds__(kMergeThreads, 6) prefix_merge_kernel(const Pr
         o.w *= old;
         top = m;
         const int n = min(32, (pieces - t0 + share - 1) / share);
-        constexpr int kAtOnce = 4;                       // on their way
         for (int i0 = 0; i0 < n; i0 += kAtOnce) {
-            float4 v[kAtOnce];
-            float wi[kAtOnce];
+            if (i0 > 0)
+                fetch(t0 + i0 * share, v);
 #pragma unroll
             for (int i = 0; i < kAtOnce; ++i) {
-                wi[i] = __shfl_sync(0xffffffffu, w, i0 + i);     // 0 behind the last
-                v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (wi[i] > 0.f) {
-                    const int t = t0 + (i0 + i) * share;
-                    const float* at = t < np ? k.state + p_place(t) * D : s_at + int64_t(t - np) * slot + xr * D;
-                    if constexpr (D == 128) {
-                        v[i] = __ldcg(reinterpret_cast<const float4*>(at) + lane);
-                    } else {
-                        const float2 x2 = __ldcg(reinterpret_cast<const float2*>(at) + lane);
-                        v[i].x = x2.x;
-                        v[i].y = x2.y;
-                    }
+                const float wi = __shfl_sync(0xffffffffu, w, i0 + i);     // 0 behind the last
+                if (wi != 0.f) {                         // (NaN too; what was not written is not used)
+                    o.x = fmaf(wi, v[i].x, o.x);
+                    o.y = fmaf(wi, v[i].y, o.y);
+                    o.z = fmaf(wi, v[i].z, o.z);
+                    o.w = fmaf(wi, v[i].w, o.w);
                 }
-            }
-#pragma unroll
-            for (int i = 0; i < kAtOnce; ++i) {
-                o.x = fmaf(wi[i], v[i].x, o.x);
-                o.y = fmaf(wi[i], v[i].y, o.y);
-                o.z = fmaf(wi[i], v[i].z, o.z);
-                o.w = fmaf(wi[i], v[i].w, o.w);
             }
         }
     }
@@ -1129,10 +1179,9 @@ cudaError_t launch_prefix(const CUtensorMap& key_map, const CUtensorMap& value_m
 cudaError_t launch_prefix_merge(PrefixMergeArgs a, int D, int sm_count, cudaStream_t stream)
 {
     const PrefixKernelArgs& k = a.prefix_args;
-    // as many warps a row as the device holds of them at once
     const int64_t rows = int64_t(k.B) * k.H_kv * k.R;
     a.share = kMergeWarps;
-    while (a.share > 1 && rows * a.share > int64_t(sm_count) * 6 * kMergeWarps)
+    while (a.share > 1 && rows * a.share > int64_t(sm_count) * kMergeWarpsPerSM)
         a.share /= 2;
     const int64_t blocks = (rows * a.share + kMergeWarps - 1) / kMergeWarps;
     if (blocks <= 0 || blocks >= (int64_t(1) << 31))
