@@ -1972,8 +1972,6 @@ struct PrefixPlan {
            total = 0;
 };
 
-constexpr int32_t kMaxPrefixes = 256;    // their table lies in shared memory
-
 pa_status plan_prefix(const pa_shape& s, int32_t page_size, int kind, int32_t count, int32_t max_prefix_len,
                       const DeviceInfo* dev, PrefixPlan* p)
 {

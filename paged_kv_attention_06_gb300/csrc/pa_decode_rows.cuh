@@ -93,10 +93,10 @@ struct Smem {
     static constexpr int kSlabs = kRing + kWarps * kStages * 2 * Sh::kTileBytes;
     static constexpr int kBars = kSlabs + 2 * kSlab;                  // [warp][stage][K, V]
     static constexpr int kMisc = kBars + kWarps * kStages * 2 * 8;
-    static constexpr int kPrefix = kMisc + 16;   // [B + 1] granules before, [B] granules, [B] lengths, kSuffix: [B] firsts
+    static constexpr int kPrefix = kMisc + 16;   // [B + 1] granules before, [B] granules, [B] lengths, kSuffix: [B] firsts, the prefixes' starts and lengths
     static size_t bytes(int B)
     {
-        return kPrefix + size_t((kMode == kSuffix ? 4 : 3) * B + 1) * 4 + 1024;
+        return kPrefix + size_t(kMode == kSuffix ? 4 * B + 1 + 2 * kMaxPrefixes + 1 : 3 * B + 1) * 4 + 1024;
     }
 };
 
@@ -341,6 +341,8 @@ __global__ void __launch_bounds__(kThreads, (Smem<D, KIND, NT, kMode>::kBlocksPe
     int32_t* gbr = pre + a.B + 1;
     int32_t* len = gbr + a.B;
     int32_t* firsts = len + a.B;                      // kSuffix
+    int32_t* prefix_starts = firsts + a.B;
+    int32_t* prefix_lens = prefix_starts + kMaxPrefixes + 1;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g = lane >> 2, q = lane & 3;
     const int MS = kCut ? a.MS : 1;
@@ -367,23 +369,40 @@ __global__ void __launch_bounds__(kThreads, (Smem<D, KIND, NT, kMode>::kBlocksPe
     grid_launch_dependents();
 
     // ---- this block's granules [x_begin, x_end) -------------------------------
+    // (A thread a request: one warp, with the prefixes' tables in global memory, took 1 to 2
+    // us more.)
+    int n = int(threadIdx.x) < a.B ? a.context_lens[threadIdx.x] : 0;
+    if constexpr (kMode == kSuffix) {
+#pragma unroll 1
+        for (int p = threadIdx.x; p <= a.prefix.count; p += kThreads) {
+            prefix_starts[p] = __ldg(a.prefix.starts + p);
+            if (p < a.prefix.count)
+                prefix_lens[p] = prefix_len(a.prefix, p);
+        }
+        __syncthreads();
+    }
+#pragma unroll 1
+    for (int b = threadIdx.x; b < a.B; b += kThreads) {
+        if (b >= kThreads)
+            n = a.context_lens[b];
+        n = clamp_context(n, cap, a.err);
+        int first = 0;
+        if constexpr (kMode == kSuffix) {
+            const int p = prefix_of(prefix_starts, a.prefix.count, b);
+            firsts[b] = first = p < 0 ? 0 : min(prefix_lens[p], n);
+        }
+        gbr[b] = tile_span<kTok, kMode>(a, n, first).granules;
+        len[b] = n;
+    }
+    __syncthreads();
     if (warp == 0) {
         int carry = 0;
         if (lane == 0)
             pre[0] = 0;
+#pragma unroll 1
         for (int base = 0; base < a.B; base += 32) {
             const int b = base + lane;
-            int gs = 0;
-            if (b < a.B) {
-                const int n = clamp_context(a.context_lens[b], cap, a.err);
-                int first = 0;
-                if constexpr (kMode == kSuffix)
-                    firsts[b] = first = min(prefix_len_of(a.prefix, b), n);
-                gs = tile_span<kTok, kMode>(a, n, first).granules;
-                gbr[b] = gs;
-                len[b] = n;
-            }
-            int incl = gs * per_req;
+            int incl = b < a.B ? gbr[b] * per_req : 0;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const int v = __shfl_up_sync(0xffffffffu, incl, o);
@@ -1029,6 +1048,7 @@ __global__ void __launch_bounds__(kThreads) decode_rows_merge_kernel(const Decod
     // The split of the first kernel, from its inputs (which were complete before
     // it let this one start).
     int before = 0, total = 0;
+#pragma unroll 1
     for (int r = threadIdx.x; r < a.B; r += kThreads) {
         const int gs = granules(r) * per_req;
         total += gs;

@@ -301,6 +301,7 @@ struct PrefixMergeArgs {
     int32_t MS, row_tiles;        // of the few-row kernel
     int32_t share;                // set by the launcher: warps a row
 };
+constexpr int kMaxPrefixes = 256;      // their tables lie in shared memory
 // A block's pieces of items that lie in shared memory; an item's units of work.
 constexpr int kPrefixMaxPieces = 64;
 inline int64_t prefix_item_units(int64_t tiles) { return tiles * 4 + 8; }

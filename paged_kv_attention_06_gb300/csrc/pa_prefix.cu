@@ -229,51 +229,57 @@ __device__ __forceinline__ void convert_run(uint8_t* mat, int block_bytes, const
     constexpr int kChunks = kQ4 ? 4 : 8;                         // 16-byte pieces of a row's codes
     constexpr int kOut = kQ4 ? 4 : 2;                            // 16-byte pieces of f16 from each
     const int c = lane % kChunks;
-    // Lanes whose pieces go to the second column block start with the other half of
-    // them: the eight lanes of a store then meet eight different bank groups.
-    const bool turned = c >= kChunks / 2;
-    uint4 codes[kChunks];                                        // all read before the first is stored
-    uint32_t params[kQ4 ? kChunks : 1];
+    // Lanes whose pieces go to the second column block take another key's: the eight lanes
+    // of a store then meet eight different bank groups.
+    const int turn = c >= kChunks / 2 ? kOut / 2 : 0;
+    // Half of them at a time, all read before the first is stored. (All at once: 1 us more a
+    // call. Instructions that a block runs for the first time cost it about 5 cycles each.)
+#pragma unroll 1
+    for (int half = 0; half < 2; ++half) {
+        uint4 codes[kChunks / 2];
+        uint32_t params[kQ4 ? kChunks / 2 : 1];
+        const int row0 = half * 16 + lane / kChunks;
 #pragma unroll
-    for (int i = 0; i < kChunks; ++i) {
-        const uint8_t* row = from + (i * (32 / kChunks) + lane / kChunks) * kRowBytes;
-        codes[i] = *(reinterpret_cast<const uint4*>(row) + c);
-        if constexpr (kQ4)
-            params[i] = *(reinterpret_cast<const uint32_t*>(row + kQ4CodeBytes) + c);
-    }
-#pragma unroll
-    for (int i = 0; i < kChunks; ++i) {
-        const int r = i * (32 / kChunks) + lane / kChunks;
-        const uint4 x = codes[i];
-        const uint32_t w[4] = {turned ? x.z : x.x, turned ? x.w : x.y, turned ? x.x : x.z, turned ? x.y : x.w};
-        uint32_t v[4 * kOut];
-        if constexpr (kQ4) {
-            const uint32_t s = __byte_perm(params[i], 0, 0x1010), m = __byte_perm(params[i], 0, 0x3232);
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    // c exactly (1024 + c - 1024, (1024 + 16 c) / 16 - 64), then m + s c
-                    const uint32_t y = w[k] >> (8 * j);
-                    const uint32_t lo = add_f16x2((y & 0x000f000fu) | 0x64006400u, 0xe400e400u);
-                    const uint32_t hi = fma_f16x2((y & 0x00f000f0u) | 0x64006400u, 0x2c002c00u, 0xd400d400u);
-                    v[4 * k + 2 * j] = fma_f16x2(lo, s, m);
-                    v[4 * k + 2 * j + 1] = fma_f16x2(hi, s, m);
-                }
-        } else {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                v[2 * k] = e4m3x2_to_f16x2(w[k]);
-                v[2 * k + 1] = e4m3x2_hi_to_f16x2(w[k]);
-            }
+        for (int i = 0; i < kChunks / 2; ++i) {
+            const uint8_t* row = from + ((row0 + i * (32 / kChunks)) ^ turn) * kRowBytes;
+            codes[i] = *(reinterpret_cast<const uint4*>(row) + c);
+            if constexpr (kQ4)
+                params[i] = *(reinterpret_cast<const uint32_t*>(row + kQ4CodeBytes) + c);
         }
-        const int key = key0 + r;
 #pragma unroll
-        for (int k = 0; k < kOut; ++k) {
-            const int ch = c * kOut + (turned ? k ^ (kOut / 2) : k);   // 16-byte piece of the f16 row
-            *reinterpret_cast<uint4*>(mat + (ch >> 3) * block_bytes + key * 128 + (((ch & 7) ^ (key & 7)) << 4)) =
-                !kEnds || r < live ? make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3])
-                                   : make_uint4(0, 0, 0, 0);
+        for (int i = 0; i < kChunks / 2; ++i) {
+            const int r = (row0 + i * (32 / kChunks)) ^ turn;
+            const uint4 x = codes[i];
+            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+            uint32_t v[4 * kOut];
+            if constexpr (kQ4) {
+                const uint32_t s = __byte_perm(params[i], 0, 0x1010), m = __byte_perm(params[i], 0, 0x3232);
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        // c exactly (1024 + c - 1024, (1024 + 16 c) / 16 - 64), then m + s c
+                        const uint32_t y = w[k] >> (8 * j);
+                        const uint32_t lo = add_f16x2((y & 0x000f000fu) | 0x64006400u, 0xe400e400u);
+                        const uint32_t hi = fma_f16x2((y & 0x00f000f0u) | 0x64006400u, 0x2c002c00u, 0xd400d400u);
+                        v[4 * k + 2 * j] = fma_f16x2(lo, s, m);
+                        v[4 * k + 2 * j + 1] = fma_f16x2(hi, s, m);
+                    }
+            } else {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    v[2 * k] = e4m3x2_to_f16x2(w[k]);
+                    v[2 * k + 1] = e4m3x2_hi_to_f16x2(w[k]);
+                }
+            }
+            const int key = key0 + r;
+#pragma unroll
+            for (int k = 0; k < kOut; ++k) {
+                const int ch = c * kOut + k;   // 16-byte piece of the f16 row
+                *reinterpret_cast<uint4*>(mat + (ch >> 3) * block_bytes + key * 128 + (((ch & 7) ^ (key & 7)) << 4)) =
+                    !kEnds || r < live ? make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3])
+                                       : make_uint4(0, 0, 0, 0);
+            }
         }
     }
 }
@@ -333,6 +339,7 @@ __global__ void __launch_bounds__((Layout<D, KIND>::kThreads), 1)
     // in 4 us after they were asked for).
     {
         const int64_t lines = (int64_t(a.B) * a.H_q * a.L * D * 2 + 127) / 128;
+#pragma unroll 1
         for (int64_t i = int64_t(blockIdx.x) * Lay::kThreads + threadIdx.x; i < lines;
              i += int64_t(gridDim.x) * Lay::kThreads)
             prefetch_l2(reinterpret_cast<const uint8_t*>(a.q) + i * 128);
@@ -344,6 +351,7 @@ __global__ void __launch_bounds__((Layout<D, KIND>::kThreads), 1)
         const int prefixes = a.prefix.count;
         int us = 0, item = 0;
         bool bad = false;
+#pragma unroll 1
         for (int base = 0; base < prefixes; base += 32) {
             const int p = base + lane;
             Group g;
@@ -384,6 +392,7 @@ __global__ void __launch_bounds__((Layout<D, KIND>::kThreads), 1)
         int found = 0;
         if (U > 0 && c < ranges.G) {
             const int s = ranges.start(c), e = ranges.start(c + 1);
+#pragma unroll 1
             for (int base = 0; base < prefixes; base += 32) {
                 const int p = base + lane;
                 int i0 = 0, n = 0;
@@ -410,6 +419,7 @@ __global__ void __launch_bounds__((Layout<D, KIND>::kThreads), 1)
                         incl += v;
                 }
                 const int blocks = n > 0 ? (g.rows + 255) / 256 : 1;
+#pragma unroll 1
                 for (int x = 0; x < n; ++x) {
                     const int at = found + incl - n + x, i = i0 + x;
                     Piece& pc = pieces[at];
@@ -436,16 +446,18 @@ __global__ void __launch_bounds__((Layout<D, KIND>::kThreads), 1)
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     const int count = piece_count;
-    // ---- notes for the merge: where each row's states are
-    if (warp == 3) {
+    // ---- notes for the merge: where each row's states are (warp 3)
+    auto write_notes = [&]() {
         const Group* groups = reinterpret_cast<const Group*>(smem + Lay::kGroups);
         const Ranges ranges(all_units, int(gridDim.x));
         const int rows = a.B * a.H_kv * a.R;
+#pragma unroll 1
         for (int row = c * 32 + lane; row < rows; row += int(gridDim.x) * 32) {
             const int bh = a.by_R.of(row), x = row - bh * a.R, b = a.by_H.of(bh), h = bh - b * a.H_kv;
             int4 note = make_int4(0, 0, 0, 0);
             if (all_units > 0 && b >= groups[0].first) {
                 int p = 0;                               // the last prefix that starts at b or before
+#pragma unroll 1
                 for (int hi = a.prefix.count; hi - p > 1;) {
                     const int mid = (p + hi) >> 1;
                     if (groups[mid].first <= b)
@@ -465,10 +477,12 @@ __global__ void __launch_bounds__((Layout<D, KIND>::kThreads), 1)
             }
             a.note_row[row] = note;
         }
-    }
+    };
     if (count == 0) {
         if (warp == 1)
             tmem_dealloc(tmem, kTmemCols);
+        if (warp == 3)
+            write_notes();
         return;
     }
 
@@ -576,6 +590,7 @@ __global__ void __launch_bounds__((Layout<D, KIND>::kThreads), 1)
                     info[slot] = make_int2(-1, 0);
                     mbar_arrive(&bar[kCodeFull + slot]);
                 }
+#pragma unroll 1
                 for (int i = 1; i < kRing; ++i) {
                     ++u;
                     slot_free(u % kRing);
@@ -631,8 +646,12 @@ __global__ void __launch_bounds__((Layout<D, KIND>::kThreads), 1)
                 }
             }
             // No copy may still be landing when the block exits.
+#pragma unroll 1
             for (int i = max(0, g - 2); i < g; ++i)
                 mbar_wait_bounded(&bar[full + (i & 1)], (i >> 1) & 1, misc, a.err);
+        } else if (warp == 3) {
+            // (not before the registers are handed over: the softmax waits for them)
+            write_notes();
         } else if (warp == 1) {
             // ===================== MMA issue (one elected thread) =====================
             const bool leader = elect_one();
@@ -779,23 +798,27 @@ __global__ void __launch_bounds__((Layout<D, KIND>::kThreads), 1)
                 constexpr int kChunks = D / 8;           // 16-byte chunks of a row
                 constexpr int kPer = 32 / kChunks;       // rows a round
                 constexpr int kRounds = 32 / kPer;
-                uint4 v[kRounds];                        // all on their way before the first is stored
                 const int ch = lane % kChunks;
-#pragma unroll
+                auto place = [&](int i) {                // of round i's
+                    const int rr = w4 * 32 + i * kPer + lane / kChunks;
+                    return reinterpret_cast<uint4*>(mat + (ch >> 3) * Lay::kBlock + rr * 128 +
+                                                    (((ch & 7) ^ (rr & 7)) << 4));
+                };
+#pragma unroll 2
                 for (int i = 0; i < kRounds; ++i) {
                     const int64_t at = __shfl_sync(0xffffffffu, q_at, i * kPer + lane / kChunks);
-                    v[i] = __ldg(reinterpret_cast<const uint4*>(a.q + at + ch * 8));
+                    cp_async_16(place(i), a.q + at + ch * 8, 16);
                 }
-#pragma unroll
-                for (int i = 0; i < kRounds; ++i) {
-                    const int rr = w4 * 32 + i * kPer + lane / kChunks;
-                    if constexpr (kCodes)
-                        v[i] = make_uint4(bf16x2_to_f16x2(v[i].x), bf16x2_to_f16x2(v[i].y), bf16x2_to_f16x2(v[i].z),
-                                          bf16x2_to_f16x2(v[i].w));
-                    if constexpr (KIND == kQ4Pool)
-                        v[i] = apart(v[i]);
-                    *reinterpret_cast<uint4*>(mat + (ch >> 3) * Lay::kBlock + rr * 128 + (((ch & 7) ^ (rr & 7)) << 4)) =
-                        v[i];
+                cp_async_commit();
+                cp_async_wait_group<0>();
+                if constexpr (kCodes) {                  // each lane what it has copied
+#pragma unroll 2
+                    for (int i = 0; i < kRounds; ++i) {
+                        uint4 v = *place(i);
+                        v = make_uint4(bf16x2_to_f16x2(v.x), bf16x2_to_f16x2(v.y), bf16x2_to_f16x2(v.z),
+                                       bf16x2_to_f16x2(v.w));
+                        *place(i) = KIND == kQ4Pool ? apart(v) : v;
+                    }
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
@@ -894,6 +917,7 @@ __global__ void __launch_bounds__((Layout<D, KIND>::kThreads), 1)
                     mbar_wait_bounded(&bar[kVFull + (g & 1)], (g >> 1) & 1, misc, a.err);
                     const int z = n - key0;
                     uint8_t* vb = smem + Lay::kV + (g & 1) * Lay::kMat;
+#pragma unroll 1
                     for (int idx = r; idx < (kKeys - z) * (D / 8); idx += 128) {
                         const int zr = z + idx / (D / 8), ch = idx % (D / 8);
                         *reinterpret_cast<uint4*>(vb + (ch >> 3) * Lay::kBlock + zr * 128 +
@@ -1014,6 +1038,7 @@ __global__ void __launch_bounds__(kMergeThreads, 4) prefix_merge_kernel(const Pr
             }
         }
     };
+#pragma unroll 1
     for (int t0 = sub; t0 < pieces; t0 += 32 * share) {
         const int mine = t0 + lane * share;
         float2 ml = make_float2(-INFINITY, 0.f);
@@ -1041,6 +1066,7 @@ __global__ void __launch_bounds__(kMergeThreads, 4) prefix_merge_kernel(const Pr
         o.w *= old;
         top = m;
         const int n = min(32, (pieces - t0 + share - 1) / share);
+#pragma unroll 1
         for (int i0 = 0; i0 < n; i0 += kAtOnce) {
             if (i0 > 0)
                 fetch(t0 + i0 * share, v);
@@ -1064,6 +1090,7 @@ __global__ void __launch_bounds__(kMergeThreads, 4) prefix_merge_kernel(const Pr
         if (sub != 0)
             return;
         float m = top;
+#pragma unroll 1
         for (int w = 1; w < share; ++w)
             m = fmaxf(m, row_ml[warp + w].x);
         const float f = top == -INFINITY ? 0.f : fast_exp2(top - m);
@@ -1072,6 +1099,7 @@ __global__ void __launch_bounds__(kMergeThreads, 4) prefix_merge_kernel(const Pr
         o.y *= f;
         o.z *= f;
         o.w *= f;
+#pragma unroll 1
         for (int w = 1; w < share; ++w) {
             const float2 ml = row_ml[warp + w];
             const float fw = ml.x == -INFINITY ? 0.f : fast_exp2(ml.x - m);

@@ -12,26 +12,21 @@ __device__ __forceinline__ int prefix_len(const PrefixArgs& x, int p)
     return n < 0 ? 0 : n > x.cap ? x.cap : n;
 }
 
-// The prefix of request b: starts[p] <= b < starts[p + 1]; -1 where it has none.
-__device__ __forceinline__ int prefix_of(const PrefixArgs& x, int b)
+// The prefix of request b, starts[p] <= b < starts[p + 1], of `count` that start in
+// ascending order (shared memory); -1 where it has none.
+__device__ __forceinline__ int prefix_of(const int* starts, int count, int b)
 {
-    if (x.count == 0 || b < __ldg(x.starts) || b >= __ldg(x.starts + x.count))
+    if (b < starts[0] || b >= starts[count])
         return -1;
-    int lo = 0, hi = x.count;              // starts[lo] <= b < starts[hi]
+    int lo = 0, hi = count;                // starts[lo] <= b < starts[hi]
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (__ldg(x.starts + mid) <= b)
+        if (starts[mid] <= b)
             lo = mid;
         else
             hi = mid;
     }
     return lo;
-}
-
-__device__ __forceinline__ int prefix_len_of(const PrefixArgs& x, int b)
-{
-    const int p = prefix_of(x, b);
-    return p < 0 ? 0 : prefix_len(x, p);
 }
 
 // The few-row kernel behind a prefix: granules (four tiles of tile_keys) of the keys
