@@ -211,10 +211,11 @@ def _dev_ptr(t: torch.Tensor, dtype: torch.dtype, name: str) -> int:
     return t.data_ptr()
 
 
-def make_shape(query_shape, pages_shape, max_pages: int) -> pa_shape:
+def make_shape(query_shape, pages_shape, max_pages: int, q4: bool = False) -> pa_shape:
+    """The sizes of a call. q4: the pools hold 4-bit rows of 80 bytes for 128 elements."""
     B, H_q, L, D = (int(x) for x in query_shape)
     P, H_kv, _, D2 = (int(x) for x in pages_shape)
-    if D2 != D:
+    if (D, D2) != (128, 80) if q4 else D2 != D:
         raise ValueError("query and pages disagree on head_dim")
     return pa_shape(B, H_q, H_kv, D, L, P, int(max_pages))
 

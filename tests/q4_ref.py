@@ -73,7 +73,7 @@ def make(lens, H_q, H_kv, L, ps, seed, poison=True, std=1.0):
 
 def reference(c, copied=False, causal=True, scale=None):
     """As window_ref.reference, with the roundings that the calls document left in: s c to
-    f16 (decode), or the value to bf16 (copied: prefill). The magnitudes are those of
+    f16 (decode), or keys to bf16 and values to f16 (copied: prefill). The magnitudes are those of
     s c and m apart, as the decode sums them."""
     ps = c["page_size"]
     B, H_q, L, _ = c["query"].shape
@@ -91,7 +91,8 @@ def reference(c, copied=False, causal=True, scale=None):
                 rows = pool[page, :, j % ps].transpose(0, 1).cpu().numpy()
                 code, s, m = parts(rows)
                 if copied:
-                    v = dense_values(rows)
+                    v = (m + s * code).astype(np.float32).astype(np.float16).astype(np.float64) if vals \
+                        else dense_values(rows)
                     w = np.abs(v)
                 else:
                     sc = (s * code).astype(np.float16).astype(np.float64)
