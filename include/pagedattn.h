@@ -609,7 +609,8 @@ pa_status pa_kv_evict_fp8(void *key_pages, void *value_pages, float *weight_page
  *   y = f16(min(max(x, -448), 448)),  m = min y,  s = f16(fp32(max y - m) / 15),
  *   code = the integer nearest to (y - m) / s, ties to even, at most 15 (0 where s
  *   is 0). A NaN makes its group's m and s NaN.
- * Same slots, checks and error reporting as pa_append_kv.
+ * Same slots, checks and error reporting as pa_append_kv. (Of two tokens with the same
+ * slot a row may get codes of the one and steps of the other.)
  */
 pa_status pa_append_kv_q4(const void *key, const void *value, void *key_pages, void *value_pages,
                           const int32_t *slot_mapping, int32_t page_size, pa_shape shape,

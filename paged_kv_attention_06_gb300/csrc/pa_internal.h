@@ -304,7 +304,7 @@ struct PrefixMergeArgs {
 constexpr int kMaxPrefixes = 256;      // their tables lie in shared memory
 // A block's pieces of items that lie in shared memory; an item's units of work.
 constexpr int kPrefixMaxPieces = 64;
-inline int64_t prefix_item_units(int64_t tiles) { return tiles * 4 + 8; }
+inline int64_t prefix_item_units(int64_t tiles) { return tiles * 4 + 16; }
 size_t prefix_smem_bytes(int D, int kind, int count);
 // The workspace of the states of `items` items, and where (m, l) and the pieces behind
 // kPrefixMaxPieces start in it.
