@@ -11,8 +11,14 @@
 // Reading back: m + s c in fp32 (s c is exact, one rounding in the sum), rounded to
 // bf16, into dense rows or into the 128-token pages that the prefill kernels read.
 //
-// Both are bound by memory. A row of 128 bf16 is 16 lanes of 16 bytes in, 4 bytes of
-// codes a lane out (or the other way round), the group's extremes found among 4 lanes.
+// A row of 128 bf16 is 16 lanes of 16 bytes in, 4 bytes of codes a lane out (or the other
+// way round), the group's extremes found among 4 lanes. Measured, both calls together: 4 x
+// 2047 tokens of 8 heads written and 49k rows read back, 108 MB, 27.3 us (4.0 TB/s, of 6.8
+// for a copy); 32 tokens written and 75k rows read back, 101 MB, 23.3; one token and 300
+// rows 5.3. Two kernels of which the second waits for the first: what bounds them is the
+// latency of one pass of loads a block, and the append's instructions (with quotients near
+// a half decided in 64 bits it took 48 us alone, 18 in the fp32 arithmetic below; streamed
+// loads or stores change nothing).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <stdint.h>
