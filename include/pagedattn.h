@@ -627,9 +627,8 @@ pa_status pa_gather_kv_q4(const void *key_pages, const void *value_pages,
                           void *value_dense, void *stream);
 
 /*
- * pa_decode over 4-bit pools, straight from the codes: s c is rounded to f16 (and s / 16
- * too, for the codes in the high halves, which shows where s is below 2^-10), m is added
- * in the products' fp32 sums. The query and the softmax weights are taken in f16 (query
+ * pa_decode over 4-bit pools, straight from the codes: s c is rounded to f16, m is added in
+ * the products' fp32 sums. The query and the softmax weights are taken in f16 (query
  * elements below 65504 in magnitude; below 2^-14 they keep fewer bits). A group whose m
  * and s are NaN gives NaN in a visible slot; slots past a request's context are never
  * read. Any L; K and V are read once per 16 rows (G * L) of a request and KV head.

@@ -295,19 +295,17 @@ struct RowState {
     }
 };
 
-// A 4-bit group's step as the multiply-adds that turn codes into f16 take it: bits
-// 0-3 of a half of 0x6400 + c are 1024 + c, bits 4-7 of 0x6400 + 16 c 1024 + 16 c, so
-//   s (1024 + c) - 1024 s  and  (s / 16) (1024 + 16 c) - 64 s
-// are s c, rounded once (-1024 s is an f16: s is at most 60; s / 16 loses bits where s is
-// below 2^-10, up to 2^-21 c of the value).
+// A 4-bit group's step as the multiply-adds that turn codes into f16 take it: bits 0-3 of
+// a half of w behind 0x6400 are 1024 + c, bits 4-7 behind 0x5400 are 64 + c, so
+//   s (1024 + c) - 1024 s  and  s (64 + c) - 64 s
+// are s c, rounded once (-1024 s is an f16: s is at most 60).
 struct Q4Step {
-    uint32_t s, s16, c, c16;      // f16x2
+    uint32_t s, c, c64;           // f16x2
     __device__ __forceinline__ explicit Q4Step(uint32_t step)
     {
         s = step;
-        s16 = mul_f16x2(step, 0x2c002c00u);    // 1/16
         c = mul_f16x2(step, 0xe400e400u);      // -1024
-        c16 = mul_f16x2(step, 0xd400d400u);    // -64
+        c64 = mul_f16x2(step, 0xd400d400u);    // -64
     }
     // The codes in bits 0-3 / 4-7 of both halves of w.
     __device__ __forceinline__ uint32_t low(uint32_t w) const
@@ -316,7 +314,7 @@ struct Q4Step {
     }
     __device__ __forceinline__ uint32_t high(uint32_t w) const
     {
-        return fma_f16x2((w & 0x00f000f0u) | 0x64006400u, s16, c16);
+        return fma_f16x2((w & 0x00f000f0u) | 0x54005400u, s, c64);
     }
 };
 
@@ -432,13 +430,12 @@ __global__ void __launch_bounds__(kThreads, (Smem<D, KIND, NT, kMode>::kBlocksPe
             grid_dependency_wait();
         return;
     }
-    const int64_t x_end = p1.x;
-
     // A place in the stream, with what its segment needs: the loads run ahead of
     // the products, across the ends of pieces.
     struct Place {
-        int64_t x;
         SegmentPos sp;
+        int in_seg;                       // granule of the segment
+        int rest;                         // the block's granules from this one on
         int n;
         TileSpan span;
     };
@@ -448,7 +445,7 @@ __global__ void __launch_bounds__(kThreads, (Smem<D, KIND, NT, kMode>::kBlocksPe
     };
     // First token of the warp's tile of place p, and the end of its run.
     auto tile_at = [&](const Place& p, int* end) {
-        const int t = int(p.x - p.sp.seg_start) * kWarps + warp;
+        const int t = p.in_seg * kWarps + warp;
         const bool first_run = kMode == kWindow && t < p.span.sink_tiles;
         *end = first_run ? a.sinks : p.n;
         return first_run ? t * kTok : p.span.start + (t - p.span.sink_tiles) * kTok;
@@ -501,13 +498,15 @@ __global__ void __launch_bounds__(kThreads, (Smem<D, KIND, NT, kMode>::kBlocksPe
     };
     // The next tile to be requested, and its rows (found a step ahead).
     Place ahead;
-    ahead.x = p0.x;
     ahead.sp = segment_at(pre, gbr, per_req, MS, p0.b, p0.hm);
+    ahead.in_seg = int(p0.x - ahead.sp.seg_start);
+    ahead.rest = int(p1.x - p0.x);
     enter(ahead);
     Place at = ahead;                     // the tile at hand
     auto step = [&](Place& p) {
-        if (++p.x < x_end && p.x == p.sp.seg_start + p.sp.seg_len) {
+        if (--p.rest > 0 && ++p.in_seg == p.sp.seg_len) {
             p.sp = next_segment(pre, gbr, per_req, MS, p.sp);
+            p.in_seg = 0;
             enter(p);
         }
     };
@@ -515,11 +514,10 @@ __global__ void __launch_bounds__(kThreads, (Smem<D, KIND, NT, kMode>::kBlocksPe
     int page = page_of(ahead, tok);
 #pragma unroll
     for (int st = 0; st < kStages; ++st) {
-        const bool live = ahead.x < x_end;
-        if (live) {
+        if (ahead.rest > 0) {
             const int row = row_of(ahead, tok, page);
             step(ahead);
-            if (ahead.x < x_end) {
+            if (ahead.rest > 0) {
                 tok = box_token(ahead);
                 page = page_of(ahead, tok);
             }
@@ -531,11 +529,13 @@ __global__ void __launch_bounds__(kThreads, (Smem<D, KIND, NT, kMode>::kBlocksPe
     int stage = 0;
     uint32_t phase = 0;
 
-    while (at.x < x_end) {
+    while (at.rest > 0) {
         const SegmentPos sp = at.sp;
         const int n = at.n;
         const TileSpan span = at.span;
-        const int64_t piece_end = min(x_end, sp.seg_start + sp.seg_len);
+        const int len_here = min(at.rest, sp.seg_len - at.in_seg);
+        const bool opens = at.in_seg == 0, closes = at.in_seg + len_here == sp.seg_len;
+        at.rest -= len_here;
         const int row0 = kCut ? sp.ms * kSegmentRows : 0;     // the segment's rows of the R
         const int rows = a.R - row0;                          // (8 NT of them at most)
         const int64_t q_row0 = (int64_t(sp.b) * a.H_q + sp.h * a.G) * a.L + row0;
@@ -624,12 +624,12 @@ __global__ void __launch_bounds__(kThreads, (Smem<D, KIND, NT, kMode>::kBlocksPe
         for (int nt = 0; nt < NT; ++nt)
             om[nt][0] = om[nt][1] = om[nt][2] = om[nt][3] = 0.f;
 
-        for (; at.x < piece_end; ++at.x) {
+        for (const int end_here = at.in_seg + len_here; at.in_seg < end_here; ++at.in_seg) {
             int end;
             const int t0 = tile_at(at, &end);
             const bool busy = t0 < end;              // the last granule may hold fewer than four tiles
             const bool first_run =
-                kMode == kWindow && int(at.x - sp.seg_start) * kWarps + warp < span.sink_tiles;
+                kMode == kWindow && at.in_seg * kWarps + warp < span.sink_tiles;
             const uint8_t* kt = ring + stage * (2 * kTileBytes);
             const uint8_t* vt = kt + kTileBytes;
             mbar_wait_warp(&bars[stage * 2], phase, misc, a.err);
@@ -720,13 +720,13 @@ __global__ void __launch_bounds__(kThreads, (Smem<D, KIND, NT, kMode>::kBlocksPe
             // The keys of the tile kStages on (into the place just read), and the
             // rows of the one after.
             int row_v = -1;
-            const bool more = ahead.x < x_end;
+            const bool more = ahead.rest > 0;
             if (more) {
                 row_v = row_of(ahead, tok, page);
                 __syncwarp();                        // every lane has read the place
                 copy(row_v, stage, 0);
                 step(ahead);
-                if (ahead.x < x_end) {
+                if (ahead.rest > 0) {
                     tok = box_token(ahead);
                     page = page_of(ahead, tok);
                 }
@@ -1001,19 +1001,20 @@ __global__ void __launch_bounds__(kThreads, (Smem<D, KIND, NT, kMode>::kBlocksPe
                 // (after a wait that ran out too: what follows finds its places by these notes)
                 st.template put_rows<KIND>(a.partials + (int64_t(sp.seg) + cta) * kSlot, rows, lane);
                 if (lane == 0) {
-                    if (sp.seg_start >= p0.x)
+                    if (opens)
                         a.note_segment[sp.seg].x = int(cta);
-                    if (sp.seg_start + sp.seg_len <= x_end)
+                    if (closes)
                         a.note_segment[sp.seg].y = int(cta);
                 }
-            } else if (sp.seg_start >= p0.x && sp.seg_start + sp.seg_len <= x_end)
+            } else if (opens && closes)
                 st.template write<KIND, kMode>(a, int64_t(sp.b) * a.H_kv + sp.h, q_row0, rows, lane);
             else                                     // a slot of its own: segment and block
                 st.put(a.partials + (int64_t(sp.seg) + cta) * kSlot, lane);
         }
         // on to the next segment
-        if (at.x < x_end) {
+        if (at.rest > 0) {
             at.sp = next_segment(pre, gbr, per_req, MS, sp);
+            at.in_seg = 0;
             enter(at);
         }
     }

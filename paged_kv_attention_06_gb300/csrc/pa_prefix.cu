@@ -270,10 +270,10 @@ __device__ __forceinline__ void convert_run(uint8_t* mat, int block_bytes, const
                 for (int k = 0; k < 4; ++k)
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
-                        // c exactly (1024 + c - 1024, (1024 + 16 c) / 16 - 64), then m + s c
+                        // c exactly (1024 + c - 1024, 64 + c - 64), then m + s c
                         const uint32_t y = w[k] >> (8 * j);
                         const uint32_t lo = add_f16x2((y & 0x000f000fu) | 0x64006400u, 0xe400e400u);
-                        const uint32_t hi = fma_f16x2((y & 0x00f000f0u) | 0x64006400u, 0x2c002c00u, 0xd400d400u);
+                        const uint32_t hi = add_f16x2((y & 0x00f000f0u) | 0x54005400u, 0xd400d400u);
                         v[4 * k + 2 * j] = fma_f16x2(lo, s, m);
                         v[4 * k + 2 * j + 1] = fma_f16x2(hi, s, m);
                     }
