@@ -183,6 +183,71 @@ def test_prefill(L, H_q, H_kv, ps):
         check_out(out, reference(c, copied=True), False, max(lens))
 
 
+@pytest.mark.parametrize("L,H_q,H_kv", [(300, 32, 8), (300, 28, 4), (700, 32, 8), (700, 28, 4)])
+def test_prefill_of_many_rows(L, H_q, H_kv):
+    """Enough (request, head pair, 128 rows) items for the kernel of pairs: even and odd groups,
+    one to two items a block (tail pieces) and more."""
+    pa = _pa()
+    lens = [L, L + 1, 0, L - 200, L + 300, L + 129]
+    c = make(lens, H_q, H_kv, L, 16, seed=L + H_q)
+    out = pa.pa_attention_q4(**c, max_context_len=max(lens))
+    check_no_device_error()
+    check_out(out, reference(c, copied=True), False, max(lens))
+
+
+@pytest.mark.parametrize("L", [1, 5, 40, 300])
+def test_captured_calls_and_another_stream(L):
+    """Attention and read-back in a graph on a stream of its own, replayed with other pools,
+    queries, tables and lengths."""
+    pa = _pa()
+    lens, other = [L + 70, L, 333 + L, 0], [L + 5, L + 400, 0, L + 16]
+    c, d = (make([n + 0 for n in x], 8, 2, L, 16, seed=L + i) for i, x in enumerate((lens, other)))
+    P, W = (max(c[k].shape[i], d[k].shape[i]) for k, i in (("key_pages", 0), ("block_table", 1)))
+    longest = max(lens + other)
+
+    def padded(x):
+        y = dict(x)
+        for k in ("key_pages", "value_pages"):
+            y[k] = torch.full((P, *x[k].shape[1:]), 0xFF, dtype=torch.uint8, device="cuda")
+            y[k][:len(x[k])] = x[k]
+        y["block_table"] = torch.full((len(lens), W), -1, dtype=torch.int32, device="cuda")
+        y["block_table"][:, :x["block_table"].shape[1]] = x["block_table"]
+        return y
+
+    c, d = padded(c), padded(d)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        pools = dict(key_pages=c["key_pages"], value_pages=c["value_pages"], block_table=c["block_table"],
+                     context_lens=c["context_lens"], page_size=16, dense_len=longest)
+        dense = [torch.zeros((4, 2, longest, 128), dtype=torch.bfloat16, device="cuda") for _ in "kv"]
+        out = pa.pa_attention_q4(**c, max_context_len=longest)
+        pa.pa_gather_kv_q4(**pools, key_dense=dense[0], value_dense=dense[1])
+        side.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            pa.pa_attention_q4(**c, max_context_len=longest, out=out)
+            pa.pa_gather_kv_q4(**pools, key_dense=dense[0], value_dense=dense[1])
+        for x in (c, d):
+            want = pa.pa_attention_q4(**x, max_context_len=longest)
+            for k in ("query", "key_pages", "value_pages", "block_table", "context_lens"):
+                c[k].copy_(x[k])
+            for t in dense:
+                t.zero_()
+            graph.replay()
+            side.synchronize()
+            assert torch.equal(out, want)
+            check_out(out, reference(x, copied=L > 8), L <= 8, longest)
+            for b, n in enumerate(x["context_lens"].tolist()):
+                j = torch.arange(n, device="cuda")
+                page = x["block_table"][b, j // 16].long()
+                for t, pool in zip(dense, (x["key_pages"], x["value_pages"])):
+                    rows = pool[page, :, j % 16].transpose(0, 1).cpu().numpy()
+                    assert torch.equal(t[b, :, :n].cpu(), torch.from_numpy(dense_values(rows)).to(torch.bfloat16))
+                    assert not t[b, :, n:].any()
+    check_no_device_error()
+
+
 def test_offsets_past_32_bits():
     """Rows whose byte offset in the pool is past 2^32."""
     pa = _pa()
