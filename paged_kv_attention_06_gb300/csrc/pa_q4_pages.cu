@@ -65,17 +65,28 @@ __device__ __forceinline__ uint32_t quantise8(const uint4& x, uint32_t* params)
     uint32_t y[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i)      // f16 first: what is past 448 is cut the same way
-        y[i] = min2(max2(bf16x2_to_f16x2(w[i]), 0xdf00df00u), 0x5f005f00u);
-    static_assert(kQ4Max == 448.f, "0x5f00");
+        y[i] = bf16x2_to_f16x2(w[i]);
     uint32_t lo = min2(min2(y[0], y[1]), min2(y[2], y[3])), hi = max2(max2(y[0], y[1]), max2(y[2], y[3]));
     // (least, negated largest) of the pair, then of the four lanes
     lo = min2(__byte_perm(lo, hi ^ 0x80008000u, 0x5410), __byte_perm(lo, hi ^ 0x80008000u, 0x7632));
 #pragma unroll
     for (int o = 1; o < 4; o <<= 1)
         lo = min2(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-    const float2 ends = widen(lo);
+    float2 ends = widen(lo);
+    static_assert(kQ4Max == 448.f, "0x5f00");
+    if (fminf(ends.x, ends.y) < -kQ4Max) {               // seldom (NaN: the codes are 0 anyway)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            y[i] = min2(max2(y[i], 0xdf00df00u), 0x5f005f00u);
+        lo = min2(max2(lo, 0xdf00df00u), 0x5f005f00u);
+        ends = widen(lo);
+    }
     const float m = ends.x;
-    const __half sh = __float2half_rn(__fdiv_rn(-ends.y - m, 15.f));
+    // (max - m) / 15, correctly rounded: Markstein's correction of the product with the
+    // rounded reciprocal. (No underflow: differences of f16 values are 0 or at least 2^-24.)
+    const float range = -ends.y - m, part = 1.f / 15.f;
+    const float near = range * part;
+    const __half sh = __float2half_rn(fmaf(fmaf(-15.f, near, range), part, near));
     const float s = __half2float(sh);
     *params = uint32_t(__half_as_ushort(sh)) | lo << 16;
     // t / s to within 2^-18 of a step, a quarter of what a half is given for it
