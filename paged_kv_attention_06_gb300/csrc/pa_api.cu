@@ -669,7 +669,8 @@ pa_status run_split_kv(const void* query, const void* key_pages, const void* val
             return st;
         while ((1 << a.ps_shift) < page_size)
             ++a.ps_shift;
-        const int rows_grid = decode_rows_launch_grid(s, kind, extra.mode, max_context_len > 0 ? granules : 0, dev->sm_count);
+        const int rows_grid =
+            decode_rows_launch_grid(s, kind, extra.mode, max_context_len > 0 ? granules : 0, dev->sm_count);
         return launch_decode_rows(kmap, vmap, a, s, kind, rows_grid, workspace, dev->id, stream) == cudaSuccess
                    ? PA_OK
                    : PA_ERR_CUDA;

@@ -1,6 +1,7 @@
 // Split-KV paged attention for few query rows (G * L <= 16 rows per request and
-// KV head), for the calls with a sliding window and those that keep their
-// scores.
+// KV head): the calls with a sliding window, those that keep their scores, the decode
+// over 4-bit pools, and a decode's own keys behind a shared prefix (the last two with
+// more rows too, in segments of 16).
 //
 // Per row r of a (request, KV head) and its visible keys j:
 //   s_rj = c q_r . k_j,  m = max s,  l = sum 2^(s - m),  o = sum 2^(s - m) v_j / l
@@ -15,15 +16,17 @@
 //   * Both sums run over an index whose order is free, so 16 contiguous bytes of
 //     a row are the very words that a lane's instructions want: K with four
 //     lanes a row, V with eight, V's pairs of keys joined by byte permutes.
-//   * Each warp has a ring of its own, two tiles (16 KiB) deep, that it fills by
-//     TMA (whole page slices, 128-byte swizzle) and empties itself: 128 KiB on
-//     their way per SM, across the ends of pieces, and no barrier between the
-//     warps but at the end of a piece. (Copies by the lanes themselves, into
+//   * Each warp has a ring of its own, two tiles (16 KiB) deep or one (Smem), that it
+//     fills by TMA (whole page slices, 128-byte swizzle; 4-bit rows as they are) and
+//     empties itself: 128 KiB on their way per SM, across the ends of pieces, and no
+//     barrier between the warps but at the end of a piece. (Copies by the lanes themselves, into
 //     registers or shared memory, came to 4.1-4.6 TB/s however many were
 //     issued.)
 //   * P is split into two bf16 parts (their sum has 16 bits), so its rounding
 //     does not show next to the output's; the tensor core has the time. e4m3
-//     pages: codes become f16 exactly, P is one f16.
+//     pages: codes become f16 exactly, P is one f16. 4-bit pages: a value is m + s c;
+//     s c becomes an f16 (Q4Step), m goes into the sums by a product of its own with the
+//     query's sums over a group (K) and with P (V).
 //   * The maximum in use moves only when a score exceeds it by 2^8 (P stays
 //     below 2^8, the softmax is the same), so the common step needs one vote
 //     instead of a shuffle tree.
@@ -37,7 +40,10 @@
 // call of a replayed graph): 64 bf16 requests, window 2048, 508 MB in 85 us
 // (6.0 TB/s, of 6.8 measured for a copy); e4m3, 255 MB in 49 us; 32 requests of
 // a window of 1024 in groups of 7, 51 MB in 16 us; one request, window 512, 8.2
-// us, of which the second kernel is about 3.
+// us, of which the second kernel is about 3. 4-bit pools, 8 requests of 16k-32k: 244
+// MB in 69.4 us (3.5 TB/s), bound by instructions: 443 a warp for 16 keys of K and V, of
+// which the codes' conversion costs 14 us; 32 requests of up to 4096 keys 16.2, one of
+// 5001 12.
 #pragma once
 
 #include <cuda.h>
@@ -58,10 +64,10 @@ constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr float kMoveLog2 = 8.f;      // scores may exceed the maximum in use by this much
 constexpr int kPieceUnits = 1;        // a piece's cost beyond its granules
-// Two blocks an SM of two tiles a warp (Smem: not for 4-bit pools, nor behind a prefix). 64 e4m3 requests, window 2048: 49 us, with three
-// blocks 62, with four tiles a warp 75; 8 bf16 requests of 16k-32k: 142, 160 and
-// 189. (Presumably the second kernel's blocks and the next call's then find no
-// room until the last block of this one ends.)
+// Two blocks an SM of two tiles a warp (Smem: not for 4-bit pools, nor behind a prefix). 64
+// e4m3 requests, window 2048: 49 us, with three blocks 62, with four tiles a warp 75; 8 bf16
+// requests of 16k-32k: 142, 160 and 189. (Presumably the second kernel's blocks and the next
+// call's then find no room until the last block of this one ends.)
 // kTok keys per step and warp: 16 rows of 256 bytes, 32 of 128, or of 80 (4-bit rows).
 template <int D, int KIND>
 struct Shape {
@@ -93,7 +99,9 @@ struct Smem {
     static constexpr int kSlabs = kRing + kWarps * kStages * 2 * Sh::kTileBytes;
     static constexpr int kBars = kSlabs + 2 * kSlab;                  // [warp][stage][K, V]
     static constexpr int kMisc = kBars + kWarps * kStages * 2 * 8;
-    static constexpr int kPrefix = kMisc + 16;   // [B + 1] granules before, [B] granules, [B] lengths, kSuffix: [B] firsts, the prefixes' starts and lengths
+    // [B + 1] granules before, [B] granules, [B] lengths; kSuffix: [B] firsts, the prefixes'
+    // starts and lengths
+    static constexpr int kPrefix = kMisc + 16;
     static size_t bytes(int B)
     {
         return kPrefix + size_t(kMode == kSuffix ? 4 * B + 1 + 2 * kMaxPrefixes + 1 : 3 * B + 1) * 4 + 1024;
@@ -665,7 +673,8 @@ __global__ void __launch_bounds__(kThreads, (Smem<D, KIND, NT, kMode>::kBlocksPe
                             const uint32_t A[4] = {s0.low(w0), s1.low(w1), s0.high(w0), s1.high(w1)};
 #pragma unroll
                             for (int nt = 0; nt < NT; ++nt)
-                                mma_f16_16816(j ? odd[s][nt] : sc[s][nt], A, qb[nt][2 * i + j][0], qb[nt][2 * i + j][1]);
+                                mma_f16_16816(j ? odd[s][nt] : sc[s][nt], A, qb[nt][2 * i + j][0],
+                                              qb[nt][2 * i + j][1]);
                         }
                     // the least values, times 32, with the query's sums over 32
                     const uint32_t A[4] = {mul_f16x2(__byte_perm(par[0], 0, 0x3232), 0x50005000u),

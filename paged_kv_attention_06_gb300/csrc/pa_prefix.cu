@@ -195,7 +195,8 @@ struct Step {
     bool first, opens, closes, valid;
 };
 struct StepIter {
-    int i, k, k1, g, sub, done;   // next piece; next tile of this one, its end, of the stream; steps of the tile, of the piece
+    int i, k, k1, g;              // next piece; next tile of this one, its end, of the stream
+    int sub, done;                // steps of the tile, of the piece
     bool pair;
     __device__ __forceinline__ Step next(const Pieces& pieces, int count)
     {

@@ -13,8 +13,8 @@
 //
 // A row of 128 bf16 is 16 lanes of 16 bytes in, 4 bytes of codes a lane out (or the other
 // way round), the group's extremes found among 4 lanes. Measured, both calls together: 4 x
-// 2047 tokens of 8 heads written and 49k rows read back, 108 MB, 27.3 us (4.0 TB/s, of 6.8
-// for a copy); 32 tokens written and 75k rows read back, 101 MB, 23.3; one token and 300
+// 2047 tokens of 8 heads written and 11.8k read back, 108 MB, 27.0 us (4.0 TB/s, of 6.8
+// for a copy); 32 tokens written and 37.6k of 4 heads read back, 101 MB, 23.3; one token and 300
 // rows 5.3. Two kernels of which the second waits for the first: what bounds them is the
 // latency of one pass of loads a block, and the append's instructions (with quotients near
 // a half decided in 64 bits it took 48 us alone, 18 in the fp32 arithmetic below; streamed
@@ -126,7 +126,8 @@ __device__ __forceinline__ uint32_t quantise8(const uint4& x, uint32_t* params)
 }
 
 // Lane group of 16 per (request, KV head, token) row, K then V.
-__global__ void __launch_bounds__(256) append_q4_kernel(const AppendArgs a, const FixedDivisor by_L, const FixedDivisor by_H)
+__global__ void __launch_bounds__(256) append_q4_kernel(const AppendArgs a, const FixedDivisor by_L,
+                                                        const FixedDivisor by_H)
 {
     grid_dependency_wait();
     grid_launch_dependents();
