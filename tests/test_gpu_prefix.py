@@ -173,3 +173,34 @@ def test_refusals():
                  prefix_starts=c["prefix_starts"][:1])
     with pytest.raises(pa.PagedAttentionError):
         call(empty)
+
+
+def _limit(fits, hi=1 << 17):
+    lo = 1
+    while lo < hi:
+        mid = (lo + hi + 1) // 2
+        lo, hi = (mid, hi) if fits(mid) else (lo, mid - 1)
+    return lo
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3", "q4"])
+def test_largest_batches(kind):
+    """The largest batch that has a workspace runs; one more request is refused."""
+    pa = _pa()
+    need = {"bf16": pa.pa_decode_prefix_workspace_bytes, "e4m3": pa.pa_decode_prefix_fp8_workspace_bytes,
+            "q4": pa.pa_decode_prefix_q4_workspace_bytes}[kind]
+    n = _limit(lambda B: need(pa.pa_shape(B, 2, 1, 128, 1, 400, 3), 16, 2, 32) > 0)
+    assert 2000 < n < 100000
+    first, second = n // 2, n // 4
+    lens = [20 + i % 9 for i in range(first)] + [32 + i % 7 for i in range(second)]
+    lens += [i % 20 for i in range(n - len(lens))]
+    c = make([(20, first), (32, second)], lens, 2, 1, 1, 128, 16, seed=3, pool=kind, poison=False)
+    out = call(c, kind, max_context_len=48)
+    check_no_device_error()
+    some = torch.cat([torch.arange(8), first + torch.arange(8), n - 8 + torch.arange(8)]).cuda()
+    part = dict(c, **{k: c[k][some] for k in ("query", "block_table", "context_lens")},
+                prefix_starts=torch.tensor([0, 8, 16], dtype=torch.int32, device="cuda"))
+    check(out[some], reference(part, kind), kind, 48, 10.0)
+    more = dict(c, **{k: torch.cat([c[k], c[k][-1:]]) for k in ("query", "block_table", "context_lens")})
+    with pytest.raises(pa.PagedAttentionError):
+        call(more, kind)

@@ -336,3 +336,24 @@ def test_empty_calls():
     kd, vd = pa.pa_gather_kv_q4(kp, vp, torch.zeros(0, 1, dtype=torch.int32, device="cuda"),
                                 torch.zeros(0, dtype=torch.int32, device="cuda"), 16, 5)
     assert kd.shape == (0, 2, 5, D) == vd.shape
+
+
+def test_largest_batch():
+    """The largest batch that has a workspace runs; one more request is refused."""
+    pa = _pa()
+    fits = lambda B: pa.pa_decode_q4_workspace_bytes(pa.pa_shape(B, 2, 1, D, 1, 400, 3)) > 0  # noqa: E731
+    lo, hi = 1, 1 << 17
+    while lo < hi:
+        mid = (lo + hi + 1) // 2
+        lo, hi = (mid, hi) if fits(mid) else (lo, mid - 1)
+    assert 2000 < lo < 100000
+    lens = [i % 37 for i in range(lo)]
+    c = make(lens, 2, 1, 1, 16, seed=11, poison=False)
+    out = pa.pa_attention_q4(**c, max_context_len=36)
+    check_no_device_error()
+    some = torch.cat([torch.arange(40), lo - 40 + torch.arange(40)]).cuda()
+    part = dict(c, **{k: c[k][some] for k in ("query", "block_table", "context_lens")})
+    check_out(out[some], reference(part), True, 36)
+    more = dict(c, **{k: torch.cat([c[k], c[k][-1:]]) for k in ("query", "block_table", "context_lens")})
+    with pytest.raises(pa.PagedAttentionError):
+        pa.pa_attention_q4(**more, max_context_len=36)
