@@ -638,6 +638,11 @@ __global__ void __launch_bounds__((Layout<D, KIND>::kThreads), 1)
                     else if (i + 1 < count)
                         next = page_at(i + 1, pieces[i + 1].k0);
                     const int st = g & 1;
+                    // The first keys are here before the first values are asked for: every block
+                    // starts at once, and the scores need the keys (32 requests behind 16384
+                    // keys 32.8 -> 32.2 us; the second keys held back too: 32.5).
+                    if (is_v && g == 0)
+                        mbar_wait_warp(&bar[kKFull], 0, misc, a.err);
                     const bool ok = mbar_wait_warp(&bar[empty + st], ((g >> 1) & 1) ^ 1u, misc, a.err);
                     if (ok) {
                         if (lane == 0)
