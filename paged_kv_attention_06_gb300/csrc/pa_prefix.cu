@@ -33,8 +33,8 @@
 //     2^-9 of a term, averages out below the output's own rounding), the states.
 // TMEM (512 columns): S_0, S_1, O_0, O_1 (128 each).
 //
-// Measured, a call (three kernels): 8 bf16 requests behind 2048 keys 14.4 us; 32 in groups
-// of 7 behind 16384 keys 32.7 (57 MB; each request over its own table: 1.1 GB); 64 e4m3
+// Measured, a call (three kernels): 8 bf16 requests behind 2048 keys 14.6 us; 32 in groups
+// of 7 behind 16384 keys 32.2 (57 MB; each request over its own table: 1.1 GB); 64 e4m3
 // requests behind 3 prefixes, 31000 keys in all, 56 (140 MB); 16 chunks of 4 rows behind 8192
 // 4-bit keys 39. What bounds them: a chain of three kernels, 2 us from one to the next, and
 // in each what a block does once (about 2 us to its pieces, 2 to its rows, 1.5 for the
