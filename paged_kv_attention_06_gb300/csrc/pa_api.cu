@@ -1961,9 +1961,9 @@ pa_status pa_attention_q4(const void* query, const void* key_pages, const void* 
 
 namespace {
 
-// A decode behind shared prefixes: whether the prefixes are attended to on copies (pools
-// that the prefix kernel cannot read by TMA, and those that are not bf16), and the
-// workspace: copies with their table, the prefixes' states, the few-row kernel's.
+// A decode behind shared prefixes: whether the prefixes are attended to on copies (bf16
+// pages too small for the prefix kernel's TMA boxes), and the workspace: copies with their
+// table, the prefixes' states, the notes for the merge, the few-row kernel's states.
 struct PrefixPlan {
     bool copies = false;
     int64_t P2 = 0;
