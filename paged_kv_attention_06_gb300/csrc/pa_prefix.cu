@@ -93,7 +93,7 @@ struct Layout {
     static constexpr int kV = kK + 2 * kMat;
     static constexpr int kCodeRing = kV + kVStages * kMat;   // [slot][key][row bytes]
     static constexpr int kBar = kCodeRing + (kCodes ? kRing * kCodeTile : 0);
-    static constexpr int kNumBars = 16 + (kCodes ? 2 * kRing : 0);
+    static constexpr int kNumBars = 16 + (kCodes ? 2 * kRing : 1);
     static constexpr int kTmemSlot = kBar + kNumBars * 8;
     static constexpr int kMisc = kTmemSlot + 16;
     static constexpr int kSlotInfo = kMisc + 16;        // [slot] (tile and matrix, keys)
@@ -110,6 +110,7 @@ constexpr int kVEmpty = 8;
 constexpr int kSFull = 10;    // + half (2)
 constexpr int kPFull = 12;    // + half
 constexpr int kPVDone = 14;   // + half
+constexpr int kFirstKeys = 16;   // bf16 pools: arrived at once
 constexpr int kCodeFull = 16; // + slot (kRing)
 constexpr int kCodeEmpty = kCodeFull + kRing;
 
@@ -339,6 +340,8 @@ __global__ void __launch_bounds__((Layout<D, KIND>::kThreads), 1)
             mbar_init(&bar[kCodeFull + i], 1);
             mbar_init(&bar[kCodeEmpty + i], kConverters);
         }
+        if (!kCodes)
+            mbar_init(&bar[kFirstKeys], 1);
         fence_barrier_init();
     }
     if (warp == 1) {
@@ -625,6 +628,17 @@ __global__ void __launch_bounds__((Layout<D, KIND>::kThreads), 1)
                 return lane * box < kKeys && key0 < pieces[i].len
                            ? __ldg(a.prefix.table + int64_t(pieces[i].p) * a.prefix.pages + (key0 >> a.ps_shift)) : 0;
             };
+            // The first keys are here before the first values are asked for: every block starts at
+            // once, and the scores need the keys (32 requests behind 16384 keys 32.8 -> 32.2 us; the
+            // second keys held back too: 32.5). Warp 0 says so, on a barrier that completes
+            // once: it refills the keys' stage itself, so it sees that stage's first phase.
+            // Warp 2 there could come two phases late, when the parity is the same again,
+            // and the keys would wait for products that wait for its values.
+            auto first_keys = [&]() {
+                mbar_wait_warp(&bar[kKFull], 0, misc, a.err);
+                if (lane == 0)
+                    mbar_arrive(&bar[kFirstKeys]);
+            };
             int g = 0, next = page_at(0, pieces[0].k0);
             for (int i = 0; i < count; ++i) {
                 const int n = pieces[i].len, k1 = pieces[i].k1, head = pieces[i].h;
@@ -638,11 +652,10 @@ __global__ void __launch_bounds__((Layout<D, KIND>::kThreads), 1)
                     else if (i + 1 < count)
                         next = page_at(i + 1, pieces[i + 1].k0);
                     const int st = g & 1;
-                    // The first keys are here before the first values are asked for: every block
-                    // starts at once, and the scores need the keys (32 requests behind 16384
-                    // keys 32.8 -> 32.2 us; the second keys held back too: 32.5).
                     if (is_v && g == 0)
-                        mbar_wait_warp(&bar[kKFull], 0, misc, a.err);
+                        mbar_wait_warp(&bar[kFirstKeys], 0, misc, a.err);
+                    if (!is_v && g == 2)             // both stages asked for
+                        first_keys();
                     const bool ok = mbar_wait_warp(&bar[empty + st], ((g >> 1) & 1) ^ 1u, misc, a.err);
                     if (ok) {
                         if (lane == 0)
@@ -663,6 +676,8 @@ __global__ void __launch_bounds__((Layout<D, KIND>::kThreads), 1)
                     __syncwarp();
                 }
             }
+            if (!is_v && g <= 2)
+                first_keys();
             // No copy may still be landing when the block exits.
 #pragma unroll 1
             for (int i = max(0, g - 2); i < g; ++i)
