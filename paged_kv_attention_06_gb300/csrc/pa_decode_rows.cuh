@@ -150,6 +150,13 @@ __device__ __forceinline__ TileSpan tile_span(const DecodeArgs& a, int n, int fi
     return s;
 }
 
+// What lies at p, behind a prefix past the first cache (see the kernel's start).
+template <int kMode, typename T>
+__device__ __forceinline__ T now(const T* p)
+{
+    return kMode == kSuffix ? __ldcg(p) : *p;
+}
+
 template <int kMode>
 __device__ __forceinline__ int context_cap(const DecodeArgs& a)
 {
@@ -368,8 +375,13 @@ __global__ void __launch_bounds__(kThreads, (Smem<D, KIND, NT, kMode>::kBlocksPe
         fence_barrier_init();
     }
     // Behind a prefix the kernel before this one in the stream is the prefix's, of
-    // which nothing is read here; it let this one start when what it waited for was
-    // complete. (The wait for it is at the end.)
+    // which nothing is read here; the wait for it is at the end. What this kernel reads
+    // was written before that one, each of whose blocks lets this one start only after
+    // its own wait: by then every write before it has been performed in the device's memory.
+    // It is read from there: lengths, tables and queries by loads that pass the first
+    // cache by, which may hold older lines (`now`), K and V by TMA. (With the wait here
+    // instead, us: 8 requests behind 2048 keys 20.3 for 15.1, 32 behind 16384 35.5 for
+    // 32.4, 64 e4m3 requests 64.2 for 56.1.)
     if constexpr (kMode != kSuffix)
         grid_dependency_wait();
     grid_launch_dependents();
@@ -377,11 +389,11 @@ __global__ void __launch_bounds__(kThreads, (Smem<D, KIND, NT, kMode>::kBlocksPe
     // ---- this block's granules [x_begin, x_end) -------------------------------
     // (A thread a request: one warp, with the prefixes' tables in global memory, took 1 to 2
     // us more.)
-    int n = int(threadIdx.x) < a.B ? a.context_lens[threadIdx.x] : 0;
+    int n = int(threadIdx.x) < a.B ? now<kMode>(a.context_lens + threadIdx.x) : 0;
     if constexpr (kMode == kSuffix) {
 #pragma unroll 1
         for (int p = threadIdx.x; p <= a.prefix.count; p += kThreads) {
-            prefix_starts[p] = __ldg(a.prefix.starts + p);
+            prefix_starts[p] = __ldcg(a.prefix.starts + p);
             if (p < a.prefix.count)
                 prefix_lens[p] = prefix_len(a.prefix, p);
         }
@@ -390,7 +402,7 @@ __global__ void __launch_bounds__(kThreads, (Smem<D, KIND, NT, kMode>::kBlocksPe
 #pragma unroll 1
     for (int b = threadIdx.x; b < a.B; b += kThreads) {
         if (b >= kThreads)
-            n = a.context_lens[b];
+            n = now<kMode>(a.context_lens + b);
         n = clamp_context(n, cap, a.err);
         int first = 0;
         if constexpr (kMode == kSuffix) {
@@ -470,7 +482,8 @@ __global__ void __launch_bounds__(kThreads, (Smem<D, KIND, NT, kMode>::kBlocksPe
         return live ? t : -1;
     };
     auto page_of = [&](const Place& p, int t) {
-        return t < 0 ? 0 : __ldg(a.block_table + int64_t(p.sp.b) * a.max_pages + (t >> a.ps_shift));
+        const int32_t* entry = a.block_table + int64_t(p.sp.b) * a.max_pages + (t >> a.ps_shift);
+        return t < 0 ? 0 : kMode == kSuffix ? __ldcg(entry) : __ldg(entry);
     };
     auto row_of = [&](const Place& p, int t, int phys) {
         if (t < 0)
@@ -563,7 +576,7 @@ __global__ void __launch_bounds__(kThreads, (Smem<D, KIND, NT, kMode>::kBlocksPe
                 for (int i = 0; i < 4; ++i) {
                     uint4 w = make_uint4(0, 0, 0, 0);
                     if (r < rows)
-                        w = *reinterpret_cast<const uint4*>(src + 64 * q + 16 * i);
+                        w = now<kMode>(reinterpret_cast<const uint4*>(src + 64 * q + 16 * i));
                     const uint32_t x = bf16x2_to_f16x2(w.x), y = bf16x2_to_f16x2(w.y);
                     const uint32_t z = bf16x2_to_f16x2(w.z), u = bf16x2_to_f16x2(w.w);
                     qb[nt][2 * i][0] = __byte_perm(x, z, 0x5410);
@@ -580,8 +593,8 @@ __global__ void __launch_bounds__(kThreads, (Smem<D, KIND, NT, kMode>::kBlocksPe
                 for (int j = 0; j < D / 64; ++j) {
                     uint4 w[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
                     if (r < rows) {
-                        w[0] = *reinterpret_cast<const uint4*>(src + 128 * j + 32 * q);
-                        w[1] = *reinterpret_cast<const uint4*>(src + 128 * j + 32 * q + 16);
+                        w[0] = now<kMode>(reinterpret_cast<const uint4*>(src + 128 * j + 32 * q));
+                        w[1] = now<kMode>(reinterpret_cast<const uint4*>(src + 128 * j + 32 * q + 16));
                     }
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
@@ -594,7 +607,7 @@ __global__ void __launch_bounds__(kThreads, (Smem<D, KIND, NT, kMode>::kBlocksPe
                 for (int j = 0; j < kKL; ++j) {
                     uint4 w = make_uint4(0, 0, 0, 0);
                     if (r < rows)
-                        w = *reinterpret_cast<const uint4*>(src + 64 * j + 16 * q);
+                        w = now<kMode>(reinterpret_cast<const uint4*>(src + 64 * j + 16 * q));
                     qb[nt][2 * j][0] = w.x;
                     qb[nt][2 * j][1] = w.y;
                     qb[nt][2 * j + 1][0] = w.z;

@@ -8,7 +8,7 @@ namespace pa {
 
 __device__ __forceinline__ int prefix_len(const PrefixArgs& x, int p)
 {
-    const int n = __ldg(x.lens + p);
+    const int n = __ldcg(x.lens + p);
     return n < 0 ? 0 : n > x.cap ? x.cap : n;
 }
 
