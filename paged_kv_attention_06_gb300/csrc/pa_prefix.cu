@@ -1088,7 +1088,8 @@ __global__ void __launch_bounds__(kMergeThreads, 4) prefix_merge_kernel(const Pr
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1)
             m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-        // nothing seen: the state was not written, and counts for nothing
+        // nothing seen: the state was not written, and counts for nothing (scores that are
+        // all NaN have no largest either: their sum is NaN, and makes this one NaN)
         const float w = ml.x == -INFINITY ? 0.f : fast_exp2(ml.x - m);
         const float old = top == -INFINITY ? 0.f : fast_exp2(top - m);
         float add = w * ml.y;
@@ -1148,7 +1149,7 @@ __global__ void __launch_bounds__(kMergeThreads, 4) prefix_merge_kernel(const Pr
         }
     }
     if (live) {
-        const float inv = sum > 0.f ? a.out_scale / sum : 0.f;
+        const float inv = sum == 0.f ? 0.f : a.out_scale / sum;     // NaN stays
         uint16_t* dst = a.out + ((int64_t(b) * k.H_q + h * k.G) * k.L + x) * D;
         if constexpr (D == 128)
             reinterpret_cast<uint2*>(dst)[lane] =
