@@ -601,7 +601,10 @@ pa_status pa_kv_evict_fp8(void *key_pages, void *value_pages, float *weight_page
  * scales follow the data, so none are passed). head_dim 128 only. A pool is
  * [P, H_kv, page_size, 80] bytes; a row's first 64 bytes are its codes (element d in
  * byte d / 2, even d in the low half), then for each group of 32 elements its step s and
- * its least value m as f16: s0 m0 s1 m1 s2 m2 s3 m3. A code c stands for m + s c.
+ * its least value m as f16: s0 m0 s1 m1 s2 m2 s3 m3. A code c stands for m + s c. Rows that
+ * another writer puts into a pool have to keep to what pa_append_kv_q4 can write, s in 0 ..
+ * 60 and m in -448 .. 448 (or both NaN): the attention calls form 1024 s and 32 m in f16, and
+ * give NaN where those do not fit. pa_gather_kv_q4 reads back any s and m.
  */
 
 /*

@@ -487,8 +487,8 @@ def pa_append_kv_q4(key: torch.Tensor, value: torch.Tensor, key_pages: torch.Ten
                     value_pages: torch.Tensor, slot_mapping: torch.Tensor, page_size: int,
                     stream=None) -> None:
     """key/value [B, H_kv, L_new, 128] bf16 -> uint8 4-bit pages [P, H_kv,
-    page_size, 80] at slot_mapping [B, L_new]: codes of 4 bits, and a step and a
-    least value as f16 for every 32 elements."""
+    page_size, 80] at slot_mapping [B, L_new]: codes of 4 bits, and a step (0 .. 60)
+    and a least value (-448 .. 448) as f16 for every 32 elements."""
     _calls.append_q4(key, value, key_pages, value_pages, slot_mapping, page_size, _raw(stream))
 
 
@@ -526,7 +526,8 @@ def pa_decode_q4(query: torch.Tensor, key_pages: torch.Tensor, value_pages: torc
                  scale: Optional[float] = None, causal: bool = True,
                  out: Optional[torch.Tensor] = None, max_context_len: int = 0,
                  workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
-    """pa_decode over uint8 4-bit pools [P, H_kv, page_size, 80]."""
+    """pa_decode over uint8 4-bit pools [P, H_kv, page_size, 80], of rows with the
+    steps and least values that pa_append_kv_q4 writes."""
     return _calls.attention_q4(0, query, key_pages, value_pages, block_table, context_lens, page_size,
                                scale, causal, out, max_context_len, workspace, _raw(stream))
 
@@ -536,8 +537,8 @@ def pa_prefill_q4(query, key_pages, value_pages, block_table, context_lens, page
                   max_context_len: Optional[int] = None,
                   workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """Tensor-core prefill over uint8 4-bit pools. max_context_len bounds
-    context_lens and sizes the bf16 copy in the workspace; None reads
-    context_lens.max() (a device-to-host copy)."""
+    context_lens and sizes the copies in the workspace (keys in bf16, values in
+    f16); None reads context_lens.max() (a device-to-host copy)."""
     if max_context_len is None:
         max_context_len = int(context_lens.max().item())
     return _calls.attention_q4(1, query, key_pages, value_pages, block_table, context_lens, page_size,

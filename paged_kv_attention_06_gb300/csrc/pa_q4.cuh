@@ -11,8 +11,8 @@ namespace pa {
 constexpr int kQ4RowBytes = 80;
 constexpr int kQ4CodeBytes = 64;
 constexpr int kQ4Group = 32;
-// Magnitudes are cut to e4m3's largest, so that 1024 s is an f16 (a decode kernel
-// turns codes into f16 by it).
+// Magnitudes are cut to e4m3's largest, so that 1024 s and 32 m are f16 (a decode kernel
+// turns codes into f16 by the one, and adds the least values up by the other).
 constexpr float kQ4Max = 448.f;
 
 }  // namespace pa
