@@ -29,15 +29,8 @@ __device__ __forceinline__ int prefix_of(const int* starts, int count, int b)
     return lo;
 }
 
-// The few-row kernel behind a prefix: granules (four tiles of tile_keys) of the keys
-// first .. n - 1, from the box that holds the first; and the blocks that share units of
-// work, two units a block at least.
-__device__ __forceinline__ int suffix_granules(int n, int first, int box_rows, int tile_keys)
-{
-    const int start = first < n ? first & ~(box_rows - 1) : n;
-    const int tiles = (n - start + tile_keys - 1) / tile_keys;
-    return max(1, (tiles + 3) / 4);
-}
+// The blocks of the few-row kernel behind a prefix that share units of work, two units a
+// block at least.
 __device__ __forceinline__ int64_t suffix_blocks(int64_t units, int grid)
 {
     const int64_t most = (units + 1) / 2;
