@@ -369,8 +369,10 @@ __global__ void __launch_bounds__(kThreads, (Smem<D, KIND, NT, kMode>::kBlocksPe
             mbar_init(&bars[i], 1);
         if (warp == 0) {
             misc[0] = 0;                              // a wait ran out
-            prefetch_tensormap(&key_map);
-            prefetch_tensormap(&value_map);
+            if constexpr (!Q4) {                      // (4-bit rows come without maps)
+                prefetch_tensormap(&key_map);
+                prefetch_tensormap(&value_map);
+            }
         }
         fence_barrier_init();
     }
