@@ -693,7 +693,11 @@ pa_status pa_attention_q4(const void *query, const void *key_pages, const void *
  *   block_table    entries of pages that lie wholly before a request's prefix_len are
  *                  not read and may hold anything.
  *   context_lens   positions in all, prefix included; a request may be shorter than its
- *                  prefix (or empty): its rows see what they see.
+ *                  prefix (or empty): its rows see what they see. (The prefix's values
+ *                  go through the products for all its rows, with weights of 0 for
+ *                  those that do not see them: an infinity or NaN among the values
+ *                  makes NaN of rows that end before it too. Keys that a row does not
+ *                  see may hold anything.)
  *   num_prefixes   1 .. 256;  max_prefix_len > 0 bounds prefix_lens and sizes the
  *                  workspace.
  *   workspace      ..._workspace_bytes(shape, page_size, num_prefixes, max_prefix_len)

@@ -58,3 +58,19 @@ def test_keys_of_nan(many):
     out = call(c)
     check_no_device_error()
     check_but(out, ref, nan, "bf16", max(lens))
+
+
+def test_keys_behind_a_shorter_request():
+    """A key of NaN in the prefix makes NaN of the rows that see it; requests, and rows of a
+    chunk, that end before it are as they would be without."""
+    lens = [260, 251, 250, 249, 100, 1, 0, 400]
+    c = make([(260, 8)], lens, 8, 2, 2, 128, 16, seed=4)
+    ref = reference(c)
+    c["key_pages"][c["prefix_table"][0, 250 // 16].item(), :, 250 % 16] = NAN
+    nan = torch.zeros(8, 8, 2, dtype=torch.bool, device="cuda")
+    for b, n in enumerate(lens):
+        for i in range(2):
+            nan[b, :, i] = n - 2 + i >= 250
+    out = call(c)
+    check_no_device_error()
+    check_but(out, ref, nan, "bf16", max(lens))
