@@ -796,8 +796,10 @@ struct Fp8PrefillPlan {
 pa_status plan_prefill_fp8(const pa_shape& s, int32_t max_context_len, DeviceInfo* dev,
                            Fp8PrefillPlan* p)
 {
-    if (max_context_len < 0 || s.batch <= 0 || s.num_kv_heads <= 0 || s.num_q_heads <= 0)
+    if (max_context_len < 0 || s.batch <= 0 || s.num_kv_heads <= 0 || s.num_q_heads <= 0 || s.q_len <= 0)
         return PA_ERR_INVALID_ARG;
+    if (s.num_q_heads % s.num_kv_heads != 0)
+        return PA_ERR_UNSUPPORTED;
     p->P2 = fp8_copy_pages(max_context_len);
     const int64_t pages = int64_t(s.batch) * p->P2;
     if (pages * s.num_kv_heads * 128 >= (int64_t(1) << 31) || p->P2 * 128 >= (int64_t(1) << 30))

@@ -132,3 +132,20 @@ def test_host_threads():
     for (kind, c), got in zip(cases, outs):
         check(got[0], reference(c, kind), kind, 800, 10.0)
         assert all(torch.equal(got[0], x) for x in got)
+
+
+def test_workspace_of_refused_sizes_is_zero():
+    import paged_kv_attention_06_gb300 as pa
+    good = dict(batch=2, num_q_heads=4, num_kv_heads=2, head_dim=128, q_len=4, num_pages=64, max_pages=8)
+
+    def sizes_of(**other):
+        shape = pa.pa_shape(*(dict(good, **other)[f] for f, *_ in pa.pa_shape._fields_))
+        return (pa.pa_decode_q4_workspace_bytes(shape), pa.pa_prefill_q4_workspace_bytes(shape, 100),
+                pa.pa_attention_q4_workspace_bytes(shape, 100),
+                pa.pa_decode_prefix_q4_workspace_bytes(shape, 16, 1, 100))
+
+    assert all(sizes_of())
+    for L in (4, 300):
+        for bad in (dict(num_q_heads=5), dict(num_q_heads=0), dict(num_kv_heads=0), dict(num_q_heads=-4),
+                    dict(q_len=0), dict(q_len=-3), dict(batch=0), dict(head_dim=64)):
+            assert not any(sizes_of(**dict(dict(q_len=L), **bad))), bad
