@@ -1844,6 +1844,16 @@ int64_t rows_granules(const pa_shape& s, int kind, int64_t keys)
     return int64_t(s.batch) * s.num_kv_heads * MS * std::max<int64_t>(1, (keys + tile - 1) / tile);
 }
 
+// Whether there are at most kMaxSegments segments, and the granules of the longest contexts
+// that the tables have room for can be counted in 32 bits, as the few-row kernel does.
+bool rows_count_ok(const pa_shape& s, int kind, int32_t page_size)
+{
+    const int64_t bh = int64_t(s.batch) * s.num_kv_heads;
+    const int64_t MS = (int64_t(s.num_q_heads / s.num_kv_heads) * s.q_len + kSegmentRows - 1) / kSegmentRows;
+    return bh <= kMaxSegments && bh * MS <= kMaxSegments &&
+           rows_granules(s, kind, int64_t(s.max_pages) * page_size) < (int64_t(1) << 31);
+}
+
 bool rows_shape_ok(const pa_shape& s)
 {
     return s.batch > 0 && s.num_q_heads > 0 && s.num_kv_heads > 0 && s.q_len > 0 &&
@@ -1871,7 +1881,7 @@ pa_status pa_decode_q4(const void* query, const void* key_pages, const void* val
                                    page_size, scale, out, shape);
     if (st != PA_OK)
         return st;
-    if (shape.head_dim != 128 || !rows_shape_ok(shape))
+    if (shape.head_dim != 128 || !rows_shape_ok(shape) || !rows_count_ok(shape, kQ4Pool, page_size))
         return PA_ERR_UNSUPPORTED;
     DeviceInfo* dev;
     if ((st = device_info(&dev)) != PA_OK)
@@ -2040,7 +2050,8 @@ pa_status run_decode_prefix(const void* query, const void* key_pages, const void
     if (!prefix_table || !prefix_lens || !prefix_starts || prefix_pages <= 0 ||
         (kind == kE4m3Pool && bad_scales(k_scale, v_scale)))
         return PA_ERR_INVALID_ARG;
-    if (int64_t(prefix_pages) * page_size >= (int64_t(1) << 30))
+    if (int64_t(prefix_pages) * page_size >= (int64_t(1) << 30) || !rows_shape_ok(shape) ||
+        !rows_count_ok(shape, kind, page_size))
         return PA_ERR_UNSUPPORTED;
     DeviceInfo* dev;
     if ((st = device_info(&dev)) != PA_OK)
