@@ -679,7 +679,10 @@ pa_status pa_attention_q4(const void *query, const void *key_pages, const void *
  * all of them: what pa_decode gives (causal) where request b's positions before
  * prefix_lens[p] lie in prefix p's pages. The rows of all requests of a prefix go through
  * the tensor cores together, so its K and V are read once per 256 of their rows; the
- * few-row kernel reads each request's own keys, and a merge joins the two.
+ * few-row kernel reads each request's own keys, and a merge joins the two. (Tables that
+ * name the same pages are legal in pa_decode too, and short prefixes then lie in L2: up to
+ * about 16000 positions, prefix length times its requests, over all prefixes, that call
+ * takes as long or less; from about 32000 this one does.)
  *   prefix_table   [num_prefixes, prefix_pages] int32, the pages of each prefix.
  *   prefix_lens    [num_prefixes] int32, tokens, 0 .. min(prefix_pages * page_size,
  *                  max_prefix_len) (a longer one records PA_DEVERR_CONTEXT_LEN and

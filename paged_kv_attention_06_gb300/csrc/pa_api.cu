@@ -1672,7 +1672,7 @@ pa_status pa_gather_kv(const void* key_pages, const void* value_pages, const int
 namespace {
 
 // Checks of a read-back's sizes.
-pa_status check_q4_pools(const pa_shape& s, int32_t page_size)
+pa_status check_gather_q4(const pa_shape& s, int32_t page_size)
 {
     if (s.batch <= 0 || s.num_kv_heads <= 0 || s.num_pages <= 0 || s.max_pages <= 0 || s.head_dim <= 0)
         return PA_ERR_INVALID_ARG;
@@ -1756,7 +1756,7 @@ pa_status pa_gather_kv_q4(const void* key_pages, const void* value_pages,
     if (!aligned16(key_pages) || !aligned16(value_pages) || !aligned16(key_dense) ||
         !aligned16(value_dense))
         return PA_ERR_INVALID_ARG;
-    pa_status st = check_q4_pools(shape, page_size);
+    pa_status st = check_gather_q4(shape, page_size);
     if (st != PA_OK)
         return st;
     if (int64_t(shape.batch) * shape.num_kv_heads * ((int64_t(dense_len) + 127) / 128) >=
@@ -1770,7 +1770,7 @@ pa_status pa_gather_kv_q4(const void* key_pages, const void* value_pages,
     a.value_out = static_cast<uint16_t*>(value_dense);
     a.head_stride = int64_t(dense_len) * 128;
     a.batch_stride = a.head_stride * shape.num_kv_heads;
-    a.block_stride = int64_t(kQ4CopyRows) * 128;
+    a.block_stride = int64_t(kCopyPageRows) * 128;
     a.max_len = dense_len;
     return launch_read_pages(a, kQ4Pool, 128, static_cast<cudaStream_t>(stream)) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
@@ -1789,18 +1789,14 @@ pa_status copy_pages(const void* key_pages, const void* value_pages, const int32
     a.key_out = reinterpret_cast<uint16_t*>(w);
     a.value_out = reinterpret_cast<uint16_t*>(w + kv_bytes);
     a.table_out = reinterpret_cast<int32_t*>(w + table_off);
-    a.head_stride = int64_t(kQ4CopyRows) * s.head_dim;
+    a.head_stride = int64_t(kCopyPageRows) * s.head_dim;
     a.block_stride = a.head_stride * s.num_kv_heads;
     a.batch_stride = a.block_stride * P2;
-    a.max_len = int32_t(P2 * kQ4CopyRows);
+    a.max_len = int32_t(P2 * kCopyPageRows);
     a.copy_pages = int32_t(P2);
     a.f16_values = kind == kQ4Pool;
     return launch_read_pages(a, kind, s.head_dim, stream) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
-
-}  // namespace
-
-namespace {
 
 // What the few-row kernel takes of a call (no tensor maps, no outputs of its modes).
 DecodeArgs rows_args(const void* query, const int32_t* block_table, const int32_t* context_lens,
@@ -1943,7 +1939,11 @@ pa_status pa_prefill_q4(const void* query, const void* key_pages, const void* va
 namespace {
 
 // Route of pa_attention_q4: the few-row kernel reads K and V once per 16 rows of a
-// (request, KV head), the prefill copies them first.
+// (request, KV head), the prefill copies them first. With 1, 4, 7 and 8 query heads a KV
+// head, us: 16 requests of 1000-4000 keys, L = 8: few rows 21, 45, 44, 80, prefill 75, 96,
+// 82, 147; 4 of 8000-16000: 25, 52, 51, 90 and 190, 137, 117, 204. (At L = 9 to 16 few rows
+// are still ahead, or level: 28, 80, 71, 148 at 16. The limit is pa_attention_fp8's, so that a
+// chunk goes the same way over either pool.)
 int32_t route_q4(const pa_shape& shape) { return shape.q_len <= 0 ? -1 : shape.q_len <= 8 ? 0 : 1; }
 
 }  // namespace
@@ -2000,16 +2000,17 @@ pa_status plan_prefix(const pa_shape& s, int32_t page_size, int kind, int32_t co
         prefix_smem_bytes(s.head_dim, kind, count) > size_t(dev->max_smem_optin))
         return PA_ERR_UNSUPPORTED;
     p->copies = kind == kBf16Pool && page_size < 8;
-    p->P2 = (int64_t(max_prefix_len) + kQ4CopyRows - 1) / kQ4CopyRows;
+    p->P2 = (int64_t(max_prefix_len) + kCopyPageRows - 1) / kCopyPageRows;
     if (p->copies) {
         const int64_t pages = count * p->P2;
-        if (pages * s.num_kv_heads * kQ4CopyRows >= (int64_t(1) << 31))
+        if (pages * s.num_kv_heads * kCopyPageRows >= (int64_t(1) << 31))
             return PA_ERR_UNSUPPORTED;
-        p->kv_bytes = size_t(pages) * s.num_kv_heads * kQ4CopyRows * s.head_dim * 2;
+        p->kv_bytes = size_t(pages) * s.num_kv_heads * kCopyPageRows * s.head_dim * 2;
         p->table_off = 2 * p->kv_bytes;
         p->state_off = (p->table_off + size_t(pages) * 4 + 255) & ~size_t(255);
     }
-    // blocks: one an SM, two tiles each at least
+    // at most a block an SM and a block a tile (Ranges leaves some without work where items
+    // are few and short)
     const int64_t items = s.num_kv_heads * (s.batch * R / 256 + count);
     p->prefix_grid = int(std::min<int64_t>(dev->sm_count, items * p->P2));
     if (items * prefix_item_units(p->P2) >= (int64_t(1) << 31))   // units are 32-bit numbers
@@ -2100,7 +2101,7 @@ pa_status run_decode_prefix(const void* query, const void* key_pages, const void
         vp = w + p.kv_bytes;
         a.prefix.table = reinterpret_cast<const int32_t*>(w + p.table_off);
         a.prefix.pages = int32_t(p.P2);
-        a.ps = kQ4CopyRows;
+        a.ps = kCopyPageRows;
         a.num_pages = pool.num_pages = int32_t(num_prefixes * p.P2);
     }
     a.box_rows = std::min(a.ps, 128);

@@ -18,10 +18,11 @@
 //     lanes a row, V with eight, V's pairs of keys joined by byte permutes.
 //   * Each warp has a ring of its own, two tiles (16 KiB) deep or one (Smem), that it
 //     fills by TMA (whole page slices, 128-byte swizzle; 4-bit rows as they are) and
-//     empties itself: 128 KiB on their way per SM, across the ends of pieces, and no
-//     barrier between the warps but at the end of a piece. (Copies by the lanes themselves, into
-//     registers or shared memory, came to 4.1-4.6 TB/s however many were
-//     issued.)
+//     empties itself, across the ends of pieces, and no barrier between the warps but
+//     at the end of a piece. On their way per SM: 128 KiB with a window or scores; 96
+//     behind a prefix (up to 8 rows; 128 beyond); 60 of 4-bit rows (40). (Copies by the
+//     lanes themselves, into registers or shared memory, came to 4.1-4.6 TB/s however
+//     many were issued.)
 //   * P is split into two bf16 parts (their sum has 16 bits), so its rounding
 //     does not show next to the output's; the tensor core has the time. e4m3
 //     pages: codes become f16 exactly, P is one f16. 4-bit pages: a value is m + s c;
@@ -37,13 +38,15 @@
 //     in their order.
 //
 // Bound by memory: every K and V byte that a row sees is read once. Measured (one
-// call of a replayed graph): 64 bf16 requests, window 2048, 508 MB in 85 us
-// (6.0 TB/s, of 6.8 measured for a copy); e4m3, 255 MB in 49 us; 32 requests of
+// call of a replayed graph): 64 bf16 requests, window 2048, 508 MB in 82 us
+// (6.2 TB/s, of 6.7 measured for a copy); e4m3, 255 MB in 47 us; 32 requests of
 // a window of 1024 in groups of 7, 51 MB in 16 us; one request, window 512, 8.2
-// us, of which the second kernel is about 3. 4-bit pools, 8 requests of 16k-32k: 244
-// MB in 69.4 us (3.5 TB/s), bound by instructions: 443 a warp for 16 keys of K and V, of
-// which the codes' conversion costs 14 us; 32 requests of up to 4096 keys 16.2, one of
-// 5001 12.
+// us, of which the second kernel is about 3.
+// 4-bit pools are not: 8 requests of 16k-32k, 244 MB, take 69 us (3.5 TB/s, DRAM at 45 %,
+// issue slots at 55 %, tensor pipe at 18 %; e4m3 pools of the same batch 78). A warp's
+// tile is one chain of wait, conversion, product, softmax, conversion, product (443
+// instructions for 16 keys of K and V), and 12 warps an SM are too few to cover it;
+// without any conversion 56 us are left. 32 requests of up to 4096 keys 16, one of 5001 12.
 #pragma once
 
 #include <cuda.h>

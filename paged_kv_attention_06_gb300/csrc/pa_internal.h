@@ -136,7 +136,7 @@ cudaError_t launch_gather(const GatherArgs& a, cudaStream_t stream);
 // KV head h) goes to element b * batch_stride + h * head_stride + (t / 128) * block_stride
 // + (t % 128) * D: dense rows, or pages of 128 tokens with a table (table_out
 // [B, copy_pages], page b * copy_pages + t / 128; rows of a bad page are zeros there).
-constexpr int kQ4CopyRows = 128;
+constexpr int kCopyPageRows = 128;
 struct PageReadArgs {
     const uint8_t* key_pages;     // [P, H_kv, ps, row bytes]
     const uint8_t* value_pages;

@@ -33,10 +33,12 @@
 //     2^-9 of a term, averages out below the output's own rounding), the states.
 // TMEM (512 columns): S_0, S_1, O_0, O_1 (128 each).
 //
-// Measured, a call (three kernels): 8 bf16 requests behind 2048 keys 14.6 us; 32 in groups
-// of 7 behind 16384 keys 32.2 (57 MB; each request over its own table: 1.1 GB); 64 e4m3
-// requests behind 3 prefixes, 31000 keys in all, 56 (140 MB); 16 chunks of 4 rows behind 8192
-// 4-bit keys 39. What bounds them: a chain of three kernels, 2 us from one to the next, and
+// Measured, a call (three kernels), and the plain decode over tables that name the same
+// pages, which then lie in L2: 8 bf16 requests behind 2048 keys 14.8 us, plain 14.1; 32 in
+// groups of 7 behind 16384 keys 32.3 (57 MB), 134; 64 e4m3 requests behind 3 prefixes, 31000
+// keys in all, 56 (140 MB), 225; 16 chunks of 4 rows behind 8192 4-bit keys 39.5, 70. The
+// plain call is ahead up to about 16000 shared positions of all requests together, this one
+// from about 32000. What bounds it: a chain of three kernels, 2 us from one to the next, and
 // in each what a block does once (about 2 us to its pieces, 2 to its rows, 1.5 for the
 // first run of its instructions, 2 to write a state); the states themselves (20 MB written
 // and read again with 38 blocks an item); from about ten tiles a block on the steps: 1.25

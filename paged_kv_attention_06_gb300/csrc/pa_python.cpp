@@ -1,10 +1,11 @@
 // The Python side of the calls that take a model's step from the projection to
 // the evicted cache (pa_qk_norm_rope_append, the window and weight calls,
-// pa_kv_evict), of the 4-bit pools' calls and of the decode behind shared prefixes: argument checks, the tensors that a call makes where none are
-// given (outputs, a workspace of this call alone, both made on the device of the
-// call and for its stream), and the call of the C ABI on that device and stream. An
-// append of one token takes 2.1 us on the GPU; a call of it 3.4 us, 10.7 with these
-// checks written in Python.
+// pa_kv_evict), of the 4-bit pools' calls and of the decode behind shared prefixes:
+// argument checks, the tensors that a call makes where none are given (outputs, a
+// workspace of this call alone, both made on the device of the call and for its
+// stream), and the call of the C ABI on that device and stream. An append of one token
+// takes 2.1 us on the GPU; a call of it 3.4 us, 10.7 with these checks written in
+// Python.
 //
 // Module _pagedattn_calls; binding.py declares the signatures and documents them.
 #include <Python.h>

@@ -12,13 +12,12 @@
 // bf16, into dense rows or into the 128-token pages that the prefill kernels read.
 //
 // A row of 128 bf16 is 16 lanes of 16 bytes in, 4 bytes of codes a lane out (or the other
-// way round), the group's extremes found among 4 lanes. Measured, both calls together: 4 x
-// 2047 tokens of 8 heads written and 11.8k read back, 108 MB, 27.0 us (4.0 TB/s, of 6.8
-// for a copy); 32 tokens written and 37.6k of 4 heads read back, 101 MB, 23.3; one token and 300
-// rows 5.3. Two kernels of which the second waits for the first: what bounds them is the
-// latency of one pass of loads a block, and the append's instructions (with quotients near
-// a half decided in 64 bits it took 48 us alone, 18 in the fp32 arithmetic below; streamed
-// loads or stores change nothing).
+// way round), the group's extremes found among 4 lanes. Measured: 4 x 2047 tokens of 8
+// heads written, 44 MB, 14.6 us, and 11.8k read back, 63 MB, 13.8; both calls together 26.8 (4.0
+// TB/s, of 6.7 for a copy); 32 tokens written 2.1 and 37.6k of 4 heads read back, 101 MB,
+// 20.6, together 23.2; one token 1.9 and 300 rows 3.3, 5.3. What bounds them is the latency
+// of one pass of loads a block, and the append's instructions (with quotients near a half
+// decided in 64 bits it took 48 us alone; streamed loads or stores change nothing).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <stdint.h>
@@ -210,8 +209,8 @@ __global__ void __launch_bounds__(256) read_pages_kernel(const PageReadArgs a)
         n = n < 0 ? 0 : cap;
     }
     if (a.table_out && h == 0 && threadIdx.x == 0)
-        a.table_out[int64_t(b) * a.copy_pages + first / kQ4CopyRows] = b * a.copy_pages + first / kQ4CopyRows;
-    static_assert(kReadTokens == kQ4CopyRows, "a block writes one page of a copy");
+        a.table_out[int64_t(b) * a.copy_pages + first / kCopyPageRows] = b * a.copy_pages + first / kCopyPageRows;
+    static_assert(kReadTokens == kCopyPageRows, "a block writes one page of a copy");
     if (first >= n)
         return;
     const int32_t* bt = a.block_table + int64_t(b) * a.max_pages;
@@ -251,7 +250,7 @@ __global__ void __launch_bounds__(256) read_pages_kernel(const PageReadArgs a)
     // (128-token blocks of dense rows follow on, copy pages are apart by the other heads'
     // pages)
     const int64_t base = int64_t(b) * a.batch_stride + int64_t(h) * a.head_stride +
-                         int64_t(first / kQ4CopyRows) * a.block_stride + c * 8;
+                         int64_t(first / kCopyPageRows) * a.block_stride + c * 8;
 #pragma unroll
     for (int k = 0; k < kRounds; ++k) {
         if (!live[k])
