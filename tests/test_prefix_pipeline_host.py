@@ -1,6 +1,6 @@
-"""The barriers between the warps of the shared-prefix kernel (bf16 pools), on the CPU: every
-order in which the loaders, the copies, the tensor core and the softmax may come is tried,
-and none may leave them waiting for one another."""
+"""The barriers between the warps of the shared-prefix kernel, on the CPU: every order in which
+the loaders, the copies, the converters (pools of codes), the tensor core and the softmax may
+come is tried, and none may leave them waiting for one another."""
 import os
 import re
 
@@ -18,11 +18,10 @@ def first_wait_of_values():
 
 
 def programs(tiles, pair, gate):
-    """Each warp's steps, one piece of `tiles` tiles: (wait, barrier, parity), (arrive,
-    barrier), (load, barrier). A barrier's phase completes with one arrival."""
-    steps = [(g, sub) for g in range(tiles) for sub in range(2 if pair else 1)]
-    closes = [not pair or sub == 1 for _, sub in steps]
-    keys, values, products = [], [], []
+    """Each warp's steps over bf16 pools, one piece of `tiles` tiles: (wait, barrier,
+    parity), (arrive, barrier), (load, barrier). A barrier's phase completes with one
+    arrival."""
+    keys, values = [], []
     first = [("wait", ("kKFull", 0), 0), ("arrive", ("kFirstKeys", 0))]
     for g in range(tiles):
         st, turn = g & 1, (g >> 1) & 1
@@ -37,6 +36,33 @@ def programs(tiles, pair, gate):
     for g in range(max(0, tiles - 2), tiles):
         keys += [("wait", ("kKFull", g & 1), (g >> 1) & 1)]
         values += [("wait", ("kVFull", g & 1), (g >> 1) & 1)]
+    return [keys, values, *products_and_softmax(tiles, pair, 2)]
+
+
+def programs_of_codes(tiles, pair, ring=3):
+    """The same over pools of codes: one loader of codes into a ring, one converter, one stage
+    of values."""
+    order = [("K", 0)]
+    for g in range(tiles):
+        order += ([("K", g + 1)] if g + 1 < tiles else []) + [("V", g)]
+    codes, converter = [], []
+    for u, (what, g) in enumerate(order):
+        slot, turn = u % ring, u // ring & 1
+        st, use = (g & 1, g >> 1) if what == "K" else (0, g)
+        codes += [("wait", ("kCodeEmpty", slot), turn ^ 1), ("load", ("kCodeFull", slot))]
+        converter += [("wait", ("kCodeFull", slot), turn), ("wait", (f"k{what}Empty", st), use & 1 ^ 1),
+                      ("arrive", (f"k{what}Full", st)), ("arrive", ("kCodeEmpty", slot))]
+    u = len(order)                                           # the end
+    codes += [("wait", ("kCodeEmpty", u % ring), u // ring & 1 ^ 1), ("arrive", ("kCodeFull", u % ring))]
+    codes += [("wait", ("kCodeEmpty", x % ring), x // ring & 1 ^ 1) for x in range(u + 1, u + ring)]
+    converter += [("wait", ("kCodeFull", u % ring), u // ring & 1)]
+    return [codes, converter, *products_and_softmax(tiles, pair, 1)]
+
+
+def products_and_softmax(tiles, pair, value_stages):
+    steps = [(g, sub) for g in range(tiles) for sub in range(2 if pair else 1)]
+    closes = [not pair or sub == 1 for _, sub in steps]
+    products = []
 
     def scores(j):
         g = steps[j][0]
@@ -47,16 +73,17 @@ def programs(tiles, pair, gate):
         products += scores(j)
     for j, (g, _) in enumerate(steps):
         phase = (j >> 1) & 1
-        products += [("wait", ("kPFull", j & 1), phase), ("wait", ("kVFull", g & 1), (g >> 1) & 1),
+        st, use = (0, g) if value_stages == 1 else (g & 1, g >> 1)
+        products += [("wait", ("kPFull", j & 1), phase), ("wait", ("kVFull", st), use & 1),
                      ("arrive", ("kPVDone", j & 1))]
         if closes[j]:
-            products += [("arrive", ("kVEmpty", g & 1))]
+            products += [("arrive", ("kVEmpty", st))]
         products += [("wait", ("kPVDone", j & 1), phase)]
         if j + 2 < len(steps):
             products += scores(j + 2)
     halves = [[x for j in range(h, len(steps), 2)
                for x in (("wait", ("kSFull", h), (j >> 1) & 1), ("arrive", ("kPFull", h)))] for h in range(2)]
-    return [keys, values, products, *halves]
+    return [products, *halves]
 
 
 def stalls(warps):
@@ -98,6 +125,12 @@ def stalls(warps):
 @pytest.mark.parametrize("tiles", [1, 2, 3, 4, 5, 6])
 def test_no_order_of_events_stalls(tiles, pair):
     assert not stalls(programs(tiles, pair, first_wait_of_values()))
+
+
+@pytest.mark.parametrize("pair", [False, True])
+@pytest.mark.parametrize("tiles", [1, 2, 3, 4, 5, 6])
+def test_no_order_of_events_stalls_over_codes(tiles, pair):
+    assert not stalls(programs_of_codes(tiles, pair))
 
 
 def test_a_wait_by_parity_from_outside_a_ring_is_found():
