@@ -1992,7 +1992,8 @@ pa_status plan_prefix(const pa_shape& s, int32_t page_size, int kind, int32_t co
         count <= 0 || max_prefix_len <= 0)
         return PA_ERR_INVALID_ARG;
     if ((s.head_dim != 128 && (kind != kBf16Pool || s.head_dim != 64)) || !pow2_in(page_size, 1, 256) ||
-        !rows_shape_ok(s) || count > kMaxPrefixes || max_prefix_len >= (1 << 30))
+        !rows_shape_ok(s) || !rows_count_ok(s, kind, page_size) || count > kMaxPrefixes ||
+        max_prefix_len >= (1 << 30))
         return PA_ERR_UNSUPPORTED;
     const int64_t R = int64_t(s.num_q_heads / s.num_kv_heads) * s.q_len;
     if (!decode_rows_fits(s, kind, kSuffix, dev->max_smem_optin) || s.batch * R >= (int64_t(1) << 30) ||
