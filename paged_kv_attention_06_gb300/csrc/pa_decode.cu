@@ -854,8 +854,12 @@ __global__ void __launch_bounds__(kThreads, 2)
                     if (out_row(sp, rw) < 0)
                         continue;
                     if (warp == 0 && quad == 0) {
+                        float l = Lr[rr];
+                        if (Mr[rr] == -INFINITY)     // 0 where nothing was seen, NaN where the scores are
+                            for (int w = 0; w < kConsumerWarps; ++w)
+                                l += wstate[w][1][rw];
                         slot[rw] = Mr[rr];
-                        slot[kDecodeRows + rw] = Lr[rr];
+                        slot[kDecodeRows + rw] = l;
                     }
                     float* dst = slot + 2 * kDecodeRows + rw * D + col0 + 2 * quad;
 #pragma unroll
@@ -1244,7 +1248,7 @@ __global__ void __launch_bounds__(kMergeThreads) decode_merge_kernel(const Decod
         const float* base = a.partials + (int64_t(seg) + first) * slot_floats + t * kTileFloats;
         // M' = max(M, m_k), l = l 2^(M - M') + l_k 2^(m_k - M'), likewise o
         // (the pieces in order, so repeated calls give the same bits).
-        float Mx = -INFINITY, L2 = 0.f;
+        float Mx = -INFINITY, L2 = 0.f, all_l = 0.f;   // all_l: NaN where a piece's sum is
         float fin[kCols];
 #pragma unroll
         for (int c = 0; c < kCols; ++c)
@@ -1266,8 +1270,9 @@ __global__ void __launch_bounds__(kMergeThreads) decode_merge_kernel(const Decod
             }
 #pragma unroll
             for (int u = 0; u < kFly; ++u) {
+                all_l += lk[u];
                 if (mk[u] == -INFINITY)
-                    continue;  // absent piece, or no visible key in it
+                    continue;  // absent piece, no visible key in it, or all its scores NaN
                 const float Mn = fmaxf(Mx, mk[u]);
                 const float co = Mx == -INFINITY ? 0.f : fast_exp2(Mx - Mn);
                 const float cn = fast_exp2(mk[u] - Mn);
@@ -1286,7 +1291,7 @@ __global__ void __launch_bounds__(kMergeThreads) decode_merge_kernel(const Decod
             if (c0 == 0)
                 a.row_state[(int64_t(b) * a.H_kv + h) * a.R + rg] = make_float2(Mx, L2);
         }
-        const float inv = L2 > 0.f ? 1.f / L2 : 0.f;
+        const float inv = all_l != all_l ? all_l : L2 > 0.f ? 1.f / L2 : 0.f;
         uint16_t* dst = a.out + orow * D + c0;
 #pragma unroll
         for (int c = 0; c < kCols; c += 4)   // 4 bf16 (8 bytes) at a time
